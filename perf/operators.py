@@ -338,7 +338,7 @@ def _own(s):
     if s["states"]:
         out["final"] = res[2]
     if s["train"]:
-        g = vs.varlen_gated_delta_bwd(*args, s["dout"], s["cu"], res[1], scale=s["scale"], initial_states=s["init"],
+        g = vs.varlen_gated_delta_bwd(*args, s["dout"], s["cu"], res[1], scale=s["scale"],
                                       d_final_states=s["dfinal"], d_initial_states=s["states"])
         out.update(dq=g["dq"], dk=g["dk"], dv=g["dv"], dg=g["dg"], dbeta=g["dbeta"])
         if s["states"]:

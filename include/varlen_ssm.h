@@ -80,6 +80,7 @@ typedef enum { VSSM_F32 = 0, VSSM_BF16 = 1 } vssm_dtype;
 #define VSSM_ERR_LOOKBACK_TIMEOUT (-17)/* a cross-chunk or tile-copy wait gave up; results invalid */
 #define VSSM_ERR_NONFINITE (-18)        /* an output holds a NaN / inf (VSSM_DBG_CHECK_FINITE on) */
 #define VSSM_ERR_DEVICE_CHECK (-19)     /* a device index check failed (VSSM_CHECKS=1 build only) */
+#define VSSM_ERR_BAD_INDEX (-20)        /* a position or state index outside its table */
 
 /* Tokens per saved scan-state chunk: the forward scan can save the state at
  * every multiple of this many tokens for the backward scan. */
@@ -318,6 +319,115 @@ int varlen_conv1d_scan_fwd(const void* x, const float* conv_weight, const float*
                            int64_t total_tokens, int32_t D, int32_t N, vssm_dtype dtype, void* u, void* out,
                            void* y, float* chunk_states, const float* initial_states, float* final_states,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------ norm and rotation of queries and keys
+ * Each head's row x of K values is normalised, scaled and rotated by its
+ * token's position in one pass:
+ *   n = x / sqrt(mean(x^2) + eps)      (l2 == 0: root mean square)
+ *   n = x / sqrt(sum(x^2) + eps)       (l2 != 0: unit length)
+ *   y = n * weight                     (weight (K) f32, nullable: ones)
+ *   out[i]        = y[i] c - y[i + h] s,  out[i + h] = y[i + h] c + y[i] s   for i < h = rot / 2,
+ *   out[i]        = y[i]                                                     for i >= rot,
+ * with c = cos[p][i], s = sin[p][i], p = positions[token].  Unit-length keys
+ * are what the gated delta rule below needs: its state transition is then a
+ * contraction for beta in (0, 1].  The array varlen_position_indices builds
+ * is a valid `positions` for a pack.
+ *   q (T, Hq, K), k (T, Hk, K) io: heads contiguous, tokens q_stride / k_stride
+ *     elements apart (at least heads * K, a multiple of 16 bytes), so that
+ *     they may be slices of one projection's rows; 16-byte aligned.  Hq or Hk
+ *     may be 0.
+ *   q_out, k_out: contiguous, 16-byte aligned.
+ *   cos, sin: (table_rows, rot / 2) f32, NULL when rot == 0 (positions unused).
+ *   K a multiple of 8, 8 to 256; rot even, 0 to K.
+ *   status: nullable device int32; a position outside the table ORs a bit into
+ *     it (vssm_status_code: VSSM_ERR_BAD_INDEX) and leaves NaN in that token's
+ *     rotated values.
+ * Sums are float32; bf16 results are rounded once.
+ */
+int varlen_qk_norm_rope_fwd(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                            const float* q_weight, const float* k_weight, const float* cos, const float* sin,
+                            const int32_t* positions, int64_t table_rows, int64_t total_tokens, int32_t Hq,
+                            int32_t Hk, int32_t K, int32_t rot, int32_t l2, float eps, vssm_dtype dtype,
+                            void* q_out, void* k_out, int32_t* status, void* stream);
+
+/* Backward: dq, dk (contiguous, io) from dq_out, dk_out (contiguous, io), and
+ * dq_weight, dk_weight (K) f32, each nullable, summed over tokens and heads in
+ * a fixed order (bitwise repeatable).  The row's length is recomputed from q
+ * and k.  Other arguments as the forward call's; the status word is the
+ * workspace's (vssm_read_status). */
+size_t varlen_qk_norm_rope_bwd_workspace_size(int32_t K);
+int varlen_qk_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                            const float* q_weight, const float* k_weight, const float* cos, const float* sin,
+                            const int32_t* positions, int64_t table_rows, const void* dq_out, const void* dk_out,
+                            int64_t total_tokens, int32_t Hq, int32_t Hk, int32_t K, int32_t rot, int32_t l2,
+                            float eps, vssm_dtype dtype, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------ gated delta rule
+ * A linear recurrence whose state is a K x V matrix per head, on the same
+ * packed batches as the selective scan: it resets at every sequence start.
+ * Per value head, with a_t = exp(g_t):
+ *   S_t = a_t S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - a_t S_{t-1}^T k_t)
+ *   out_t = scale * S_t^T q_t
+ * q, k (T, Hk, K), v (T, Hv, V) io: heads contiguous, tokens q_stride /
+ *   k_stride / v_stride elements apart (multiples of 16 bytes, at least the
+ *   row), 16-byte aligned.  Hv is a multiple of Hk: value head j uses the
+ *   query and key head j / (Hv / Hk).
+ * g, beta (T, Hv) f32.  g is a log decay, usually <= 0 (values below -256 are
+ *   taken as -256: both decay to zero).
+ * out (T, Hv, V) io, contiguous, 16-byte aligned.
+ * K a multiple of 8, 8 to 128; V a multiple of 8, 8 to 1024.
+ * initial_states / final_states: nullable f32 (num_seqs, Hv, K, V), 16-byte
+ *   aligned, as the selective scan's (an empty sequence's final state is its
+ *   initial one).
+ * saved: nullable; varlen_gated_delta_saved_size bytes, 16-byte aligned, that
+ *   the backward call needs: per chunk of 64 tokens the state before it and
+ *   the chunk's solved triangular systems.
+ * Products run on the tensor cores with every FP32 operand carried as a sum of
+ *   bf16 terms: three (all 24 bits) for f32 I/O, two (16 bits) for
+ *   bf16 I/O; accumulation and the state are float32.
+ * workspace: 16-byte aligned; its status word (vssm_read_status) reports a
+ *   malformed cu_seqlens (nothing is written then) and waits that gave up.
+ */
+size_t varlen_gated_delta_saved_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv, int32_t K,
+                                     int32_t V, vssm_dtype dtype);
+size_t varlen_gated_delta_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
+                                             int32_t K, int32_t V, vssm_dtype dtype);
+int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const float* g, const float* beta, float scale,
+                           const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
+                           int32_t Hv, int32_t K, int32_t V, vssm_dtype dtype, void* out,
+                           const float* initial_states, float* final_states, void* saved, size_t saved_bytes,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward: dq, dk (T, Hk, K), dv (T, Hv, V) io, contiguous; dg, dbeta (T, Hv)
+ * f32; d_initial_states nullable.  saved is the array the forward call on the
+ * same inputs filled (read only); d_final_states: nullable, the gradient
+ * reaching the final states.  dq and dk add the value heads that share a key head, in
+ * order; no atomics, bitwise repeatable. */
+size_t varlen_gated_delta_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
+                                             int32_t K, int32_t V, vssm_dtype dtype);
+int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seqlens, int32_t num_seqs,
+                           int64_t total_tokens, int32_t Hk, int32_t Hv, int32_t K, int32_t V, vssm_dtype dtype,
+                           const void* saved, size_t saved_bytes, const float* d_final_states,
+                           float* d_initial_states, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of `batch` sequences, against a pool of states updated in
+ * place: the recurrence above, once.  q, k (batch, Hk, K), v (batch, Hv, V)
+ * with strides as above; g, beta (batch, Hv); out (batch, Hv, V) contiguous.
+ * states: (num_slots, Hv, K, V) f32, 16-byte aligned.
+ * state_indices: nullable int32 (batch), the slot of each sequence (NULL: its
+ *   own number).  The slots of one call must differ.  A negative index is a
+ *   padded entry: its output is zero and no state is touched.
+ * status: nullable device int32; an index of num_slots or more ORs a bit into
+ *   it (VSSM_ERR_BAD_INDEX), leaves NaN in that output and touches no state.
+ */
+int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const float* g, const float* beta, float scale, float* states,
+                            const int32_t* state_indices, int64_t num_slots, int64_t batch, int32_t Hk,
+                            int32_t Hv, int32_t K, int32_t V, vssm_dtype dtype, void* out, int32_t* status,
+                            void* stream);
 
 /* ------------------------------------------------------------ status, errors, knobs
  * vssm_read_status: synchronises `stream`, reads the status word the last call

@@ -27,9 +27,10 @@ KERNEL_KINDS = {"conv_fwd": 0, "scan_fwd": 1, "scan_bwd": 2, "conv_bwd": 3}
 ERR = {0: "VSSM_OK", -1: "VSSM_ERR_ARG", -2: "VSSM_ERR_DTYPE", -3: "VSSM_ERR_ALIGN",
        -4: "VSSM_ERR_WORKSPACE", -5: "VSSM_ERR_CUDA", -6: "VSSM_ERR_UNSUPPORTED",
        -16: "VSSM_ERR_BAD_CU_SEQLENS", -17: "VSSM_ERR_LOOKBACK_TIMEOUT", -18: "VSSM_ERR_NONFINITE",
-       -19: "VSSM_ERR_DEVICE_CHECK"}
+       -19: "VSSM_ERR_DEVICE_CHECK", -20: "VSSM_ERR_BAD_INDEX"}
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -61,6 +62,21 @@ SIGNATURES = {
                                                          ctypes.c_float, _i32,
                                                          _vp, _vp, _i32, _i64, _i32, _i32, ctypes.c_int,
                                                          _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "varlen_qk_norm_rope_fwd": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32,
+                                               _i32, _i32, _i32, _f32, ctypes.c_int, _vp, _vp, _vp, _vp]),
+    "varlen_qk_norm_rope_bwd_workspace_size": (_sz, [_i32]),
+    "varlen_qk_norm_rope_bwd": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64,
+                                               _i32, _i32, _i32, _i32, _i32, _f32, ctypes.c_int, _vp, _vp, _vp, _vp,
+                                               _vp, _sz, _vp]),
+    "varlen_gated_delta_saved_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "varlen_gated_delta_fwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "varlen_gated_delta_bwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "varlen_gated_delta_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _i32, _i64, _i32,
+                                              _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp]),
+    "varlen_gated_delta_bwd": (ctypes.c_int, [_vp, _f32, _vp, _i32, _i64, _i32, _i32, _i32, _i32, ctypes.c_int, _vp,
+                                              _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "varlen_gated_delta_step": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _vp, _i64, _i64,
+                                               _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp]),
     "varlen_pack_sequences": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _vp,
                                              ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double)]),
     "vssm_read_status": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(ctypes.c_int)]),
@@ -403,6 +419,200 @@ def varlen_selective_scan_bwd(u, delta_raw, A, B, C, Dskip, z, dt_bias, dout, cu
         _ptr(g["dz"], "dz", dt), _ptr(g["d_dt_bias"], "d_dt_bias", torch.float32),
         _ptr(ws, "workspace"), ws.numel(), _stream(stream)), "varlen_selective_scan_bwd")
     return g
+
+
+# ------------------------------------------------------------------ heads of a token
+def _heads(t, name, dtype=None, heads=None, width=None):
+    """(pointer, token stride) of a (T, H, K) CUDA tensor whose heads are
+    contiguous and whose tokens may be any distance apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be (tokens, heads, width), got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    T, H, K = t.shape
+    if (heads is not None and H != heads) or (width is not None and K != width):
+        raise ValueError(f"{name} must be (tokens, {heads or H}, {width or K}), got {tuple(t.shape)}")
+    if t.numel() and ((K > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != K)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr() or None, (t.stride(0) if T > 1 else H * K)
+
+
+def _shaped(t, name, shape, dtype=torch.float32):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return _ptr(t, name, dtype)
+
+
+def _asked(t, shape, like, dtype=torch.float32):
+    """None / False: not wanted; True: allocated; a tensor: filled."""
+    if t is None or t is False:
+        return None
+    return torch.empty(shape, dtype=dtype, device=like.device) if t is True else t
+
+
+# ------------------------------------------------------------------ norm and rotation of queries and keys
+QK_NORM_MODES = {"rms": 0, "l2": 1}
+
+
+def _norm_args(q, k, q_weight, k_weight, cos, sin, positions, mode):
+    if mode not in QK_NORM_MODES:
+        raise ValueError(f"mode must be one of {sorted(QK_NORM_MODES)}, got {mode!r}")
+    T, Hq, K = q.shape
+    Hk = k.shape[1]
+    if k.shape[0] != T:
+        raise ValueError(f"q has {T} tokens, k has {k.shape[0]}")
+    qp, sq = _heads(q, "q")
+    kp, sk = _heads(k, "k", q.dtype, width=K)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin must be given together")
+    rows = half = 0
+    if cos is not None:
+        rows, half = cos.shape
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+    return [qp, kp, sq, sk, _shaped(q_weight, "q_weight", (K,)), _shaped(k_weight, "k_weight", (K,)),
+            _ptr(cos, "cos", torch.float32), _shaped(sin, "sin", (rows, half)),
+            _shaped(positions, "positions", (T,), torch.int32) if cos is not None else None, rows], (T, Hq, Hk, K, 2 * half)
+
+
+def varlen_qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, mode="rms",
+                            eps=1e-6, q_out=None, k_out=None, status=None, stream=None):
+    """Returns (q_out, k_out): each head of q (T, Hq, K) and k (T, Hk, K)
+    normalised (mode "rms" or "l2"), scaled by its weight (K) and rotated by
+    its token's position with the tables cos, sin (P, rot / 2); cos None: no
+    rotation.  q and k may be slices of wider rows (heads contiguous).
+    status: optional int32 tensor for positions outside the tables."""
+    lead, (T, Hq, Hk, K, rot) = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, mode)
+    q_out = torch.empty((T, Hq, K), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty((T, Hk, K), dtype=q.dtype, device=q.device) if k_out is None else k_out
+    _check(lib().varlen_qk_norm_rope_fwd(
+        *lead, T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), _shaped(q_out, "q_out", (T, Hq, K), q.dtype),
+        _shaped(k_out, "k_out", (T, Hk, K), q.dtype), _ptr(status, "status", torch.int32), _stream(stream)),
+        "varlen_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def varlen_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, mode="rms", eps=1e-6,
+                            grads=None, workspace=None, stream=None):
+    """Returns dict dq, dk and, where the forward call had weights, dq_weight,
+    dk_weight (else None); grads: tensors to fill instead, by those names."""
+    lead, (T, Hq, Hk, K, rot) = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, mode)
+    g = dict(grads or {})
+    make = {"dq": lambda: torch.empty((T, Hq, K), dtype=q.dtype, device=q.device),
+            "dk": lambda: torch.empty((T, Hk, K), dtype=q.dtype, device=q.device),
+            "dq_weight": lambda: torch.empty_like(q_weight) if q_weight is not None else None,
+            "dk_weight": lambda: torch.empty_like(k_weight) if k_weight is not None else None}
+    for n, f in make.items():
+        if n not in g:
+            g[n] = f()
+    ws = _ws(workspace, lib().varlen_qk_norm_rope_bwd_workspace_size(K), q.device)
+    _check(lib().varlen_qk_norm_rope_bwd(
+        *lead, _shaped(dq_out, "dq_out", (T, Hq, K), q.dtype), _shaped(dk_out, "dk_out", (T, Hk, K), q.dtype),
+        T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), _shaped(g["dq"], "dq", (T, Hq, K), q.dtype),
+        _shaped(g["dk"], "dk", (T, Hk, K), q.dtype), _shaped(g["dq_weight"], "dq_weight", (K,)),
+        _shaped(g["dk_weight"], "dk_weight", (K,)), _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+        "varlen_qk_norm_rope_bwd")
+    return g
+
+
+# ------------------------------------------------------------------ gated delta rule
+def gated_delta_saved_size(T, S, Hk, Hv, K, V, dtype):
+    return lib().varlen_gated_delta_saved_size(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype))
+
+
+def gated_delta_fwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
+    return lib().varlen_gated_delta_fwd_workspace_size(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype))
+
+
+def gated_delta_bwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
+    return lib().varlen_gated_delta_bwd_workspace_size(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype))
+
+
+def _delta_args(q, k, v, g, beta):
+    T, Hk, K = q.shape
+    Hv, V = v.shape[1], v.shape[2]
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k and v have {T}, {k.shape[0]} and {v.shape[0]} tokens")
+    qp, sq = _heads(q, "q")
+    kp, sk = _heads(k, "k", q.dtype, Hk, K)
+    vp, sv = _heads(v, "v", q.dtype)
+    return [qp, kp, vp, sq, sk, sv, _shaped(g, "g", (T, Hv)), _shaped(beta, "beta", (T, Hv))], (T, Hk, Hv, K, V)
+
+
+def varlen_gated_delta_fwd(q, k, v, g, beta, cu_seqlens, scale=None, out=None, saved=True, workspace=None, stream=None,
+                           initial_states=None, final_states=None):
+    """Returns (out, saved), and final_states last when they are asked for.
+    q, k (T, Hk, K), v (T, Hv, V) may be slices of wider rows; g, beta (T, Hv)
+    f32; scale: K ** -0.5 when None.  saved=True allocates the array the
+    backward call needs (None / False: not written, None returned), a uint8
+    tensor is filled.  initial_states, final_states: (S, Hv, K, V) f32, the
+    latter None / False, True or a tensor to fill."""
+    args, (T, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
+    S, dt = cu_seqlens.numel() - 1, _dt(q)
+    sizes = (T, S, Hk, Hv, K, V, dt)
+    out = torch.empty((T, Hv, V), dtype=q.dtype, device=q.device) if out is None else out
+    want_final = final_states is not None and final_states is not False
+    final_states = _asked(final_states, (S, Hv, K, V), q)
+    if saved is True:
+        saved = torch.empty(max(gated_delta_saved_size(*sizes), 16), dtype=torch.uint8, device=q.device)
+    elif saved is False:
+        saved = None
+    ws = _ws(workspace, 256 if saved is not None else gated_delta_fwd_workspace_size(*sizes), q.device)
+    _check(lib().varlen_gated_delta_fwd(
+        *args, float(K ** -0.5 if scale is None else scale), _ptr(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hk, Hv,
+        K, V, dt, _shaped(out, "out", (T, Hv, V), q.dtype), _shaped(initial_states, "initial_states", (S, Hv, K, V)),
+        _shaped(final_states, "final_states", (S, Hv, K, V)), _ptr(saved, "saved", torch.uint8),
+        saved.numel() if saved is not None else 0, _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+        "varlen_gated_delta_fwd")
+    return (out, saved) + ((final_states,) if want_final else ())
+
+
+def varlen_gated_delta_bwd(q, k, v, g, beta, dout, cu_seqlens, saved, scale=None, grads=None, workspace=None,
+                           stream=None, d_final_states=None, d_initial_states=None):
+    """Returns dict dq, dk, dv, dg, dbeta, d_initial_states.  The inputs, scale
+    and saved are the forward call's (saved holds what the gradients need of
+    q .. beta: only their shapes are read).  d_final_states: (S, Hv, K, V) f32,
+    the gradient reaching the final states; d_initial_states: None / False,
+    True or a tensor to fill.  grads: tensors to fill, by name."""
+    _, (T, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
+    S, dt = cu_seqlens.numel() - 1, _dt(q)
+    sizes = (T, S, Hk, Hv, K, V, dt)
+    r = dict(grads or {})
+    shapes = {"dq": ((T, Hk, K), q.dtype), "dk": ((T, Hk, K), q.dtype), "dv": ((T, Hv, V), q.dtype),
+              "dg": ((T, Hv), torch.float32), "dbeta": ((T, Hv), torch.float32)}
+    for n, (shape, d) in shapes.items():
+        if n not in r:
+            r[n] = torch.empty(shape, dtype=d, device=q.device)
+    r["d_initial_states"] = _asked(d_initial_states, (S, Hv, K, V), q)
+    ws = _ws(workspace, gated_delta_bwd_workspace_size(*sizes), q.device)
+    _check(lib().varlen_gated_delta_bwd(
+        _shaped(dout, "dout", (T, Hv, V), q.dtype), float(K ** -0.5 if scale is None else scale),
+        _ptr(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hk, Hv, K, V, dt, _ptr(saved, "saved", torch.uint8),
+        saved.numel(), _shaped(d_final_states, "d_final_states", (S, Hv, K, V)),
+        _shaped(r["d_initial_states"], "d_initial_states", (S, Hv, K, V)),
+        *(_shaped(r[n], n, shape, d) for n, (shape, d) in shapes.items()),
+        _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)), "varlen_gated_delta_bwd")
+    return r
+
+
+def varlen_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale=None, out=None, status=None,
+                            stream=None):
+    """Returns out (B, Hv, V): one token of each of B sequences, q, k (B, Hk, K),
+    v (B, Hv, V), g, beta (B, Hv), against states (slots, Hv, K, V) f32, which
+    are updated in place.  state_indices: int32 (B) slots, all different,
+    negative for a padded entry (None: entry b uses slot b).  status: optional
+    int32 tensor for indices outside the pool."""
+    args, (B, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
+    slots = states.shape[0]
+    out = torch.empty((B, Hv, V), dtype=q.dtype, device=q.device) if out is None else out
+    _check(lib().varlen_gated_delta_step(
+        *args, float(K ** -0.5 if scale is None else scale), _shaped(states, "states", (slots, Hv, K, V)),
+        _shaped(state_indices, "state_indices", (B,), torch.int32), slots, B, Hk, Hv, K, V, _dt(q),
+        _shaped(out, "out", (B, Hv, V), q.dtype), _ptr(status, "status", torch.int32), _stream(stream)),
+        "varlen_gated_delta_step")
+    return out
 
 
 # ------------------------------------------------------------------ packing (host)

@@ -29,8 +29,10 @@ LIB_PATH = os.path.join(BUILD_DIR, "libvarlen_ssm.so")
 CHECKS_BUILD_DIR = os.path.join(HERE, "_build_checks")
 CHECKS_LIB_PATH = os.path.join(CHECKS_BUILD_DIR, "libvarlen_ssm_checks.so")
 
-SOURCES = ["api.cu", "misc.cu", "conv.cu", "scan_fwd.cu", "scan_bwd.cu", "noalloc.cu", "packer.cu"]
-HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"),
+SOURCES = ["api.cu", "misc.cu", "conv.cu", "scan_fwd.cu", "scan_bwd.cu", "noalloc.cu", "packer.cu",
+           "delta_api.cu", "delta_prep.cu", "delta_fwd.cu", "delta_bwd.cu", "delta_grad.cu", "delta_step.cu",
+           "qk_norm.cu"]
+HEADERS = [*(os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "umma.cuh", "delta.cuh", "delta.h")),
            os.path.join(INCLUDE, "varlen_ssm.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

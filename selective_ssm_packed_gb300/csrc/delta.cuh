@@ -1,0 +1,90 @@
+// delta.cuh -- device helpers of the chunked gated delta rule's kernels.
+#pragma once
+
+#include "delta.h"
+#include "umma.cuh"
+
+namespace vssm {
+
+template <IO kIO> struct IoType { using type = float; };
+template <> struct IoType<IO::BF16> { using type = __nv_bfloat16; };
+
+// exp(x) with the error of x * log2(e) carried along: the MUFU's 2^-22
+// remains, at any |x| whose exponential is a normal number.
+__device__ __forceinline__ float exp_f(float x) {
+  const float t = x * kLog2e;
+  const float r = fmaf(x, kLog2e, -t) + x * 1.925963033500e-8f;  // log2(e) - kLog2e
+  const float p = ex2(t);
+  // t = -inf (or an overflow) leaves r meaningless: the power is then 0 or inf by itself
+  return fabsf(t) < 126.0f ? fmaf(p, r * 0.6931471805599453f, p) : p;
+}
+
+// 8 consecutive io values as floats (16-byte aligned).
+__device__ __forceinline__ void ld_io8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void ld_io8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+  v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+}
+__device__ __forceinline__ void st_io8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void st_io8(__nv_bfloat16* p, const float* v) {
+  uint32_t t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    t[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(t[0], t[1], t[2], t[3]);
+}
+
+// Writes 8 values as chunk `chunk` of row `row` of NT images term_bytes apart
+// (shared or global memory).
+template <int NT, int kRowBytes>
+__device__ __forceinline__ void put_chunk(uint8_t* image, int term_bytes, int row, int chunk, const float* v) {
+  uint32_t t[4][NT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_pair<NT>(v[2 * i], v[2 * i + 1], t[i]);
+  const uint32_t o = image_chunk<kRowBytes>(row, chunk);
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    *reinterpret_cast<uint4*>(image + i * term_bytes + o) = make_uint4(t[0][i], t[1][i], t[2][i], t[3][i]);
+}
+
+// `count` values of this thread's row, columns from chunk0 * 8.
+template <int NT, int kRowBytes, int kCount>
+__device__ __forceinline__ void put_row(uint8_t* image, int term_bytes, int row, int chunk0, const float (&v)[kCount]) {
+#pragma unroll
+  for (int c = 0; c < kCount / 8; ++c) put_chunk<NT, kRowBytes>(image, term_bytes, row, chunk0 + c, v + 8 * c);
+}
+
+// Waits of one thread of a chunk kernel: after one that runs out of time the
+// status word says so and the later ones no longer wait.
+struct Waiter {
+  unsigned long long limit;
+  int* status;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait(bar, parity, limit)) {
+      if (limit) atomicOr(status, kStatusTmaTimeout);
+      limit = 0;
+    }
+  }
+};
+
+template <typename P>
+__device__ __forceinline__ P* align1024(P* p) {
+  return reinterpret_cast<P*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~(uintptr_t)1023);
+}
+
+// The work one chunk kernel's CTA finds for itself.
+inline cudaError_t set_smem(const void* f, size_t bytes) {
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+}  // namespace vssm

@@ -1,0 +1,287 @@
+// delta_prep.cu -- the gated delta rule's plan of a pack and everything of a
+// chunk that no earlier chunk enters: gates, the images of [K; Q], and X.
+#include "delta.cuh"
+
+namespace vssm {
+namespace {
+
+// ------------------------------------------------------------------ plan
+// Every block sums the sequences' chunk counts for itself (a pack has a few
+// thousand sequences, so that costs less than a second launch), block 0
+// writes the sums, and each block fills its share of the chunk table.
+constexpr int kPlanThreads = 512;
+
+__global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
+  __shared__ int warp_sum[kPlanThreads / 32];
+  __shared__ int carry, bad;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, S = a.num_seqs;
+  if (t == 0) carry = bad = 0;
+  __syncthreads();
+  for (int base = 0; base < S; base += kPlanThreads) {
+    const int s = base + t;
+    int n = 0;
+    if (s < S) {
+      const int64_t lo = a.cu[s], hi = a.cu[s + 1];
+      if ((s == 0 && lo != 0) || hi < lo || lo < 0 || hi > a.T || (s == S - 1 && hi != a.T)) {
+        bad = 1;
+      } else {
+        n = (int)((hi - lo + kDeltaChunk - 1) / kDeltaChunk);
+      }
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    // every block writes the same values: the later fill reads its own block's
+    if (s < S) a.first[s] = before + incl - n;
+    __syncthreads();
+    if (t == kPlanThreads - 1) carry = before + incl;
+    __syncthreads();
+  }
+  const bool ok = !bad && carry <= a.max_chunks && (S > 0 || a.T == 0);
+  const int total = ok ? carry : -1;
+  if (t == 0) {
+    a.first[S] = carry;
+    if (blockIdx.x == 0) {
+      a.info[0] = total;
+      if (!ok) atomicOr(a.status, kStatusBadCu);
+    }
+  }
+  __threadfence_block();
+  __syncthreads();
+  for (int c = blockIdx.x * kPlanThreads + t; c < total; c += gridDim.x * kPlanThreads) {
+    int lo = 0, hi = S - 1;  // the last sequence whose first chunk is at or before c
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.first[mid] <= c) lo = mid; else hi = mid - 1;
+    }
+    const int place = c - a.first[lo];
+    const int start = a.cu[lo] + place * kDeltaChunk;
+    a.table[c] = make_int4(lo, start, min(kDeltaChunk, a.cu[lo + 1] - start), place);
+  }
+}
+
+// ------------------------------------------------------------------ prep
+// One CTA of 128 threads per chunk and key head; the value heads that share
+// the key head follow each other.  Thread r < 64 owns row r of K K^T, N and
+// Tm, thread 64 + r row r of Q K^T, P and P Tm: both halves of X solve
+// X (I + N) = [I; P] by substitution from the last column, x_j final, then
+// x_l -= x_j N_jl for l < j, with the row in registers and N read from shared
+// memory as one broadcast for the whole warp.  Substitution is taken over
+// summing powers of N because those grow without bound for keys that
+// resemble each other, while the entries of Tm do not.
+constexpr int kNPitch = 68;  // floats a row of N: 16-byte writes of a warp's rows hit all banks
+
+template <IO kIO, int KP>
+struct PrepSmem {
+  static constexpr int kImages = DeltaTerms<kIO>::kIn * KP * 16384;
+  static constexpr int kBytes = kImages + 64 * kNPitch * 4 + 64 * 8 + 64 * 4 + 64 + 1024;
+};
+
+__device__ __forceinline__ void substitute(float2 (&x)[32], const float* n, int from_row, bool upper) {
+  (void)from_row;
+  if (upper) {
+#pragma unroll
+    for (int j = 63; j >= 32; --j) {
+      const float xj = (j & 1) ? x[j / 2].y : x[j / 2].x;
+      const float2 m = splat2(-xj);
+      const float4* row = reinterpret_cast<const float4*>(n + j * kNPitch);
+#pragma unroll
+      for (int q = 0; q <= (j - 1) / 4; ++q) {
+        const float4 f = row[q];
+        x[2 * q] = fma2(m, make_float2(f.x, f.y), x[2 * q]);
+        if (4 * q + 2 < j) x[2 * q + 1] = fma2(m, make_float2(f.z, f.w), x[2 * q + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 31; j >= 1; --j) {
+    const float xj = (j & 1) ? x[j / 2].y : x[j / 2].x;
+    const float2 m = splat2(-xj);
+    const float4* row = reinterpret_cast<const float4*>(n + j * kNPitch);
+#pragma unroll
+    for (int q = 0; q <= (j - 1) / 4; ++q) {
+      const float4 f = row[q];
+      x[2 * q] = fma2(m, make_float2(f.x, f.y), x[2 * q]);
+      if (4 * q + 2 < j) x[2 * q + 1] = fma2(m, make_float2(f.z, f.w), x[2 * q + 1]);
+    }
+  }
+}
+
+template <IO kIO, int KP>
+__global__ void __launch_bounds__(128) delta_prep_kernel(DeltaArgs a) {
+  using T = typename IoType<kIO>::type;
+  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid;
+  constexpr int kTerm = KP * 16384;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* images = align1024(smem_raw);
+  float* sn = reinterpret_cast<float*>(images + PrepSmem<kIO, KP>::kImages);
+  float2* sg = reinterpret_cast<float2*>(sn + 64 * kNPitch);
+  float* sbeta = reinterpret_cast<float*>(sg + 64);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sbeta + 64);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
+
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int kh = blockIdx.x % a.Hk;
+  const int64_t c = blockIdx.x / a.Hk;
+  if (c >= a.info[0]) return;
+  const int4 chunk = a.table[c];
+  const int64_t start = chunk.y;
+  const int len = chunk.z;
+  const int rep = a.Hv / a.Hk;
+
+  if (t == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc<64>(tmem_at);
+
+  // the images of [K; Q]: rows past the chunk's end and columns past K are zero
+  const T* kbase = static_cast<const T*>(a.k) + start * a.sk + (int64_t)kh * a.K;
+  const T* qbase = static_cast<const T*>(a.q) + start * a.sq + (int64_t)kh * a.K;
+  for (int i = t; i < 128 * KP * 8; i += 128) {
+    const int row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
+    uint8_t* image = images + (ch >> 3) * 16384;
+    const T* src = (row < 64 ? kbase + r * a.sk : qbase + r * a.sq) + ch * 8;
+    const bool in = r < len && ch * 8 < a.K;
+    if constexpr (kIO == IO::BF16) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (in) q = *reinterpret_cast<const uint4*>(src);
+      *reinterpret_cast<uint4*>(image + image_chunk<128>(row, ch & 7)) = q;
+    } else {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (in) ld_io8(src, v);
+      put_chunk<NQ, 128>(image, kTerm, row, ch & 7, v);
+    }
+  }
+  fence_async_smem();
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = *tmem_at;
+  if (t == 0) {
+    const Operand<128, kKMajor, NQ, kTerm, 16384> kq(smem_u32(images));
+    umma_terms<64, KP * 4, NQ>(tm, kq, kq, false);  // B: the K rows
+    umma_commit(bar);
+    bulk_store_1d(a.kq + (size_t)(c * a.Hk + kh) * (NQ * kTerm), images, NQ * kTerm);
+    bulk_commit();
+  }
+  Waiter wait{a.wait_ns, a.status};
+  wait(bar, 0);
+  tmem_fence_after_sync();
+
+  for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
+    const int64_t ch = c * a.Hv + h;
+    if (warp == 0) {
+      // the running sum of g, in double: differences of it enter exp
+      float g[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * lane + i;
+        const int64_t at = (start + r) * a.Hv + h;
+        g[i] = r < len ? a.g[at] : 0.0f;
+        b[i] = r < len ? a.beta[at] : 0.0f;
+        g[i] = g[i] < -256.0f ? -256.0f : g[i];  // exp of either is 0; -inf would leave inf - inf
+      }
+      double incl = (double)g[0] + (double)g[1];
+      const double own = incl;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const double last = __shfl_sync(0xffffffffu, incl, 31);
+      const double G[2] = {incl - own + (double)g[0], incl};
+      float* gates = a.gates + ch * kDeltaGates;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * lane + i;
+        const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
+        const float dec = exp_f((float)(last - G[i]));
+        sg[r] = make_float2(hi, lo);
+        sbeta[r] = b[i];
+        gates[r] = exp_f(hi) * (1.0f + lo);
+        gates[64 + r] = dec * b[i];
+        gates[128 + r] = b[i];
+        gates[192 + r] = hi;
+        gates[256 + r] = lo;
+      }
+    }
+    __syncthreads();
+    const int r = t & 63;
+    float2 x[32];
+    {
+      const float2 gi = sg[r];
+      const bool is_k = t < 64;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float d[32];
+        tmem_row<32>(tm + ((uint32_t)(warp * 32) << 16) + half * 32, d);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int j = half * 32 + i;
+          const float2 gj = sg[j];
+          const float w = exp_f((gi.x - gj.x) + (gi.y - gj.y)) * sbeta[j] * d[i];
+          d[i] = (is_k ? j < r : j <= r) ? (is_k ? w : w * a.scale) : 0.0f;
+        }
+        if (is_k) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(sn + r * kNPitch + half * 32 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const int j = half * 32 + i;
+          x[j / 2] = is_k ? make_float2(j == r ? 1.0f : 0.0f, j + 1 == r ? 1.0f : 0.0f) : make_float2(d[i], d[i + 1]);
+        }
+      }
+    }
+    __syncthreads();
+    substitute(x, sn, r, (warp & 1) != 0);
+    uint8_t* out = a.x + (size_t)ch * (NT * 16384);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float v[8] = {x[4 * q].x, x[4 * q].y, x[4 * q + 1].x, x[4 * q + 1].y,
+                          x[4 * q + 2].x, x[4 * q + 2].y, x[4 * q + 3].x, x[4 * q + 3].y};
+      put_chunk<NT, 128>(out, 16384, t, q, v);
+    }
+    __syncthreads();
+  }
+  if (t == 0) bulk_wait_all();
+  tmem_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc<64>(tm);
+}
+
+template <IO kIO, int KP>
+cudaError_t run_prep(const DeltaArgs& a, cudaStream_t st) {
+  constexpr size_t bytes = PrepSmem<kIO, KP>::kBytes;
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_prep_kernel<kIO, KP>), bytes);
+  if (e != cudaSuccess) return e;
+  delta_prep_kernel<kIO, KP><<<(unsigned)(a.max_chunks * a.Hk), 128, bytes, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_plan(const DeltaArgs& a, cudaStream_t st) {
+  int64_t blocks = (a.max_chunks + kPlanThreads - 1) / kPlanThreads;
+  blocks = blocks < 1 ? 1 : blocks > 64 ? 64 : blocks;
+  delta_plan_kernel<<<(unsigned)blocks, kPlanThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_delta_prep(const DeltaArgs& a, IO io, cudaStream_t st) {
+  if (a.max_chunks == 0) return cudaSuccess;
+  const bool two = delta_panels_k(a.K) == 2;
+  if (io == IO::BF16) return two ? run_prep<IO::BF16, 2>(a, st) : run_prep<IO::BF16, 1>(a, st);
+  return two ? run_prep<IO::F32, 2>(a, st) : run_prep<IO::F32, 1>(a, st);
+}
+
+}  // namespace vssm

@@ -31,20 +31,25 @@
 namespace vssm {
 
 constexpr int kDeltaChunk = 64;      // tokens of a chunk
-constexpr int kDeltaGates = 5 * 64;  // floats a chunk and value head keep: exp(G), dec beta, beta, G high, G low
+constexpr int kDeltaGates = 5 * 64;  // floats a chunk and value head keep: exp(G), dec beta, beta, G / ln 2 high, low
 constexpr int kDeltaMaxK = 128, kDeltaMaxV = 1024;
 
-// bf16 terms of an input and of an FP32 intermediate, and the state columns
-// one work item holds.  bf16 inputs are exact in one term and their
-// intermediates carry two (16 bits, far below the rounding of the outputs
-// to bf16, and about 5e-6 on the FP32 ones); FP32 I/O carries three,
+// The state's columns are cut into tiles of 32, the unit in which states and
+// per-token vectors pass from kernel to kernel as images of 64-byte rows.
+constexpr int kDeltaTile = 32;
+constexpr int kRowTile = 64 * 64;  // bytes of one term of 64 token rows of a tile
+
+// bf16 terms of an input and of an FP32 intermediate, the tiles of a walk, and
+// how many chunks of [K; Q] the walks hold.  bf16 inputs are exact in one term
+// and their intermediates carry two (16 bits, far below the rounding of the
+// outputs to bf16, and about 5e-6 on the FP32 ones); FP32 I/O carries three,
 // all 24 bits.
 template <IO kIO> struct DeltaTerms;
-template <> struct DeltaTerms<IO::BF16> { static constexpr int kIn = 1, kMid = 2, kCols = 64, kStages = 2; };
-template <> struct DeltaTerms<IO::F32> { static constexpr int kIn = 3, kMid = 3, kCols = 32, kStages = 1; };
+template <> struct DeltaTerms<IO::BF16> { static constexpr int kIn = 1, kMid = 2, kTiles = 2, kStages = 2; };
+template <> struct DeltaTerms<IO::F32> { static constexpr int kIn = 3, kMid = 3, kTiles = 1, kStages = 1; };
 inline int delta_in_terms(IO io) { return io == IO::BF16 ? 1 : 3; }
 inline int delta_mid_terms(IO io) { return io == IO::BF16 ? 2 : 3; }
-inline int delta_cols(IO io) { return io == IO::BF16 ? 64 : 32; }
+__host__ __device__ inline int delta_tiles(int V) { return (V + kDeltaTile - 1) / kDeltaTile; }
 inline int delta_panels_k(int K) { return (K + 63) / 64; }
 
 struct DeltaArgs {
@@ -70,10 +75,11 @@ struct DeltaArgs {
   float* gates;   // (chunks, Hv, kDeltaGates)
   uint8_t* kq;    // (chunks, Hk, in terms, K panels) images of [K; Q], 128 rows of 64
   uint8_t* x;     // (chunks, Hv, mid terms) images of X, 128 rows of 64
-  uint8_t* s0;    // (chunks, Hv, V panels, mid terms) images of S0, or null
-  uint8_t* e;     // (chunks, Hv, V panels, mid terms) images of E, or null
+  uint8_t* s0;    // (chunks, Hv, tiles, mid terms) images of S0, 64 or 128 rows of a tile, or null
+  uint8_t* e;     // (chunks, Hv, tiles, mid terms) images of E, 64 rows of a tile, or null
   uint8_t* ds;    // bwd: images of dS1, laid out as s0
   uint8_t* dvi;   // bwd: images of dV, laid out as e
+  uint8_t* doi;   // bwd: images of dO, (chunks, Hv, tiles, in terms)
   int* status;
   unsigned long long wait_ns;
   int64_t max_chunks;
@@ -82,6 +88,12 @@ struct DeltaArgs {
 // The most chunks a pack of T tokens in num_seqs sequences can have.
 inline int64_t delta_max_chunks(int64_t T, int64_t num_seqs) {
   return T / kDeltaChunk + (num_seqs < T ? num_seqs : T);
+}
+
+// bf16 walks: two panels (128 columns) to a CTA, unless the panels are so few
+// that one each leaves no SM with two.
+inline bool delta_two_walks(const DeltaArgs& a) {
+  return a.V > 64 && (int64_t)a.num_seqs * a.Hv * ((a.V + 63) / 64) > 152;
 }
 
 cudaError_t launch_delta_plan(const DeltaArgs& a, cudaStream_t st);

@@ -72,14 +72,13 @@ int check_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
   return VSSM_OK;
 }
 
-int check_pack(int64_t T, int32_t S, const int32_t* cu, int32_t Hk, int32_t Hv, int32_t K, int32_t V, IO io) {
+int check_pack(int64_t T, int32_t S, const int32_t* cu, int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
   if (T < 0 || T > 2147483647LL) return bad(VSSM_ERR_ARG, "total_tokens %lld out of range", (long long)T);
   if (S < 0) return bad(VSSM_ERR_ARG, "num_seqs must be >= 0 (got %d)", S);
   if (T > 0 && S < 1) return bad(VSSM_ERR_ARG, "%lld tokens but num_seqs = %d", (long long)T, S);
   if (!cu) return bad(VSSM_ERR_ARG, "cu_seqlens is NULL");
   TRY(check_heads(Hk, Hv, K, V));
-  const int64_t panels = (V + delta_cols(io) - 1) / delta_cols(io);
-  if ((int64_t)S * Hv * panels > 2147483647LL || delta_max_chunks(T, S) * Hk > 2147483647LL)
+  if ((int64_t)S * Hv * delta_tiles(V) > 2147483647LL || delta_max_chunks(T, S) * Hk > 2147483647LL)
     return bad(VSSM_ERR_UNSUPPORTED, "too many sequences, chunks and heads for one call");
   return VSSM_OK;
 }
@@ -88,15 +87,14 @@ int check_pack(int64_t T, int32_t S, const int32_t* cu, int32_t Hk, int32_t Hv, 
 // [info][first chunks][chunk table][gates][images of [K; Q]][images of X], and
 // in a saved array [images of S0][images of E] behind them.
 struct DeltaLayout {
-  size_t first, table, gates, kq, x, plan_end, s0, e, saved_end, ds, dvi, bwd_end;
+  size_t first, table, gates, kq, x, plan_end, s0, e, saved_end, ds, dvi, doi, bwd_end;
 };
 
 DeltaLayout delta_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io) {
   DeltaLayout l;
   const size_t nc = (size_t)delta_max_chunks(T, S);
-  const size_t panels = (V + delta_cols(io) - 1) / delta_cols(io), row = delta_cols(io) * 2;
-  const size_t mid = delta_mid_terms(io), kp = delta_panels_k(K);
-  const size_t states = nc * Hv * panels * mid * kp * 64 * row, rows = nc * Hv * panels * mid * 64 * row;
+  const size_t mid = delta_mid_terms(io), kp = delta_panels_k(K), tiles = nc * Hv * delta_tiles(V);
+  const size_t rows = tiles * mid * kRowTile, states = rows * kp;
   size_t o = 256;
   l.first = o; o += up((S + 1) * sizeof(int));
   l.table = o; o += up(nc * sizeof(int4));
@@ -109,14 +107,15 @@ DeltaLayout delta_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO 
   l.saved_end = o;
   l.ds = 256;
   l.dvi = l.ds + up(states);
-  l.bwd_end = l.dvi + up(rows);
+  l.doi = l.dvi + up(rows);
+  l.bwd_end = l.doi + up(tiles * delta_in_terms(io) * kRowTile);
   return l;
 }
 
 bool sizes_ok(int64_t T, int32_t S, int32_t Hk, int32_t Hv, int32_t K, int32_t V, vssm_dtype dt) {
   IO io;
   const int32_t cu = 0;
-  return check_dtype(dt, &io) == VSSM_OK && check_pack(T, S, &cu, Hk, Hv, K, V, io) == VSSM_OK;
+  return check_dtype(dt, &io) == VSSM_OK && check_pack(T, S, &cu, Hk, Hv, K, V) == VSSM_OK;
 }
 
 void set_plan(DeltaArgs& a, const void* base, const DeltaLayout& l, bool saved) {
@@ -159,7 +158,7 @@ int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t 
   IO io;
   TRY(check_dtype(dtype, &io));
   const int64_t T = total_tokens;
-  TRY(check_pack(T, num_seqs, cu_seqlens, Hk, Hv, K, V, io));
+  TRY(check_pack(T, num_seqs, cu_seqlens, Hk, Hv, K, V));
   TRY(check_ptr(q, "q", T > 0));
   TRY(check_ptr(k, "k", T > 0));
   TRY(check_ptr(v, "v", T > 0));
@@ -203,7 +202,7 @@ int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seql
   IO io;
   TRY(check_dtype(dtype, &io));
   const int64_t T = total_tokens;
-  TRY(check_pack(T, num_seqs, cu_seqlens, Hk, Hv, K, V, io));
+  TRY(check_pack(T, num_seqs, cu_seqlens, Hk, Hv, K, V));
   TRY(check_ptr(dout, "dout", T > 0));
   TRY(check_ptr(dq, "dq", T > 0));
   TRY(check_ptr(dk, "dk", T > 0));
@@ -227,6 +226,7 @@ int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seql
   set_plan(a, saved, l, true);
   a.ds = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.ds);
   a.dvi = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.dvi);
+  a.doi = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.doi);
   TRY(check(cudaMemsetAsync(workspace, 0, 128, st), "clearing the status word"));
   TRY(check(launch_delta_bwd(a, io, st), "gated delta backward launch"));
   TRY(check(launch_delta_grads(a, io, st), "gated delta gradients launch"));

@@ -5,240 +5,303 @@
 namespace vssm {
 namespace {
 
-// One CTA of 256 threads per (sequence, value head, panel of kCols state
-// columns), as the forward walk: dS in registers (FP32) and as bf16 terms in
-// shared memory.  A chunk is
+// CTAs and walks as in the forward.  dS lives in registers (FP32) and as bf16
+// terms in shared memory; a chunk is
 //   D1 = [K; Q] dS1                     rows 0-63, times dec beta, become Z
-//   D2 = X^T [Z; dO] = dV               (64 rows; 64 to 127 are not used)
-//   D3 = [K; Q]^T [-exp(G) dV; scale exp(G) dO] and dS0 = exp(G_63) dS1 + D3
-// Threads of rows 64-127 bring dO in: as it is for D2, and scaled, as the
-// lower half of D3's operand, whose upper half first holds Z.  dS1 of every
-// chunk and dV leave as images for the gradients that need no walk.
-template <IO kIO, int KP>
+//   D2 = (P Tm)^T dO                    beside it
+//   D2 += Tm^T Z = dV                   (64 rows; 64 to 127 are not used)
+//   D1 = [K; Q]^T [-exp(G) dV; scale exp(G) dO] and dS0 = exp(G_63) dS1 + D1
+// sZ holds 128 rows: dO as it is, then Z, then -exp(G) dV in the upper 64, and
+// dO scaled in the lower 64.  dS1, dO and dV of every chunk leave as images
+// for the gradients that need no walk.
+template <IO kIO, int KP, int kWalks>
 struct BwdSmem {
   using D = DeltaTerms<kIO>;
-  static constexpr int kRow = D::kCols * 2;
   static constexpr int kKq = D::kIn * KP * 16384, kX = D::kMid * 16384;
-  static constexpr int kSTerm = KP * 64 * kRow, kRTerm = 64 * kRow, kZTerm = 128 * kRow;
-  static constexpr int oKq = 0, oX = oKq + D::kStages * kKq, oS = oX + D::kStages * kX;
-  static constexpr int oZ = oS + D::kMid * kSTerm, oDo = oZ + D::kMid * kZTerm;
-  static constexpr int oBar = oDo + D::kIn * kRTerm;
+  static constexpr int kSTile = KP * 64 * 64, kSTerm = D::kTiles * kSTile;
+  static constexpr int kZTile = 128 * 64, kZTerm = D::kTiles * kZTile;
+  static constexpr int kS = D::kMid * kSTerm, kZ = D::kMid * kZTerm;
+  static constexpr int oKq = 0, oX = oKq + D::kStages * kKq, oWalk = oX + kX;
+  static constexpr int kWalk = kS + kZ;
+  static constexpr int oBar = oWalk + kWalks * kWalk;
   static constexpr int kBytes = oBar + 128 + 1024;
 };
 
-template <IO kIO, int KP>
-__global__ void __launch_bounds__(256, 1) delta_bwd_kernel(DeltaArgs a) {
+template <IO kIO, int KP, int kWalks>
+__global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
-  using L = BwdSmem<kIO, KP>;
-  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, BV = DeltaTerms<kIO>::kCols,
-                ST = DeltaTerms<kIO>::kStages, HC = BV / 2;
+  using L = BwdSmem<kIO, KP, kWalks>;
+  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, NB = DeltaTerms<kIO>::kTiles,
+                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2;
+  constexpr int kTmemCols = 2 * kWalks * NT * BV > 256 ? 512 : 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);
   uint64_t* x_full = kq_full + ST;
-  uint64_t* done = x_full + ST;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* done_all = x_full + 1;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done_all + kWalks);
+  int* kq_used = reinterpret_cast<int*>(tmem_at + 1);  // walks that are through with what a buffer holds
+  int* x_used = kq_used + ST;
 
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
-  const int row = quad * 32 + lane;
-  const int panels = (a.V + BV - 1) / BV;
-  const int panel = blockIdx.x % panels;
-  const int h = blockIdx.x / panels % a.Hv;
-  const int s = blockIdx.x / panels / a.Hv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int panels = (a.V + BV - 1) / BV, groups = (panels + kWalks - 1) / kWalks;
+  const int group = blockIdx.x % groups;
+  const int h = blockIdx.x / groups % a.Hv;
+  const int s = blockIdx.x / groups / a.Hv;
   if (a.info[0] < 0) return;
   const int c0 = a.first[s], n = a.first[s + 1] - c0;
-  const int col0 = panel * BV + half * HC;
-  const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
+  const int64_t seq_start = a.cu[s], seq_len = a.cu[s + 1] - seq_start;
   const int kh = h / (a.Hv / a.Hk);
+  const int walks = min(kWalks, panels - group * kWalks);
+  if (n == 0 && !a.d_initial) return;
 
-  float S[HC];
-#pragma unroll
-  for (int i = 0; i < HC; ++i) S[i] = 0.0f;
-  if (a.d_final && row < a.K) {
-#pragma unroll
-    for (int i = 0; i < HC; i += 4)
-      if (col0 + i < a.V) {
-        const float4 f = *reinterpret_cast<const float4*>(a.d_final + state_at + i);
-        S[i] = f.x; S[i + 1] = f.y; S[i + 2] = f.z; S[i + 3] = f.w;
-      }
-  }
-
-  if (n > 0) {
-    // i counts the chunks walked: chunk n - 1 - i
-    auto load_kq = [&](int i) {
-      const int st = i % ST;
-      mbar_arrive_expect_tx(&kq_full[st], L::kKq);
-      bulk_load_1d(sm + L::oKq + st * L::kKq, a.kq + ((size_t)(c0 + n - 1 - i) * a.Hk + kh) * L::kKq, L::kKq,
-                   &kq_full[st]);
-    };
-    auto load_x = [&](int i) {
-      const int st = i % ST;
-      mbar_arrive_expect_tx(&x_full[st], L::kX);
-      bulk_load_1d(sm + L::oX + st * L::kX, a.x + ((size_t)(c0 + n - 1 - i) * a.Hv + h) * L::kX, L::kX, &x_full[st]);
-    };
-    if (t == 0) {
-      for (int i = 0; i < ST; ++i) {
-        mbar_init(&kq_full[i], 1);
-        mbar_init(&x_full[i], 1);
-      }
-      mbar_init(done, 1);
-      fence_mbar_init();
-      for (int i = 0; i < ST && i < n; ++i) {
-        load_kq(i);
-        load_x(i);
-      }
+  // i counts the chunks walked: chunk n - 1 - i
+  auto load_kq = [&](int i) {
+    const int st = i % ST;
+    mbar_arrive_expect_tx(&kq_full[st], L::kKq);
+    bulk_load_1d(sm + L::oKq + st * L::kKq, a.kq + ((size_t)(c0 + n - 1 - i) * a.Hk + kh) * L::kKq, L::kKq, &kq_full[st]);
+  };
+  auto load_x = [&](int i) {
+    mbar_arrive_expect_tx(x_full, L::kX);
+    bulk_load_1d(sm + L::oX, a.x + ((size_t)(c0 + n - 1 - i) * a.Hv + h) * L::kX, L::kX, x_full);
+  };
+  // a walk's leader is through with a buffer: the last one may have it filled again
+  auto last_user = [&](int* used) {
+    __threadfence_block();
+    const bool last = (atomicAdd(used, 1) + 1) % walks == 0;
+    __threadfence_block();
+    return last;
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&kq_full[i], 1);
+      kq_used[i] = 0;
     }
-    if (warp == 0) tmem_alloc<256>(tmem_at);
-    if (row < KP * 64) put_row<NT, L::kRow>(sm + L::oS, L::kSTerm, row, half * HC / 8, S);
+    mbar_init(x_full, 1);
+    *x_used = 0;
+    for (int i = 0; i < kWalks; ++i) mbar_init(&done_all[i], 1);
+    fence_mbar_init();
+    for (int i = 0; i < ST && i < n; ++i) load_kq(i);
+    if (n > 0) load_x(0);
+  }
+  if (warp == 0) tmem_alloc<kTmemCols>(tmem_at);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = *tmem_at;
+  Waiter wait{a.wait_ns, a.status};
+
+  if (warp / 8 < walks) {
+    const int walk = warp / 8, quad = warp & 3, half = warp >> 2 & 1;
+    const int row = quad * 32 + lane, r = row & 63;
+    const bool leader = (threadIdx.x & 255) == 0;
+    const int panel = group * kWalks + walk;
+    const int col0 = panel * BV + half * HC;
+    const int tiles = delta_tiles(a.V);
+    const int tile0 = panel * NB;
+    constexpr bool kTileEach = NB == 2;
+    const int in_tile = kTileEach ? half : 0, chunk0 = kTileEach ? 0 : half * HC / 8;
+    uint8_t* sS = sm + L::oWalk + walk * L::kWalk;
+    uint8_t* sZ = sS + L::kS;
+    uint8_t* z_mine = sZ + in_tile * L::kZTile;
+    uint64_t* done = done_all + walk;
+    const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
+    const uint32_t lane_at = ((uint32_t)(quad * 32) << 16) + half * HC;
+    const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
+
+    float S[HC];
+#pragma unroll
+    for (int i = 0; i < HC; ++i) S[i] = 0.0f;
+    if (a.d_final && row < a.K) {
+#pragma unroll
+      for (int i = 0; i < HC; i += 4)
+        if (col0 + i < a.V) {
+          const float4 f = *reinterpret_cast<const float4*>(a.d_final + state_at + i);
+          S[i] = f.x; S[i + 1] = f.y; S[i + 2] = f.z; S[i + 3] = f.w;
+        }
+    }
+    // the next chunk's dO, raw, and gates: read a chunk ahead
+    constexpr int kRaw = HC * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T);
+    uint4 raw[kRaw];
+    float gam, decb, gam_end;
+    auto prefetch = [&](int c) {
+      const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
+      gam = gates[r];
+      decb = gates[64 + r];
+      gam_end = gates[63];
+      const int64_t at = (int64_t)c * kDeltaChunk + r;
+#pragma unroll
+      for (int i = 0; i < kRaw; ++i) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (row >= 64 && at < seq_len && col0 + i * kPer < a.V)
+          raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + ((seq_start + at) * a.Hv + h) * a.V +
+                                                   col0 + i * kPer);
+      }
+    };
+    // rows 64-127: dO into sZ, as it is and scaled
+    auto put_dout = [&]() {
+      float d[HC];
+#pragma unroll
+      for (int i = 0; i < kRaw; ++i) {
+        if constexpr (kIO == IO::BF16) {
+          d[8 * i] = bf16_lo(raw[i].x); d[8 * i + 1] = bf16_hi(raw[i].x); d[8 * i + 2] = bf16_lo(raw[i].y);
+          d[8 * i + 3] = bf16_hi(raw[i].y); d[8 * i + 4] = bf16_lo(raw[i].z); d[8 * i + 5] = bf16_hi(raw[i].z);
+          d[8 * i + 6] = bf16_lo(raw[i].w); d[8 * i + 7] = bf16_hi(raw[i].w);
+        } else {
+          d[4 * i] = __uint_as_float(raw[i].x); d[4 * i + 1] = __uint_as_float(raw[i].y);
+          d[4 * i + 2] = __uint_as_float(raw[i].z); d[4 * i + 3] = __uint_as_float(raw[i].w);
+        }
+      }
+      put_row<NQ, 64>(z_mine, L::kZTerm, r, chunk0, d);
+      const float f = a.scale * gam;
+#pragma unroll
+      for (int i = 0; i < HC; ++i) d[i] *= f;
+      put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0, d);
+    };
+    if (n > 0) {
+      prefetch(n - 1);
+      if (row >= 64) put_dout();
+    }
+    if (row < KP * 64) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
     fence_async_smem();
-    tmem_fence_before_sync();
-    __syncthreads();
-    tmem_fence_after_sync();
-    const uint32_t tm = *tmem_at;
-    const uint32_t mine = tm + ((uint32_t)(quad * 32) << 16) + half * HC;
-    Waiter wait{a.wait_ns, a.status};
+    named_barrier(1 + walk, 256);
     uint32_t phase = 0;
 
     for (int i = 0; i < n; ++i) {
-      const int st = i % ST, parity = (i / ST) & 1;
+      const int st = i % ST, c = n - 1 - i;
       const bool has_state = i > 0 || a.d_final != nullptr;
       const bool last = i + 1 == n;
-      const int64_t c = c0 + n - 1 - i;
-      const int64_t ch = c * a.Hv + h;
-      const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq);
-      if (t == 0) {
-        bulk_store_1d(a.ds + (ch * panels + panel) * (size_t)(NT * L::kSTerm), sm + L::oS, NT * L::kSTerm);
+      const int64_t ch = (int64_t)(c0 + c) * a.Hv + h;
+      const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq), x = smem_u32(sm + L::oX);
+      if (leader) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          if (tile0 + b < tiles)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
+              bulk_store_1d(a.doi + ((ch * tiles + tile0 + b) * NQ + j) * (size_t)kRowTile,
+                            sZ + j * L::kZTerm + b * L::kZTile, kRowTile);
         bulk_commit();
-        wait(&kq_full[st], parity);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          if (tile0 + b < tiles)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              bulk_store_1d(a.ds + ((ch * tiles + tile0 + b) * NT + j) * (size_t)L::kSTile,
+                            sS + j * L::kSTerm + b * L::kSTile, L::kSTile);
+        bulk_commit();
+        wait(&kq_full[st], (i / ST) & 1);
+        tmem_fence_after_sync();
         if (has_state) {
           const Operand<128, kKMajor, NQ, KP * 16384, 16384> A(kq);
-          const Operand<L::kRow, kMnMajor, NT, L::kSTerm> B(smem_u32(sm + L::oS));
-          umma_terms<BV, KP * 4, NT>(tm, A, B, false);
-          umma_commit(done);
+          const Operand<64, kMnMajor, NT, L::kSTerm, 0, L::kSTile> B(smem_u32(sS));
+          umma_blocks<BV, KP * 4, NT, true>(tD1, A, B);
         }
-      }
-      const int4 chunk = a.table[c];
-      const int r = row & 63;
-      const bool valid = r < chunk.z;
-      const int64_t tok = (int64_t)chunk.y + r;
-      const float* gates = a.gates + ch * kDeltaGates;
-      const float gam = gates[r], decb = gates[64 + r], gam_end = gates[63];
-      float d[HC];
-      if (row >= 64) {
-#pragma unroll
-        for (int k = 0; k < HC; ++k) d[k] = 0.0f;
-        if (valid) {
-          const T* p = static_cast<const T*>(a.dout) + (tok * a.Hv + h) * a.V + col0;
-#pragma unroll
-          for (int k = 0; k < HC; k += 8)
-            if (col0 + k < a.V) {
-              float w[8];
-              ld_io8(p + k, w);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) d[k + j] = w[j];
-            }
-        }
-        put_row<NQ, L::kRow>(sm + L::oDo, L::kRTerm, r, half * HC / 8, d);
-        const float f = a.scale * gam;
-#pragma unroll
-        for (int k = 0; k < HC; ++k) d[k] *= f;
-        put_row<NT, L::kRow>(sm + L::oZ, L::kZTerm, row, half * HC / 8, d);
-      }
-      if (has_state) {
-        wait(done, phase);
-        phase ^= 1;
-        tmem_fence_after_sync();
-        if (row < 64) tmem_row<HC>(mine, d);
-      } else if (row < 64) {
-#pragma unroll
-        for (int k = 0; k < HC; ++k) d[k] = 0.0f;
-      }
-      if (row < 64) {
-#pragma unroll
-        for (int k = 0; k < HC; ++k) d[k] *= decb;
-        put_row<NT, L::kRow>(sm + L::oZ, L::kZTerm, row, half * HC / 8, d);
-      }
-      fence_async_smem();
-      tmem_fence_before_sync();
-      __syncthreads();
-      if (t == 0) {
-        tmem_fence_after_sync();
-        wait(&x_full[st], parity);
-        const uint32_t x = smem_u32(sm + L::oX + st * L::kX);
-        // X^T: 64 rows; the instruction's other 64 come from whatever lies 8 KB further and are not read back
-        const Operand<128, kMnMajor, NT, 16384, 0, 8192> A0(x), A1(x + 64 * 128);
-        const Operand<L::kRow, kMnMajor, NT, L::kZTerm> B0(smem_u32(sm + L::oZ));
-        const Operand<L::kRow, kMnMajor, NQ, L::kRTerm> B1(smem_u32(sm + L::oDo));
-        umma_terms<BV, 4, NT>(tm + BV, A0, B0, false);
-        umma_terms<BV, 4, NT>(tm + BV, A1, B1, true);
+        wait(x_full, i & 1);
+        // (P Tm)^T: 64 rows; the instruction's other 64 come from whatever lies 8 KB further and are not read back
+        const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x + 64 * 128);
+        const Operand<64, kMnMajor, NQ, L::kZTerm, 0, L::kZTile> B(smem_u32(sZ));
+        umma_blocks<BV, 4, NT, true>(tD2, A, B);
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // dO's image has left, before Z takes its place
         umma_commit(done);
       }
+      const int64_t at = (int64_t)c * kDeltaChunk + r;
+      const bool valid = at < seq_len;
+      const float g_row = gam, db_row = decb, g_end = gam_end;
+      float d[HC];
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (t == 0 && i + ST < n) load_x(i + ST);
       if (row < 64) {
-        tmem_row<HC>(mine + BV, d);
-        put_row<NT, L::kRow>(a.dvi + (ch * panels + panel) * (size_t)(NT * L::kRTerm), L::kRTerm, row, half * HC / 8, d);
+        if (has_state) {
+          tmem_sum<HC, NT>(tD1 + lane_at, BV, d);
+        } else {
+#pragma unroll
+          for (int k = 0; k < HC; ++k) d[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < HC; ++k) d[k] *= db_row;
+        put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0, d);
+      }
+      fence_async_smem();
+      tmem_fence_before_sync();
+      named_barrier(1 + walk, 256);
+      if (leader) {
+        tmem_fence_after_sync();
+        const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x);
+        const Operand<64, kMnMajor, NT, L::kZTerm, 0, L::kZTile> B(smem_u32(sZ));
+        umma_blocks<BV, 4, NT, false>(tD2, A, B);
+        umma_commit(done);
+      }
+      if (!last) prefetch(c - 1);
+      wait(done, phase);
+      phase ^= 1;
+      tmem_fence_after_sync();
+      if (leader && i + 1 < n && last_user(x_used)) load_x(i + 1);
+      if (row < 64) {
+        tmem_sum<HC, NT>(tD2 + lane_at, BV, d);
+        const int tile = tile0 + in_tile;
+        if (tile < tiles)
+          put_row<NT, 64>(a.dvi + (ch * tiles + tile) * (size_t)(NT * kRowTile), kRowTile, row, chunk0, d);
         if (valid) {
-          T* p = static_cast<T*>(a.dv) + (tok * a.Hv + h) * a.V + col0;
+          T* p = static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0;
 #pragma unroll
           for (int k = 0; k < HC; k += 8)
             if (col0 + k < a.V) st_io8(p + k, d + k);
         }
 #pragma unroll
-        for (int k = 0; k < HC; ++k) d[k] *= -gam;
-        put_row<NT, L::kRow>(sm + L::oZ, L::kZTerm, row, half * HC / 8, d);
+        for (int k = 0; k < HC; ++k) d[k] *= -g_row;
+        put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0, d);
       }
       if (last && !a.d_initial) break;
       fence_async_smem();
       tmem_fence_before_sync();
-      if (t == 0) bulk_wait_read();
-      __syncthreads();
-      if (t == 0) {
+      if (leader) bulk_wait_read();
+      named_barrier(1 + walk, 256);
+      if (leader) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);
-        const Operand<L::kRow, kMnMajor, NT, L::kZTerm> B(smem_u32(sm + L::oZ));
-        umma_terms<BV, 8, NT>(tm + 2 * BV, A, B, false);
+        const Operand<64, kMnMajor, NT, L::kZTerm, 0, L::kZTile> B(smem_u32(sZ));
+        umma_blocks<BV, 8, NT, true>(tD1, A, B);
         umma_commit(done);
       }
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (t == 0 && i + ST < n) load_kq(i + ST);
-      tmem_row<HC>(mine + 2 * BV, d);
+      if (leader && i + ST < n && last_user(&kq_used[st])) load_kq(i + ST);
+      tmem_sum<HC, NT>(tD1 + lane_at, BV, d);
       if (row < KP * 64) {
 #pragma unroll
-        for (int k = 0; k < HC; ++k) S[k] = fmaf(gam_end, S[k], d[k]);
-        if (!last) put_row<NT, L::kRow>(sm + L::oS, L::kSTerm, row, half * HC / 8, S);
+        for (int k = 0; k < HC; ++k) S[k] = fmaf(g_end, S[k], d[k]);
+        if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
       }
+      if (!last && row >= 64) put_dout();
       fence_async_smem();
       tmem_fence_before_sync();
-      __syncthreads();
-      if (t == 0) tmem_fence_after_sync();
+      named_barrier(1 + walk, 256);
     }
-    if (t == 0) bulk_wait_all();
-    tmem_fence_before_sync();
-    __syncthreads();
-    if (warp == 0) tmem_dealloc<256>(tm);
-  }
-
-  if (a.d_initial && row < a.K) {
+    if (leader) bulk_wait_all();
+    if (a.d_initial && row < a.K) {
 #pragma unroll
-    for (int i = 0; i < HC; i += 4)
-      if (col0 + i < a.V)
-        *reinterpret_cast<float4*>(a.d_initial + state_at + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      for (int i = 0; i < HC; i += 4)
+        if (col0 + i < a.V)
+          *reinterpret_cast<float4*>(a.d_initial + state_at + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+    }
   }
+  tmem_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc<kTmemCols>(tm);
 }
 
-template <IO kIO, int KP>
+template <IO kIO, int KP, int kWalks>
 cudaError_t run_bwd(const DeltaArgs& a, cudaStream_t st) {
-  constexpr size_t bytes = BwdSmem<kIO, KP>::kBytes;
+  constexpr size_t bytes = BwdSmem<kIO, KP, kWalks>::kBytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_bwd_kernel<kIO, KP>), bytes);
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_bwd_kernel<kIO, KP, kWalks>), bytes);
   if (e != cudaSuccess) return e;
-  const int panels = (a.V + DeltaTerms<kIO>::kCols - 1) / DeltaTerms<kIO>::kCols;
-  delta_bwd_kernel<kIO, KP><<<(unsigned)((int64_t)a.num_seqs * a.Hv * panels), 256, bytes, st>>>(a);
+  const int cols = DeltaTerms<kIO>::kTiles * kDeltaTile * kWalks;
+  delta_bwd_kernel<kIO, KP, kWalks>
+      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * ((a.V + cols - 1) / cols)), 256 * kWalks, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -247,8 +310,11 @@ cudaError_t run_bwd(const DeltaArgs& a, cudaStream_t st) {
 cudaError_t launch_delta_bwd(const DeltaArgs& a, IO io, cudaStream_t st) {
   if (a.num_seqs == 0) return cudaSuccess;
   const bool two = delta_panels_k(a.K) == 2;
-  if (io == IO::BF16) return two ? run_bwd<IO::BF16, 2>(a, st) : run_bwd<IO::BF16, 1>(a, st);
-  return two ? run_bwd<IO::F32, 2>(a, st) : run_bwd<IO::F32, 1>(a, st);
+  if (io == IO::BF16) {
+    if (delta_two_walks(a)) return two ? run_bwd<IO::BF16, 2, 2>(a, st) : run_bwd<IO::BF16, 1, 2>(a, st);
+    return two ? run_bwd<IO::BF16, 2, 1>(a, st) : run_bwd<IO::BF16, 1, 1>(a, st);
+  }
+  return two ? run_bwd<IO::F32, 2, 1>(a, st) : run_bwd<IO::F32, 1, 1>(a, st);
 }
 
 }  // namespace vssm

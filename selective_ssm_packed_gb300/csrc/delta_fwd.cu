@@ -4,235 +4,298 @@
 namespace vssm {
 namespace {
 
-// One CTA of 256 threads per (sequence, value head, panel of kCols state
-// columns; the columns of S never mix).  The state lives in registers (FP32,
-// thread = one row, half a panel) and as bf16 terms in shared memory.  A chunk
-// is three products on the matrix unit, each read back from tensor memory by
-// all threads (warp w: lanes 32 (w % 4) .., column half w / 4):
-//   D1 = [K; Q] S0        rows 0-63 become R, rows 64-127 wait as exp(G) Q S0
-//   D2 = [Tm; P Tm] R     rows 0-63 are E, rows 64-127 finish O
-//   D3 = K^T (dec beta E) and S1 = exp(G_63) S0 + D3
-// The images of [K; Q] and X arrive by bulk copies, kStages ahead.  bf16 I/O
-// holds 160 KB of shared memory and FP32 I/O 180 KB, so one CTA has the SM.
-template <IO kIO, int KP>
+// One CTA per (sequence, value head, kWalks panels of the state's columns; the
+// columns never mix).  A walk is 256 threads and one panel of kTiles tiles:
+// the state lives in registers (FP32; thread = one row, half a panel) and as
+// bf16 terms in shared memory.  A chunk is three products on the matrix unit,
+// each read back from tensor memory by the walk's threads (warp w: lanes
+// 32 (w % 4) .., column half w / 4 % 2):
+//   D = [K; Q] S0        rows 0-63 become R, rows 64-127 wait as exp(G) Q S0
+//   D = [Tm; P Tm] R     rows 0-63 are E, rows 64-127 finish O
+//   D = K^T (dec beta E) and S1 = exp(G_63) S0 + D
+// The chain product - read back - product bounds a walk, not the matrix unit,
+// so two walks share a CTA (and its [K; Q] and X) where there are enough
+// CTAs to fill the GPU: one multiplies while the other reads back.  [K; Q] and
+// X come by bulk copies, ahead of the walks, asked for by whichever walk is
+// through with the buffer last.
+template <IO kIO, int KP, int kWalks>
 struct FwdSmem {
   using D = DeltaTerms<kIO>;
-  static constexpr int kRow = D::kCols * 2;  // bytes of an image row of a panel
   static constexpr int kKq = D::kIn * KP * 16384, kX = D::kMid * 16384;
-  static constexpr int kSTerm = KP * 64 * kRow, kRTerm = 64 * kRow;
-  static constexpr int oKq = 0, oX = oKq + D::kStages * kKq, oS = oX + D::kStages * kX;
-  static constexpr int oR = oS + D::kMid * kSTerm, oBar = oR + D::kMid * kRTerm;
+  static constexpr int kSTile = KP * 64 * 64, kSTerm = D::kTiles * kSTile, kRTerm = D::kTiles * kRowTile;
+  static constexpr int kS = D::kMid * kSTerm, kR = D::kMid * kRTerm;
+  static constexpr int oKq = 0, oX = oKq + D::kStages * kKq, oWalk = oX + kX;
+  static constexpr int kWalk = kS + 2 * kR;  // S, R, E
+  static constexpr int oBar = oWalk + kWalks * kWalk;
   static constexpr int kBytes = oBar + 128 + 1024;
 };
 
-template <IO kIO, int KP>
-__global__ void __launch_bounds__(256, 1) delta_fwd_kernel(DeltaArgs a) {
+template <IO kIO, int KP, int kWalks>
+__global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
-  using L = FwdSmem<kIO, KP>;
-  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, BV = DeltaTerms<kIO>::kCols,
-                ST = DeltaTerms<kIO>::kStages, HC = BV / 2;
+  using L = FwdSmem<kIO, KP, kWalks>;
+  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, NB = DeltaTerms<kIO>::kTiles,
+                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2;
+  constexpr int kTmemCols = kWalks * NT * BV > 128 ? 256 : 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);
   uint64_t* x_full = kq_full + ST;
-  uint64_t* done = x_full + ST;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* done_all = x_full + 1;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done_all + kWalks);
+  int* kq_used = reinterpret_cast<int*>(tmem_at + 1);  // walks that are through with what a buffer holds
+  int* x_used = kq_used + ST;
 
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
-  const int row = quad * 32 + lane;  // of a product: token (K rows, then Q rows) or state row
-  const int panels = (a.V + BV - 1) / BV;
-  const int panel = blockIdx.x % panels;
-  const int h = blockIdx.x / panels % a.Hv;
-  const int s = blockIdx.x / panels / a.Hv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int panels = (a.V + BV - 1) / BV, groups = (panels + kWalks - 1) / kWalks;
+  const int group = blockIdx.x % groups;
+  const int h = blockIdx.x / groups % a.Hv;
+  const int s = blockIdx.x / groups / a.Hv;
   if (a.info[0] < 0) return;
   const int c0 = a.first[s], n = a.first[s + 1] - c0;
-  const int col0 = panel * BV + half * HC;  // this thread's first state column
-  const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
+  const int64_t seq_start = a.cu[s], seq_len = a.cu[s + 1] - seq_start;
   const int kh = h / (a.Hv / a.Hk);
+  const int walks = min(kWalks, panels - group * kWalks);  // panels there are for this CTA
+  if (n == 0 && !a.final_states) return;
 
-  float S[HC];
-#pragma unroll
-  for (int i = 0; i < HC; ++i) S[i] = 0.0f;
-  if (a.initial && row < a.K) {
-#pragma unroll
-    for (int i = 0; i < HC; i += 4)
-      if (col0 + i < a.V) {
-        const float4 f = *reinterpret_cast<const float4*>(a.initial + state_at + i);
-        S[i] = f.x; S[i + 1] = f.y; S[i + 2] = f.z; S[i + 3] = f.w;
-      }
-  }
-
-  if (n > 0) {
-    auto load_kq = [&](int c) {
-      const int st = c % ST;
-      mbar_arrive_expect_tx(&kq_full[st], L::kKq);
-      bulk_load_1d(sm + L::oKq + st * L::kKq, a.kq + ((size_t)(c0 + c) * a.Hk + kh) * L::kKq, L::kKq, &kq_full[st]);
-    };
-    auto load_x = [&](int c) {
-      const int st = c % ST;
-      mbar_arrive_expect_tx(&x_full[st], L::kX);
-      bulk_load_1d(sm + L::oX + st * L::kX, a.x + ((size_t)(c0 + c) * a.Hv + h) * L::kX, L::kX, &x_full[st]);
-    };
-    if (t == 0) {
-      for (int i = 0; i < ST; ++i) {
-        mbar_init(&kq_full[i], 1);
-        mbar_init(&x_full[i], 1);
-      }
-      mbar_init(done, 1);
-      fence_mbar_init();
-      for (int c = 0; c < ST && c < n; ++c) {
-        load_kq(c);
-        load_x(c);
-      }
+  auto load_kq = [&](int c) {
+    const int st = c % ST;
+    mbar_arrive_expect_tx(&kq_full[st], L::kKq);
+    bulk_load_1d(sm + L::oKq + st * L::kKq, a.kq + ((size_t)(c0 + c) * a.Hk + kh) * L::kKq, L::kKq, &kq_full[st]);
+  };
+  auto load_x = [&](int c) {
+    mbar_arrive_expect_tx(x_full, L::kX);
+    bulk_load_1d(sm + L::oX, a.x + ((size_t)(c0 + c) * a.Hv + h) * L::kX, L::kX, x_full);
+  };
+  // a walk's leader is through with a buffer: the last one may have it filled again
+  auto last_user = [&](int* used) {
+    __threadfence_block();
+    const bool last = (atomicAdd(used, 1) + 1) % walks == 0;
+    __threadfence_block();
+    return last;
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&kq_full[i], 1);
+      kq_used[i] = 0;
     }
-    if (warp == 0) tmem_alloc<256>(tmem_at);
-    if (row < KP * 64) put_row<NT, L::kRow>(sm + L::oS, L::kSTerm, row, half * HC / 8, S);
+    mbar_init(x_full, 1);
+    *x_used = 0;
+    for (int i = 0; i < kWalks; ++i) mbar_init(&done_all[i], 1);
+    fence_mbar_init();
+    for (int i = 0; i < ST && i < n; ++i) load_kq(i);
+    if (n > 0) load_x(0);
+  }
+  if (warp == 0) tmem_alloc<kTmemCols>(tmem_at);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = *tmem_at;
+  Waiter wait{a.wait_ns, a.status};
+
+  if (warp / 8 < walks) {
+    const int walk = warp / 8, quad = warp & 3, half = warp >> 2 & 1;
+    const int row = quad * 32 + lane, r = row & 63;  // of a product: token (K rows, then Q rows) or state row
+    const bool leader = (threadIdx.x & 255) == 0;
+    const int panel = group * kWalks + walk;
+    const int col0 = panel * BV + half * HC;  // this thread's first state column
+    const int tiles = delta_tiles(a.V);
+    const int tile0 = panel * NB;
+    // where this thread's columns lie in an image of a panel: tile and first 16-byte chunk
+    constexpr bool kTileEach = NB == 2;  // a half panel is a tile, or half a tile
+    const int in_tile = kTileEach ? half : 0, chunk0 = kTileEach ? 0 : half * HC / 8;
+    uint8_t* sS = sm + L::oWalk + walk * L::kWalk;
+    uint8_t* sR = sS + L::kS;
+    uint8_t* sE = sR + L::kR;
+    uint64_t* done = done_all + walk;
+    const uint32_t tD = tm + walk * NT * BV;
+    const uint32_t mine = tD + ((uint32_t)(quad * 32) << 16) + half * HC;
+    const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
+
+    float S[HC];
+#pragma unroll
+    for (int i = 0; i < HC; ++i) S[i] = 0.0f;
+    if (a.initial && row < a.K) {
+#pragma unroll
+      for (int i = 0; i < HC; i += 4)
+        if (col0 + i < a.V) {
+          const float4 f = *reinterpret_cast<const float4*>(a.initial + state_at + i);
+          S[i] = f.x; S[i + 1] = f.y; S[i + 2] = f.z; S[i + 3] = f.w;
+        }
+    }
+    // the next chunk's v, raw, and gates: read a chunk ahead
+    constexpr int kRaw = HC * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T);
+    uint4 raw[kRaw];
+    float gam, decb, gam_end;
+    auto prefetch = [&](int c) {
+      const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
+      gam = gates[r];
+      decb = gates[64 + r];
+      gam_end = gates[63];
+      const int64_t at = (int64_t)c * kDeltaChunk + r;
+#pragma unroll
+      for (int i = 0; i < kRaw; ++i) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (row < 64 && at < seq_len && col0 + i * kPer < a.V)
+          raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + (seq_start + at) * a.sv + (int64_t)h * a.V +
+                                                   col0 + i * kPer);
+      }
+    };
+    if (n > 0) prefetch(0);
+    if (row < KP * 64) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
     fence_async_smem();
-    tmem_fence_before_sync();
-    __syncthreads();
-    tmem_fence_after_sync();
-    const uint32_t tm = *tmem_at;
-    const uint32_t mine = tm + ((uint32_t)(quad * 32) << 16) + half * HC;
-    Waiter wait{a.wait_ns, a.status};
+    named_barrier(1 + walk, 256);
     uint32_t phase = 0;
 
     for (int c = 0; c < n; ++c) {
-      const int st = c % ST, parity = (c / ST) & 1;
+      const int st = c % ST;
       const bool has_state = c > 0 || a.initial != nullptr;
       const bool last = c + 1 == n;
       const int64_t ch = (int64_t)(c0 + c) * a.Hv + h;
       const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq);
-      if (t == 0) {
+      if (leader) {
         if (a.s0) {
-          bulk_store_1d(a.s0 + (ch * panels + panel) * (size_t)(NT * L::kSTerm), sm + L::oS, NT * L::kSTerm);
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            if (tile0 + i < tiles)
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+                bulk_store_1d(a.s0 + ((ch * tiles + tile0 + i) * NT + j) * (size_t)L::kSTile,
+                              sS + j * L::kSTerm + i * L::kSTile, L::kSTile);
           bulk_commit();
         }
-        wait(&kq_full[st], parity);
+        wait(&kq_full[st], (c / ST) & 1);
+        tmem_fence_after_sync();
         if (has_state) {
           const Operand<128, kKMajor, NQ, KP * 16384, 16384> A(kq);
-          const Operand<L::kRow, kMnMajor, NT, L::kSTerm> B(smem_u32(sm + L::oS));
-          umma_terms<BV, KP * 4, NT>(tm, A, B, false);
+          const Operand<64, kMnMajor, NT, L::kSTerm, 0, L::kSTile> B(smem_u32(sS));
+          umma_blocks<BV, KP * 4, NT, true>(tD, A, B);
           umma_commit(done);
         }
       }
-      // while that runs: the chunk's gates and this row's v
-      const int4 chunk = a.table[c0 + c];
-      const int r = row & 63;
-      const bool valid = r < chunk.z;
-      const int64_t tok = (int64_t)chunk.y + r;
-      const float* gates = a.gates + ch * kDeltaGates;
-      const float gam = gates[r], decb = gates[64 + r], gam_end = gates[63];
-      float v[HC];
-#pragma unroll
-      for (int i = 0; i < HC; ++i) v[i] = 0.0f;
-      if (row < 64 && valid) {
-        const T* vp = static_cast<const T*>(a.v) + tok * a.sv + (int64_t)h * a.V + col0;
-#pragma unroll
-        for (int i = 0; i < HC; i += 8)
-          if (col0 + i < a.V) {
-            float w[8];
-            ld_io8(vp + i, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i + j] = w[j];
-          }
-      }
-      float d[HC];
+      const int64_t at = (int64_t)c * kDeltaChunk + r;
+      const bool valid = at < seq_len;
+      const float g_row = gam, db_row = decb, g_end = gam_end;
+      float d[HC], o[HC];
       if (has_state) {
         wait(done, phase);
         phase ^= 1;
         tmem_fence_after_sync();
-        tmem_row<HC>(mine, d);
+        tmem_sum<HC, NT>(mine, BV, d);
       } else {
 #pragma unroll
         for (int i = 0; i < HC; ++i) d[i] = 0.0f;
       }
       if (row < 64) {
 #pragma unroll
-        for (int i = 0; i < HC; ++i) v[i] = valid ? fmaf(-gam, d[i], v[i]) : 0.0f;
-        put_row<NT, L::kRow>(sm + L::oR, L::kRTerm, row, half * HC / 8, v);
+        for (int i = 0; i < kRaw; ++i) {
+          float w[kPer];
+          if constexpr (kIO == IO::BF16) {
+            w[0] = bf16_lo(raw[i].x); w[1] = bf16_hi(raw[i].x); w[2] = bf16_lo(raw[i].y); w[3] = bf16_hi(raw[i].y);
+            w[4] = bf16_lo(raw[i].z); w[5] = bf16_hi(raw[i].z); w[6] = bf16_lo(raw[i].w); w[7] = bf16_hi(raw[i].w);
+          } else {
+            w[0] = __uint_as_float(raw[i].x); w[1] = __uint_as_float(raw[i].y);
+            w[2] = __uint_as_float(raw[i].z); w[3] = __uint_as_float(raw[i].w);
+          }
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) d[i * kPer + j] = valid ? fmaf(-g_row, d[i * kPer + j], w[j]) : 0.0f;
+        }
+        put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0, d);
       } else {
 #pragma unroll
-        for (int i = 0; i < HC; ++i) v[i] = a.scale * gam * d[i];
+        for (int i = 0; i < HC; ++i) o[i] = a.scale * g_row * d[i];
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      __syncthreads();
-      if (t == 0) {
+      if (leader && a.s0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last chunk's E has left
+      named_barrier(1 + walk, 256);
+      if (leader) {
         tmem_fence_after_sync();
-        wait(&x_full[st], parity);
-        const Operand<128, kKMajor, NT, 16384> A(smem_u32(sm + L::oX + st * L::kX));
-        const Operand<L::kRow, kMnMajor, NT, L::kRTerm> B(smem_u32(sm + L::oR));
-        umma_terms<BV, 4, NT>(tm + BV, A, B, false);
+        wait(x_full, c & 1);
+        const Operand<128, kKMajor, NT, 16384> A(smem_u32(sm + L::oX));
+        const Operand<64, kMnMajor, NT, L::kRTerm, 0, kRowTile> B(smem_u32(sR));
+        umma_blocks<BV, 4, NT, true>(tD, A, B);
         umma_commit(done);
       }
+      if (!last) prefetch(c + 1);
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (t == 0 && c + ST < n) load_x(c + ST);
-      tmem_row<HC>(mine + BV, d);
+      if (leader && c + 1 < n && last_user(x_used)) load_x(c + 1);
+      tmem_sum<HC, NT>(mine, BV, d);
       if (row < 64) {
-        if (a.e)
-          put_row<NT, L::kRow>(a.e + (ch * panels + panel) * (size_t)(NT * L::kRTerm), L::kRTerm, row, half * HC / 8, d);
+        if (a.e) put_row<NT, 64>(sE + in_tile * kRowTile, L::kRTerm, row, chunk0, d);
 #pragma unroll
-        for (int i = 0; i < HC; ++i) d[i] *= decb;
-        put_row<NT, L::kRow>(sm + L::oR, L::kRTerm, row, half * HC / 8, d);
+        for (int i = 0; i < HC; ++i) d[i] *= db_row;
+        put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0, d);
       } else if (valid) {
-        T* op = static_cast<T*>(a.out) + (tok * a.Hv + h) * a.V + col0;
+        T* op = static_cast<T*>(a.out) + ((seq_start + at) * a.Hv + h) * a.V + col0;
 #pragma unroll
-        for (int i = 0; i < HC; ++i) v[i] += d[i];
+        for (int i = 0; i < HC; ++i) o[i] += d[i];
 #pragma unroll
         for (int i = 0; i < HC; i += 8)
-          if (col0 + i < a.V) st_io8(op + i, v + i);
+          if (col0 + i < a.V) st_io8(op + i, o + i);
       }
-      if (last && !a.final_states) break;
+      const bool stop = last && !a.final_states;
+      if (stop && !a.e) break;
       fence_async_smem();
       tmem_fence_before_sync();
-      if (t == 0) bulk_wait_read();  // S0's images are free to be overwritten
-      __syncthreads();
-      if (t == 0) {
+      if (leader) bulk_wait_read();  // S0's images are free to be overwritten
+      named_barrier(1 + walk, 256);
+      if (leader && a.e) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          if (tile0 + i < tiles)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              bulk_store_1d(a.e + ((ch * tiles + tile0 + i) * NT + j) * (size_t)kRowTile,
+                            sE + j * L::kRTerm + i * kRowTile, kRowTile);
+        bulk_commit();
+      }
+      if (stop) break;
+      if (leader) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);  // K^T: the first 64 rows
-        const Operand<L::kRow, kMnMajor, NT, L::kRTerm> B(smem_u32(sm + L::oR));
-        umma_terms<BV, 4, NT>(tm + 2 * BV, A, B, false);
+        const Operand<64, kMnMajor, NT, L::kRTerm, 0, kRowTile> B(smem_u32(sR));
+        umma_blocks<BV, 4, NT, true>(tD, A, B);
         umma_commit(done);
       }
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (t == 0 && c + ST < n) load_kq(c + ST);
-      tmem_row<HC>(mine + 2 * BV, d);
+      if (leader && c + ST < n && last_user(&kq_used[st])) load_kq(c + ST);
+      tmem_sum<HC, NT>(mine, BV, d);
       if (row < KP * 64) {
 #pragma unroll
-        for (int i = 0; i < HC; ++i) S[i] = fmaf(gam_end, S[i], d[i]);
-        if (!last) put_row<NT, L::kRow>(sm + L::oS, L::kSTerm, row, half * HC / 8, S);
+        for (int i = 0; i < HC; ++i) S[i] = fmaf(g_end, S[i], d[i]);
+        if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      __syncthreads();
-      if (t == 0) tmem_fence_after_sync();
+      named_barrier(1 + walk, 256);
     }
-    if (t == 0) bulk_wait_all();
-    tmem_fence_before_sync();
-    __syncthreads();
-    if (warp == 0) tmem_dealloc<256>(tm);
-  }
-
-  if (a.final_states && row < a.K) {
+    if (leader) bulk_wait_all();
+    if (a.final_states && row < a.K) {
 #pragma unroll
-    for (int i = 0; i < HC; i += 4)
-      if (col0 + i < a.V)
-        *reinterpret_cast<float4*>(a.final_states + state_at + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      for (int i = 0; i < HC; i += 4)
+        if (col0 + i < a.V)
+          *reinterpret_cast<float4*>(a.final_states + state_at + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+    }
   }
+  tmem_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc<kTmemCols>(tm);
 }
 
-template <IO kIO, int KP>
+template <IO kIO, int KP, int kWalks>
 cudaError_t run_fwd(const DeltaArgs& a, cudaStream_t st) {
-  constexpr size_t bytes = FwdSmem<kIO, KP>::kBytes;
+  constexpr size_t bytes = FwdSmem<kIO, KP, kWalks>::kBytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_fwd_kernel<kIO, KP>), bytes);
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_fwd_kernel<kIO, KP, kWalks>), bytes);
   if (e != cudaSuccess) return e;
-  const int panels = (a.V + DeltaTerms<kIO>::kCols - 1) / DeltaTerms<kIO>::kCols;
-  delta_fwd_kernel<kIO, KP><<<(unsigned)((int64_t)a.num_seqs * a.Hv * panels), 256, bytes, st>>>(a);
+  const int cols = DeltaTerms<kIO>::kTiles * kDeltaTile * kWalks;
+  delta_fwd_kernel<kIO, KP, kWalks>
+      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * ((a.V + cols - 1) / cols)), 256 * kWalks, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -241,8 +304,11 @@ cudaError_t run_fwd(const DeltaArgs& a, cudaStream_t st) {
 cudaError_t launch_delta_fwd(const DeltaArgs& a, IO io, cudaStream_t st) {
   if (a.num_seqs == 0) return cudaSuccess;
   const bool two = delta_panels_k(a.K) == 2;
-  if (io == IO::BF16) return two ? run_fwd<IO::BF16, 2>(a, st) : run_fwd<IO::BF16, 1>(a, st);
-  return two ? run_fwd<IO::F32, 2>(a, st) : run_fwd<IO::F32, 1>(a, st);
+  if (io == IO::BF16) {
+    if (delta_two_walks(a)) return two ? run_fwd<IO::BF16, 2, 2>(a, st) : run_fwd<IO::BF16, 1, 2>(a, st);
+    return two ? run_fwd<IO::BF16, 2, 1>(a, st) : run_fwd<IO::BF16, 1, 1>(a, st);
+  }
+  return two ? run_fwd<IO::F32, 2, 1>(a, st) : run_fwd<IO::F32, 1, 1>(a, st);
 }
 
 }  // namespace vssm

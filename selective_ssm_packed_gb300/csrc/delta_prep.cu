@@ -70,38 +70,33 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
 // ------------------------------------------------------------------ prep
 // One CTA of 128 threads per chunk and key head; the value heads that share
 // the key head follow each other.  Thread r < 64 owns row r of K K^T, N and
-// Tm, thread 64 + r row r of Q K^T, P and P Tm: both halves of X solve
-// X (I + N) = [I; P] by substitution from the last column, x_j final, then
-// x_l -= x_j N_jl for l < j, with the row in registers and N read from shared
-// memory as one broadcast for the whole warp.  Substitution is taken over
-// summing powers of N because those grow without bound for keys that
-// resemble each other, while the entries of Tm do not.
-constexpr int kNPitch = 68;  // floats a row of N: 16-byte writes of a warp's rows hit all banks
+// Tm, thread 64 + r row r of Q K^T, P and P Tm.
+// Tm = (I + N)^-1 row by row, by substitution from the last column: x starts as
+// a row of I, x_j is final, then x_l -= x_j N_jl for l < j, with the row in
+// registers and N read from shared memory as one broadcast for the whole
+// warp.  Substitution is taken over summing powers of N because those grow
+// without bound for keys that resemble each other, while the entries of Tm do
+// not.  Rows 32-63 take four times the work of rows 0-31, and the remaining
+// warps none, so the CTAs of an SM give the long part to different warps.
+// P Tm is a product on the matrix unit, from and into X's own images.
+// Four CTAs fit an SM, so that one's substitution hides another's waits.
+constexpr int kNPitch = 68;    // floats a row of N: 16-byte writes of a warp's rows hit all banks
+constexpr int kPrepHeads = 4;  // value heads whose gates are made at once, one a warp
 
 template <IO kIO, int KP>
 struct PrepSmem {
-  static constexpr int kImages = DeltaTerms<kIO>::kIn * KP * 16384;
-  static constexpr int kBytes = kImages + 64 * kNPitch * 4 + 64 * 8 + 64 * 4 + 64 + 1024;
+  using D = DeltaTerms<kIO>;
+  static constexpr int kKq = D::kIn * KP * 16384, kX = D::kMid * 16384;
+  static constexpr int kImages = kKq > kX ? kKq : kX;  // [K; Q], later X
+  static constexpr int oN = kImages, oG = oN + 64 * kNPitch * 4, oBeta = oG + kPrepHeads * 64 * 8;
+  static constexpr int oBar = oBeta + kPrepHeads * 64 * 4;
+  static constexpr int kBytes = oBar + 64 + 1024;
 };
 
-__device__ __forceinline__ void substitute(float2 (&x)[32], const float* n, int from_row, bool upper) {
-  (void)from_row;
-  if (upper) {
+template <int kFrom, int kTo>
+__device__ __forceinline__ void substitute(float2 (&x)[32], const float* n) {
 #pragma unroll
-    for (int j = 63; j >= 32; --j) {
-      const float xj = (j & 1) ? x[j / 2].y : x[j / 2].x;
-      const float2 m = splat2(-xj);
-      const float4* row = reinterpret_cast<const float4*>(n + j * kNPitch);
-#pragma unroll
-      for (int q = 0; q <= (j - 1) / 4; ++q) {
-        const float4 f = row[q];
-        x[2 * q] = fma2(m, make_float2(f.x, f.y), x[2 * q]);
-        if (4 * q + 2 < j) x[2 * q + 1] = fma2(m, make_float2(f.z, f.w), x[2 * q + 1]);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 31; j >= 1; --j) {
+  for (int j = kFrom; j >= kTo; --j) {
     const float xj = (j & 1) ? x[j / 2].y : x[j / 2].x;
     const float2 m = splat2(-xj);
     const float4* row = reinterpret_cast<const float4*>(n + j * kNPitch);
@@ -115,16 +110,17 @@ __device__ __forceinline__ void substitute(float2 (&x)[32], const float* n, int 
 }
 
 template <IO kIO, int KP>
-__global__ void __launch_bounds__(128) delta_prep_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
+  using L = PrepSmem<kIO, KP>;
   constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid;
   constexpr int kTerm = KP * 16384;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* images = align1024(smem_raw);
-  float* sn = reinterpret_cast<float*>(images + PrepSmem<kIO, KP>::kImages);
-  float2* sg = reinterpret_cast<float2*>(sn + 64 * kNPitch);
-  float* sbeta = reinterpret_cast<float*>(sg + 64);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sbeta + 64);
+  float* sn = reinterpret_cast<float*>(images + L::oN);
+  float2* sg_all = reinterpret_cast<float2*>(images + L::oG);  // running sum of g over ln 2, in two floats
+  float* sbeta_all = reinterpret_cast<float*>(images + L::oBeta);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(images + L::oBar);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -140,11 +136,12 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaArgs a) {
     mbar_init(bar, 1);
     fence_mbar_init();
   }
-  if (warp == 0) tmem_alloc<64>(tmem_at);
+  if (warp == 0) tmem_alloc<128>(tmem_at);
 
   // the images of [K; Q]: rows past the chunk's end and columns past K are zero
   const T* kbase = static_cast<const T*>(a.k) + start * a.sk + (int64_t)kh * a.K;
   const T* qbase = static_cast<const T*>(a.q) + start * a.sq + (int64_t)kh * a.K;
+#pragma unroll 4
   for (int i = t; i < 128 * KP * 8; i += 128) {
     const int row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
     uint8_t* image = images + (ch >> 3) * 16384;
@@ -165,26 +162,28 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaArgs a) {
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tm = *tmem_at;
+  const uint32_t mine = tm + ((uint32_t)(warp * 32) << 16);
   if (t == 0) {
     const Operand<128, kKMajor, NQ, kTerm, 16384> kq(smem_u32(images));
     umma_terms<64, KP * 4, NQ>(tm, kq, kq, false);  // B: the K rows
     umma_commit(bar);
-    bulk_store_1d(a.kq + (size_t)(c * a.Hk + kh) * (NQ * kTerm), images, NQ * kTerm);
+    bulk_store_1d(a.kq + (size_t)(c * a.Hk + kh) * L::kKq, images, L::kKq);
     bulk_commit();
   }
   Waiter wait{a.wait_ns, a.status};
-  wait(bar, 0);
-  tmem_fence_after_sync();
+  uint32_t phase = 0;
 
-  for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
+  for (int hh = 0; hh < rep; ++hh) {
+    const int h = kh * rep + hh;
     const int64_t ch = c * a.Hv + h;
-    if (warp == 0) {
+    if (hh % kPrepHeads == 0 && hh + warp < rep) {
       // the running sum of g, in double: differences of it enter exp
+      const int hw = h + warp;
       float g[2], b[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 2 * lane + i;
-        const int64_t at = (start + r) * a.Hv + h;
+        const int64_t at = (start + r) * a.Hv + hw;
         g[i] = r < len ? a.g[at] : 0.0f;
         b[i] = r < len ? a.beta[at] : 0.0f;
         g[i] = g[i] < -256.0f ? -256.0f : g[i];  // exp of either is 0; -inf would leave inf - inf
@@ -198,65 +197,112 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(DeltaArgs a) {
       }
       const double last = __shfl_sync(0xffffffffu, incl, 31);
       const double G[2] = {incl - own + (double)g[0], incl};
-      float* gates = a.gates + ch * kDeltaGates;
+      float* gates = a.gates + (ch + warp) * kDeltaGates;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 2 * lane + i;
-        const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
-        const float dec = exp_f((float)(last - G[i]));
-        sg[r] = make_float2(hi, lo);
-        sbeta[r] = b[i];
-        gates[r] = exp_f(hi) * (1.0f + lo);
-        gates[64 + r] = dec * b[i];
+        const double G2 = G[i] * 1.4426950408889634;
+        const float hi = (float)G2, lo = (float)(G2 - (double)hi);
+        sg_all[warp * 64 + r] = make_float2(hi, lo);
+        sbeta_all[warp * 64 + r] = b[i];
+        const float gh = (float)G[i], dh = (float)(last - G[i]);
+        gates[r] = exp_f(gh) * (1.0f + (float)(G[i] - (double)gh));
+        gates[64 + r] = exp_f(dh) * (1.0f + (float)(last - G[i] - (double)dh)) * b[i];
         gates[128 + r] = b[i];
         gates[192 + r] = hi;
         gates[256 + r] = lo;
       }
     }
+    if (t == 0) bulk_wait_read();  // [K; Q], or the last head's X, has left
     __syncthreads();
+    if (hh == 0) {
+      wait(bar, phase);
+      phase ^= 1;
+      tmem_fence_after_sync();
+    }
+    const float2* sg = sg_all + (hh % kPrepHeads) * 64;
+    const float* sbeta = sbeta_all + (hh % kPrepHeads) * 64;
     const int r = t & 63;
-    float2 x[32];
+    const bool is_k = t < 64;
     {
       const float2 gi = sg[r];
-      const bool is_k = t < 64;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        if (half && !(warp & 1)) {  // rows 0-31 end before column 32
+          if (!is_k) {
+            const float zero[32] = {};
+            put_row<NT, 128>(images, 16384, t, 4, zero);
+          }
+          continue;
+        }
         float d[32];
-        tmem_row<32>(tm + ((uint32_t)(warp * 32) << 16) + half * 32, d);
+        tmem_row<32>(mine + half * 32, d);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int j = half * 32 + i;
           const float2 gj = sg[j];
-          const float w = exp_f((gi.x - gj.x) + (gi.y - gj.y)) * sbeta[j] * d[i];
+          const float w = ex2((gi.x - gj.x) + (gi.y - gj.y)) * sbeta[j] * d[i];
           d[i] = (is_k ? j < r : j <= r) ? (is_k ? w : w * a.scale) : 0.0f;
         }
         if (is_k) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(sn + r * kNPitch + half * 32 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const int j = half * 32 + i;
-          x[j / 2] = is_k ? make_float2(j == r ? 1.0f : 0.0f, j + 1 == r ? 1.0f : 0.0f) : make_float2(d[i], d[i + 1]);
+        } else {
+          put_row<NT, 128>(images, 16384, t, half * 4, d);
         }
       }
     }
     __syncthreads();
-    substitute(x, sn, r, (warp & 1) != 0);
-    uint8_t* out = a.x + (size_t)ch * (NT * 16384);
+    const int role = (warp + blockIdx.x) & 3;
+    if (role < 2) {
+      const int tr = role * 32 + lane;
+      float2 x[32];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float v[8] = {x[4 * q].x, x[4 * q].y, x[4 * q + 1].x, x[4 * q + 1].y,
-                          x[4 * q + 2].x, x[4 * q + 2].y, x[4 * q + 3].x, x[4 * q + 3].y};
-      put_chunk<NT, 128>(out, 16384, t, q, v);
+      for (int i = 0; i < 32; ++i) x[i] = make_float2(2 * i == tr ? 1.0f : 0.0f, 2 * i + 1 == tr ? 1.0f : 0.0f);
+      if (role == 1) substitute<63, 32>(x, sn);
+      substitute<31, 1>(x, sn);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float v[8] = {x[4 * q].x, x[4 * q].y, x[4 * q + 1].x, x[4 * q + 1].y,
+                            x[4 * q + 2].x, x[4 * q + 2].y, x[4 * q + 3].x, x[4 * q + 3].y};
+        put_chunk<NT, 128>(images, 16384, tr, q, v);
+      }
     }
+    fence_async_smem();
+    tmem_fence_before_sync();
     __syncthreads();
+    if (t == 0) {
+      tmem_fence_after_sync();
+      const Operand<128, kKMajor, NT, 16384> A(smem_u32(images));
+      const Operand<128, kMnMajor, NT, 16384> B(smem_u32(images));  // the rows of Tm
+      umma_terms<64, 4, NT>(tm + 64, A, B, false);
+      umma_commit(bar);
+    }
+    wait(bar, phase);
+    phase ^= 1;
+    tmem_fence_after_sync();
+    if (!is_k) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half && !(warp & 1)) continue;
+        float d[32];
+        tmem_row<32>(mine + 64 + half * 32, d);
+        put_row<NT, 128>(images, 16384, t, half * 4, d);
+      }
+    }
+    fence_async_smem();
+    tmem_fence_before_sync();
+    __syncthreads();
+    if (t == 0) {
+      bulk_store_1d(a.x + (size_t)ch * L::kX, images, L::kX);
+      bulk_commit();
+    }
   }
   if (t == 0) bulk_wait_all();
   tmem_fence_before_sync();
   __syncthreads();
-  if (warp == 0) tmem_dealloc<64>(tm);
+  if (warp == 0) tmem_dealloc<128>(tm);
 }
 
 template <IO kIO, int KP>

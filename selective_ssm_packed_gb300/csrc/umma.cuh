@@ -145,6 +145,29 @@ __device__ __forceinline__ void umma_terms(uint32_t tmem_d, const A& a, const B&
   }
 }
 
+// The same product with the terms of B side by side along N: B's image is
+// [term][column block][rows], MN-major, so that one instruction multiplies a
+// term of A with several terms of B and reads A from shared memory once (at
+// N = 64 reading A takes longer than the products).  Order s = i + j of the
+// pairs has its own kCols columns of D, and the sum of D's kKeep blocks,
+// smallest first, is the product:
+//   D[block i ..] += A_i [B_0 .. B_{kKeep - 1 - i}]
+// kFresh: overwrite D.  A B of one term leaves the blocks from A's other terms.
+template <int kCols, int kSteps, int kKeep, bool kFresh, typename A, typename B>
+__device__ __forceinline__ void umma_blocks(uint32_t tmem_d, const A& a, const B& b) {
+  static_assert(B::kMajor == kMnMajor, "terms along N need an MN-major B");
+  static_assert(B::kTerms >= kKeep || B::kTerms == 1, "");
+#pragma unroll
+  for (int i = 0; i < kKeep && i < A::kTerms; ++i) {
+    const int terms = B::kTerms < kKeep - i ? B::kTerms : kKeep - i;
+    const uint32_t idesc = umma_idesc(A::kMajor, kMnMajor, (uint32_t)(terms * kCols));
+    const bool fresh = kFresh && (i == 0 || B::kTerms == 1);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      umma(tmem_d + i * kCols, a.at(i, s), b.at(0, s), idesc, fresh && s == 0 ? 0u : 1u);
+  }
+}
+
 // ------------------------------------------------------------------ tensor memory of `kCols` columns
 template <int kCols>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst) {  // warp-collective
@@ -158,6 +181,10 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr) {  // warp-collecti
   __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
 }
+
+// The sum of kBlocks blocks, `stride` columns apart, last block first.
+template <int kCount, int kBlocks>
+__device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float (&v)[kCount]);
 
 // kCount (16 or 32) consecutive columns of this thread's lane, as floats.
 template <int kCount>
@@ -174,6 +201,18 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[kCount]) {
   }
 #pragma unroll
   for (int i = 0; i < kCount; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int kCount, int kBlocks>
+__device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float (&v)[kCount]) {
+  tmem_row<kCount>(taddr + (kBlocks - 1) * stride, v);
+#pragma unroll
+  for (int b = kBlocks - 2; b >= 0; --b) {
+    float w[kCount];
+    tmem_row<kCount>(taddr + b * stride, w);
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) v[i] += w[i];
+  }
 }
 
 }  // namespace vssm

@@ -47,32 +47,125 @@ __device__ __forceinline__ void st_io8(__nv_bfloat16* p, const float* v) {
 // Writes 8 values as chunk `chunk` of row `row` of NT images term_bytes apart
 // (shared or global memory).
 template <int NT, int kRowBytes>
-__device__ __forceinline__ void put_chunk(uint8_t* image, int term_bytes, int row, int chunk, const float* v) {
+__device__ __forceinline__ void put_chunk(uint8_t* image, int term_bytes, int row, int chunk, const float2* v) {
   uint32_t t[4][NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) split_pair<NT>(v[2 * i], v[2 * i + 1], t[i]);
+  for (int i = 0; i < 4; ++i) split_pair<NT>(v[i], t[i]);
   const uint32_t o = image_chunk<kRowBytes>(row, chunk);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
     *reinterpret_cast<uint4*>(image + i * term_bytes + o) = make_uint4(t[0][i], t[1][i], t[2][i], t[3][i]);
 }
 
-// `count` values of this thread's row, columns from chunk0 * 8.
-template <int NT, int kRowBytes, int kCount>
-__device__ __forceinline__ void put_row(uint8_t* image, int term_bytes, int row, int chunk0, const float (&v)[kCount]) {
+// kPairs pairs of this thread's row, columns from chunk0 * 8.
+template <int NT, int kRowBytes, int kPairs>
+__device__ __forceinline__ void put_row(uint8_t* image, int term_bytes, int row, int chunk0, const float2 (&v)[kPairs]) {
 #pragma unroll
-  for (int c = 0; c < kCount / 8; ++c) put_chunk<NT, kRowBytes>(image, term_bytes, row, chunk0 + c, v + 8 * c);
+  for (int c = 0; c < kPairs / 4; ++c) put_chunk<NT, kRowBytes>(image, term_bytes, row, chunk0 + c, v + 4 * c);
+}
+
+template <int kPairs>
+__device__ __forceinline__ void scale_row(float2 (&v)[kPairs], float f) {
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) v[i] = mul2(v[i], splat2(f));
+}
+
+// 16 bytes of io values as pairs (4 of bf16, 2 of float).
+__device__ __forceinline__ void unpack(uint4 q, float2 (&v)[4]) {
+  v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+  v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+  v[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z));
+  v[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
+}
+__device__ __forceinline__ void unpack(uint4 q, float2 (&v)[2]) {
+  v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+  v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+}
+
+// Four lanes, four chunks each: lane j's chunk i becomes lane i's chunk j.
+// A warp reads or writes 32 rows of 64 bytes with it four lanes to a row, eight
+// rows an instruction; a lane to a row would touch 32 lines with every
+// instruction (the forward walk spent more time on that than on its products).
+__device__ __forceinline__ void transpose4(uint4 (&q)[4], int lane) {
+#pragma unroll
+  for (int o = 2; o >= 1; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & o) continue;
+      const uint4 give = up ? q[a] : q[a + o];
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, o);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, o);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, o);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, o);
+      if (up) q[a] = got; else q[a + o] = got;
+    }
+  }
+}
+
+// 32 rows of 64 bytes, row i of a warp at base + i * stride (in T); `rows` of
+// them exist and `cols` values of each.  Lane l gets (or gives) row l.
+template <typename T>
+__device__ __forceinline__ void load_rows(const T* base, int64_t stride, int rows, int cols, int lane, uint4 (&q)[4]) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (lane & ~3) + i, c = (lane & 3) * kPer;
+    q[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows && c < cols) q[i] = *reinterpret_cast<const uint4*>(base + r * stride + c);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_rows(T* base, int64_t stride, int rows, int cols, int lane, uint4 (&q)[4]) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+  transpose4(q, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (lane & ~3) + i, c = (lane & 3) * kPer;
+    if (r < rows && c < cols) *reinterpret_cast<uint4*>(base + r * stride + c) = q[i];
+  }
+}
+
+// Eight pairs as 16-byte chunks of io values (two of bf16, four of float).
+__device__ __forceinline__ void pack(const float2 (&v)[8], uint4* q, __nv_bfloat16) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[4 * i + j].x, v[4 * i + j].y);
+      t[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    q[i] = make_uint4(t[0], t[1], t[2], t[3]);
+  }
+}
+__device__ __forceinline__ void pack(const float2 (&v)[8], uint4* q, float) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    q[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y), __float_as_uint(v[2 * i + 1].x),
+                      __float_as_uint(v[2 * i + 1].y));
 }
 
 // Waits of one thread of a chunk kernel: after one that runs out of time the
-// status word says so and the later ones no longer wait.
+// status word says so and the later ones no longer wait.  The timer is read
+// once in 64 tries.
 struct Waiter {
   unsigned long long limit;
   int* status;
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (!mbar_wait(bar, parity, limit)) {
-      if (limit) atomicOr(status, kStatusTmaTimeout);
-      limit = 0;
+    if (mbar_try_wait(bar, parity)) return;
+    uint64_t t0 = 0;
+    while (limit) {
+#pragma unroll 1
+      for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit) {
+        atomicOr(status, kStatusTmaTimeout);
+        limit = 0;
+      }
     }
   }
 };

@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
   using T = typename IoType<kIO>::type;
   using L = BwdSmem<kIO, KP, kWalks>;
   constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, NB = DeltaTerms<kIO>::kTiles,
-                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2;
+                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2, HP = HC / 2;
   constexpr int kTmemCols = 2 * kWalks * NT * BV > 256 ? 512 : 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
     }
     mbar_init(x_full, 1);
     *x_used = 0;
-    for (int i = 0; i < kWalks; ++i) mbar_init(&done_all[i], 1);
+    for (int i = 0; i < kWalks; ++i) mbar_init(&done_all[i], 2);  // the products, and the porter
     fence_mbar_init();
     for (int i = 0; i < ST && i < n; ++i) load_kq(i);
     if (n > 0) load_x(0);
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
   if (warp / 8 < walks) {
     const int walk = warp / 8, quad = warp & 3, half = warp >> 2 & 1;
     const int row = quad * 32 + lane, r = row & 63;
-    const bool leader = (threadIdx.x & 255) == 0;
+    const bool leader = (threadIdx.x & 255) == 96, porter = (threadIdx.x & 255) == 64;  // as in the forward
     const int panel = group * kWalks + walk;
     const int col0 = panel * BV + half * HC;
     const int tiles = delta_tiles(a.V);
@@ -107,56 +107,52 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
     uint64_t* done = done_all + walk;
     const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
     const uint32_t lane_at = ((uint32_t)(quad * 32) << 16) + half * HC;
+    constexpr int kSteps = HC / 16;  // of 16 columns: two chunks of an image's row, eight pairs
     const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
 
-    float S[HC];
+    float2 S[HP];
 #pragma unroll
-    for (int i = 0; i < HC; ++i) S[i] = 0.0f;
+    for (int i = 0; i < HP; ++i) S[i] = splat2(0.0f);
     if (a.d_final && row < a.K) {
 #pragma unroll
-      for (int i = 0; i < HC; i += 4)
-        if (col0 + i < a.V) {
-          const float4 f = *reinterpret_cast<const float4*>(a.d_final + state_at + i);
-          S[i] = f.x; S[i + 1] = f.y; S[i + 2] = f.z; S[i + 3] = f.w;
+      for (int i = 0; i < HP; i += 2)
+        if (col0 + 2 * i < a.V) {
+          const float4 f = *reinterpret_cast<const float4*>(a.d_final + state_at + 2 * i);
+          S[i] = make_float2(f.x, f.y);
+          S[i + 1] = make_float2(f.z, f.w);
         }
     }
     // the next chunk's dO, raw, and gates: read a chunk ahead
-    constexpr int kRaw = HC * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T);
-    uint4 raw[kRaw];
+    constexpr int kPer = 16 / (int)sizeof(T);
+    uint4 raw[4];
     float gam, decb, gam_end;
     auto prefetch = [&](int c) {
       const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
       gam = gates[r];
       decb = gates[64 + r];
       gam_end = gates[63];
-      const int64_t at = (int64_t)c * kDeltaChunk + r;
-#pragma unroll
-      for (int i = 0; i < kRaw; ++i) {
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (row >= 64 && at < seq_len && col0 + i * kPer < a.V)
-          raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + ((seq_start + at) * a.Hv + h) * a.V +
-                                                   col0 + i * kPer);
-      }
+      const int64_t at = (int64_t)c * kDeltaChunk + (quad & 1) * 32;  // the warp's first token
+      if (row >= 64)
+        load_rows(static_cast<const T*>(a.dout) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V,
+                  (int)min((int64_t)32, seq_len - at), a.V - col0, lane, raw);
     };
     // rows 64-127: dO into sZ, as it is and scaled
     auto put_dout = [&]() {
-      float d[HC];
+      transpose4(raw, lane);
 #pragma unroll
-      for (int i = 0; i < kRaw; ++i) {
-        if constexpr (kIO == IO::BF16) {
-          d[8 * i] = bf16_lo(raw[i].x); d[8 * i + 1] = bf16_hi(raw[i].x); d[8 * i + 2] = bf16_lo(raw[i].y);
-          d[8 * i + 3] = bf16_hi(raw[i].y); d[8 * i + 4] = bf16_lo(raw[i].z); d[8 * i + 5] = bf16_hi(raw[i].z);
-          d[8 * i + 6] = bf16_lo(raw[i].w); d[8 * i + 7] = bf16_hi(raw[i].w);
-        } else {
-          d[4 * i] = __uint_as_float(raw[i].x); d[4 * i + 1] = __uint_as_float(raw[i].y);
-          d[4 * i + 2] = __uint_as_float(raw[i].z); d[4 * i + 3] = __uint_as_float(raw[i].w);
+      for (int u = 0; u < kSteps; ++u) {
+        float2 d[8];
+#pragma unroll
+        for (int i = 0; i < 16 / kPer; ++i) {
+          float2 w[kPer / 2];
+          unpack(raw[u * (16 / kPer) + i], w);
+#pragma unroll
+          for (int j = 0; j < kPer / 2; ++j) d[i * (kPer / 2) + j] = w[j];
         }
+        put_row<NQ, 64>(z_mine, L::kZTerm, r, chunk0 + 2 * u, d);
+        scale_row(d, a.scale * gam);
+        put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0 + 2 * u, d);
       }
-      put_row<NQ, 64>(z_mine, L::kZTerm, r, chunk0, d);
-      const float f = a.scale * gam;
-#pragma unroll
-      for (int i = 0; i < HC; ++i) d[i] *= f;
-      put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0, d);
     };
     if (n > 0) {
       prefetch(n - 1);
@@ -173,7 +169,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       const bool last = i + 1 == n;
       const int64_t ch = (int64_t)(c0 + c) * a.Hv + h;
       const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq), x = smem_u32(sm + L::oX);
-      if (leader) {
+      if (porter) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
           if (tile0 + b < tiles)
@@ -190,6 +186,10 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
               bulk_store_1d(a.ds + ((ch * tiles + tile0 + b) * NT + j) * (size_t)L::kSTile,
                             sS + j * L::kSTerm + b * L::kSTile, L::kSTile);
         bulk_commit();
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        mbar_arrive(done);  // dO's image has left, before Z takes its place
+      }
+      if (leader) {
         wait(&kq_full[st], (i / ST) & 1);
         tmem_fence_after_sync();
         if (has_state) {
@@ -202,29 +202,29 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
         const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x + 64 * 128);
         const Operand<64, kMnMajor, NQ, L::kZTerm, 0, L::kZTile> B(smem_u32(sZ));
         umma_blocks<BV, 4, NT, true>(tD2, A, B);
-        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // dO's image has left, before Z takes its place
         umma_commit(done);
       }
-      const int64_t at = (int64_t)c * kDeltaChunk + r;
-      const bool valid = at < seq_len;
       const float g_row = gam, db_row = decb, g_end = gam_end;
-      float d[HC];
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
       if (row < 64) {
-        if (has_state) {
-          tmem_sum<HC, NT>(tD1 + lane_at, BV, d);
-        } else {
 #pragma unroll
-          for (int k = 0; k < HC; ++k) d[k] = 0.0f;
+        for (int u = 0; u < kSteps; ++u) {
+          float2 d[8];
+          if (has_state) {
+            tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
+            scale_row(d, db_row);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = splat2(0.0f);
+          }
+          put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0 + 2 * u, d);
         }
-#pragma unroll
-        for (int k = 0; k < HC; ++k) d[k] *= db_row;
-        put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0, d);
       }
       fence_async_smem();
       tmem_fence_before_sync();
+      if (porter) mbar_arrive(done);
       named_barrier(1 + walk, 256);
       if (leader) {
         tmem_fence_after_sync();
@@ -237,26 +237,31 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (leader && i + 1 < n && last_user(x_used)) load_x(i + 1);
+      if (porter && i + 1 < n && last_user(x_used)) load_x(i + 1);
       if (row < 64) {
-        tmem_sum<HC, NT>(tD2 + lane_at, BV, d);
         const int tile = tile0 + in_tile;
-        if (tile < tiles)
-          put_row<NT, 64>(a.dvi + (ch * tiles + tile) * (size_t)(NT * kRowTile), kRowTile, row, chunk0, d);
-        if (valid) {
-          T* p = static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0;
+        uint8_t* to = a.dvi + (ch * tiles + tile) * (size_t)(NT * kRowTile);
+        uint4 q[4];
 #pragma unroll
-          for (int k = 0; k < HC; k += 8)
-            if (col0 + k < a.V) st_io8(p + k, d + k);
+        for (int u = 0; u < kSteps; ++u) {
+          float2 d[8];
+          tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
+          if (tile < tiles) put_row<NT, 64>(to, kRowTile, row, chunk0 + 2 * u, d);
+          pack(d, q + u * (4 / kSteps), T());
+          scale_row(d, -g_row);
+          put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0 + 2 * u, d);
         }
-#pragma unroll
-        for (int k = 0; k < HC; ++k) d[k] *= -g_row;
-        put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0, d);
+        const int64_t at = (int64_t)c * kDeltaChunk + quad * 32;
+        store_rows(static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V,
+                   (int)min((int64_t)32, seq_len - at), a.V - col0, lane, q);
       }
       if (last && !a.d_initial) break;
       fence_async_smem();
       tmem_fence_before_sync();
-      if (leader) bulk_wait_read();
+      if (porter) {
+        bulk_wait_read();
+        mbar_arrive(done);
+      }
       named_barrier(1 + walk, 256);
       if (leader) {
         tmem_fence_after_sync();
@@ -268,24 +273,28 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (leader && i + ST < n && last_user(&kq_used[st])) load_kq(i + ST);
-      tmem_sum<HC, NT>(tD1 + lane_at, BV, d);
+      if (porter && i + ST < n && last_user(&kq_used[st])) load_kq(i + ST);
       if (row < KP * 64) {
 #pragma unroll
-        for (int k = 0; k < HC; ++k) S[k] = fmaf(g_end, S[k], d[k]);
-        if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
+        for (int u = 0; u < kSteps; ++u) {
+          float2 d[8];
+          tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) S[8 * u + k] = d[k] = fma2(splat2(g_end), S[8 * u + k], d[k]);
+          if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0 + 2 * u, d);
+        }
       }
       if (!last && row >= 64) put_dout();
       fence_async_smem();
       tmem_fence_before_sync();
       named_barrier(1 + walk, 256);
     }
-    if (leader) bulk_wait_all();
+    if (porter) bulk_wait_all();
     if (a.d_initial && row < a.K) {
 #pragma unroll
-      for (int i = 0; i < HC; i += 4)
-        if (col0 + i < a.V)
-          *reinterpret_cast<float4*>(a.d_initial + state_at + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      for (int i = 0; i < HP; i += 2)
+        if (col0 + 2 * i < a.V)
+          *reinterpret_cast<float4*>(a.d_initial + state_at + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
     }
   }
   tmem_fence_before_sync();

@@ -10,14 +10,16 @@ namespace {
 // bf16 terms in shared memory.  A chunk is three products on the matrix unit,
 // each read back from tensor memory by the walk's threads (warp w: lanes
 // 32 (w % 4) .., column half w / 4 % 2):
-//   D = [K; Q] S0        rows 0-63 become R, rows 64-127 wait as exp(G) Q S0
-//   D = [Tm; P Tm] R     rows 0-63 are E, rows 64-127 finish O
-//   D = K^T (dec beta E) and S1 = exp(G_63) S0 + D
+//   D1 = [K; Q] S0        rows 0-63 become R, rows 64-127 wait in tensor memory
+//   D2 = [Tm; P Tm] R     rows 0-63 are E, rows 64-127 with D1's make O
+//   D1 = K^T (dec beta E) and S1 = exp(G_63) S0 + D1
 // The chain product - read back - product bounds a walk, not the matrix unit,
 // so two walks share a CTA (and its [K; Q] and X) where there are enough
 // CTAs to fill the GPU: one multiplies while the other reads back.  [K; Q] and
 // X come by bulk copies, ahead of the walks, asked for by whichever walk is
-// through with the buffer last.
+// through with the buffer last.  Two walks leave a thread 128 registers, so
+// they read back 16 columns at a time: one spilled register is a trip to L2,
+// shared memory having taken nearly all of L1.
 template <IO kIO, int KP, int kWalks>
 struct FwdSmem {
   using D = DeltaTerms<kIO>;
@@ -35,8 +37,8 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
   using T = typename IoType<kIO>::type;
   using L = FwdSmem<kIO, KP, kWalks>;
   constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, NB = DeltaTerms<kIO>::kTiles,
-                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2;
-  constexpr int kTmemCols = kWalks * NT * BV > 128 ? 256 : 128;
+                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2, HP = HC / 2;
+  constexpr int kTmemCols = 2 * kWalks * NT * BV > 256 ? 512 : 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);
@@ -96,7 +98,8 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
   if (warp / 8 < walks) {
     const int walk = warp / 8, quad = warp & 3, half = warp >> 2 & 1;
     const int row = quad * 32 + lane, r = row & 63;  // of a product: token (K rows, then Q rows) or state row
-    const bool leader = (threadIdx.x & 255) == 0;
+    // one thread issues the products, another the bulk copies: in warps of Q rows, whose read-backs are the shorter ones
+    const bool leader = (threadIdx.x & 255) == 96, porter = (threadIdx.x & 255) == 64;
     const int panel = group * kWalks + walk;
     const int col0 = panel * BV + half * HC;  // this thread's first state column
     const int tiles = delta_tiles(a.V);
@@ -108,38 +111,36 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
     uint8_t* sR = sS + L::kS;
     uint8_t* sE = sR + L::kR;
     uint64_t* done = done_all + walk;
-    const uint32_t tD = tm + walk * NT * BV;
-    const uint32_t mine = tD + ((uint32_t)(quad * 32) << 16) + half * HC;
+    const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
+    const uint32_t lane_at = ((uint32_t)(quad * 32) << 16) + half * HC;
+    constexpr int kSteps = HC / 16;  // of 16 columns: two chunks of an image's row, eight pairs
     const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
 
-    float S[HC];
+    float2 S[HP];
 #pragma unroll
-    for (int i = 0; i < HC; ++i) S[i] = 0.0f;
+    for (int i = 0; i < HP; ++i) S[i] = splat2(0.0f);
     if (a.initial && row < a.K) {
 #pragma unroll
-      for (int i = 0; i < HC; i += 4)
-        if (col0 + i < a.V) {
-          const float4 f = *reinterpret_cast<const float4*>(a.initial + state_at + i);
-          S[i] = f.x; S[i + 1] = f.y; S[i + 2] = f.z; S[i + 3] = f.w;
+      for (int i = 0; i < HP; i += 2)
+        if (col0 + 2 * i < a.V) {
+          const float4 f = *reinterpret_cast<const float4*>(a.initial + state_at + 2 * i);
+          S[i] = make_float2(f.x, f.y);
+          S[i + 1] = make_float2(f.z, f.w);
         }
     }
     // the next chunk's v, raw, and gates: read a chunk ahead
-    constexpr int kRaw = HC * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T);
-    uint4 raw[kRaw];
+    constexpr int kPer = 16 / (int)sizeof(T);
+    uint4 raw[4];
     float gam, decb, gam_end;
     auto prefetch = [&](int c) {
       const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
       gam = gates[r];
       decb = gates[64 + r];
       gam_end = gates[63];
-      const int64_t at = (int64_t)c * kDeltaChunk + r;
-#pragma unroll
-      for (int i = 0; i < kRaw; ++i) {
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (row < 64 && at < seq_len && col0 + i * kPer < a.V)
-          raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + (seq_start + at) * a.sv + (int64_t)h * a.V +
-                                                   col0 + i * kPer);
-      }
+      const int64_t at = (int64_t)c * kDeltaChunk + quad * 32;  // the warp's first token
+      if (row < 64)
+        load_rows(static_cast<const T*>(a.v) + (seq_start + at) * a.sv + (int64_t)h * a.V + col0, a.sv,
+                  (int)min((int64_t)32, seq_len - at), a.V - col0, lane, raw);
     };
     if (n > 0) prefetch(0);
     if (row < KP * 64) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
@@ -153,96 +154,102 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       const bool last = c + 1 == n;
       const int64_t ch = (int64_t)(c0 + c) * a.Hv + h;
       const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq);
+      if (porter && a.s0) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          if (tile0 + i < tiles)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              bulk_store_1d(a.s0 + ((ch * tiles + tile0 + i) * NT + j) * (size_t)L::kSTile,
+                            sS + j * L::kSTerm + i * L::kSTile, L::kSTile);
+        bulk_commit();
+      }
       if (leader) {
-        if (a.s0) {
-#pragma unroll
-          for (int i = 0; i < NB; ++i)
-            if (tile0 + i < tiles)
-#pragma unroll
-              for (int j = 0; j < NT; ++j)
-                bulk_store_1d(a.s0 + ((ch * tiles + tile0 + i) * NT + j) * (size_t)L::kSTile,
-                              sS + j * L::kSTerm + i * L::kSTile, L::kSTile);
-          bulk_commit();
-        }
         wait(&kq_full[st], (c / ST) & 1);
         tmem_fence_after_sync();
         if (has_state) {
           const Operand<128, kKMajor, NQ, KP * 16384, 16384> A(kq);
           const Operand<64, kMnMajor, NT, L::kSTerm, 0, L::kSTile> B(smem_u32(sS));
-          umma_blocks<BV, KP * 4, NT, true>(tD, A, B);
+          umma_blocks<BV, KP * 4, NT, true>(tD1, A, B);
           umma_commit(done);
         }
       }
-      const int64_t at = (int64_t)c * kDeltaChunk + r;
-      const bool valid = at < seq_len;
       const float g_row = gam, db_row = decb, g_end = gam_end;
-      float d[HC], o[HC];
+      if (row < 64) transpose4(raw, lane);
       if (has_state) {
         wait(done, phase);
         phase ^= 1;
         tmem_fence_after_sync();
-        tmem_sum<HC, NT>(mine, BV, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < HC; ++i) d[i] = 0.0f;
       }
       if (row < 64) {
+        // past the chunk's end v and the rows of K are zero, and so is R
 #pragma unroll
-        for (int i = 0; i < kRaw; ++i) {
-          float w[kPer];
-          if constexpr (kIO == IO::BF16) {
-            w[0] = bf16_lo(raw[i].x); w[1] = bf16_hi(raw[i].x); w[2] = bf16_lo(raw[i].y); w[3] = bf16_hi(raw[i].y);
-            w[4] = bf16_lo(raw[i].z); w[5] = bf16_hi(raw[i].z); w[6] = bf16_lo(raw[i].w); w[7] = bf16_hi(raw[i].w);
-          } else {
-            w[0] = __uint_as_float(raw[i].x); w[1] = __uint_as_float(raw[i].y);
-            w[2] = __uint_as_float(raw[i].z); w[3] = __uint_as_float(raw[i].w);
+        for (int u = 0; u < kSteps; ++u) {
+          float2 d[8];
+          if (has_state) tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
+#pragma unroll
+          for (int i = 0; i < 16 / kPer; ++i) {
+            float2 w[kPer / 2];
+            unpack(raw[u * (16 / kPer) + i], w);
+#pragma unroll
+            for (int j = 0; j < kPer / 2; ++j) {
+              const int k = i * (kPer / 2) + j;
+              d[k] = has_state ? fma2(splat2(-g_row), d[k], w[j]) : w[j];
+            }
           }
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) d[i * kPer + j] = valid ? fmaf(-g_row, d[i * kPer + j], w[j]) : 0.0f;
+          put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0 + 2 * u, d);
         }
-        put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < HC; ++i) o[i] = a.scale * g_row * d[i];
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      if (leader && a.s0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last chunk's E has left
+      if (porter && a.s0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last chunk's E has left
       named_barrier(1 + walk, 256);
       if (leader) {
         tmem_fence_after_sync();
         wait(x_full, c & 1);
         const Operand<128, kKMajor, NT, 16384> A(smem_u32(sm + L::oX));
         const Operand<64, kMnMajor, NT, L::kRTerm, 0, kRowTile> B(smem_u32(sR));
-        umma_blocks<BV, 4, NT, true>(tD, A, B);
+        umma_blocks<BV, 4, NT, true>(tD2, A, B);
         umma_commit(done);
       }
       if (!last) prefetch(c + 1);
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (leader && c + 1 < n && last_user(x_used)) load_x(c + 1);
-      tmem_sum<HC, NT>(mine, BV, d);
+      if (porter && c + 1 < n && last_user(x_used)) load_x(c + 1);
       if (row < 64) {
-        if (a.e) put_row<NT, 64>(sE + in_tile * kRowTile, L::kRTerm, row, chunk0, d);
 #pragma unroll
-        for (int i = 0; i < HC; ++i) d[i] *= db_row;
-        put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0, d);
-      } else if (valid) {
-        T* op = static_cast<T*>(a.out) + ((seq_start + at) * a.Hv + h) * a.V + col0;
+        for (int u = 0; u < kSteps; ++u) {
+          float2 d[8];
+          tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
+          if (a.e) put_row<NT, 64>(sE + in_tile * kRowTile, L::kRTerm, row, chunk0 + 2 * u, d);
+          scale_row(d, db_row);
+          put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0 + 2 * u, d);
+        }
+      } else {
+        uint4 q[4];
 #pragma unroll
-        for (int i = 0; i < HC; ++i) o[i] += d[i];
+        for (int u = 0; u < kSteps; ++u) {
+          float2 d[8], o[8];
+          tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
+          if (has_state) {
+            tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, o);
 #pragma unroll
-        for (int i = 0; i < HC; i += 8)
-          if (col0 + i < a.V) st_io8(op + i, o + i);
+            for (int i = 0; i < 8; ++i) d[i] = fma2(splat2(a.scale * g_row), o[i], d[i]);
+          }
+          pack(d, q + u * (4 / kSteps), T());
+        }
+        const int64_t at = (int64_t)c * kDeltaChunk + (quad & 1) * 32;
+        store_rows(static_cast<T*>(a.out) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V,
+                   (int)min((int64_t)32, seq_len - at), a.V - col0, lane, q);
       }
       const bool stop = last && !a.final_states;
       if (stop && !a.e) break;
       fence_async_smem();
       tmem_fence_before_sync();
-      if (leader) bulk_wait_read();  // S0's images are free to be overwritten
+      if (porter && a.s0) bulk_wait_read();  // S0's images are free to be overwritten
       named_barrier(1 + walk, 256);
-      if (leader && a.e) {
+      if (porter && a.e) {
 #pragma unroll
         for (int i = 0; i < NB; ++i)
           if (tile0 + i < tiles)
@@ -257,29 +264,33 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);  // K^T: the first 64 rows
         const Operand<64, kMnMajor, NT, L::kRTerm, 0, kRowTile> B(smem_u32(sR));
-        umma_blocks<BV, 4, NT, true>(tD, A, B);
+        umma_blocks<BV, 4, NT, true>(tD1, A, B);
         umma_commit(done);
       }
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (leader && c + ST < n && last_user(&kq_used[st])) load_kq(c + ST);
-      tmem_sum<HC, NT>(mine, BV, d);
+      if (porter && c + ST < n && last_user(&kq_used[st])) load_kq(c + ST);
       if (row < KP * 64) {
 #pragma unroll
-        for (int i = 0; i < HC; ++i) S[i] = fmaf(g_end, S[i], d[i]);
-        if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
+        for (int u = 0; u < kSteps; ++u) {
+          float2 d[8];
+          tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) S[8 * u + i] = d[i] = fma2(splat2(g_end), S[8 * u + i], d[i]);
+          if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0 + 2 * u, d);
+        }
       }
       fence_async_smem();
       tmem_fence_before_sync();
       named_barrier(1 + walk, 256);
     }
-    if (leader) bulk_wait_all();
+    if (porter) bulk_wait_all();
     if (a.final_states && row < a.K) {
 #pragma unroll
-      for (int i = 0; i < HC; i += 4)
-        if (col0 + i < a.V)
-          *reinterpret_cast<float4*>(a.final_states + state_at + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      for (int i = 0; i < HP; i += 2)
+        if (col0 + 2 * i < a.V)
+          *reinterpret_cast<float4*>(a.final_states + state_at + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
     }
   }
   tmem_fence_before_sync();

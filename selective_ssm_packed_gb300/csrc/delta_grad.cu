@@ -233,7 +233,10 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
           }
           rows = fmaf(qk[i], b, rows);
         }
-        put_row<NT, 128>(sm + (is_k ? L::oM2 : L::oM1), 8192, r, half * 4, m);
+        float2 mp[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mp[i] = make_float2(m[2 * i], m[2 * i + 1]);
+        put_row<NT, 128>(sm + (is_k ? L::oM2 : L::oM1), 8192, r, half * 4, mp);
         srow[half * 128 + row] = rows;
         scol[quad * 64 + half * 32 + lane] = lane_column_sum(qk, lane);
       }

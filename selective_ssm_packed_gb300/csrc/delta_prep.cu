@@ -71,15 +71,15 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
 // One CTA of 128 threads per chunk and key head; the value heads that share
 // the key head follow each other.  Thread r < 64 owns row r of K K^T, N and
 // Tm, thread 64 + r row r of Q K^T, P and P Tm.
-// Tm = (I + N)^-1 row by row, by substitution from the last column: x starts as
-// a row of I, x_j is final, then x_l -= x_j N_jl for l < j, with the row in
-// registers and N read from shared memory as one broadcast for the whole
-// warp.  Substitution is taken over summing powers of N because those grow
-// without bound for keys that resemble each other, while the entries of Tm do
-// not.  Rows 32-63 take four times the work of rows 0-31, and the remaining
-// warps none, so the CTAs of an SM give the long part to different warps.
+// Tm = (I + N)^-1 in place of N, in shared memory: the four 16 x 16 blocks of
+// the diagonal by substitution, then twice two neighbouring blocks' inverses
+// T1, T2 and the block N21 below T1 are joined by T21 = -T2 N21 T1 (16, then
+// 32 wide), in FP32.  The sum of powers of N would take fewer steps, but powers
+// grow without bound for keys that resemble each other, while Tm's entries do
+// not.  Substitution over all 64 columns took one warp 8300 cycles, most of
+// them waiting for itself; here every step but the first has all four warps.
 // P Tm is a product on the matrix unit, from and into X's own images.
-// Four CTAs fit an SM, so that one's substitution hides another's waits.
+// Four CTAs fit an SM, so that one's waits hide behind the others.
 constexpr int kNPitch = 68;    // floats a row of N: 16-byte writes of a warp's rows hit all banks
 constexpr int kPrepHeads = 4;  // value heads whose gates are made at once, one a warp
 
@@ -93,20 +93,79 @@ struct PrepSmem {
   static constexpr int kBytes = oBar + 64 + 1024;
 };
 
-template <int kFrom, int kTo>
-__device__ __forceinline__ void substitute(float2 (&x)[32], const float* n) {
+// Rows i0 .. i0 + kRows - 1, columns c .. c + 3 of -A B or A B, for A and B in
+// shared memory, row pitches pa and pb, kDepth deep.
+template <int kRows, int kDepth, bool kNegate>
+__device__ __forceinline__ void small_product(const float* A, int pa, const float* B, int pb, float* out, int po) {
+  float2 acc[kRows][2];
 #pragma unroll
-  for (int j = kFrom; j >= kTo; --j) {
-    const float xj = (j & 1) ? x[j / 2].y : x[j / 2].x;
-    const float2 m = splat2(-xj);
-    const float4* row = reinterpret_cast<const float4*>(n + j * kNPitch);
+  for (int i = 0; i < kRows; ++i) acc[i][0] = acc[i][1] = splat2(0.0f);
+#pragma unroll 2
+  for (int k = 0; k < kDepth; k += 4) {
+    float4 f[kRows];
 #pragma unroll
-    for (int q = 0; q <= (j - 1) / 4; ++q) {
-      const float4 f = row[q];
-      x[2 * q] = fma2(m, make_float2(f.x, f.y), x[2 * q]);
-      if (4 * q + 2 < j) x[2 * q + 1] = fma2(m, make_float2(f.z, f.w), x[2 * q + 1]);
+    for (int i = 0; i < kRows; ++i) f[i] = *reinterpret_cast<const float4*>(A + i * pa + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 b = *reinterpret_cast<const float4*>(B + (k + j) * pb);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float a = j == 0 ? f[i].x : j == 1 ? f[i].y : j == 2 ? f[i].z : f[i].w;
+        acc[i][0] = fma2(splat2(a), make_float2(b.x, b.y), acc[i][0]);
+        acc[i][1] = fma2(splat2(a), make_float2(b.z, b.w), acc[i][1]);
+      }
     }
   }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const float s = kNegate ? -1.0f : 1.0f;
+    *reinterpret_cast<float4*>(out + i * po) =
+        make_float4(s * acc[i][0].x, s * acc[i][0].y, s * acc[i][1].x, s * acc[i][1].y);
+  }
+}
+
+// (I + N)^-1 over N (64 rows, kNPitch floats apart, zero above the diagonal),
+// by 128 threads; y: 32 x 36 floats of scratch.
+__device__ __forceinline__ void invert(float* n, float* y, int t) {
+  if (t < 64) {
+    const int r = t & 15;
+    const float* block = n + (t & ~15) * (kNPitch + 1);
+    float2 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = make_float2(2 * i == r ? 1.0f : 0.0f, 2 * i + 1 == r ? 1.0f : 0.0f);
+    // x_j is final, then x_l -= x_j N_jl for l < j
+#pragma unroll
+    for (int j = 15; j >= 1; --j) {
+      const float2 m = splat2(-((j & 1) ? x[j / 2].y : x[j / 2].x));
+      const float4* row = reinterpret_cast<const float4*>(block + j * kNPitch);
+#pragma unroll
+      for (int q = 0; q <= (j - 1) / 4; ++q) {
+        const float4 f = row[q];
+        x[2 * q] = fma2(m, make_float2(f.x, f.y), x[2 * q]);
+        if (4 * q + 2 < j) x[2 * q + 1] = fma2(m, make_float2(f.z, f.w), x[2 * q + 1]);
+      }
+    }
+    __syncwarp();  // a warp holds whole blocks: all of its rows have been read
+    float* out = n + t * kNPitch + (t & ~15);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) *reinterpret_cast<float4*>(out + 2 * i) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
+  }
+  __syncthreads();
+  {
+    const int at = (t >> 6) * 32, i = (t >> 2) & 15, c = (t & 3) * 4;  // pair of blocks, row, columns
+    float* y1 = y + (t >> 6) * 16 * 20;
+    const float* n21 = n + (at + 16) * kNPitch + at;
+    small_product<1, 16, false>(n21 + i * kNPitch, 0, n + at * kNPitch + at + c, kNPitch, y1 + i * 20 + c, 0);
+    __syncthreads();
+    small_product<1, 16, true>(n + (at + 16 + i) * kNPitch + at + 16, 0, y1 + c, 20,
+                               n + (at + 16 + i) * kNPitch + at + c, 0);
+    __syncthreads();
+  }
+  const int i = (t >> 3) * 2, c = (t & 7) * 4;
+  small_product<2, 32, false>(n + (32 + i) * kNPitch, kNPitch, n + c, kNPitch, y + i * 36 + c, 36);
+  __syncthreads();
+  small_product<2, 32, true>(n + (32 + i) * kNPitch + 32, kNPitch, y + c, 36, n + (32 + i) * kNPitch + c, kNPitch);
+  __syncthreads();
 }
 
 template <IO kIO, int KP>
@@ -137,26 +196,89 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc<128>(tmem_at);
+  if (t < 32)  // N's upper right quarter, which nothing writes
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(sn + t * kNPitch + 32 + 4 * i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
+  // warp w: the gates of value head hh + w
+  auto make_gates = [&](int hh) {
+    if (hh + warp >= rep) return;
+    // the running sum of g, in double: differences of it enter exp
+    const int hw = kh * rep + hh + warp;
+    float g[2], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 2 * lane + i;
+      const int64_t at = (start + r) * a.Hv + hw;
+      g[i] = r < len ? a.g[at] : 0.0f;
+      b[i] = r < len ? a.beta[at] : 0.0f;
+      g[i] = g[i] < -256.0f ? -256.0f : g[i];  // exp of either is 0; -inf would leave inf - inf
+    }
+    double incl = (double)g[0] + (double)g[1];
+    const double own = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const double last = __shfl_sync(0xffffffffu, incl, 31);
+    const double G[2] = {incl - own + (double)g[0], incl};
+    float* gates = a.gates + (c * a.Hv + hw) * kDeltaGates;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 2 * lane + i;
+      const double G2 = G[i] * 1.4426950408889634;
+      const float hi = (float)G2, lo = (float)(G2 - (double)hi);
+      sg_all[warp * 64 + r] = make_float2(hi, lo);
+      sbeta_all[warp * 64 + r] = b[i];
+      const float gh = (float)G[i], dh = (float)(last - G[i]);
+      gates[r] = exp_f(gh) * (1.0f + (float)(G[i] - (double)gh));
+      gates[64 + r] = exp_f(dh) * (1.0f + (float)(last - G[i] - (double)dh)) * b[i];
+      gates[128 + r] = b[i];
+      gates[192 + r] = hi;
+      gates[256 + r] = lo;
+    }
+  };
   // the images of [K; Q]: rows past the chunk's end and columns past K are zero
   const T* kbase = static_cast<const T*>(a.k) + start * a.sk + (int64_t)kh * a.K;
   const T* qbase = static_cast<const T*>(a.q) + start * a.sq + (int64_t)kh * a.K;
-#pragma unroll 4
-  for (int i = t; i < 128 * KP * 8; i += 128) {
-    const int row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
-    uint8_t* image = images + (ch >> 3) * 16384;
-    const T* src = (row < 64 ? kbase + r * a.sk : qbase + r * a.sq) + ch * 8;
-    const bool in = r < len && ch * 8 < a.K;
-    if constexpr (kIO == IO::BF16) {
-      uint4 q = make_uint4(0, 0, 0, 0);
-      if (in) q = *reinterpret_cast<const uint4*>(src);
-      *reinterpret_cast<uint4*>(image + image_chunk<128>(row, ch & 7)) = q;
-    } else {
-      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (in) ld_io8(src, v);
-      put_chunk<NQ, 128>(image, kTerm, row, ch & 7, v);
+  if constexpr (kIO == IO::BF16) {
+#pragma unroll
+    for (int u = 0; u < KP * 8; ++u) {
+      const int i = t + u * 128, row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
+      const bool in = r < len && ch * 8 < a.K;
+      const T* src = in ? (row < 64 ? kbase + r * a.sk : qbase + r * a.sq) + ch * 8 : kbase;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       smem_u32(images + (ch >> 3) * 16384 + image_chunk<128>(row, ch & 7))),
+                   "l"(src), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  } else {
+    constexpr int kBatch = 4;  // reads in flight
+    for (int u = 0; u < KP * 8; u += kBatch) {
+      float4 f[kBatch][2];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = t + (u + k) * 128, row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
+        f[k][0] = f[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < len && ch * 8 < a.K) {
+          const float4* src = reinterpret_cast<const float4*>((row < 64 ? kbase + r * a.sk : qbase + r * a.sq) + ch * 8);
+          f[k][0] = src[0];
+          f[k][1] = src[1];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = t + (u + k) * 128, row = i / (KP * 8), ch = i % (KP * 8);
+        const float2 v[4] = {make_float2(f[k][0].x, f[k][0].y), make_float2(f[k][0].z, f[k][0].w),
+                             make_float2(f[k][1].x, f[k][1].y), make_float2(f[k][1].z, f[k][1].w)};
+        put_chunk<NQ, 128>(images + (ch >> 3) * 16384, kTerm, row, ch & 7, v);
+      }
     }
   }
+  make_gates(0);  // while [K; Q] is on its way
+  if constexpr (kIO == IO::BF16) asm volatile("cp.async.wait_group 0;" ::: "memory");
   fence_async_smem();
   tmem_fence_before_sync();
   __syncthreads();
@@ -176,43 +298,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
   for (int hh = 0; hh < rep; ++hh) {
     const int h = kh * rep + hh;
     const int64_t ch = c * a.Hv + h;
-    if (hh % kPrepHeads == 0 && hh + warp < rep) {
-      // the running sum of g, in double: differences of it enter exp
-      const int hw = h + warp;
-      float g[2], b[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * lane + i;
-        const int64_t at = (start + r) * a.Hv + hw;
-        g[i] = r < len ? a.g[at] : 0.0f;
-        b[i] = r < len ? a.beta[at] : 0.0f;
-        g[i] = g[i] < -256.0f ? -256.0f : g[i];  // exp of either is 0; -inf would leave inf - inf
-      }
-      double incl = (double)g[0] + (double)g[1];
-      const double own = incl;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const double last = __shfl_sync(0xffffffffu, incl, 31);
-      const double G[2] = {incl - own + (double)g[0], incl};
-      float* gates = a.gates + (ch + warp) * kDeltaGates;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * lane + i;
-        const double G2 = G[i] * 1.4426950408889634;
-        const float hi = (float)G2, lo = (float)(G2 - (double)hi);
-        sg_all[warp * 64 + r] = make_float2(hi, lo);
-        sbeta_all[warp * 64 + r] = b[i];
-        const float gh = (float)G[i], dh = (float)(last - G[i]);
-        gates[r] = exp_f(gh) * (1.0f + (float)(G[i] - (double)gh));
-        gates[64 + r] = exp_f(dh) * (1.0f + (float)(last - G[i] - (double)dh)) * b[i];
-        gates[128 + r] = b[i];
-        gates[192 + r] = hi;
-        gates[256 + r] = lo;
-      }
-    }
+    if (hh && hh % kPrepHeads == 0) make_gates(hh);
     if (t == 0) bulk_wait_read();  // [K; Q], or the last head's X, has left
     __syncthreads();
     if (hh == 0) {
@@ -226,12 +312,13 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
     const bool is_k = t < 64;
     {
       const float2 gi = sg[r];
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         if (half && !(warp & 1)) {  // rows 0-31 end before column 32
           if (!is_k) {
-            const float zero[32] = {};
-            put_row<NT, 128>(images, 16384, t, 4, zero);
+#pragma unroll
+            for (int k = 0; k < 4 * NT; ++k)
+              *reinterpret_cast<uint4*>(images + k / 4 * 16384 + image_chunk<128>(t, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
           }
           continue;
         }
@@ -249,24 +336,23 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(sn + r * kNPitch + half * 32 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
         } else {
-          put_row<NT, 128>(images, 16384, t, half * 4, d);
+          float2 p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = make_float2(d[2 * i], d[2 * i + 1]);
+          put_row<NT, 128>(images, 16384, t, half * 4, p);
         }
       }
     }
     __syncthreads();
-    const int role = (warp + blockIdx.x) & 3;
-    if (role < 2) {
-      const int tr = role * 32 + lane;
-      float2 x[32];
+    invert(sn, reinterpret_cast<float*>(images), t);  // scratch: where the rows of Tm go next
+    {
+      const int tr = t >> 1, side = t & 1;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = make_float2(2 * i == tr ? 1.0f : 0.0f, 2 * i + 1 == tr ? 1.0f : 0.0f);
-      if (role == 1) substitute<63, 32>(x, sn);
-      substitute<31, 1>(x, sn);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float v[8] = {x[4 * q].x, x[4 * q].y, x[4 * q + 1].x, x[4 * q + 1].y,
-                            x[4 * q + 2].x, x[4 * q + 2].y, x[4 * q + 3].x, x[4 * q + 3].y};
-        put_chunk<NT, 128>(images, 16384, tr, q, v);
+      for (int q = 0; q < 4; ++q) {
+        const float4* src = reinterpret_cast<const float4*>(sn + tr * kNPitch + side * 32 + q * 8);
+        const float4 f = src[0], g = src[1];
+        const float2 v[4] = {make_float2(f.x, f.y), make_float2(f.z, f.w), make_float2(g.x, g.y), make_float2(g.z, g.w)};
+        put_chunk<NT, 128>(images, 16384, tr, side * 4 + q, v);
       }
     }
     fence_async_smem();
@@ -283,11 +369,10 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
     phase ^= 1;
     tmem_fence_after_sync();
     if (!is_k) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half && !(warp & 1)) continue;
-        float d[32];
-        tmem_row<32>(mine + 64 + half * 32, d);
+#pragma unroll 1
+      for (int half = 0; half <= (warp & 1); ++half) {
+        float2 d[16];
+        tmem_sum<16, 1>(mine + 64 + half * 32, 0, d);
         put_row<NT, 128>(images, 16384, t, half * 4, d);
       }
     }

@@ -22,6 +22,8 @@
 
 namespace vssm {
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+
 // ------------------------------------------------------------------ images
 template <int kRowBytes>
 __device__ __forceinline__ uint32_t image_chunk(int row, int chunk) {
@@ -32,15 +34,13 @@ __device__ __forceinline__ uint32_t image_chunk(int row, int chunk) {
 
 // Two FP32 values as NT bf16 pairs (first value in the low half).
 template <int NT>
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&t)[NT]) {
+__device__ __forceinline__ void split_pair(float2 v, uint32_t (&t)[NT]) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     t[i] = *reinterpret_cast<const uint32_t*>(&h);
-    if (i + 1 < NT) {
-      a -= __uint_as_float(t[i] << 16);
-      b -= __uint_as_float(t[i] & 0xffff0000u);
-    }
+    if (i + 1 < NT)  // what this term leaves (exact)
+      v = fma2(make_float2(__uint_as_float(t[i] << 16), __uint_as_float(t[i] & 0xffff0000u)), splat2(-1.0f), v);
   }
 }
 
@@ -182,36 +182,42 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr) {  // warp-collecti
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
 }
 
-// The sum of kBlocks blocks, `stride` columns apart, last block first.
-template <int kCount, int kBlocks>
-__device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float (&v)[kCount]);
+// kPairs pairs of consecutive columns of this thread's lane, summed over
+// kBlocks blocks `stride` columns apart, last block first.  All loads are in
+// flight together.
+template <int kPairs, int kBlocks>
+__device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float2 (&v)[kPairs]) {
+  static_assert(kPairs == 8 || kPairs == 16, "16 or 32 columns");
+  __syncwarp();  // the load is warp-collective; a thread may come from a wait or from issuing products
+  uint32_t r[kBlocks][2 * kPairs];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    if constexpr (kPairs == 16) tmem_ld32(taddr + b * stride, r[b]);
+    else tmem_ld16(taddr + b * stride, r[b]);
+  }
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    if constexpr (kPairs == 16) tmem_wait_ld32(r[b]);
+    else tmem_wait_ld16(r[b]);
+  }
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    v[i] = make_float2(__uint_as_float(r[kBlocks - 1][2 * i]), __uint_as_float(r[kBlocks - 1][2 * i + 1]));
+#pragma unroll
+    for (int b = kBlocks - 2; b >= 0; --b)
+      v[i] = add2(v[i], make_float2(__uint_as_float(r[b][2 * i]), __uint_as_float(r[b][2 * i + 1])));
+  }
+}
 
 // kCount (16 or 32) consecutive columns of this thread's lane, as floats.
 template <int kCount>
 __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[kCount]) {
-  static_assert(kCount == 16 || kCount == 32, "16 or 32 columns");
-  __syncwarp();  // the load is warp-collective; a thread may come from a wait or from issuing products
-  uint32_t r[kCount];
-  if constexpr (kCount == 32) {
-    tmem_ld32(taddr, r);
-    tmem_wait_ld32(r);
-  } else {
-    tmem_ld16(taddr, r);
-    tmem_wait_ld16(r);
-  }
+  float2 p[kCount / 2];
+  tmem_sum<kCount / 2, 1>(taddr, 0, p);
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-template <int kCount, int kBlocks>
-__device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float (&v)[kCount]) {
-  tmem_row<kCount>(taddr + (kBlocks - 1) * stride, v);
-#pragma unroll
-  for (int b = kBlocks - 2; b >= 0; --b) {
-    float w[kCount];
-    tmem_row<kCount>(taddr + b * stride, w);
-#pragma unroll
-    for (int i = 0; i < kCount; ++i) v[i] += w[i];
+  for (int i = 0; i < kCount / 2; ++i) {
+    v[2 * i] = p[i].x;
+    v[2 * i + 1] = p[i].y;
   }
 }
 

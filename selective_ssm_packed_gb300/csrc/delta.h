@@ -71,6 +71,7 @@ struct DeltaArgs {
   // the plan of the pack and what the chunks keep (see DeltaLayout)
   int* info;      // [0]: chunks in the pack, -1 when cu_seqlens is malformed
   int* first;     // (S + 1): each sequence's first chunk
+  int* order;     // (S): the sequences, longest (about) first
   int4* table;    // per chunk: sequence, first token, tokens, place in the sequence
   float* gates;   // (chunks, Hv, kDeltaGates)
   uint8_t* kq;    // (chunks, Hk, in terms, K panels) images of [K; Q], 128 rows of 64

@@ -84,10 +84,10 @@ int check_pack(int64_t T, int32_t S, const int32_t* cu, int32_t Hk, int32_t Hv, 
 }
 
 // What the chunks keep for each other, one after the other:
-// [info][first chunks][chunk table][gates][images of [K; Q]][images of X], and
+// [info][first chunks][order][chunk table][gates][images of [K; Q]][images of X], and
 // in a saved array [images of S0][images of E] behind them.
 struct DeltaLayout {
-  size_t first, table, gates, kq, x, plan_end, s0, e, saved_end, ds, dvi, doi, bwd_end;
+  size_t first, order, table, gates, kq, x, plan_end, s0, e, saved_end, ds, dvi, doi, bwd_end;
 };
 
 DeltaLayout delta_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io) {
@@ -97,6 +97,7 @@ DeltaLayout delta_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO 
   const size_t rows = tiles * mid * kRowTile, states = rows * kp;
   size_t o = 256;
   l.first = o; o += up((S + 1) * sizeof(int));
+  l.order = o; o += up(S * sizeof(int));
   l.table = o; o += up(nc * sizeof(int4));
   l.gates = o; o += up(nc * Hv * kDeltaGates * sizeof(float));
   l.kq = o; o += up(nc * Hk * delta_in_terms(io) * kp * 16384);
@@ -122,6 +123,7 @@ void set_plan(DeltaArgs& a, const void* base, const DeltaLayout& l, bool saved) 
   char* p = const_cast<char*>(static_cast<const char*>(base));
   a.info = reinterpret_cast<int*>(p) + 32;  // past the status word
   a.first = reinterpret_cast<int*>(p + l.first);
+  a.order = reinterpret_cast<int*>(p + l.order);
   a.table = reinterpret_cast<int4*>(p + l.table);
   a.gates = reinterpret_cast<float*>(p + l.gates);
   a.kq = reinterpret_cast<uint8_t*>(p + l.kq);

@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
   const int panels = (a.V + BV - 1) / BV, groups = (panels + kWalks - 1) / kWalks;
   const int group = blockIdx.x % groups;
   const int h = blockIdx.x / groups % a.Hv;
-  const int s = blockIdx.x / groups / a.Hv;
   if (a.info[0] < 0) return;
+  const int s = a.order[blockIdx.x / groups / a.Hv];
   const int c0 = a.first[s], n = a.first[s + 1] - c0;
   const int64_t seq_start = a.cu[s], seq_len = a.cu[s + 1] - seq_start;
   const int kh = h / (a.Hv / a.Hk);

@@ -8,14 +8,26 @@ namespace {
 // ------------------------------------------------------------------ plan
 // Every block sums the sequences' chunk counts for itself (a pack has a few
 // thousand sequences, so that costs less than a second launch), block 0
-// writes the sums, and each block fills its share of the chunk table.
+// writes the sums, and each block fills its share of the chunk table.  Block 0
+// also orders the sequences by length for the walks, whose CTAs start in that
+// order: a long one that starts last would be walked alone.  The order is
+// exact to 16 chunks and to a quarter of a power of two above, and within a
+// class left to chance: it decides when a sequence is walked, not how.
 constexpr int kPlanThreads = 512;
+
+// Length class, longest first, of a sequence of n chunks.
+__device__ __forceinline__ int length_class(int n) {
+  if (n < 16) return 63 - n;
+  const int e = 31 - __clz(n);
+  return 63 - min(63, 16 + 4 * (e - 4) + ((n >> (e - 2)) & 3));
+}
 
 __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
   __shared__ int warp_sum[kPlanThreads / 32];
-  __shared__ int carry, bad;
+  __shared__ int carry, bad, classes[64];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, S = a.num_seqs;
   if (t == 0) carry = bad = 0;
+  if (t < 64) classes[t] = 0;
   __syncthreads();
   for (int base = 0; base < S; base += kPlanThreads) {
     const int s = base + t;
@@ -27,6 +39,7 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
       } else {
         n = (int)((hi - lo + kDeltaChunk - 1) / kDeltaChunk);
       }
+      if (blockIdx.x == 0) atomicAdd(&classes[length_class(n)], 1);
     }
     int incl = n;
 #pragma unroll
@@ -55,6 +68,19 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
   }
   __threadfence_block();
   __syncthreads();
+  if (blockIdx.x == 0 && ok) {
+    if (t == 0) {
+      int at = 0;
+      for (int i = 0; i < 64; ++i) {
+        const int k = classes[i];
+        classes[i] = at;
+        at += k;
+      }
+    }
+    __syncthreads();
+    for (int s = t; s < S; s += kPlanThreads)
+      a.order[atomicAdd(&classes[length_class(a.first[s + 1] - a.first[s])], 1)] = s;
+  }
   for (int c = blockIdx.x * kPlanThreads + t; c < total; c += gridDim.x * kPlanThreads) {
     int lo = 0, hi = S - 1;  // the last sequence whose first chunk is at or before c
     while (lo < hi) {

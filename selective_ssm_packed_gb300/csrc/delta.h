@@ -39,14 +39,14 @@ constexpr int kDeltaMaxK = 128, kDeltaMaxV = 1024;
 constexpr int kDeltaTile = 32;
 constexpr int kRowTile = 64 * 64;  // bytes of one term of 64 token rows of a tile
 
-// bf16 terms of an input and of an FP32 intermediate, the tiles of a walk, and
-// how many chunks of [K; Q] the walks hold.  bf16 inputs are exact in one term
+// bf16 terms of an input and of an FP32 intermediate, and how many chunks of
+// [K; Q] the walks hold.  bf16 inputs are exact in one term
 // and their intermediates carry two (16 bits, far below the rounding of the
 // outputs to bf16, and about 5e-6 on the FP32 ones); FP32 I/O carries three,
 // all 24 bits.
 template <IO kIO> struct DeltaTerms;
-template <> struct DeltaTerms<IO::BF16> { static constexpr int kIn = 1, kMid = 2, kTiles = 2, kStages = 2; };
-template <> struct DeltaTerms<IO::F32> { static constexpr int kIn = 3, kMid = 3, kTiles = 1, kStages = 1; };
+template <> struct DeltaTerms<IO::BF16> { static constexpr int kIn = 1, kMid = 2, kStages = 2; };
+template <> struct DeltaTerms<IO::F32> { static constexpr int kIn = 3, kMid = 3, kStages = 1; };
 inline int delta_in_terms(IO io) { return io == IO::BF16 ? 1 : 3; }
 inline int delta_mid_terms(IO io) { return io == IO::BF16 ? 2 : 3; }
 __host__ __device__ inline int delta_tiles(int V) { return (V + kDeltaTile - 1) / kDeltaTile; }
@@ -91,10 +91,13 @@ inline int64_t delta_max_chunks(int64_t T, int64_t num_seqs) {
   return T / kDeltaChunk + (num_seqs < T ? num_seqs : T);
 }
 
-// bf16 walks: two panels (128 columns) to a CTA, unless the panels are so few
-// that one each leaves no SM with two.
-inline bool delta_two_walks(const DeltaArgs& a) {
-  return a.V > 64 && (int64_t)a.num_seqs * a.Hv * ((a.V + 63) / 64) > 152;
+// Tiles a CTA of the walks takes: four (bf16) share what they read; fewer
+// where that leaves SMs without a CTA.
+inline int delta_walks(const DeltaArgs& a, IO io) {
+  if (io == IO::F32) return 1;  // three terms fill shared memory
+  const int64_t heads = (int64_t)a.num_seqs * a.Hv, tiles = delta_tiles(a.V);
+  if (tiles == 1 || heads * tiles <= 152) return 1;
+  return tiles == 2 || heads * ((tiles + 1) / 2) <= 152 ? 2 : 4;
 }
 
 cudaError_t launch_delta_plan(const DeltaArgs& a, cudaStream_t st);

@@ -18,9 +18,8 @@ template <IO kIO, int KP, int kWalks>
 struct BwdSmem {
   using D = DeltaTerms<kIO>;
   static constexpr int kKq = D::kIn * KP * 16384, kX = D::kMid * 16384;
-  static constexpr int kSTile = KP * 64 * 64, kSTerm = D::kTiles * kSTile;
-  static constexpr int kZTile = 128 * 64, kZTerm = D::kTiles * kZTile;
-  static constexpr int kS = D::kMid * kSTerm, kZ = D::kMid * kZTerm;
+  static constexpr int kSTile = KP * 64 * 64, kZTile = 128 * 64;
+  static constexpr int kS = D::kMid * kSTile, kZ = D::kMid * kZTile;
   static constexpr int oKq = 0, oX = oKq + D::kStages * kKq, oWalk = oX + kX;
   static constexpr int kWalk = kS + kZ;
   static constexpr int oBar = oWalk + kWalks * kWalk;
@@ -28,12 +27,12 @@ struct BwdSmem {
 };
 
 template <IO kIO, int KP, int kWalks>
-__global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
   using L = BwdSmem<kIO, KP, kWalks>;
-  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, NB = DeltaTerms<kIO>::kTiles,
-                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2, HP = HC / 2;
-  constexpr int kTmemCols = 2 * kWalks * NT * BV > 256 ? 512 : 256;
+  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, ST = DeltaTerms<kIO>::kStages, BV = kDeltaTile, HP = BV / 2;
+  constexpr int kTmemUsed = 2 * kWalks * NT * BV;
+  constexpr int kTmemCols = kTmemUsed > 256 ? 512 : kTmemUsed > 128 ? 256 : 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);
@@ -44,7 +43,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
   int* x_used = kq_used + ST;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int panels = (a.V + BV - 1) / BV, groups = (panels + kWalks - 1) / kWalks;
+  const int tiles = delta_tiles(a.V), groups = (tiles + kWalks - 1) / kWalks;
   const int group = blockIdx.x % groups;
   const int h = blockIdx.x / groups % a.Hv;
   if (a.info[0] < 0) return;
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
   const int c0 = a.first[s], n = a.first[s + 1] - c0;
   const int64_t seq_start = a.cu[s], seq_len = a.cu[s + 1] - seq_start;
   const int kh = h / (a.Hv / a.Hk);
-  const int walks = min(kWalks, panels - group * kWalks);
+  const int walks = min(kWalks, tiles - group * kWalks);
   if (n == 0 && !a.d_initial) return;
 
   // i counts the chunks walked: chunk n - 1 - i
@@ -91,23 +90,19 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
   const uint32_t tm = *tmem_at;
   Waiter wait{a.wait_ns, a.status};
 
-  if (warp / 8 < walks) {
-    const int walk = warp / 8, quad = warp & 3, half = warp >> 2 & 1;
+  if (warp / 4 < walks) {
+    const int walk = warp / 4, quad = warp & 3;
     const int row = quad * 32 + lane, r = row & 63;
-    const bool leader = (threadIdx.x & 255) == 96, porter = (threadIdx.x & 255) == 64;  // as in the forward
-    const int panel = group * kWalks + walk;
-    const int col0 = panel * BV + half * HC;
-    const int tiles = delta_tiles(a.V);
-    const int tile0 = panel * NB;
-    constexpr bool kTileEach = NB == 2;
-    const int in_tile = kTileEach ? half : 0, chunk0 = kTileEach ? 0 : half * HC / 8;
+    const bool leader = (threadIdx.x & 127) == 96, porter = (threadIdx.x & 127) == 64;  // as in the forward
+    const int tile = group * kWalks + walk;
+    const int col0 = tile * BV;
     uint8_t* sS = sm + L::oWalk + walk * L::kWalk;
     uint8_t* sZ = sS + L::kS;
-    uint8_t* z_mine = sZ + in_tile * L::kZTile;
     uint64_t* done = done_all + walk;
     const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
-    const uint32_t lane_at = ((uint32_t)(quad * 32) << 16) + half * HC;
-    constexpr int kSteps = HC / 16;  // of 16 columns: two chunks of an image's row, eight pairs
+    const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
+    constexpr int kSteps = BV / 16;  // of 16 columns: two chunks of an image's row, eight pairs
+    constexpr int kParts = 32 * (int)sizeof(T) / 64;  // 64-byte pieces of a row of io values
     const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
 
     float2 S[HP];
@@ -124,7 +119,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
     }
     // the next chunk's dO, raw, and gates: read a chunk ahead
     constexpr int kPer = 16 / (int)sizeof(T);
-    uint4 raw[4];
+    uint4 raw[kParts][4];
     float gam, decb, gam_end;
     auto prefetch = [&](int c) {
       const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
@@ -133,34 +128,37 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       gam_end = gates[63];
       const int64_t at = (int64_t)c * kDeltaChunk + (quad & 1) * 32;  // the warp's first token
       if (row >= 64)
-        load_rows(static_cast<const T*>(a.dout) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V,
-                  (int)min((int64_t)32, seq_len - at), a.V - col0, lane, raw);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          load_rows(static_cast<const T*>(a.dout) + ((seq_start + at) * a.Hv + h) * a.V + col0 + 16 * i,
+                    (int64_t)a.Hv * a.V, (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, raw[i]);
     };
     // rows 64-127: dO into sZ, as it is and scaled
     auto put_dout = [&]() {
-      transpose4(raw, lane);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) transpose4(raw[i], lane);
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
         float2 d[8];
 #pragma unroll
         for (int i = 0; i < 16 / kPer; ++i) {
           float2 w[kPer / 2];
-          unpack(raw[u * (16 / kPer) + i], w);
+          unpack(raw[u * kParts / 2][u * (16 / kPer) % 4 + i], w);
 #pragma unroll
           for (int j = 0; j < kPer / 2; ++j) d[i * (kPer / 2) + j] = w[j];
         }
-        put_row<NQ, 64>(z_mine, L::kZTerm, r, chunk0 + 2 * u, d);
+        put_row<NQ, 64>(sZ, L::kZTile, r, 2 * u, d);
         scale_row(d, a.scale * gam);
-        put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0 + 2 * u, d);
+        put_row<NT, 64>(sZ, L::kZTile, row, 2 * u, d);
       }
     };
     if (n > 0) {
       prefetch(n - 1);
       if (row >= 64) put_dout();
     }
-    if (row < KP * 64) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
+    if (row < KP * 64) put_row<NT, 64>(sS, L::kSTile, row, 0, S);
     fence_async_smem();
-    named_barrier(1 + walk, 256);
+    named_barrier(1 + walk, 128);
     uint32_t phase = 0;
 
     for (int i = 0; i < n; ++i) {
@@ -170,21 +168,12 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       const int64_t ch = (int64_t)(c0 + c) * a.Hv + h;
       const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq), x = smem_u32(sm + L::oX);
       if (porter) {
+
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          if (tile0 + b < tiles)
-#pragma unroll
-            for (int j = 0; j < NQ; ++j)
-              bulk_store_1d(a.doi + ((ch * tiles + tile0 + b) * NQ + j) * (size_t)kRowTile,
-                            sZ + j * L::kZTerm + b * L::kZTile, kRowTile);
+        for (int j = 0; j < NQ; ++j)
+          bulk_store_1d(a.doi + ((ch * tiles + tile) * NQ + j) * (size_t)kRowTile, sZ + j * L::kZTile, kRowTile);
         bulk_commit();
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          if (tile0 + b < tiles)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              bulk_store_1d(a.ds + ((ch * tiles + tile0 + b) * NT + j) * (size_t)L::kSTile,
-                            sS + j * L::kSTerm + b * L::kSTile, L::kSTile);
+        bulk_store_1d(a.ds + (ch * tiles + tile) * (size_t)(NT * L::kSTile), sS, NT * L::kSTile);
         bulk_commit();
         asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         mbar_arrive(done);  // dO's image has left, before Z takes its place
@@ -194,13 +183,13 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
         tmem_fence_after_sync();
         if (has_state) {
           const Operand<128, kKMajor, NQ, KP * 16384, 16384> A(kq);
-          const Operand<64, kMnMajor, NT, L::kSTerm, 0, L::kSTile> B(smem_u32(sS));
+          const Operand<64, kMnMajor, NT, L::kSTile, 0, L::kSTile> B(smem_u32(sS));
           umma_blocks<BV, KP * 4, NT, true>(tD1, A, B);
         }
         wait(x_full, i & 1);
         // (P Tm)^T: 64 rows; the instruction's other 64 come from whatever lies 8 KB further and are not read back
         const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x + 64 * 128);
-        const Operand<64, kMnMajor, NQ, L::kZTerm, 0, L::kZTile> B(smem_u32(sZ));
+        const Operand<64, kMnMajor, NQ, L::kZTile, 0, L::kZTile> B(smem_u32(sZ));
         umma_blocks<BV, 4, NT, true>(tD2, A, B);
         umma_commit(done);
       }
@@ -219,17 +208,17 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
 #pragma unroll
             for (int k = 0; k < 8; ++k) d[k] = splat2(0.0f);
           }
-          put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0 + 2 * u, d);
+          put_row<NT, 64>(sZ, L::kZTile, row, 2 * u, d);
         }
       }
       fence_async_smem();
       tmem_fence_before_sync();
       if (porter) mbar_arrive(done);
-      named_barrier(1 + walk, 256);
+      named_barrier(1 + walk, 128);
       if (leader) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x);
-        const Operand<64, kMnMajor, NT, L::kZTerm, 0, L::kZTile> B(smem_u32(sZ));
+        const Operand<64, kMnMajor, NT, L::kZTile, 0, L::kZTile> B(smem_u32(sZ));
         umma_blocks<BV, 4, NT, false>(tD2, A, B);
         umma_commit(done);
       }
@@ -239,21 +228,22 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       tmem_fence_after_sync();
       if (porter && i + 1 < n && last_user(x_used)) load_x(i + 1);
       if (row < 64) {
-        const int tile = tile0 + in_tile;
         uint8_t* to = a.dvi + (ch * tiles + tile) * (size_t)(NT * kRowTile);
-        uint4 q[4];
+        uint4 q[kParts][4];
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
           float2 d[8];
           tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
-          if (tile < tiles) put_row<NT, 64>(to, kRowTile, row, chunk0 + 2 * u, d);
-          pack(d, q + u * (4 / kSteps), T());
+          put_row<NT, 64>(to, kRowTile, row, 2 * u, d);
+          pack(d, q[u * kParts / 2] + u * (16 / kPer) % 4, T());
           scale_row(d, -g_row);
-          put_row<NT, 64>(z_mine, L::kZTerm, row, chunk0 + 2 * u, d);
+          put_row<NT, 64>(sZ, L::kZTile, row, 2 * u, d);
         }
         const int64_t at = (int64_t)c * kDeltaChunk + quad * 32;
-        store_rows(static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V,
-                   (int)min((int64_t)32, seq_len - at), a.V - col0, lane, q);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          store_rows(static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0 + 16 * i, (int64_t)a.Hv * a.V,
+                     (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, q[i]);
       }
       if (last && !a.d_initial) break;
       fence_async_smem();
@@ -262,11 +252,11 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
         bulk_wait_read();
         mbar_arrive(done);
       }
-      named_barrier(1 + walk, 256);
+      named_barrier(1 + walk, 128);
       if (leader) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);
-        const Operand<64, kMnMajor, NT, L::kZTerm, 0, L::kZTile> B(smem_u32(sZ));
+        const Operand<64, kMnMajor, NT, L::kZTile, 0, L::kZTile> B(smem_u32(sZ));
         umma_blocks<BV, 8, NT, true>(tD1, A, B);
         umma_commit(done);
       }
@@ -281,13 +271,13 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
           tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
 #pragma unroll
           for (int k = 0; k < 8; ++k) S[8 * u + k] = d[k] = fma2(splat2(g_end), S[8 * u + k], d[k]);
-          if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0 + 2 * u, d);
+          if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * u, d);
         }
       }
       if (!last && row >= 64) put_dout();
       fence_async_smem();
       tmem_fence_before_sync();
-      named_barrier(1 + walk, 256);
+      named_barrier(1 + walk, 128);
     }
     if (porter) bulk_wait_all();
     if (a.d_initial && row < a.K) {
@@ -308,9 +298,9 @@ cudaError_t run_bwd(const DeltaArgs& a, cudaStream_t st) {
   static_assert(bytes <= 227 * 1024, "shared memory");
   cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_bwd_kernel<kIO, KP, kWalks>), bytes);
   if (e != cudaSuccess) return e;
-  const int cols = DeltaTerms<kIO>::kTiles * kDeltaTile * kWalks;
+  const int groups = (delta_tiles(a.V) + kWalks - 1) / kWalks;
   delta_bwd_kernel<kIO, KP, kWalks>
-      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * ((a.V + cols - 1) / cols)), 256 * kWalks, bytes, st>>>(a);
+      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * groups), 128 * kWalks, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -319,8 +309,10 @@ cudaError_t run_bwd(const DeltaArgs& a, cudaStream_t st) {
 cudaError_t launch_delta_bwd(const DeltaArgs& a, IO io, cudaStream_t st) {
   if (a.num_seqs == 0) return cudaSuccess;
   const bool two = delta_panels_k(a.K) == 2;
+  const int walks = delta_walks(a, io);
   if (io == IO::BF16) {
-    if (delta_two_walks(a)) return two ? run_bwd<IO::BF16, 2, 2>(a, st) : run_bwd<IO::BF16, 1, 2>(a, st);
+    if (walks == 4) return two ? run_bwd<IO::BF16, 2, 4>(a, st) : run_bwd<IO::BF16, 1, 4>(a, st);
+    if (walks == 2) return two ? run_bwd<IO::BF16, 2, 2>(a, st) : run_bwd<IO::BF16, 1, 2>(a, st);
     return two ? run_bwd<IO::BF16, 2, 1>(a, st) : run_bwd<IO::BF16, 1, 1>(a, st);
   }
   return two ? run_bwd<IO::F32, 2, 1>(a, st) : run_bwd<IO::F32, 1, 1>(a, st);

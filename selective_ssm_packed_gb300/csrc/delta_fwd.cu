@@ -4,28 +4,29 @@
 namespace vssm {
 namespace {
 
-// One CTA per (sequence, value head, kWalks panels of the state's columns; the
-// columns never mix).  A walk is 256 threads and one panel of kTiles tiles:
-// the state lives in registers (FP32; thread = one row, half a panel) and as
-// bf16 terms in shared memory.  A chunk is three products on the matrix unit,
-// each read back from tensor memory by the walk's threads (warp w: lanes
-// 32 (w % 4) .., column half w / 4 % 2):
+// One CTA per (sequence, value head, kWalks tiles of the state's columns; the
+// columns never mix).  A walk is 128 threads and one tile: the state lives in
+// registers (FP32; thread = one row) and as bf16 terms in shared memory.  A
+// chunk is three products on the matrix unit, each read back from tensor
+// memory by the walk's threads:
 //   D1 = [K; Q] S0        rows 0-63 become R, rows 64-127 wait in tensor memory
 //   D2 = [Tm; P Tm] R     rows 0-63 are E, rows 64-127 with D1's make O
 //   D1 = K^T (dec beta E) and S1 = exp(G_63) S0 + D1
-// The chain product - read back - product bounds a walk, not the matrix unit,
-// so two walks share a CTA (and its [K; Q] and X) where there are enough
-// CTAs to fill the GPU: one multiplies while the other reads back.  [K; Q] and
-// X come by bulk copies, ahead of the walks, asked for by whichever walk is
-// through with the buffer last.  Two walks leave a thread 128 registers, so
-// they read back 16 columns at a time: one spilled register is a trip to L2,
-// shared memory having taken nearly all of L1.
+// The chain product - read back - product bounds a walk, not the matrix unit
+// (25% busy), so up to four walks share a CTA, its [K; Q] and its X: one
+// multiplies while others read back.  Wider tiles would read [K; Q] and X from
+// shared memory less often, but two walks of 64 columns took 1.6 times as long
+// as four of 32: with as many instructions to issue there were fewer chains to
+// issue them from.  [K; Q] and X come by bulk copies, ahead of the walks, asked
+// for by whichever walk is through with the buffer last.  Four walks leave a
+// thread 128 registers, so they read back 16 columns at a time: one spilled
+// register is a trip to L2, shared memory having taken nearly all of L1.
 template <IO kIO, int KP, int kWalks>
 struct FwdSmem {
   using D = DeltaTerms<kIO>;
   static constexpr int kKq = D::kIn * KP * 16384, kX = D::kMid * 16384;
-  static constexpr int kSTile = KP * 64 * 64, kSTerm = D::kTiles * kSTile, kRTerm = D::kTiles * kRowTile;
-  static constexpr int kS = D::kMid * kSTerm, kR = D::kMid * kRTerm;
+  static constexpr int kSTile = KP * 64 * 64;
+  static constexpr int kS = D::kMid * kSTile, kR = D::kMid * kRowTile;
   static constexpr int oKq = 0, oX = oKq + D::kStages * kKq, oWalk = oX + kX;
   static constexpr int kWalk = kS + 2 * kR;  // S, R, E
   static constexpr int oBar = oWalk + kWalks * kWalk;
@@ -33,12 +34,12 @@ struct FwdSmem {
 };
 
 template <IO kIO, int KP, int kWalks>
-__global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
   using L = FwdSmem<kIO, KP, kWalks>;
-  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, NB = DeltaTerms<kIO>::kTiles,
-                ST = DeltaTerms<kIO>::kStages, BV = NB * kDeltaTile, HC = BV / 2, HP = HC / 2;
-  constexpr int kTmemCols = 2 * kWalks * NT * BV > 256 ? 512 : 256;
+  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, ST = DeltaTerms<kIO>::kStages, BV = kDeltaTile, HP = BV / 2;
+  constexpr int kTmemUsed = 2 * kWalks * NT * BV;
+  constexpr int kTmemCols = kTmemUsed > 256 ? 512 : kTmemUsed > 128 ? 256 : 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
   int* x_used = kq_used + ST;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int panels = (a.V + BV - 1) / BV, groups = (panels + kWalks - 1) / kWalks;
+  const int tiles = delta_tiles(a.V), groups = (tiles + kWalks - 1) / kWalks;
   const int group = blockIdx.x % groups;
   const int h = blockIdx.x / groups % a.Hv;
   if (a.info[0] < 0) return;
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
   const int c0 = a.first[s], n = a.first[s + 1] - c0;
   const int64_t seq_start = a.cu[s], seq_len = a.cu[s + 1] - seq_start;
   const int kh = h / (a.Hv / a.Hk);
-  const int walks = min(kWalks, panels - group * kWalks);  // panels there are for this CTA
+  const int walks = min(kWalks, tiles - group * kWalks);  // tiles there are for this CTA
   if (n == 0 && !a.final_states) return;
 
   auto load_kq = [&](int c) {
@@ -95,25 +96,21 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
   const uint32_t tm = *tmem_at;
   Waiter wait{a.wait_ns, a.status};
 
-  if (warp / 8 < walks) {
-    const int walk = warp / 8, quad = warp & 3, half = warp >> 2 & 1;
+  if (warp / 4 < walks) {
+    const int walk = warp / 4, quad = warp & 3;
     const int row = quad * 32 + lane, r = row & 63;  // of a product: token (K rows, then Q rows) or state row
     // one thread issues the products, another the bulk copies: in warps of Q rows, whose read-backs are the shorter ones
-    const bool leader = (threadIdx.x & 255) == 96, porter = (threadIdx.x & 255) == 64;
-    const int panel = group * kWalks + walk;
-    const int col0 = panel * BV + half * HC;  // this thread's first state column
-    const int tiles = delta_tiles(a.V);
-    const int tile0 = panel * NB;
-    // where this thread's columns lie in an image of a panel: tile and first 16-byte chunk
-    constexpr bool kTileEach = NB == 2;  // a half panel is a tile, or half a tile
-    const int in_tile = kTileEach ? half : 0, chunk0 = kTileEach ? 0 : half * HC / 8;
+    const bool leader = (threadIdx.x & 127) == 96, porter = (threadIdx.x & 127) == 64;
+    const int tile = group * kWalks + walk;
+    const int col0 = tile * BV;
     uint8_t* sS = sm + L::oWalk + walk * L::kWalk;
     uint8_t* sR = sS + L::kS;
     uint8_t* sE = sR + L::kR;
     uint64_t* done = done_all + walk;
     const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
-    const uint32_t lane_at = ((uint32_t)(quad * 32) << 16) + half * HC;
-    constexpr int kSteps = HC / 16;  // of 16 columns: two chunks of an image's row, eight pairs
+    const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
+    constexpr int kSteps = BV / 16;  // of 16 columns: two chunks of an image's row, eight pairs
+    constexpr int kParts = 32 * (int)sizeof(T) / 64;  // 64-byte pieces of a row of io values
     const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
 
     float2 S[HP];
@@ -130,7 +127,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
     }
     // the next chunk's v, raw, and gates: read a chunk ahead
     constexpr int kPer = 16 / (int)sizeof(T);
-    uint4 raw[4];
+    uint4 raw[kParts][4];
     float gam, decb, gam_end;
     auto prefetch = [&](int c) {
       const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
@@ -139,13 +136,15 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       gam_end = gates[63];
       const int64_t at = (int64_t)c * kDeltaChunk + quad * 32;  // the warp's first token
       if (row < 64)
-        load_rows(static_cast<const T*>(a.v) + (seq_start + at) * a.sv + (int64_t)h * a.V + col0, a.sv,
-                  (int)min((int64_t)32, seq_len - at), a.V - col0, lane, raw);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          load_rows(static_cast<const T*>(a.v) + (seq_start + at) * a.sv + (int64_t)h * a.V + col0 + 16 * i, a.sv,
+                    (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, raw[i]);
     };
     if (n > 0) prefetch(0);
-    if (row < KP * 64) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0, S);
+    if (row < KP * 64) put_row<NT, 64>(sS, L::kSTile, row, 0, S);
     fence_async_smem();
-    named_barrier(1 + walk, 256);
+    named_barrier(1 + walk, 128);
     uint32_t phase = 0;
 
     for (int c = 0; c < n; ++c) {
@@ -155,13 +154,7 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       const int64_t ch = (int64_t)(c0 + c) * a.Hv + h;
       const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq);
       if (porter && a.s0) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-          if (tile0 + i < tiles)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              bulk_store_1d(a.s0 + ((ch * tiles + tile0 + i) * NT + j) * (size_t)L::kSTile,
-                            sS + j * L::kSTerm + i * L::kSTile, L::kSTile);
+        bulk_store_1d(a.s0 + (ch * tiles + tile) * (size_t)(NT * L::kSTile), sS, NT * L::kSTile);
         bulk_commit();
       }
       if (leader) {
@@ -169,13 +162,15 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
         tmem_fence_after_sync();
         if (has_state) {
           const Operand<128, kKMajor, NQ, KP * 16384, 16384> A(kq);
-          const Operand<64, kMnMajor, NT, L::kSTerm, 0, L::kSTile> B(smem_u32(sS));
+          const Operand<64, kMnMajor, NT, L::kSTile, 0, L::kSTile> B(smem_u32(sS));
           umma_blocks<BV, KP * 4, NT, true>(tD1, A, B);
           umma_commit(done);
         }
       }
       const float g_row = gam, db_row = decb, g_end = gam_end;
-      if (row < 64) transpose4(raw, lane);
+      if (row < 64)
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) transpose4(raw[i], lane);
       if (has_state) {
         wait(done, phase);
         phase ^= 1;
@@ -190,25 +185,25 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
 #pragma unroll
           for (int i = 0; i < 16 / kPer; ++i) {
             float2 w[kPer / 2];
-            unpack(raw[u * (16 / kPer) + i], w);
+            unpack(raw[u * kParts / 2][u * (16 / kPer) % 4 + i], w);
 #pragma unroll
             for (int j = 0; j < kPer / 2; ++j) {
               const int k = i * (kPer / 2) + j;
               d[k] = has_state ? fma2(splat2(-g_row), d[k], w[j]) : w[j];
             }
           }
-          put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0 + 2 * u, d);
+          put_row<NT, 64>(sR, kRowTile, row, 2 * u, d);
         }
       }
       fence_async_smem();
       tmem_fence_before_sync();
       if (porter && a.s0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last chunk's E has left
-      named_barrier(1 + walk, 256);
+      named_barrier(1 + walk, 128);
       if (leader) {
         tmem_fence_after_sync();
         wait(x_full, c & 1);
         const Operand<128, kKMajor, NT, 16384> A(smem_u32(sm + L::oX));
-        const Operand<64, kMnMajor, NT, L::kRTerm, 0, kRowTile> B(smem_u32(sR));
+        const Operand<64, kMnMajor, NT, kRowTile, 0, kRowTile> B(smem_u32(sR));
         umma_blocks<BV, 4, NT, true>(tD2, A, B);
         umma_commit(done);
       }
@@ -222,12 +217,12 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
         for (int u = 0; u < kSteps; ++u) {
           float2 d[8];
           tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
-          if (a.e) put_row<NT, 64>(sE + in_tile * kRowTile, L::kRTerm, row, chunk0 + 2 * u, d);
+          if (a.e) put_row<NT, 64>(sE, kRowTile, row, 2 * u, d);
           scale_row(d, db_row);
-          put_row<NT, 64>(sR + in_tile * kRowTile, L::kRTerm, row, chunk0 + 2 * u, d);
+          put_row<NT, 64>(sR, kRowTile, row, 2 * u, d);
         }
       } else {
-        uint4 q[4];
+        uint4 q[kParts][4];
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
           float2 d[8], o[8];
@@ -237,33 +232,29 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] = fma2(splat2(a.scale * g_row), o[i], d[i]);
           }
-          pack(d, q + u * (4 / kSteps), T());
+          pack(d, q[u * kParts / 2] + u * (16 / kPer) % 4, T());
         }
         const int64_t at = (int64_t)c * kDeltaChunk + (quad & 1) * 32;
-        store_rows(static_cast<T*>(a.out) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V,
-                   (int)min((int64_t)32, seq_len - at), a.V - col0, lane, q);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          store_rows(static_cast<T*>(a.out) + ((seq_start + at) * a.Hv + h) * a.V + col0 + 16 * i, (int64_t)a.Hv * a.V,
+                     (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, q[i]);
       }
       const bool stop = last && !a.final_states;
       if (stop && !a.e) break;
       fence_async_smem();
       tmem_fence_before_sync();
       if (porter && a.s0) bulk_wait_read();  // S0's images are free to be overwritten
-      named_barrier(1 + walk, 256);
+      named_barrier(1 + walk, 128);
       if (porter && a.e) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-          if (tile0 + i < tiles)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              bulk_store_1d(a.e + ((ch * tiles + tile0 + i) * NT + j) * (size_t)kRowTile,
-                            sE + j * L::kRTerm + i * kRowTile, kRowTile);
+        bulk_store_1d(a.e + (ch * tiles + tile) * (size_t)(NT * kRowTile), sE, NT * kRowTile);
         bulk_commit();
       }
       if (stop) break;
       if (leader) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);  // K^T: the first 64 rows
-        const Operand<64, kMnMajor, NT, L::kRTerm, 0, kRowTile> B(smem_u32(sR));
+        const Operand<64, kMnMajor, NT, kRowTile, 0, kRowTile> B(smem_u32(sR));
         umma_blocks<BV, 4, NT, true>(tD1, A, B);
         umma_commit(done);
       }
@@ -278,12 +269,12 @@ __global__ void __launch_bounds__(256 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
           tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
 #pragma unroll
           for (int i = 0; i < 8; ++i) S[8 * u + i] = d[i] = fma2(splat2(g_end), S[8 * u + i], d[i]);
-          if (!last) put_row<NT, 64>(sS + in_tile * L::kSTile, L::kSTerm, row, chunk0 + 2 * u, d);
+          if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * u, d);
         }
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      named_barrier(1 + walk, 256);
+      named_barrier(1 + walk, 128);
     }
     if (porter) bulk_wait_all();
     if (a.final_states && row < a.K) {
@@ -304,9 +295,9 @@ cudaError_t run_fwd(const DeltaArgs& a, cudaStream_t st) {
   static_assert(bytes <= 227 * 1024, "shared memory");
   cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_fwd_kernel<kIO, KP, kWalks>), bytes);
   if (e != cudaSuccess) return e;
-  const int cols = DeltaTerms<kIO>::kTiles * kDeltaTile * kWalks;
+  const int groups = (delta_tiles(a.V) + kWalks - 1) / kWalks;
   delta_fwd_kernel<kIO, KP, kWalks>
-      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * ((a.V + cols - 1) / cols)), 256 * kWalks, bytes, st>>>(a);
+      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * groups), 128 * kWalks, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -315,8 +306,10 @@ cudaError_t run_fwd(const DeltaArgs& a, cudaStream_t st) {
 cudaError_t launch_delta_fwd(const DeltaArgs& a, IO io, cudaStream_t st) {
   if (a.num_seqs == 0) return cudaSuccess;
   const bool two = delta_panels_k(a.K) == 2;
+  const int walks = delta_walks(a, io);
   if (io == IO::BF16) {
-    if (delta_two_walks(a)) return two ? run_fwd<IO::BF16, 2, 2>(a, st) : run_fwd<IO::BF16, 1, 2>(a, st);
+    if (walks == 4) return two ? run_fwd<IO::BF16, 2, 4>(a, st) : run_fwd<IO::BF16, 1, 4>(a, st);
+    if (walks == 2) return two ? run_fwd<IO::BF16, 2, 2>(a, st) : run_fwd<IO::BF16, 1, 2>(a, st);
     return two ? run_fwd<IO::BF16, 2, 1>(a, st) : run_fwd<IO::BF16, 1, 1>(a, st);
   }
   return two ? run_fwd<IO::F32, 2, 1>(a, st) : run_fwd<IO::F32, 1, 1>(a, st);

@@ -427,22 +427,40 @@ def _heads(t, name, dtype=None, heads=None, width=None):
     contiguous and whose tokens may be any distance apart."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be (tokens, heads, width), got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    T, H, K = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be (tokens, heads, width), got {tuple(shape)}")
+    T, H, K = shape
     if (heads is not None and H != heads) or (width is not None and K != width):
-        raise ValueError(f"{name} must be (tokens, {heads or H}, {width or K}), got {tuple(t.shape)}")
-    if t.numel() and ((K > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != K)):
+        raise ValueError(f"{name} must be (tokens, {heads or H}, {width or K}), got {tuple(shape)}")
+    along, across, inner = t.stride()
+    if ((K > 1 and inner != 1) or (H > 1 and across != K)) and t.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr() or None, (t.stride(0) if T > 1 else H * K)
+    return t.data_ptr() or None, (along if T > 1 else H * K)
 
 
 def _shaped(t, name, shape, dtype=torch.float32):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    """_ptr of a tensor of the given shape."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return _ptr(t, name, dtype)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _stream_of(t, stream):
+    """The raw handle of `stream`, or of the current stream of t's device
+    (looked up without building a torch.cuda.Stream, which takes longer than
+    a launch)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _asked(t, shape, like, dtype=torch.float32):
@@ -489,7 +507,7 @@ def varlen_qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=No
     k_out = torch.empty((T, Hk, K), dtype=q.dtype, device=q.device) if k_out is None else k_out
     _check(lib().varlen_qk_norm_rope_fwd(
         *lead, T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), _shaped(q_out, "q_out", (T, Hq, K), q.dtype),
-        _shaped(k_out, "k_out", (T, Hk, K), q.dtype), _ptr(status, "status", torch.int32), _stream(stream)),
+        _shaped(k_out, "k_out", (T, Hk, K), q.dtype), _ptr(status, "status", torch.int32), _stream_of(q, stream)),
         "varlen_qk_norm_rope_fwd")
     return q_out, k_out
 
@@ -512,7 +530,7 @@ def varlen_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_ou
         *lead, _shaped(dq_out, "dq_out", (T, Hq, K), q.dtype), _shaped(dk_out, "dk_out", (T, Hk, K), q.dtype),
         T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), _shaped(g["dq"], "dq", (T, Hq, K), q.dtype),
         _shaped(g["dk"], "dk", (T, Hk, K), q.dtype), _shaped(g["dq_weight"], "dq_weight", (K,)),
-        _shaped(g["dk_weight"], "dk_weight", (K,)), _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+        _shaped(g["dk_weight"], "dk_weight", (K,)), _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_of(q, stream)),
         "varlen_qk_norm_rope_bwd")
     return g
 
@@ -564,7 +582,7 @@ def varlen_gated_delta_fwd(q, k, v, g, beta, cu_seqlens, scale=None, out=None, s
         *args, float(K ** -0.5 if scale is None else scale), _ptr(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hk, Hv,
         K, V, dt, _shaped(out, "out", (T, Hv, V), q.dtype), _shaped(initial_states, "initial_states", (S, Hv, K, V)),
         _shaped(final_states, "final_states", (S, Hv, K, V)), _ptr(saved, "saved", torch.uint8),
-        saved.numel() if saved is not None else 0, _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)),
+        saved.numel() if saved is not None else 0, _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_of(q, stream)),
         "varlen_gated_delta_fwd")
     return (out, saved) + ((final_states,) if want_final else ())
 
@@ -593,7 +611,7 @@ def varlen_gated_delta_bwd(q, k, v, g, beta, dout, cu_seqlens, saved, scale=None
         saved.numel(), _shaped(d_final_states, "d_final_states", (S, Hv, K, V)),
         _shaped(r["d_initial_states"], "d_initial_states", (S, Hv, K, V)),
         *(_shaped(r[n], n, shape, d) for n, (shape, d) in shapes.items()),
-        _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)), "varlen_gated_delta_bwd")
+        _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_of(q, stream)), "varlen_gated_delta_bwd")
     return r
 
 
@@ -610,7 +628,7 @@ def varlen_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale=
     _check(lib().varlen_gated_delta_step(
         *args, float(K ** -0.5 if scale is None else scale), _shaped(states, "states", (slots, Hv, K, V)),
         _shaped(state_indices, "state_indices", (B,), torch.int32), slots, B, Hk, Hv, K, V, _dt(q),
-        _shaped(out, "out", (B, Hv, V), q.dtype), _ptr(status, "status", torch.int32), _stream(stream)),
+        _shaped(out, "out", (B, Hv, V), q.dtype), _ptr(status, "status", torch.int32), _stream_of(q, stream)),
         "varlen_gated_delta_step")
     return out
 

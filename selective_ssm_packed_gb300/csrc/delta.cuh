@@ -1,6 +1,8 @@
 // delta.cuh -- device helpers of the chunked gated delta rule's kernels.
 #pragma once
 
+#include <atomic>
+
 #include "delta.h"
 #include "umma.cuh"
 
@@ -175,9 +177,17 @@ __device__ __forceinline__ P* align1024(P* p) {
   return reinterpret_cast<P*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~(uintptr_t)1023);
 }
 
-// The work one chunk kernel's CTA finds for itself.
-inline cudaError_t set_smem(const void* f, size_t bytes) {
-  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Lets kernel f (one per call site: `done` is that site's own) use `bytes` of
+// shared memory, once per device.
+inline cudaError_t set_smem(const void* f, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
 }
 
 }  // namespace vssm

@@ -138,7 +138,7 @@ struct QkNormArgs {
   float* partial;               // bwd: per CTA sums of the weights' gradients
   int* status;
 };
-// Rows of K floats the backward's partial sums need (each of q and k).
+// Rows of K floats the backward's partial sums need.
 int qk_norm_partial_rows();
 cudaError_t launch_qk_norm_fwd(const QkNormArgs& a, IO io, cudaStream_t st);
 cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, IO io, cudaStream_t st);

@@ -304,7 +304,7 @@ int varlen_qk_norm_rope_fwd(const void* q, const void* k, int64_t q_stride, int6
 }
 
 size_t varlen_qk_norm_rope_bwd_workspace_size(int32_t K) {
-  return K < 8 || K > 256 || K % 8 ? 0 : 256 + sizeof(float) * 2 * (size_t)K * qk_norm_partial_rows();
+  return K < 8 || K > 256 || K % 8 ? 0 : 256 + sizeof(float) * (size_t)K * qk_norm_partial_rows();
 }
 
 int varlen_qk_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int64_t k_stride,

@@ -293,7 +293,8 @@ template <IO kIO, int KP, int kWalks>
 cudaError_t run_fwd(const DeltaArgs& a, cudaStream_t st) {
   constexpr size_t bytes = FwdSmem<kIO, KP, kWalks>::kBytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_fwd_kernel<kIO, KP, kWalks>), bytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_fwd_kernel<kIO, KP, kWalks>), bytes, done);
   if (e != cudaSuccess) return e;
   const int groups = (delta_tiles(a.V) + kWalks - 1) / kWalks;
   delta_fwd_kernel<kIO, KP, kWalks>

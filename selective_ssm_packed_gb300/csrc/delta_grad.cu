@@ -369,7 +369,8 @@ template <IO kIO, int KP>
 cudaError_t run_grads(const DeltaArgs& a, cudaStream_t st) {
   constexpr size_t bytes = GradSmem<kIO, KP>::kBytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_grad_kernel<kIO, KP>), bytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_grad_kernel<kIO, KP>), bytes, done);
   if (e != cudaSuccess) return e;
   delta_grad_kernel<kIO, KP><<<(unsigned)(a.max_chunks * a.Hk), 256, bytes, st>>>(a);
   return cudaGetLastError();

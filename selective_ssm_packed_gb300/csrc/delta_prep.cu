@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
 template <IO kIO, int KP>
 cudaError_t run_prep(const DeltaArgs& a, cudaStream_t st) {
   constexpr size_t bytes = PrepSmem<kIO, KP>::kBytes;
-  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_prep_kernel<kIO, KP>), bytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_prep_kernel<kIO, KP>), bytes, done);
   if (e != cudaSuccess) return e;
   delta_prep_kernel<kIO, KP><<<(unsigned)(a.max_chunks * a.Hk), 128, bytes, st>>>(a);
   return cudaGetLastError();

@@ -5,35 +5,36 @@
 namespace vssm {
 namespace {
 
-// One CTA of 256 threads per (token, value head, 32 state columns): 8 threads
-// along the columns (float4 each), 32 along the state rows, up to four rows a
-// thread, so that a thread has its whole share of the state in flight at once
-// and in registers until it is written back.  With S' = exp(g) S, both sums
+// One CTA of 256 threads per (token, value head, kCols state columns): kCols / 4
+// threads along the columns (float4 each), the others along the state rows, so
+// that a thread has its whole share of the state (16 to 64 bytes a row, up to 8
+// rows) in flight at once and in registers until it is written back.  With S' = exp(g) S, both sums
 // over the state rows come from S' in one pass:
 //   p = S'^T k, w = S'^T q;  u = beta (v - p);  S = S' + k u^T;
 //   o = scale (w + (k . q) u)
 // since S^T q = S'^T q + u (k . q).  The state is read and written once, which
 // is all the traffic that counts.
-constexpr int kStepThreads = 256, kStepCols = 32, kStepRows = 32;
+constexpr int kStepThreads = 256;
 
-template <typename T>
+template <typename T, int kCols>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(DeltaStepArgs a) {
-  __shared__ float part[8][2][kStepCols];
+  constexpr int kAlong = kCols / 4, kStep = kStepThreads / kAlong, kPer = kDeltaMaxK / kStep;
+  __shared__ float part[8][2][kCols];
   __shared__ float part_kq[8];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int cx = t & 7, ry = t >> 3;
-  const int slabs = (a.V + kStepCols - 1) / kStepCols;
+  const int cx = t % kAlong, ry = t / kAlong;
+  const int slabs = (a.V + kCols - 1) / kCols;
   const int slab = blockIdx.x % slabs;
   const int h = blockIdx.x / slabs % a.Hv;
   const int64_t b = blockIdx.x / slabs / a.Hv;
-  const int col = slab * kStepCols + cx * 4;
+  const int col = slab * kCols + cx * 4;
   T* out = static_cast<T*>(a.out) + (b * a.Hv + h) * a.V;
   const int64_t slot = a.indices ? (int64_t)a.indices[b] : b;
   if (slot < 0 || slot >= a.slots) {  // a padded entry, or an index outside the pool
     const bool outside = slot >= a.slots;
     if (outside && t == 0 && a.status) atomicOr(a.status, kStatusBadIndex);
-    const int c = slab * kStepCols + t;
-    if (t < kStepCols && c < a.V) out[c] = from_f<T>(outside ? __int_as_float(0x7fffffff) : 0.0f);
+    const int c = slab * kCols + t;
+    if (t < kCols && c < a.V) out[c] = from_f<T>(outside ? __int_as_float(0x7fffffff) : 0.0f);
     return;
   }
   float* state = a.states + (slot * a.Hv + h) * (int64_t)a.K * a.V;
@@ -41,11 +42,11 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(DeltaStepArgs 
   const T* kp = static_cast<const T*>(a.k) + b * a.sk + (int64_t)kh * a.K;
   const T* qp = static_cast<const T*>(a.q) + b * a.sq + (int64_t)kh * a.K;
 
-  float4 s[4];
-  float kv[4], qv[4];
+  float4 s[kPer];
+  float kv[kPer], qv[kPer];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = ry + kStepRows * i;
+  for (int i = 0; i < kPer; ++i) {
+    const int row = ry + kStep * i;
     s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     kv[i] = qv[i] = 0.0f;
     if (row < a.K) {
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(DeltaStepArgs 
   float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = p;
   float kq = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     s[i].x *= alpha; s[i].y *= alpha; s[i].z *= alpha; s[i].w *= alpha;
     p.x = fmaf(kv[i], s[i].x, p.x); p.y = fmaf(kv[i], s[i].y, p.y);
     p.z = fmaf(kv[i], s[i].z, p.z); p.w = fmaf(kv[i], s[i].w, p.w);
@@ -69,16 +70,16 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(DeltaStepArgs 
     w.z = fmaf(qv[i], s[i].z, w.z); w.w = fmaf(qv[i], s[i].w, w.w);
     kq = fmaf(kv[i], qv[i], kq);
   }
-  // over the warp's four row groups, then over the warps
+  // over the warp's row groups, then over the warps
 #pragma unroll
-  for (int o = 8; o <= 16; o <<= 1) {
+  for (int o = kAlong; o <= 16; o <<= 1) {
     p.x += __shfl_xor_sync(0xffffffffu, p.x, o); p.y += __shfl_xor_sync(0xffffffffu, p.y, o);
     p.z += __shfl_xor_sync(0xffffffffu, p.z, o); p.w += __shfl_xor_sync(0xffffffffu, p.w, o);
     w.x += __shfl_xor_sync(0xffffffffu, w.x, o); w.y += __shfl_xor_sync(0xffffffffu, w.y, o);
     w.z += __shfl_xor_sync(0xffffffffu, w.z, o); w.w += __shfl_xor_sync(0xffffffffu, w.w, o);
     kq += __shfl_xor_sync(0xffffffffu, kq, o);
   }
-  if (lane < 8) {
+  if (lane < kAlong) {
     *reinterpret_cast<float4*>(&part[warp][0][cx * 4]) = p;
     *reinterpret_cast<float4*>(&part[warp][1][cx * 4]) = w;
     if (lane == 0) part_kq[warp] = kq;
@@ -94,8 +95,8 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(DeltaStepArgs 
   }
   const float4 u = make_float4(beta * (v.x - p.x), beta * (v.y - p.y), beta * (v.z - p.z), beta * (v.w - p.w));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = ry + kStepRows * i;
+  for (int i = 0; i < kPer; ++i) {
+    const int row = ry + kStep * i;
     if (row < a.K && col < a.V)
       __stcs(reinterpret_cast<float4*>(state + (int64_t)row * a.V + col),
              make_float4(fmaf(kv[i], u.x, s[i].x), fmaf(kv[i], u.y, s[i].y), fmaf(kv[i], u.z, s[i].z),
@@ -115,12 +116,18 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(DeltaStepArgs 
 }  // namespace
 
 cudaError_t launch_delta_step(const DeltaStepArgs& a, IO io, cudaStream_t st) {
-  const int64_t blocks = a.B * a.Hv * ((a.V + kStepCols - 1) / kStepCols);
-  if (blocks == 0) return cudaSuccess;
-  if (io == IO::BF16)
-    delta_step_kernel<__nv_bfloat16><<<(unsigned)blocks, kStepThreads, 0, st>>>(a);
-  else
-    delta_step_kernel<float><<<(unsigned)blocks, kStepThreads, 0, st>>>(a);
+  if (a.B == 0) return cudaSuccess;
+  // wide CTAs have twice the bytes in flight, once there are enough of them
+  const int64_t heads = a.B * a.Hv, wide = heads * ((a.V + 63) / 64), narrow = heads * ((a.V + 31) / 32);
+  const bool use_wide = wide >= 152 * 4;
+  const unsigned blocks = (unsigned)(use_wide ? wide : narrow);
+  if (io == IO::BF16) {
+    if (use_wide) delta_step_kernel<__nv_bfloat16, 64><<<blocks, kStepThreads, 0, st>>>(a);
+    else delta_step_kernel<__nv_bfloat16, 32><<<blocks, kStepThreads, 0, st>>>(a);
+  } else {
+    if (use_wide) delta_step_kernel<float, 64><<<blocks, kStepThreads, 0, st>>>(a);
+    else delta_step_kernel<float, 32><<<blocks, kStepThreads, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -5,16 +5,17 @@
 namespace vssm {
 namespace {
 
-// One CTA of 256 threads per chunk and key head; the value heads that share the key head follow each other, and dq and dk are summed
-// over them in registers, in that order.  Products over the state's columns
-// (tile by tile) and over the chunk's tokens; dq and dk appear transposed,
-// state row by token, so that every product fills the matrix unit's 128 rows:
-//   A1 = S0 dV^T   A2 = dS1 E^T   A3 = S0 dO^T   (rows: state rows)
-//   W  = [dV; dO] E^T             QK = [K; Q] K^T
-//   CK = K^T M2^T + K^T M2 + Q^T M1               CQ = K^T M1^T
-// All are 64 columns wide: 448 of the SM's 512 columns of tensor memory.
-// What the call reads (two states and three sets of rows per head) bounds it,
-// so the next tiles are on their way through everything else.
+// One CTA of 256 threads per chunk and key head; the value heads that share
+// the key head follow each other, and dq and dk are summed over them in
+// registers, in that order.  Products over the state's columns (tile by tile)
+// and over the chunk's tokens, rows 0-63 for the keys' tokens and 64-127 for
+// the queries':
+//   A = [dV; dO] S0^T    B = E dS1^T (rows 0-63)    W = [dV; dO] E^T    QK = [K; Q] K^T
+//   C = [M2; M1] K       F = [M2; M1]^T [K; Q] (rows 0-63)
+// A, B, C and F are as wide as a state has rows; C takes W's and QK's columns,
+// so the four fill the SM's tensor memory.  Thread = one row, half the columns
+// (warp w: lanes 32 (w % 4) .., half w / 4).  The next tiles are on their way
+// through everything else.
 template <IO kIO, int KP>
 struct GradSmem {
   using D = DeltaTerms<kIO>;
@@ -24,11 +25,12 @@ struct GradSmem {
   static constexpr int kSTerm = KP * 64 * 64, kS = NT * kSTerm, kE = NT * kRowTile, kW = NT * 2 * kRowTile;
   // a stage: S0, dS1, E, then term by term 64 rows of dV and 64 of dO
   static constexpr int oS0 = 0, oDs = kS, oE = 2 * kS, oW = oE + kE, kStage = oW + kW;
-  static constexpr int kM = NT * 8192;
-  // M2 and M1: of their own, or (FP32, one stage) over S0 and dS1
+  static constexpr int kM = NT * 16384;  // [M2; M1], 128 rows of 64
+  // M of its own, or (FP32, one stage) over the stage
   static constexpr bool kOwnM = kIO == IO::BF16;
-  static constexpr int oKq = 0, oStage = kKq, oM2 = kOwnM ? oStage + kStages * kStage : oStage, oM1 = oM2 + kM;
-  static constexpr int kBehindM = oM1 + kM, kBehindStage = oStage + kStages * kStage;
+  static constexpr int oKq = 0, oStage = kKq, oM = kOwnM ? oStage + kStages * kStage : oStage;
+  // F's instructions read 8 KB past M's last image for rows that are not read back
+  static constexpr int kBehindM = oM + kM + 8192, kBehindStage = oStage + kStages * kStage;
   static constexpr int oF = kBehindM > kBehindStage ? kBehindM : kBehindStage;  // floats below
   static constexpr int kFloats = 320 + 256 + 256 + 256 + 256 + 64 + 64;
   static constexpr int oBar = oF + kFloats * 4;
@@ -49,14 +51,19 @@ __device__ __forceinline__ float lane_column_sum(float (&v)[32], int lane) {
   return v[0];
 }
 
-// Element (row, col) of the [K; Q] images: the sum of its terms.
+// 8 elements of row `row` of the [K; Q] images, from column col: the sums of
+// their terms.
 template <int NQ, int KP>
-__device__ __forceinline__ float kq_at(const uint8_t* images, int row, int col) {
-  const uint8_t* p = images + (col >> 6) * 16384 + image_chunk<128>(row, (col >> 3) & 7) + (col & 7) * 2;
-  float v = 0.0f;
+__device__ __forceinline__ void kq_at(const uint8_t* images, int row, int col, float2 (&v)[4]) {
+  const uint8_t* p = images + (col >> 6) * 16384 + image_chunk<128>(row, (col >> 3) & 7);
+  unpack(*reinterpret_cast<const uint4*>(p + (NQ - 1) * KP * 16384), v);
 #pragma unroll
-  for (int i = NQ - 1; i >= 0; --i) v += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p + i * KP * 16384));
-  return v;
+  for (int i = NQ - 2; i >= 0; --i) {
+    float2 w[4];
+    unpack(*reinterpret_cast<const uint4*>(p + i * KP * 16384), w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = add2(v[j], w[j]);
+  }
 }
 
 template <IO kIO, int KP>
@@ -68,9 +75,9 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   uint8_t* sm = align1024(smem_raw);
   float* sgate = reinterpret_cast<float*>(sm + L::oF);
   float* scol = sgate + 320;   // [quad][64]: column sums of W / beta, no diagonal
-  float* skap = scol + 256;    // [quad][64]
-  float* stau = skap + 256;    // [quad][64]
-  float* srow = stau + 256;    // [half][128]: row sums of W, no diagonal
+  float* sdots = scol + 256;   // [half][128]: rows of A times rows of [K; Q]
+  float* skap = sdots + 256;   // [half][64]: rows of B times rows of K
+  float* srow = skap + 256;    // [half][128]: row sums of W, no diagonal
   float* sdot = srow + 256;    // [warp]: parts of <dS1, S0>
   float* sdiag = sdot + 64;    // diagonal of W / beta
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::oBar);
@@ -143,221 +150,238 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
     bulk_load_1d(sm + L::oKq, a.kq + (size_t)(c * a.Hk + kh) * L::kKq, L::kKq, kq_full);
     for (int i = 0; i < ST && i < rep * tiles; ++i) load(i);
   }
-  {
-    const int row = quad * 32 + lane, r = row & 63;
-    const bool is_k = row < 64;
-    const uint32_t tA1 = tm, tA2 = tm + 64, tA3 = tm + 128, tW = tm + 192, tQK = tm + 256, tCK = tm + 320, tCQ = tm + 384;
-    const uint32_t mine = ((uint32_t)(quad * 32) << 16) + half * 32;
-    const uint32_t kq = smem_u32(sm + L::oKq);
-    uint32_t done_phase = 0;
+  constexpr int kWide = KP * 64, kMine = kWide / 2, kSteps = kMine / 16;  // state rows, and a thread's share of them
+  const int row = quad * 32 + lane, r = row & 63;
+  const bool is_k = row < 64;
+  const uint32_t tA = tm, tB = tm + 128, tC = tm + 256, tW = tC, tQK = tC + 64, tF = tm + 384;
+  const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
+  const uint32_t kq = smem_u32(sm + L::oKq), m_at = smem_u32(sm + L::oM);
+  const bool leader = t == 3 * 32;  // issues the products; its warp takes no part in <dS1, S0>
+  uint32_t done_phase = 0;
+  wait(kq_full, 0);
 
-    float acc_k[32], acc_q[32];
+  float2 acc[kMine / 2];  // of dk (rows 0-63) or dq
 #pragma unroll
-    for (int i = 0; i < 32; ++i) acc_k[i] = acc_q[i] = 0.0f;
+  for (int i = 0; i < kMine / 2; ++i) acc[i] = splat2(0.0f);
 
-    for (int hh = 0; hh < rep; ++hh) {
-      const int h = kh * rep + hh;
-      const int64_t ch = c * a.Hv + h;
-      float dot = 0.0f;
-      for (int i = t; i < 320; i += 256) sgate[i] = a.gates[ch * kDeltaGates + i];
-      if (t == 0 && hh == 0) {
-        wait(kq_full, 0);
-        tmem_fence_after_sync();
-        const Operand<128, kKMajor, NQ, KP * 16384, 16384> KQ(kq);
-        umma_terms<64, KP * 4, NQ>(tQK, KQ, KQ, false);
-      }
-      for (int p = 0; p < tiles; ++p) {
-        const int i = hh * tiles + p, st = i % ST;
-        uint8_t* stage = sm + L::oStage + st * L::kStage;
-        wait(&full[st], (i / ST) & 1);
-        if (t == 0) {
-          tmem_fence_after_sync();
+  for (int hh = 0; hh < rep; ++hh) {
+    const int h = kh * rep + hh;
+    const int64_t ch = c * a.Hv + h;
+    float dot = 0.0f;
+    for (int i = t; i < 320; i += 256) sgate[i] = a.gates[ch * kDeltaGates + i];
+    if (leader) {
+      tmem_fence_after_sync();
+      const Operand<128, kKMajor, NQ, KP * 16384, 16384> KQ(kq);
+      umma_terms<64, KP * 4, NQ>(tQK, KQ, KQ, false);
+    }
+    for (int p = 0; p < tiles; ++p) {
+      const int i = hh * tiles + p, st = i % ST;
+      uint8_t* stage = sm + L::oStage + st * L::kStage;
+      wait(&full[st], (i / ST) & 1);
+      if (warp == 3) {
+        if (leader) {
           const uint32_t at = smem_u32(stage);
           const Operand<64, kKMajor, NT, L::kSTerm> S0(at + L::oS0), dS(at + L::oDs);
           const Operand<64, kKMajor, NT, kRowTile> E(at + L::oE);
           const Operand<64, kKMajor, NT, 2 * kRowTile> dW(at + L::oW);
-          const Operand<64, kKMajor, NQ, 2 * kRowTile> dO(at + L::oW + kRowTile);
           umma_terms<64, 2, NT>(tW, dW, E, p > 0);
-          umma_terms<64, 2, NT>(tA1, S0, dW, p > 0);
-          umma_terms<64, 2, NT>(tA3, S0, dO, p > 0);
-          umma_terms<64, 2, NT>(tA2, dS, E, p > 0);
+          umma_terms<kWide, 2, NT>(tA, dW, S0, p > 0);
+          umma_terms<kWide, 2, NT>(tB, E, dS, p > 0);
           umma_commit(&empty[st]);
           if (p + 1 == tiles) umma_commit(done);
         }
+        __syncwarp();
+      } else {
         // <dS1, S0> over the tile: both images are permuted alike
-        for (int k = t; k < L::kSTerm / 16; k += 256) {
-          float x[8], y[8];
+        for (int k = t - (warp > 3 ? 32 : 0); k < L::kSTerm / 16; k += 224) {
+          float2 x[4], y[4], w[4];
+          unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + (NT - 1) * L::kSTerm + k * 16), x);
+          unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + (NT - 1) * L::kSTerm + k * 16), y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+          for (int m = NT - 2; m >= 0; --m) {
+            unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + m * L::kSTerm + k * 16), w);
 #pragma unroll
-          for (int m = NT - 1; m >= 0; --m) {
-            float w[8];
-            ld_io8(reinterpret_cast<const __nv_bfloat16*>(stage + L::oS0 + m * L::kSTerm + k * 16), w);
+            for (int j = 0; j < 4; ++j) x[j] = add2(x[j], w[j]);
+            unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + m * L::kSTerm + k * 16), w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] += w[j];
-            ld_io8(reinterpret_cast<const __nv_bfloat16*>(stage + L::oDs + m * L::kSTerm + k * 16), w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] += w[j];
+            for (int j = 0; j < 4; ++j) y[j] = add2(y[j], w[j]);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
+          for (int j = 0; j < 4; ++j) dot = fmaf(x[j].x, y[j].x, fmaf(x[j].y, y[j].y, dot));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
-        if (copier && (L::kOwnM || p + 1 < tiles)) refill(i);
       }
-      wait(done, done_phase);
-      done_phase ^= 1;
-      tmem_fence_after_sync();
-      named_barrier(1, 256);  // the gates are in; every warp is through with the last tile
-
-      // M1 and M2, and what their elements add to dg and dbeta
-      {
-        float m[32], qk[32];
-        tmem_row<32>(tW + mine, m);
-        tmem_row<32>(tQK + mine, qk);
-        const float gi = sgate[192 + r], gl = sgate[256 + r];
-        float rows = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int j = half * 32 + i;
-          const float d = ex2((gi - sgate[192 + j]) + (gl - sgate[256 + j]));
-          const bool in = is_k ? j < r : j <= r;
-          const float w = in ? (is_k ? -d : a.scale * d) * m[i] : 0.0f;
-          const float b = sgate[128 + j];
-          m[i] = w * b;
-          qk[i] = in ? w * qk[i] : 0.0f;
-          if (j == r) {
-            if (!is_k) sdiag[r] = qk[i];
-            qk[i] = 0.0f;
-          }
-          rows = fmaf(qk[i], b, rows);
-        }
-        float2 mp[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mp[i] = make_float2(m[2 * i], m[2 * i + 1]);
-        put_row<NT, 128>(sm + (is_k ? L::oM2 : L::oM1), 8192, r, half * 4, mp);
-        srow[half * 128 + row] = rows;
-        scol[quad * 64 + half * 32 + lane] = lane_column_sum(qk, lane);
-      }
-      fence_async_smem();
-      tmem_fence_before_sync();
-      named_barrier(1, 256);
-      if (t == 0) {
-        tmem_fence_after_sync();
-        const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> K(kq), Q(kq + 64 * 128);
-        const Operand<128, kKMajor, NT, 8192> M2t(smem_u32(sm + L::oM2)), M1t(smem_u32(sm + L::oM1));
-        const Operand<128, kMnMajor, NT, 8192> M2(smem_u32(sm + L::oM2)), M1(smem_u32(sm + L::oM1));
-        umma_terms<64, 4, NT>(tCK, K, M2t, false);
-        umma_terms<64, 4, NT>(tCK, K, M2, true);
-        umma_terms<64, 4, NT>(tCK, Q, M1, true);
-        umma_terms<64, 4, NT>(tCQ, K, M1t, false);
-        umma_commit(done);
-      }
-      // while that runs: the parts of dq and dk from the states
-      {
-        float kap[32], tau[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) kap[i] = tau[i] = 0.0f;
-        if (row < KP * 64) {
-          float x[32];
-          tmem_row<32>(tA1 + mine, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = half * 32 + i;
-            const float w = -sgate[j] * x[i];
-            acc_k[i] += w;
-            tau[i] = w * kq_at<NQ, KP>(sm + L::oKq, j, row);
-          }
-          tmem_row<32>(tA3 + mine, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = half * 32 + i;
-            const float w = a.scale * sgate[j] * x[i];
-            acc_q[i] += w;
-            tau[i] = fmaf(w, kq_at<NQ, KP>(sm + L::oKq, 64 + j, row), tau[i]);
-          }
-        }
-        stau[quad * 64 + half * 32 + lane] = lane_column_sum(tau, lane);
-        if (row < KP * 64) {
-          float x[32];
-          tmem_row<32>(tA2 + mine, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = half * 32 + i;
-            acc_k[i] = fmaf(sgate[64 + j], x[i], acc_k[i]);
-            kap[i] = x[i] * kq_at<NQ, KP>(sm + L::oKq, j, row);
-          }
-        }
-        skap[quad * 64 + half * 32 + lane] = lane_column_sum(kap, lane);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) sdot[warp] = dot;
-      }
-      wait(done, done_phase);
-      done_phase ^= 1;
-      tmem_fence_after_sync();
-      if (copier && !L::kOwnM) refill((hh + 1) * tiles - 1);  // M lay in the stage
-      {
-        float x[32];
-        tmem_row<32>(tCK + mine, x);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc_k[i] += x[i];
-        tmem_row<32>(tCQ + mine, x);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc_q[i] += x[i];
-      }
-      tmem_fence_before_sync();
-      named_barrier(1, 256);
-      if (warp == 0) {
-        // tokens 2 lane and 2 lane + 1
-        float dg[2], end = 0.0f;
-        const float g_last = sgate[192 + 63], l_last = sgate[256 + 63];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = 2 * lane + i;
-          const float kap = (skap[j] + skap[64 + j]) + (skap[128 + j] + skap[192 + j]);
-          const float tau = (stau[j] + stau[64 + j]) + (stau[128 + j] + stau[192 + j]);
-          const float col = (scol[j] + scol[64 + j]) + (scol[128 + j] + scol[192 + j]);
-          const float rows = (srow[j] + srow[128 + j]) + (srow[64 + j] + srow[192 + j]);
-          const float dec = ex2((g_last - sgate[192 + j]) + (l_last - sgate[256 + j]));
-          const float beta = sgate[128 + j];
-          const float db = fmaf(dec, kap, col);
-          end = fmaf(sgate[64 + j], kap, end);
-          dg[i] = tau + (rows - beta * db);
-          if (j < len) a.dbeta[(start + j) * a.Hv + h] = db + sdiag[j];
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
-        float d = 0.0f;
-        for (int w = 0; w < 8; ++w) d += sdot[w];
-        end = fmaf(sgate[63], d, end);
-        float suffix = dg[0] + dg[1];
-        const float own = suffix;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float v = __shfl_down_sync(0xffffffffu, suffix, o);
-          if (lane + o < 32) suffix += v;
-        }
-        float next = __shfl_down_sync(0xffffffffu, suffix, 1);
-        if (lane == 31) next = 0.0f;
-        const int j = 2 * lane;
-        if (j < len) a.dg[(start + j) * a.Hv + h] = end + (next + own);
-        if (j + 1 < len) a.dg[(start + j + 1) * a.Hv + h] = end + (next + dg[1]);
-      }
-      if (hh + 1 < rep) named_barrier(1, 256);  // before the next head's gates and sums
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (copier && (L::kOwnM || p + 1 < tiles)) refill(i);
     }
+    wait(done, done_phase);
+    done_phase ^= 1;
+    tmem_fence_after_sync();
+    named_barrier(1, 256);  // the gates are in; every warp is through with the last tile
 
-    if (row < a.K) {
+    // M1 and M2, and what their elements add to dg and dbeta
+    {
+      float rows = 0.0f, cols[32];
+      if (half && (quad & 1) == 0) {  // rows 0-31 end before column 32
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int j = half * 32 + i;
-        if (j < len) {
-          const int64_t at = ((start + j) * a.Hk + kh) * a.K + row;
-          static_cast<T*>(a.dk)[at] = from_f<T>(acc_k[i]);
-          static_cast<T*>(a.dq)[at] = from_f<T>(acc_q[i]);
+        for (int k = 0; k < 4 * NT; ++k)
+          *reinterpret_cast<uint4*>(sm + L::oM + k / 4 * 16384 + image_chunk<128>(row, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) cols[i] = 0.0f;
+      } else {
+        const float gi = sgate[192 + r], gl = sgate[256 + r], sign = is_k ? -1.0f : a.scale;
+        const int end = is_k ? r : r + 1;  // columns j < end
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float m[16], qk[16];
+          tmem_row<16>(tW + lane_at + half * 32 + u * 16, m);
+          tmem_row<16>(tQK + lane_at + half * 32 + u * 16, qk);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int j0 = half * 32 + u * 16 + 4 * q;
+            const float4 gh = *reinterpret_cast<const float4*>(sgate + 192 + j0);
+            const float4 gw = *reinterpret_cast<const float4*>(sgate + 256 + j0);
+            const float4 bt = *reinterpret_cast<const float4*>(sgate + 128 + j0);
+            const float g4[4] = {gh.x, gh.y, gh.z, gh.w}, l4[4] = {gw.x, gw.y, gw.z, gw.w}, b4[4] = {bt.x, bt.y, bt.z, bt.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 4 * q + i, j = j0 + i;
+              const float d = ex2((gi - g4[i]) + (gl - l4[i])) * sign;
+              const float w = j < end ? d * m[k] : 0.0f;
+              const float x = j < end ? w * qk[k] : 0.0f;
+              m[k] = w * b4[i];
+              if (j == r && !is_k) sdiag[r] = x;
+              cols[u * 16 + k] = j == r ? 0.0f : x;
+              rows = fmaf(cols[u * 16 + k], b4[i], rows);
+            }
+          }
+          float2 mp[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mp[i] = make_float2(m[2 * i], m[2 * i + 1]);
+          put_row<NT, 128>(sm + L::oM, 16384, row, half * 4 + 2 * u, mp);
         }
       }
+      srow[half * 128 + row] = rows;
+      scol[quad * 64 + half * 32 + lane] = lane_column_sum(cols, lane);
+    }
+    fence_async_smem();
+    tmem_fence_before_sync();
+    named_barrier(1, 256);
+    if (leader) {
+      tmem_fence_after_sync();
+      const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> KQ(kq);
+      const Operand<128, kKMajor, NT, 16384> M(m_at);
+      const Operand<128, kMnMajor, NT, 16384, 0, 8192> Mt(m_at);
+      umma_terms<kWide, 4, NT>(tC, M, KQ, false);   // the rows of K
+      umma_terms<kWide, 8, NT>(tF, Mt, KQ, false);
+      umma_commit(done);
+    }
+    // while that runs: the parts of dq and dk from the states
+    {
+      const float f = is_k ? -sgate[r] : a.scale * sgate[r], db = sgate[64 + r];
+      float2 da = splat2(0.0f), dk = splat2(0.0f);
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        const int col = half * kMine + 16 * u;
+        float2 x[8], k0[4], k1[4];
+        tmem_sum<8, 1>(tA + lane_at + col, 0, x);
+        kq_at<NQ, KP>(sm + L::oKq, row, col, k0);
+        kq_at<NQ, KP>(sm + L::oKq, row, col + 8, k1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          da = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], da);
+          acc[8 * u + i] = fma2(splat2(f), x[i], acc[8 * u + i]);
+        }
+        if (is_k) {
+          tmem_sum<8, 1>(tB + lane_at + col, 0, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dk = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], dk);
+            acc[8 * u + i] = fma2(splat2(db), x[i], acc[8 * u + i]);
+          }
+        }
+      }
+      sdots[half * 128 + row] = f * (da.x + da.y);
+      if (is_k) skap[half * 64 + row] = dk.x + dk.y;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) sdot[warp] = dot;
+    }
+    named_barrier(1, 256);
+    if (warp == 0) {
+      // tokens 2 lane and 2 lane + 1
+      float dg[2], end = 0.0f;
+      const float g_last = sgate[192 + 63], l_last = sgate[256 + 63];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = 2 * lane + i;
+        const float kap = skap[j] + skap[64 + j];
+        const float tau = (sdots[j] + sdots[128 + j]) + (sdots[64 + j] + sdots[192 + j]);
+        const float col = (scol[j] + scol[64 + j]) + (scol[128 + j] + scol[192 + j]);
+        const float rows = (srow[j] + srow[128 + j]) + (srow[64 + j] + srow[192 + j]);
+        const float dec = ex2((g_last - sgate[192 + j]) + (l_last - sgate[256 + j]));
+        const float beta = sgate[128 + j];
+        const float db = fmaf(dec, kap, col);
+        end = fmaf(sgate[64 + j], kap, end);
+        dg[i] = tau + (rows - beta * db);
+        if (j < len) a.dbeta[(start + j) * a.Hv + h] = db + sdiag[j];
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+      float d = 0.0f;
+      for (int w = 0; w < 8; ++w) d += sdot[w];
+      end = fmaf(sgate[63], d, end);
+      float suffix = dg[0] + dg[1];
+      const float own = suffix;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float v = __shfl_down_sync(0xffffffffu, suffix, o);
+        if (lane + o < 32) suffix += v;
+      }
+      float next = __shfl_down_sync(0xffffffffu, suffix, 1);
+      if (lane == 31) next = 0.0f;
+      const int j = 2 * lane;
+      if (j < len) a.dg[(start + j) * a.Hv + h] = end + (next + own);
+      if (j + 1 < len) a.dg[(start + j + 1) * a.Hv + h] = end + (next + dg[1]);
+    }
+    wait(done, done_phase);
+    done_phase ^= 1;
+    tmem_fence_after_sync();
+    if (copier && !L::kOwnM) refill((hh + 1) * tiles - 1);  // M lay in the stage
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const int col = half * kMine + 16 * u;
+      float2 x[8];
+      tmem_sum<8, 1>(tC + lane_at + col, 0, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
+      if (is_k) {
+        tmem_sum<8, 1>(tF + lane_at + col, 0, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
+      }
+    }
+    tmem_fence_before_sync();
+    if (hh + 1 < rep) named_barrier(1, 256);  // before the next head's products, gates and sums
+  }
+
+  {
+    constexpr int kPer = 64 / (int)sizeof(T);  // values of a 64-byte piece of a row
+    const int first = (quad & 1) * 32;
+    T* out = static_cast<T*>(is_k ? a.dk : a.dq) + ((start + first) * a.Hk + kh) * a.K;
+#pragma unroll
+    for (int p = 0; p < kMine / kPer; ++p) {
+      uint4 q[4];
+#pragma unroll
+      for (int u = 0; u < kPer / 16; ++u) {
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = acc[p * (kPer / 2) + 8 * u + i];
+        pack(v, q + u * 2, T());
+      }
+      const int col = half * kMine + p * kPer;
+      store_rows(out + col, (int64_t)a.Hk * a.K, len - first, a.K - col, lane, q);
     }
   }
   tmem_fence_before_sync();

@@ -12,7 +12,7 @@ namespace {
 //   D2 += Tm^T Z = dV                   (64 rows; 64 to 127 are not used)
 //   D1 = [K; Q]^T [-exp(G) dV; scale exp(G) dO] and dS0 = exp(G_63) dS1 + D1
 // sZ holds 128 rows: dO as it is, then Z, then -exp(G) dV in the upper 64, and
-// dO scaled in the lower 64.  dS1, dO and dV of every chunk leave as images
+// dO scaled in the lower 64; sS dS1, then dV on its way out.  dS1, dO and dV of every chunk leave as images
 // for the gradients that need no walk.
 template <IO kIO, int KP, int kWalks>
 struct BwdSmem {
@@ -213,7 +213,10 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      if (porter) mbar_arrive(done);
+      if (porter) {
+        bulk_wait_read();  // dS1's image has left too, before dV takes its place
+        mbar_arrive(done);
+      }
       named_barrier(1 + walk, 128);
       if (leader) {
         tmem_fence_after_sync();
@@ -228,13 +231,12 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       tmem_fence_after_sync();
       if (porter && i + 1 < n && last_user(x_used)) load_x(i + 1);
       if (row < 64) {
-        uint8_t* to = a.dvi + (ch * tiles + tile) * (size_t)(NT * kRowTile);
         uint4 q[kParts][4];
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
           float2 d[8];
           tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
-          put_row<NT, 64>(to, kRowTile, row, 2 * u, d);
+          put_row<NT, 64>(sS, kRowTile, row, 2 * u, d);  // dS1's images have been read
           pack(d, q[u * kParts / 2] + u * (16 / kPer) % 4, T());
           scale_row(d, -g_row);
           put_row<NT, 64>(sZ, L::kZTile, row, 2 * u, d);
@@ -245,14 +247,18 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
           store_rows(static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0 + 16 * i, (int64_t)a.Hv * a.V,
                      (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, q[i]);
       }
-      if (last && !a.d_initial) break;
       fence_async_smem();
       tmem_fence_before_sync();
-      if (porter) {
-        bulk_wait_read();
-        mbar_arrive(done);
-      }
       named_barrier(1 + walk, 128);
+      if (porter) {
+        bulk_store_1d(a.dvi + (ch * tiles + tile) * (size_t)(NT * kRowTile), sS, NT * kRowTile);
+        bulk_commit();
+        if (!(last && !a.d_initial)) {
+          bulk_wait_read();
+          mbar_arrive(done);  // dV's image has left, before dS0 takes its place
+        }
+      }
+      if (last && !a.d_initial) break;
       if (leader) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);

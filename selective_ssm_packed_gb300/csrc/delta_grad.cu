@@ -5,22 +5,22 @@
 namespace vssm {
 namespace {
 
-// One CTA of 256 threads per chunk and key head; the value heads that share
-// the key head follow each other, and dq and dk are summed over them in
-// registers, in that order.  Products over the state's columns (tile by tile)
+// An item is a chunk and a key head; the value heads that share the key head
+// follow each other, and dq and dk are summed over them in registers, in that
+// order.  CTAs of 256 threads, one an SM, take every gridDim-th item, so that the
+// next item's tiles and [K; Q] arrive while this one is worked on.  Products over the state's columns (tile by tile)
 // and over the chunk's tokens, rows 0-63 for the keys' tokens and 64-127 for
 // the queries':
 //   A = [dV; dO] S0^T    B = E dS1^T (rows 0-63)    W = [dV; dO] E^T    QK = [K; Q] K^T
 //   C = [M2; M1] K       F = [M2; M1]^T [K; Q] (rows 0-63)
 // A, B, C and F are as wide as a state has rows; C takes W's and QK's columns,
 // so the four fill the SM's tensor memory.  Thread = one row, half the columns
-// (warp w: lanes 32 (w % 4) .., half w / 4).  The next tiles are on their way
-// through everything else.
+// (warp w: lanes 32 (w % 4) .., half w / 4).
 template <IO kIO, int KP>
 struct GradSmem {
   using D = DeltaTerms<kIO>;
   static constexpr int NT = D::kMid;
-  static constexpr int kStages = kIO == IO::BF16 ? 2 : 1;
+  static constexpr int kStages = kIO == IO::BF16 ? 2 : 1;  // of tiles, and of [K; Q]
   static constexpr int kKq = D::kIn * KP * 16384;
   static constexpr int kSTerm = KP * 64 * 64, kS = NT * kSTerm, kE = NT * kRowTile, kW = NT * 2 * kRowTile;
   // a stage: S0, dS1, E, then term by term 64 rows of dV and 64 of dO
@@ -28,13 +28,13 @@ struct GradSmem {
   static constexpr int kM = NT * 16384;  // [M2; M1], 128 rows of 64
   // M of its own, or (FP32, one stage) over the stage
   static constexpr bool kOwnM = kIO == IO::BF16;
-  static constexpr int oKq = 0, oStage = kKq, oM = kOwnM ? oStage + kStages * kStage : oStage;
+  static constexpr int oKq = 0, oStage = kStages * kKq, oM = kOwnM ? oStage + kStages * kStage : oStage;
   // F's instructions read 8 KB past M's last image for rows that are not read back
   static constexpr int kBehindM = oM + kM + 8192, kBehindStage = oStage + kStages * kStage;
   static constexpr int oF = kBehindM > kBehindStage ? kBehindM : kBehindStage;  // floats below
   static constexpr int kFloats = 320 + 256 + 256 + 256 + 256 + 64 + 64;
   static constexpr int oBar = oF + kFloats * 4;
-  static constexpr int kBytes = oBar + 64 + 1024;
+  static constexpr int kBytes = oBar + 128 + 1024;
 };
 
 // Lane l gets the sum over the warp's lanes of v[l]: 31 exchanges, fixed order.
@@ -83,26 +83,23 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::oBar);
   uint64_t* empty = full + ST;  // the products and the 8 warps have read a stage
   uint64_t* kq_full = empty + ST;
-  uint64_t* done = kq_full + 1;
+  uint64_t* done = kq_full + ST;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
-  const int kh = blockIdx.x % a.Hk;
-  const int64_t c = blockIdx.x / a.Hk;
-  if (c >= a.info[0]) return;
-  const int4 chunk = a.table[c];
-  const int64_t start = chunk.y;
-  const int len = chunk.z;
   const int rep = a.Hv / a.Hk;
   const int tiles = delta_tiles(a.V);
+  const int64_t all = a.info[0] < 0 ? 0 : (int64_t)a.info[0] * a.Hk;
+  if (blockIdx.x >= all) return;
+  const int items = (int)((all - 1 - blockIdx.x) / gridDim.x) + 1, per_item = rep * tiles;
   Waiter wait{a.wait_ns, a.status};
 
   if (t == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 9);
+      mbar_init(&kq_full[i], 1);
     }
-    mbar_init(kq_full, 1);
     mbar_init(done, 1);
     fence_mbar_init();
   }
@@ -122,11 +119,12 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   tmem_fence_after_sync();
   const uint32_t tm = *tmem_at;
 
-  // tile i of the (head, tile) pairs, which run on in every array
-  auto load = [&](int i) {
-    const int st = i % ST;
+  auto item_of = [&](int k) { return (int64_t)blockIdx.x + (int64_t)k * gridDim.x; };  // chunk * Hk + key head
+  // tile i of this CTA's (item, head, tile) triples; an item's run on in every array
+  auto load = [&](int64_t i) {
+    const int st = (int)(i % ST);
     uint8_t* to = sm + L::oStage + st * L::kStage;
-    const size_t at = (c * a.Hv + kh * rep) * tiles + i;
+    const size_t at = item_of((int)(i / per_item)) * per_item + i % per_item;
     mbar_arrive_expect_tx(&full[st], 2 * L::kS + L::kE + (NT + NQ) * kRowTile);
     bulk_load_1d(to + L::oS0, a.s0 + at * L::kS, L::kS, &full[st]);
     bulk_load_1d(to + L::oDs, a.ds + at * L::kS, L::kS, &full[st]);
@@ -139,250 +137,267 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
     }
   };
   // one thread: once tile i's stage has been read, fill it for tile i + ST
-  auto refill = [&](int i) {
-    if (i + ST >= rep * tiles) return;
-    wait(&empty[i % ST], (i / ST) & 1);
+  auto refill = [&](int64_t i) {
+    if (i + ST >= (int64_t)items * per_item) return;
+    wait(&empty[i % ST], (uint32_t)(i / ST) & 1);
     load(i + ST);
+  };
+  auto load_kq = [&](int k) {
+    mbar_arrive_expect_tx(&kq_full[k % ST], L::kKq);
+    bulk_load_1d(sm + L::oKq + k % ST * L::kKq, a.kq + item_of(k) * (size_t)L::kKq, L::kKq, &kq_full[k % ST]);
   };
   const bool copier = t == 7 * 32;
   if (copier) {
-    mbar_arrive_expect_tx(kq_full, L::kKq);
-    bulk_load_1d(sm + L::oKq, a.kq + (size_t)(c * a.Hk + kh) * L::kKq, L::kKq, kq_full);
-    for (int i = 0; i < ST && i < rep * tiles; ++i) load(i);
+    for (int i = 0; i < ST && i < items; ++i) load_kq(i);
+    for (int i = 0; i < ST && i < items * per_item; ++i) load(i);
   }
   constexpr int kWide = KP * 64, kMine = kWide / 2, kSteps = kMine / 16;  // state rows, and a thread's share of them
   const int row = quad * 32 + lane, r = row & 63;
   const bool is_k = row < 64;
   const uint32_t tA = tm, tB = tm + 128, tC = tm + 256, tW = tC, tQK = tC + 64, tF = tm + 384;
   const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
-  const uint32_t kq = smem_u32(sm + L::oKq), m_at = smem_u32(sm + L::oM);
+  const uint32_t m_at = smem_u32(sm + L::oM);
   const bool leader = t == 3 * 32;  // issues the products; its warp takes no part in <dS1, S0>
   uint32_t done_phase = 0;
-  wait(kq_full, 0);
 
-  float2 acc[kMine / 2];  // of dk (rows 0-63) or dq
-#pragma unroll
-  for (int i = 0; i < kMine / 2; ++i) acc[i] = splat2(0.0f);
+  for (int k = 0; k < items; ++k) {
+    const int kh = (int)(item_of(k) % a.Hk);
+    const int64_t c = item_of(k) / a.Hk;
+    const int4 chunk = a.table[c];
+    const int64_t start = chunk.y;
+    const int len = chunk.z;
+    uint8_t* kq_image = sm + L::oKq + k % ST * L::kKq;
+    const uint32_t kq = smem_u32(kq_image);
+    wait(&kq_full[k % ST], (uint32_t)(k / ST) & 1);
 
-  for (int hh = 0; hh < rep; ++hh) {
-    const int h = kh * rep + hh;
-    const int64_t ch = c * a.Hv + h;
-    float dot = 0.0f;
-    for (int i = t; i < 320; i += 256) sgate[i] = a.gates[ch * kDeltaGates + i];
-    if (leader) {
-      tmem_fence_after_sync();
-      const Operand<128, kKMajor, NQ, KP * 16384, 16384> KQ(kq);
-      umma_terms<64, KP * 4, NQ>(tQK, KQ, KQ, false);
-    }
-    for (int p = 0; p < tiles; ++p) {
-      const int i = hh * tiles + p, st = i % ST;
-      uint8_t* stage = sm + L::oStage + st * L::kStage;
-      wait(&full[st], (i / ST) & 1);
-      if (warp == 3) {
-        if (leader) {
-          const uint32_t at = smem_u32(stage);
-          const Operand<64, kKMajor, NT, L::kSTerm> S0(at + L::oS0), dS(at + L::oDs);
-          const Operand<64, kKMajor, NT, kRowTile> E(at + L::oE);
-          const Operand<64, kKMajor, NT, 2 * kRowTile> dW(at + L::oW);
-          umma_terms<64, 2, NT>(tW, dW, E, p > 0);
-          umma_terms<kWide, 2, NT>(tA, dW, S0, p > 0);
-          umma_terms<kWide, 2, NT>(tB, E, dS, p > 0);
-          umma_commit(&empty[st]);
-          if (p + 1 == tiles) umma_commit(done);
-        }
-        __syncwarp();
-      } else {
-        // <dS1, S0> over the tile: both images are permuted alike
-        for (int k = t - (warp > 3 ? 32 : 0); k < L::kSTerm / 16; k += 224) {
-          float2 x[4], y[4], w[4];
-          unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + (NT - 1) * L::kSTerm + k * 16), x);
-          unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + (NT - 1) * L::kSTerm + k * 16), y);
+    float2 acc[kMine / 2];  // of dk (rows 0-63) or dq
 #pragma unroll
-          for (int m = NT - 2; m >= 0; --m) {
-            unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + m * L::kSTerm + k * 16), w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = add2(x[j], w[j]);
-            unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + m * L::kSTerm + k * 16), w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = add2(y[j], w[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) dot = fmaf(x[j].x, y[j].x, fmaf(x[j].y, y[j].y, dot));
-        }
-        __syncwarp();
+    for (int i = 0; i < kMine / 2; ++i) acc[i] = splat2(0.0f);
+
+    for (int hh = 0; hh < rep; ++hh) {
+      const int h = kh * rep + hh;
+      const float* gates = a.gates + (c * a.Hv + h) * kDeltaGates;
+      const float gate0 = gates[t], gate1 = t < 64 ? gates[256 + t] : 0.0f;  // on their way through the tiles
+      float dot = 0.0f;
+      if (leader) {
+        tmem_fence_after_sync();
+        const Operand<128, kKMajor, NQ, KP * 16384, 16384> KQ(kq);
+        umma_terms<64, KP * 4, NQ>(tQK, KQ, KQ, false);
       }
-      if (lane == 0) mbar_arrive(&empty[st]);
-      if (copier && (L::kOwnM || p + 1 < tiles)) refill(i);
-    }
-    wait(done, done_phase);
-    done_phase ^= 1;
-    tmem_fence_after_sync();
-    named_barrier(1, 256);  // the gates are in; every warp is through with the last tile
+      for (int p = 0; p < tiles; ++p) {
+        const int64_t i = (int64_t)k * per_item + hh * tiles + p;
+        const int st = (int)(i % ST);
+        uint8_t* stage = sm + L::oStage + st * L::kStage;
+        wait(&full[st], (uint32_t)(i / ST) & 1);
+        if (warp == 3) {
+          if (leader) {
+            const uint32_t at = smem_u32(stage);
+            const Operand<64, kKMajor, NT, L::kSTerm> S0(at + L::oS0), dS(at + L::oDs);
+            const Operand<64, kKMajor, NT, kRowTile> E(at + L::oE);
+            const Operand<64, kKMajor, NT, 2 * kRowTile> dW(at + L::oW);
+            umma_terms<64, 2, NT>(tW, dW, E, p > 0);
+            umma_terms<kWide, 2, NT>(tA, dW, S0, p > 0);
+            umma_terms<kWide, 2, NT>(tB, E, dS, p > 0);
+            umma_commit(&empty[st]);
+            if (p + 1 == tiles) umma_commit(done);
+          }
+          __syncwarp();
+        } else {
+          // <dS1, S0> over the tile: both images are permuted alike
+          for (int q = t - (warp > 3 ? 32 : 0); q < L::kSTerm / 16; q += 224) {
+            float2 x[4], y[4], w[4];
+            unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + (NT - 1) * L::kSTerm + q * 16), x);
+            unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + (NT - 1) * L::kSTerm + q * 16), y);
+#pragma unroll
+            for (int m = NT - 2; m >= 0; --m) {
+              unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + m * L::kSTerm + q * 16), w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[j] = add2(x[j], w[j]);
+              unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + m * L::kSTerm + q * 16), w);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = add2(y[j], w[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dot = fmaf(x[j].x, y[j].x, fmaf(x[j].y, y[j].y, dot));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&empty[st]);
+        if (copier && (L::kOwnM || p + 1 < tiles)) refill(i);
+      }
+      wait(done, done_phase);
+      done_phase ^= 1;
+      tmem_fence_after_sync();
+      named_barrier(1, 256);  // every warp is through with the last tile, and with the last head's sums
+      sgate[t] = gate0;
+      if (t < 64) sgate[256 + t] = gate1;
+      named_barrier(1, 256);
 
-    // M1 and M2, and what their elements add to dg and dbeta
-    {
-      float rows = 0.0f, cols[32];
-      if (half && (quad & 1) == 0) {  // rows 0-31 end before column 32
+      // M1 and M2, and what their elements add to dg and dbeta
+      {
+        float rows = 0.0f, cols[32];
+        if (half && (quad & 1) == 0) {  // rows 0-31 end before column 32
 #pragma unroll
-        for (int k = 0; k < 4 * NT; ++k)
-          *reinterpret_cast<uint4*>(sm + L::oM + k / 4 * 16384 + image_chunk<128>(row, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 4 * NT; ++k)
+            *reinterpret_cast<uint4*>(sm + L::oM + k / 4 * 16384 + image_chunk<128>(row, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) cols[i] = 0.0f;
-      } else {
-        const float gi = sgate[192 + r], gl = sgate[256 + r], sign = is_k ? -1.0f : a.scale;
-        const int end = is_k ? r : r + 1;  // columns j < end
+          for (int i = 0; i < 32; ++i) cols[i] = 0.0f;
+        } else {
+          const float gi = sgate[192 + r], gl = sgate[256 + r], sign = is_k ? -1.0f : a.scale;
+          const int end = is_k ? r : r + 1;  // columns j < end
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float m[16], qk[16];
-          tmem_row<16>(tW + lane_at + half * 32 + u * 16, m);
-          tmem_row<16>(tQK + lane_at + half * 32 + u * 16, qk);
+          for (int u = 0; u < 2; ++u) {
+            float m[16], qk[16];
+            tmem_row<16>(tW + lane_at + half * 32 + u * 16, m);
+            tmem_row<16>(tQK + lane_at + half * 32 + u * 16, qk);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int j0 = half * 32 + u * 16 + 4 * q;
-            const float4 gh = *reinterpret_cast<const float4*>(sgate + 192 + j0);
-            const float4 gw = *reinterpret_cast<const float4*>(sgate + 256 + j0);
-            const float4 bt = *reinterpret_cast<const float4*>(sgate + 128 + j0);
-            const float g4[4] = {gh.x, gh.y, gh.z, gh.w}, l4[4] = {gw.x, gw.y, gw.z, gw.w}, b4[4] = {bt.x, bt.y, bt.z, bt.w};
+            for (int q = 0; q < 4; ++q) {
+              const int j0 = half * 32 + u * 16 + 4 * q;
+              const float4 gh = *reinterpret_cast<const float4*>(sgate + 192 + j0);
+              const float4 gw = *reinterpret_cast<const float4*>(sgate + 256 + j0);
+              const float4 bt = *reinterpret_cast<const float4*>(sgate + 128 + j0);
+              const float g4[4] = {gh.x, gh.y, gh.z, gh.w}, l4[4] = {gw.x, gw.y, gw.z, gw.w}, b4[4] = {bt.x, bt.y, bt.z, bt.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = 4 * q + i, j = j0 + i;
-              const float d = ex2((gi - g4[i]) + (gl - l4[i])) * sign;
-              const float w = j < end ? d * m[k] : 0.0f;
-              const float x = j < end ? w * qk[k] : 0.0f;
-              m[k] = w * b4[i];
-              if (j == r && !is_k) sdiag[r] = x;
-              cols[u * 16 + k] = j == r ? 0.0f : x;
-              rows = fmaf(cols[u * 16 + k], b4[i], rows);
+              for (int i = 0; i < 4; ++i) {
+                const int k = 4 * q + i, j = j0 + i;
+                const float d = ex2((gi - g4[i]) + (gl - l4[i])) * sign;
+                const float w = j < end ? d * m[k] : 0.0f;
+                const float x = j < end ? w * qk[k] : 0.0f;
+                m[k] = w * b4[i];
+                if (j == r && !is_k) sdiag[r] = x;
+                cols[u * 16 + k] = j == r ? 0.0f : x;
+                rows = fmaf(cols[u * 16 + k], b4[i], rows);
+              }
+            }
+            float2 mp[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mp[i] = make_float2(m[2 * i], m[2 * i + 1]);
+            put_row<NT, 128>(sm + L::oM, 16384, row, half * 4 + 2 * u, mp);
+          }
+        }
+        srow[half * 128 + row] = rows;
+        scol[quad * 64 + half * 32 + lane] = lane_column_sum(cols, lane);
+      }
+      fence_async_smem();
+      tmem_fence_before_sync();
+      named_barrier(1, 256);
+      if (leader) {
+        tmem_fence_after_sync();
+        const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> KQ(kq);
+        const Operand<128, kKMajor, NT, 16384> M(m_at);
+        const Operand<128, kMnMajor, NT, 16384, 0, 8192> Mt(m_at);
+        umma_terms<kWide, 4, NT>(tC, M, KQ, false);   // the rows of K
+        umma_terms<kWide, 8, NT>(tF, Mt, KQ, false);
+        umma_commit(done);
+      }
+      // while that runs: the parts of dq and dk from the states
+      {
+        const float f = is_k ? -sgate[r] : a.scale * sgate[r], db = sgate[64 + r];
+        float2 da = splat2(0.0f), dk = splat2(0.0f);
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int col = half * kMine + 16 * u;
+          float2 x[8], k0[4], k1[4];
+          tmem_sum<8, 1>(tA + lane_at + col, 0, x);
+          kq_at<NQ, KP>(kq_image, row, col, k0);
+          kq_at<NQ, KP>(kq_image, row, col + 8, k1);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            da = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], da);
+            acc[8 * u + i] = fma2(splat2(f), x[i], acc[8 * u + i]);
+          }
+          if (is_k) {
+            tmem_sum<8, 1>(tB + lane_at + col, 0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              dk = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], dk);
+              acc[8 * u + i] = fma2(splat2(db), x[i], acc[8 * u + i]);
             }
           }
-          float2 mp[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mp[i] = make_float2(m[2 * i], m[2 * i + 1]);
-          put_row<NT, 128>(sm + L::oM, 16384, row, half * 4 + 2 * u, mp);
         }
+        sdots[half * 128 + row] = f * (da.x + da.y);
+        if (is_k) skap[half * 64 + row] = dk.x + dk.y;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) sdot[warp] = dot;
       }
-      srow[half * 128 + row] = rows;
-      scol[quad * 64 + half * 32 + lane] = lane_column_sum(cols, lane);
-    }
-    fence_async_smem();
-    tmem_fence_before_sync();
-    named_barrier(1, 256);
-    if (leader) {
+      wait(done, done_phase);
+      done_phase ^= 1;
       tmem_fence_after_sync();
-      const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> KQ(kq);
-      const Operand<128, kKMajor, NT, 16384> M(m_at);
-      const Operand<128, kMnMajor, NT, 16384, 0, 8192> Mt(m_at);
-      umma_terms<kWide, 4, NT>(tC, M, KQ, false);   // the rows of K
-      umma_terms<kWide, 8, NT>(tF, Mt, KQ, false);
-      umma_commit(done);
-    }
-    // while that runs: the parts of dq and dk from the states
-    {
-      const float f = is_k ? -sgate[r] : a.scale * sgate[r], db = sgate[64 + r];
-      float2 da = splat2(0.0f), dk = splat2(0.0f);
+      if (copier && !L::kOwnM) refill((int64_t)k * per_item + (hh + 1) * tiles - 1);  // M lay in the stage
+      __syncwarp();
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
         const int col = half * kMine + 16 * u;
-        float2 x[8], k0[4], k1[4];
-        tmem_sum<8, 1>(tA + lane_at + col, 0, x);
-        kq_at<NQ, KP>(sm + L::oKq, row, col, k0);
-        kq_at<NQ, KP>(sm + L::oKq, row, col + 8, k1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          da = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], da);
-          acc[8 * u + i] = fma2(splat2(f), x[i], acc[8 * u + i]);
-        }
-        if (is_k) {
-          tmem_sum<8, 1>(tB + lane_at + col, 0, x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dk = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], dk);
-            acc[8 * u + i] = fma2(splat2(db), x[i], acc[8 * u + i]);
-          }
-        }
-      }
-      sdots[half * 128 + row] = f * (da.x + da.y);
-      if (is_k) skap[half * 64 + row] = dk.x + dk.y;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) sdot[warp] = dot;
-    }
-    named_barrier(1, 256);
-    if (warp == 0) {
-      // tokens 2 lane and 2 lane + 1
-      float dg[2], end = 0.0f;
-      const float g_last = sgate[192 + 63], l_last = sgate[256 + 63];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = 2 * lane + i;
-        const float kap = skap[j] + skap[64 + j];
-        const float tau = (sdots[j] + sdots[128 + j]) + (sdots[64 + j] + sdots[192 + j]);
-        const float col = (scol[j] + scol[64 + j]) + (scol[128 + j] + scol[192 + j]);
-        const float rows = (srow[j] + srow[128 + j]) + (srow[64 + j] + srow[192 + j]);
-        const float dec = ex2((g_last - sgate[192 + j]) + (l_last - sgate[256 + j]));
-        const float beta = sgate[128 + j];
-        const float db = fmaf(dec, kap, col);
-        end = fmaf(sgate[64 + j], kap, end);
-        dg[i] = tau + (rows - beta * db);
-        if (j < len) a.dbeta[(start + j) * a.Hv + h] = db + sdiag[j];
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
-      float d = 0.0f;
-      for (int w = 0; w < 8; ++w) d += sdot[w];
-      end = fmaf(sgate[63], d, end);
-      float suffix = dg[0] + dg[1];
-      const float own = suffix;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float v = __shfl_down_sync(0xffffffffu, suffix, o);
-        if (lane + o < 32) suffix += v;
-      }
-      float next = __shfl_down_sync(0xffffffffu, suffix, 1);
-      if (lane == 31) next = 0.0f;
-      const int j = 2 * lane;
-      if (j < len) a.dg[(start + j) * a.Hv + h] = end + (next + own);
-      if (j + 1 < len) a.dg[(start + j + 1) * a.Hv + h] = end + (next + dg[1]);
-    }
-    wait(done, done_phase);
-    done_phase ^= 1;
-    tmem_fence_after_sync();
-    if (copier && !L::kOwnM) refill((hh + 1) * tiles - 1);  // M lay in the stage
-    __syncwarp();
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int col = half * kMine + 16 * u;
-      float2 x[8];
-      tmem_sum<8, 1>(tC + lane_at + col, 0, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
-      if (is_k) {
-        tmem_sum<8, 1>(tF + lane_at + col, 0, x);
+        float2 x[8];
+        tmem_sum<8, 1>(tC + lane_at + col, 0, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
+        if (is_k) {
+          tmem_sum<8, 1>(tF + lane_at + col, 0, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
+        }
+      }
+      tmem_fence_before_sync();
+      named_barrier(1, 256);  // the sums are in; the next head's products may begin
+      if (warp == 0) {
+        // tokens 2 lane and 2 lane + 1
+        float dg[2], end = 0.0f;
+        const float g_last = sgate[192 + 63], l_last = sgate[256 + 63];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = 2 * lane + i;
+          const float kap = skap[j] + skap[64 + j];
+          const float tau = (sdots[j] + sdots[128 + j]) + (sdots[64 + j] + sdots[192 + j]);
+          const float col = (scol[j] + scol[64 + j]) + (scol[128 + j] + scol[192 + j]);
+          const float rows = (srow[j] + srow[128 + j]) + (srow[64 + j] + srow[192 + j]);
+          const float dec = ex2((g_last - sgate[192 + j]) + (l_last - sgate[256 + j]));
+          const float beta = sgate[128 + j];
+          const float db = fmaf(dec, kap, col);
+          end = fmaf(sgate[64 + j], kap, end);
+          dg[i] = tau + (rows - beta * db);
+          if (j < len) a.dbeta[(start + j) * a.Hv + h] = db + sdiag[j];
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+        float d = 0.0f;
+        for (int w = 0; w < 8; ++w) d += sdot[w];
+        end = fmaf(sgate[63], d, end);
+        float suffix = dg[0] + dg[1];
+        const float own = suffix;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float v = __shfl_down_sync(0xffffffffu, suffix, o);
+          if (lane + o < 32) suffix += v;
+        }
+        float next = __shfl_down_sync(0xffffffffu, suffix, 1);
+        if (lane == 31) next = 0.0f;
+        const int j = 2 * lane;
+        if (j < len) a.dg[(start + j) * a.Hv + h] = end + (next + own);
+        if (j + 1 < len) a.dg[(start + j + 1) * a.Hv + h] = end + (next + dg[1]);
       }
     }
-    tmem_fence_before_sync();
-    if (hh + 1 < rep) named_barrier(1, 256);  // before the next head's products, gates and sums
-  }
 
-  {
-    constexpr int kPer = 64 / (int)sizeof(T);  // values of a 64-byte piece of a row
-    const int first = (quad & 1) * 32;
-    T* out = static_cast<T*>(is_k ? a.dk : a.dq) + ((start + first) * a.Hk + kh) * a.K;
+    {
+      constexpr int kPer = 64 / (int)sizeof(T);  // values of a 64-byte piece of a row
+      const int first = (quad & 1) * 32;
+      T* out = static_cast<T*>(is_k ? a.dk : a.dq) + ((start + first) * a.Hk + kh) * a.K;
 #pragma unroll
-    for (int p = 0; p < kMine / kPer; ++p) {
-      uint4 q[4];
+      for (int p = 0; p < kMine / kPer; ++p) {
+        uint4 q[4];
 #pragma unroll
-      for (int u = 0; u < kPer / 16; ++u) {
-        float2 v[8];
+        for (int u = 0; u < kPer / 16; ++u) {
+          float2 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = acc[p * (kPer / 2) + 8 * u + i];
-        pack(v, q + u * 2, T());
+          for (int i = 0; i < 8; ++i) v[i] = acc[p * (kPer / 2) + 8 * u + i];
+          pack(v, q + u * 2, T());
+        }
+        const int col = half * kMine + p * kPer;
+        store_rows(out + col, (int64_t)a.Hk * a.K, len - first, a.K - col, lane, q);
       }
-      const int col = half * kMine + p * kPer;
-      store_rows(out + col, (int64_t)a.Hk * a.K, len - first, a.K - col, lane, q);
     }
+    if (copier && k + ST < items) load_kq(k + ST);  // behind the last barrier nothing reads this item's
   }
   tmem_fence_before_sync();
   __syncthreads();
@@ -396,7 +411,8 @@ cudaError_t run_grads(const DeltaArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_grad_kernel<kIO, KP>), bytes, done);
   if (e != cudaSuccess) return e;
-  delta_grad_kernel<kIO, KP><<<(unsigned)(a.max_chunks * a.Hk), 256, bytes, st>>>(a);
+  const int64_t items = a.max_chunks * a.Hk;
+  delta_grad_kernel<kIO, KP><<<(unsigned)(items < 152 ? items : 152), 256, bytes, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -94,16 +94,16 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
 }
 
 // ------------------------------------------------------------------ prep
-// One CTA of 128 threads per chunk and key head; the value heads that share
-// the key head follow each other.  Thread r < 64 owns row r of K K^T, N and
-// Tm, thread 64 + r row r of Q K^T, P and P Tm.
+// One CTA of 256 threads per chunk and key head; the value heads that share
+// the key head follow each other.  Rows 0-63 of a product are K K^T, N and Tm,
+// rows 64-127 Q K^T, P and P Tm; a thread has half a row.
 // Tm = (I + N)^-1 in place of N, in shared memory: the four 16 x 16 blocks of
 // the diagonal by substitution, then twice two neighbouring blocks' inverses
 // T1, T2 and the block N21 below T1 are joined by T21 = -T2 N21 T1 (16, then
 // 32 wide), in FP32.  The sum of powers of N would take fewer steps, but powers
 // grow without bound for keys that resemble each other, while Tm's entries do
 // not.  Substitution over all 64 columns took one warp 8300 cycles, most of
-// them waiting for itself; here every step but the first has all four warps.
+// them waiting for itself.
 // P Tm is a product on the matrix unit, from and into X's own images.
 // Four CTAs fit an SM, so that one's waits hide behind the others.
 constexpr int kNPitch = 68;    // floats a row of N: 16-byte writes of a warp's rows hit all banks
@@ -151,7 +151,8 @@ __device__ __forceinline__ void small_product(const float* A, int pa, const floa
 }
 
 // (I + N)^-1 over N (64 rows, kNPitch floats apart, zero above the diagonal),
-// by 128 threads; y: 32 x 36 floats of scratch.
+// by 256 threads numbered t in any order of whole warps; y: 32 x 36 floats of
+// scratch.
 __device__ __forceinline__ void invert(float* n, float* y, int t) {
   if (t < 64) {
     const int r = t & 15;
@@ -177,25 +178,30 @@ __device__ __forceinline__ void invert(float* n, float* y, int t) {
     for (int i = 0; i < 8; i += 2) *reinterpret_cast<float4*>(out + 2 * i) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
   }
   __syncthreads();
+  // Products of 4 x 4 values a thread: shared memory serves one float of a
+  // vector read a cycle, repeated or not, and its cycles bound this kernel.
   {
-    const int at = (t >> 6) * 32, i = (t >> 2) & 15, c = (t & 3) * 4;  // pair of blocks, row, columns
-    float* y1 = y + (t >> 6) * 16 * 20;
-    const float* n21 = n + (at + 16) * kNPitch + at;
-    small_product<1, 16, false>(n21 + i * kNPitch, 0, n + at * kNPitch + at + c, kNPitch, y1 + i * 20 + c, 0);
-    __syncthreads();
-    small_product<1, 16, true>(n + (at + 16 + i) * kNPitch + at + 16, 0, y1 + c, 20,
-                               n + (at + 16 + i) * kNPitch + at + c, 0);
+    const int at = (t >> 4) * 32, i = (t >> 2 & 3) * 4, c = (t & 3) * 4;  // pair of blocks, rows, columns
+    float* y1 = y + (t >> 4) * 16 * 20;
+    if (t < 32)
+      small_product<4, 16, false>(n + (at + 16 + i) * kNPitch + at, kNPitch, n + at * kNPitch + at + c, kNPitch,
+                                  y1 + i * 20 + c, 20);
+    __syncwarp();
+    if (t < 32)
+      small_product<4, 16, true>(n + (at + 16 + i) * kNPitch + at + 16, kNPitch, y1 + c, 20,
+                                 n + (at + 16 + i) * kNPitch + at + c, kNPitch);
     __syncthreads();
   }
-  const int i = (t >> 3) * 2, c = (t & 7) * 4;
-  small_product<2, 32, false>(n + (32 + i) * kNPitch, kNPitch, n + c, kNPitch, y + i * 36 + c, 36);
+  const int i = (t >> 3) * 4, c = (t & 7) * 4;
+  if (t < 64) small_product<4, 32, false>(n + (32 + i) * kNPitch, kNPitch, n + c, kNPitch, y + i * 36 + c, 36);
   __syncthreads();
-  small_product<2, 32, true>(n + (32 + i) * kNPitch + 32, kNPitch, y + c, 36, n + (32 + i) * kNPitch + c, kNPitch);
+  if (t < 64)
+    small_product<4, 32, true>(n + (32 + i) * kNPitch + 32, kNPitch, y + c, 36, n + (32 + i) * kNPitch + c, kNPitch);
   __syncthreads();
 }
 
 template <IO kIO, int KP>
-__global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
   using L = PrepSmem<kIO, KP>;
   constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid;
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
   uint64_t* bar = reinterpret_cast<uint64_t*>(images + L::oBar);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
 
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
   const int kh = blockIdx.x % a.Hk;
   const int64_t c = blockIdx.x / a.Hk;
   if (c >= a.info[0]) return;
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
 
   // warp w: the gates of value head hh + w
   auto make_gates = [&](int hh) {
-    if (hh + warp >= rep) return;
+    if (warp >= kPrepHeads || hh + warp >= rep) return;
     // the running sum of g, in double: differences of it enter exp
     const int hw = kh * rep + hh + warp;
     float g[2], b[2];
@@ -270,8 +276,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
   const T* qbase = static_cast<const T*>(a.q) + start * a.sq + (int64_t)kh * a.K;
   if constexpr (kIO == IO::BF16) {
 #pragma unroll
-    for (int u = 0; u < KP * 8; ++u) {
-      const int i = t + u * 128, row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
+    for (int u = 0; u < KP * 4; ++u) {
+      const int i = t + u * 256, row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
       const bool in = r < len && ch * 8 < a.K;
       const T* src = in ? (row < 64 ? kbase + r * a.sk : qbase + r * a.sq) + ch * 8 : kbase;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -282,11 +288,11 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
     asm volatile("cp.async.commit_group;" ::: "memory");
   } else {
     constexpr int kBatch = 4;  // reads in flight
-    for (int u = 0; u < KP * 8; u += kBatch) {
+    for (int u = 0; u < KP * 4; u += kBatch) {
       float4 f[kBatch][2];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int i = t + (u + k) * 128, row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
+        const int i = t + (u + k) * 256, row = i / (KP * 8), ch = i % (KP * 8), r = row & 63;
         f[k][0] = f[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (r < len && ch * 8 < a.K) {
           const float4* src = reinterpret_cast<const float4*>((row < 64 ? kbase + r * a.sk : qbase + r * a.sq) + ch * 8);
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int i = t + (u + k) * 128, row = i / (KP * 8), ch = i % (KP * 8);
+        const int i = t + (u + k) * 256, row = i / (KP * 8), ch = i % (KP * 8);
         const float2 v[4] = {make_float2(f[k][0].x, f[k][0].y), make_float2(f[k][0].z, f[k][0].w),
                              make_float2(f[k][1].x, f[k][1].y), make_float2(f[k][1].z, f[k][1].w)};
         put_chunk<NQ, 128>(images + (ch >> 3) * 16384, kTerm, row, ch & 7, v);
@@ -310,7 +316,10 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tm = *tmem_at;
-  const uint32_t mine = tm + ((uint32_t)(warp * 32) << 16);
+  const int row = quad * 32 + lane, r = row & 63;
+  const bool is_k = row < 64;
+  const bool empty = half && !(quad & 1);  // rows 0-31 end before column 32
+  const uint32_t mine = tm + ((uint32_t)(quad * 32) << 16) + half * 32;
   if (t == 0) {
     const Operand<128, kKMajor, NQ, kTerm, 16384> kq(smem_u32(images));
     umma_terms<64, KP * 4, NQ>(tm, kq, kq, false);  // B: the K rows
@@ -334,51 +343,47 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
     }
     const float2* sg = sg_all + (hh % kPrepHeads) * 64;
     const float* sbeta = sbeta_all + (hh % kPrepHeads) * 64;
-    const int r = t & 63;
-    const bool is_k = t < 64;
-    {
+    if (!empty) {
       const float2 gi = sg[r];
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (half && !(warp & 1)) {  // rows 0-31 end before column 32
-          if (!is_k) {
+      const float f = is_k ? 1.0f : a.scale;
+      const int end = is_k ? r : r + 1;  // columns j < end
 #pragma unroll
-            for (int k = 0; k < 4 * NT; ++k)
-              *reinterpret_cast<uint4*>(images + k / 4 * 16384 + image_chunk<128>(t, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
-          }
-          continue;
-        }
-        float d[32];
-        tmem_row<32>(mine + half * 32, d);
+      for (int u = 0; u < 2; ++u) {
+        float d[16];
+        tmem_row<16>(mine + u * 16, d);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int j = half * 32 + i;
+        for (int i = 0; i < 16; ++i) {
+          const int j = half * 32 + u * 16 + i;
           const float2 gj = sg[j];
-          const float w = ex2((gi.x - gj.x) + (gi.y - gj.y)) * sbeta[j] * d[i];
-          d[i] = (is_k ? j < r : j <= r) ? (is_k ? w : w * a.scale) : 0.0f;
+          const float w = ex2((gi.x - gj.x) + (gi.y - gj.y)) * (sbeta[j] * f) * d[i];
+          d[i] = j < end ? w : 0.0f;
         }
         if (is_k) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(sn + r * kNPitch + half * 32 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(sn + r * kNPitch + half * 32 + u * 16 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
         } else {
-          float2 p[16];
+          float2 p[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = make_float2(d[2 * i], d[2 * i + 1]);
-          put_row<NT, 128>(images, 16384, t, half * 4, p);
+          for (int i = 0; i < 8; ++i) p[i] = make_float2(d[2 * i], d[2 * i + 1]);
+          put_row<NT, 128>(images, 16384, row, half * 4 + 2 * u, p);
         }
       }
+    } else if (!is_k) {
+#pragma unroll
+      for (int k = 0; k < 4 * NT; ++k)
+        *reinterpret_cast<uint4*>(images + k / 4 * 16384 + image_chunk<128>(row, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
-    invert(sn, reinterpret_cast<float*>(images), t);  // scratch: where the rows of Tm go next
+    invert(sn, reinterpret_cast<float*>(images), (t + 64 * blockIdx.x) & 255);  // scratch: where the rows of Tm go next
     {
-      const int tr = t >> 1, side = t & 1;
+      const int tr = t >> 2, side = t & 3;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4* src = reinterpret_cast<const float4*>(sn + tr * kNPitch + side * 32 + q * 8);
+      for (int q = 0; q < 2; ++q) {
+        const float4* src = reinterpret_cast<const float4*>(sn + tr * kNPitch + side * 16 + q * 8);
         const float4 f = src[0], g = src[1];
         const float2 v[4] = {make_float2(f.x, f.y), make_float2(f.z, f.w), make_float2(g.x, g.y), make_float2(g.z, g.w)};
-        put_chunk<NT, 128>(images, 16384, tr, side * 4 + q, v);
+        put_chunk<NT, 128>(images, 16384, tr, side * 2 + q, v);
       }
     }
     fence_async_smem();
@@ -394,12 +399,12 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(DeltaArgs a) {
     wait(bar, phase);
     phase ^= 1;
     tmem_fence_after_sync();
-    if (!is_k) {
-#pragma unroll 1
-      for (int half = 0; half <= (warp & 1); ++half) {
-        float2 d[16];
-        tmem_sum<16, 1>(mine + 64 + half * 32, 0, d);
-        put_row<NT, 128>(images, 16384, t, half * 4, d);
+    if (!is_k && !empty) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float2 d[8];
+        tmem_sum<8, 1>(mine + 64 + u * 16, 0, d);
+        put_row<NT, 128>(images, 16384, row, half * 4 + 2 * u, d);
       }
     }
     fence_async_smem();
@@ -422,7 +427,7 @@ cudaError_t run_prep(const DeltaArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_prep_kernel<kIO, KP>), bytes, done);
   if (e != cudaSuccess) return e;
-  delta_prep_kernel<kIO, KP><<<(unsigned)(a.max_chunks * a.Hk), 128, bytes, st>>>(a);
+  delta_prep_kernel<kIO, KP><<<(unsigned)(a.max_chunks * a.Hk), 256, bytes, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -91,13 +91,28 @@ inline int64_t delta_max_chunks(int64_t T, int64_t num_seqs) {
   return T / kDeltaChunk + (num_seqs < T ? num_seqs : T);
 }
 
-// Tiles a CTA of the walks takes: four (bf16) share what they read; fewer
-// where that leaves SMs without a CTA.
-inline int delta_walks(const DeltaArgs& a, IO io) {
-  if (io == IO::F32) return 1;  // three terms fill shared memory
-  const int64_t heads = (int64_t)a.num_seqs * a.Hv, tiles = delta_tiles(a.V);
-  if (tiles == 1 || heads * tiles <= 152) return 1;
-  return tiles == 2 || heads * ((tiles + 1) / 2) <= 152 ? 2 : 4;
+// Tiles a CTA of the bf16 walks takes, which share what they read.  A step of
+// one, two or four walks on an SM takes 2.2, 3.2 or 4.0 us (one sequence of
+// 32768 tokens, 32 heads of 128 x 128): four are the fastest way through much
+// work, one is the fastest way along a sequence.  What a pack takes is about
+// the longer of all its steps over the SMs and of its longest sequence, which
+// only the GPU knows and which is taken for four times the mean.
+inline int delta_walks(const DeltaArgs& a) {
+  const double chunks = (double)a.T / kDeltaChunk + 1.0, longest = 4.0 * chunks / (a.num_seqs > 0 ? a.num_seqs : 1) + 1.0;
+  const int tiles = delta_tiles(a.V);
+  const double step[3] = {2.2, 3.2, 4.0};
+  int best = 1;
+  double least = 0.0;
+  for (int i = 0; i < 3 && (i == 0 || (1 << i) / 2 < tiles); ++i) {
+    const int groups = (tiles + (1 << i) - 1) >> i;
+    const double all = chunks * a.Hv * groups / 152.0, along = longest < chunks ? longest : chunks;
+    const double time = step[i] * (all > along ? all : along);
+    if (i == 0 || time < least) {
+      best = 1 << i;
+      least = time;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_delta_plan(const DeltaArgs& a, cudaStream_t st);

@@ -17,7 +17,7 @@ namespace {
 constexpr int kStepThreads = 256;
 
 template <typename T, int kCols>
-__global__ void __launch_bounds__(kStepThreads) delta_step_kernel(DeltaStepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 4) delta_step_kernel(DeltaStepArgs a) {
   constexpr int kAlong = kCols / 4, kStep = kStepThreads / kAlong, kPer = kDeltaMaxK / kStep;
   __shared__ float part[8][2][kCols];
   __shared__ float part_kq[8];

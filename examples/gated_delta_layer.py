@@ -8,7 +8,7 @@ After training, the prompt of each sequence is run once with its final states
 kept (prefill), and the remaining tokens one at a time against the state pool
 (varlen_gated_delta_step); both ways give the same answers.
 
-    python examples/gated_delta_layer.py [--steps 200]
+    python examples/gated_delta_layer.py [--steps 400]
 """
 import argparse
 import os
@@ -122,15 +122,13 @@ class Model(torch.nn.Module):
         super().__init__()
         self.embed = torch.nn.Embedding(vocab, d_model)
         self.layers = torch.nn.ModuleList(GatedDeltaLayer(d_model) for _ in range(layers))
-        self.norm = torch.nn.LayerNorm(d_model)
-
-    def head(self, x):
-        return self.norm(x) @ self.embed.weight.T
+        self.norms = torch.nn.ModuleList(torch.nn.LayerNorm(d_model) for _ in range(layers))
+        self.head = torch.nn.Sequential(torch.nn.LayerNorm(d_model), torch.nn.Linear(d_model, vocab))
 
     def forward(self, tokens, cu, pos):
         x = self.embed(tokens)
-        for m in self.layers:
-            x = x + m(x, cu, pos)
+        for norm, m in zip(self.norms, self.layers):
+            x = x + m(norm(x), cu, pos)
         return self.head(x)
 
 
@@ -150,16 +148,16 @@ def recall_batch(gen, sequences, keys=32, max_pairs=12, asked=4):
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    ap.add_argument("--steps", type=int, default=200)
+    ap.add_argument("--steps", type=int, default=400)
     args = ap.parse_args()
     torch.manual_seed(0)
     gen = torch.Generator().manual_seed(0)
     dev, asked = torch.device("cuda"), 4
     model = Model(vocab=64).to(dev)
-    opt = torch.optim.AdamW(model.parameters(), lr=3e-3)
+    opt = torch.optim.AdamW(model.parameters(), lr=2e-3)
     first = loss = None
     for i in range(args.steps):
-        tokens, targets, lens = recall_batch(gen, 64, asked=asked)
+        tokens, targets, lens = recall_batch(gen, 256, asked=asked)
         cu = torch.tensor([0, *torch.tensor(lens).cumsum(0).tolist()], dtype=torch.int32, device=dev)
         pos = vs.varlen_position_indices(cu, len(tokens))
         loss = torch.nn.functional.cross_entropy(model(tokens.to(dev), cu, pos), targets.to(dev), ignore_index=-1)
@@ -182,16 +180,16 @@ def main():
     pcu = torch.tensor([0, *torch.tensor([n - asked for n in lens]).cumsum(0).tolist()], dtype=torch.int32, device=dev)
     with torch.no_grad():
         x, kept = model.embed(prompts), []
-        for m in model.layers:
-            y, tails, states = m.prefill(x, pcu)
+        for norm, m in zip(model.norms, model.layers):
+            y, tails, states = m.prefill(norm(x), pcu)
             kept.append([tails, states])
             x = x + y
         right = worst = 0
         for j in range(asked):
             at = torch.tensor([b - asked + j for b in starts[1:]], device=dev)
             x = model.embed(tokens[at])
-            for m, state in zip(model.layers, kept):
-                y, state[0] = m.step(x, *state)
+            for norm, m, state in zip(model.norms, model.layers, kept):
+                y, state[0] = m.step(norm(x), *state)
                 x = x + y
             logits = model.head(x)
             worst = max(worst, (logits - whole[at]).abs().max().item() / whole.abs().max().item())

@@ -81,6 +81,7 @@ typedef enum { VSSM_F32 = 0, VSSM_BF16 = 1 } vssm_dtype;
 #define VSSM_ERR_NONFINITE (-18)        /* an output holds a NaN / inf (VSSM_DBG_CHECK_FINITE on) */
 #define VSSM_ERR_DEVICE_CHECK (-19)     /* a device index check failed (VSSM_CHECKS=1 build only) */
 #define VSSM_ERR_BAD_INDEX (-20)        /* a position or state index outside its table */
+#define VSSM_ERR_BAD_SAVED (-21)        /* a saved array that no forward call of this shape filled */
 
 /* Tokens per saved scan-state chunk: the forward scan can save the state at
  * every multiple of this many tokens for the backward scan. */
@@ -402,7 +403,9 @@ int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t 
 
 /* Backward: dq, dk (T, Hk, K), dv (T, Hv, V) io, contiguous; dg, dbeta (T, Hv)
  * f32; d_initial_states nullable.  saved is the array the forward call on the
- * same inputs filled (read only); d_final_states: nullable, the gradient
+ * same inputs filled (read only; it holds the pack's plan too, which is what the
+ * backward goes by, and an array that no forward call of this shape filled is
+ * reported as VSSM_ERR_BAD_SAVED); scale is the forward call's; d_final_states: nullable, the gradient
  * reaching the final states.  dq and dk add the value heads that share a key head, in
  * order; no atomics, bitwise repeatable. */
 size_t varlen_gated_delta_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,

@@ -27,7 +27,8 @@ KERNEL_KINDS = {"conv_fwd": 0, "scan_fwd": 1, "scan_bwd": 2, "conv_bwd": 3}
 ERR = {0: "VSSM_OK", -1: "VSSM_ERR_ARG", -2: "VSSM_ERR_DTYPE", -3: "VSSM_ERR_ALIGN",
        -4: "VSSM_ERR_WORKSPACE", -5: "VSSM_ERR_CUDA", -6: "VSSM_ERR_UNSUPPORTED",
        -16: "VSSM_ERR_BAD_CU_SEQLENS", -17: "VSSM_ERR_LOOKBACK_TIMEOUT", -18: "VSSM_ERR_NONFINITE",
-       -19: "VSSM_ERR_DEVICE_CHECK", -20: "VSSM_ERR_BAD_INDEX"}
+       -19: "VSSM_ERR_DEVICE_CHECK", -20: "VSSM_ERR_BAD_INDEX",
+       -21: "VSSM_ERR_BAD_SAVED"}
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _f32 = ctypes.c_float

@@ -357,6 +357,7 @@ extern "C" {
 
 int vssm_status_code(int32_t w) {
   if (w & kStatusBadCu) return VSSM_ERR_BAD_CU_SEQLENS;
+  if (w & kStatusBadSaved) return VSSM_ERR_BAD_SAVED;
   if (w & kStatusBadIndex) return VSSM_ERR_BAD_INDEX;
   if (w & (kStatusLookbackTimeout | kStatusTmaTimeout)) return VSSM_ERR_LOOKBACK_TIMEOUT;
   if (w & kStatusDeviceCheck) return VSSM_ERR_DEVICE_CHECK;
@@ -376,6 +377,7 @@ const char* vssm_strerror(int code) {
     case VSSM_ERR_BAD_CU_SEQLENS: return "malformed cu_seqlens, or position indices that disagree with it (device check)";
     case VSSM_ERR_LOOKBACK_TIMEOUT: return "a device-side wait timed out: look-back or tile copy (device check)";
     case VSSM_ERR_NONFINITE: return "an output holds a NaN or an infinity (VSSM_DBG_CHECK_FINITE)";
+    case VSSM_ERR_BAD_SAVED: return "a saved array that no forward call of this shape filled (device check)";
     case VSSM_ERR_BAD_INDEX: return "a position or state index outside its table (device check)";
     case VSSM_ERR_DEVICE_CHECK: return "a device-side index check failed (VSSM_CHECKS build)";
   }

@@ -69,9 +69,10 @@ struct DeltaArgs {
   void *dq, *dk, *dv;         // (T, Hk, K) x2, (T, Hv, V)
   float *dg, *dbeta;          // (T, Hv)
   // the plan of the pack and what the chunks keep (see DeltaLayout)
-  int* info;      // [0]: chunks in the pack, -1 when cu_seqlens is malformed
+  int* info;      // [0]: chunks in the pack, -1 when cu_seqlens is malformed; [1]: key
+  int key;        // what says that a plan is this shape's
   int* first;     // (S + 1): each sequence's first chunk
-  int* order;     // (S): the sequences, longest (about) first
+  int4* order;    // (S): sequence, first token, tokens, first chunk; longest (about) first
   int4* table;    // per chunk: sequence, first token, tokens, place in the sequence
   float* gates;   // (chunks, Hv, kDeltaGates)
   uint8_t* kq;    // (chunks, Hk, in terms, K panels) images of [K; Q], 128 rows of 64

@@ -2,6 +2,7 @@
 // rotation of queries and keys: argument checks, workspace layout, launches.
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -97,7 +98,7 @@ DeltaLayout delta_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO 
   const size_t rows = tiles * mid * kRowTile, states = rows * kp;
   size_t o = 256;
   l.first = o; o += up((S + 1) * sizeof(int));
-  l.order = o; o += up(S * sizeof(int));
+  l.order = o; o += up(S * sizeof(int4));
   l.table = o; o += up(nc * sizeof(int4));
   l.gates = o; o += up(nc * Hv * kDeltaGates * sizeof(float));
   l.kq = o; o += up(nc * Hk * delta_in_terms(io) * kp * 16384);
@@ -119,11 +120,18 @@ bool sizes_ok(int64_t T, int32_t S, int32_t Hk, int32_t Hv, int32_t K, int32_t V
   return check_dtype(dt, &io) == VSSM_OK && check_pack(T, S, &cu, Hk, Hv, K, V) == VSSM_OK;
 }
 
+// Tells the plan of one shape from another's, and both from memory that holds none.
+int plan_key(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io) {
+  uint64_t h = 0x9e3779b97f4a7c15ull;
+  for (int64_t v : {T, S, (int64_t)Hk, (int64_t)Hv, (int64_t)K, (int64_t)V, (int64_t)io}) h = (h ^ (uint64_t)v) * 0x100000001b3ull;
+  return (int)(h >> 16 | 1);
+}
+
 void set_plan(DeltaArgs& a, const void* base, const DeltaLayout& l, bool saved) {
   char* p = const_cast<char*>(static_cast<const char*>(base));
   a.info = reinterpret_cast<int*>(p) + 32;  // past the status word
   a.first = reinterpret_cast<int*>(p + l.first);
-  a.order = reinterpret_cast<int*>(p + l.order);
+  a.order = reinterpret_cast<int4*>(p + l.order);
   a.table = reinterpret_cast<int4*>(p + l.table);
   a.gates = reinterpret_cast<float*>(p + l.gates);
   a.kq = reinterpret_cast<uint8_t*>(p + l.kq);
@@ -184,6 +192,7 @@ int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t 
   a.status = static_cast<int*>(workspace);
   a.wait_ns = debug_knobs().wait_ns;
   a.max_chunks = delta_max_chunks(T, num_seqs);
+  a.key = plan_key(T, num_seqs, Hk, Hv, K, V, io);
   set_plan(a, saved ? saved : workspace, l, saved != nullptr);
   TRY(check(cudaMemsetAsync(workspace, 0, 128, st), "clearing the status word"));
   TRY(check(launch_delta_plan(a, st), "gated delta plan launch"));
@@ -218,13 +227,14 @@ int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seql
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DeltaArgs a{};
-  a.cu = cu_seqlens; a.T = T; a.num_seqs = num_seqs;
+  a.T = T; a.num_seqs = num_seqs;
   a.Hk = Hk; a.Hv = Hv; a.K = K; a.V = V; a.scale = scale; a.dout = dout;
   a.d_final = d_final_states; a.d_initial = d_initial_states;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta;
   a.status = static_cast<int*>(workspace);
   a.wait_ns = debug_knobs().wait_ns;
   a.max_chunks = delta_max_chunks(T, num_seqs);
+  a.key = plan_key(T, num_seqs, Hk, Hv, K, V, io);
   set_plan(a, saved, l, true);
   a.ds = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.ds);
   a.dvi = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.dvi);

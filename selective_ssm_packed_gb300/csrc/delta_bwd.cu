@@ -46,10 +46,13 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
   const int tiles = delta_tiles(a.V), groups = (tiles + kWalks - 1) / kWalks;
   const int group = blockIdx.x % groups;
   const int h = blockIdx.x / groups % a.Hv;
-  if (a.info[0] < 0) return;
-  const int s = a.order[blockIdx.x / groups / a.Hv];
-  const int c0 = a.first[s], n = a.first[s + 1] - c0;
-  const int64_t seq_start = a.cu[s], seq_len = a.cu[s + 1] - seq_start;
+  if (a.info[1] != a.key || a.info[0] < 0) {
+    if (threadIdx.x == 0) atomicOr(a.status, a.info[1] != a.key ? kStatusBadSaved : kStatusBadCu);
+    return;
+  }
+  const int4 sequence = a.order[blockIdx.x / groups / a.Hv];
+  const int s = sequence.x, c0 = sequence.w, n = (sequence.z + kDeltaChunk - 1) / kDeltaChunk;
+  const int64_t seq_start = sequence.y, seq_len = sequence.z;
   const int kh = h / (a.Hv / a.Hk);
   const int walks = min(kWalks, tiles - group * kWalks);
   if (n == 0 && !a.d_initial) return;

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
   const int rep = a.Hv / a.Hk;
   const int tiles = delta_tiles(a.V);
-  const int64_t all = a.info[0] < 0 ? 0 : (int64_t)a.info[0] * a.Hk;
+  const int64_t all = a.info[1] != a.key || a.info[0] < 0 ? 0 : (int64_t)a.info[0] * a.Hk;
   if (blockIdx.x >= all) return;
   const int items = (int)((all - 1 - blockIdx.x) / gridDim.x) + 1, per_item = rep * tiles;
   Waiter wait{a.wait_ns, a.status};

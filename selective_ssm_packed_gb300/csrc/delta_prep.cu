@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
     a.first[S] = carry;
     if (blockIdx.x == 0) {
       a.info[0] = total;
+      a.info[1] = a.key;
       if (!ok) atomicOr(a.status, kStatusBadCu);
     }
   }
@@ -79,7 +80,8 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
     }
     __syncthreads();
     for (int s = t; s < S; s += kPlanThreads)
-      a.order[atomicAdd(&classes[length_class(a.first[s + 1] - a.first[s])], 1)] = s;
+      a.order[atomicAdd(&classes[length_class(a.first[s + 1] - a.first[s])], 1)] =
+          make_int4(s, a.cu[s], a.cu[s + 1] - a.cu[s], a.first[s]);
   }
   for (int c = blockIdx.x * kPlanThreads + t; c < total; c += gridDim.x * kPlanThreads) {
     int lo = 0, hi = S - 1;  // the last sequence whose first chunk is at or before c
@@ -152,8 +154,8 @@ __device__ __forceinline__ void small_product(const float* A, int pa, const floa
 
 // (I + N)^-1 over N (64 rows, kNPitch floats apart, zero above the diagonal),
 // by 256 threads numbered t in any order of whole warps; y: 32 x 36 floats of
-// scratch.
-__device__ __forceinline__ void invert(float* n, float* y, int t) {
+// scratch.  N's rows from len on are zero, so a short chunk has nothing to join.
+__device__ __forceinline__ void invert(float* n, float* y, int t, int len) {
   if (t < 64) {
     const int r = t & 15;
     const float* block = n + (t & ~15) * (kNPitch + 1);
@@ -178,6 +180,7 @@ __device__ __forceinline__ void invert(float* n, float* y, int t) {
     for (int i = 0; i < 8; i += 2) *reinterpret_cast<float4*>(out + 2 * i) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
   }
   __syncthreads();
+  if (len <= 16) return;
   // Products of 4 x 4 values a thread: shared memory serves one float of a
   // vector read a cycle, repeated or not, and its cycles bound this kernel.
   {
@@ -192,6 +195,7 @@ __device__ __forceinline__ void invert(float* n, float* y, int t) {
                                  n + (at + 16 + i) * kNPitch + at + c, kNPitch);
     __syncthreads();
   }
+  if (len <= 32) return;
   const int i = (t >> 3) * 4, c = (t & 7) * 4;
   if (t < 64) small_product<4, 32, false>(n + (32 + i) * kNPitch, kNPitch, n + c, kNPitch, y + i * 36 + c, 36);
   __syncthreads();
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a) {
         *reinterpret_cast<uint4*>(images + k / 4 * 16384 + image_chunk<128>(row, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
-    invert(sn, reinterpret_cast<float*>(images), (t + 64 * blockIdx.x) & 255);  // scratch: where the rows of Tm go next
+    invert(sn, reinterpret_cast<float*>(images), (t + 64 * blockIdx.x) & 255, len);  // scratch: where the rows of Tm go next
     {
       const int tr = t >> 2, side = t & 3;
 #pragma unroll

@@ -22,7 +22,7 @@ constexpr int kStateChunk = 32;  // tokens per saved scan-state chunk
 
 // status-word bits written by kernels (the host maps them to VSSM_ERR_* codes)
 enum : int { kStatusBadCu = 1, kStatusLookbackTimeout = 2, kStatusTmaTimeout = 4, kStatusNonFinite = 8,
-             kStatusDeviceCheck = 16, kStatusBadIndex = 32 };
+             kStatusDeviceCheck = 16, kStatusBadIndex = 32, kStatusBadSaved = 64 };
 
 // ---------------------------------------------------------------- position indices
 // seq[t] = the sequence holding token t (read where sequences start or end).

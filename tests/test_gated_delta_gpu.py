@@ -257,6 +257,39 @@ def test_malformed_cu_seqlens_is_reported(cu):
     torch.cuda.synchronize()
 
 
+def test_a_saved_array_of_another_call_is_reported():
+    x = inputs([20], 1, 1, 16, 16, "f32", 13)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    size = binding.gated_delta_saved_size(20, 1, 1, 1, 16, 16, 0)
+    ws = torch.empty(binding.gated_delta_bwd_workspace_size(20, 1, 1, 1, 16, 16, 0), dtype=torch.uint8, device="cuda")
+    for saved in (torch.zeros(size, dtype=torch.uint8, device="cuda"),
+                  torch.full((size,), 255, dtype=torch.uint8, device="cuda")):
+        vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], saved, workspace=ws)
+        assert binding.read_status(ws) == -21
+    y = inputs([10, 10], 1, 1, 16, 16, "f32", 13)
+    _, saved = vs.varlen_gated_delta_fwd(*(y[n] for n in ("q", "k", "v", "g", "beta")), y["cu"])
+    vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], saved, workspace=ws)
+    assert binding.read_status(ws) == -21
+
+
+def test_the_calls_can_be_captured_in_a_graph():
+    x = inputs([70, 130], 1, 2, 64, 64, "bf16", 14, states=True)
+    ref = run(x, states=True)  # also sizes the kernels' shared memory, before the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, saved, final = vs.varlen_gated_delta_fwd(*(x[n] for n in ("q", "k", "v", "g", "beta")), x["cu"],
+                                                      initial_states=x["init"], final_states=True)
+        g = vs.varlen_gated_delta_bwd(*(x[n] for n in ("q", "k", "v", "g", "beta")), x["dout"], x["cu"], saved,
+                                      d_final_states=x["dfinal"], d_initial_states=True)
+    for t in (out, final, g["dq"]):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref["out"]) and torch.equal(final, ref["final"])
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "d_initial_states"):
+        assert torch.equal(g[n], ref[n]), n
+
+
 def test_non_finite_outputs_are_reported_when_asked():
     x = inputs([20], 1, 1, 16, 16, "f32", 12)
     ws = torch.empty(binding.gated_delta_fwd_workspace_size(20, 1, 1, 1, 16, 16, 0), dtype=torch.uint8, device="cuda")

@@ -157,3 +157,4 @@ def test_sizes(lib):
     assert binding.gated_delta_saved_size(16, 4, 3, 2, 64, 64, 0) == 0
     assert binding.gated_delta_saved_size(16, 4, 1, 2, 63, 64, 0) == 0
     assert binding.strerror(-20) and binding.status_code(32) == -20
+    assert binding.strerror(-21) and binding.status_code(64) == -21

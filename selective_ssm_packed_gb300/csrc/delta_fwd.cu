@@ -15,12 +15,16 @@ namespace {
 // The chain product - read back - product bounds a walk, not the matrix unit
 // (25% busy), so up to four walks share a CTA, its [K; Q] and its X: one
 // multiplies while others read back.  Wider tiles would read [K; Q] and X from
-// shared memory less often, but two walks of 64 columns took 1.6 times as long
-// as four of 32: with as many instructions to issue there were fewer chains to
-// issue them from.  [K; Q] and X come by bulk copies, ahead of the walks, asked
-// for by whichever walk is through with the buffer last.  Four walks leave a
-// thread 128 registers, so they read back 16 columns at a time: one spilled
-// register is a trip to L2, shared memory having taken nearly all of L1.
+// shared memory less often, but a step of 128 columns took two walks of 64 8900
+// cycles and four of 32 7600: with as many instructions to issue there were
+// fewer chains to issue them from.  [K; Q] and X come by bulk copies, ahead of
+// the walks, asked for by whichever walk is through with the buffer last.  Four
+// walks leave a thread 128 registers, so they read back 16 columns at a time:
+// one spilled register is a trip to L2, shared memory having taken nearly all
+// of L1.  CTAs that stay, with a fixed deal of the items and the next one's
+// operands already on their way, took 726 us at 32768 tokens where these take
+// 448: sequences are unequal, and the hardware hands the next CTA to the SM
+// that is free.
 template <IO kIO, int KP, int kWalks>
 struct FwdSmem {
   using D = DeltaTerms<kIO>;

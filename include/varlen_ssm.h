@@ -337,7 +337,7 @@ int varlen_conv1d_scan_fwd(const void* x, const float* conv_weight, const float*
  *     elements apart (at least heads * K, a multiple of 16 bytes), so that
  *     they may be slices of one projection's rows; 16-byte aligned.  Hq or Hk
  *     may be 0.
- *   q_out, k_out: contiguous, 16-byte aligned.
+ *   q_out, k_out: contiguous, 16-byte aligned, not overlapping q or k.
  *   cos, sin: (table_rows, rot / 2) f32, NULL when rot == 0 (positions unused).
  *   K a multiple of 8, 8 to 256; rot even, 0 to K.
  *   status: nullable device int32; a position outside the table ORs a bit into
@@ -373,10 +373,10 @@ int varlen_qk_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int6
  * q, k (T, Hk, K), v (T, Hv, V) io: heads contiguous, tokens q_stride /
  *   k_stride / v_stride elements apart (multiples of 16 bytes, at least the
  *   row), 16-byte aligned.  Hv is a multiple of Hk: value head j uses the
- *   query and key head j / (Hv / Hk).
+ *   query and key head j / (Hv / Hk); Hv is at most 65535.
  * g, beta (T, Hv) f32.  g is a log decay, usually <= 0 (values below -256 are
  *   taken as -256: both decay to zero).
- * out (T, Hv, V) io, contiguous, 16-byte aligned.
+ * out (T, Hv, V) io, contiguous, 16-byte aligned, not overlapping the inputs.
  * K a multiple of 8, 8 to 128; V a multiple of 8, 8 to 1024.
  * initial_states / final_states: nullable f32 (num_seqs, Hv, K, V), 16-byte
  *   aligned, as the selective scan's (an empty sequence's final state is its
@@ -403,11 +403,12 @@ int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t 
 
 /* Backward: dq, dk (T, Hk, K), dv (T, Hv, V) io, contiguous; dg, dbeta (T, Hv)
  * f32; d_initial_states nullable.  saved is the array the forward call on the
- * same inputs filled (read only; it holds the pack's plan too, which is what the
- * backward goes by, and an array that no forward call of this shape filled is
- * reported as VSSM_ERR_BAD_SAVED); scale is the forward call's; d_final_states: nullable, the gradient
- * reaching the final states.  dq and dk add the value heads that share a key head, in
- * order; no atomics, bitwise repeatable. */
+ * same inputs filled (read only; it holds the pack's plan too, which is what
+ * the backward goes by, and an array that no forward call of this shape filled is
+ * reported as VSSM_ERR_BAD_SAVED); scale is the forward call's;
+ * d_final_states: nullable, the gradient reaching the final states.  dq and dk
+ * add the value heads that share a key head, in order; no atomics, bitwise
+ * repeatable. */
 size_t varlen_gated_delta_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
                                              int32_t K, int32_t V, vssm_dtype dtype);
 int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seqlens, int32_t num_seqs,

@@ -464,11 +464,40 @@ def _stream_of(t, stream):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _asked(t, shape, like, dtype=torch.float32):
-    """None / False: not wanted; True: allocated; a tensor: filled."""
+def _new(shape, dtype, like, stream):
+    """Memory on like's device that belongs to the stream the call runs on, so
+    that it can neither still be in use by another one nor go back to it
+    before the call's kernels are through."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _result(t, name, like, stream):
+    """(tensor, pointer) of a result of like's shape and type: t, looked over,
+    or new memory, as _new's."""
+    if t is not None:
+        return t, _shaped(t, name, like.shape, like.dtype)
+    if stream is None:
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    else:
+        t = _new(like.shape, like.dtype, like, stream)
+    return t, t.data_ptr() or None
+
+
+def _room(workspace, nbytes, like, stream):
+    """_ws, new memory being the call's stream's."""
+    if workspace is None:
+        return _new((max(int(nbytes), 16),), torch.uint8, like, stream)
+    return _ws(workspace, nbytes, like.device)
+
+
+def _asked(t, shape, like, stream):
+    """f32 result; None / False: not wanted; True: allocated; a tensor: filled."""
     if t is None or t is False:
         return None
-    return torch.empty(shape, dtype=dtype, device=like.device) if t is True else t
+    return _new(shape, torch.float32, like, stream) if t is True else t
 
 
 # ------------------------------------------------------------------ norm and rotation of queries and keys
@@ -478,12 +507,12 @@ QK_NORM_MODES = {"rms": 0, "l2": 1}
 def _norm_args(q, k, q_weight, k_weight, cos, sin, positions, mode):
     if mode not in QK_NORM_MODES:
         raise ValueError(f"mode must be one of {sorted(QK_NORM_MODES)}, got {mode!r}")
+    qp, sq = _heads(q, "q")
     T, Hq, K = q.shape
+    kp, sk = _heads(k, "k", q.dtype, width=K)
     Hk = k.shape[1]
     if k.shape[0] != T:
         raise ValueError(f"q has {T} tokens, k has {k.shape[0]}")
-    qp, sq = _heads(q, "q")
-    kp, sk = _heads(k, "k", q.dtype, width=K)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin must be given together")
     rows = half = 0
@@ -504,12 +533,11 @@ def varlen_qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=No
     rotation.  q and k may be slices of wider rows (heads contiguous).
     status: optional int32 tensor for positions outside the tables."""
     lead, (T, Hq, Hk, K, rot) = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, mode)
-    q_out = torch.empty((T, Hq, K), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty((T, Hk, K), dtype=q.dtype, device=q.device) if k_out is None else k_out
+    q_out, qp = _result(q_out, "q_out", q, stream)
+    k_out, kp = _result(k_out, "k_out", k, stream)
     _check(lib().varlen_qk_norm_rope_fwd(
-        *lead, T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), _shaped(q_out, "q_out", (T, Hq, K), q.dtype),
-        _shaped(k_out, "k_out", (T, Hk, K), q.dtype), _ptr(status, "status", torch.int32), _stream_of(q, stream)),
-        "varlen_qk_norm_rope_fwd")
+        *lead, T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), qp, kp, _ptr(status, "status", torch.int32),
+        _stream_of(q, stream)), "varlen_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -519,20 +547,16 @@ def varlen_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_ou
     dk_weight (else None); grads: tensors to fill instead, by those names."""
     lead, (T, Hq, Hk, K, rot) = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, mode)
     g = dict(grads or {})
-    make = {"dq": lambda: torch.empty((T, Hq, K), dtype=q.dtype, device=q.device),
-            "dk": lambda: torch.empty((T, Hk, K), dtype=q.dtype, device=q.device),
-            "dq_weight": lambda: torch.empty_like(q_weight) if q_weight is not None else None,
-            "dk_weight": lambda: torch.empty_like(k_weight) if k_weight is not None else None}
-    for n, f in make.items():
+    make = {"dq": ((T, Hq, K), q.dtype), "dk": ((T, Hk, K), q.dtype), "dq_weight": ((K,), torch.float32),
+            "dk_weight": ((K,), torch.float32)}
+    for n, w in (("dq", q), ("dk", k), ("dq_weight", q_weight), ("dk_weight", k_weight)):
         if n not in g:
-            g[n] = f()
-    ws = _ws(workspace, lib().varlen_qk_norm_rope_bwd_workspace_size(K), q.device)
+            g[n] = _new(*make[n], q, stream) if w is not None else None
+    ws = _room(workspace, lib().varlen_qk_norm_rope_bwd_workspace_size(K), q, stream)
     _check(lib().varlen_qk_norm_rope_bwd(
         *lead, _shaped(dq_out, "dq_out", (T, Hq, K), q.dtype), _shaped(dk_out, "dk_out", (T, Hk, K), q.dtype),
-        T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), _shaped(g["dq"], "dq", (T, Hq, K), q.dtype),
-        _shaped(g["dk"], "dk", (T, Hk, K), q.dtype), _shaped(g["dq_weight"], "dq_weight", (K,)),
-        _shaped(g["dk_weight"], "dk_weight", (K,)), _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_of(q, stream)),
-        "varlen_qk_norm_rope_bwd")
+        T, Hq, Hk, K, rot, QK_NORM_MODES[mode], float(eps), _dt(q), *(_shaped(g[n], n, *make[n]) for n in make),
+        _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_of(q, stream)), "varlen_qk_norm_rope_bwd")
     return g
 
 
@@ -550,13 +574,13 @@ def gated_delta_bwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
 
 
 def _delta_args(q, k, v, g, beta):
-    T, Hk, K = q.shape
-    Hv, V = v.shape[1], v.shape[2]
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError(f"q, k and v have {T}, {k.shape[0]} and {v.shape[0]} tokens")
     qp, sq = _heads(q, "q")
+    T, Hk, K = q.shape
     kp, sk = _heads(k, "k", q.dtype, Hk, K)
     vp, sv = _heads(v, "v", q.dtype)
+    _, Hv, V = v.shape
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k and v have {T}, {k.shape[0]} and {v.shape[0]} tokens")
     return [qp, kp, vp, sq, sk, sv, _shaped(g, "g", (T, Hv)), _shaped(beta, "beta", (T, Hv))], (T, Hk, Hv, K, V)
 
 
@@ -571,17 +595,19 @@ def varlen_gated_delta_fwd(q, k, v, g, beta, cu_seqlens, scale=None, out=None, s
     args, (T, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
     S, dt = cu_seqlens.numel() - 1, _dt(q)
     sizes = (T, S, Hk, Hv, K, V, dt)
-    out = torch.empty((T, Hv, V), dtype=q.dtype, device=q.device) if out is None else out
+    if S < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    out, op = _result(out, "out", v, stream)
     want_final = final_states is not None and final_states is not False
-    final_states = _asked(final_states, (S, Hv, K, V), q)
+    final_states = _asked(final_states, (S, Hv, K, V), q, stream)
     if saved is True:
-        saved = torch.empty(max(gated_delta_saved_size(*sizes), 16), dtype=torch.uint8, device=q.device)
+        saved = _new((max(gated_delta_saved_size(*sizes), 16),), torch.uint8, q, stream)
     elif saved is False:
         saved = None
-    ws = _ws(workspace, 256 if saved is not None else gated_delta_fwd_workspace_size(*sizes), q.device)
+    ws = _room(workspace, 256 if saved is not None else gated_delta_fwd_workspace_size(*sizes), q, stream)
     _check(lib().varlen_gated_delta_fwd(
         *args, float(K ** -0.5 if scale is None else scale), _ptr(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hk, Hv,
-        K, V, dt, _shaped(out, "out", (T, Hv, V), q.dtype), _shaped(initial_states, "initial_states", (S, Hv, K, V)),
+        K, V, dt, op, _shaped(initial_states, "initial_states", (S, Hv, K, V)),
         _shaped(final_states, "final_states", (S, Hv, K, V)), _ptr(saved, "saved", torch.uint8),
         saved.numel() if saved is not None else 0, _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_of(q, stream)),
         "varlen_gated_delta_fwd")
@@ -603,9 +629,9 @@ def varlen_gated_delta_bwd(q, k, v, g, beta, dout, cu_seqlens, saved, scale=None
               "dg": ((T, Hv), torch.float32), "dbeta": ((T, Hv), torch.float32)}
     for n, (shape, d) in shapes.items():
         if n not in r:
-            r[n] = torch.empty(shape, dtype=d, device=q.device)
-    r["d_initial_states"] = _asked(d_initial_states, (S, Hv, K, V), q)
-    ws = _ws(workspace, gated_delta_bwd_workspace_size(*sizes), q.device)
+            r[n] = _new(shape, d, q, stream)
+    r["d_initial_states"] = _asked(d_initial_states, (S, Hv, K, V), q, stream)
+    ws = _room(workspace, gated_delta_bwd_workspace_size(*sizes), q, stream)
     _check(lib().varlen_gated_delta_bwd(
         _shaped(dout, "dout", (T, Hv, V), q.dtype), float(K ** -0.5 if scale is None else scale),
         _ptr(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hk, Hv, K, V, dt, _ptr(saved, "saved", torch.uint8),
@@ -625,11 +651,11 @@ def varlen_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale=
     int32 tensor for indices outside the pool."""
     args, (B, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
     slots = states.shape[0]
-    out = torch.empty((B, Hv, V), dtype=q.dtype, device=q.device) if out is None else out
+    out, op = _result(out, "out", v, stream)
     _check(lib().varlen_gated_delta_step(
         *args, float(K ** -0.5 if scale is None else scale), _shaped(states, "states", (slots, Hv, K, V)),
-        _shaped(state_indices, "state_indices", (B,), torch.int32), slots, B, Hk, Hv, K, V, _dt(q),
-        _shaped(out, "out", (B, Hv, V), q.dtype), _ptr(status, "status", torch.int32), _stream_of(q, stream)),
+        _shaped(state_indices, "state_indices", (B,), torch.int32), slots, B, Hk, Hv, K, V, _dt(q), op,
+        _ptr(status, "status", torch.int32), _stream_of(q, stream)),
         "varlen_gated_delta_step")
     return out
 

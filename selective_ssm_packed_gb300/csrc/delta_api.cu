@@ -53,7 +53,7 @@ int check_ptr(const void* p, const char* name, bool needed) {
 
 int check_stride(int64_t stride, int64_t row, IO io, const char* name) {
   if (stride < row) return bad(VSSM_ERR_ARG, "%s %lld is below the row's %lld values", name, (long long)stride, (long long)row);
-  if (stride * io_bytes(io) % 16) return bad(VSSM_ERR_ALIGN, "%s %lld is not a multiple of 16 bytes", name, (long long)stride);
+  if (stride % (16 / io_bytes(io))) return bad(VSSM_ERR_ALIGN, "%s %lld is not a multiple of 16 bytes", name, (long long)stride);
   return VSSM_OK;
 }
 
@@ -67,6 +67,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // ---------------------------------------------------------------- gated delta rule
 int check_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
+  if (Hv > 65535) return bad(VSSM_ERR_UNSUPPORTED, "Hv = %d is above 65535", Hv);  // sizes then stay within 64 bits
   if (Hk < 1 || Hv < 1 || Hv % Hk) return bad(VSSM_ERR_ARG, "Hv = %d must be a positive multiple of Hk = %d", Hv, Hk);
   if (K < 8 || K > kDeltaMaxK || K % 8) return bad(VSSM_ERR_UNSUPPORTED, "K = %d is not a multiple of 8 in 8..%d", K, kDeltaMaxK);
   if (V < 8 || V > kDeltaMaxV || V % 8) return bad(VSSM_ERR_UNSUPPORTED, "V = %d is not a multiple of 8 in 8..%d", V, kDeltaMaxV);
@@ -258,7 +259,7 @@ int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t
   TRY(check_dtype(dtype, &io));
   if (batch < 0 || num_slots < 0) return bad(VSSM_ERR_ARG, "batch and num_slots must be >= 0");
   TRY(check_heads(Hk, Hv, K, V));
-  if (batch * Hv * ((V + 31) / 32) > 2147483647LL) return bad(VSSM_ERR_UNSUPPORTED, "batch %lld too large", (long long)batch);
+  if (batch > 2147483647LL || batch * Hv * ((V + 31) / 32) > 2147483647LL) return bad(VSSM_ERR_UNSUPPORTED, "batch %lld too large", (long long)batch);
   if (!state_indices && batch > num_slots)
     return bad(VSSM_ERR_ARG, "batch %lld exceeds num_slots %lld and state_indices is NULL", (long long)batch, (long long)num_slots);
   const bool any = batch > 0;

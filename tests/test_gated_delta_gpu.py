@@ -201,6 +201,62 @@ def test_repeats_streams_and_given_buffers(dtype):
     assert none is None and torch.equal(o2, ref["out"]) and torch.equal(f2, ref["final"])
 
 
+def test_new_memory_belongs_to_the_calls_stream():
+    # the calls wait behind a busy stream while their workspaces' memory, were it the current stream's, is written
+    # over by that one
+    x = inputs([130, 70, 300], 2, 4, 64, 72, "bf16", 11, states=True)
+    w, cos = torch.ones(64, device="cuda"), torch.ones(500, 16, device="cuda")
+    pos = torch.arange(500, dtype=torch.int32, device="cuda")
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    side = torch.cuda.Stream()
+
+    def calls(stream):
+        pool = x["init"].clone()
+        idx = torch.arange(3, dtype=torch.int32, device="cuda")
+        if stream is not None:
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(40_000_000)
+        out, saved, final = vs.varlen_gated_delta_fwd(*a, x["cu"], initial_states=x["init"], final_states=True, stream=stream)
+        again = vs.varlen_gated_delta_fwd(*a, x["cu"], saved=False, stream=stream)[0]
+        g = vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], saved, d_initial_states=True, stream=stream)
+        qo, ko = vs.varlen_qk_norm_rope_fwd(x["q"], x["k"], w, w, cos, cos, pos, stream=stream)
+        gn = vs.varlen_qk_norm_rope_bwd(x["q"], x["k"], w, w, cos, cos, pos, x["q"], x["k"], stream=stream)
+        o1 = vs.varlen_gated_delta_step(*(t[:3] for t in a), pool, idx, stream=stream)
+        res = dict(out=out, saved=saved, final=final, again=again, qo=qo, ko=ko, o1=o1, pool=pool,
+                   **{k: t for k, t in g.items()}, **{"n" + k: t for k, t in gn.items()})
+        if stream is not None:
+            junk = [torch.full((1 << n,), 255, dtype=torch.uint8, device="cuda") for n in range(9, 25) for _ in range(4)]
+            torch.cuda.synchronize()
+            del junk
+        return res
+
+    ref = calls(None)
+    got = calls(side)
+    torch.cuda.synchronize()
+    mine = [(s["address"], s["address"] + s["total_size"]) for s in torch.cuda.memory_snapshot()
+            if s["stream"] == side.cuda_stream]
+    for n, t in got.items():
+        if n != "pool":
+            assert any(lo <= t.data_ptr() < hi for lo, hi in mine), n
+        if n != "saved":
+            assert torch.equal(t, ref[n]), n
+
+
+def test_binding_refuses_what_has_no_three_axes():
+    x = inputs([4], 1, 2, 16, 16, "f32", 31)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    for i, bad in ((0, a[0].flatten(1)), (2, a[2].flatten(1)), (1, a[1][0])):
+        with pytest.raises(ValueError, match="tokens, "):
+            vs.varlen_gated_delta_fwd(*a[:i], bad, *a[i + 1:], x["cu"])
+    with pytest.raises(TypeError):
+        vs.varlen_gated_delta_fwd(None, *a[1:], x["cu"])
+    with pytest.raises(ValueError):
+        vs.varlen_gated_delta_fwd(*a, x["cu"][:0])
+    with pytest.raises(ValueError, match="tokens, "):
+        vs.varlen_qk_norm_rope_fwd(a[0].flatten(1), a[1])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_a_cut_sequence_continues_from_its_state(dtype):
     x = inputs([257], 1, 2, 64, 64, dtype, 8, states=True)

@@ -158,3 +158,13 @@ def test_sizes(lib):
     assert binding.gated_delta_saved_size(16, 4, 1, 2, 63, 64, 0) == 0
     assert binding.strerror(-20) and binding.status_code(32) == -20
     assert binding.strerror(-21) and binding.status_code(64) == -21
+
+
+def test_sizes_past_64_bits_are_refused(lib):
+    # products of these wrap around to small ones
+    assert fwd(lib, T=0, S=2**30, Hk=2**30, Hv=2**30, V=1024, K=8, sq=2**33, sk=2**33, sv=2**40) == -6
+    assert binding.gated_delta_saved_size(0, 2**30, 2**30, 2**30, 8, 1024, 0) == 0
+    assert fwd(lib, sq=2**62 + 1) == -3 and fwd(lib, sq=2**62 + 4, wsb=0) == -4  # in bytes 2^64 + 4 and 2^64 + 16
+    assert lib.varlen_gated_delta_step(16, 16, 16, 64, 64, 128, 16, 16, 1.0, 16, 16, 4, 2**60, 1, 16, 64, 64, 0, 16, None,
+                                       None) != 0
+    assert "too large" in binding.last_error()

@@ -195,7 +195,6 @@ int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t 
   a.max_chunks = delta_max_chunks(T, num_seqs);
   a.key = plan_key(T, num_seqs, Hk, Hv, K, V, io);
   set_plan(a, saved ? saved : workspace, l, saved != nullptr);
-  TRY(check(cudaMemsetAsync(workspace, 0, 128, st), "clearing the status word"));
   TRY(check(launch_delta_plan(a, st), "gated delta plan launch"));
   TRY(check(launch_delta_prep(a, io, st), "gated delta chunk launch"));
   TRY(check(launch_delta_fwd(a, io, st), "gated delta forward launch"));

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
     if (blockIdx.x == 0) {
       a.info[0] = total;
       a.info[1] = a.key;
-      if (!ok) atomicOr(a.status, kStatusBadCu);
+      *a.status = ok ? 0 : kStatusBadCu;  // the call's first word on it
     }
   }
   __threadfence_block();
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
 
 // ------------------------------------------------------------------ prep
 // One CTA of 256 threads per chunk and key head; the value heads that share
-// the key head follow each other.  Rows 0-63 of a product are K K^T, N and Tm,
+// the key head follow each other, or go to `split` CTAs where there are too few
+// of them to fill the GPU.  Rows 0-63 of a product are K K^T, N and Tm,
 // rows 64-127 Q K^T, P and P Tm; a thread has half a row.
 // Tm = (I + N)^-1 in place of N, in shared memory: the four 16 x 16 blocks of
 // the diagonal by substitution, then twice two neighbouring blocks' inverses
@@ -116,7 +117,9 @@ struct PrepSmem {
   using D = DeltaTerms<kIO>;
   static constexpr int kKq = D::kIn * KP * 16384, kX = D::kMid * 16384;
   static constexpr int kImages = kKq > kX ? kKq : kX;  // [K; Q], later X
-  static constexpr int oN = kImages, oG = oN + 64 * kNPitch * 4, oBeta = oG + kPrepHeads * 64 * 8;
+  // N, too, in the place of [K; Q] where X leaves room: two CTAs an SM then for K > 64 in f32, not one
+  static constexpr int kN = 64 * kNPitch * 4, oN = kX + kN <= kImages ? kX : kImages;
+  static constexpr int oG = oN + kN > kImages ? oN + kN : kImages, oBeta = oG + kPrepHeads * 64 * 8;
   static constexpr int oBar = oBeta + kPrepHeads * 64 * 4;
   static constexpr int kBytes = oBar + 64 + 1024;
 };
@@ -205,7 +208,7 @@ __device__ __forceinline__ void invert(float* n, float* y, int t, int len) {
 }
 
 template <IO kIO, int KP>
-__global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int split) {
   using T = typename IoType<kIO>::type;
   using L = PrepSmem<kIO, KP>;
   constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid;
@@ -219,28 +222,26 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a) {
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
-  const int kh = blockIdx.x % a.Hk;
-  const int64_t c = blockIdx.x / a.Hk;
+  const int share = blockIdx.x % split, kh = blockIdx.x / split % a.Hk;
+  const int64_t c = blockIdx.x / split / a.Hk;
   if (c >= a.info[0]) return;
   const int4 chunk = a.table[c];
   const int64_t start = chunk.y;
   const int len = chunk.z;
   const int rep = a.Hv / a.Hk;
+  const int h0 = kh * rep + rep * share / split, h1 = kh * rep + rep * (share + 1) / split;  // value heads
 
   if (t == 0) {
     mbar_init(bar, 1);
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc<128>(tmem_at);
-  if (t < 32)  // N's upper right quarter, which nothing writes
-#pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(sn + t * kNPitch + 32 + 4 * i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
-  // warp w: the gates of value head hh + w
-  auto make_gates = [&](int hh) {
-    if (warp >= kPrepHeads || hh + warp >= rep) return;
+  // warp w: the gates of value head h + w
+  auto make_gates = [&](int h) {
+    const int hw = h + warp;
+    if (warp >= kPrepHeads || hw >= h1) return;
     // the running sum of g, in double: differences of it enter exp
-    const int hw = kh * rep + hh + warp;
     float g[2], b[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a) {
       }
     }
   }
-  make_gates(0);  // while [K; Q] is on its way
+  make_gates(h0);  // while [K; Q] is on its way
   if constexpr (kIO == IO::BF16) asm volatile("cp.async.wait_group 0;" ::: "memory");
   fence_async_smem();
   tmem_fence_before_sync();
@@ -328,25 +329,27 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a) {
     const Operand<128, kKMajor, NQ, kTerm, 16384> kq(smem_u32(images));
     umma_terms<64, KP * 4, NQ>(tm, kq, kq, false);  // B: the K rows
     umma_commit(bar);
-    bulk_store_1d(a.kq + (size_t)(c * a.Hk + kh) * L::kKq, images, L::kKq);
+    if (share == 0) bulk_store_1d(a.kq + (size_t)(c * a.Hk + kh) * L::kKq, images, L::kKq);
     bulk_commit();
   }
   Waiter wait{a.wait_ns, a.status};
   uint32_t phase = 0;
 
-  for (int hh = 0; hh < rep; ++hh) {
-    const int h = kh * rep + hh;
+  for (int h = h0; h < h1; ++h) {
     const int64_t ch = c * a.Hv + h;
-    if (hh && hh % kPrepHeads == 0) make_gates(hh);
+    if (h > h0 && (h - h0) % kPrepHeads == 0) make_gates(h);
     if (t == 0) bulk_wait_read();  // [K; Q], or the last head's X, has left
     __syncthreads();
-    if (hh == 0) {
+    if (h == h0) {
       wait(bar, phase);
       phase ^= 1;
       tmem_fence_after_sync();
+      if (t < 32)  // N's upper right quarter, which nothing else writes
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(sn + t * kNPitch + 32 + 4 * i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    const float2* sg = sg_all + (hh % kPrepHeads) * 64;
-    const float* sbeta = sbeta_all + (hh % kPrepHeads) * 64;
+    const float2* sg = sg_all + ((h - h0) % kPrepHeads) * 64;
+    const float* sbeta = sbeta_all + ((h - h0) % kPrepHeads) * 64;
     if (!empty) {
       const float2 gi = sg[r];
       const float f = is_k ? 1.0f : a.scale;
@@ -431,7 +434,9 @@ cudaError_t run_prep(const DeltaArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_prep_kernel<kIO, KP>), bytes, done);
   if (e != cudaSuccess) return e;
-  delta_prep_kernel<kIO, KP><<<(unsigned)(a.max_chunks * a.Hk), 256, bytes, st>>>(a);
+  const int64_t blocks = a.max_chunks * a.Hk, rep = a.Hv / a.Hk, free = 152 * 2 / blocks;
+  const int split = (int)(free < 1 ? 1 : free < rep ? free : rep);
+  delta_prep_kernel<kIO, KP><<<(unsigned)(blocks * split), 256, bytes, st>>>(a, split);
   return cudaGetLastError();
 }
 

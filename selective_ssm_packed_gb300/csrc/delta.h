@@ -82,6 +82,7 @@ struct DeltaArgs {
   uint8_t* ds;    // bwd: images of dS1, laid out as s0
   uint8_t* dvi;   // bwd: images of dV, laid out as e
   uint8_t* doi;   // bwd: images of dO, (chunks, Hv, tiles, in terms)
+  float* partial; // bwd: the value heads' parts of dk and dq, (chunks, Hv, 2, 64, K), or null
   int* status;
   unsigned long long wait_ns;
   int64_t max_chunks;
@@ -90,6 +91,17 @@ struct DeltaArgs {
 // The most chunks a pack of T tokens in num_seqs sequences can have.
 inline int64_t delta_max_chunks(int64_t T, int64_t num_seqs) {
   return T / kDeltaChunk + (num_seqs < T ? num_seqs : T);
+}
+
+// Whether the gradients' value heads go to CTAs of their own: where that
+// spares a third of the rounds of 152 CTAs, each of which takes a CTA 16 us a
+// value head in f32 and 8.5 us in bf16 (128 x 128), while the parts are added
+// up in 3 to 7 us.  Four heads of one chunk: 63 -> 20 + 4 us in f32, 32 ->
+// 12 + 4 us in bf16; a quarter spared (192 chunks and key heads of four):
+// 145 -> 126 + 7 us and 72 -> 66 + 7 us.  The parts are 80 MB at most.
+inline bool delta_split_grads(int64_t max_chunks, int Hk, int Hv) {
+  const int64_t whole = (max_chunks * Hk + 151) / 152 * (Hv / Hk), split = (max_chunks * Hv + 151) / 152;
+  return 3 * split <= 2 * whole && split <= 8;
 }
 
 // Tiles a CTA of the bf16 walks takes, which share what they read.  A step of

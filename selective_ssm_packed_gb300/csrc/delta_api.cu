@@ -89,7 +89,7 @@ int check_pack(int64_t T, int32_t S, const int32_t* cu, int32_t Hk, int32_t Hv, 
 // [info][first chunks][order][chunk table][gates][images of [K; Q]][images of X], and
 // in a saved array [images of S0][images of E] behind them.
 struct DeltaLayout {
-  size_t first, order, table, gates, kq, x, plan_end, s0, e, saved_end, ds, dvi, doi, bwd_end;
+  size_t first, order, table, gates, kq, x, plan_end, s0, e, saved_end, ds, dvi, doi, partial, bwd_end;
 };
 
 DeltaLayout delta_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io) {
@@ -111,7 +111,8 @@ DeltaLayout delta_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO 
   l.ds = 256;
   l.dvi = l.ds + up(states);
   l.doi = l.dvi + up(rows);
-  l.bwd_end = l.doi + up(tiles * delta_in_terms(io) * kRowTile);
+  l.partial = l.doi + up(tiles * delta_in_terms(io) * kRowTile);
+  l.bwd_end = l.partial + (delta_split_grads((int64_t)nc, Hk, Hv) ? up(nc * Hv * 128 * K * sizeof(float)) : 0);
   return l;
 }
 
@@ -239,6 +240,7 @@ int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seql
   a.ds = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.ds);
   a.dvi = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.dvi);
   a.doi = reinterpret_cast<uint8_t*>(static_cast<char*>(workspace) + l.doi);
+  a.partial = l.bwd_end > l.partial ? reinterpret_cast<float*>(static_cast<char*>(workspace) + l.partial) : nullptr;
   TRY(check(cudaMemsetAsync(workspace, 0, 128, st), "clearing the status word"));
   TRY(check(launch_delta_bwd(a, io, st), "gated delta backward launch"));
   TRY(check(launch_delta_grads(a, io, st), "gated delta gradients launch"));

@@ -7,7 +7,9 @@ namespace {
 
 // An item is a chunk and a key head; the value heads that share the key head
 // follow each other, and dq and dk are summed over them in registers, in that
-// order.  CTAs of 256 threads, one an SM, take every gridDim-th item, so that the
+// order.  Where that leaves SMs idle (delta_split_grads) an item is one value
+// head, whose part of dq and dk goes to `partial` and is added to the others by
+// a second kernel, in the same order and so with the same bits.  CTAs of 256 threads, one an SM, take every gridDim-th item, so that the
 // next item's tiles and [K; Q] arrive while this one is worked on.  Products over the state's columns (tile by tile)
 // and over the chunk's tokens, rows 0-63 for the keys' tokens and 64-127 for
 // the queries':
@@ -66,6 +68,26 @@ __device__ __forceinline__ void kq_at(const uint8_t* images, int row, int col, f
   }
 }
 
+// A warp's 32 rows, kMine columns from half * kMine on: lane = row.
+template <typename T, int kMine>
+__device__ __forceinline__ void write_rows(T* out, int64_t stride, int rows, int width, int half, int lane,
+                                           const float2 (&x)[kMine / 2]) {
+  constexpr int kPer = 64 / (int)sizeof(T);  // values of a 64-byte piece of a row
+#pragma unroll
+  for (int p = 0; p < kMine / kPer; ++p) {
+    uint4 q[4];
+#pragma unroll
+    for (int u = 0; u < kPer / 16; ++u) {
+      float2 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[p * (kPer / 2) + 8 * u + i];
+      pack(v, q + u * 2, T());
+    }
+    const int col = half * kMine + p * kPer;
+    store_rows(out + col, stride, rows, width - col, lane, q);
+  }
+}
+
 template <IO kIO, int KP>
 __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
@@ -89,9 +111,10 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
   const int rep = a.Hv / a.Hk;
   const int tiles = delta_tiles(a.V);
-  const int64_t all = a.info[1] != a.key || a.info[0] < 0 ? 0 : (int64_t)a.info[0] * a.Hk;
+  const int heads = a.partial ? 1 : rep, shares = rep / heads;  // value heads of an item, items of a key head
+  const int64_t all = a.info[1] != a.key || a.info[0] < 0 ? 0 : (int64_t)a.info[0] * a.Hk * shares;
   if (blockIdx.x >= all) return;
-  const int items = (int)((all - 1 - blockIdx.x) / gridDim.x) + 1, per_item = rep * tiles;
+  const int items = (int)((all - 1 - blockIdx.x) / gridDim.x) + 1, per_item = heads * tiles;
   Waiter wait{a.wait_ns, a.status};
 
   if (t == 0) {
@@ -119,7 +142,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   tmem_fence_after_sync();
   const uint32_t tm = *tmem_at;
 
-  auto item_of = [&](int k) { return (int64_t)blockIdx.x + (int64_t)k * gridDim.x; };  // chunk * Hk + key head
+  auto item_of = [&](int k) { return (int64_t)blockIdx.x + (int64_t)k * gridDim.x; };  // (chunk * Hk + key head) * shares + share
   // tile i of this CTA's (item, head, tile) triples; an item's run on in every array
   auto load = [&](int64_t i) {
     const int st = (int)(i % ST);
@@ -144,7 +167,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   };
   auto load_kq = [&](int k) {
     mbar_arrive_expect_tx(&kq_full[k % ST], L::kKq);
-    bulk_load_1d(sm + L::oKq + k % ST * L::kKq, a.kq + item_of(k) * (size_t)L::kKq, L::kKq, &kq_full[k % ST]);
+    bulk_load_1d(sm + L::oKq + k % ST * L::kKq, a.kq + item_of(k) / shares * (size_t)L::kKq, L::kKq, &kq_full[k % ST]);
   };
   const bool copier = t == 7 * 32;
   if (copier) {
@@ -161,8 +184,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   uint32_t done_phase = 0;
 
   for (int k = 0; k < items; ++k) {
-    const int kh = (int)(item_of(k) % a.Hk);
-    const int64_t c = item_of(k) / a.Hk;
+    const int kh = (int)(item_of(k) / shares % a.Hk), share = (int)(item_of(k) % shares);
+    const int64_t c = item_of(k) / shares / a.Hk;
     const int4 chunk = a.table[c];
     const int64_t start = chunk.y;
     const int len = chunk.z;
@@ -170,12 +193,13 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
     const uint32_t kq = smem_u32(kq_image);
     wait(&kq_full[k % ST], (uint32_t)(k / ST) & 1);
 
-    float2 acc[kMine / 2];  // of dk (rows 0-63) or dq
+    float2 sum[kMine / 2];  // of dk (rows 0-63) or dq
 #pragma unroll
-    for (int i = 0; i < kMine / 2; ++i) acc[i] = splat2(0.0f);
+    for (int i = 0; i < kMine / 2; ++i) sum[i] = splat2(0.0f);
 
-    for (int hh = 0; hh < rep; ++hh) {
-      const int h = kh * rep + hh;
+    for (int hh = 0; hh < heads; ++hh) {
+      const int h = kh * rep + share + hh;
+      float2 acc[kMine / 2];  // this head's part
       const float* gates = a.gates + (c * a.Hv + h) * kDeltaGates;
       const float gate0 = gates[t], gate1 = t < 64 ? gates[256 + t] : 0.0f;  // on their way through the tiles
       float dot = 0.0f;
@@ -304,7 +328,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             da = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], da);
-            acc[8 * u + i] = fma2(splat2(f), x[i], acc[8 * u + i]);
+            acc[8 * u + i] = mul2(splat2(f), x[i]);
           }
           if (is_k) {
             tmem_sum<8, 1>(tB + lane_at + col, 0, x);
@@ -338,6 +362,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[8 * u + i] = add2(sum[8 * u + i], acc[8 * u + i]);
       }
       tmem_fence_before_sync();
       named_barrier(1, 256);  // the sums are in; the next head's products may begin
@@ -379,29 +405,42 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       }
     }
 
-    {
-      constexpr int kPer = 64 / (int)sizeof(T);  // values of a 64-byte piece of a row
-      const int first = (quad & 1) * 32;
+    const int first = (quad & 1) * 32;
+    if (a.partial) {
+      float* out = a.partial + ((item_of(k) * 2 + !is_k) * 64 + first) * a.K;
+      write_rows<float, kMine>(out, a.K, len - first, a.K, half, lane, sum);
+    } else {
       T* out = static_cast<T*>(is_k ? a.dk : a.dq) + ((start + first) * a.Hk + kh) * a.K;
-#pragma unroll
-      for (int p = 0; p < kMine / kPer; ++p) {
-        uint4 q[4];
-#pragma unroll
-        for (int u = 0; u < kPer / 16; ++u) {
-          float2 v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = acc[p * (kPer / 2) + 8 * u + i];
-          pack(v, q + u * 2, T());
-        }
-        const int col = half * kMine + p * kPer;
-        store_rows(out + col, (int64_t)a.Hk * a.K, len - first, a.K - col, lane, q);
-      }
+      write_rows<T, kMine>(out, (int64_t)a.Hk * a.K, len - first, a.K, half, lane, sum);
     }
     if (copier && k + ST < items) load_kq(k + ST);  // behind the last barrier nothing reads this item's
   }
   tmem_fence_before_sync();
   __syncthreads();
   if (warp == 0) tmem_dealloc<512>(tm);
+}
+
+// The value heads' parts of dk or dq of a chunk and key head, added in order:
+// 16 rows a CTA.
+template <typename T>
+__global__ void __launch_bounds__(256) delta_grad_sum_kernel(DeltaArgs a) {
+  if (a.info[1] != a.key || (int64_t)blockIdx.x >= (int64_t)a.info[0] * a.Hk) return;
+  const int rep = a.Hv / a.Hk, kh = blockIdx.x % a.Hk, wide = a.K / 4;
+  const int4 chunk = a.table[blockIdx.x / a.Hk];
+  const float* part = a.partial + ((int64_t)blockIdx.x * rep * 2 + blockIdx.y / 4) * 64 * a.K;
+  T* out = static_cast<T*>(blockIdx.y / 4 ? a.dq : a.dk) + ((int64_t)chunk.y * a.Hk + kh) * a.K;
+  const int r0 = blockIdx.y % 4 * 16, rows = min(16, chunk.z - r0);
+  for (int i = threadIdx.x; i < rows * wide; i += 256) {
+    const int r = r0 + i / wide, c = i % wide * 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int h = 0; h < rep; ++h) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)h * 128 * a.K + r * a.K + c);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    st_io2(out + (int64_t)r * a.Hk * a.K + c, make_float2(s.x, s.y));
+    st_io2(out + (int64_t)r * a.Hk * a.K + c + 2, make_float2(s.z, s.w));
+  }
 }
 
 template <IO kIO, int KP>
@@ -411,8 +450,11 @@ cudaError_t run_grads(const DeltaArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_smem(reinterpret_cast<const void*>(delta_grad_kernel<kIO, KP>), bytes, done);
   if (e != cudaSuccess) return e;
-  const int64_t items = a.max_chunks * a.Hk;
+  const int64_t items = a.max_chunks * (a.partial ? a.Hv : a.Hk);
   delta_grad_kernel<kIO, KP><<<(unsigned)(items < 152 ? items : 152), 256, bytes, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.partial) return e;
+  delta_grad_sum_kernel<typename IoType<kIO>::type><<<dim3((unsigned)(a.max_chunks * a.Hk), 8), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

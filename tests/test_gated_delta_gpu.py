@@ -243,6 +243,20 @@ def test_new_memory_belongs_to_the_calls_stream():
             assert torch.equal(t, ref[n]), n
 
 
+def test_a_sequence_has_the_same_bits_in_packs_of_any_size():
+    # few chunks spread their value heads over CTAs, many do not
+    r = []
+    for lens in ([100], [100, 64 * 40], [100, 64 * 400]):
+        x = inputs(lens, 2, 8, 64, 40, "bf16", 12)
+        small = inputs([100], 2, 8, 64, 40, "bf16", 13)
+        for n in ("q", "k", "v", "g", "beta", "dout"):
+            x[n][:100] = small[n]
+        r.append({n: t[:100] for n, t in run(x).items()})
+    for other in r[1:]:
+        for n, t in other.items():
+            assert torch.equal(t, r[0][n]), n
+
+
 def test_binding_refuses_what_has_no_three_axes():
     x = inputs([4], 1, 2, 16, 16, "f32", 31)
     a = [x[n] for n in ("q", "k", "v", "g", "beta")]

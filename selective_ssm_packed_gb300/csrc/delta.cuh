@@ -84,16 +84,17 @@ __device__ __forceinline__ void unpack(uint4 q, float2 (&v)[2]) {
   v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
 }
 
-// Four lanes, four chunks each: lane j's chunk i becomes lane i's chunk j.
-// A warp reads or writes 32 rows of 64 bytes with it four lanes to a row, eight
-// rows an instruction; a lane to a row would touch 32 lines with every
+// N lanes (four or two), N chunks each: lane j's chunk i becomes lane i's chunk
+// j.  A warp reads or writes 32 rows of 16 N bytes with it N lanes to a row,
+// 32 / N rows an instruction; a lane to a row would touch 32 lines with every
 // instruction (the forward walk spent more time on that than on its products).
-__device__ __forceinline__ void transpose4(uint4 (&q)[4], int lane) {
+template <int N>
+__device__ __forceinline__ void transpose(uint4 (&q)[N], int lane) {
 #pragma unroll
-  for (int o = 2; o >= 1; o >>= 1) {
+  for (int o = N / 2; o >= 1; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int a = 0; a < N; ++a) {
       if (a & o) continue;
       const uint4 give = up ? q[a] : q[a + o];
       uint4 got;
@@ -106,25 +107,26 @@ __device__ __forceinline__ void transpose4(uint4 (&q)[4], int lane) {
   }
 }
 
-// 32 rows of 64 bytes, row i of a warp at base + i * stride (in T); `rows` of
-// them exist and `cols` values of each.  Lane l gets (or gives) row l.
-template <typename T>
-__device__ __forceinline__ void load_rows(const T* base, int64_t stride, int rows, int cols, int lane, uint4 (&q)[4]) {
+// 32 rows of 16 N bytes, row i of a warp at base + i * stride (in T); `rows` of
+// them exist and `cols` values of each.  Lane l gets (or gives) row l, once
+// transposed.
+template <typename T, int N>
+__device__ __forceinline__ void load_rows(const T* base, int64_t stride, int rows, int cols, int lane, uint4 (&q)[N]) {
   constexpr int kPer = 16 / (int)sizeof(T);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (lane & ~3) + i, c = (lane & 3) * kPer;
+  for (int i = 0; i < N; ++i) {
+    const int r = (lane & ~(N - 1)) + i, c = (lane & (N - 1)) * kPer;
     q[i] = make_uint4(0, 0, 0, 0);
     if (r < rows && c < cols) q[i] = *reinterpret_cast<const uint4*>(base + r * stride + c);
   }
 }
-template <typename T>
-__device__ __forceinline__ void store_rows(T* base, int64_t stride, int rows, int cols, int lane, uint4 (&q)[4]) {
+template <typename T, int N>
+__device__ __forceinline__ void store_rows(T* base, int64_t stride, int rows, int cols, int lane, uint4 (&q)[N]) {
   constexpr int kPer = 16 / (int)sizeof(T);
-  transpose4(q, lane);
+  transpose(q, lane);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (lane & ~3) + i, c = (lane & 3) * kPer;
+  for (int i = 0; i < N; ++i) {
+    const int r = (lane & ~(N - 1)) + i, c = (lane & (N - 1)) * kPer;
     if (r < rows && c < cols) *reinterpret_cast<uint4*>(base + r * stride + c) = q[i];
   }
 }
@@ -148,6 +150,48 @@ __device__ __forceinline__ void pack(const float2 (&v)[8], uint4* q, float) {
     q[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y), __float_as_uint(v[2 * i + 1].x),
                       __float_as_uint(v[2 * i + 1].y));
 }
+
+// A thread's part of a tile's row in the walks: a walk alone on its SM has two
+// threads to a row, 16 columns each, the others one.
+template <int kWalks>
+constexpr int walk_threads() { return kWalks <= 2 ? 256 * kWalks : 128 * kWalks; }  // of a CTA
+
+template <typename T, int kWalks>
+struct WalkRow {
+  static constexpr int kThreads = walk_threads<kWalks>() / kWalks, kHalves = kThreads / 128;
+  static constexpr int kCols = kDeltaTile / kHalves, kSteps = kCols / 16;  // steps of 16 columns: two chunks of an image's row
+  static constexpr int kBytes = kCols * (int)sizeof(T), kPiece = kBytes < 64 ? kBytes : 64;  // as io values, in pieces
+  static constexpr int kParts = kBytes / kPiece, kChunks = kPiece / 16, kWide = kPiece / (int)sizeof(T);
+  static constexpr int kPer = 16 / (int)sizeof(T);
+  typedef uint4 Raw[kParts][kChunks];
+  // f(k, pair 8 u + k of the row) for k < 8
+  template <typename F>
+  static __device__ __forceinline__ void each(const Raw& raw, int u, F f) {
+#pragma unroll
+    for (int i = 0; i < 16 / kPer; ++i) {
+      const int at = u * (16 / kPer) + i;
+      float2 w[kPer / 2];
+      unpack(raw[at / kChunks][at % kChunks], w);
+#pragma unroll
+      for (int j = 0; j < kPer / 2; ++j) f(i * (kPer / 2) + j, w[j]);
+    }
+  }
+  static __device__ __forceinline__ void put(Raw& raw, int u, const float2 (&v)[8]) {
+    const int at = u * (16 / kPer);
+    pack(v, raw[at / kChunks] + at % kChunks, T());
+  }
+  // the warp's 32 rows from base on, of which `rows` exist and `cols` columns
+  static __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t rows, int cols, int lane, Raw& raw) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      load_rows(base + kWide * i, stride, (int)min((int64_t)32, rows), cols - kWide * i, lane, raw[i]);
+  }
+  static __device__ __forceinline__ void store(T* base, int64_t stride, int64_t rows, int cols, int lane, Raw& raw) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      store_rows(base + kWide * i, stride, (int)min((int64_t)32, rows), cols - kWide * i, lane, raw[i]);
+  }
+};
 
 // Waits of one thread of a chunk kernel: after one that runs out of time the
 // status word says so and the later ones no longer wait.  The timer is read

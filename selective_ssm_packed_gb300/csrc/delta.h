@@ -105,7 +105,7 @@ inline bool delta_split_grads(int64_t max_chunks, int Hk, int Hv) {
 }
 
 // Tiles a CTA of the bf16 walks takes, which share what they read.  A step of
-// one, two or four walks on an SM takes 2.2, 3.2 or 4.0 us (one sequence of
+// one, two or four walks on an SM takes 2.1, 3.1 or 4.0 us (one sequence of
 // 32768 tokens, 32 heads of 128 x 128): four are the fastest way through much
 // work, one is the fastest way along a sequence.  What a pack takes is about
 // the longer of all its steps over the SMs and of its longest sequence, which
@@ -113,7 +113,7 @@ inline bool delta_split_grads(int64_t max_chunks, int Hk, int Hv) {
 inline int delta_walks(const DeltaArgs& a) {
   const double chunks = (double)a.T / kDeltaChunk + 1.0, longest = 4.0 * chunks / (a.num_seqs > 0 ? a.num_seqs : 1) + 1.0;
   const int tiles = delta_tiles(a.V);
-  const double step[3] = {2.2, 3.2, 4.0};
+  const double step[3] = {2.1, 3.1, 4.0};
   int best = 1;
   double least = 0.0;
   for (int i = 0; i < 3 && (i == 0 || (1 << i) / 2 < tiles); ++i) {

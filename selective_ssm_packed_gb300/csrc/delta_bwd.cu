@@ -12,8 +12,8 @@ namespace {
 //   D2 += Tm^T Z = dV                   (64 rows; 64 to 127 are not used)
 //   D1 = [K; Q]^T [-exp(G) dV; scale exp(G) dO] and dS0 = exp(G_63) dS1 + D1
 // sZ holds 128 rows: dO as it is, then Z, then -exp(G) dV in the upper 64, and
-// dO scaled in the lower 64; sS dS1, then dV on its way out.  dS1, dO and dV of every chunk leave as images
-// for the gradients that need no walk.
+// dO scaled in the lower 64; sS dS1, then dV on its way out.  dS1, dO and dV of
+// every chunk leave as images for the gradients that need no walk.
 template <IO kIO, int KP, int kWalks>
 struct BwdSmem {
   using D = DeltaTerms<kIO>;
@@ -27,10 +27,11 @@ struct BwdSmem {
 };
 
 template <IO kIO, int KP, int kWalks>
-__global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
+  using R = WalkRow<T, kWalks>;
   using L = BwdSmem<kIO, KP, kWalks>;
-  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, ST = DeltaTerms<kIO>::kStages, BV = kDeltaTile, HP = BV / 2;
+  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, ST = DeltaTerms<kIO>::kStages, BV = kDeltaTile, HP = R::kCols / 2;
   constexpr int kTmemUsed = 2 * kWalks * NT * BV;
   constexpr int kTmemCols = kTmemUsed > 256 ? 512 : kTmemUsed > 128 ? 256 : 128;
   extern __shared__ uint8_t smem_raw[];
@@ -93,19 +94,17 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
   const uint32_t tm = *tmem_at;
   Waiter wait{a.wait_ns, a.status};
 
-  if (warp / 4 < walks) {
-    const int walk = warp / 4, quad = warp & 3;
+  if ((int)threadIdx.x / R::kThreads < walks) {
+    const int walk = threadIdx.x / R::kThreads, quad = warp & 3, half = warp / 4 % R::kHalves;
     const int row = quad * 32 + lane, r = row & 63;
-    const bool leader = (threadIdx.x & 127) == 96, porter = (threadIdx.x & 127) == 64;  // as in the forward
+    const bool leader = threadIdx.x % R::kThreads == 96, porter = threadIdx.x % R::kThreads == 64;  // as in the forward
     const int tile = group * kWalks + walk;
-    const int col0 = tile * BV;
+    const int col0 = tile * BV + half * R::kCols, step0 = half * R::kSteps;  // this thread's columns
     uint8_t* sS = sm + L::oWalk + walk * L::kWalk;
     uint8_t* sZ = sS + L::kS;
     uint64_t* done = done_all + walk;
     const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
     const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
-    constexpr int kSteps = BV / 16;  // of 16 columns: two chunks of an image's row, eight pairs
-    constexpr int kParts = 32 * (int)sizeof(T) / 64;  // 64-byte pieces of a row of io values
     const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
 
     float2 S[HP];
@@ -121,8 +120,7 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
         }
     }
     // the next chunk's dO, raw, and gates: read a chunk ahead
-    constexpr int kPer = 16 / (int)sizeof(T);
-    uint4 raw[kParts][4];
+    typename R::Raw raw;
     float gam, decb, gam_end;
     auto prefetch = [&](int c) {
       const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
@@ -131,37 +129,29 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       gam_end = gates[63];
       const int64_t at = (int64_t)c * kDeltaChunk + (quad & 1) * 32;  // the warp's first token
       if (row >= 64)
-#pragma unroll
-        for (int i = 0; i < kParts; ++i)
-          load_rows(static_cast<const T*>(a.dout) + ((seq_start + at) * a.Hv + h) * a.V + col0 + 16 * i,
-                    (int64_t)a.Hv * a.V, (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, raw[i]);
+        R::load(static_cast<const T*>(a.dout) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V, seq_len - at,
+                a.V - col0, lane, raw);
     };
     // rows 64-127: dO into sZ, as it is and scaled
     auto put_dout = [&]() {
 #pragma unroll
-      for (int i = 0; i < kParts; ++i) transpose4(raw[i], lane);
+      for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
+      for (int u = 0; u < R::kSteps; ++u) {
         float2 d[8];
-#pragma unroll
-        for (int i = 0; i < 16 / kPer; ++i) {
-          float2 w[kPer / 2];
-          unpack(raw[u * kParts / 2][u * (16 / kPer) % 4 + i], w);
-#pragma unroll
-          for (int j = 0; j < kPer / 2; ++j) d[i * (kPer / 2) + j] = w[j];
-        }
-        put_row<NQ, 64>(sZ, L::kZTile, r, 2 * u, d);
+        R::each(raw, u, [&](int k, float2 w) { d[k] = w; });
+        put_row<NQ, 64>(sZ, L::kZTile, r, 2 * (step0 + u), d);
         scale_row(d, a.scale * gam);
-        put_row<NT, 64>(sZ, L::kZTile, row, 2 * u, d);
+        put_row<NT, 64>(sZ, L::kZTile, row, 2 * (step0 + u), d);
       }
     };
     if (n > 0) {
       prefetch(n - 1);
       if (row >= 64) put_dout();
     }
-    if (row < KP * 64) put_row<NT, 64>(sS, L::kSTile, row, 0, S);
+    if (row < KP * 64) put_row<NT, 64>(sS, L::kSTile, row, 2 * step0, S);
     fence_async_smem();
-    named_barrier(1 + walk, 128);
+    named_barrier(1 + walk, R::kThreads);
     uint32_t phase = 0;
 
     for (int i = 0; i < n; ++i) {
@@ -202,16 +192,16 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       tmem_fence_after_sync();
       if (row < 64) {
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
+        for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
           if (has_state) {
-            tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
+            tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
             scale_row(d, db_row);
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) d[k] = splat2(0.0f);
           }
-          put_row<NT, 64>(sZ, L::kZTile, row, 2 * u, d);
+          put_row<NT, 64>(sZ, L::kZTile, row, 2 * (step0 + u), d);
         }
       }
       fence_async_smem();
@@ -220,7 +210,7 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
         bulk_wait_read();  // dS1's image has left too, before dV takes its place
         mbar_arrive(done);
       }
-      named_barrier(1 + walk, 128);
+      named_barrier(1 + walk, R::kThreads);
       if (leader) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x);
@@ -234,25 +224,23 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       tmem_fence_after_sync();
       if (porter && i + 1 < n && last_user(x_used)) load_x(i + 1);
       if (row < 64) {
-        uint4 q[kParts][4];
+        typename R::Raw q;
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
+        for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
-          put_row<NT, 64>(sS, kRowTile, row, 2 * u, d);  // dS1's images have been read
-          pack(d, q[u * kParts / 2] + u * (16 / kPer) % 4, T());
+          tmem_sum<8, NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
+          put_row<NT, 64>(sS, kRowTile, row, 2 * (step0 + u), d);  // dS1's images have been read
+          R::put(q, u, d);
           scale_row(d, -g_row);
-          put_row<NT, 64>(sZ, L::kZTile, row, 2 * u, d);
+          put_row<NT, 64>(sZ, L::kZTile, row, 2 * (step0 + u), d);
         }
         const int64_t at = (int64_t)c * kDeltaChunk + quad * 32;
-#pragma unroll
-        for (int i = 0; i < kParts; ++i)
-          store_rows(static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0 + 16 * i, (int64_t)a.Hv * a.V,
-                     (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, q[i]);
+        R::store(static_cast<T*>(a.dv) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V, seq_len - at,
+                 a.V - col0, lane, q);
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      named_barrier(1 + walk, 128);
+      named_barrier(1 + walk, R::kThreads);
       if (porter) {
         bulk_store_1d(a.dvi + (ch * tiles + tile) * (size_t)(NT * kRowTile), sS, NT * kRowTile);
         bulk_commit();
@@ -275,18 +263,18 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_bwd_kernel(DeltaArgs a)
       if (porter && i + ST < n && last_user(&kq_used[st])) load_kq(i + ST);
       if (row < KP * 64) {
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
+        for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
+          tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
 #pragma unroll
           for (int k = 0; k < 8; ++k) S[8 * u + k] = d[k] = fma2(splat2(g_end), S[8 * u + k], d[k]);
-          if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * u, d);
+          if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * (step0 + u), d);
         }
       }
       if (!last && row >= 64) put_dout();
       fence_async_smem();
       tmem_fence_before_sync();
-      named_barrier(1 + walk, 128);
+      named_barrier(1 + walk, R::kThreads);
     }
     if (porter) bulk_wait_all();
     if (a.d_initial && row < a.K) {
@@ -310,7 +298,7 @@ cudaError_t run_bwd(const DeltaArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int groups = (delta_tiles(a.V) + kWalks - 1) / kWalks;
   delta_bwd_kernel<kIO, KP, kWalks>
-      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * groups), 128 * kWalks, bytes, st>>>(a);
+      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * groups), walk_threads<kWalks>(), bytes, st>>>(a);
   return cudaGetLastError();
 }
 

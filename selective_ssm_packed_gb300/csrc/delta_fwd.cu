@@ -5,9 +5,9 @@ namespace vssm {
 namespace {
 
 // One CTA per (sequence, value head, kWalks tiles of the state's columns; the
-// columns never mix).  A walk is 128 threads and one tile: the state lives in
-// registers (FP32; thread = one row) and as bf16 terms in shared memory.  A
-// chunk is three products on the matrix unit, each read back from tensor
+// columns never mix).  A walk is one tile and 128 threads, or 256 where at most
+// two share a CTA: the state lives in registers (FP32; thread = one row or
+// half of one) and as bf16 terms in shared memory.  A chunk is three products on the matrix unit, each read back from tensor
 // memory by the walk's threads:
 //   D1 = [K; Q] S0        rows 0-63 become R, rows 64-127 wait in tensor memory
 //   D2 = [Tm; P Tm] R     rows 0-63 are E, rows 64-127 with D1's make O
@@ -38,10 +38,11 @@ struct FwdSmem {
 };
 
 template <IO kIO, int KP, int kWalks>
-__global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(DeltaArgs a) {
   using T = typename IoType<kIO>::type;
+  using R = WalkRow<T, kWalks>;
   using L = FwdSmem<kIO, KP, kWalks>;
-  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, ST = DeltaTerms<kIO>::kStages, BV = kDeltaTile, HP = BV / 2;
+  constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, ST = DeltaTerms<kIO>::kStages, BV = kDeltaTile, HP = R::kCols / 2;
   constexpr int kTmemUsed = 2 * kWalks * NT * BV;
   constexpr int kTmemCols = kTmemUsed > 256 ? 512 : kTmemUsed > 128 ? 256 : 128;
   extern __shared__ uint8_t smem_raw[];
@@ -100,21 +101,19 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
   const uint32_t tm = *tmem_at;
   Waiter wait{a.wait_ns, a.status};
 
-  if (warp / 4 < walks) {
-    const int walk = warp / 4, quad = warp & 3;
+  if ((int)threadIdx.x / R::kThreads < walks) {
+    const int walk = threadIdx.x / R::kThreads, quad = warp & 3, half = warp / 4 % R::kHalves;
     const int row = quad * 32 + lane, r = row & 63;  // of a product: token (K rows, then Q rows) or state row
     // one thread issues the products, another the bulk copies: in warps of Q rows, whose read-backs are the shorter ones
-    const bool leader = (threadIdx.x & 127) == 96, porter = (threadIdx.x & 127) == 64;
+    const bool leader = threadIdx.x % R::kThreads == 96, porter = threadIdx.x % R::kThreads == 64;
     const int tile = group * kWalks + walk;
-    const int col0 = tile * BV;
+    const int col0 = tile * BV + half * R::kCols, step0 = half * R::kSteps;  // this thread's columns
     uint8_t* sS = sm + L::oWalk + walk * L::kWalk;
     uint8_t* sR = sS + L::kS;
     uint8_t* sE = sR + L::kR;
     uint64_t* done = done_all + walk;
     const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
     const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
-    constexpr int kSteps = BV / 16;  // of 16 columns: two chunks of an image's row, eight pairs
-    constexpr int kParts = 32 * (int)sizeof(T) / 64;  // 64-byte pieces of a row of io values
     const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
 
     float2 S[HP];
@@ -130,8 +129,7 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
         }
     }
     // the next chunk's v, raw, and gates: read a chunk ahead
-    constexpr int kPer = 16 / (int)sizeof(T);
-    uint4 raw[kParts][4];
+    typename R::Raw raw;
     float gam, decb, gam_end;
     auto prefetch = [&](int c) {
       const float* gates = a.gates + ((int64_t)(c0 + c) * a.Hv + h) * kDeltaGates;
@@ -140,15 +138,13 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       gam_end = gates[63];
       const int64_t at = (int64_t)c * kDeltaChunk + quad * 32;  // the warp's first token
       if (row < 64)
-#pragma unroll
-        for (int i = 0; i < kParts; ++i)
-          load_rows(static_cast<const T*>(a.v) + (seq_start + at) * a.sv + (int64_t)h * a.V + col0 + 16 * i, a.sv,
-                    (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, raw[i]);
+        R::load(static_cast<const T*>(a.v) + (seq_start + at) * a.sv + (int64_t)h * a.V + col0, a.sv, seq_len - at,
+                a.V - col0, lane, raw);
     };
     if (n > 0) prefetch(0);
-    if (row < KP * 64) put_row<NT, 64>(sS, L::kSTile, row, 0, S);
+    if (row < KP * 64) put_row<NT, 64>(sS, L::kSTile, row, 2 * step0, S);
     fence_async_smem();
-    named_barrier(1 + walk, 128);
+    named_barrier(1 + walk, R::kThreads);
     uint32_t phase = 0;
 
     for (int c = 0; c < n; ++c) {
@@ -174,7 +170,7 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       const float g_row = gam, db_row = decb, g_end = gam_end;
       if (row < 64)
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) transpose4(raw[i], lane);
+        for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
       if (has_state) {
         wait(done, phase);
         phase ^= 1;
@@ -183,26 +179,17 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       if (row < 64) {
         // past the chunk's end v and the rows of K are zero, and so is R
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
+        for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          if (has_state) tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
-#pragma unroll
-          for (int i = 0; i < 16 / kPer; ++i) {
-            float2 w[kPer / 2];
-            unpack(raw[u * kParts / 2][u * (16 / kPer) % 4 + i], w);
-#pragma unroll
-            for (int j = 0; j < kPer / 2; ++j) {
-              const int k = i * (kPer / 2) + j;
-              d[k] = has_state ? fma2(splat2(-g_row), d[k], w[j]) : w[j];
-            }
-          }
-          put_row<NT, 64>(sR, kRowTile, row, 2 * u, d);
+          if (has_state) tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
+          R::each(raw, u, [&](int k, float2 w) { d[k] = has_state ? fma2(splat2(-g_row), d[k], w) : w; });
+          put_row<NT, 64>(sR, kRowTile, row, 2 * (step0 + u), d);
         }
       }
       fence_async_smem();
       tmem_fence_before_sync();
       if (porter && a.s0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last chunk's E has left
-      named_barrier(1 + walk, 128);
+      named_barrier(1 + walk, R::kThreads);
       if (leader) {
         tmem_fence_after_sync();
         wait(x_full, c & 1);
@@ -218,38 +205,36 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       if (porter && c + 1 < n && last_user(x_used)) load_x(c + 1);
       if (row < 64) {
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
+        for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
-          if (a.e) put_row<NT, 64>(sE, kRowTile, row, 2 * u, d);
+          tmem_sum<8, NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
+          if (a.e) put_row<NT, 64>(sE, kRowTile, row, 2 * (step0 + u), d);
           scale_row(d, db_row);
-          put_row<NT, 64>(sR, kRowTile, row, 2 * u, d);
+          put_row<NT, 64>(sR, kRowTile, row, 2 * (step0 + u), d);
         }
       } else {
-        uint4 q[kParts][4];
+        typename R::Raw q;
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
+        for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8], o[8];
-          tmem_sum<8, NT>(tD2 + lane_at + 16 * u, BV, d);
+          tmem_sum<8, NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
           if (has_state) {
-            tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, o);
+            tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, o);
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] = fma2(splat2(a.scale * g_row), o[i], d[i]);
           }
-          pack(d, q[u * kParts / 2] + u * (16 / kPer) % 4, T());
+          R::put(q, u, d);
         }
         const int64_t at = (int64_t)c * kDeltaChunk + (quad & 1) * 32;
-#pragma unroll
-        for (int i = 0; i < kParts; ++i)
-          store_rows(static_cast<T*>(a.out) + ((seq_start + at) * a.Hv + h) * a.V + col0 + 16 * i, (int64_t)a.Hv * a.V,
-                     (int)min((int64_t)32, seq_len - at), a.V - col0 - 16 * i, lane, q[i]);
+        R::store(static_cast<T*>(a.out) + ((seq_start + at) * a.Hv + h) * a.V + col0, (int64_t)a.Hv * a.V, seq_len - at,
+                 a.V - col0, lane, q);
       }
       const bool stop = last && !a.final_states;
       if (stop && !a.e) break;
       fence_async_smem();
       tmem_fence_before_sync();
       if (porter && a.s0) bulk_wait_read();  // S0's images are free to be overwritten
-      named_barrier(1 + walk, 128);
+      named_barrier(1 + walk, R::kThreads);
       if (porter && a.e) {
         bulk_store_1d(a.e + (ch * tiles + tile) * (size_t)(NT * kRowTile), sE, NT * kRowTile);
         bulk_commit();
@@ -268,17 +253,17 @@ __global__ void __launch_bounds__(128 * kWalks, 1) delta_fwd_kernel(DeltaArgs a)
       if (porter && c + ST < n && last_user(&kq_used[st])) load_kq(c + ST);
       if (row < KP * 64) {
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
+        for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD1 + lane_at + 16 * u, BV, d);
+          tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
 #pragma unroll
           for (int i = 0; i < 8; ++i) S[8 * u + i] = d[i] = fma2(splat2(g_end), S[8 * u + i], d[i]);
-          if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * u, d);
+          if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * (step0 + u), d);
         }
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      named_barrier(1 + walk, 128);
+      named_barrier(1 + walk, R::kThreads);
     }
     if (porter) bulk_wait_all();
     if (a.final_states && row < a.K) {
@@ -302,7 +287,7 @@ cudaError_t run_fwd(const DeltaArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int groups = (delta_tiles(a.V) + kWalks - 1) / kWalks;
   delta_fwd_kernel<kIO, KP, kWalks>
-      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * groups), 128 * kWalks, bytes, st>>>(a);
+      <<<(unsigned)((int64_t)a.num_seqs * a.Hv * groups), walk_threads<kWalks>(), bytes, st>>>(a);
   return cudaGetLastError();
 }
 

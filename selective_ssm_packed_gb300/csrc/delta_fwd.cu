@@ -7,8 +7,8 @@ namespace {
 // One CTA per (sequence, value head, kWalks tiles of the state's columns; the
 // columns never mix).  A walk is one tile and 128 threads, or 256 where at most
 // two share a CTA: the state lives in registers (FP32; thread = one row or
-// half of one) and as bf16 terms in shared memory.  A chunk is three products on the matrix unit, each read back from tensor
-// memory by the walk's threads:
+// half of one) and as bf16 terms in shared memory.  A chunk is three products
+// on the matrix unit, each read back from tensor memory by the walk's threads:
 //   D1 = [K; Q] S0        rows 0-63 become R, rows 64-127 wait in tensor memory
 //   D2 = [Tm; P Tm] R     rows 0-63 are E, rows 64-127 with D1's make O
 //   D1 = K^T (dec beta E) and S1 = exp(G_63) S0 + D1
@@ -24,7 +24,9 @@ namespace {
 // of L1.  CTAs that stay, with a fixed deal of the items and the next one's
 // operands already on their way, took 726 us at 32768 tokens where these take
 // 448: sequences are unequal, and the hardware hands the next CTA to the SM
-// that is free.
+// that is free.  Two threads to a row shorten the read-backs of a chain that
+// has little else to wait for: the walk of a 3001-token f32 pack 122 -> 108 us
+// (the walk back 168 -> 134), of one 32768-token bf16 sequence 1150 -> 1096 us.
 template <IO kIO, int KP, int kWalks>
 struct FwdSmem {
   using D = DeltaTerms<kIO>;

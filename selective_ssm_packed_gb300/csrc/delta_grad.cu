@@ -13,7 +13,7 @@ namespace {
 // next item's tiles and [K; Q] arrive while this one is worked on.  Products over the state's columns (tile by tile)
 // and over the chunk's tokens, rows 0-63 for the keys' tokens and 64-127 for
 // the queries':
-//   A = [dV; dO] S0^T    B = E dS1^T (rows 0-63)    W = [dV; dO] E^T    QK = [K; Q] K^T
+//   [A, W] = [dV; dO] [S0; E]^T    B = E dS1^T (rows 0-63)    QK = [K; Q] K^T
 //   C = [M2; M1] K       F = [M2; M1]^T [K; Q] (rows 0-63)
 // A, B, C and F are as wide as a state has rows; C takes W's and QK's columns,
 // so the four fill the SM's tensor memory.  Thread = one row, half the columns
@@ -25,8 +25,9 @@ struct GradSmem {
   static constexpr int kStages = kIO == IO::BF16 ? 2 : 1;  // of tiles, and of [K; Q]
   static constexpr int kKq = D::kIn * KP * 16384;
   static constexpr int kSTerm = KP * 64 * 64, kS = NT * kSTerm, kE = NT * kRowTile, kW = NT * 2 * kRowTile;
-  // a stage: S0, dS1, E, then term by term 64 rows of dV and 64 of dO
-  static constexpr int oS0 = 0, oDs = kS, oE = 2 * kS, oW = oE + kE, kStage = oW + kW;
+  // a stage: term by term S0 and, below it, E, so that one instruction has both for columns; dS1; then
+  // term by term 64 rows of dV and 64 of dO
+  static constexpr int kSE = kSTerm + kRowTile, oS0 = 0, oE = kSTerm, oDs = NT * kSE, oW = oDs + kS, kStage = oW + kW;
   static constexpr int kM = NT * 16384;  // [M2; M1], 128 rows of 64
   // M of its own, or (FP32, one stage) over the stage
   static constexpr bool kOwnM = kIO == IO::BF16;
@@ -149,11 +150,11 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
     uint8_t* to = sm + L::oStage + st * L::kStage;
     const size_t at = item_of((int)(i / per_item)) * per_item + i % per_item;
     mbar_arrive_expect_tx(&full[st], 2 * L::kS + L::kE + (NT + NQ) * kRowTile);
-    bulk_load_1d(to + L::oS0, a.s0 + at * L::kS, L::kS, &full[st]);
     bulk_load_1d(to + L::oDs, a.ds + at * L::kS, L::kS, &full[st]);
-    bulk_load_1d(to + L::oE, a.e + at * L::kE, L::kE, &full[st]);
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
+      bulk_load_1d(to + L::oS0 + k * L::kSE, a.s0 + (at * NT + k) * L::kSTerm, L::kSTerm, &full[st]);
+      bulk_load_1d(to + L::oE + k * L::kSE, a.e + (at * NT + k) * kRowTile, kRowTile, &full[st]);
       bulk_load_1d(to + L::oW + 2 * k * kRowTile, a.dvi + (at * NT + k) * kRowTile, kRowTile, &full[st]);
       if (k < NQ)
         bulk_load_1d(to + L::oW + (2 * k + 1) * kRowTile, a.doi + (at * NQ + k) * kRowTile, kRowTile, &full[st]);
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   constexpr int kWide = KP * 64, kMine = kWide / 2, kSteps = kMine / 16;  // state rows, and a thread's share of them
   const int row = quad * 32 + lane, r = row & 63;
   const bool is_k = row < 64;
-  const uint32_t tA = tm, tB = tm + 128, tC = tm + 256, tW = tC, tQK = tC + 64, tF = tm + 384;
+  const uint32_t tA = tm, tW = tm + kWide, tQK = tW + 64, tC = tW, tB = tm + 256, tF = tm + 384;
   const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
   const uint32_t m_at = smem_u32(sm + L::oM);
   const bool leader = t == 3 * 32;  // issues the products; its warp takes no part in <dS1, S0>
@@ -216,11 +217,10 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
         if (warp == 3) {
           if (leader) {
             const uint32_t at = smem_u32(stage);
-            const Operand<64, kKMajor, NT, L::kSTerm> S0(at + L::oS0), dS(at + L::oDs);
-            const Operand<64, kKMajor, NT, kRowTile> E(at + L::oE);
+            const Operand<64, kKMajor, NT, L::kSE> SE(at + L::oS0), E(at + L::oE);
+            const Operand<64, kKMajor, NT, L::kSTerm> dS(at + L::oDs);
             const Operand<64, kKMajor, NT, 2 * kRowTile> dW(at + L::oW);
-            umma_terms<64, 2, NT>(tW, dW, E, p > 0);
-            umma_terms<kWide, 2, NT>(tA, dW, S0, p > 0);
+            umma_terms<kWide + 64, 2, NT>(tA, dW, SE, p > 0);
             umma_terms<kWide, 2, NT>(tB, E, dS, p > 0);
             umma_commit(&empty[st]);
             if (p + 1 == tiles) umma_commit(done);
@@ -230,11 +230,11 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
           // <dS1, S0> over the tile: both images are permuted alike
           for (int q = t - (warp > 3 ? 32 : 0); q < L::kSTerm / 16; q += 224) {
             float2 x[4], y[4], w[4];
-            unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + (NT - 1) * L::kSTerm + q * 16), x);
+            unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + (NT - 1) * L::kSE + q * 16), x);
             unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + (NT - 1) * L::kSTerm + q * 16), y);
 #pragma unroll
             for (int m = NT - 2; m >= 0; --m) {
-              unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + m * L::kSTerm + q * 16), w);
+              unpack(*reinterpret_cast<const uint4*>(stage + L::oS0 + m * L::kSE + q * 16), w);
 #pragma unroll
               for (int j = 0; j < 4; ++j) x[j] = add2(x[j], w[j]);
               unpack(*reinterpret_cast<const uint4*>(stage + L::oDs + m * L::kSTerm + q * 16), w);

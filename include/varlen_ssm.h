@@ -464,7 +464,10 @@ int vssm_checks_build(void);
  * conv calls, the CTA with this index reports its tile-copy wait as timed out
  * once the copy has landed (-1 = off), so a test sees VSSM_ERR_LOOKBACK_TIMEOUT
  * in the call's status word without any copy failing; the conv calls' copy
- * waits also take their limit from VSSM_DBG_WAIT_NS.
+ * waits also take their limit from VSSM_DBG_WAIT_NS.  Both hold for the gated
+ * delta rule's packed calls too: the CTA with this index of each of their
+ * kernels reports its first wait as run out, and the whole CTA then leaves,
+ * once what it asked for has come in.
  * Returns VSSM_OK or VSSM_ERR_ARG. */
 #define VSSM_DBG_DROP_FLAG 1
 #define VSSM_DBG_WAIT_NS 2

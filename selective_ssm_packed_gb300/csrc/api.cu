@@ -349,7 +349,7 @@ int vssm::encode_tile_map(CUtensorMap* m, const void* base, IO io, int64_t T, in
 
 vssm::DebugKnobs vssm::debug_knobs() {
   return DebugKnobs{g_drop_ticket.load(), g_wait_ns.load(), g_delay_ticket.load(), g_delay_ns.load(),
-                    g_check_finite.load() != 0};
+                    g_force_copy_timeout.load(), g_check_finite.load() != 0};
 }
 
 // ============================================================================ C ABI

@@ -193,28 +193,69 @@ struct WalkRow {
   }
 };
 
-// Waits of one thread of a chunk kernel: after one that runs out of time the
-// status word says so and the later ones no longer wait.  The timer is read
-// once in 64 tries.
-struct Waiter {
-  unsigned long long limit;
-  int* status;
-  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return;
-    uint64_t t0 = 0;
-    while (limit) {
+// A thread's wait for a phase of `bar`; false once it has run out of time, which
+// it then says in the status word and to the CTA's other threads, who give up
+// theirs (*stop, a word in shared memory, 0 at first).  The timer is read once
+// in 64 tries.  forced: a test's wait, which counts as run out once it is over.
+__device__ __forceinline__ bool wait_or_stop(const DeltaArgs& a, volatile int* stop, uint64_t* bar, uint32_t parity,
+                                             bool forced = false) {
+  if (!forced && mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (;;) {
 #pragma unroll 1
-      for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > limit) {
-        atomicOr(status, kStatusTmaTimeout);
-        limit = 0;
-      }
+    for (int i = 0; i < 64; ++i) {
+      if (!mbar_try_wait(bar, parity)) continue;
+      if (!forced) return true;
+      t0 = 1;  // long ago
+      break;
     }
+    if (*stop) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > a.wait_ns) break;
+  }
+  *stop = 1;
+  atomicOr(a.status, kStatusTmaTimeout);
+  return false;
+}
+__device__ __forceinline__ bool forced_here(const DeltaArgs& a) { return (long long)blockIdx.x == a.force_timeout_cta; }
+
+// The waits of one thread of a CTA.  After one that has run out the thread
+// waits for nothing and, by `ok`, asks for no copy, issues no product and
+// arrives nowhere, so that what others wait for stays out and every wait of the
+// CTA ends; it still takes part in the barriers, up to one at which all threads
+// leave together, by a vote or by one thread's word from before an earlier
+// barrier (the forward walk's way: a vote in every chunk cost a walk alone on
+// its SM 3%, where this costs 1.5%).  What the CTA has asked for is then waited
+// for (drain_copies, and a commit behind the products) before its memory is
+// given back.
+struct Waiter {
+  const DeltaArgs& a;
+  volatile int* stop;
+  bool ok = true;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, bool forced = false) {
+    return ok = ok && wait_or_stop(a, stop, bar, parity, forced);
   }
 };
+
+// Barrier `id` over `count` threads; whether all of them are ok.
+__device__ __forceinline__ bool vote(int id, int count, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(count), "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+
+// Waits, with a limit, for all `count` copies that were asked for on `bar`.
+__device__ __forceinline__ void drain_copies(uint64_t* bar, int64_t count) {
+  if (count > 0) mbar_wait(bar, (uint32_t)(count - 1) & 1, kCopyDrainNs);
+}
 
 template <typename P>
 __device__ __forceinline__ P* align1024(P* p) {

@@ -85,6 +85,7 @@ struct DeltaArgs {
   float* partial; // bwd: the value heads' parts of dk and dq, (chunks, Hv, 2, 64, K), or null
   int* status;
   unsigned long long wait_ns;
+  long long force_timeout_cta;  // test knob: this CTA reports its first wait as run out
   int64_t max_chunks;
 };
 

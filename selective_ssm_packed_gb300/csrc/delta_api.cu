@@ -193,6 +193,7 @@ int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t 
   a.initial = initial_states; a.final_states = final_states;
   a.status = static_cast<int*>(workspace);
   a.wait_ns = debug_knobs().wait_ns;
+  a.force_timeout_cta = debug_knobs().force_copy_timeout;
   a.max_chunks = delta_max_chunks(T, num_seqs);
   a.key = plan_key(T, num_seqs, Hk, Hv, K, V, io);
   set_plan(a, saved ? saved : workspace, l, saved != nullptr);
@@ -234,6 +235,7 @@ int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seql
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta;
   a.status = static_cast<int*>(workspace);
   a.wait_ns = debug_knobs().wait_ns;
+  a.force_timeout_cta = debug_knobs().force_copy_timeout;
   a.max_chunks = delta_max_chunks(T, num_seqs);
   a.key = plan_key(T, num_seqs, Hk, Hv, K, V, io);
   set_plan(a, saved, l, true);

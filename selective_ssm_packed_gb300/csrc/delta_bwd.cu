@@ -39,9 +39,11 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);
   uint64_t* x_full = kq_full + ST;
   uint64_t* done_all = x_full + 1;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done_all + kWalks);
+  uint64_t* drained = done_all + kWalks;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
   int* kq_used = reinterpret_cast<int*>(tmem_at + 1);  // walks that are through with what a buffer holds
   int* x_used = kq_used + ST;
+  volatile int* stop = x_used + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = delta_tiles(a.V), groups = (tiles + kWalks - 1) / kWalks;
@@ -81,7 +83,8 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
       kq_used[i] = 0;
     }
     mbar_init(x_full, 1);
-    *x_used = 0;
+    *x_used = *stop = 0;
+    mbar_init(drained, walks);
     for (int i = 0; i < kWalks; ++i) mbar_init(&done_all[i], 2);  // the products, and the porter
     fence_mbar_init();
     for (int i = 0; i < ST && i < n; ++i) load_kq(i);
@@ -92,7 +95,8 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tm = *tmem_at;
-  Waiter wait{a.wait_ns, a.status};
+  Waiter wait{a, stop};
+  if (threadIdx.x == 96 && n > 0 && forced_here(a)) wait(&kq_full[0], 0, true);  // the first walk's leader
 
   if ((int)threadIdx.x / R::kThreads < walks) {
     const int walk = threadIdx.x / R::kThreads, quad = warp & 3, half = warp / 4 % R::kHalves;
@@ -169,22 +173,23 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
         bulk_store_1d(a.ds + (ch * tiles + tile) * (size_t)(NT * L::kSTile), sS, NT * L::kSTile);
         bulk_commit();
         asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        mbar_arrive(done);  // dO's image has left, before Z takes its place
+        if (wait.ok) mbar_arrive(done);  // dO's image has left, before Z takes its place
       }
       if (leader) {
         wait(&kq_full[st], (i / ST) & 1);
         tmem_fence_after_sync();
-        if (has_state) {
+        if (has_state && wait.ok) {
           const Operand<128, kKMajor, NQ, KP * 16384, 16384> A(kq);
           const Operand<64, kMnMajor, NT, L::kSTile, 0, L::kSTile> B(smem_u32(sS));
           umma_blocks<BV, KP * 4, NT, true>(tD1, A, B);
         }
-        wait(x_full, i & 1);
-        // (P Tm)^T: 64 rows; the instruction's other 64 come from whatever lies 8 KB further and are not read back
-        const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x + 64 * 128);
-        const Operand<64, kMnMajor, NQ, L::kZTile, 0, L::kZTile> B(smem_u32(sZ));
-        umma_blocks<BV, 4, NT, true>(tD2, A, B);
-        umma_commit(done);
+        if (wait(x_full, i & 1)) {
+          // (P Tm)^T: 64 rows; the instruction's other 64 come from whatever lies 8 KB further and are not read back
+          const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x + 64 * 128);
+          const Operand<64, kMnMajor, NQ, L::kZTile, 0, L::kZTile> B(smem_u32(sZ));
+          umma_blocks<BV, 4, NT, true>(tD2, A, B);
+          umma_commit(done);
+        }
       }
       const float g_row = gam, db_row = decb, g_end = gam_end;
       wait(done, phase);
@@ -208,10 +213,10 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
       tmem_fence_before_sync();
       if (porter) {
         bulk_wait_read();  // dS1's image has left too, before dV takes its place
-        mbar_arrive(done);
+        if (wait.ok) mbar_arrive(done);
       }
       named_barrier(1 + walk, R::kThreads);
-      if (leader) {
+      if (leader && wait.ok) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NT, 16384, 0, 8192> A(x);
         const Operand<64, kMnMajor, NT, L::kZTile, 0, L::kZTile> B(smem_u32(sZ));
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (porter && i + 1 < n && last_user(x_used)) load_x(i + 1);
+      if (porter && wait.ok && i + 1 < n && last_user(x_used)) load_x(i + 1);
       if (row < 64) {
         typename R::Raw q;
 #pragma unroll
@@ -246,11 +251,11 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
         bulk_commit();
         if (!(last && !a.d_initial)) {
           bulk_wait_read();
-          mbar_arrive(done);  // dV's image has left, before dS0 takes its place
+          if (wait.ok) mbar_arrive(done);  // dV's image has left, before dS0 takes its place
         }
       }
       if (last && !a.d_initial) break;
-      if (leader) {
+      if (leader && wait.ok) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);
         const Operand<64, kMnMajor, NT, L::kZTile, 0, L::kZTile> B(smem_u32(sZ));
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (porter && i + ST < n && last_user(&kq_used[st])) load_kq(i + ST);
+      if (porter && wait.ok && i + ST < n && last_user(&kq_used[st])) load_kq(i + ST);
       if (row < KP * 64) {
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
       if (!last && row >= 64) put_dout();
       fence_async_smem();
       tmem_fence_before_sync();
-      named_barrier(1 + walk, R::kThreads);
+      if (!vote(1 + walk, R::kThreads, wait.ok)) break;
     }
     if (porter) bulk_wait_all();
     if (a.d_initial && row < a.K) {
@@ -285,7 +290,16 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
     }
   }
   tmem_fence_before_sync();
-  __syncthreads();
+  if (!__syncthreads_and(wait.ok)) {
+    // nobody asks for anything any more: what is on its way comes in before the memory is given back
+    if ((int)threadIdx.x / R::kThreads < walks && threadIdx.x % R::kThreads == 96) umma_commit(drained);
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < ST; ++i) drain_copies(&kq_full[i], (i < n) + kq_used[i] / walks);
+      drain_copies(x_full, (n > 0) + *x_used / walks);
+      mbar_wait(drained, 0, kCopyDrainNs);
+    }
+    __syncthreads();
+  }
   if (warp == 0) tmem_dealloc<kTmemCols>(tm);
 }
 

@@ -52,9 +52,11 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);
   uint64_t* x_full = kq_full + ST;
   uint64_t* done_all = x_full + 1;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done_all + kWalks);
+  uint64_t* drained = done_all + kWalks;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
   int* kq_used = reinterpret_cast<int*>(tmem_at + 1);  // walks that are through with what a buffer holds
   int* x_used = kq_used + ST;
+  volatile int* stop = x_used + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = delta_tiles(a.V), groups = (tiles + kWalks - 1) / kWalks;
@@ -90,7 +92,8 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
       kq_used[i] = 0;
     }
     mbar_init(x_full, 1);
-    *x_used = 0;
+    *x_used = *stop = 0;
+    mbar_init(drained, walks);
     for (int i = 0; i < kWalks; ++i) mbar_init(&done_all[i], 1);
     fence_mbar_init();
     for (int i = 0; i < ST && i < n; ++i) load_kq(i);
@@ -101,7 +104,8 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tm = *tmem_at;
-  Waiter wait{a.wait_ns, a.status};
+  Waiter wait{a, stop};
+  if (threadIdx.x == 96 && n > 0 && forced_here(a)) wait(&kq_full[0], 0, true);  // the first walk's leader
 
   if ((int)threadIdx.x / R::kThreads < walks) {
     const int walk = threadIdx.x / R::kThreads, quad = warp & 3, half = warp / 4 % R::kHalves;
@@ -114,6 +118,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
     uint8_t* sR = sS + L::kS;
     uint8_t* sE = sR + L::kR;
     uint64_t* done = done_all + walk;
+    volatile int* leave = stop + 1 + walk;  // the porter's word on whether this chunk is the last
     const uint32_t tD1 = tm + walk * 2 * NT * BV, tD2 = tD1 + NT * BV;
     const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
     const int64_t state_at = (((int64_t)s * a.Hv + h) * a.K + row) * a.V + col0;
@@ -155,6 +160,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
       const bool last = c + 1 == n;
       const int64_t ch = (int64_t)(c0 + c) * a.Hv + h;
       const uint32_t kq = smem_u32(sm + L::oKq + st * L::kKq);
+      if (porter) *leave = *stop;
       if (porter && a.s0) {
         bulk_store_1d(a.s0 + (ch * tiles + tile) * (size_t)(NT * L::kSTile), sS, NT * L::kSTile);
         bulk_commit();
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
       if (leader) {
         wait(&kq_full[st], (c / ST) & 1);
         tmem_fence_after_sync();
-        if (has_state) {
+        if (has_state && wait.ok) {
           const Operand<128, kKMajor, NQ, KP * 16384, 16384> A(kq);
           const Operand<64, kMnMajor, NT, L::kSTile, 0, L::kSTile> B(smem_u32(sS));
           umma_blocks<BV, KP * 4, NT, true>(tD1, A, B);
@@ -194,17 +200,18 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
       named_barrier(1 + walk, R::kThreads);
       if (leader) {
         tmem_fence_after_sync();
-        wait(x_full, c & 1);
-        const Operand<128, kKMajor, NT, 16384> A(smem_u32(sm + L::oX));
-        const Operand<64, kMnMajor, NT, kRowTile, 0, kRowTile> B(smem_u32(sR));
-        umma_blocks<BV, 4, NT, true>(tD2, A, B);
-        umma_commit(done);
+        if (wait(x_full, c & 1)) {
+          const Operand<128, kKMajor, NT, 16384> A(smem_u32(sm + L::oX));
+          const Operand<64, kMnMajor, NT, kRowTile, 0, kRowTile> B(smem_u32(sR));
+          umma_blocks<BV, 4, NT, true>(tD2, A, B);
+          umma_commit(done);
+        }
       }
       if (!last) prefetch(c + 1);
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (porter && c + 1 < n && last_user(x_used)) load_x(c + 1);
+      if (porter && wait.ok && c + 1 < n && last_user(x_used)) load_x(c + 1);
       if (row < 64) {
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
@@ -242,17 +249,18 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
         bulk_commit();
       }
       if (stop) break;
-      if (leader) {
+      if (leader && wait.ok) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> A(kq);  // K^T: the first 64 rows
         const Operand<64, kMnMajor, NT, kRowTile, 0, kRowTile> B(smem_u32(sR));
         umma_blocks<BV, 4, NT, true>(tD1, A, B);
         umma_commit(done);
       }
+      const int left = *leave;
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
-      if (porter && c + ST < n && last_user(&kq_used[st])) load_kq(c + ST);
+      if (porter && wait.ok && c + ST < n && last_user(&kq_used[st])) load_kq(c + ST);
       if (row < KP * 64) {
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
@@ -266,6 +274,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
       fence_async_smem();
       tmem_fence_before_sync();
       named_barrier(1 + walk, R::kThreads);
+      if (left) break;
     }
     if (porter) bulk_wait_all();
     if (a.final_states && row < a.K) {
@@ -276,7 +285,16 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
     }
   }
   tmem_fence_before_sync();
-  __syncthreads();
+  if (!__syncthreads_and(wait.ok)) {
+    // nobody asks for anything any more: what is on its way comes in before the memory is given back
+    if ((int)threadIdx.x / R::kThreads < walks && threadIdx.x % R::kThreads == 96) umma_commit(drained);
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < ST; ++i) drain_copies(&kq_full[i], (i < n) + kq_used[i] / walks);
+      drain_copies(x_full, (n > 0) + *x_used / walks);
+      mbar_wait(drained, 0, kCopyDrainNs);
+    }
+    __syncthreads();
+  }
   if (warp == 0) tmem_dealloc<kTmemCols>(tm);
 }
 

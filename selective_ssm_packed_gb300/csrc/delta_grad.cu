@@ -107,7 +107,9 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   uint64_t* empty = full + ST;  // the products and the 8 warps have read a stage
   uint64_t* kq_full = empty + ST;
   uint64_t* done = kq_full + ST;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* drained = done + 1;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+  int* stop = reinterpret_cast<int*>(tmem_at + 1);
 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
   const int rep = a.Hv / a.Hk;
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   const int64_t all = a.info[1] != a.key || a.info[0] < 0 ? 0 : (int64_t)a.info[0] * a.Hk * shares;
   if (blockIdx.x >= all) return;
   const int items = (int)((all - 1 - blockIdx.x) / gridDim.x) + 1, per_item = heads * tiles;
-  Waiter wait{a.wait_ns, a.status};
+  Waiter wait{a, stop};
 
   if (t == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -125,6 +127,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       mbar_init(&kq_full[i], 1);
     }
     mbar_init(done, 1);
+    mbar_init(drained, 1);
+    *stop = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc<512>(tmem_at);
@@ -160,11 +164,13 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
         bulk_load_1d(to + L::oW + (2 * k + 1) * kRowTile, a.doi + (at * NQ + k) * kRowTile, kRowTile, &full[st]);
     }
   };
+  int64_t asked = 0, kq_asked = 0;  // tiles and [K; Q] that the copier has asked for, from the first on
   // one thread: once tile i's stage has been read, fill it for tile i + ST
   auto refill = [&](int64_t i) {
     if (i + ST >= (int64_t)items * per_item) return;
-    wait(&empty[i % ST], (uint32_t)(i / ST) & 1);
+    if (!wait(&empty[i % ST], (uint32_t)(i / ST) & 1)) return;
     load(i + ST);
+    asked = i + ST + 1;
   };
   auto load_kq = [&](int k) {
     mbar_arrive_expect_tx(&kq_full[k % ST], L::kKq);
@@ -172,8 +178,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   };
   const bool copier = t == 7 * 32;
   if (copier) {
-    for (int i = 0; i < ST && i < items; ++i) load_kq(i);
-    for (int i = 0; i < ST && i < items * per_item; ++i) load(i);
+    for (; kq_asked < ST && kq_asked < items; ++kq_asked) load_kq((int)kq_asked);
+    for (; asked < ST && asked < items * per_item; ++asked) load(asked);
   }
   constexpr int kWide = KP * 64, kMine = kWide / 2, kSteps = kMine / 16;  // state rows, and a thread's share of them
   const int row = quad * 32 + lane, r = row & 63;
@@ -184,6 +190,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   const bool leader = t == 3 * 32;  // issues the products; its warp takes no part in <dS1, S0>
   uint32_t done_phase = 0;
 
+  bool fine = true;
   for (int k = 0; k < items; ++k) {
     const int kh = (int)(item_of(k) / shares % a.Hk), share = (int)(item_of(k) % shares);
     const int64_t c = item_of(k) / shares / a.Hk;
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
     const int len = chunk.z;
     uint8_t* kq_image = sm + L::oKq + k % ST * L::kKq;
     const uint32_t kq = smem_u32(kq_image);
-    wait(&kq_full[k % ST], (uint32_t)(k / ST) & 1);
+    wait(&kq_full[k % ST], (uint32_t)(k / ST) & 1, k == 0 && leader && forced_here(a));
 
     float2 sum[kMine / 2];  // of dk (rows 0-63) or dq
 #pragma unroll
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       const float* gates = a.gates + (c * a.Hv + h) * kDeltaGates;
       const float gate0 = gates[t], gate1 = t < 64 ? gates[256 + t] : 0.0f;  // on their way through the tiles
       float dot = 0.0f;
-      if (leader) {
+      if (leader && wait.ok) {
         tmem_fence_after_sync();
         const Operand<128, kKMajor, NQ, KP * 16384, 16384> KQ(kq);
         umma_terms<64, KP * 4, NQ>(tQK, KQ, KQ, false);
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
         uint8_t* stage = sm + L::oStage + st * L::kStage;
         wait(&full[st], (uint32_t)(i / ST) & 1);
         if (warp == 3) {
-          if (leader) {
+          if (leader && wait.ok) {
             const uint32_t at = smem_u32(stage);
             const Operand<64, kKMajor, NT, L::kSE> SE(at + L::oS0), E(at + L::oE);
             const Operand<64, kKMajor, NT, L::kSTerm> dS(at + L::oDs);
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
           }
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive(&empty[st]);
+        if (lane == 0 && wait.ok) mbar_arrive(&empty[st]);
         if (copier && (L::kOwnM || p + 1 < tiles)) refill(i);
       }
       wait(done, done_phase);
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       fence_async_smem();
       tmem_fence_before_sync();
       named_barrier(1, 256);
-      if (leader) {
+      if (leader && wait.ok) {
         tmem_fence_after_sync();
         const Operand<128, kMnMajor, NQ, KP * 16384, 0, 16384> KQ(kq);
         const Operand<128, kKMajor, NT, 16384> M(m_at);
@@ -366,7 +373,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
         for (int i = 0; i < 8; ++i) sum[8 * u + i] = add2(sum[8 * u + i], acc[8 * u + i]);
       }
       tmem_fence_before_sync();
-      named_barrier(1, 256);  // the sums are in; the next head's products may begin
+      fine = vote(1, 256, wait.ok);  // the sums are in; the next head's products may begin
+      if (!fine) break;
       if (warp == 0) {
         // tokens 2 lane and 2 lane + 1
         float dg[2], end = 0.0f;
@@ -405,6 +413,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       }
     }
 
+    if (!fine) break;
     const int first = (quad & 1) * 32;
     if (a.partial) {
       float* out = a.partial + ((item_of(k) * 2 + !is_k) * 64 + first) * a.K;
@@ -413,10 +422,24 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       T* out = static_cast<T*>(is_k ? a.dk : a.dq) + ((start + first) * a.Hk + kh) * a.K;
       write_rows<T, kMine>(out, (int64_t)a.Hk * a.K, len - first, a.K, half, lane, sum);
     }
-    if (copier && k + ST < items) load_kq(k + ST);  // behind the last barrier nothing reads this item's
+    if (copier && k + ST < items) {
+      load_kq(k + ST);
+      kq_asked = k + ST + 1;
+    }  // behind the last barrier nothing reads this item's
   }
   tmem_fence_before_sync();
-  __syncthreads();
+  if (!__syncthreads_and(wait.ok)) {
+    // nobody asks for anything any more: what is on its way comes in before the memory is given back
+    if (leader) umma_commit(drained);
+    if (copier) {
+      for (int i = 0; i < ST; ++i) {
+        drain_copies(&full[i], (asked - i + ST - 1) / ST);
+        drain_copies(&kq_full[i], (kq_asked - i + ST - 1) / ST);
+      }
+      mbar_wait(drained, 0, kCopyDrainNs);
+    }
+    __syncthreads();
+  }
   if (warp == 0) tmem_dealloc<512>(tm);
 }
 

@@ -219,7 +219,9 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
   float2* sg_all = reinterpret_cast<float2*>(images + L::oG);  // running sum of g over ln 2, in two floats
   float* sbeta_all = reinterpret_cast<float*>(images + L::oBeta);
   uint64_t* bar = reinterpret_cast<uint64_t*>(images + L::oBar);
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 1);
+  uint64_t* drained = bar + 1;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* stop = reinterpret_cast<int*>(tmem_at + 1);
 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
   const int share = blockIdx.x % split, kh = blockIdx.x / split % a.Hk;
@@ -233,6 +235,8 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
 
   if (t == 0) {
     mbar_init(bar, 1);
+    mbar_init(drained, 1);
+    *stop = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc<128>(tmem_at);
@@ -332,7 +336,6 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
     if (share == 0) bulk_store_1d(a.kq + (size_t)(c * a.Hk + kh) * L::kKq, images, L::kKq);
     bulk_commit();
   }
-  Waiter wait{a.wait_ns, a.status};
   uint32_t phase = 0;
 
   for (int h = h0; h < h1; ++h) {
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
     if (t == 0) bulk_wait_read();  // [K; Q], or the last head's X, has left
     __syncthreads();
     if (h == h0) {
-      wait(bar, phase);
+      wait_or_stop(a, stop, bar, phase, t == 0 && forced_here(a));
       phase ^= 1;
       tmem_fence_after_sync();
       if (t < 32)  // N's upper right quarter, which nothing else writes
@@ -396,14 +399,14 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
     fence_async_smem();
     tmem_fence_before_sync();
     __syncthreads();
-    if (t == 0) {
+    if (t == 0 && !*stop) {
       tmem_fence_after_sync();
       const Operand<128, kKMajor, NT, 16384> A(smem_u32(images));
       const Operand<128, kMnMajor, NT, 16384> B(smem_u32(images));  // the rows of Tm
       umma_terms<64, 4, NT>(tm + 64, A, B, false);
       umma_commit(bar);
     }
-    wait(bar, phase);
+    wait_or_stop(a, stop, bar, phase);
     phase ^= 1;
     tmem_fence_after_sync();
     if (!is_k && !empty) {
@@ -416,13 +419,19 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
     }
     fence_async_smem();
     tmem_fence_before_sync();
-    __syncthreads();
+    if (!__syncthreads_and(!*stop)) break;  // a wait ran out: one that did has said so before it came here
     if (t == 0) {
       bulk_store_1d(a.x + (size_t)ch * L::kX, images, L::kX);
       bulk_commit();
     }
   }
-  if (t == 0) bulk_wait_all();
+  if (t == 0) {
+    bulk_wait_all();
+    if (*stop) {  // products that were not waited for
+      umma_commit(drained);
+      mbar_wait(drained, 0, kCopyDrainNs);
+    }
+  }
   tmem_fence_before_sync();
   __syncthreads();
   if (warp == 0) tmem_dealloc<128>(tm);

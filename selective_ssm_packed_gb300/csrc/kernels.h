@@ -232,6 +232,7 @@ struct DebugKnobs {
   unsigned long long wait_ns;
   long long delay_ticket;
   unsigned long long delay_ns;
+  long long force_copy_timeout;
   bool check_finite;
 };
 DebugKnobs debug_knobs();

@@ -387,6 +387,10 @@ int varlen_qk_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int6
  * Products run on the tensor cores with every FP32 operand carried as a sum of
  *   bf16 terms: three (all 24 bits) for f32 I/O, two (16 bits) for
  *   bf16 I/O; accumulation and the state are float32.
+ * A value that is not finite, in any input, reaches what the recurrence carries
+ *   it to and nothing else: earlier tokens and other sequences keep their bits,
+ *   and where it reaches, out and final_states are not finite either (NaN,
+ *   whichever it was).
  * workspace: 16-byte aligned; its status word (vssm_read_status) reports a
  *   malformed cu_seqlens (nothing is written then) and waits that gave up.
  */
@@ -408,7 +412,12 @@ int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t 
  * reported as VSSM_ERR_BAD_SAVED); scale is the forward call's;
  * d_final_states: nullable, the gradient reaching the final states.  dq and dk
  * add the value heads that share a key head, in order; no atomics, bitwise
- * repeatable. */
+ * repeatable.
+ * Where a sequence's inputs, dout or d_final_states hold a value that is not
+ * finite, its gradients are finite at most where the formula's are, and right
+ * there; but NaN can stand where the formula's are finite, through the whole
+ * chunk of 64 tokens and the gradients that depend on it.  Other sequences keep
+ * their bits. */
 size_t varlen_gated_delta_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
                                              int32_t K, int32_t V, vssm_dtype dtype);
 int varlen_gated_delta_bwd(const void* dout, float scale, const int32_t* cu_seqlens, int32_t num_seqs,

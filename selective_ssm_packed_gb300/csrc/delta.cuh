@@ -66,6 +66,14 @@ __device__ __forceinline__ void put_row(uint8_t* image, int term_bytes, int row,
   for (int c = 0; c < kPairs / 4; ++c) put_chunk<NT, kRowBytes>(image, term_bytes, row, chunk0 + c, v + 4 * c);
 }
 
+// x * 0 added up: not 0 once any x is NaN or infinite.
+template <int kPairs>
+__device__ __forceinline__ float2 trace_row(const float2 (&v)[kPairs], float2 z) {
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) z = fma2(v[i], splat2(0.0f), z);
+  return z;
+}
+
 template <int kPairs>
 __device__ __forceinline__ void scale_row(float2 (&v)[kPairs], float f) {
 #pragma unroll

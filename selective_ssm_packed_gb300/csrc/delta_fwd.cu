@@ -36,11 +36,78 @@ struct FwdSmem {
   static constexpr int oKq = 0, oX = oKq + D::kStages * kKq, oWalk = oX + kX;
   static constexpr int kWalk = kS + 2 * kR;  // S, R, E
   static constexpr int oBar = oWalk + kWalks * kWalk;
-  static constexpr int kBytes = oBar + 128 + 1024;
+  static constexpr int oBad = oBar + 128;  // of a walk's columns: the first token that is not finite
+  static constexpr int kBytes = oBad + kWalks * kDeltaTile * 4 + 1024;
 };
 
+// What is not finite stays out of the products, where 0 times it, above Tm's
+// diagonal, would reach earlier tokens: a walk takes 0 in its place, keeps each
+// column's first token that has it, and in the end writes NaN from there on.
+// Both are calls that find their places anew, so that the walk, which has no
+// register to spare, keeps nothing for them.
 template <IO kIO, int KP, int kWalks>
-__global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(DeltaArgs a) {
+__device__ __forceinline__ int* bad_tokens() {  // of this thread's columns
+  extern __shared__ uint8_t smem_raw[];
+  using R = WalkRow<typename IoType<kIO>::type, kWalks>;
+  const int walk = threadIdx.x / R::kThreads, half = threadIdx.x / 128 % R::kHalves;
+  return reinterpret_cast<int*>(align1024(smem_raw) + FwdSmem<kIO, KP, kWalks>::oBad) + walk * kDeltaTile + half * R::kCols;
+}
+
+// This thread's columns of its row of R, in chunk c.
+template <IO kIO, int KP, int kWalks>
+__device__ __noinline__ void clear_row(int c) {
+  extern __shared__ uint8_t smem_raw[];
+  using R = WalkRow<typename IoType<kIO>::type, kWalks>;
+  using L = FwdSmem<kIO, KP, kWalks>;
+  const int walk = threadIdx.x / R::kThreads, half = threadIdx.x / 128 % R::kHalves, row = threadIdx.x % 128;
+  uint8_t* image = align1024(smem_raw) + L::oWalk + walk * L::kWalk + L::kS;
+  int* bad = bad_tokens<kIO, KP, kWalks>();
+#pragma unroll 1
+  for (int i = 0; i < R::kCols; ++i) {
+    const int col = half * R::kCols + i;
+    uint8_t* p = image + image_chunk<64>(row, col / 8) + col % 8 * 2;
+    if ((*reinterpret_cast<const uint16_t*>(p) & 0x7f80) != 0x7f80) continue;
+    for (int k = 0; k < DeltaTerms<kIO>::kMid; ++k) *reinterpret_cast<uint16_t*>(p + k * kRowTile) = 0;
+    atomicMin(bad + i, c * kDeltaChunk + row);
+  }
+}
+
+// NaN for this thread's columns from their bad tokens on: in out, in the saved images of E and S0, in the final state.
+template <IO kIO, int KP, int kWalks>
+__device__ __noinline__ void spoil_columns(const DeltaArgs& a) {
+  using T = typename IoType<kIO>::type;
+  using R = WalkRow<T, kWalks>;
+  using L = FwdSmem<kIO, KP, kWalks>;
+  constexpr int NT = DeltaTerms<kIO>::kMid;
+  const int tiles = delta_tiles(a.V), groups = (tiles + kWalks - 1) / kWalks;
+  const int tile = blockIdx.x % groups * kWalks + threadIdx.x / R::kThreads, half = threadIdx.x / 128 % R::kHalves;
+  const int h = blockIdx.x / groups % a.Hv, row = threadIdx.x % 128, r = row & 63;
+  const int4 sequence = a.order[blockIdx.x / groups / a.Hv];
+  const int n = (sequence.z + kDeltaChunk - 1) / kDeltaChunk;
+  const int* bad = bad_tokens<kIO, KP, kWalks>();
+  const float nan = __int_as_float(0x7fffffff);
+#pragma unroll 1
+  for (int i = 0; i < R::kCols; ++i) {
+    const int from = bad[i], in_tile = half * R::kCols + i, col = tile * kDeltaTile + in_tile;
+    if (from == 0x7fffffff || col >= a.V) continue;
+    const int in_image = in_tile % 8 * 2;
+#pragma unroll 1
+    for (int c = from / kDeltaChunk; c < n; ++c) {
+      const int token = c * kDeltaChunk + r;
+      const int64_t image = ((int64_t)(sequence.w + c) * a.Hv + h) * tiles + tile;
+      if (row >= 64 && token >= from && token < sequence.z)
+        static_cast<T*>(a.out)[(((int64_t)sequence.y + token) * a.Hv + h) * a.V + col] = from_f<T>(nan);
+      if (a.e && row < 64 && token >= from)
+        *reinterpret_cast<uint16_t*>(a.e + image * (NT * kRowTile) + image_chunk<64>(row, in_tile / 8) + in_image) = 0x7fff;
+      if (a.s0 && row < KP * 64 && c * kDeltaChunk > from)
+        *reinterpret_cast<uint16_t*>(a.s0 + image * (NT * L::kSTile) + image_chunk<64>(row, in_tile / 8) + in_image) = 0x7fff;
+    }
+    if (a.final_states && row < a.K) a.final_states[(((int64_t)sequence.x * a.Hv + h) * a.K + row) * a.V + col] = nan;
+  }
+}
+
+template <IO kIO, int KP, int kWalks>
+__global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(const __grid_constant__ DeltaArgs a) {
   using T = typename IoType<kIO>::type;
   using R = WalkRow<T, kWalks>;
   using L = FwdSmem<kIO, KP, kWalks>;
@@ -99,6 +166,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
     for (int i = 0; i < ST && i < n; ++i) load_kq(i);
     if (n > 0) load_x(0);
   }
+  if (threadIdx.x < kWalks * BV) reinterpret_cast<int*>(sm + L::oBad)[threadIdx.x] = 0x7fffffff;
   if (warp == 0) tmem_alloc<kTmemCols>(tmem_at);
   tmem_fence_before_sync();
   __syncthreads();
@@ -134,6 +202,15 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
           S[i] = make_float2(f.x, f.y);
           S[i + 1] = make_float2(f.z, f.w);
         }
+    }
+    const float2 trace = trace_row(S, splat2(0.0f));
+    if (trace.x + trace.y != 0.0f && n > 0) {  // a column that is not finite is 0 for the walk, and NaN in the end
+#pragma unroll
+      for (int i = 0; i < HP; ++i) {
+        if (S[i].x * 0.0f != 0.0f) bad_tokens<kIO, KP, kWalks>()[2 * i] = -1;
+        if (S[i].y * 0.0f != 0.0f) bad_tokens<kIO, KP, kWalks>()[2 * i + 1] = -1;
+        S[i] = make_float2(S[i].x * 0.0f != 0.0f ? 0.0f : S[i].x, S[i].y * 0.0f != 0.0f ? 0.0f : S[i].y);
+      }
     }
     // the next chunk's v, raw, and gates: read a chunk ahead
     typename R::Raw raw;
@@ -176,9 +253,15 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
         }
       }
       const float g_row = gam, db_row = decb, g_end = gam_end;
-      if (row < 64)
+      bool odd = false;  // whether this row of R may hold what is not finite, by v or by the chunk's keys and gates
+      if (row < 64) {
 #pragma unroll
         for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
+        float2 trace = splat2(0.0f);
+#pragma unroll
+        for (int u = 0; u < R::kSteps; ++u) R::each(raw, u, [&](int, float2 w) { trace = fma2(w, splat2(0.0f), trace); });
+        odd = fmaf(g_end, 0.0f, trace.x + trace.y) != 0.0f;
+      }
       if (has_state) {
         wait(done, phase);
         phase ^= 1;
@@ -193,6 +276,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
           R::each(raw, u, [&](int k, float2 w) { d[k] = has_state ? fma2(splat2(-g_row), d[k], w) : w; });
           put_row<NT, 64>(sR, kRowTile, row, 2 * (step0 + u), d);
         }
+        if (odd) clear_row<kIO, KP, kWalks>(c);
       }
       fence_async_smem();
       tmem_fence_before_sync();
@@ -256,7 +340,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
         umma_blocks<BV, 4, NT, true>(tD1, A, B);
         umma_commit(done);
       }
-      const int left = *leave;
+      const int left = kWalks < 4 ? *leave : 0;  // four walks rather vote: a vote needs no register
       wait(done, phase);
       phase ^= 1;
       tmem_fence_after_sync();
@@ -273,8 +357,8 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
       }
       fence_async_smem();
       tmem_fence_before_sync();
-      named_barrier(1 + walk, R::kThreads);
-      if (left) break;
+      if (kWalks < 4) named_barrier(1 + walk, R::kThreads);
+      if (kWalks < 4 ? left != 0 : !vote(1 + walk, R::kThreads, wait.ok)) break;
     }
     if (porter) bulk_wait_all();
     if (a.final_states && row < a.K) {
@@ -283,6 +367,11 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(De
         if (col0 + 2 * i < a.V)
           *reinterpret_cast<float4*>(a.final_states + state_at + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
     }
+    named_barrier(1 + walk, R::kThreads);
+    bool spoilt = false;
+#pragma unroll 1
+    for (int i = 0; i < R::kCols; ++i) spoilt |= bad_tokens<kIO, KP, kWalks>()[i] != 0x7fffffff;
+    if (spoilt) spoil_columns<kIO, KP, kWalks>(a);
   }
   tmem_fence_before_sync();
   if (!__syncthreads_and(wait.ok)) {

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
 // not.  Substitution over all 64 columns took one warp 8300 cycles, most of
 // them waiting for itself.
 // P Tm is a product on the matrix unit, from and into X's own images.
-// Four CTAs fit an SM, so that one's waits hide behind the others.
+// Four CTAs fit an SM (bf16; two or three in f32), so that one's waits hide behind the others.
 constexpr int kNPitch = 68;    // floats a row of N: 16-byte writes of a warp's rows hit all banks
 constexpr int kPrepHeads = 4;  // value heads whose gates are made at once, one a warp
 
@@ -122,6 +122,8 @@ struct PrepSmem {
   static constexpr int oG = oN + kN > kImages ? oN + kN : kImages, oBeta = oG + kPrepHeads * 64 * 8;
   static constexpr int oBar = oBeta + kPrepHeads * 64 * 4;
   static constexpr int kBytes = oBar + 64 + 1024;
+  static constexpr int kCtas = kIO == IO::BF16 ? 4 : KP == 1 ? 3 : 2;  // that fit an SM
+  static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 // Rows i0 .. i0 + kRows - 1, columns c .. c + 3 of -A B or A B, for A and B in
@@ -208,7 +210,7 @@ __device__ __forceinline__ void invert(float* n, float* y, int t, int len) {
 }
 
 template <IO kIO, int KP>
-__global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int split) {
+__global__ void __launch_bounds__(256, PrepSmem<kIO, KP>::kCtas) delta_prep_kernel(DeltaArgs a, int split) {
   using T = typename IoType<kIO>::type;
   using L = PrepSmem<kIO, KP>;
   constexpr int NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid;
@@ -222,6 +224,7 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
   uint64_t* drained = bar + 1;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* stop = reinterpret_cast<int*>(tmem_at + 1);
+  int* bad = const_cast<int*>(stop) + 1;  // the first row of N that is not finite
 
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, quad = warp & 3, half = warp >> 2;
   const int share = blockIdx.x % split, kh = blockIdx.x / split % a.Hk;
@@ -237,6 +240,7 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
     mbar_init(bar, 1);
     mbar_init(drained, 1);
     *stop = 0;
+    *bad = 64;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc<128>(tmem_at);
@@ -256,14 +260,15 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
       g[i] = g[i] < -256.0f ? -256.0f : g[i];  // exp of either is 0; -inf would leave inf - inf
     }
     double incl = (double)g[0] + (double)g[1];
-    const double own = incl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
     const double last = __shfl_sync(0xffffffffu, incl, 31);
-    const double G[2] = {incl - own + (double)g[0], incl};
+    double before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = 0.0;
+    const double G[2] = {before + (double)g[0], incl};
     float* gates = a.gates + (c * a.Hv + hw) * kDeltaGates;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -357,6 +362,7 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
       const float2 gi = sg[r];
       const float f = is_k ? 1.0f : a.scale;
       const int end = is_k ? r : r + 1;  // columns j < end
+      float2 trace = splat2(0.0f);  // not 0 once there is a value that is not finite
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float d[16];
@@ -370,6 +376,8 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
         }
         if (is_k) {
 #pragma unroll
+          for (int i = 0; i < 16; i += 2) trace = fma2(make_float2(d[i], d[i + 1]), splat2(0.0f), trace);
+#pragma unroll
           for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<float4*>(sn + r * kNPitch + half * 32 + u * 16 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
         } else {
@@ -379,12 +387,27 @@ __global__ void __launch_bounds__(256, 4) delta_prep_kernel(DeltaArgs a, int spl
           put_row<NT, 128>(images, 16384, row, half * 4 + 2 * u, p);
         }
       }
+      if (trace.x + trace.y != 0.0f) atomicMin(bad, r);
     } else if (!is_k) {
 #pragma unroll
       for (int k = 0; k < 4 * NT; ++k)
         *reinterpret_cast<uint4*>(images + k / 4 * 16384 + image_chunk<128>(row, 4 + k % 4)) = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
+    if (*bad < 64) {
+      // From this token on nothing of the head is finite.  Its rows leave N, so that the products of the inverse (0
+      // times them) do not carry them to earlier tokens, and NaN takes their place where they would have come out.
+      const float nan = __int_as_float(0x7fffffff);
+      const int first = *bad;
+      for (int i = t; i < 64 * 64; i += 256)
+        if (i / 64 >= first) sn[i / 64 * kNPitch + i % 64] = 0.0f;
+      if (t >= first && t < 64) {
+        *reinterpret_cast<uint16_t*>(images + image_chunk<128>(64 + t, 0)) = 0x7fff;
+        a.gates[ch * kDeltaGates + t] = nan;  // exp(G), the last of which scales the state
+      }
+      __syncthreads();
+      if (t == 0) *bad = 64;
+    }
     invert(sn, reinterpret_cast<float*>(images), (t + 64 * blockIdx.x) & 255, len);  // scratch: where the rows of Tm go next
     {
       const int tr = t >> 2, side = t & 3;

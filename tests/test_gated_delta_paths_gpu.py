@@ -6,7 +6,8 @@ import torch
 
 import selective_ssm_packed_gb300 as vs
 from selective_ssm_packed_gb300 import binding
-from test_gated_delta_gpu import inputs, run
+from oracle import gated_delta as od
+from test_gated_delta_gpu import NET, host, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,78 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(dtype, lens
         assert binding.read_status(ws) == 0
         for n in ("dq", "dk", "dv", "dg", "dbeta", "d_initial_states"):
             assert torch.equal(g[n], ref[n]), n
+
+
+def bad_case(kind, dtype, lens, Hk, Hv, K, V, states):
+    """Inputs with a value that is not finite at one token of a sequence, and the same without it."""
+    x = inputs(lens, Hk, Hv, K, V, dtype, 41, states=states)
+    s = int(np.argmax(lens))
+    start, end = int(sum(lens[:s])), int(sum(lens[:s + 1]))
+    at = start + 64 * ((end - start) // 128) + 21  # inside a chunk, others before and behind it
+    y = dict(x, **{n: x[n].clone() for n in ("q", "k", "v", "g", "beta")}, init=x["init"].clone() if states else None)
+    nan, inf = float("nan"), float("inf")
+    if kind == "v":
+        y["v"][at, 0, 3], y["v"][at, Hv - 1, V - 1], y["v"][at + 2, 0, 5] = inf, nan, -inf
+    elif kind == "k":
+        y["k"][at, 0, K - 1] = nan
+    elif kind == "k first":
+        at = start + 64 * ((end - start) // 128)
+        y["k"][at, 0, 0] = inf
+    elif kind == "q":
+        y["q"][at, 0, 1] = nan
+    elif kind == "g":
+        y["g"][at, Hv - 1] = nan
+    elif kind == "beta":
+        y["beta"][at, 0] = nan
+    elif kind == "last beta":
+        at = start + 64 * ((end - start) // 128) + 63
+        y["beta"][at, 0] = inf
+    else:
+        at = start
+        y["init"][s, 0, 0, 2] = nan
+    return x, y, at, s
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["v", "k", "k first", "q", "g", "beta", "last beta", "init"])
+@pytest.mark.parametrize("lens,Hk,Hv,K,V", [([5, 300, 77], 1, 2, 64, 72), ([40, 130, 10, 60] * 10, 3, 12, 40, 72),
+                                            ([64, 200, 30, 90, 16] * 5, 8, 32, 128, 136)])
+def test_what_is_not_finite_reaches_later_tokens_only(lens, Hk, Hv, K, V, kind, dtype):
+    x, y, at, s = bad_case(kind, dtype, lens, Hk, Hv, K, V, states=True)
+    ref, got = run(x, states=True, bwd=False), run(y, states=True, bwd=False)
+    assert torch.equal(got["out"][:at], ref["out"][:at])
+    # where the recurrence is finite, so are the results, and they are as if the value were not there
+    with np.errstate(invalid="ignore"):
+        out, final = od.delta_fwd(*(host(y[n]) for n in ("q", "k", "v", "g", "beta")), y["cu"].cpu().numpy(), K ** -0.5,
+                                  host(y["init"]))
+    for n, want in (("out", out), ("final", final)):
+        fine = torch.from_numpy(np.isfinite(want)).cuda()
+        assert torch.equal(torch.isfinite(got[n]), fine), n
+        assert torch.equal(got[n][fine], ref[n][fine]), n
+    assert not np.isfinite(out[at:]).all() and np.isfinite(out[:at]).all()
+    # with the saved array the outputs are the same
+    saved = run(y, states=True)
+    assert torch.equal(saved["out"].nan_to_num(7.0), got["out"].nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["v", "k", "q", "g", "beta", "init", "dout", "dfinal"])
+def test_gradients_of_what_is_not_finite_are_nan_or_right(kind, dtype):
+    K, V = 64, 72
+    if kind.startswith("d"):
+        y = inputs([5, 300, 77], 1, 2, K, V, dtype, 41, states=True)
+        y["dout"][200, 1, 5] = float("nan") if kind == "dout" else 1.0
+        y["dfinal"][1, 0, 3, 7] = float("inf") if kind == "dfinal" else 1.0
+    else:
+        y = bad_case(kind, dtype, [5, 300, 77], 1, 2, K, V, states=True)[1]
+    got = run(y, states=True)
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = od.delta_bwd(*(host(y[n]) for n in ("q", "k", "v", "g", "beta", "dout")), y["cu"].cpu().numpy(), K ** -0.5,
+                            host(y["init"]), host(y["dfinal"]))
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "d_initial_states"):
+        g, w = host(got[n]), want["dinit" if n == "d_initial_states" else n]
+        fine = np.isfinite(g)
+        assert np.isfinite(w[fine]).all(), n
+        tol = NET[dtype] + (2.0 ** -8 if got[n].dtype == torch.bfloat16 else 0.0)
+        assert np.linalg.norm(g[fine] - w[fine]) <= tol * np.linalg.norm(w[fine]), n
+        assert fine[np.r_[0:1, 2:3] if n == "d_initial_states" else np.r_[0:5, 305:382]].all(), n  # the other sequences

@@ -584,6 +584,19 @@ def _delta_args(q, k, v, g, beta):
     return [qp, kp, vp, sq, sk, sv, _shaped(g, "g", (T, Hv)), _shaped(beta, "beta", (T, Hv))], (T, Hk, Hv, K, V)
 
 
+def _cuda(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t
+
+
+def _num_seqs(cu_seqlens):
+    S = _cuda(cu_seqlens, "cu_seqlens").numel() - 1
+    if S < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    return S
+
+
 def varlen_gated_delta_fwd(q, k, v, g, beta, cu_seqlens, scale=None, out=None, saved=True, workspace=None, stream=None,
                            initial_states=None, final_states=None):
     """Returns (out, saved), and final_states last when they are asked for.
@@ -593,10 +606,8 @@ def varlen_gated_delta_fwd(q, k, v, g, beta, cu_seqlens, scale=None, out=None, s
     tensor is filled.  initial_states, final_states: (S, Hv, K, V) f32, the
     latter None / False, True or a tensor to fill."""
     args, (T, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
-    S, dt = cu_seqlens.numel() - 1, _dt(q)
+    S, dt = _num_seqs(cu_seqlens), _dt(q)
     sizes = (T, S, Hk, Hv, K, V, dt)
-    if S < 0:
-        raise ValueError("cu_seqlens must have at least one entry")
     out, op = _result(out, "out", v, stream)
     want_final = final_states is not None and final_states is not False
     final_states = _asked(final_states, (S, Hv, K, V), q, stream)
@@ -622,8 +633,9 @@ def varlen_gated_delta_bwd(q, k, v, g, beta, dout, cu_seqlens, saved, scale=None
     the gradient reaching the final states; d_initial_states: None / False,
     True or a tensor to fill.  grads: tensors to fill, by name."""
     _, (T, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
-    S, dt = cu_seqlens.numel() - 1, _dt(q)
+    S, dt = _num_seqs(cu_seqlens), _dt(q)
     sizes = (T, S, Hk, Hv, K, V, dt)
+    _cuda(saved, "saved (the forward call's array)")
     r = dict(grads or {})
     shapes = {"dq": ((T, Hk, K), q.dtype), "dk": ((T, Hk, K), q.dtype), "dv": ((T, Hv, V), q.dtype),
               "dg": ((T, Hv), torch.float32), "dbeta": ((T, Hv), torch.float32)}
@@ -650,6 +662,8 @@ def varlen_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale=
     negative for a padded entry (None: entry b uses slot b).  status: optional
     int32 tensor for indices outside the pool."""
     args, (B, Hk, Hv, K, V) = _delta_args(q, k, v, g, beta)
+    if _cuda(states, "states").dim() != 4:
+        raise ValueError(f"states must be (slots, {Hv}, {K}, {V}), got {tuple(states.shape)}")
     slots = states.shape[0]
     out, op = _result(out, "out", v, stream)
     _check(lib().varlen_gated_delta_step(

@@ -137,3 +137,23 @@ def test_gradients_of_what_is_not_finite_are_nan_or_right(kind, dtype):
         tol = NET[dtype] + (2.0 ** -8 if got[n].dtype == torch.bfloat16 else 0.0)
         assert np.linalg.norm(g[fine] - w[fine]) <= tol * np.linalg.norm(w[fine]), n
         assert fine[np.r_[0:1, 2:3] if n == "d_initial_states" else np.r_[0:5, 305:382]].all(), n  # the other sequences
+
+
+def test_a_missing_tensor_is_refused_by_name():
+    x = inputs([4], 1, 2, 16, 16, "f32", 42)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    out, saved = vs.varlen_gated_delta_fwd(*a, x["cu"], saved=False)
+    assert saved is None
+    with pytest.raises(TypeError, match="saved"):
+        vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], saved)
+    with pytest.raises(TypeError, match="saved"):
+        vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], torch.zeros(4, dtype=torch.uint8))
+    for call in (lambda cu: vs.varlen_gated_delta_fwd(*a, cu), lambda cu: vs.varlen_gated_delta_bwd(*a, x["dout"], cu, out)):
+        with pytest.raises(TypeError, match="cu_seqlens"):
+            call(None)
+        with pytest.raises(ValueError, match="cu_seqlens"):
+            call(x["cu"][:0])
+    with pytest.raises(TypeError, match="states"):
+        vs.varlen_gated_delta_step(*a, None)
+    with pytest.raises(ValueError, match="states"):
+        vs.varlen_gated_delta_step(*a, torch.zeros((), device="cuda"))

@@ -508,6 +508,12 @@ int vssm_debug_set(int knob, int64_t value);
  * VSSM_ERR_ARG (bad kind or NULL pointers) or VSSM_ERR_CUDA. */
 int vssm_kernel_time(int kind, double* total_ms, int64_t* launches);
 
+/* How many walks (tiles of 32 state columns of one sequence and value head)
+ * share a CTA in the gated delta calls on such a pack: 1, 2 or 4, for tests
+ * that mean to reach each; VSSM_ERR_ARG for sizes that the calls refuse. */
+int vssm_gated_delta_walks(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv, int32_t K, int32_t V,
+                           vssm_dtype dtype);
+
 #ifdef __cplusplus
 }
 #endif

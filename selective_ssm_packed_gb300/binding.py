@@ -72,6 +72,7 @@ SIGNATURES = {
     "varlen_gated_delta_saved_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
     "varlen_gated_delta_fwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
     "varlen_gated_delta_bwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "vssm_gated_delta_walks": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
     "varlen_gated_delta_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _i32, _i64, _i32,
                                               _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp]),
     "varlen_gated_delta_bwd": (ctypes.c_int, [_vp, _f32, _vp, _i32, _i64, _i32, _i32, _i32, _i32, ctypes.c_int, _vp,
@@ -571,6 +572,10 @@ def gated_delta_fwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
 
 def gated_delta_bwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
     return lib().varlen_gated_delta_bwd_workspace_size(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype))
+
+
+def gated_delta_walks(T, S, Hk, Hv, K, V, dtype):
+    return lib().vssm_gated_delta_walks(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype))
 
 
 def _delta_args(q, k, v, g, beta):

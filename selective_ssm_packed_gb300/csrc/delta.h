@@ -111,7 +111,8 @@ inline bool delta_split_grads(int64_t max_chunks, int Hk, int Hv) {
 // work, one is the fastest way along a sequence.  What a pack takes is about
 // the longer of all its steps over the SMs and of its longest sequence, which
 // only the GPU knows and which is taken for four times the mean.
-inline int delta_walks(const DeltaArgs& a) {
+inline int delta_walks(const DeltaArgs& a, IO io) {
+  if (io == IO::F32) return 1;  // three terms fill shared memory
   const double chunks = (double)a.T / kDeltaChunk + 1.0, longest = 4.0 * chunks / (a.num_seqs > 0 ? a.num_seqs : 1) + 1.0;
   const int tiles = delta_tiles(a.V);
   const double step[3] = {2.1, 3.1, 4.0};

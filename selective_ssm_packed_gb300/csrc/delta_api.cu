@@ -160,6 +160,13 @@ size_t varlen_gated_delta_bwd_workspace_size(int64_t T, int32_t S, int32_t Hk, i
   return sizes_ok(T, S, Hk, Hv, K, V, dt) ? delta_layout(T, S, Hk, Hv, K, V, dt == VSSM_F32 ? IO::F32 : IO::BF16).bwd_end : 0;
 }
 
+int vssm_gated_delta_walks(int64_t T, int32_t S, int32_t Hk, int32_t Hv, int32_t K, int32_t V, vssm_dtype dt) {
+  if (!sizes_ok(T, S, Hk, Hv, K, V, dt)) return VSSM_ERR_ARG;
+  DeltaArgs a{};
+  a.T = T; a.num_seqs = S; a.Hv = Hv; a.V = V;
+  return delta_walks(a, dt == VSSM_F32 ? IO::F32 : IO::BF16);
+}
+
 int varlen_gated_delta_fwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                            int64_t v_stride, const float* g, const float* beta, float scale,
                            const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,

@@ -406,12 +406,12 @@ cudaError_t launch_delta_fwd(const DeltaArgs& a, IO io, cudaStream_t st) {
   if (a.num_seqs == 0) return cudaSuccess;
   const bool two = delta_panels_k(a.K) == 2;
   if (io == IO::BF16) {
-    const int walks = delta_walks(a);
+    const int walks = delta_walks(a, io);
     if (walks == 4) return two ? run_fwd<IO::BF16, 2, 4>(a, st) : run_fwd<IO::BF16, 1, 4>(a, st);
     if (walks == 2) return two ? run_fwd<IO::BF16, 2, 2>(a, st) : run_fwd<IO::BF16, 1, 2>(a, st);
     return two ? run_fwd<IO::BF16, 2, 1>(a, st) : run_fwd<IO::BF16, 1, 1>(a, st);
   }
-  return two ? run_fwd<IO::F32, 2, 1>(a, st) : run_fwd<IO::F32, 1, 1>(a, st);  // three terms fill shared memory
+  return two ? run_fwd<IO::F32, 2, 1>(a, st) : run_fwd<IO::F32, 1, 1>(a, st);
 }
 
 }  // namespace vssm

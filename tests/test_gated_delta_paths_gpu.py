@@ -7,7 +7,7 @@ import torch
 import selective_ssm_packed_gb300 as vs
 from selective_ssm_packed_gb300 import binding
 from oracle import gated_delta as od
-from test_gated_delta_gpu import NET, host, inputs, run
+from test_gated_delta_gpu import NET, check, host, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +157,63 @@ def test_a_missing_tensor_is_refused_by_name():
         vs.varlen_gated_delta_step(*a, None)
     with pytest.raises(ValueError, match="states"):
         vs.varlen_gated_delta_step(*a, torch.zeros((), device="cuda"))
+
+
+# packs of every walk width, with CTAs that have fewer tiles than walks (V = 72, 136) and sequences of several chunks
+PACKS = {2: [([40, 130, 10, 260] * 8, 4, 12, 64, 72), ([40, 130, 10, 60] * 10, 12, 12, 128, 128)],
+         4: [([64, 200, 30, 90, 16] * 5, 8, 32, 40, 136), ([64, 200, 30, 90, 16] * 5, 8, 32, 128, 128)]}
+
+
+def walks(lens, Hk, Hv, K, V, dtype="bf16"):
+    return binding.gated_delta_walks(sum(lens), len(lens), Hk, Hv, K, V, 0 if dtype == "f32" else 1)
+
+
+@pytest.mark.parametrize("pack", [(w, i) for w in PACKS for i in range(2)], ids=str)
+def test_every_walk_width_against_the_oracle(pack):
+    # the last pack's gradients are more than two items a CTA as well
+    w, i = pack
+    assert walks(*PACKS[w][i]) == w and walks(*PACKS[w][i], "f32") == 1
+    x = inputs(*PACKS[w][i], "bf16", 43, states=True)
+    check(x, run(x, states=True), "bf16")
+
+
+@pytest.mark.parametrize("w", [2, 4])
+def test_every_walk_width_gives_a_sequence_the_same_bits(w):
+    for lens, Hk, Hv, K, V in PACKS[w]:
+        x = inputs(lens, Hk, Hv, K, V, "bf16", 44, states=True)
+        ref = run(x, states=True)
+        for _ in range(5):
+            again = run(x, states=True)
+            assert all(torch.equal(again[n], t) for n, t in ref.items())
+        for s in (0, 1, len(lens) // 2, len(lens) - 1):
+            lo = sum(lens[:s])
+            one = {n: x[n][lo:lo + lens[s]].contiguous() for n in ("q", "k", "v", "g", "beta", "dout")}
+            one.update(init=x["init"][s:s + 1], dfinal=x["dfinal"][s:s + 1],
+                       cu=torch.tensor([0, lens[s]], dtype=torch.int32, device="cuda"))
+            assert walks(lens[s:s + 1], Hk, Hv, K, V) == 1
+            for n, t in run(one, states=True).items():
+                whole = ref[n][s:s + 1] if n in ("final", "d_initial_states") else ref[n][lo:lo + lens[s]]
+                assert torch.equal(t, whole), (n, s)
+
+
+def test_a_training_pack_gives_its_last_sequence_the_same_bits():
+    # 32768 tokens, 32 heads of 128 x 128: two and four walks to a CTA, tens of gradient items to another
+    lens, Hk, Hv, K, V = [4096, 700, 3396, 64, 8000, 16000, 212, 300], 16, 32, 128, 128
+    assert sum(lens) == 32768
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+
+    T = sum(lens)
+    q, k = (torch.nn.functional.normalize(normal(T, Hk, K), dim=-1).bfloat16() for _ in range(2))
+    x = dict(q=q, k=k, v=normal(T, Hv, V).bfloat16(), g=-normal(T, Hv).square(), beta=normal(T, Hv).sigmoid(),
+             dout=normal(T, Hv, V).bfloat16(), init=None, dfinal=None)
+    for cuts, w in ((lens, 2), ([n // 4 for n in lens for _ in range(4)], 4)):
+        assert walks(cuts, Hk, Hv, K, V) == w
+        x["cu"] = torch.tensor(np.cumsum([0] + cuts), dtype=torch.int32, device="cuda")
+        ref = run(x, states=True)
+        one = dict(x, **{n: x[n][-cuts[-1]:] for n in ("q", "k", "v", "g", "beta", "dout")},
+                   cu=torch.tensor([0, cuts[-1]], dtype=torch.int32, device="cuda"))
+        for n, t in run(one, states=True).items():
+            assert torch.equal(t, ref[n][-1:] if n in ("final", "d_initial_states") else ref[n][-cuts[-1]:]), n

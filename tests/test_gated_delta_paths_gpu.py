@@ -217,3 +217,20 @@ def test_a_training_pack_gives_its_last_sequence_the_same_bits():
                    cu=torch.tensor([0, cuts[-1]], dtype=torch.int32, device="cuda"))
         for n, t in run(one, states=True).items():
             assert torch.equal(t, ref[n][-1:] if n in ("final", "d_initial_states") else ref[n][-cuts[-1]:]), n
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,K,V", [([700], 1, 2, 128, 128), PACKS[2][0], PACKS[4][1]])
+def test_bf16_results_lose_no_more_than_their_rounding(lens, Hk, Hv, K, V):
+    # A bf16 result is a value that is NET off, rounded.  Rounding to nearest moves a value by some e that depends on it
+    # as if at random, so the errors' squares add: |result - exact|^2 = |bf16(exact) - exact|^2 + (NET |exact|)^2, the
+    # latter under (1.2e-4 / 1.66e-3)^2 = 0.6% of the former.  An operand of one term (2^-9 a value, 3e-3 over the whole)
+    # would make it four times as much.  10% of the norm is 21% of the squares.
+    x = inputs(lens, Hk, Hv, K, V, "bf16", 45, states=True)
+    res = run(x, states=True)
+    a, cu = [host(x[n]) for n in ("q", "k", "v", "g", "beta")], x["cu"].cpu().numpy()
+    want = od.delta_bwd(*a, host(x["dout"]), cu, K ** -0.5, host(x["init"]), host(x["dfinal"]))
+    want["out"] = od.delta_fwd(*a, cu, K ** -0.5, host(x["init"]))[0]
+    for n in ("out", "dq", "dk", "dv"):
+        w = torch.from_numpy(want[n])
+        rounded = (w.float().bfloat16().double() - w).norm()
+        assert (res[n].double().cpu() - w).norm() <= 1.1 * rounded, n

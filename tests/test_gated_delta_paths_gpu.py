@@ -234,3 +234,37 @@ def test_bf16_results_lose_no_more_than_their_rounding(lens, Hk, Hv, K, V):
         w = torch.from_numpy(want[n])
         rounded = (w.float().bfloat16().double() - w).norm()
         assert (res[n].double().cpu() - w).norm() <= 1.1 * rounded, n
+
+
+def sentinels(x):
+    """Result tensors full of a value of their own, and a check that they still are."""
+    T, Hk, K = x["q"].shape
+    Hv, V = x["v"].shape[1:]
+    S = x["cu"].numel() - 1
+    io = x["q"].dtype
+    shapes = {"out": ((T, Hv, V), io), "final": ((S, Hv, K, V), torch.float32), "dq": ((T, Hk, K), io),
+              "dk": ((T, Hk, K), io), "dv": ((T, Hv, V), io), "dg": ((T, Hv), torch.float32),
+              "dbeta": ((T, Hv), torch.float32), "dinit": ((S, Hv, K, V), torch.float32)}
+    t = {n: torch.full(s, -7.0, dtype=d, device="cuda") for n, (s, d) in shapes.items()}
+    return t, lambda: all(bool((v == -7.0).all()) for v in t.values())
+
+
+@pytest.mark.parametrize("dtype,Hv,V", [("f32", 1, 16), ("f32", 4, 40), ("bf16", 2, 136)])
+@pytest.mark.parametrize("cu", [[0, 10, 5, 20], [1, 20], [0, 30], [0, 19], [0, -5, 20]])
+def test_a_refused_pack_or_saved_array_leaves_every_result_alone(cu, dtype, Hv, V):
+    x = inputs([20], 1, Hv, 16, V, dtype, 46)
+    x["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    saved, ws = buffers(x, dtype)
+    t, untouched = sentinels(x)
+    vs.varlen_gated_delta_fwd(*a, x["cu"], out=t["out"], saved=saved, workspace=ws, final_states=t["final"])
+    assert binding.read_status(ws) == -16 and untouched()
+    vs.varlen_gated_delta_fwd(*a, x["cu"], out=t["out"], saved=False, workspace=ws, final_states=t["final"])
+    assert binding.read_status(ws) == -16 and untouched()
+    grads = {n: t[n] for n in ("dq", "dk", "dv", "dg", "dbeta")}
+    vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], saved, grads=grads, workspace=ws, d_initial_states=t["dinit"])
+    assert binding.read_status(ws) == -16 and untouched()
+    for fill in (0, 255):
+        saved.fill_(fill)
+        vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], saved, grads=grads, workspace=ws, d_initial_states=t["dinit"])
+        assert binding.read_status(ws) == -21 and untouched()

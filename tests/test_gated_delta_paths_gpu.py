@@ -268,3 +268,37 @@ def test_a_refused_pack_or_saved_array_leaves_every_result_alone(cu, dtype, Hv, 
         saved.fill_(fill)
         vs.varlen_gated_delta_bwd(*a, x["dout"], x["cu"], saved, grads=grads, workspace=ws, d_initial_states=t["dinit"])
         assert binding.read_status(ws) == -21 and untouched()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_serving_calls_can_be_captured_in_a_graph(dtype):
+    # a decode loop's token: norm and rotation of q and k, the step against its pool; and the norm's gradients
+    x = inputs([5], 2, 4, 64, 72, dtype, 47)
+    pool = torch.randn(7, 4, 64, 72, generator=torch.Generator().manual_seed(1)).cuda()
+    at = torch.tensor([3, -1, 0, 6, 2], dtype=torch.int32, device="cuda")
+    w = torch.linspace(0.5, 1.5, 64, device="cuda")
+    cos, sin = (f(torch.arange(50, device="cuda")[:, None] * torch.rand(32, device="cuda")) for f in (torch.cos, torch.sin))
+    pos = torch.tensor([7, 0, 49, 3, 3], dtype=torch.int32, device="cuda")
+
+    def token(states):
+        norm = (x["q"], x["k"], w, w, cos, sin, pos)
+        q, k = vs.varlen_qk_norm_rope_fwd(*norm)
+        out = vs.varlen_gated_delta_step(q, k, x["v"], x["g"], x["beta"], states, state_indices=at)
+        g = vs.varlen_qk_norm_rope_bwd(*norm, x["q"], x["k"])
+        return dict(q=q, k=k, out=out, **g)
+
+    states = pool.clone()
+    ref = [token(states), token(states)]
+    mine = pool.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = token(mine)
+    assert torch.equal(mine, pool)
+    for r in ref:
+        for t in got.values():
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[n], t) for n, t in r.items())
+    assert torch.equal(mine, states)

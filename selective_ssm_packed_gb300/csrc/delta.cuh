@@ -11,14 +11,16 @@ namespace vssm {
 template <IO kIO> struct IoType { using type = float; };
 template <> struct IoType<IO::BF16> { using type = __nv_bfloat16; };
 
-// exp(x) with the error of x * log2(e) carried along: the MUFU's 2^-22
-// remains, at any |x| whose exponential is a normal number.
+// exp(x) with the error of x * log2(e) carried along, that of the product's
+// rounding and that of kLog2e's own: the MUFU's 2^-22 remains, at every x whose
+// exponential is a normal number.
 __device__ __forceinline__ float exp_f(float x) {
+  constexpr float kLog2eRest = (float)(1.44269504088896340736 - (double)kLog2e);
   const float t = x * kLog2e;
-  const float r = fmaf(x, kLog2e, -t) + x * 1.925963033500e-8f;  // log2(e) - kLog2e
+  const float r = fmaf(x, kLog2e, -t) + x * kLog2eRest;
   const float p = ex2(t);
-  // t = -inf (or an overflow) leaves r meaningless: the power is then 0 or inf by itself
-  return fabsf(t) < 126.0f ? fmaf(p, r * 0.6931471805599453f, p) : p;
+  // outside, the power is 0 or infinite by itself, and r, where t is, means nothing
+  return t > -126.0f && t < 128.0f ? fmaf(p, r * 0.6931471805599453f, p) : p;
 }
 
 // 8 consecutive io values as floats (16-byte aligned).

@@ -302,3 +302,17 @@ def test_the_serving_calls_can_be_captured_in_a_graph(dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(got[n], t) for n, t in r.items())
     assert torch.equal(mine, states)
+
+
+def test_a_gate_near_the_largest_exponential_keeps_its_digits():
+    # exp(g) up to 2^128: 2^-22 for the exponential, and four roundings of 2^-24 in it and in the product with the state
+    B = 400
+    g = torch.cat([torch.linspace(85.0, 88.7, B // 2), torch.linspace(-87.0, 0.0, B // 2)]).cuda()[:, None]
+    q = torch.zeros(B, 1, 8, device="cuda")
+    q[:, 0, 0] = 1.0
+    states = torch.full((B, 1, 8, 8), 0.5, device="cuda")
+    zero = torch.zeros_like(q)
+    out = vs.varlen_gated_delta_step(q, zero, zero, g, torch.zeros_like(g), states, scale=1.0)
+    want = 0.5 * np.exp(host(g))[:, :, None]
+    for t in (host(out), host(states)[:, :, 0]):
+        assert np.abs(t / want - 1).max() <= 2.0 ** -22 + 4 * 2.0 ** -24

@@ -23,17 +23,7 @@ __device__ __forceinline__ float exp_f(float x) {
   return t > -126.0f && t < 128.0f ? fmaf(p, r * 0.6931471805599453f, p) : p;
 }
 
-// 8 consecutive io values as floats (16-byte aligned).
-__device__ __forceinline__ void ld_io8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void ld_io8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
-  v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
-}
+// 8 consecutive io values from floats (16-byte aligned).
 __device__ __forceinline__ void st_io8(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -161,8 +151,8 @@ __device__ __forceinline__ void pack(const float2 (&v)[8], uint4* q, float) {
                       __float_as_uint(v[2 * i + 1].y));
 }
 
-// A thread's part of a tile's row in the walks: a walk alone on its SM has two
-// threads to a row, 16 columns each, the others one.
+// A thread's part of a tile's row in the walks: where at most two walks share a
+// CTA they have two threads to a row, 16 columns each, otherwise one.
 template <int kWalks>
 constexpr int walk_threads() { return kWalks <= 2 ? 256 * kWalks : 128 * kWalks; }  // of a CTA
 

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
         for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
           if (has_state) {
-            tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
+            tmem_sum<NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
             scale_row(d, db_row);
           } else {
 #pragma unroll
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
+          tmem_sum<NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
           put_row<NT, 64>(sS, kRowTile, row, 2 * (step0 + u), d);  // dS1's images have been read
           R::put(q, u, d);
           scale_row(d, -g_row);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_bwd_kernel(De
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
+          tmem_sum<NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
 #pragma unroll
           for (int k = 0; k < 8; ++k) S[8 * u + k] = d[k] = fma2(splat2(g_end), S[8 * u + k], d[k]);
           if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * (step0 + u), d);

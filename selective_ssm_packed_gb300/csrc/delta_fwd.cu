@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(co
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          if (has_state) tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
+          if (has_state) tmem_sum<NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
           R::each(raw, u, [&](int k, float2 w) { d[k] = has_state ? fma2(splat2(-g_row), d[k], w) : w; });
           put_row<NT, 64>(sR, kRowTile, row, 2 * (step0 + u), d);
         }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(co
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
+          tmem_sum<NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
           if (a.e) put_row<NT, 64>(sE, kRowTile, row, 2 * (step0 + u), d);
           scale_row(d, db_row);
           put_row<NT, 64>(sR, kRowTile, row, 2 * (step0 + u), d);
@@ -310,9 +310,9 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(co
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8], o[8];
-          tmem_sum<8, NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
+          tmem_sum<NT>(tD2 + lane_at + 16 * (step0 + u), BV, d);
           if (has_state) {
-            tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, o);
+            tmem_sum<NT>(tD1 + lane_at + 16 * (step0 + u), BV, o);
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] = fma2(splat2(a.scale * g_row), o[i], d[i]);
           }
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(co
 #pragma unroll
         for (int u = 0; u < R::kSteps; ++u) {
           float2 d[8];
-          tmem_sum<8, NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
+          tmem_sum<NT>(tD1 + lane_at + 16 * (step0 + u), BV, d);
 #pragma unroll
           for (int i = 0; i < 8; ++i) S[8 * u + i] = d[i] = fma2(splat2(g_end), S[8 * u + i], d[i]);
           if (!last) put_row<NT, 64>(sS, L::kSTile, row, 2 * (step0 + u), d);

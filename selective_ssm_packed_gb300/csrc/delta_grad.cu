@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             float m[16], qk[16];
-            tmem_row<16>(tW + lane_at + half * 32 + u * 16, m);
-            tmem_row<16>(tQK + lane_at + half * 32 + u * 16, qk);
+            tmem_row(tW + lane_at + half * 32 + u * 16, m);
+            tmem_row(tQK + lane_at + half * 32 + u * 16, qk);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int j0 = half * 32 + u * 16 + 4 * q;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
         for (int u = 0; u < kSteps; ++u) {
           const int col = half * kMine + 16 * u;
           float2 x[8], k0[4], k1[4];
-          tmem_sum<8, 1>(tA + lane_at + col, 0, x);
+          tmem_sum<1>(tA + lane_at + col, 0, x);
           kq_at<NQ, KP>(kq_image, row, col, k0);
           kq_at<NQ, KP>(kq_image, row, col + 8, k1);
 #pragma unroll
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
             acc[8 * u + i] = mul2(splat2(f), x[i]);
           }
           if (is_k) {
-            tmem_sum<8, 1>(tB + lane_at + col, 0, x);
+            tmem_sum<1>(tB + lane_at + col, 0, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               dk = fma2(x[i], i < 4 ? k0[i & 3] : k1[i & 3], dk);
@@ -361,11 +361,11 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       for (int u = 0; u < kSteps; ++u) {
         const int col = half * kMine + 16 * u;
         float2 x[8];
-        tmem_sum<8, 1>(tC + lane_at + col, 0, x);
+        tmem_sum<1>(tC + lane_at + col, 0, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
         if (is_k) {
-          tmem_sum<8, 1>(tF + lane_at + col, 0, x);
+          tmem_sum<1>(tF + lane_at + col, 0, x);
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[8 * u + i] = add2(acc[8 * u + i], x[i]);
         }

@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(256, PrepSmem<kIO, KP>::kCtas) delta_prep_kern
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float d[16];
-        tmem_row<16>(mine + u * 16, d);
+        tmem_row(mine + u * 16, d);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = half * 32 + u * 16 + i;
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(256, PrepSmem<kIO, KP>::kCtas) delta_prep_kern
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float2 d[8];
-        tmem_sum<8, 1>(mine + 64 + u * 16, 0, d);
+        tmem_sum<1>(mine + 64 + u * 16, 0, d);
         put_row<NT, 128>(images, 16384, row, half * 4 + 2 * u, d);
       }
     }

@@ -182,26 +182,19 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr) {  // warp-collecti
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
 }
 
-// kPairs pairs of consecutive columns of this thread's lane, summed over
-// kBlocks blocks `stride` columns apart, last block first.  All loads are in
-// flight together.
-template <int kPairs, int kBlocks>
-__device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float2 (&v)[kPairs]) {
-  static_assert(kPairs == 8 || kPairs == 16, "16 or 32 columns");
+// 16 consecutive columns of this thread's lane as pairs, summed over kBlocks
+// blocks `stride` columns apart, last block first.  All loads are in flight
+// together.
+template <int kBlocks>
+__device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float2 (&v)[8]) {
   __syncwarp();  // the load is warp-collective; a thread may come from a wait or from issuing products
-  uint32_t r[kBlocks][2 * kPairs];
+  uint32_t r[kBlocks][16];
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b) {
-    if constexpr (kPairs == 16) tmem_ld32(taddr + b * stride, r[b]);
-    else tmem_ld16(taddr + b * stride, r[b]);
-  }
+  for (int b = 0; b < kBlocks; ++b) tmem_ld16(taddr + b * stride, r[b]);
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b) {
-    if constexpr (kPairs == 16) tmem_wait_ld32(r[b]);
-    else tmem_wait_ld16(r[b]);
-  }
+  for (int b = 0; b < kBlocks; ++b) tmem_wait_ld16(r[b]);
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
+  for (int i = 0; i < 8; ++i) {
     v[i] = make_float2(__uint_as_float(r[kBlocks - 1][2 * i]), __uint_as_float(r[kBlocks - 1][2 * i + 1]));
 #pragma unroll
     for (int b = kBlocks - 2; b >= 0; --b)
@@ -209,13 +202,12 @@ __device__ __forceinline__ void tmem_sum(uint32_t taddr, int stride, float2 (&v)
   }
 }
 
-// kCount (16 or 32) consecutive columns of this thread's lane, as floats.
-template <int kCount>
-__device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[kCount]) {
-  float2 p[kCount / 2];
-  tmem_sum<kCount / 2, 1>(taddr, 0, p);
+// 16 consecutive columns of this thread's lane, as floats.
+__device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[16]) {
+  float2 p[8];
+  tmem_sum<1>(taddr, 0, p);
 #pragma unroll
-  for (int i = 0; i < kCount / 2; ++i) {
+  for (int i = 0; i < 8; ++i) {
     v[2 * i] = p[i].x;
     v[2 * i + 1] = p[i].y;
   }

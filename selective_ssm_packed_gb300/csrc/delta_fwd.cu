@@ -37,7 +37,8 @@ struct FwdSmem {
   static constexpr int kWalk = kS + 2 * kR;  // S, R, E
   static constexpr int oBar = oWalk + kWalks * kWalk;
   static constexpr int oBad = oBar + 128;  // of a walk's columns: the first token that is not finite
-  static constexpr int kBytes = oBad + kWalks * kDeltaTile * 4 + 1024;
+  static constexpr int oAnyBad = oBad + kWalks * kDeltaTile * 4;  // whether a walk has met one
+  static constexpr int kBytes = oAnyBad + 16 + 1024;
 };
 
 // What is not finite stays out of the products, where 0 times it, above Tm's
@@ -51,6 +52,13 @@ __device__ __forceinline__ int* bad_tokens() {  // of this thread's columns
   using R = WalkRow<typename IoType<kIO>::type, kWalks>;
   const int walk = threadIdx.x / R::kThreads, half = threadIdx.x / 128 % R::kHalves;
   return reinterpret_cast<int*>(align1024(smem_raw) + FwdSmem<kIO, KP, kWalks>::oBad) + walk * kDeltaTile + half * R::kCols;
+}
+
+template <IO kIO, int KP, int kWalks>
+__device__ __forceinline__ volatile int* any_bad_token() {  // of this thread's walk
+  extern __shared__ uint8_t smem_raw[];
+  using R = WalkRow<typename IoType<kIO>::type, kWalks>;
+  return reinterpret_cast<int*>(align1024(smem_raw) + FwdSmem<kIO, KP, kWalks>::oAnyBad) + threadIdx.x / R::kThreads;
 }
 
 // This thread's columns of its row of R, in chunk c.
@@ -69,6 +77,7 @@ __device__ __noinline__ void clear_row(int c) {
     if ((*reinterpret_cast<const uint16_t*>(p) & 0x7f80) != 0x7f80) continue;
     for (int k = 0; k < DeltaTerms<kIO>::kMid; ++k) *reinterpret_cast<uint16_t*>(p + k * kRowTile) = 0;
     atomicMin(bad + i, c * kDeltaChunk + row);
+    *any_bad_token<kIO, KP, kWalks>() = 1;
   }
 }
 
@@ -167,6 +176,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(co
     if (n > 0) load_x(0);
   }
   if (threadIdx.x < kWalks * BV) reinterpret_cast<int*>(sm + L::oBad)[threadIdx.x] = 0x7fffffff;
+  if (threadIdx.x < kWalks) reinterpret_cast<int*>(sm + L::oAnyBad)[threadIdx.x] = 0;
   if (warp == 0) tmem_alloc<kTmemCols>(tmem_at);
   tmem_fence_before_sync();
   __syncthreads();
@@ -205,6 +215,7 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(co
     }
     const float2 trace = trace_row(S, splat2(0.0f));
     if (trace.x + trace.y != 0.0f && n > 0) {  // a column that is not finite is 0 for the walk, and NaN in the end
+      *any_bad_token<kIO, KP, kWalks>() = 1;
 #pragma unroll
       for (int i = 0; i < HP; ++i) {
         if (S[i].x * 0.0f != 0.0f) bad_tokens<kIO, KP, kWalks>()[2 * i] = -1;
@@ -367,11 +378,10 @@ __global__ void __launch_bounds__(walk_threads<kWalks>(), 1) delta_fwd_kernel(co
         if (col0 + 2 * i < a.V)
           *reinterpret_cast<float4*>(a.final_states + state_at + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
     }
-    named_barrier(1 + walk, R::kThreads);
-    bool spoilt = false;
-#pragma unroll 1
-    for (int i = 0; i < R::kCols; ++i) spoilt |= bad_tokens<kIO, KP, kWalks>()[i] != 0x7fffffff;
-    if (spoilt) spoil_columns<kIO, KP, kWalks>(a);
+    if (*any_bad_token<kIO, KP, kWalks>()) {  // said before a barrier that all of the walk have passed
+      named_barrier(1 + walk, R::kThreads);
+      spoil_columns<kIO, KP, kWalks>(a);
+    }
   }
   tmem_fence_before_sync();
   if (!__syncthreads_and(wait.ok)) {

@@ -386,7 +386,10 @@ int varlen_qk_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int6
  *   the chunk's solved triangular systems.
  * Products run on the tensor cores with every FP32 operand carried as a sum of
  *   bf16 terms: three (all 24 bits) for f32 I/O, two (16 bits) for
- *   bf16 I/O; accumulation and the state are float32.
+ *   bf16 I/O; accumulation and the state are float32.  Results in bf16 lose
+ *   nothing by that, those in f32 are about 5e-6 off (f32 I/O: 1e-6).  Data in
+ *   bf16 whose final states, dg and dbeta are wanted with all bits are passed
+ *   as f32, which holds them exactly.
  * A value that is not finite, in any input, reaches what the recurrence carries
  *   it to and nothing else: earlier tokens and other sequences keep their bits,
  *   and where it reaches, out and final_states are not finite either (NaN,
@@ -456,7 +459,9 @@ const char* vssm_last_error(void);      /* thread-local; "" if none */
  * access, ORing a bit into the status word instead (vssm_read_status then
  * returns VSSM_ERR_DEVICE_CHECK; nothing traps), and calls given position
  * indices check them against cu_seqlens (VSSM_ERR_BAD_CU_SEQLENS).  0 in the
- * ordinary build, where neither check runs. */
+ * ordinary build, where neither check runs.  The gated delta and q/k norm
+ * calls check what their inputs index (cu_seqlens, positions, state_indices,
+ * a saved array's plan) in every build. */
 int vssm_checks_build(void);
 
 /* Test knobs (process-wide).  VSSM_DBG_DROP_FLAG: the scan work item with this
@@ -483,7 +488,8 @@ int vssm_checks_build(void);
 #define VSSM_DBG_DELAY_ITEM 3
 #define VSSM_DBG_DELAY_NS 4
 #define VSSM_DBG_FORCE_COPY_TIMEOUT 5
-/* VSSM_DBG_CHECK_FINITE: 1 makes every conv / scan call check its outputs
+/* VSSM_DBG_CHECK_FINITE: 1 makes every conv, scan and packed gated delta call
+ * and the q/k norm's backward check its outputs
  * after its kernels and OR a bit into its status word when any output holds a
  * NaN or an infinity (vssm_read_status then returns VSSM_ERR_NONFINITE); 0
  * (the default) skips the check.  It makes a run whose values have gone bad

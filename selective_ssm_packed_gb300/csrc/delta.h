@@ -106,8 +106,9 @@ inline bool delta_split_grads(int64_t max_chunks, int Hk, int Hv) {
 }
 
 // Tiles a CTA of the bf16 walks takes, which share what they read.  A step of
-// one, two or four walks on an SM takes 2.1, 3.1 or 4.0 us (one sequence of
-// 32768 tokens, 32 heads of 128 x 128): four are the fastest way through much
+// one, two or four walks on an SM took 2.1, 3.1 or 4.0 us (one sequence of
+// 32768 tokens, 32 heads of 128 x 128; the first is 2.2 with the checks of its
+// waits and values): four are the fastest way through much
 // work, one is the fastest way along a sequence.  What a pack takes is about
 // the longer of all its steps over the SMs and of its longest sequence, which
 // only the GPU knows and which is taken for four times the mean.

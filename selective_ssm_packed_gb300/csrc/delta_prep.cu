@@ -108,7 +108,10 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(DeltaArgs a) {
 // not.  Substitution over all 64 columns took one warp 8300 cycles, most of
 // them waiting for itself.
 // P Tm is a product on the matrix unit, from and into X's own images.
-// Four CTAs fit an SM (bf16; two or three in f32), so that one's waits hide behind the others.
+// Four CTAs fit an SM (bf16; two or three in f32), so that one's waits hide
+// behind the others; four leave 64 registers, of which 12 bytes spill (f32, K <=
+// 64: 28; beyond, none).  336 us at 32768 tokens of 16 + 32 heads in bf16, 55 us
+// at 4096 of 12 in f32 (K = 128).
 constexpr int kNPitch = 68;    // floats a row of N: 16-byte writes of a warp's rows hit all banks
 constexpr int kPrepHeads = 4;  // value heads whose gates are made at once, one a warp
 

@@ -16,9 +16,12 @@ namespace {
 // partners' values once more, from L1.  q and k are separate CTAs, so that a
 // lane needs one set of weights.  Every value is read from and written to
 // DRAM once, which bounds the pass: kUnroll rows of a lane are in flight, and
-// as many CTAs as their registers allow (32768 x 48 heads of 128 in bf16: 138
-// us, 5.9 TB/s; twice the rows and three CTAs an SM, whose registers spill,
-// 152 us; asking for the rows ahead of the cosines 146 to 170 us).
+// four CTAs an SM (32768 x 48 heads of 128 in bf16: 139 us, 5.8 TB/s, although
+// 64 registers a thread spill 56 bytes, 20 in f32; twice the rows and three CTAs
+// an SM 152 us; asking for the rows ahead of the cosines 146 to 170 us).  Pairs
+// that are read again cost more than twice as much: 367 us with 24 or 40 of the
+// 128 values rotated, and 815 us with the backward, which spills 200 bytes there,
+// against 398.
 constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
 
 // A chunk as it is read, unpacked when it is its row's turn.

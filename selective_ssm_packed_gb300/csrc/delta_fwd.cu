@@ -22,14 +22,14 @@ namespace {
 // walks leave a thread 128 registers, so they read back 16 columns at a time:
 // a register spilled within a step is a trip to L2, shared memory having taken
 // nearly all of L1 (a build that spilled 28 bytes took 560 us at 32768 tokens,
-// this one, with 4, takes 500; with 28 for K <= 64 444).  CTAs that stay, with a fixed deal of the items and the next one's
-// operands already on their way, took 726 us at 32768 tokens where these take
-// 446: sequences are unequal, and the hardware hands the next CTA to the SM
-// that is free.  Two threads to a row shorten the read-backs of a chain that
-// has little else to wait for: the walk of a 3001-token f32 pack took 122 us
-// with one and 108 with two (the walk back 168 and 134), of one 32768-token bf16
-// sequence 1150 and 1096.  With what the waits and values that are not finite
-// have added since, 117, 137 and 1142.
+// this one, with 4, takes 500; with 28 for K <= 64 444).  CTAs that stay, with a
+// fixed deal of the items and the next one's operands already on their way, took
+// 726 us at 32768 tokens where these take 446: sequences are unequal, and the
+// hardware hands the next CTA to the SM that is free.  Two threads to a row
+// shorten the read-backs of a chain that has little else to wait for: the walk
+// of a 3001-token f32 pack took 122 us with one and 108 with two (the walk back
+// 168 and 134), of one 32768-token bf16 sequence 1150 and 1096.  The checks of
+// waits and of values that are not finite cost these walks 2%, 0 and 3%.
 template <IO kIO, int KP, int kWalks>
 struct FwdSmem {
   using D = DeltaTerms<kIO>;

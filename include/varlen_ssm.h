@@ -445,6 +445,96 @@ int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t
                             int32_t Hv, int32_t K, int32_t V, vssm_dtype dtype, void* out, int32_t* status,
                             void* stream);
 
+/* ------------------------------------------------------------ linear attention with a decay for each head
+ * The recurrence whose state is a K x V matrix per head, without the delta
+ * rule's correction, on the same packed batches; the state resets at every
+ * sequence start.  Per value head, with a_t = exp(g_t):
+ *   S_t = a_t S_{t-1} + k_t v_t^T,   out_t = scale * S_t^T q_t
+ * q, k (T, Hk, K), v (T, Hv, V) io, out, initial_states, final_states: as the
+ *   gated delta rule's (value head j uses the query and key head
+ *   j / (Hv / Hk)); K and V multiples of 8, 8 to 128 each.
+ * g: f32 log decays, usually <= 0 (values below -256 are taken as -256: both
+ *   decay to zero).  g_per_token != 0: (T, Hv); 0: (Hv), one decay a head for
+ *   every token.
+ * Precision as the gated delta rule's: FP32 operands of the tensor cores'
+ *   products are sums of bf16 terms, three for f32 I/O, two for bf16 I/O;
+ *   accumulation and the state are float32.
+ * A value that is not finite reaches what the recurrence carries it to and
+ *   nothing else, as there.
+ * Long sequences are cut into segments that are walked at once; their length
+ *   goes by the sizes alone (vssm_linear_attn_segment), so equal calls have
+ *   equal bits.
+ * workspace: 16-byte aligned; its status word (vssm_read_status) reports a
+ *   malformed cu_seqlens (nothing is written then) and waits that gave up.
+ */
+size_t varlen_linear_attn_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
+                                             int32_t K, int32_t V, vssm_dtype dtype);
+int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const float* g, int32_t g_per_token, float scale,
+                           const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
+                           int32_t Hv, int32_t K, int32_t V, vssm_dtype dtype, void* out,
+                           const float* initial_states, float* final_states, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Backward: dq, dk (T, Hk, K), dv (T, Hv, V) io, contiguous; dg, nullable, f32
+ * (T, Hv) or, for one decay a head, (Hv); d_initial_states nullable.  The
+ * inputs, initial_states and scale are the forward call's, from which the
+ * states are made again; nothing of the forward call has to be kept.
+ * d_final_states: nullable, the gradient reaching the final states.  dq and dk
+ * add the value heads that share a head, in order; no atomics, bitwise
+ * repeatable.  A value that is not finite in q, k, v, dout or the states
+ * reaches the gradients that the formula carries it to; dg, a sum over a
+ * segment, is not finite before it in the sequence's segments, and a g that is
+ * not finite leaves NaN in its whole chunk.  Other sequences keep their bits. */
+size_t varlen_linear_attn_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
+                                             int32_t K, int32_t V, vssm_dtype dtype);
+int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const float* g, int32_t g_per_token, const void* dout, float scale,
+                           const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
+                           int32_t Hv, int32_t K, int32_t V, vssm_dtype dtype, const float* initial_states,
+                           const float* d_final_states, float* d_initial_states, void* dq, void* dk, void* dv,
+                           float* dg, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of `batch` sequences, against a pool of states updated in
+ * place; arguments as varlen_gated_delta_step's, g (batch, Hv) or, with
+ * g_per_token 0, (Hv). */
+int varlen_linear_attn_step(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const float* g, int32_t g_per_token, float scale, float* states,
+                            const int32_t* state_indices, int64_t num_slots, int64_t batch, int32_t Hk,
+                            int32_t Hv, int32_t K, int32_t V, vssm_dtype dtype, void* out, int32_t* status,
+                            void* stream);
+
+/* ------------------------------------------------------------ layer norm
+ * Over a token's D channels, or each of `groups` groups of D / groups
+ * neighbouring ones (the heads behind an attention):
+ *   h = x + residual (residual nullable),
+ *   out = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias,
+ * var the mean of the squared differences, weight and bias (D) f32, nullable
+ * (ones, zeros).
+ * x (T, D) io, rows x_stride elements apart (at least D, a multiple of 16
+ *   bytes); residual (T, D) and sum (T, D), nullable, float32 whatever the
+ *   dtype: the residual stream, which sum receives with x added, unrounded.  sum
+ *   may be residual.
+ * out (T, D) io, contiguous; all pointers 16-byte aligned.
+ * D / groups a multiple of 8, 8 to 8192; groups at most 65535.
+ * Statistics are float32, of the differences from the mean.
+ */
+int varlen_layer_norm_fwd(const void* x, int64_t x_stride, const float* residual, const float* weight,
+                          const float* bias, int64_t total_tokens, int32_t D, int32_t groups, float eps,
+                          vssm_dtype dtype, void* out, float* sum, void* stream);
+
+/* Backward.  x: what was normalised, io, or f32 with x_f32 != 0 (the forward
+ * call's sum); the statistics are made again from it.  dout (T, D) io; dsum
+ * (T, D) f32, nullable: the gradient that reaches the sum from elsewhere, which
+ * is added.  dx (T, D) io and dresidual (T, D) f32, nullable, receive the same
+ * gradient.  dweight, dbias (D) f32, nullable, are summed over the tokens in a
+ * fixed order (bitwise repeatable).  The status word is the workspace's. */
+size_t varlen_layer_norm_bwd_workspace_size(int64_t total_tokens, int32_t D, int32_t groups);
+int varlen_layer_norm_bwd(const void* x, int64_t x_stride, int32_t x_f32, const float* weight, const void* dout,
+                          const float* dsum, int64_t total_tokens, int32_t D, int32_t groups, float eps,
+                          vssm_dtype dtype, void* dx, float* dresidual, float* dweight, float* dbias,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------ status, errors, knobs
  * vssm_read_status: synchronises `stream`, reads the status word the last call
  * using `workspace` left there, and stores VSSM_OK or a VSSM_ERR_* code in
@@ -459,8 +549,8 @@ const char* vssm_last_error(void);      /* thread-local; "" if none */
  * access, ORing a bit into the status word instead (vssm_read_status then
  * returns VSSM_ERR_DEVICE_CHECK; nothing traps), and calls given position
  * indices check them against cu_seqlens (VSSM_ERR_BAD_CU_SEQLENS).  0 in the
- * ordinary build, where neither check runs.  The gated delta and q/k norm
- * calls check what their inputs index (cu_seqlens, positions, state_indices,
+ * ordinary build, where neither check runs.  The gated delta, linear attention
+ * and q/k norm calls check what their inputs index (cu_seqlens, positions, state_indices,
  * a saved array's plan) in every build. */
 int vssm_checks_build(void);
 
@@ -478,9 +568,9 @@ int vssm_checks_build(void);
  * conv calls, the CTA with this index reports its tile-copy wait as timed out
  * once the copy has landed (-1 = off), so a test sees VSSM_ERR_LOOKBACK_TIMEOUT
  * in the call's status word without any copy failing; the conv calls' copy
- * waits also take their limit from VSSM_DBG_WAIT_NS.  Both hold for the gated
- * delta rule's packed calls too: the CTA with this index of each of their
- * kernels reports its first wait as run out, and the whole CTA then leaves,
+ * waits also take their limit from VSSM_DBG_WAIT_NS.  Both hold for the packed
+ * calls of the gated delta rule and of linear attention too: the CTA with this
+ * index of each of their kernels reports its first wait as run out, and the whole CTA then leaves,
  * once what it asked for has come in.
  * Returns VSSM_OK or VSSM_ERR_ARG. */
 #define VSSM_DBG_DROP_FLAG 1
@@ -488,8 +578,8 @@ int vssm_checks_build(void);
 #define VSSM_DBG_DELAY_ITEM 3
 #define VSSM_DBG_DELAY_NS 4
 #define VSSM_DBG_FORCE_COPY_TIMEOUT 5
-/* VSSM_DBG_CHECK_FINITE: 1 makes every conv, scan and packed gated delta call
- * and the q/k norm's backward check its outputs
+/* VSSM_DBG_CHECK_FINITE: 1 makes every conv, scan, packed gated delta and
+ * packed linear attention call and the norms' backward check its outputs
  * after its kernels and OR a bit into its status word when any output holds a
  * NaN or an infinity (vssm_read_status then returns VSSM_ERR_NONFINITE); 0
  * (the default) skips the check.  It makes a run whose values have gone bad
@@ -513,6 +603,12 @@ int vssm_debug_set(int knob, int64_t value);
  * the recorded events to complete, then forgets them.  Returns VSSM_OK,
  * VSSM_ERR_ARG (bad kind or NULL pointers) or VSSM_ERR_CUDA. */
 int vssm_kernel_time(int kind, double* total_ms, int64_t* launches);
+
+/* Tokens of a segment in the linear attention calls on such a pack (a longer
+ * sequence is cut), for tests that mean to cross its end; backward != 0: in
+ * the backward call.  VSSM_ERR_ARG for sizes that the calls refuse. */
+int vssm_linear_attn_segment(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv, int32_t K, int32_t V,
+                             vssm_dtype dtype, int32_t backward);
 
 /* How many walks (tiles of 32 state columns of one sequence and value head)
  * share a CTA in the gated delta calls on such a pack: 1, 2 or 4, for tests

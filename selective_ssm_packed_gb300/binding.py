@@ -79,6 +79,21 @@ SIGNATURES = {
                                               _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "varlen_gated_delta_step": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _vp, _i64, _i64,
                                                _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp]),
+    "varlen_linear_attn_fwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "varlen_linear_attn_bwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "vssm_linear_attn_segment": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int, _i32]),
+    "varlen_linear_attn_fwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _f32, _vp, _i32, _i64, _i32,
+                                              _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "varlen_linear_attn_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _f32, _vp, _i32, _i64,
+                                              _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _vp, _sz, _vp]),
+    "varlen_linear_attn_step": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _f32, _vp, _vp, _i64, _i64,
+                                               _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp]),
+    "varlen_layer_norm_fwd": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _f32, ctypes.c_int, _vp, _vp,
+                                             _vp]),
+    "varlen_layer_norm_bwd_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "varlen_layer_norm_bwd": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp, _i64, _i32, _i32, _f32, ctypes.c_int, _vp,
+                                             _vp, _vp, _vp, _vp, _sz, _vp]),
     "varlen_pack_sequences": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _vp,
                                              ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double)]),
     "vssm_read_status": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(ctypes.c_int)]),
@@ -677,6 +692,187 @@ def varlen_gated_delta_step(q, k, v, g, beta, states, state_indices=None, scale=
         _ptr(status, "status", torch.int32), _stream_of(q, stream)),
         "varlen_gated_delta_step")
     return out
+
+
+# ------------------------------------------------------------------ linear attention with a decay for each head
+class _Here:
+    """A context that leaves the current device alone."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *_):
+        return False
+
+
+_HERE = _Here()
+
+
+def _device_of(t):
+    """A context in which t's device is the current one, which the library
+    launches on."""
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def linear_attn_fwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
+    return lib().varlen_linear_attn_fwd_workspace_size(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype))
+
+
+def linear_attn_bwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
+    return lib().varlen_linear_attn_bwd_workspace_size(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype))
+
+
+def linear_attn_segment(T, S, Hk, Hv, K, V, dtype, backward=False):
+    return lib().vssm_linear_attn_segment(int(T), int(S), int(Hk), int(Hv), int(K), int(V), int(dtype), int(backward))
+
+
+def _linear_args(q, k, v, g):
+    qp, sq = _heads(q, "q")
+    T, Hk, K = q.shape
+    kp, sk = _heads(k, "k", q.dtype, Hk, K)
+    vp, sv = _heads(v, "v", q.dtype)
+    _, Hv, V = v.shape
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k and v have {T}, {k.shape[0]} and {v.shape[0]} tokens")
+    per_token = _cuda(g, "g").dim() != 1
+    return [qp, kp, vp, sq, sk, sv, _shaped(g, "g", (T, Hv) if per_token else (Hv,)), int(per_token)], (T, Hk, Hv, K, V)
+
+
+def varlen_linear_attn_fwd(q, k, v, g, cu_seqlens, scale=None, out=None, workspace=None, stream=None,
+                           initial_states=None, final_states=None):
+    """Returns out, or (out, final_states) when those are asked for.  q, k
+    (T, Hk, K), v (T, Hv, V) may be slices of wider rows; g f32 log decays,
+    (T, Hv) or one for each head, (Hv); scale: K ** -0.5 when None.
+    initial_states, final_states: (S, Hv, K, V) f32, the latter None / False,
+    True or a tensor to fill."""
+    args, (T, Hk, Hv, K, V) = _linear_args(q, k, v, g)
+    S, dt = _num_seqs(cu_seqlens), _dt(q)
+    with _device_of(q):
+        out, op = _result(out, "out", v, stream)
+        want_final = final_states is not None and final_states is not False
+        final_states = _asked(final_states, (S, Hv, K, V), q, stream)
+        ws = _room(workspace, linear_attn_fwd_workspace_size(T, S, Hk, Hv, K, V, dt), q, stream)
+        _check(lib().varlen_linear_attn_fwd(
+            *args, float(K ** -0.5 if scale is None else scale), _ptr(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hk,
+            Hv, K, V, dt, op, _shaped(initial_states, "initial_states", (S, Hv, K, V)),
+            _shaped(final_states, "final_states", (S, Hv, K, V)), _ptr(ws, "workspace"),
+            ws.numel() * ws.element_size(), _stream_of(q, stream)), "varlen_linear_attn_fwd")
+    return (out, final_states) if want_final else out
+
+
+def varlen_linear_attn_bwd(q, k, v, g, dout, cu_seqlens, scale=None, grads=None, workspace=None, stream=None,
+                           initial_states=None, d_final_states=None, d_initial_states=None, dg=True):
+    """Returns dict dq, dk, dv, dg, d_initial_states.  The inputs,
+    initial_states and scale are the forward call's.  dg: False for decays
+    that are not trained (None is returned for it then).  d_final_states:
+    (S, Hv, K, V) f32, the gradient reaching the final states;
+    d_initial_states: None / False, True or a tensor to fill.  grads: tensors
+    to fill, by name."""
+    args, (T, Hk, Hv, K, V) = _linear_args(q, k, v, g)
+    S, dt = _num_seqs(cu_seqlens), _dt(q)
+    r = dict(grads or {})
+    shapes = {"dq": ((T, Hk, K), q.dtype), "dk": ((T, Hk, K), q.dtype), "dv": ((T, Hv, V), q.dtype),
+              "dg": (tuple(g.shape), torch.float32)}
+    with _device_of(q):
+        for n, (shape, d) in shapes.items():
+            if n not in r:
+                r[n] = _new(shape, d, q, stream) if n != "dg" or dg else None
+        r["d_initial_states"] = _asked(d_initial_states, (S, Hv, K, V), q, stream)
+        ws = _room(workspace, linear_attn_bwd_workspace_size(T, S, Hk, Hv, K, V, dt), q, stream)
+        _check(lib().varlen_linear_attn_bwd(
+            *args, _shaped(dout, "dout", (T, Hv, V), q.dtype), float(K ** -0.5 if scale is None else scale),
+            _ptr(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hk, Hv, K, V, dt,
+            _shaped(initial_states, "initial_states", (S, Hv, K, V)),
+            _shaped(d_final_states, "d_final_states", (S, Hv, K, V)),
+            _shaped(r["d_initial_states"], "d_initial_states", (S, Hv, K, V)),
+            *(_shaped(r[n], n, shape, d) for n, (shape, d) in shapes.items()),
+            _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream_of(q, stream)), "varlen_linear_attn_bwd")
+    return r
+
+
+def varlen_linear_attn_step(q, k, v, g, states, state_indices=None, scale=None, out=None, status=None, stream=None):
+    """Returns out (B, Hv, V): one token of each of B sequences, q, k (B, Hk, K),
+    v (B, Hv, V), g (B, Hv) or (Hv,), against states (slots, Hv, K, V) f32,
+    which are updated in place.  state_indices: int32 (B) slots, all
+    different, negative for a padded entry (None: entry b uses slot b).
+    status: optional int32 tensor for indices outside the pool."""
+    args, (B, Hk, Hv, K, V) = _linear_args(q, k, v, g)
+    if _cuda(states, "states").dim() != 4:
+        raise ValueError(f"states must be (slots, {Hv}, {K}, {V}), got {tuple(states.shape)}")
+    slots = states.shape[0]
+    with _device_of(q):
+        out, op = _result(out, "out", v, stream)
+        _check(lib().varlen_linear_attn_step(
+            *args, float(K ** -0.5 if scale is None else scale), _shaped(states, "states", (slots, Hv, K, V)),
+            _shaped(state_indices, "state_indices", (B,), torch.int32), slots, B, Hk, Hv, K, V, _dt(q), op,
+            _ptr(status, "status", torch.int32), _stream_of(q, stream)), "varlen_linear_attn_step")
+    return out
+
+
+# ------------------------------------------------------------------ layer norm
+def _rows(t, name):
+    """(pointer, row stride) of a (T, D) CUDA tensor whose rows may be any
+    distance apart."""
+    if _cuda(t, name).dim() != 2:
+        raise ValueError(f"{name} must be (tokens, channels), got {tuple(t.shape)}")
+    T, D = t.shape
+    if D > 1 and t.stride(1) != 1 and t.numel():
+        raise ValueError(f"{name}: the channels of a token must be contiguous")
+    return t.data_ptr() or None, (t.stride(0) if T > 1 else D)
+
+
+def varlen_layer_norm_fwd(x, weight=None, bias=None, groups=1, eps=1e-5, residual=None, out=None, sum_out=None,
+                          stream=None):
+    """Returns out, or (out, sum) with a residual: the rows of x (T, D), or of
+    sum = residual + x, with mean 0 and variance 1, scaled by weight and moved
+    by bias (D) f32, over all D channels or each of `groups` groups of them.
+    x may be slices of wider rows; residual and sum (T, D) are float32
+    whatever x is.  out, sum_out: tensors to fill (sum_out may be residual)."""
+    xp, sx = _rows(x, "x")
+    T, D = x.shape
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    with _device_of(x):
+        out, op = _result(out, "out", x, stream)
+        rp = _shaped(residual, "residual", (T, D))
+        if residual is not None and sum_out is None:
+            sum_out = _new((T, D), torch.float32, x, stream)
+        _check(lib().varlen_layer_norm_fwd(
+            xp, sx, rp, _shaped(weight, "weight", (D,)), _shaped(bias, "bias", (D,)), T, D, int(groups), float(eps),
+            _dt(x), op, _shaped(sum_out, "sum_out", (T, D)), _stream_of(x, stream)), "varlen_layer_norm_fwd")
+    return out if residual is None else (out, sum_out)
+
+
+def varlen_layer_norm_bwd(x, weight, bias, dout, groups=1, eps=1e-5, residual=False, dsum=None, grads=None,
+                          workspace=None, stream=None):
+    """Returns dict dx and, where the forward call had them, dweight, dbias and
+    dresidual (else None).  x: what was normalised: the forward call's x, or,
+    with residual=True, its sum, float32; dout (T, D) has dx's type.  dsum:
+    (T, D) f32, the gradient that reaches the sum from elsewhere, or None.
+    grads: tensors to fill, by name."""
+    xp, sx = _rows(x, "x")
+    T, D = x.shape
+    dt = _dt(_cuda(dout, "dout"))
+    want = torch.float32 if residual else dout.dtype
+    if x.dtype is not want:
+        raise TypeError(f"x must be {want}, got {x.dtype}")
+    if dsum is not None and not residual:
+        raise ValueError("dsum needs residual=True")
+    g = dict(grads or {})
+    make = {"dx": ((T, D), dout.dtype), "dresidual": ((T, D), torch.float32), "dweight": ((D,), torch.float32),
+            "dbias": ((D,), torch.float32)}
+    with _device_of(x):
+        for n, wanted in (("dx", True), ("dresidual", residual), ("dweight", weight is not None),
+                          ("dbias", bias is not None)):
+            if n not in g:
+                g[n] = _new(*make[n], x, stream) if wanted else None
+        ws = _room(workspace, lib().varlen_layer_norm_bwd_workspace_size(T, D, int(groups)), x, stream)
+        _check(lib().varlen_layer_norm_bwd(
+            xp, sx, int(bool(residual)), _shaped(weight, "weight", (D,)), _shaped(dout, "dout", (T, D), dout.dtype),
+            _shaped(dsum, "dsum", (T, D)), T, D, int(groups), float(eps), dt,
+            *(_shaped(g[n], n, *make[n]) for n in make), _ptr(ws, "workspace"), ws.numel() * ws.element_size(),
+            _stream_of(x, stream)), "varlen_layer_norm_bwd")
+    return g
 
 
 # ------------------------------------------------------------------ packing (host)

@@ -84,6 +84,29 @@ __device__ __forceinline__ void unpack(uint4 q, float2 (&v)[2]) {
   v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
 }
 
+// Eight io values as they are read, unpacked when it is their row's turn (the norms).
+template <typename T>
+struct Chunk8 {
+  static constexpr int kWords = (int)sizeof(T) / 2;
+  uint4 q[kWords];
+  __device__ __forceinline__ void load(const T* p, bool there) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) q[i] = there ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      float2 w[8 / kWords / 2];
+      unpack(q[i], w);
+#pragma unroll
+      for (int j = 0; j < 8 / kWords / 2; ++j) {
+        v[i * 4 + 2 * j] = w[j].x;
+        v[i * 4 + 2 * j + 1] = w[j].y;
+      }
+    }
+  }
+};
+
 // N lanes (four or two), N chunks each: lane j's chunk i becomes lane i's chunk
 // j.  A warp reads or writes 32 rows of 16 N bytes with it N lanes to a row,
 // 32 / N rows an instruction; a lane to a row would touch 32 lines with every
@@ -197,7 +220,8 @@ struct WalkRow {
 // it then says in the status word and to the CTA's other threads, who give up
 // theirs (*stop, a word in shared memory, 0 at first).  The timer is read once
 // in 64 tries.  forced: a test's wait, which counts as run out once it is over.
-__device__ __forceinline__ bool wait_or_stop(const DeltaArgs& a, volatile int* stop, uint64_t* bar, uint32_t parity,
+template <typename Args>
+__device__ __forceinline__ bool wait_or_stop(const Args& a, volatile int* stop, uint64_t* bar, uint32_t parity,
                                              bool forced = false) {
   if (!forced && mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;
@@ -218,7 +242,8 @@ __device__ __forceinline__ bool wait_or_stop(const DeltaArgs& a, volatile int* s
   atomicOr(a.status, kStatusTmaTimeout);
   return false;
 }
-__device__ __forceinline__ bool forced_here(const DeltaArgs& a) { return (long long)blockIdx.x == a.force_timeout_cta; }
+template <typename Args>
+__device__ __forceinline__ bool forced_here(const Args& a) { return (long long)blockIdx.x == a.force_timeout_cta; }
 
 // The waits of one thread of a CTA.  After one that has run out the thread
 // waits for nothing and, by `ok`, asks for no copy, issues no product and

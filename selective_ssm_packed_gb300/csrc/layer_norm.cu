@@ -1,0 +1,345 @@
+// layer_norm.cu -- layer norm over a token's channels or over each group of
+// them, with the addition to the residual stream in the same pass; and the
+// gradients.
+#include "delta.cuh"
+#include "linear.h"
+
+namespace vssm {
+namespace {
+
+// A row is one group of one token.  kTeam threads share it, 16 values each as
+// two chunks of 8 (chunk i of thread l at 8 (l + i kTeam), so that neighbours
+// read neighbouring chunks): part of a warp for rows of up to 512 values, a
+// whole CTA for longer ones.  The row stays in registers: its mean first, then
+// the sum of the squared differences from it (a sum of squares would lose them
+// where the mean is far from 0), both in f32.  A team walks over rows of one
+// group, so that its weights, and in the backward their gradients, are
+// registers too; the next row is on its way while one is worked on.
+// Everything is read and written once, which bounds the pass.
+template <int kTeam>
+struct Team {
+  static constexpr int kThreads = kTeam <= 32 ? 256 : kTeam, kUnits = kThreads / kTeam;
+};
+constexpr int kNormSms = 152;
+// Threads an SM: they bound the registers of a thread, 64 and 128.
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;
+
+// v[i] summed over the team, in a fixed order.  flip: which half of the scratch
+// is this sum's; one barrier a sum is enough with two.
+template <int kTeam, int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*scratch)[3][16], int& flip) {
+  constexpr int kWidth = kTeam < 32 ? kTeam : 32;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int o = kWidth / 2; o >= 1; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if constexpr (kTeam > 32) {
+    constexpr int kWarps = kTeam / 32;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) scratch[flip][i][threadIdx.x >> 5] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += scratch[flip][i][w];
+      v[i] = s;
+    }
+    flip ^= 1;
+  }
+}
+
+template <int kTeam>
+struct Place {  // of a thread: its group's first channel, its chunks in the row, whether they exist
+  int local, col0, d[2];
+  bool in[2];
+  __device__ __forceinline__ Place(const LayerNormArgs& a, int64_t slot) {
+    const int l = threadIdx.x % kTeam, width = a.D / a.groups;
+    local = threadIdx.x / kTeam;
+    col0 = (int)(slot % a.groups) * width;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      d[i] = (l + i * kTeam) * 8;
+      in[i] = d[i] < width;
+    }
+  }
+};
+
+// Channels' f32 parameters, or `none` where there are none.
+template <int kTeam>
+__device__ __forceinline__ void load_params(const float* p, const Place<kTeam>& at, float none, float (&v)[2][8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    Chunk8<float> c;
+    c.load(p + at.col0 + at.d[i], p != nullptr && at.in[i]);
+    c.get(v[i]);
+    if (!p)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = none;
+  }
+}
+
+// The row's centred values and 1 / its standard deviation.
+template <int kTeam>
+__device__ __forceinline__ void centre(float (&h)[2][8], const Place<kTeam>& at, float inv_count, float (*scratch)[3][16], int& flip) {
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[0] += h[i][j];  // 0 past the row
+  team_sum<kTeam>(s, scratch, flip);
+  const float mean = s[0] * inv_count;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[i][j] = at.in[i] ? h[i][j] - mean : 0.0f;
+}
+
+template <typename T, bool kRes, int kTeam>
+__global__ void __launch_bounds__(Team<kTeam>::kThreads, kFwdThreads / Team<kTeam>::kThreads)
+    layer_norm_fwd_kernel(LayerNormArgs a, int64_t slots) {
+  __shared__ float scratch[2][3][16];
+  const int64_t slot = (int64_t)blockIdx.x * Team<kTeam>::kUnits + threadIdx.x / kTeam;
+  const Place<kTeam> at(a, slot);
+  const float inv_count = 1.0f / (float)(a.D / a.groups);
+  const int64_t units = a.T * a.groups, tokens = slots / a.groups;  // tokens a step of the team moves on
+  float w[2][8], b[2][8];
+  load_params(a.weight, at, 1.0f, w);
+  load_params(a.bias, at, 0.0f, b);
+  Chunk8<T> rx[2];
+  Chunk8<float> rr[2];
+  int64_t tok = slot / a.groups;
+  bool there = slot < slots && tok < a.T;
+  auto load = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rx[i].load(static_cast<const T*>(a.x) + tok * a.sx + at.col0 + at.d[i], there && at.in[i]);
+      if (kRes) rr[i].load(a.residual + tok * a.D + at.col0 + at.d[i], there && at.in[i]);
+    }
+  };
+  load();
+  int flip = 0;
+  for (int64_t base = (int64_t)blockIdx.x * Team<kTeam>::kUnits; base < units; base += slots) {  // the same turns for all of the CTA
+    float h[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rx[i].get(h[i]);
+      if (kRes) {
+        float r[8];
+        rr[i].get(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+      }
+    }
+    const int64_t row = tok * a.D + at.col0;
+    const bool mine = there;
+    tok += tokens;
+    there = slot < slots && tok < a.T;
+    load();
+    if (kRes && a.sum)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (mine && at.in[i]) st_io8(a.sum + row + at.d[i], h[i]);
+    centre(h, at, inv_count, scratch, flip);
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);
+    team_sum<kTeam>(s, scratch, flip);
+    const float r = 1.0f / sqrtf(fmaf(s[0], inv_count, a.eps));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j] * r, w[i][j], b[i][j]);
+      if (mine && at.in[i]) st_io8(static_cast<T*>(a.out) + row + at.d[i], h[i]);
+    }
+  }
+}
+
+// With c the centred row, r = 1 / its standard deviation, n = c r and u = dy w:
+//   dh = r (u - mean(u) - n mean(u n)) + dsum
+//   dweight = sum over tokens of dy n,  dbias = sum of dy
+// One row of sums per team goes to `partial`, which a second kernel adds in
+// the teams' order: no atomics, the same bits every time.
+template <typename T, typename H, int kTeam>
+__global__ void __launch_bounds__(Team<kTeam>::kThreads, kBwdThreads / Team<kTeam>::kThreads)
+    layer_norm_bwd_kernel(LayerNormArgs a, int64_t slots) {
+  __shared__ float scratch[2][3][16];
+  const int64_t slot = (int64_t)blockIdx.x * Team<kTeam>::kUnits + threadIdx.x / kTeam;
+  const Place<kTeam> at(a, slot);
+  const int width = a.D / a.groups;
+  const float inv_count = 1.0f / (float)width;
+  const int64_t units = a.T * a.groups, tokens = slots / a.groups;
+  float w[2][8], gw[2][8], gb[2][8];
+  load_params(a.weight, at, 1.0f, w);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[i][j] = gb[i][j] = 0.0f;
+  Chunk8<H> rx[2];
+  Chunk8<T> rg[2];
+  int64_t tok = slot / a.groups;
+  bool there = slot < slots && tok < a.T;
+  auto load = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rx[i].load(static_cast<const H*>(a.x) + tok * a.sx + at.col0 + at.d[i], there && at.in[i]);
+      rg[i].load(static_cast<const T*>(a.dout) + tok * a.D + at.col0 + at.d[i], there && at.in[i]);
+    }
+  };
+  load();
+  int flip = 0;
+  for (int64_t base = (int64_t)blockIdx.x * Team<kTeam>::kUnits; base < units; base += slots) {
+    float h[2][8], g[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rx[i].get(h[i]);
+      rg[i].get(g[i]);
+    }
+    const int64_t row = tok * a.D + at.col0;
+    const bool mine = there;
+    tok += tokens;
+    there = slot < slots && tok < a.T;
+    load();
+    Chunk8<float> rs[2];
+    if (a.dsum)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) rs[i].load(a.dsum + row + at.d[i], mine && at.in[i]);
+    centre(h, at, inv_count, scratch, flip);
+    float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = g[i][j] * w[i][j];
+        s[0] = fmaf(h[i][j], h[i][j], s[0]);
+        s[1] += u;
+        s[2] = fmaf(u, h[i][j], s[2]);
+      }
+    team_sum<kTeam>(s, scratch, flip);
+    const float r = 1.0f / sqrtf(fmaf(s[0], inv_count, a.eps));
+    const float mean_u = s[1] * inv_count, f = s[2] * inv_count * r * r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (mine) {
+          gw[i][j] = fmaf(g[i][j], h[i][j] * r, gw[i][j]);
+          gb[i][j] += g[i][j];
+        }
+        o[j] = r * (fmaf(g[i][j], w[i][j], -mean_u) - h[i][j] * f);
+      }
+      if (a.dsum) {
+        float d[8];
+        rs[i].get(d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += d[j];
+      }
+      if (mine && at.in[i]) {
+        st_io8(static_cast<T*>(a.dx) + row + at.d[i], o);
+        if (a.dresidual) st_io8(a.dresidual + row + at.d[i], o);
+      }
+    }
+  }
+  if (slot >= slots || !(a.dweight || a.dbias)) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (at.in[i]) {
+      float* p = a.partial + slot * 2 * width + at.d[i];
+      st_io8(p, gw[i]);
+      st_io8(p + width, gb[i]);
+    }
+}
+
+// blockIdx.x: 32 channels; blockIdx.y: weight or bias.  The teams of a group in
+// eight stretches, each added up in order by a warp, then the eight in order.
+__global__ void __launch_bounds__(256) layer_norm_sum_kernel(LayerNormArgs a, int64_t slots) {
+  __shared__ float s[8][32];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5, width = a.D / a.groups;
+  float* out = blockIdx.y ? a.dbias : a.dweight;
+  if (!out) return;
+  const int64_t rows = a.T > 0 ? slots / a.groups : 0, per = (rows + 7) / 8;
+  float v = 0.0f;
+  if (col < a.D) {
+    const int group = col / width;
+    const float* p = a.partial + blockIdx.y * width + (col - group * width);
+    const int64_t end = rows < (part + 1) * per ? rows : (part + 1) * per;
+#pragma unroll 8
+    for (int64_t i = part * per; i < end; ++i) v += p[(i * a.groups + group) * 2 * width];
+  }
+  s[part][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (part == 0 && col < a.D) {
+    for (int p = 1; p < 8; ++p) v += s[p][threadIdx.x & 31];
+    out[col] = v;
+  }
+}
+
+int team_of(int width) {
+  int t = 4;
+  while (t * 16 < width) t *= 2;
+  return t;
+}
+
+// Teams that walk, a multiple of the groups: as many as an SM's threads allow, no more than there are rows.
+int64_t slots_of(int64_t T, int D, int groups, int sm_threads) {
+  const int64_t most = (int64_t)kNormSms * sm_threads / team_of(D / groups), units = T * groups;
+  const int64_t use = units < most ? units : most;
+  return use < groups ? groups : use / groups * groups;
+}
+
+template <typename F>
+cudaError_t with_team(int width, F f) {
+  switch (team_of(width)) {
+    case 4: return f(std::integral_constant<int, 4>());
+    case 8: return f(std::integral_constant<int, 8>());
+    case 16: return f(std::integral_constant<int, 16>());
+    case 32: return f(std::integral_constant<int, 32>());
+    case 64: return f(std::integral_constant<int, 64>());
+    case 128: return f(std::integral_constant<int, 128>());
+    case 256: return f(std::integral_constant<int, 256>());
+    default: return f(std::integral_constant<int, 512>());
+  }
+}
+
+template <typename T, bool kRes>
+cudaError_t run_fwd(const LayerNormArgs& a, cudaStream_t st) {
+  return with_team(a.D / a.groups, [&](auto team) {
+    constexpr int kTeam = decltype(team)::value, kUnits = Team<kTeam>::kUnits;
+    const int64_t slots = slots_of(a.T, a.D, a.groups, kFwdThreads);
+    layer_norm_fwd_kernel<T, kRes, kTeam><<<(unsigned)((slots + kUnits - 1) / kUnits), Team<kTeam>::kThreads, 0, st>>>(a, slots);
+    return cudaGetLastError();
+  });
+}
+
+template <typename T, typename H>
+cudaError_t run_bwd(const LayerNormArgs& a, cudaStream_t st) {
+  return with_team(a.D / a.groups, [&](auto team) {
+    constexpr int kTeam = decltype(team)::value, kUnits = Team<kTeam>::kUnits;
+    const int64_t slots = slots_of(a.T, a.D, a.groups, kBwdThreads);
+    if (a.T > 0)
+      layer_norm_bwd_kernel<T, H, kTeam><<<(unsigned)((slots + kUnits - 1) / kUnits), Team<kTeam>::kThreads, 0, st>>>(a, slots);
+    if (a.dweight || a.dbias) layer_norm_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), 256, 0, st>>>(a, slots);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace
+
+int64_t layer_norm_slots(int64_t T, int D, int groups) { return slots_of(T, D, groups, kBwdThreads); }
+
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, IO io, cudaStream_t st) {
+  if (a.T == 0) return cudaSuccess;
+  if (io == IO::BF16) return a.residual ? run_fwd<__nv_bfloat16, true>(a, st) : run_fwd<__nv_bfloat16, false>(a, st);
+  return a.residual ? run_fwd<float, true>(a, st) : run_fwd<float, false>(a, st);
+}
+
+cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, IO io, bool x_f32, cudaStream_t st) {
+  if (io == IO::F32) return run_bwd<float, float>(a, st);
+  return x_f32 ? run_bwd<__nv_bfloat16, float>(a, st) : run_bwd<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+}  // namespace vssm

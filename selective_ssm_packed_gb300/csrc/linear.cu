@@ -1,0 +1,622 @@
+// linear.cu -- linear attention's walk over the chunks of a segment: the
+// forward, each of its three gradients, and the states between segments.
+#include "delta.cuh"
+#include "linear.h"
+
+namespace vssm {
+namespace {
+
+// One CTA per (segment, value head, role, 64 columns of the state; the columns
+// never mix).  A chunk (128 tokens in bf16, 64 in f32) is four products on the
+// matrix unit:
+//   A  = X Y^T             read back, weighted and masked: P, bf16 terms in tensor memory
+//   D1 = X S
+//   U  = Y^T (up * W)      S = exp(G_end) S + U, in registers and as bf16 terms in shared memory
+//   D2 = P W               out = in * D1 + D2
+// with in and up the weights of a row for the state and in it.  Eight warps
+// work on the operands and results, two threads to a row; a ninth issues the
+// products and makes the next chunk's gates meanwhile.  What one product
+// leaves is worked on while the next one runs: up * W during A and D1, P
+// during U, S during D2.
+constexpr int kLinThreads = 288, kLinWorkers = 256;
+
+template <IO kIO>
+struct LinGeo {
+  static constexpr int kC = kIO == IO::BF16 ? 128 : 64;
+  static constexpr int kBlocks = kC / 32;  // of 16 columns in half a row of P
+  static constexpr int kPWords = kIO == IO::BF16 ? 16 : 32;  // columns of tensor memory a block of P takes
+  static constexpr bool kBf16 = kIO == IO::BF16;
+  // columns of tensor memory: in bf16 P takes A's place, and the products with the state's and W's terms side by side
+  // (see umma_blocks) have 64 columns for each
+  static constexpr int kD = kBf16 ? 128 : 64;
+  static constexpr int tA = 0, tP = kBf16 ? 0 : 64, tD1 = kBf16 ? 128 : 192, tU = tD1 + kD, tO = tU + kD;
+  static_assert(tO + 64 <= 512, "tensor memory");
+};
+
+template <IO kIO, int KP>
+struct LinSmem {
+  using D = DeltaTerms<kIO>;
+  static constexpr int kC = LinGeo<kIO>::kC, kPanel = kC * 128;  // bytes of 64 columns of a chunk's rows
+  static constexpr int kX = D::kIn * KP * kPanel, kW = D::kIn * kPanel, kUp = D::kMid * kPanel;
+  static constexpr int kSTerm = KP * 64 * 128, kS = D::kMid * kSTerm;
+  static constexpr int kBufs = kIO == IO::BF16 ? 2 : 1;  // of Y and W
+  // (in f32 the products take 128 rows of X's 64: what follows it counts as rows whose results nobody reads)
+  static constexpr int oX = 0, oY = kX, oW = oY + kBufs * kX, oUp = oW + kBufs * kW, oS = oUp + kUp, oGates = oS + kS;
+  static constexpr int kGates = 16 * kC;                 // (G / ln 2 as two floats, in, up) of the tokens
+  static constexpr int oEnd = oGates + 2 * kGates;       // exp(G_end) of either buffer
+  static constexpr int oDiag = oEnd + 16, oBad = oDiag + 4 * kC, oAnyBad = oBad + 2 * 64 * 4;
+  static constexpr int oBar = oAnyBad + 16, kBytes = oBar + 64 + 1024;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+struct LinWaiter {
+  const LinArgs& a;
+  volatile int* stop;
+  bool ok = true;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity, bool forced = false) {
+    ok = ok && wait_or_stop(a, stop, bar, parity, forced);
+  }
+};
+
+// Like umma, A in tensor memory: its rows in the lanes, two bf16 to a column.
+__device__ __forceinline__ void umma_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t desc_b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(desc_b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ bool odd_bf16(uint32_t pair) {  // either half NaN or infinite
+  return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
+}
+
+template <IO kIO, int KP, bool kStateOnly>
+__global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_constant__ LinArgs a, int roles, int all_tiles) {
+  using T = typename IoType<kIO>::type;
+  using L = LinSmem<kIO, KP>;
+  using G = LinGeo<kIO>;
+  using R = WalkRow<T, 4>;  // 32 columns to a thread
+  using RF = WalkRow<float, 4>;
+  constexpr int kC = L::kC, NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, kBufs = L::kBufs;
+  constexpr bool kBf16 = kIO == IO::BF16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  uint64_t* bar_a = reinterpret_cast<uint64_t*>(sm + L::oBar);
+  uint64_t *bar_u = bar_a + 1, *bar_o = bar_a + 2, *drained = bar_a + 3;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar_a + 4);
+  volatile int* stop = reinterpret_cast<int*>(tmem_at + 1);
+  volatile int* leave = stop + 1;
+  float* s_end = reinterpret_cast<float*>(sm + L::oEnd);
+  float* s_diag = reinterpret_cast<float*>(sm + L::oDiag);
+  int* s_bad = reinterpret_cast<int*>(sm + L::oBad);
+  volatile int* any_bad = reinterpret_cast<int*>(sm + L::oAnyBad);
+
+  // what this CTA walks
+  int tile = blockIdx.x % all_tiles, which = 0;
+  const int h = blockIdx.x / all_tiles % a.Hv;
+  const int64_t item = blockIdx.x / all_tiles / a.Hv;
+  while (which + 1 < roles && tile >= lin_tiles(a.role[which].n2)) tile -= lin_tiles(a.role[which++].n2);
+  const LinRole& role = a.role[which];
+  const bool back = role.back != 0;
+  if (item >= a.info[kStateOnly ? 1 : 0]) return;
+  const int seg = kStateOnly ? a.inner[item] + (back ? 1 : 0) : a.order[item];
+  const int4 entry = a.table[seg];
+  const int64_t start = entry.y;
+  const int len = entry.z, n = (len + kC - 1) / kC;
+  const bool is_first = entry.w & kLinFirst, is_last = entry.w & kLinLast;
+  const int64_t inner_before = (unsigned)entry.w >> kLinPlaceShift;
+  const int n1 = role.n1, n2 = role.n2, tiles = lin_tiles(n2);
+
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  auto bad_none = [&]() { return back ? -1 : kC; };
+  if (t == 0) {
+    mbar_init(bar_a, 1);
+    mbar_init(bar_u, 1);
+    mbar_init(bar_o, 1);
+    mbar_init(drained, 1);
+    *stop = *leave = 0;
+    any_bad[0] = any_bad[1] = 0;
+    fence_mbar_init();
+  }
+  if (t < 128) s_bad[t] = bad_none();
+  if (warp == 8) tmem_alloc<512>(tmem_at);
+
+  const float* g_base = a.g + start * a.g_token + h;
+  // warp 8: the gates of chunk c.  Its running sum of g in double: differences of it enter exp.
+  auto make_gates = [&](int c, int buf) -> double {
+    constexpr int kPer = kC / 32;
+    const int rows = min(kC, len - c * kC);
+    double gs[kPer], incl = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = lane * kPer + i;
+      float v = r < rows ? g_base[(int64_t)(c * kC + r) * a.g_token] : 0.0f;
+      v = v < -256.0f ? -256.0f : v;  // exp of either is 0; -inf would leave inf - inf
+      incl += (double)v;
+      gs[i] = incl;
+    }
+    const double own = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const double last = __shfl_sync(0xffffffffu, incl, 31);
+    double before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = 0.0;
+    (void)own;
+    float4* gates = reinterpret_cast<float4*>(sm + L::oGates + buf * L::kGates);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const double Gi = before + gs[i], G2 = Gi * 1.4426950408889634;
+      const float hi = (float)G2, lo = (float)(G2 - (double)hi);
+      const float gh = (float)Gi, dh = (float)(last - Gi);
+      const float from = a.scale * (exp_f(gh) * (1.0f + (float)(Gi - (double)gh)));
+      const float to = exp_f(dh) * (1.0f + (float)(last - Gi - (double)dh));
+      gates[lane * kPer + i] = back ? make_float4(hi, lo, to, from) : make_float4(hi, lo, from, to);
+    }
+    if (lane == 0) {
+      const float lh = (float)last;
+      s_end[buf] = exp_f(lh) * (1.0f + (float)(last - (double)lh));
+    }
+    return last;
+  };
+
+  const T* xb = static_cast<const T*>(role.x) + start * role.sx + (int64_t)(h / role.rx) * n1;
+  const T* yb = static_cast<const T*>(role.y) + start * role.sy + (int64_t)(h / role.ry) * n1;
+  const T* wb = static_cast<const T*>(role.w) + start * role.sw + (int64_t)(h / role.rw) * n2 + tile * kLinTile;
+  const int wcols = n2 - tile * kLinTile;  // of W from this tile on
+
+  // bf16: rows of kPanels * 64 columns as an image, zero past the chunk's end and the width
+  auto copy_image = [&](uint8_t* image, const T* base, int64_t stride, int panels, int cols, int rows) {
+    const int per_row = panels * 8;
+#pragma unroll 4
+    for (int i = t; i < kC * per_row; i += kLinWorkers) {
+      const int r = i / per_row, ch = i - r * per_row;
+      const bool in = r < rows && ch * 8 < cols;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       smem_u32(image + (ch >> 3) * L::kPanel + image_chunk<128>(r, ch & 7))),
+                   "l"(in ? base + r * stride + ch * 8 : base), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+  };
+  auto load_x = [&](int c) {
+    if constexpr (kBf16 && !kStateOnly) {
+      copy_image(sm + L::oX, xb + (int64_t)c * kC * role.sx, role.sx, KP, n1, len - c * kC);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  auto load_yw = [&](int c, int buf) {
+    if constexpr (kBf16) {
+      copy_image(sm + L::oY + buf * L::kX, yb + (int64_t)c * kC * role.sy, role.sy, KP, n1, len - c * kC);
+      copy_image(sm + L::oW + buf * L::kW, wb + (int64_t)c * kC * role.sw, role.sw, 1, wcols, len - c * kC);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  auto note_bad = [&](int which_buf, int col, int r) {
+    if (back) atomicMax(s_bad + which_buf * 64 + col, r); else atomicMin(s_bad + which_buf * 64 + col, r);
+    any_bad[which_buf] = 1;
+  };
+  // f32: the images of X, Y, W and up * W, through registers
+  constexpr int kLoadX = kC * KP * 8 / kLinWorkers, kLoadW = kC * 8 / kLinWorkers;
+  auto load_f32 = [&](int c, int buf) {
+    if constexpr (!kBf16) {
+      const int rows = len - c * kC;
+      float4 x[kLoadX][2], y[kLoadX][2], w[kLoadW][2];
+      auto get = [&](float4 (&f)[2], const T* base, int64_t stride, int r, int ch, int cols) {
+        f[0] = f[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < rows && ch * 8 < cols) {
+          const float4* src = reinterpret_cast<const float4*>(base + (c * kC + r) * stride + ch * 8);
+          f[0] = src[0];
+          f[1] = src[1];
+        }
+      };
+#pragma unroll
+      for (int u = 0; u < kLoadX; ++u) {
+        const int i = t + u * kLinWorkers, r = i / (KP * 8), ch = i % (KP * 8);
+        get(y[u], yb, role.sy, r, ch, n1);
+        if (!kStateOnly) get(x[u], xb, role.sx, r, ch, n1);
+      }
+#pragma unroll
+      for (int u = 0; u < kLoadW; ++u) get(w[u], wb, role.sw, (t + u * kLinWorkers) / 8, t % 8, wcols);
+#pragma unroll
+      for (int u = 0; u < kLoadX; ++u) {
+        const int i = t + u * kLinWorkers, r = i / (KP * 8), ch = i % (KP * 8);
+        auto put = [&](int o, const float4 (&f)[2]) {
+          const float2 v[4] = {make_float2(f[0].x, f[0].y), make_float2(f[0].z, f[0].w), make_float2(f[1].x, f[1].y),
+                               make_float2(f[1].z, f[1].w)};
+          put_chunk<NQ, 128>(sm + o + (ch >> 3) * L::kPanel, KP * L::kPanel, r, ch & 7, v);
+        };
+        put(L::oY, y[u]);
+        if (!kStateOnly) put(L::oX, x[u]);
+      }
+      const float4* gates = reinterpret_cast<const float4*>(sm + L::oGates + buf * L::kGates);
+#pragma unroll
+      for (int u = 0; u < kLoadW; ++u) {
+        const int r = (t + u * kLinWorkers) / 8, ch = t % 8;
+        float2 v[4] = {make_float2(w[u][0].x, w[u][0].y), make_float2(w[u][0].z, w[u][0].w),
+                       make_float2(w[u][1].x, w[u][1].y), make_float2(w[u][1].z, w[u][1].w)};
+        float2 up[4];
+        float2 trace = splat2(0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          up[i] = mul2(v[i], splat2(gates[r].w));
+          trace = fma2(v[i], splat2(0.0f), trace);
+        }
+        put_chunk<NT, 128>(sm + L::oUp, L::kPanel, r, ch, up);
+        if (trace.x + trace.y != 0.0f) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (v[i].x * 0.0f != 0.0f) { note_bad(buf, ch * 8 + 2 * i, r); v[i].x = 0.0f; }
+            if (v[i].y * 0.0f != 0.0f) { note_bad(buf, ch * 8 + 2 * i + 1, r); v[i].y = 0.0f; }
+          }
+        }
+        if (!kStateOnly) put_chunk<NQ, 128>(sm + L::oW, L::kPanel, r, ch, v);
+      }
+    }
+  };
+  // bf16: up * W from W's image.  A value of W that is not finite reaches the
+  // state, and so every later row, through up * W; in D2, where 0 times it would
+  // reach earlier rows, 0 takes its place, and its column's rows from it on are
+  // made NaN when they are written.
+  auto weigh = [&](int buf) {
+    if constexpr (kBf16) {
+      const float4* gates = reinterpret_cast<const float4*>(sm + L::oGates + buf * L::kGates);
+      uint8_t* image = sm + L::oW + buf * L::kW;
+#pragma unroll
+      for (int u = 0; u < kC * 8 / kLinWorkers; ++u) {
+        const int i = t + u * kLinWorkers, r = i / 8, ch = i % 8;
+        uint4* at = reinterpret_cast<uint4*>(image + image_chunk<128>(r, ch));
+        const uint4 q = *at;
+        float2 v[4];
+        unpack(q, v);
+        float2 trace = splat2(0.0f);
+        const float f = gates[r].w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          trace = fma2(v[k], splat2(0.0f), trace);
+          v[k] = mul2(v[k], splat2(f));
+        }
+        put_chunk<NT, 128>(sm + L::oUp, L::kPanel, r, ch, v);
+        if (!kStateOnly && trace.x + trace.y != 0.0f) {
+          uint32_t p[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (odd_bf16(p[k])) {
+              if ((p[k] & 0x7f80u) == 0x7f80u) { note_bad(buf, ch * 8 + 2 * k, r); p[k] &= 0xffff0000u; }
+              if ((p[k] & 0x7f800000u) == 0x7f800000u) { note_bad(buf, ch * 8 + 2 * k + 1, r); p[k] &= 0xffffu; }
+            }
+          *at = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+    }
+  };
+
+  const int quad = warp & 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
+  const int col0 = tile * kLinTile + half * 32;  // this thread's columns of the state and of the results
+  const bool state_row = row < n1 && warp < 8;
+  // the state the segment starts from, if any
+  const int64_t state_at = (int64_t)row * role.srow + (int64_t)col0 * role.scol;
+  const int64_t state_size = (int64_t)n1 * n2;
+  const float* carry = nullptr;
+  if (back ? is_last : is_first) {
+    if (role.first) carry = role.first + ((int64_t)entry.x * a.Hv + h) * state_size;
+  } else if (!kStateOnly) {
+    carry = role.slots + ((back ? inner_before : inner_before - 1) * a.Hv + h) * state_size;
+  }
+  float2 S[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) S[i] = splat2(0.0f);
+  auto state_io = [&](auto f) {  // f(i, offset) for the pairs i of this thread's columns that exist
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (state_row && col0 + 2 * i < n2) f(i, state_at + 2 * i * role.scol);
+  };
+  if (carry) state_io([&](int i, int64_t at) { S[i] = make_float2(carry[at], carry[at + role.scol]); });
+  const bool has_carry = carry != nullptr;
+
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = *tmem_at;
+  const uint32_t lane_at = (uint32_t)(quad * 32) << 16;
+  LinWaiter wait{a, stop};
+  auto chunk_of = [&](int k) { return back ? n - 1 - k : k; };
+
+  if (warp == 8) {
+    double total = 0.0;
+    if (n > 0) total = make_gates(chunk_of(0), 0);
+    if (!kBf16 && n > 0) named_barrier(4, kLinThreads);
+    for (int k = 0; k < n; ++k) {
+      const int buf = k & 1, lb = kBufs == 2 ? buf : 0;
+      if (lane == 0) *leave = *stop;
+      named_barrier(1, kLinThreads);
+      if (*leave) break;
+      const uint32_t sx = smem_u32(sm + L::oX), sy = smem_u32(sm + L::oY + lb * L::kX), sw = smem_u32(sm + L::oW + lb * L::kW);
+      if (!kStateOnly && lane == 0 && !*stop) {
+        tmem_fence_after_sync();
+        const Operand<128, kKMajor, NQ, KP * L::kPanel, L::kPanel> X(sx), Y(sy);
+        umma_terms<kC, KP * 4, NQ>(tm + G::tA, X, Y, false);
+        umma_commit(bar_a);
+        if (k > 0 || has_carry) {
+          const Operand<128, kMnMajor, NT, L::kSTerm, 0, L::kSTerm> St(smem_u32(sm + L::oS));
+          if constexpr (kBf16) umma_blocks<64, KP * 4, NT, true>(tm + G::tD1, X, St);
+          else umma_terms<64, KP * 4, NT>(tm + G::tD1, X, St, false);
+        }
+      }
+      __syncwarp();
+      named_barrier(2, kLinThreads);
+      if (lane == 0 && !*stop) {
+        tmem_fence_after_sync();
+        const Operand<128, kMnMajor, NQ, KP * L::kPanel, 0, L::kPanel> Yt(sy);
+        const Operand<128, kMnMajor, NT, L::kPanel, 0, L::kPanel> Up(smem_u32(sm + L::oUp));
+        if constexpr (kBf16) umma_blocks<64, kC / 16, NT, true>(tm + G::tU, Yt, Up);
+        else umma_terms<64, kC / 16, NT>(tm + G::tU, Yt, Up, false);
+        umma_commit(bar_u);
+      }
+      __syncwarp();
+      if (k + 1 < n) total += make_gates(chunk_of(k + 1), buf ^ 1);
+      if constexpr (!kStateOnly) {
+        named_barrier(3, kLinThreads);
+        if (lane == 0 && !*stop) {
+          tmem_fence_after_sync();
+          const Operand<128, kMnMajor, NQ, L::kPanel> W(sw);
+          constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, 64);
+          uint32_t acc = 0;
+#pragma unroll
+          for (int sum = NT - 1; sum >= 0; --sum)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              const int j = sum - i;
+              if (j < 0 || j >= NQ) continue;
+#pragma unroll
+              for (int s = 0; s < kC / 16; ++s) {
+                umma_ta(tm + G::tO, tm + G::tP + G::kPWords * s + 8 * i, W.at(j, s), idesc, acc);
+                acc = 1;
+              }
+            }
+          umma_commit(bar_o);
+        }
+        __syncwarp();
+      }
+      if (!kBf16 && k + 1 < n) named_barrier(4, kLinThreads);
+    }
+    if (kStateOnly && lane == 0 && tile == 0) {
+      const float th = (float)total;
+      role.decay[item * a.Hv + h] = exp_f(th) * (1.0f + (float)(total - (double)th));
+    }
+  } else {
+    uint32_t phase = 0;
+    if (n > 0) {
+      if constexpr (kBf16) {
+        load_x(chunk_of(0));
+        load_yw(chunk_of(0), 0);
+      } else {
+        named_barrier(4, kLinThreads);  // the gates
+        load_f32(chunk_of(0), 0);
+      }
+    }
+    if (!kStateOnly && has_carry && row < KP * 64)
+      put_row<NT, 128>(sm + L::oS, L::kSTerm, row, half * 4, S);
+    for (int k = 0; k < n; ++k, phase ^= 1) {
+      const int c = chunk_of(k), buf = k & 1, lb = kBufs == 2 ? buf : 0;
+      const int rows = min(kC, len - c * kC);
+      const bool more = k + 1 < n, has_state = k > 0 || has_carry;
+      if constexpr (kBf16) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_async_smem();
+      tmem_fence_before_sync();
+      named_barrier(1, kLinThreads);
+      tmem_fence_after_sync();
+      if (*leave) break;
+      if (t < 64) s_bad[(buf ^ 1) * 64 + t] = bad_none();
+      if (t == 0) any_bad[buf ^ 1] = 0;
+      if (more) load_yw(chunk_of(k + 1), lb ^ 1);
+      const float4* gates = reinterpret_cast<const float4*>(sm + L::oGates + buf * L::kGates);
+      weigh(lb);
+      fence_async_smem();
+      asm volatile("bar.arrive %0, %1;" ::"r"(2), "r"(kLinThreads) : "memory");
+
+      if constexpr (!kStateOnly) {
+        wait(bar_a, phase, k == 0 && t == 0 && forced_here(a));
+        tmem_fence_after_sync();
+        if (row < kC) {
+          const float4 mine = gates[row];
+          const float sign = back ? -1.0f : 1.0f;
+#pragma unroll
+          for (int u = 0; u < G::kBlocks; ++u) {
+            const int j0 = half * (kC / 2) + 16 * u;
+            uint32_t words[G::kPWords];
+#pragma unroll
+            for (int i = 0; i < G::kPWords; ++i) words[i] = 0;
+            if (back ? j0 + 15 >= quad * 32 : j0 <= quad * 32 + 31) {  // the warp has rows that see these columns
+              float d[16];
+              tmem_row(tm + G::tA + lane_at + j0, d);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int j = j0 + i;
+                const float4 gj = gates[j];
+                const float w = ex2(sign * ((mine.x - gj.x) + (mine.y - gj.y))) * a.scale * d[i];
+                if (role.dot && j == row) s_diag[row] = a.scale * d[i];
+                const bool seen = back ? j >= row && j < rows : j <= row;
+                d[i] = seen && !(role.dot && j == row) ? w : 0.0f;
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint32_t term[NT];
+                split_pair<NT>(make_float2(d[2 * i], d[2 * i + 1]), term);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) words[8 * q + i] = term[q];
+              }
+            }
+            __syncwarp();
+            if constexpr (kBf16) tmem_st16(tm + G::tP + lane_at + j0, words);
+            else tmem_st32(tm + G::tP + lane_at + 2 * j0, words);
+          }
+          tmem_wait_st();
+        }
+        tmem_fence_before_sync();
+        named_barrier(3, kLinThreads);
+      }
+
+      wait(bar_u, phase, kStateOnly && k == 0 && t == 0 && forced_here(a));
+      tmem_fence_after_sync();
+      if (more) load_x(chunk_of(k + 1));
+      if (row < KP * 64) {
+        const float end = s_end[buf];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float2 d[8];
+          tmem_sum<kBf16 ? NT : 1>(tm + G::tU + lane_at + half * 32 + 16 * u, 64, d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) S[8 * u + i] = d[i] = fma2(splat2(end), S[8 * u + i], d[i]);
+          if (!kStateOnly && more) put_row<NT, 128>(sm + L::oS, L::kSTerm, row, half * 4 + 2 * u, d);
+        }
+      }
+
+      if constexpr (!kStateOnly) {
+        wait(bar_o, phase);
+        tmem_fence_after_sync();
+        if (row < kC) {
+          const float in = gates[row].z;
+          const int64_t at = (int64_t)c * kC + quad * 32;  // the warp's first token
+          float2 o[16];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float2 d[8];
+            tmem_sum<1>(tm + G::tO + lane_at + half * 32 + 16 * u, 0, d);
+            if (has_state) {
+              float2 e[8];
+              tmem_sum<kBf16 ? NT : 1>(tm + G::tD1 + lane_at + half * 32 + 16 * u, 64, e);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) d[i] = fma2(splat2(in), e[i], d[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[8 * u + i] = d[i];
+          }
+          if (role.dot) {  // rho or sigma, then the token's own pair
+            typename R::Raw raw;
+            R::load(static_cast<const T*>(role.dot) + (start + at) * role.sdot + (int64_t)(h / role.rdot) * n2 + col0, role.sdot,
+                    len - at, n2 - col0, lane, raw);
+#pragma unroll
+            for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
+            float2 sum = splat2(0.0f);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) R::each(raw, u, [&](int i, float2 y) { sum = fma2(y, o[8 * u + i], sum); });
+            if (row < rows) role.dots[((int64_t)(tile * 2 + half) * a.T + start + at + lane) * a.Hv + h] = sum.x + sum.y;
+            const float self = s_diag[row];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t place = image_chunk<128>(row, half * 4 + q);
+#pragma unroll
+              for (int term = NQ - 1; term >= 0; --term) {
+                float2 w[4];
+                unpack(*reinterpret_cast<const uint4*>(sm + L::oW + lb * L::kW + term * L::kPanel + place), w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[4 * q + i] = fma2(splat2(self), w[i], o[4 * q + i]);
+              }
+            }
+          }
+          if (any_bad[buf]) {
+            const float nan = __int_as_float(0x7fffffff);
+            const int* bad = s_bad + buf * 64 + half * 32;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (back ? row <= bad[2 * i] : row >= bad[2 * i]) o[i].x = nan;
+              if (back ? row <= bad[2 * i + 1] : row >= bad[2 * i + 1]) o[i].y = nan;
+            }
+          }
+          const int64_t out_at = ((start + at) * a.Hv + h) * n2 + col0;
+          auto store = [&](auto rows_of, auto* base) {
+            using Q = decltype(rows_of);
+            typename Q::Raw raw;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float2 d[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) d[i] = o[8 * u + i];
+              Q::put(raw, u, d);
+            }
+            Q::store(base + out_at, (int64_t)a.Hv * n2, len - at, n2 - col0, lane, raw);
+          };
+          if (kBf16 && role.part) store(RF(), static_cast<float*>(role.out));
+          else store(R(), static_cast<T*>(role.out));
+        }
+      }
+      if constexpr (!kBf16) {
+        if (more) {
+          named_barrier(4, kLinThreads);  // everyone is through with the images, and the next gates are there
+          load_f32(chunk_of(k + 1), buf ^ 1);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // the state the segment leaves
+    float* to = nullptr;
+    if (kStateOnly) to = role.slots + (item * a.Hv + h) * state_size;
+    else if (role.last && (back ? is_first : is_last)) to = role.last + ((int64_t)entry.x * a.Hv + h) * state_size;
+    if (to) state_io([&](int i, int64_t at) {
+      to[at] = S[i].x;
+      to[at + role.scol] = S[i].y;
+    });
+    if (!kStateOnly && role.cross) {
+      const float* e = is_last ? (role.against_last ? role.against_last + ((int64_t)entry.x * a.Hv + h) * state_size : nullptr)
+                               : role.against + (inner_before * a.Hv + h) * state_size;
+      float2 sum = splat2(0.0f);
+      if (e) state_io([&](int i, int64_t at) { sum = fma2(S[i], make_float2(e[at], e[at + role.scol]), sum); });
+      float v = sum.x + sum.y;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      float* part = reinterpret_cast<float*>(sm + L::oGates);  // the gates are not needed any more
+      named_barrier(5, kLinWorkers);
+      if (lane == 0) part[warp] = v;
+      named_barrier(5, kLinWorkers);
+      if (t == 0) {
+        for (int i = 1; i < 8; ++i) v += part[i];
+        role.cross[((int64_t)seg * a.Hv + h) * tiles + tile] = v;
+      }
+    }
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  if (warp == 8) {
+    if (lane == 0 && *stop) {  // products that were not waited for
+      umma_commit(drained);
+      mbar_wait(drained, 0, kCopyDrainNs);
+    }
+    __syncwarp();
+    tmem_dealloc<512>(tm);
+  }
+}
+
+template <IO kIO, int KP, bool kStateOnly>
+cudaError_t run_walk(const LinArgs& a, int roles, cudaStream_t st) {
+  constexpr size_t bytes = LinSmem<kIO, KP>::kBytes;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(lin_walk_kernel<kIO, KP, kStateOnly>), bytes, done);
+  if (e != cudaSuccess) return e;
+  int tiles = 0;
+  for (int i = 0; i < roles; ++i) tiles += lin_tiles(a.role[i].n2);
+  const int64_t blocks = (kStateOnly ? a.max_inner : a.max_segs) * a.Hv * tiles;
+  lin_walk_kernel<kIO, KP, kStateOnly><<<(unsigned)blocks, kLinThreads, bytes, st>>>(a, roles, tiles);
+  return cudaGetLastError();
+}
+
+template <IO kIO, bool kStateOnly>
+cudaError_t pick_walk(const LinArgs& a, int roles, cudaStream_t st) {
+  int width = 0;
+  for (int i = 0; i < roles; ++i) width = width > a.role[i].n1 ? width : a.role[i].n1;
+  return width > 64 ? run_walk<kIO, 2, kStateOnly>(a, roles, st) : run_walk<kIO, 1, kStateOnly>(a, roles, st);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_walk(const LinArgs& a, int roles, bool state_only, IO io, cudaStream_t st) {
+  if ((state_only ? a.max_inner : a.max_segs) == 0) return cudaSuccess;
+  if (io == IO::BF16) return state_only ? pick_walk<IO::BF16, true>(a, roles, st) : pick_walk<IO::BF16, false>(a, roles, st);
+  return state_only ? pick_walk<IO::F32, true>(a, roles, st) : pick_walk<IO::F32, false>(a, roles, st);
+}
+
+}  // namespace vssm

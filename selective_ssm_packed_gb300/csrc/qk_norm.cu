@@ -24,29 +24,6 @@ namespace {
 // against 398.
 constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
 
-// A chunk as it is read, unpacked when it is its row's turn.
-template <typename T>
-struct Chunk8 {
-  static constexpr int kWords = (int)sizeof(T) / 2;
-  uint4 q[kWords];
-  __device__ __forceinline__ void load(const T* p, bool there) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) q[i] = there ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      float2 w[8 / kWords / 2];
-      unpack(q[i], w);
-#pragma unroll
-      for (int j = 0; j < 8 / kWords / 2; ++j) {
-        v[i * 4 + 2 * j] = w[j].x;
-        v[i * 4 + 2 * j + 1] = w[j].y;
-      }
-    }
-  }
-};
-
 template <typename T>
 struct NormSide {  // q or k
   const T *x, *dy;

@@ -31,8 +31,10 @@ CHECKS_LIB_PATH = os.path.join(CHECKS_BUILD_DIR, "libvarlen_ssm_checks.so")
 
 SOURCES = ["api.cu", "misc.cu", "conv.cu", "scan_fwd.cu", "scan_bwd.cu", "noalloc.cu", "packer.cu",
            "delta_api.cu", "delta_prep.cu", "delta_fwd.cu", "delta_bwd.cu", "delta_grad.cu", "delta_step.cu",
-           "qk_norm.cu", "linear_api.cu", "linear_plan.cu", "linear.cu", "linear_step.cu", "layer_norm.cu"]
-HEADERS = [*(os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "umma.cuh", "delta.cuh", "delta.h", "linear.h", "api_checks.h")),
+           "qk_norm.cu", "linear_api.cu", "linear_plan.cu", "linear.cu", "linear_bf16.cu",
+           "linear_step.cu", "layer_norm.cu"]
+HEADERS = [*(os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "umma.cuh", "delta.cuh", "delta.h", "linear.h", "linear.cuh",
+                                                    "api_checks.h")),
            os.path.join(INCLUDE, "varlen_ssm.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -343,6 +343,22 @@ vssm::ScanLayout vssm::scan_workspace_layout(int64_t T, int D, int N, int chunk,
 
 int vssm::scan_tile_width(int N, bool bwd) { return scan_tile(N, bwd); }
 
+int vssm::encode_heads_map(CUtensorMap* m, const void* base, int64_t T, int H, int n, int64_t stride, int box_n, int box_t) {
+  auto enc = encoder();
+  if (!enc) return fail(VSSM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {(cuuint64_t)n, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)n * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)box_n, 1, (cuuint32_t)box_t};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(VSSM_ERR_ARG, "no tensor map for %lld tokens of %d heads of %d, %lld apart (%d)", (long long)T, H, n,
+                (long long)stride, (int)r);
+  return VSSM_OK;
+}
+
 int vssm::encode_tile_map(CUtensorMap* m, const void* base, IO io, int64_t T, int D, int box_x, int box_y) {
   return make_map(m, base, io, T, D, box_x, box_y);
 }

@@ -226,6 +226,10 @@ int scan_tile_width(int N, bool bwd);
 // 2-D tensor map over a (T, D) row-major tensor, box = box_x channels x
 // box_y tokens; returns VSSM_OK or a VSSM_ERR_* code (message recorded).
 int encode_tile_map(CUtensorMap* m, const void* base, IO io, int64_t T, int D, int box_x, int box_y);
+// 3-D map over bf16 rows (T, H, n), tokens `stride` elements apart: boxes of
+// box_n values of one head and box_t tokens as an operand image of 128-byte rows
+// (umma.cuh); zero past the width and the last token.
+int encode_heads_map(CUtensorMap* m, const void* base, int64_t T, int H, int n, int64_t stride, int box_n, int box_t);
 // The test knobs set by vssm_debug_set, as the kernels take them.
 struct DebugKnobs {
   long long drop_ticket;

@@ -1,7 +1,6 @@
 // linear.cu -- linear attention's walk over the chunks of a segment: the
 // forward, each of its three gradients, and the states between segments.
-#include "delta.cuh"
-#include "linear.h"
+#include "linear.cuh"
 
 namespace vssm {
 namespace {
@@ -13,17 +12,17 @@ namespace {
 //   D1 = X S
 //   U  = Y^T (up * W)      S = exp(G_end) S + U, in registers and as bf16 terms in shared memory
 //   D2 = P W               out = in * D1 + D2
-// with in and up the weights of a row for the state and in it.  Eight warps
-// work on the operands and results, two threads to a row; a ninth issues the
+// with in and up the weights of a row for the state and in it.  Sixteen warps
+// work on the operands and results, four threads to a row; another issues the
 // products and makes the next chunk's gates meanwhile.  What one product
 // leaves is worked on while the next one runs: up * W during A and D1, P
 // during U, S during D2.
-constexpr int kLinThreads = 288, kLinWorkers = 256;
+constexpr int kLinWorkers = 128 * kLinParts, kLinThreads = kLinWorkers + 32, kLinCtrl = kLinWorkers / 32;
 
 template <IO kIO>
 struct LinGeo {
   static constexpr int kC = kIO == IO::BF16 ? 128 : 64;
-  static constexpr int kBlocks = kC / 32;  // of 16 columns in half a row of P
+  static constexpr int kBlocks = kC / 16 / kLinParts;  // of 16 columns of P to a thread
   static constexpr int kPWords = kIO == IO::BF16 ? 16 : 32;  // columns of tensor memory a block of P takes
   static constexpr bool kBf16 = kIO == IO::BF16;
   // columns of tensor memory: in bf16 P takes A's place, and the products with the state's and W's terms side by side
@@ -42,32 +41,13 @@ struct LinSmem {
   static constexpr int kBufs = kIO == IO::BF16 ? 2 : 1;  // of Y and W
   // (in f32 the products take 128 rows of X's 64: what follows it counts as rows whose results nobody reads)
   static constexpr int oX = 0, oY = kX, oW = oY + kBufs * kX, oUp = oW + kBufs * kW, oS = oUp + kUp, oGates = oS + kS;
-  static constexpr int kGates = 16 * kC;                 // (G / ln 2 as two floats, in, up) of the tokens
-  static constexpr int oEnd = oGates + 2 * kGates;       // exp(G_end) of either buffer
+  // of the tokens: G / ln 2 as two floats; in and up; the two factors of P's weights
+  static constexpr int oInUp = 8 * kC, oRow = 16 * kC, oCol = 20 * kC, kGates = 24 * kC;
+  static constexpr int oEnd = oGates + 2 * kGates;       // exp(G_end) of either buffer, and whether the factors serve
   static constexpr int oDiag = oEnd + 16, oBad = oDiag + 4 * kC, oAnyBad = oBad + 2 * 64 * 4;
   static constexpr int oBar = oAnyBad + 16, kBytes = oBar + 64 + 1024;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
-
-struct LinWaiter {
-  const LinArgs& a;
-  volatile int* stop;
-  bool ok = true;
-  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity, bool forced = false) {
-    ok = ok && wait_or_stop(a, stop, bar, parity, forced);
-  }
-};
-
-// Like umma, A in tensor memory: its rows in the lanes, two bf16 to a column.
-__device__ __forceinline__ void umma_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t desc_b, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(desc_b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 __device__ __forceinline__ bool odd_bf16(uint32_t pair) {  // either half NaN or infinite
   return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
@@ -78,8 +58,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   using T = typename IoType<kIO>::type;
   using L = LinSmem<kIO, KP>;
   using G = LinGeo<kIO>;
-  using R = WalkRow<T, 4>;  // 32 columns to a thread
-  using RF = WalkRow<float, 4>;
+  using R = WalkRow<T, 2>;  // 16 columns to a thread
+  using RF = WalkRow<float, 2>;
   constexpr int kC = L::kC, NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, kBufs = L::kBufs;
   constexpr bool kBf16 = kIO == IO::BF16;
   extern __shared__ uint8_t smem_raw[];
@@ -90,6 +70,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   volatile int* stop = reinterpret_cast<int*>(tmem_at + 1);
   volatile int* leave = stop + 1;
   float* s_end = reinterpret_cast<float*>(sm + L::oEnd);
+  int* s_near = reinterpret_cast<int*>(s_end + 2);
   float* s_diag = reinterpret_cast<float*>(sm + L::oDiag);
   int* s_bad = reinterpret_cast<int*>(sm + L::oBad);
   volatile int* any_bad = reinterpret_cast<int*>(sm + L::oAnyBad);
@@ -100,7 +81,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   const int64_t item = blockIdx.x / all_tiles / a.Hv;
   while (which + 1 < roles && tile >= lin_tiles(a.role[which].n2)) tile -= lin_tiles(a.role[which++].n2);
   const LinRole& role = a.role[which];
-  const bool back = role.back != 0;
+  const bool back = role.back != 0, has_dot = role.dot != nullptr;
   if (item >= a.info[kStateOnly ? 1 : 0]) return;
   const int seg = kStateOnly ? a.inner[item] + (back ? 1 : 0) : a.order[item];
   const int4 entry = a.table[seg];
@@ -122,46 +103,49 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
     fence_mbar_init();
   }
   if (t < 128) s_bad[t] = bad_none();
-  if (warp == 8) tmem_alloc<512>(tmem_at);
+  if (warp == kLinCtrl) tmem_alloc<512>(tmem_at);
 
   const float* g_base = a.g + start * a.g_token + h;
-  // warp 8: the gates of chunk c.  Its running sum of g in double: differences of it enter exp.
-  auto make_gates = [&](int c, int buf) -> double {
+  // warp 8: the gates of chunk c; returns the chunk's sum of g over ln 2
+  auto make_gates = [&](int c, int buf) -> Pair {
     constexpr int kPer = kC / 32;
     const int rows = min(kC, len - c * kC);
-    double gs[kPer], incl = 0.0;
+    Pair own[kPer], incl{0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = lane * kPer + i;
       float v = r < rows ? g_base[(int64_t)(c * kC + r) * a.g_token] : 0.0f;
       v = v < -256.0f ? -256.0f : v;  // exp of either is 0; -inf would leave inf - inf
-      incl += (double)v;
-      gs[i] = incl;
+      incl = add(incl, Pair{v, 0.0f});
+      own[i] = incl;
     }
-    const double own = incl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const Pair v{__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
+      if (lane >= o) incl = add(v, incl);
     }
-    const double last = __shfl_sync(0xffffffffu, incl, 31);
-    double before = __shfl_up_sync(0xffffffffu, incl, 1);
-    if (lane == 0) before = 0.0;
-    (void)own;
-    float4* gates = reinterpret_cast<float4*>(sm + L::oGates + buf * L::kGates);
+    const Pair last = over_ln2(Pair{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)});
+    Pair before{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+    if (lane == 0) before = Pair{0.0f, 0.0f};
+    uint8_t* gates = sm + L::oGates + buf * L::kGates;
+    const float mid = 0.5f * last.hi;
+    bool near = true;  // both factors of every weight are normal numbers
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const double Gi = before + gs[i], G2 = Gi * 1.4426950408889634;
-      const float hi = (float)G2, lo = (float)(G2 - (double)hi);
-      const float gh = (float)Gi, dh = (float)(last - Gi);
-      const float from = a.scale * (exp_f(gh) * (1.0f + (float)(Gi - (double)gh)));
-      const float to = exp_f(dh) * (1.0f + (float)(last - Gi - (double)dh));
-      gates[lane * kPer + i] = back ? make_float4(hi, lo, to, from) : make_float4(hi, lo, from, to);
+      const int r = lane * kPer + i;
+      const Pair G = over_ln2(add(before, own[i]));
+      const float from = a.scale * exp2_of(G), to = exp2_of(add(last, Pair{-G.hi, -G.lo}));
+      const Pair d = add(G, Pair{-mid, 0.0f});
+      const float up = exp2_of(d), down = exp2_of(Pair{-d.hi, -d.lo});
+      near = near && fabsf(d.hi) < 120.0f;
+      reinterpret_cast<float2*>(gates)[r] = make_float2(G.hi, G.lo);
+      reinterpret_cast<float2*>(gates + L::oInUp)[r] = back ? make_float2(to, from) : make_float2(from, to);
+      reinterpret_cast<float*>(gates + L::oRow)[r] = a.scale * (back ? down : up);
+      reinterpret_cast<float*>(gates + L::oCol)[r] = back ? up : down;
     }
-    if (lane == 0) {
-      const float lh = (float)last;
-      s_end[buf] = exp_f(lh) * (1.0f + (float)(last - (double)lh));
-    }
+    near = __all_sync(0xffffffffu, near);
+    if (lane == 0) s_near[buf] = near;
+    if (lane == 0) s_end[buf] = exp2_of(last);
     return last;
   };
 
@@ -233,7 +217,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         put(L::oY, y[u]);
         if (!kStateOnly) put(L::oX, x[u]);
       }
-      const float4* gates = reinterpret_cast<const float4*>(sm + L::oGates + buf * L::kGates);
+      const float2* in_up = reinterpret_cast<const float2*>(sm + L::oGates + buf * L::kGates + L::oInUp);
 #pragma unroll
       for (int u = 0; u < kLoadW; ++u) {
         const int r = (t + u * kLinWorkers) / 8, ch = t % 8;
@@ -243,7 +227,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         float2 trace = splat2(0.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          up[i] = mul2(v[i], splat2(gates[r].w));
+          up[i] = mul2(v[i], splat2(in_up[r].y));
           trace = fma2(v[i], splat2(0.0f), trace);
         }
         put_chunk<NT, 128>(sm + L::oUp, L::kPanel, r, ch, up);
@@ -264,7 +248,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   // made NaN when they are written.
   auto weigh = [&](int buf) {
     if constexpr (kBf16) {
-      const float4* gates = reinterpret_cast<const float4*>(sm + L::oGates + buf * L::kGates);
+      const float2* in_up = reinterpret_cast<const float2*>(sm + L::oGates + buf * L::kGates + L::oInUp);
       uint8_t* image = sm + L::oW + buf * L::kW;
 #pragma unroll
       for (int u = 0; u < kC * 8 / kLinWorkers; ++u) {
@@ -274,7 +258,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         float2 v[4];
         unpack(q, v);
         float2 trace = splat2(0.0f);
-        const float f = gates[r].w;
+        const float f = in_up[r].y;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           trace = fma2(v[k], splat2(0.0f), trace);
@@ -295,9 +279,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
     }
   };
 
-  const int quad = warp & 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
-  const int col0 = tile * kLinTile + half * 32;  // this thread's columns of the state and of the results
-  const bool state_row = row < n1 && warp < 8;
+  const int quad = warp & 3, part = (warp >> 2) & (kLinParts - 1), row = quad * 32 + lane;
+  const int col0 = tile * kLinTile + part * 16;  // this thread's columns of the state and of the results
+  const bool state_row = row < n1 && warp < kLinCtrl;
   // the state the segment starts from, if any
   const int64_t state_at = (int64_t)row * role.srow + (int64_t)col0 * role.scol;
   const int64_t state_size = (int64_t)n1 * n2;
@@ -307,12 +291,12 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   } else if (!kStateOnly) {
     carry = role.slots + ((back ? inner_before : inner_before - 1) * a.Hv + h) * state_size;
   }
-  float2 S[16];
+  float2 S[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) S[i] = splat2(0.0f);
+  for (int i = 0; i < 8; ++i) S[i] = splat2(0.0f);
   auto state_io = [&](auto f) {  // f(i, offset) for the pairs i of this thread's columns that exist
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       if (state_row && col0 + 2 * i < n2) f(i, state_at + 2 * i * role.scol);
   };
   if (carry) state_io([&](int i, int64_t at) { S[i] = make_float2(carry[at], carry[at + role.scol]); });
@@ -326,8 +310,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   LinWaiter wait{a, stop};
   auto chunk_of = [&](int k) { return back ? n - 1 - k : k; };
 
-  if (warp == 8) {
-    double total = 0.0;
+  if (warp == kLinCtrl) {
+    Pair total{0.0f, 0.0f};
     if (n > 0) total = make_gates(chunk_of(0), 0);
     if (!kBf16 && n > 0) named_barrier(4, kLinThreads);
     for (int k = 0; k < n; ++k) {
@@ -358,7 +342,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         umma_commit(bar_u);
       }
       __syncwarp();
-      if (k + 1 < n) total += make_gates(chunk_of(k + 1), buf ^ 1);
+      if (k + 1 < n) total = add(total, make_gates(chunk_of(k + 1), buf ^ 1));
       if constexpr (!kStateOnly) {
         named_barrier(3, kLinThreads);
         if (lane == 0 && !*stop) {
@@ -384,10 +368,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
       }
       if (!kBf16 && k + 1 < n) named_barrier(4, kLinThreads);
     }
-    if (kStateOnly && lane == 0 && tile == 0) {
-      const float th = (float)total;
-      role.decay[item * a.Hv + h] = exp_f(th) * (1.0f + (float)(total - (double)th));
-    }
+    if (kStateOnly && lane == 0 && tile == 0) role.decay[item * a.Hv + h] = exp2_of(total);
   } else {
     uint32_t phase = 0;
     if (n > 0) {
@@ -400,7 +381,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
       }
     }
     if (!kStateOnly && has_carry && row < KP * 64)
-      put_row<NT, 128>(sm + L::oS, L::kSTerm, row, half * 4, S);
+      put_row<NT, 128>(sm + L::oS, L::kSTerm, row, part * 2, S);
     for (int k = 0; k < n; ++k, phase ^= 1) {
       const int c = chunk_of(k), buf = k & 1, lb = kBufs == 2 ? buf : 0;
       const int rows = min(kC, len - c * kC);
@@ -414,7 +395,6 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
       if (t < 64) s_bad[(buf ^ 1) * 64 + t] = bad_none();
       if (t == 0) any_bad[buf ^ 1] = 0;
       if (more) load_yw(chunk_of(k + 1), lb ^ 1);
-      const float4* gates = reinterpret_cast<const float4*>(sm + L::oGates + buf * L::kGates);
       weigh(lb);
       fence_async_smem();
       asm volatile("bar.arrive %0, %1;" ::"r"(2), "r"(kLinThreads) : "memory");
@@ -423,30 +403,58 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         wait(bar_a, phase, k == 0 && t == 0 && forced_here(a));
         tmem_fence_after_sync();
         if (row < kC) {
-          const float4 mine = gates[row];
-          const float sign = back ? -1.0f : 1.0f;
+          const uint8_t* gates = sm + L::oGates + buf * L::kGates;
+          const float row_factor = reinterpret_cast<const float*>(gates + L::oRow)[row];
+          // the columns a row sees: fwd j < see, back see <= j < rows
+          const int see = back ? row + (has_dot ? 1 : 0) : row + (has_dot ? 0 : 1);
+          const bool near = s_near[buf];
 #pragma unroll
           for (int u = 0; u < G::kBlocks; ++u) {
-            const int j0 = half * (kC / 2) + 16 * u;
+            // the blocks of a part are one from either end: P is triangular
+            const int block = u == 0 ? part : 2 * kLinParts - 1 - part, j0 = 16 * block;
             uint32_t words[G::kPWords];
 #pragma unroll
             for (int i = 0; i < G::kPWords; ++i) words[i] = 0;
-            if (back ? j0 + 15 >= quad * 32 : j0 <= quad * 32 + 31) {  // the warp has rows that see these columns
-              float d[16];
-              tmem_row(tm + G::tA + lane_at + j0, d);
+            if (back ? j0 + 15 >= quad * 32 && j0 < rows : j0 <= quad * 32 + 31) {  // the warp has rows that see these columns
+              float2 d[8];
+              tmem_sum<1>(tm + G::tA + lane_at + j0, 0, d);
+              const bool all = back ? j0 > quad * 32 + 31 && j0 + 15 < rows : j0 + 15 < quad * 32;
+              if (!all && has_dot) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int j = j0 + i;
-                const float4 gj = gates[j];
-                const float w = ex2(sign * ((mine.x - gj.x) + (mine.y - gj.y))) * a.scale * d[i];
-                if (role.dot && j == row) s_diag[row] = a.scale * d[i];
-                const bool seen = back ? j >= row && j < rows : j <= row;
-                d[i] = seen && !(role.dot && j == row) ? w : 0.0f;
+                for (int i = 0; i < 16; ++i)
+                  if (j0 + i == row) s_diag[row] = a.scale * (i % 2 ? d[i / 2].y : d[i / 2].x);
+              }
+              if (near) {
+                const float4* col = reinterpret_cast<const float4*>(gates + L::oCol) + j0 / 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float4 f = col[i];
+                  d[2 * i] = mul2(d[2 * i], mul2(make_float2(f.x, f.y), splat2(row_factor)));
+                  d[2 * i + 1] = mul2(d[2 * i + 1], mul2(make_float2(f.z, f.w), splat2(row_factor)));
+                }
+              } else {
+                const float2* sums = reinterpret_cast<const float2*>(gates);
+                const float2 mine = sums[row];
+                const float sign = back ? -1.0f : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float2 x = sums[j0 + 2 * i], y = sums[j0 + 2 * i + 1];
+                  d[i].x *= a.scale * ex2(sign * ((mine.x - x.x) + (mine.y - x.y)));
+                  d[i].y *= a.scale * ex2(sign * ((mine.x - y.x) + (mine.y - y.y)));
+                }
+              }
+              if (!all) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int j = j0 + 2 * i;
+                  if (back ? j < see || j >= rows : j >= see) d[i].x = 0.0f;
+                  if (back ? j + 1 < see || j + 1 >= rows : j + 1 >= see) d[i].y = 0.0f;
+                }
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 uint32_t term[NT];
-                split_pair<NT>(make_float2(d[2 * i], d[2 * i + 1]), term);
+                split_pair<NT>(d[i], term);
 #pragma unroll
                 for (int q = 0; q < NT; ++q) words[8 * q + i] = term[q];
               }
@@ -466,50 +474,40 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
       if (more) load_x(chunk_of(k + 1));
       if (row < KP * 64) {
         const float end = s_end[buf];
+        float2 d[8];
+        tmem_sum<kBf16 ? NT : 1>(tm + G::tU + lane_at + part * 16, 64, d);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float2 d[8];
-          tmem_sum<kBf16 ? NT : 1>(tm + G::tU + lane_at + half * 32 + 16 * u, 64, d);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) S[8 * u + i] = d[i] = fma2(splat2(end), S[8 * u + i], d[i]);
-          if (!kStateOnly && more) put_row<NT, 128>(sm + L::oS, L::kSTerm, row, half * 4 + 2 * u, d);
-        }
+        for (int i = 0; i < 8; ++i) S[i] = fma2(splat2(end), S[i], d[i]);
+        if (!kStateOnly && more) put_row<NT, 128>(sm + L::oS, L::kSTerm, row, part * 2, S);
       }
 
       if constexpr (!kStateOnly) {
         wait(bar_o, phase);
         tmem_fence_after_sync();
         if (row < kC) {
-          const float in = gates[row].z;
           const int64_t at = (int64_t)c * kC + quad * 32;  // the warp's first token
-          float2 o[16];
+          float2 o[8];
+          tmem_sum<1>(tm + G::tO + lane_at + part * 16, 0, o);
+          if (has_state) {
+            const float in = reinterpret_cast<const float2*>(sm + L::oGates + buf * L::kGates + L::oInUp)[row].x;
+            float2 e[8];
+            tmem_sum<kBf16 ? NT : 1>(tm + G::tD1 + lane_at + part * 16, 64, e);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float2 d[8];
-            tmem_sum<1>(tm + G::tO + lane_at + half * 32 + 16 * u, 0, d);
-            if (has_state) {
-              float2 e[8];
-              tmem_sum<kBf16 ? NT : 1>(tm + G::tD1 + lane_at + half * 32 + 16 * u, 64, e);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) d[i] = fma2(splat2(in), e[i], d[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[8 * u + i] = d[i];
+            for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(in), e[i], o[i]);
           }
-          if (role.dot) {  // rho or sigma, then the token's own pair
+          if (has_dot) {  // rho or sigma, then the token's own pair
             typename R::Raw raw;
             R::load(static_cast<const T*>(role.dot) + (start + at) * role.sdot + (int64_t)(h / role.rdot) * n2 + col0, role.sdot,
                     len - at, n2 - col0, lane, raw);
 #pragma unroll
             for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
             float2 sum = splat2(0.0f);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) R::each(raw, u, [&](int i, float2 y) { sum = fma2(y, o[8 * u + i], sum); });
-            if (row < rows) role.dots[((int64_t)(tile * 2 + half) * a.T + start + at + lane) * a.Hv + h] = sum.x + sum.y;
+            R::each(raw, 0, [&](int i, float2 y) { sum = fma2(y, o[i], sum); });
+            if (row < rows) role.dots[((int64_t)(tile * kLinParts + part) * a.T + start + at + lane) * a.Hv + h] = sum.x + sum.y;
             const float self = s_diag[row];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t place = image_chunk<128>(row, half * 4 + q);
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t place = image_chunk<128>(row, part * 2 + q);
 #pragma unroll
               for (int term = NQ - 1; term >= 0; --term) {
                 float2 w[4];
@@ -521,9 +519,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
           }
           if (any_bad[buf]) {
             const float nan = __int_as_float(0x7fffffff);
-            const int* bad = s_bad + buf * 64 + half * 32;
+            const int* bad = s_bad + buf * 64 + part * 16;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               if (back ? row <= bad[2 * i] : row >= bad[2 * i]) o[i].x = nan;
               if (back ? row <= bad[2 * i + 1] : row >= bad[2 * i + 1]) o[i].y = nan;
             }
@@ -532,13 +530,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
           auto store = [&](auto rows_of, auto* base) {
             using Q = decltype(rows_of);
             typename Q::Raw raw;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float2 d[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) d[i] = o[8 * u + i];
-              Q::put(raw, u, d);
-            }
+            Q::put(raw, 0, o);
             Q::store(base + out_at, (int64_t)a.Hv * n2, len - at, n2 - col0, lane, raw);
           };
           if (kBf16 && role.part) store(RF(), static_cast<float*>(role.out));
@@ -569,19 +561,19 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
       float v = sum.x + sum.y;
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      float* part = reinterpret_cast<float*>(sm + L::oGates);  // the gates are not needed any more
+      float* sums = reinterpret_cast<float*>(sm + L::oGates);  // the gates are not needed any more
       named_barrier(5, kLinWorkers);
-      if (lane == 0) part[warp] = v;
+      if (lane == 0) sums[warp] = v;
       named_barrier(5, kLinWorkers);
       if (t == 0) {
-        for (int i = 1; i < 8; ++i) v += part[i];
+        for (int i = 1; i < kLinCtrl; ++i) v += sums[i];
         role.cross[((int64_t)seg * a.Hv + h) * tiles + tile] = v;
       }
     }
   }
   tmem_fence_before_sync();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kLinCtrl) {
     if (lane == 0 && *stop) {  // products that were not waited for
       umma_commit(drained);
       mbar_wait(drained, 0, kCopyDrainNs);
@@ -613,9 +605,9 @@ cudaError_t pick_walk(const LinArgs& a, int roles, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_lin_walk(const LinArgs& a, int roles, bool state_only, IO io, cudaStream_t st) {
+cudaError_t launch_lin_walk(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, IO io, cudaStream_t st) {
+  if (io == IO::BF16) return launch_lin_walk_bf16(a, maps, roles, state_only, st);
   if ((state_only ? a.max_inner : a.max_segs) == 0) return cudaSuccess;
-  if (io == IO::BF16) return state_only ? pick_walk<IO::BF16, true>(a, roles, st) : pick_walk<IO::BF16, false>(a, roles, st);
   return state_only ? pick_walk<IO::F32, true>(a, roles, st) : pick_walk<IO::F32, false>(a, roles, st);
 }
 

@@ -32,6 +32,8 @@
 // scan over a sequence's segments adds them up.
 #pragma once
 
+#include <cuda.h>
+
 #include "kernels.h"
 
 namespace vssm {
@@ -39,7 +41,12 @@ namespace vssm {
 constexpr int kLinTile = 64;   // columns of the state that a CTA walks
 constexpr int kLinMaxK = 128, kLinMaxV = 128;
 constexpr int kLinRoles = 3;
+constexpr int kLinParts = 4;   // threads to a row, 16 columns of the tile each
 
+// CTAs that share the columns of a state: in bf16 one walks them all.
+inline int lin_ctas(IO io, int n2) { return io == IO::BF16 ? 1 : (n2 + kLinTile - 1) / kLinTile; }
+// Parts that rho and sigma come in: the threads that share a row.
+inline int lin_dot_parts(IO io, int n2) { return io == IO::BF16 ? 2 : kLinParts * lin_ctas(io, n2); }
 inline int lin_chunk(IO io) { return io == IO::BF16 ? 128 : 64; }  // tokens
 __host__ __device__ inline int lin_tiles(int n) { return (n + kLinTile - 1) / kLinTile; }
 
@@ -49,12 +56,13 @@ struct LinRole {
   int64_t sx, sy, sw;
   int rx, ry, rw;          // value heads that share a head of each
   int n1, n2;              // widths of x and y, and of w
+  int mx, my, mw;          // bf16: their tensor maps
   void* out;               // contiguous (T, Hv, n2), io or, where part, f32; null: the state only
   int part;
   const void* dot;         // rho's or sigma's partner rows, or null
   int64_t sdot;
   int rdot;
-  float* dots;             // (2 tiles, T, Hv)
+  float* dots;             // (lin_dot_parts, T, Hv)
   int back;                // reversed time
   int64_t srow, scol;      // a state's element (row of n1, column of n2) in memory
   const float* first;      // states that the sequences come with, (S, Hv, ., .), or null
@@ -63,7 +71,7 @@ struct LinRole {
   float* decay;            // (inner segments, Hv): exp of the segment's sum of g (the state-only walks write it)
   const float* against;    // gradient of the state at a segment's end, as `slots` and `first` of a reversed role
   const float* against_last;
-  float* cross;            // (segments, Hv, tiles): its product with that state
+  float* cross;            // (segments, Hv, lin_ctas): its product with that state
 };
 
 struct LinArgs {
@@ -91,14 +99,19 @@ struct LinArgs {
   unsigned long long wait_ns;
   long long force_timeout_cta;
 };
+// The tensor maps of the calls' bf16 rows: (width, heads, tokens), boxes of 64 x 1 x 128.
+struct LinMaps {
+  CUtensorMap m[4];
+};
 // A table entry's w: flags and, above them, the inner segments before it.
 constexpr int kLinFirst = 1, kLinLast = 2, kLinPlaceShift = 2;
 
 cudaError_t launch_lin_plan(const LinArgs& a, cudaStream_t st);
 // state_only: the inner segments of roles [0, roles), otherwise all segments.
-cudaError_t launch_lin_walk(const LinArgs& a, int roles, bool state_only, IO io, cudaStream_t st);
+cudaError_t launch_lin_walk(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, IO io, cudaStream_t st);
+cudaError_t launch_lin_walk_bf16(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, cudaStream_t st);
 cudaError_t launch_lin_scan(const LinArgs& a, int roles, cudaStream_t st);
-cudaError_t launch_lin_dg(const LinArgs& a, cudaStream_t st);
+cudaError_t launch_lin_dg(const LinArgs& a, IO io, cudaStream_t st);
 cudaError_t launch_lin_head_sum(const LinArgs& a, IO io, cudaStream_t st);
 
 struct LinStepArgs {

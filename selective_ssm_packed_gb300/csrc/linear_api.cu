@@ -18,8 +18,8 @@ int check_lin_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
 // no shorter than two chunks, which the walks before and the scan would cost
 // more than they bring, and no longer than 4096 tokens, whose states are 3% of
 // the data and over which dg's sums run.
-int lin_segment(int64_t T, int Hv, int tiles, IO io) {
-  const int64_t chunk = lin_chunk(io), share = T * Hv * tiles / (152 * 4);
+int lin_segment(int64_t T, int Hv, int ctas, IO io) {
+  const int64_t chunk = lin_chunk(io), share = T * Hv * ctas / (152 * 4);
   int64_t seg = (share + chunk - 1) / chunk * chunk;
   seg = seg < 2 * chunk ? 2 * chunk : seg > 4096 ? 4096 : seg;
   return (int)seg;
@@ -34,7 +34,7 @@ struct LinLayout {
 
 LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, bool bwd) {
   LinLayout l;
-  const int tk = lin_tiles(K), tv = lin_tiles(V);
+  const int tk = lin_ctas(io, K), tv = lin_ctas(io, V);
   l.seg = lin_segment(T, Hv, bwd ? 2 * tk + tv : tv, io);
   l.max_inner = T > l.seg ? T / l.seg : 0;
   l.max_segs = T / l.seg + S;
@@ -50,8 +50,8 @@ LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, 
   const size_t tokens = (size_t)T * Hv * sizeof(float);
   l.slots_back = o; o += up(inner * state);
   l.decay_back = o; o += up(inner * Hv * sizeof(float));
-  l.rho = o; o += up(2 * tk * tokens);
-  l.sigma = o; o += up(2 * tv * tokens);
+  l.rho = o; o += up(lin_dot_parts(io, K) * tokens);
+  l.sigma = o; o += up(lin_dot_parts(io, V) * tokens);
   l.cross = o; o += up(segs * Hv * tk * sizeof(float));
   l.seg_dg = o; o += up(segs * Hv * sizeof(double));
   l.dq_part = o; o += Hk == Hv ? 0 : up(tokens * K);
@@ -94,6 +94,12 @@ LinArgs lin_args(const float* g, int32_t g_per_token, float scale, const int32_t
   a.wait_ns = debug_knobs().wait_ns;
   a.force_timeout_cta = debug_knobs().force_copy_timeout;
   return a;
+}
+
+// rows (T, H, n) of bf16, their tokens `stride` apart
+int lin_map(CUtensorMap* m, const void* base, int64_t T, int H, int n, int64_t stride, IO io) {
+  if (io != IO::BF16 || T == 0) return VSSM_OK;
+  return encode_heads_map(m, base, T, H, n, stride, 64, 128);
 }
 
 int check_lin_inputs(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
@@ -178,10 +184,15 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
   r.srow = V; r.scol = 1; r.first = initial_states; r.last = final_states;
   r.slots = reinterpret_cast<float*>(p + l.slots);
   r.decay = reinterpret_cast<float*>(p + l.decay);
+  r.mx = 0; r.my = 1; r.mw = 2;
+  LinMaps maps{};
+  TRY(lin_map(maps.m + 0, q, T, Hk, K, q_stride, io));
+  TRY(lin_map(maps.m + 1, k, T, Hk, K, k_stride, io));
+  TRY(lin_map(maps.m + 2, v, T, Hv, V, v_stride, io));
   TRY(check(launch_lin_plan(a, st), "linear attention plan launch"));
-  TRY(check(launch_lin_walk(a, 1, true, io, st), "linear attention state launch"));
+  TRY(check(launch_lin_walk(a, maps, 1, true, io, st), "linear attention state launch"));
   TRY(check(launch_lin_scan(a, 1, st), "linear attention scan launch"));
-  TRY(check(launch_lin_walk(a, 1, false, io, st), "linear attention forward launch"));
+  TRY(check(launch_lin_walk(a, maps, 1, false, io, st), "linear attention forward launch"));
   const void* outs[] = {out, final_states};
   const int64_t counts[] = {T * Hv * V, (int64_t)num_seqs * Hv * K * V};
   const bool f32[] = {io == IO::F32, true};
@@ -222,6 +233,11 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   a.dq = dq; a.dk = dk;
   a.dq_part = reinterpret_cast<float*>(p + l.dq_part);
   a.dk_part = reinterpret_cast<float*>(p + l.dk_part);
+  LinMaps maps{};
+  TRY(lin_map(maps.m + 0, q, T, Hk, K, q_stride, io));
+  TRY(lin_map(maps.m + 1, k, T, Hk, K, k_stride, io));
+  TRY(lin_map(maps.m + 2, v, T, Hv, V, v_stride, io));
+  TRY(lin_map(maps.m + 3, dout, T, Hv, V, so, io));
   TRY(check(launch_lin_plan(a, st), "linear attention plan launch"));
 
   LinArgs s = a;  // the states before the segments and their gradients behind them
@@ -229,11 +245,13 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   fs.y = k; fs.w = v; fs.sy = k_stride; fs.sw = v_stride; fs.rx = 1; fs.ry = rep; fs.rw = 1; fs.n1 = K; fs.n2 = V;
   fs.srow = V; fs.scol = 1; fs.first = initial_states; fs.slots = slots;
   fs.decay = reinterpret_cast<float*>(p + l.decay);
+  fs.my = 1; fs.mw = 2;
   LinRole& bs = s.role[1];
   bs = fs;
   bs.y = q; bs.w = dout; bs.sy = q_stride; bs.sw = so; bs.back = 1; bs.first = d_final_states; bs.slots = slots_back;
   bs.decay = reinterpret_cast<float*>(p + l.decay_back);
-  TRY(check(launch_lin_walk(s, 2, true, io, st), "linear attention state launch"));
+  bs.my = 0; bs.mw = 3;
+  TRY(check(launch_lin_walk(s, maps, 2, true, io, st), "linear attention state launch"));
   TRY(check(launch_lin_scan(s, 2, st), "linear attention scan launch"));
 
   LinRole& rq = a.role[0];
@@ -250,13 +268,16 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   rk.rx = rk.ry = 1; rk.rw = rep; rk.n1 = V; rk.n2 = K;
   rk.out = rep > 1 ? a.dk_part : dk; rk.part = rep > 1; rk.back = 1;
   rk.srow = 1; rk.scol = V; rk.first = d_final_states; rk.slots = slots_back;
+  rq.mx = 3; rq.my = 2; rq.mw = 1;
+  rv.mx = 1; rv.my = 0; rv.mw = 3;
+  rk.mx = 2; rk.my = 3; rk.mw = 0;
   if (dg) {
     rq.dot = q; rq.sdot = q_stride; rq.rdot = rep; rq.dots = reinterpret_cast<float*>(p + l.rho);
     rq.against = slots_back; rq.against_last = d_final_states; rq.cross = reinterpret_cast<float*>(p + l.cross);
     rv.dot = v; rv.sdot = v_stride; rv.rdot = 1; rv.dots = reinterpret_cast<float*>(p + l.sigma);
   }
-  TRY(check(launch_lin_walk(a, 3, false, io, st), "linear attention backward launch"));
-  if (dg) TRY(check(launch_lin_dg(a, st), "linear attention decay gradient launch"));
+  TRY(check(launch_lin_walk(a, maps, 3, false, io, st), "linear attention backward launch"));
+  if (dg) TRY(check(launch_lin_dg(a, io, st), "linear attention decay gradient launch"));
   if (rep > 1) TRY(check(launch_lin_head_sum(a, io, st), "linear attention head sum launch"));
   const void* outs[] = {dq, dk, dv, dg, d_initial_states};
   const int64_t counts[] = {T * Hk * K, T * Hk * K, T * Hv * V, dg ? (g_per_token ? T * Hv : Hv) : 0,

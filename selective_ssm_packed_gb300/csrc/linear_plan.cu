@@ -1,7 +1,6 @@
 // linear_plan.cu -- linear attention: the plan of a pack, the scan over a
 // sequence's segments, the decays' gradient, and the sum over shared heads.
-#include "delta.cuh"
-#include "linear.h"
+#include "linear.cuh"
 
 namespace vssm {
 namespace {
@@ -137,50 +136,57 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs a, int blocks) {
 }
 
 // ------------------------------------------------------------------ gradient of the decays
-// One CTA per (segment, 32 heads or the power of two that holds them): lanes
-// along the heads, the others along stretches of the segment's tokens, each
-// summed up first and then walked from its end.  Sums in double: a token's dg
-// is the sum of all later differences, in which most cancels.
-__global__ void __launch_bounds__(256) lin_dg_kernel(LinArgs a, int lanes, int parts_q, int parts_v, int tiles) {
-  __shared__ double sums[256];
+// One CTA per (segment, kDgHeads heads): a thread has one head and a stretch of
+// the segment's tokens, which it sums up first and then walks from its end.
+// Sums are of two floats: a token's dg is the sum of all later differences, in
+// which most cancels.
+constexpr int kDgHeads = 8, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads;
+
+__global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts_q, int parts_v, int tiles) {
+  __shared__ Pair sums[2][kDgThreads];
   const int seg = blockIdx.x;
   if (seg >= a.info[0]) return;
   const int4 entry = a.table[seg];
-  const int hl = threadIdx.x % lanes, part = threadIdx.x / lanes, parts = 256 / lanes;
-  const int h = blockIdx.y * lanes + hl;
+  const int t = threadIdx.x, part = t / kDgHeads, h = blockIdx.y * kDgHeads + t % kDgHeads;
   const bool in = h < a.Hv;
-  const int per = (entry.z + parts - 1) / parts, lo = min(entry.z, part * per), hi = min(entry.z, lo + per);
+  const int per = (entry.z + kDgParts - 1) / kDgParts, lo = min(entry.z, part * per), hi = in ? min(entry.z, lo + per) : lo;
   const float *rho = a.role[0].dots, *sigma = a.role[1].dots;
+  const int64_t plane = a.T * a.Hv;
   auto diff = [&](int i) {
     const int64_t at = ((int64_t)entry.y + i) * a.Hv + h;
-    double v = 0.0;
-    for (int p = 0; p < parts_q; ++p) v += (double)rho[(int64_t)p * a.T * a.Hv + at];
-    for (int p = 0; p < parts_v; ++p) v -= (double)sigma[(int64_t)p * a.T * a.Hv + at];
+    Pair v{0.0f, 0.0f};
+    for (int p = 0; p < parts_q; ++p) v = add(v, Pair{rho[p * plane + at], 0.0f});
+    for (int p = 0; p < parts_v; ++p) v = add(v, Pair{-sigma[p * plane + at], 0.0f});
     return v;
   };
-  double own = 0.0;
-  if (in)
-    for (int i = lo; i < hi; ++i) own += diff(i);
-  sums[threadIdx.x] = own;
+  Pair own{0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = hi - 1; i >= lo; --i) own = add(own, diff(i));
+  sums[0][t] = own;
   __syncthreads();
-  double run = 0.0, total = 0.0;
-  if (in) {
-    for (int t = 0; t < tiles; ++t) run += (double)a.role[0].cross[((int64_t)seg * a.Hv + h) * tiles + t];
-    for (int p = parts - 1; p > part; --p) run += sums[p * lanes + hl];
-    for (int i = hi - 1; i >= lo; --i) {
-      run += diff(i);
-      if (a.g_token) a.dg[((int64_t)entry.y + i) * a.Hv + h] = (float)run;
-      total += run;
-    }
+  int from = 0;  // the sums over this part and the next 1, 3, 7, ..
+  for (int o = 1; o < kDgParts; o *= 2, from ^= 1) {
+    sums[from ^ 1][t] = part + o < kDgParts ? add(sums[from][t], sums[from][t + o * kDgHeads]) : sums[from][t];
+    __syncthreads();
+  }
+  Pair run = part + 1 < kDgParts ? sums[from][t + kDgHeads] : Pair{0.0f, 0.0f}, total{0.0f, 0.0f};
+  if (in)
+    for (int i = 0; i < tiles; ++i) run = add(run, Pair{a.role[0].cross[((int64_t)seg * a.Hv + h) * tiles + i], 0.0f});
+#pragma unroll 4
+  for (int i = hi - 1; i >= lo; --i) {
+    run = add(run, diff(i));
+    if (a.g_token) a.dg[((int64_t)entry.y + i) * a.Hv + h] = run.hi + run.lo;
+    else total = add(total, run);
   }
   if (a.g_token) return;
   __syncthreads();
-  sums[threadIdx.x] = total;
+  sums[0][t] = total;
   __syncthreads();
-  if (in && part == 0) {
-    for (int p = 1; p < parts; ++p) total += sums[p * lanes + hl];
-    a.seg_dg[(int64_t)seg * a.Hv + h] = total;
+  for (int o = kDgParts / 2; o >= 1; o /= 2) {
+    if (part < o) sums[0][t] = add(sums[0][t], sums[0][t + o * kDgHeads]);
+    __syncthreads();
   }
+  if (in && part == 0) a.seg_dg[(int64_t)seg * a.Hv + h] = (double)sums[0][t].hi + (double)sums[0][t].lo;
 }
 
 // One decay a head: the segments' sums, in order.
@@ -234,12 +240,10 @@ cudaError_t launch_lin_scan(const LinArgs& a, int roles, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_lin_dg(const LinArgs& a, cudaStream_t st) {
-  int lanes = 1;
-  while (lanes < 32 && lanes < a.Hv) lanes *= 2;
+cudaError_t launch_lin_dg(const LinArgs& a, IO io, cudaStream_t st) {
   if (a.max_segs > 0)
-    lin_dg_kernel<<<dim3((unsigned)a.max_segs, (unsigned)((a.Hv + lanes - 1) / lanes)), 256, 0, st>>>(
-        a, lanes, 2 * lin_tiles(a.K), 2 * lin_tiles(a.V), lin_tiles(a.K));
+    lin_dg_kernel<<<dim3((unsigned)a.max_segs, (unsigned)((a.Hv + kDgHeads - 1) / kDgHeads)), kDgThreads, 0, st>>>(
+        a, lin_dot_parts(io, a.K), lin_dot_parts(io, a.V), lin_ctas(io, a.K));
   if (!a.g_token) lin_dg_head_kernel<<<(unsigned)((a.Hv + 31) / 32), 256, 0, st>>>(a);
   return cudaGetLastError();
 }

@@ -6,12 +6,48 @@
 
 namespace vssm {
 
+// The waits of a role of a CTA: as wait_or_stop, in a loop that takes little
+// code, of which these kernels' many roles have much: instructions that have to
+// be fetched again cost the walk more than any other stall.  After one that has
+// run out (ok is false then) the role waits for nothing any more.
+// A try sleeps until the phase is over, or for about a microsecond.
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+
+static __device__ __noinline__ bool lin_wait(const LinArgs& a, volatile int* stop, uint64_t* bar, uint32_t parity, bool forced) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_sleep_wait(bar, parity)) {
+      if (!forced) return true;
+      break;
+    }
+    if (i & 15) continue;
+    if (*stop) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > a.wait_ns) break;
+  }
+  *stop = 1;
+  atomicOr(a.status, kStatusTmaTimeout);
+  return false;
+}
+
 struct LinWaiter {
   const LinArgs& a;
   volatile int* stop;
   bool ok = true;
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity, bool forced = false) {
-    ok = ok && wait_or_stop(a, stop, bar, parity, forced);
+    if (ok && (forced || !mbar_try_wait(bar, parity))) ok = lin_wait(a, stop, bar, parity, forced);
   }
 };
 
@@ -23,6 +59,31 @@ __device__ __forceinline__ void umma_ta(uint32_t tmem_d, uint32_t tmem_a, uint64
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
       "r"(tmem_a), "l"(desc_b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same instructions, issued by the lane for which `lead` holds of a warp
+// that goes through them together: the operands then come from the uniform
+// registers that the instruction takes them from, where a lane by itself would
+// move each of them there (a step took 110 cycles to issue, of 64 that it runs).
+__device__ __forceinline__ void umma_if(bool lead, uint32_t tmem_d, uint64_t desc_a, uint64_t desc_b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(desc_a), "l"(desc_b), "r"(idesc), "r"(accumulate), "r"(lead ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ta_if(bool lead, uint32_t tmem_d, uint32_t tmem_a, uint64_t desc_b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(desc_b), "r"(idesc), "r"(accumulate), "r"(lead ? 1u : 0u)
       : "memory");
 }
 
@@ -51,29 +112,24 @@ __device__ __forceinline__ float exp2_of(Pair x) {
   return x.hi > -126.0f && x.hi < 128.0f ? fmaf(p, x.lo * 0.6931471805599453f, p) : p;
 }
 
-// A chunk's running sums of g over ln 2, a lane's tokens, and the sum over all.
-template <int kPer>
-struct GateSums {
-  Pair G[kPer], last;
-  __device__ __forceinline__ GateSums(const float (&g)[kPer], int lane) {
-    Pair incl{0.0f, 0.0f};
+// exp of either is 0; -inf would leave inf - inf
+__device__ __forceinline__ float clamp_g(float g) { return g < -256.0f ? -256.0f : g; }
+
+// The sum of g before a lane's four tokens of a chunk of 128, and over all of them, that one over ln 2.
+__device__ __forceinline__ Pair running_sums(const float (&g)[4], int lane, Pair& last) {
+  Pair incl{0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float v = g[i] < -256.0f ? -256.0f : g[i];  // exp of either is 0; -inf would leave inf - inf
-      G[i] = incl = add(incl, Pair{v, 0.0f});
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const Pair v{__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
-      if (lane >= o) incl = add(v, incl);
-    }
-    last = over_ln2(Pair{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)});
-    Pair before{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
-    if (lane == 0) before = Pair{0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) G[i] = over_ln2(add(before, G[i]));
+  for (int i = 0; i < 4; ++i) incl = add(incl, Pair{clamp_g(g[i]), 0.0f});
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair v{__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
+    if (lane >= o) incl = add(v, incl);
   }
-};
+  last = over_ln2(Pair{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)});
+  Pair before{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+  if (lane == 0) before = Pair{0.0f, 0.0f};
+  return before;
+}
 __device__ __forceinline__ Pair minus(Pair a) { return Pair{-a.hi, -a.lo}; }
 
 }  // namespace vssm

@@ -14,13 +14,16 @@ int check_lin_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
   return VSSM_OK;
 }
 
-// Tokens of a segment: about four for each SM, so that they fill the GPU, but
-// no shorter than two chunks, which the walks before and the scan would cost
-// more than they bring, and no longer than 4096 tokens, whose states are 3% of
-// the data and over which dg's sums run.
-int lin_segment(int64_t T, int Hv, int ctas, IO io) {
-  const int64_t chunk = lin_chunk(io), share = T * Hv * ctas / (152 * 4);
-  int64_t seg = (share + chunk - 1) / chunk * chunk;
+// Tokens of a segment, at most 4096 (whose state is 3% of the data, and over
+// which dg's sums run).  An SM has `share` tokens to walk; where no sequence is
+// likely to be longer than that (the longest is taken for four times the mean:
+// only the GPU knows it) they are better left whole, which spares the walk
+// before and the scan; otherwise a quarter of it each fills the GPU evenly, but
+// no fewer than two chunks.
+int lin_segment(int64_t T, int64_t S, int Hv, int ctas, IO io) {
+  const int64_t chunk = lin_chunk(io), share = T * Hv * ctas / 152, longest = 4 * T / (S > 0 ? S : 1);
+  if (longest <= share) return 4096;
+  int64_t seg = (share / 4 + chunk - 1) / chunk * chunk;
   seg = seg < 2 * chunk ? 2 * chunk : seg > 4096 ? 4096 : seg;
   return (int)seg;
 }
@@ -35,7 +38,7 @@ struct LinLayout {
 LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, bool bwd) {
   LinLayout l;
   const int tk = lin_ctas(io, K), tv = lin_ctas(io, V);
-  l.seg = lin_segment(T, Hv, bwd ? 2 * tk + tv : tv, io);
+  l.seg = lin_segment(T, S, Hv, bwd ? 2 * tk + tv : tv, io);
   l.max_inner = T > l.seg ? T / l.seg : 0;
   l.max_segs = T / l.seg + S;
   const size_t segs = (size_t)l.max_segs, inner = (size_t)l.max_inner, state = (size_t)Hv * K * V * sizeof(float);

@@ -17,19 +17,30 @@ namespace {
 // through the products, so each has warps of its own, and one thread issues the
 // products, one the copies and one warp makes the gates; every hand-over is an
 // mbarrier, and each phase of one is a chunk.
-constexpr int kC = 128, kPathWarps = 8, kProducts = 16, kCopies = 17, kGatesWarp = 18, kWarps = 20;
+constexpr int kC = 128, kStateWarps = 8, kOutWarps = 8, kParts = kOutWarps / 4;
+constexpr int kProducts = kStateWarps + kOutWarps, kCopies = kProducts + 1, kGatesWarp = kProducts + 2, kWarps = kProducts + 4;
 constexpr int kPanel = kC * 128;  // bytes of 64 columns of a chunk's rows
+constexpr int kStep = 16 * 128;   // bytes of 16 rows, a step of a product over the rows
 
-enum Bar : int { kFullX, kFullY, kFullW, kGatesFull, kGatesFree, kUpReady, kStateReady, kPReady, kOutDone, kDoneA, kDoneX, kDoneU, kDoneO, kDrained, kBars };
+enum Bar : int { kFullX, kFullY, kFullW, kFullW2, kGatesFull, kGatesFree, kUpReady, kStateReady, kPReady, kOutDone, kDoneA, kDoneX, kDoneU, kDoneO, kDrained, kBars };
 
 template <int KP, int NP>  // panels of 64 columns of X and Y, and of W
 struct WalkSmem {
   static constexpr int kX = KP * kPanel, kW = NP * kPanel, kUp = 2 * kW, kSBlock = KP * 8192, kSTerm = NP * kSBlock;
   static constexpr int oX = 0, oY = kX, oW = 2 * kX, oUp = oW + kW, oS = oUp + kUp, oGates = oS + 2 * kSTerm;
-  static constexpr int oDiag = oGates + 4 * 4 * kC, oMisc = oDiag + 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
+  // W's second buffer: where nothing else is left, the place of S's second term, which only rows with a dot product use
+  static constexpr bool kRoom = KP == 1 || NP == 1;
+  static constexpr int oW2 = kRoom ? oGates : oS + kSTerm, oTokens = kRoom ? oGates + kW : oGates;
+  static_assert(kRoom || kSTerm == kW, "");
+  static constexpr int oDiag = oTokens + 4 * 4 * kC, oMisc = oDiag + 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 constexpr int tA = 0, tD1 = 128, tU = 256, tO = 384;  // columns of tensor memory
+
+// S in tensor memory is left undecayed, in a unit that shrinks with the sum of
+// g, until that is down to 2^-kFar, which leaves the rest of a float's range to
+// the values; it is read and written for its decay no more often than that.
+constexpr float kFar = 48.0f;
 
 struct Segment {
   int64_t start, inner_before;
@@ -49,52 +60,140 @@ __device__ __forceinline__ void copy_panels(const CUtensorMap* map, uint8_t* to,
         : "memory");
 }
 
+// The warps of a path wait at a barrier for one that waits for the mbarrier:
+// two dozen that ask for its phase keep the others from their work.
+
 // A warp's arrival, behind what all its lanes wrote.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Up * W as images of two terms from W's image, by kThreads threads.  Rows past
-// the segment, which the copies fill with another's, become zero in W too.  A
-// value of W that is not finite reaches the state, and so every later row,
-// through up * W; in D2, where 0 times it would reach earlier rows, 0 takes its
-// place in W, and *odd has the rows it should reach made NaN when they are written.
-template <int NP, int kThreads>
-__device__ __forceinline__ void weigh(uint8_t* w_image, uint8_t* up_image, const float* up, int rows, int t, volatile int* odd) {
-#pragma unroll 2
-  for (int u = 0; u < kC * NP * 8 / kThreads; ++u) {
-    const int i = t + u * kThreads, r = i / (NP * 8), ch = i % (NP * 8);
-    uint4* at = reinterpret_cast<uint4*>(w_image + (ch >> 3) * kPanel + image_chunk<128>(r, ch & 7));
-    uint4 q = *at;
-    if (r >= rows) {
-      q = make_uint4(0, 0, 0, 0);
-      if (odd) *at = q;
+// 16 columns each from two places of this thread's lane, on their way together.
+__device__ __forceinline__ void load_two(uint32_t from0, uint32_t from1, float2 (&v)[2][8]) {
+  uint32_t w[2][16];
+  __syncwarp();
+  tmem_ld16(from0, w[0]);
+  tmem_ld16(from1, w[1]);
+  tmem_wait_ld16(w[0]);
+  tmem_wait_ld16(w[1]);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = make_float2(__uint_as_float(w[u][2 * i]), __uint_as_float(w[u][2 * i + 1]));
+}
+
+// kCols columns of this thread's row of S, times `decay`.
+template <int kCols>
+__device__ __noinline__ void decay_state(uint32_t at, float decay) {
+#pragma unroll 1
+  for (int u = 0; u < kCols / 16; ++u) {
+    uint32_t w[16];
+    __syncwarp();
+    tmem_ld16(at + 16 * u, w);
+    tmem_wait_ld16(w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * decay);
+    tmem_st16(at + 16 * u, w);
+  }
+  tmem_wait_st();
+}
+
+// Whether 16 values of every row of every head lie on 32-byte boundaries.
+__device__ __forceinline__ bool whole_rows(const void* base, int64_t stride, int n) {
+  return ((reinterpret_cast<uintptr_t>(base) | (uintptr_t)(2 * stride) | (uintptr_t)(2 * n)) & 31) == 0;
+}
+
+// 16 bf16 values of a row, of which `cols` exist (a multiple of 8): a sector, read and written at once where it is
+// one, so that a warp's access of 32 rows touches each of its sectors once.
+struct Row16 {
+  uint32_t v[8];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int cols, bool whole) {
+    if (whole && cols >= 16) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                   : "l"(p));
+      return;
     }
-    float2 v[4];
-    unpack(q, v);
-    float2 trace = splat2(0.0f);
-    const float f = up[r];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 q = 8 * i < cols ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+      v[4 * i] = q.x;
+      v[4 * i + 1] = q.y;
+      v[4 * i + 2] = q.z;
+      v[4 * i + 3] = q.w;
+    }
+  }
+  __device__ __forceinline__ void store_whole(__nv_bfloat16* p) const {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int cols, bool whole) const {
+    if (whole && cols >= 16) {
+      store_whole(p);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (8 * i < cols) reinterpret_cast<uint4*>(p)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+  __device__ __forceinline__ float2 get(int i) const { return make_float2(bf16_lo(v[i]), bf16_hi(v[i])); }
+  __device__ __forceinline__ void put(int i, float2 x) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    v[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// 0 in the place of what is not finite, in `count` chunks `step` bytes apart.
+__device__ __noinline__ void clear_odd(uint8_t* at, int step, int count) {
+  for (int u = 0; u < count; ++u)
+    for (int k = 0; k < 4; ++k) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(at + u * step) + k;
+      if ((*p & 0x7f80u) == 0x7f80u) *p &= 0xffff0000u;
+      if ((*p & 0x7f800000u) == 0x7f800000u) *p &= 0xffffu;
+    }
+}
+
+// Up * W as images of two terms from W's image, by kThreads threads, each along
+// a column of 16-byte chunks whose place in the swizzle is the same in all its
+// rows.  A value of W that is not finite reaches the state, and so every later
+// row, through up * W; in D2, where 0 times it would reach earlier rows, 0 takes
+// its place in W, and *odd has the rows it should reach made NaN when they are
+// written.
+template <int NP, int kThreads>
+__device__ __forceinline__ void weigh(uint8_t* w_image, uint8_t* up_image, const float* up, int t, volatile int* odd) {
+  constexpr int kRowChunks = NP * 8, kRows = kThreads / kRowChunks;
+  static_assert(kRows % 8 == 0, "the swizzle repeats every 8 rows");
+  const int r0 = t / kRowChunks, ch = t % kRowChunks;
+  const uint32_t at = (ch >> 3) * kPanel + image_chunk<128>(r0, ch & 7);
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+  __nv_bfloat162 trace = zero;  // not 0 once a value is not finite
+#pragma unroll 2
+  for (int u = 0; u < kC / kRows; ++u) {
+    const uint4 q = *reinterpret_cast<const uint4*>(w_image + at + u * kRows * 128);
+    const float2 f = splat2(up[r0 + u * kRows]);
+    const uint32_t p[4] = {q.x, q.y, q.z, q.w};
+    uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      trace = fma2(v[k], splat2(0.0f), trace);
-      v[k] = mul2(v[k], splat2(r < rows ? f : 0.0f));
+      if (odd) trace = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&p[k]), zero, trace);
+      uint32_t term[2];
+      split_pair<2>(mul2(make_float2(bf16_lo(p[k]), bf16_hi(p[k])), f), term);
+      hi[k] = term[0];
+      lo[k] = term[1];
     }
-    put_chunk<2, 128>(up_image + (ch >> 3) * kPanel, NP * kPanel, r, ch & 7, v);
-    if (odd && trace.x + trace.y != 0.0f) {
-      uint32_t p[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if ((p[k] & 0x7f80u) == 0x7f80u) p[k] &= 0xffff0000u;
-        if ((p[k] & 0x7f800000u) == 0x7f800000u) p[k] &= 0xffffu;
-      }
-      *at = make_uint4(p[0], p[1], p[2], p[3]);
-      *odd = 1;
-    }
+    uint8_t* to = up_image + at + u * kRows * 128;
+    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(to + NP * kPanel) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  if (odd && (*reinterpret_cast<const uint32_t*>(&trace) & 0x7fff7fffu)) {
+    clear_odd(w_image + at, kRows * 128, kC / kRows);
+    *odd = 1;
   }
 }
 
-// Rows of Y past the segment: 0 times what the copies brought could be NaN.
+// Rows past the segment, which the copies fill with another's: 0 times them could be NaN.
 template <int KP>
 __device__ __forceinline__ void clear_rows(uint8_t* image, int rows, int t, int threads) {
   for (int i = rows * KP * 8 + t; i < kC * KP * 8; i += threads) {
@@ -115,39 +214,37 @@ __device__ __noinline__ uint32_t odd_columns(const LinRole& role, const __nv_bfl
   return mask;
 }
 
-template <int KP, int NP>
-__global__ void __launch_bounds__(kWarps * 32, 1)
-    lin_walk_bf16_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps, int roles) {
+// `role`'s walk of the segment a.order[item], head h.  Its direction, and whether rows have a dot product, are known
+// where it is compiled.
+template <int KP, int NP, bool back, bool has_dot>
+__device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, const LinRole& role, int h, int64_t item) {
   using T = __nv_bfloat16;
   using L = WalkSmem<KP, NP>;
-  using R = WalkRow<T, 2>;  // 16 columns of a thread's at a time
-  using RF = WalkRow<float, 2>;
-  constexpr int kN = NP * 64, kCols = NP * 32;  // columns of W, and to a thread
+  constexpr int kN = NP * 64, kCols = NP * 32;  // columns of W, and to a thread of the state's path
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
-  const float* s_in = reinterpret_cast<const float*>(sm + L::oGates);  // in, up, and two of P's factors or of G
-  const float *s_up = s_in + kC, *s_f = s_in + 2 * kC, *s_h = s_in + 3 * kC;
+  const float* s_up = reinterpret_cast<const float*>(sm + L::oTokens);  // up, G / ln 2 in two floats, P's columns' factors
+  const float *s_hi = s_up + kC, *s_lo = s_up + 2 * kC, *s_col = s_up + 3 * kC;
   float* s_diag = reinterpret_cast<float*>(sm + L::oDiag);
   float* s_sums = reinterpret_cast<float*>(sm + L::oMisc);  // 8
-  float* s_end = s_sums + 8;
-  volatile int* s_near = reinterpret_cast<int*>(s_end + 1);
-  volatile int *odd = s_near + 1, *stop = s_near + 2;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(s_end + 4);
+  float *s_decay = s_sums + 8, *s_unit = s_sums + 9;
+  volatile int *odd = reinterpret_cast<int*>(s_sums + 10), *stop = odd + 1, *s_steep = odd + 2;
+  Pair* s_last = reinterpret_cast<Pair*>(s_sums + 14);  // the chunk's sum
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(s_sums + 13);
 
-  const int which = blockIdx.x % roles, h = blockIdx.x / roles % a.Hv;
-  const int64_t item = blockIdx.x / roles / a.Hv;
-  if (item >= a.info[0]) return;
-  const LinRole& role = a.role[which];
-  const bool back = role.back != 0, has_dot = role.dot != nullptr;
+  constexpr int terms = has_dot ? 2 : 1;  // of P, and of S in D1
+  constexpr bool two_w = L::kRoom || !has_dot;
+  auto w_image = [&](int k) { return sm + (two_w && (k & 1) ? L::oW2 : L::oW); };
   const int seg_at = a.order[item];
   const Segment seg(a.table[seg_at]);
   const int n1 = role.n1, n2 = role.n2, n = seg.n;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, part = (warp >> 2) & 1, row = quad * 32 + lane;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, row = quad * 32 + lane;
   if (t == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bars + i, i == kUpReady || i == kStateReady || i == kPReady || i == kOutDone ? kPathWarps
-                          : i == kGatesFree                                                  ? 2 * kPathWarps
-                                                                                             : 1);
+      mbar_init(bars + i, i == kUpReady || i == kStateReady ? kStateWarps
+                          : i == kPReady || i == kOutDone   ? kOutWarps
+                          : i == kGatesFree                 ? kStateWarps + kOutWarps
+                                                            : 1);
     *stop = *odd = 0;
     fence_mbar_init();
   }
@@ -168,137 +265,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   LinWaiter wait{a, stop};
   auto chunk_of = [&](int k) { return back ? n - 1 - k : k; };
 
-  if (warp == kProducts) {
-    if (lane == 0) {
-      const Operand<128, kKMajor, 1, L::kX, kPanel> X(smem_u32(sm + L::oX)), Y(smem_u32(sm + L::oY));
-      const Operand<128, kMnMajor, 1, L::kX, 0, kPanel> Yt(smem_u32(sm + L::oY));
-      const Operand<128, kMnMajor, 2, L::kSTerm, 0, L::kSBlock> S(smem_u32(sm + L::oS));
-      const Operand<128, kMnMajor, 2, L::kW, 0, kPanel> Up(smem_u32(sm + L::oUp));
-      const Operand<128, kMnMajor, 1, L::kW, 0, kPanel> W(smem_u32(sm + L::oW));
-      for (int k = 0; k < n; ++k) {
-        const uint32_t p = k & 1;
-        const bool has_state = k > 0 || has_carry;
-        wait(bars + kFullX, p, k == 0 && forced_here(a));
-        wait(bars + kFullY, p);
-        if (k > 0) wait(bars + kDoneO, p ^ 1);  // P's place
-        if (wait.ok) {
-          tmem_fence_after_sync();
-          umma_terms<kC, KP * 4, 1>(tm + tA, X, Y, false);
-          umma_commit(bars + kDoneA);
-        }
-        wait(bars + kStateReady, p);
-        if (k > 0) wait(bars + kOutDone, p ^ 1);
-        if (wait.ok) {
-          tmem_fence_after_sync();
-          if (has_state) umma_terms<kN, KP * 4, 2>(tm + tD1, X, S, false);
-          umma_commit(bars + kDoneX);
-        }
-        wait(bars + kUpReady, p);
-        if (wait.ok) {
-          tmem_fence_after_sync();
-          umma_terms<kN, kC / 16, 2>(tm + tU, Yt, Up, has_state);
-          umma_commit(bars + kDoneU);
-        }
-        wait(bars + kPReady, p);
-        if (wait.ok) {
-          tmem_fence_after_sync();
-          constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
-#pragma unroll
-          for (int term = 1; term >= 0; --term)
-#pragma unroll
-            for (int s = 0; s < kC / 16; ++s)
-              umma_ta(tm + tO, tm + tA + 16 * s + 8 * term, W.at(0, s), idesc, term == 1 && s == 0 ? 0u : 1u);
-          umma_commit(bars + kDoneO);
-        }
-      }
-      if (*stop) {  // products that were not waited for
-        umma_commit(bars + kDrained);
-        mbar_wait(bars + kDrained, 0, kCopyDrainNs);
-      }
-    }
-    __syncwarp();
-  } else if (warp == kCopies) {
-    if (lane == 0 && n > 0) {
-      int xs = 0, ys = 0, ws = 0;  // copies asked for
-      auto load = [&](int map, int head, int at, int panels, int bar, int& asked, int c) {
-        mbar_arrive_expect_tx(bars + bar, (uint32_t)(panels * kPanel));
-        copy_panels(maps.m + map, sm + at, panels, head, seg.start + (int64_t)c * kC, bars + bar);
-        ++asked;
-      };
-      auto load_x = [&](int c) { load(role.mx, h / role.rx, L::oX, KP, kFullX, xs, c); };
-      auto load_y = [&](int c) { load(role.my, h / role.ry, L::oY, KP, kFullY, ys, c); };
-      auto load_w = [&](int c) { load(role.mw, h / role.rw, L::oW, NP, kFullW, ws, c); };
-      load_x(chunk_of(0));
-      load_y(chunk_of(0));
-      load_w(chunk_of(0));
-      for (int k = 0; k + 1 < n; ++k) {
-        const uint32_t p = k & 1;
-        wait(bars + kDoneX, p);
-        if (wait.ok) load_x(chunk_of(k + 1));
-        wait(bars + kDoneU, p);
-        if (wait.ok) load_y(chunk_of(k + 1));
-        wait(bars + kDoneO, p);
-        if (wait.ok) load_w(chunk_of(k + 1));
-      }
-      // what is on its way comes in before the memory is given back
-      drain_copies(bars + kFullX, xs);
-      drain_copies(bars + kFullY, ys);
-      drain_copies(bars + kFullW, ws);
-    }
-    __syncwarp();
-  } else if (warp == kGatesWarp) {
-    const float* g_base = a.g + seg.start * a.g_token + h;
-    auto load_g = [&](int c, float (&g)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = c * kC + lane * 4 + i;
-        g[i] = r < seg.len ? g_base[(int64_t)r * a.g_token] : 0.0f;
-      }
-    };
-    float g[4];
-    if (n > 0) load_g(chunk_of(0), g);
-    for (int k = 0; k < n; ++k) {
-      const GateSums<4> sums(g, lane);
-      if (k + 1 < n) load_g(chunk_of(k + 1), g);
-      const float mid = 0.5f * sums.last.hi;
-      bool near = true;  // both factors of every weight are normal numbers
-      float in[4], up[4], f[4], q[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Pair G = sums.G[i], d = add(G, Pair{-mid, 0.0f});
-        const float from = a.scale * exp2_of(G), to = exp2_of(add(sums.last, minus(G)));
-        in[i] = back ? to : from;
-        up[i] = back ? from : to;
-        f[i] = a.scale * exp2_of(back ? minus(d) : d);
-        q[i] = exp2_of(back ? d : minus(d));
-        near = near && fabsf(d.hi) < 120.0f;
-      }
-      near = __all_sync(0xffffffffu, near);
-      if (!near) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[i] = sums.G[i].hi;
-          q[i] = sums.G[i].lo;
-        }
-      }
-      const float end = exp2_of(sums.last);
-      if (k > 0) wait(bars + kGatesFree, (k - 1) & 1);
-      __syncwarp();
-      float4* to = reinterpret_cast<float4*>(sm + L::oGates) + lane;
-      to[0] = make_float4(in[0], in[1], in[2], in[3]);
-      to[kC / 4] = make_float4(up[0], up[1], up[2], up[3]);
-      to[kC / 2] = make_float4(f[0], f[1], f[2], f[3]);
-      to[3 * kC / 4] = make_float4(q[0], q[1], q[2], q[3]);
-      if (lane == 0) {
-        *s_end = end;
-        *s_near = near;
-      }
-      warp_arrive(bars + kGatesFull, lane);
-    }
-  } else if (warp < kPathWarps) {  // the state's path
-    const int c0 = part * kCols;
+  if (warp < kStateWarps) {  // the state's path
+    const int c0 = (warp >> 2) * kCols;
+    float unit = 1.0f;  // S is this many times what tensor memory has
     const bool has_row = row < KP * 64;
     auto state_at = [&](int col) { return (int64_t)row * role.srow + (int64_t)col * role.scol; };
+    auto put_state = [&](int col, const float2 (&d)[8]) {
+      uint8_t* image = sm + L::oS + col / 64 * L::kSBlock;
+      if (terms == 2) put_row<2, 128>(image, L::kSTerm, row, col % 64 / 8, d);
+      else put_row<1, 128>(image, 0, row, col % 64 / 8, d);
+    };
     auto load_state = [&](const float* from, int col, float2 (&d)[8]) {  // 16 columns of this thread's row
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
@@ -312,12 +288,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         d[i + 1] = make_float2(f.z, f.w);
       }
     };
-    if (has_carry && has_row) {
+    if (has_row && n > 0 || has_carry && has_row) {  // without one, zeros: D1 is added in any case
 #pragma unroll 1
       for (int u = 0; u < kCols / 16; ++u) {
         float2 d[8];
         uint32_t words[16];
-        load_state(carry, c0 + 16 * u, d);
+        if (has_carry) {
+          load_state(carry, c0 + 16 * u, d);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = splat2(0.0f);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           words[2 * i] = __float_as_uint(d[i].x);
@@ -325,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
         __syncwarp();
         tmem_st16(tm + tU + lane_at + c0 + 16 * u, words);
-        put_row<2, 128>(sm + L::oS + (c0 + 16 * u) / 64 * L::kSBlock, L::kSTerm, row, (c0 + 16 * u) % 64 / 8, d);
+        put_state(c0 + 16 * u, d);
       }
       tmem_wait_st();
       tmem_fence_before_sync();
@@ -337,45 +318,42 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const uint32_t p = k & 1;
       const bool more = k + 1 < n;
       const int rows = min(kC, seg.len - chunk_of(k) * kC);
-      wait(bars + kGatesFull, p);
-      wait(bars + kFullW, p);
-      const float end = *s_end;
-      weigh<NP, 256>(sm + L::oW, sm + L::oUp, s_up, rows, t, odd);
-      warp_arrive(bars + kGatesFree, lane);
+      if (warp == 0) {
+        wait(bars + kGatesFull, p);
+        if (two_w) wait(bars + kFullW + p, (k >> 1) & 1);
+        else wait(bars + kFullW, p);
+        if (rows < kC) wait(bars + kFullY, p);
+      }
+      named_barrier(1, 32 * kStateWarps);
+      const float decay = *s_decay;
+      unit = *s_unit;
       if (rows < kC) {
-        wait(bars + kFullY, p);
-        clear_rows<KP>(sm + L::oY, rows, t, 256);
+        clear_rows<KP>(sm + L::oY, rows, t, 32 * kStateWarps);
+        clear_rows<NP>(w_image(k), rows, t, 32 * kStateWarps);
+        named_barrier(1, 32 * kStateWarps);
       }
-      if ((k > 0 || has_carry) && has_row) {
-#pragma unroll
-        for (int u = 0; u < kCols / 32; ++u) {
-          uint32_t w[32];
-          __syncwarp();
-          tmem_ld32(tm + tU + lane_at + c0 + 32 * u, w);
-          tmem_wait_ld32(w);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 d = mul2(make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), splat2(end));
-            w[i] = __float_as_uint(d.x);
-            w[i + 1] = __float_as_uint(d.y);
-          }
-          tmem_st32(tm + tU + lane_at + c0 + 32 * u, w);
-        }
-        tmem_wait_st();
-      }
+      weigh<NP, 32 * kStateWarps>(w_image(k), sm + L::oUp, s_up, t, odd);
+      warp_arrive(bars + kGatesFree, lane);
+      if (decay != 1.0f && has_row) decay_state<kCols>(tm + tU + lane_at + c0, decay);
       tmem_fence_before_sync();
       fence_async_smem();
       warp_arrive(bars + kUpReady, lane);
-      if (more || wanted) wait(bars + kDoneU, p);
+      if (more || wanted) {
+        if (warp == 0) {
+          wait(bars + kDoneX, p);
+          wait(bars + kDoneU, p);
+        }
+        named_barrier(1, 32 * kStateWarps);
+      }
       if (more) {
-        wait(bars + kDoneX, p);
         tmem_fence_after_sync();
         if (has_row) {
-#pragma unroll
+#pragma unroll 1
           for (int u = 0; u < kCols / 16; ++u) {
             float2 d[8];
             tmem_sum<1>(tm + tU + lane_at + c0 + 16 * u, 0, d);
-            put_row<2, 128>(sm + L::oS + (c0 + 16 * u) / 64 * L::kSBlock, L::kSTerm, row, (c0 + 16 * u) % 64 / 8, d);
+            scale_row(d, unit);
+            put_state(c0 + 16 * u, d);
           }
         }
         fence_async_smem();
@@ -399,6 +377,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] = splat2(0.0f);
           if (n > 0 || has_carry) tmem_sum<1>(tm + tU + lane_at + c0 + 16 * u, 0, d);
+          scale_row(d, unit);
           if (e) {
             float2 x[8];
             load_state(e, c0 + 16 * u, x);
@@ -421,70 +400,100 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane == 0) s_sums[warp] = v;
-        named_barrier(1, 32 * kPathWarps);
+        named_barrier(1, 32 * kStateWarps);
         if (t == 0) {
-          for (int i = 1; i < kPathWarps; ++i) v += s_sums[i];
+          for (int i = 1; i < kStateWarps; ++i) v += s_sums[i];
           role.cross[(int64_t)seg_at * a.Hv + h] = v;
         }
       }
     }
-  } else if (warp < 2 * kPathWarps) {  // the results' path
+  } else if (warp < kStateWarps + kOutWarps) {  // the results' path
+    const int part = (warp - kStateWarps) >> 2;
+    const int64_t dot_at = has_dot ? (int64_t)(h / role.rdot) * n2 : 0, w_at = (int64_t)(h / role.rw) * n2;
+    const bool whole_out = !role.part && whole_rows(role.out, (int64_t)a.Hv * n2, n2), whole_w = whole_rows(role.w, role.sw, n2),
+               whole_dot = whole_rows(role.dot, role.sdot, n2);
     for (int k = 0; k < n; ++k) {
       const uint32_t p = k & 1;
       const int c = chunk_of(k), rows = min(kC, seg.len - c * kC);
-      const bool has_state = k > 0 || has_carry;
-      wait(bars + kGatesFull, p);
-      const float in = s_in[row], mine = s_f[row], rest = s_h[row];
-      const bool near = *s_near;
+      if (warp == kStateWarps) {
+        wait(bars + kGatesFull, p);
+        wait(bars + kDoneA, p);
+      }
+      named_barrier(2, 32 * kOutWarps);
+      const float hi = s_hi[row], lo = s_lo[row];
+      const Pair G{hi, lo};
+      const float in = back ? exp2_of(add(*s_last, minus(G))) : a.scale * exp2_of(G);
+      const bool steep = *s_steep;
       const int see = back ? row + (has_dot ? 1 : 0) : row + (has_dot ? 0 : 1);  // the columns a row sees: j < see, back: see <= j < rows
-      wait(bars + kDoneA, p);
       tmem_fence_after_sync();
 #pragma unroll 1
-      for (int u = 0; u < 4; ++u) {
-        // a thread's blocks of 16 columns, spread: P is triangular
-        const int j0 = 16 * (u & 1 ? 2 * u + 1 - part : 2 * u + part);
+      for (int u = 0; u < 8 / kParts; ++u) {
+        // a thread's blocks of 16 columns of P, spread over its columns: P is triangular
+        const int j0 = 16 * (kParts * u + (u & 1 ? kParts - 1 - part : part));
         uint32_t words[16];
+        if (back ? j0 + 15 < quad * 32 || j0 >= rows : j0 > quad * 32 + 31) {  // no row of the warp sees these columns
 #pragma unroll
-        for (int i = 0; i < 16; ++i) words[i] = 0;
-        if (back ? j0 + 15 >= quad * 32 && j0 < rows : j0 <= quad * 32 + 31) {  // the warp has rows that see these columns
+          for (int i = 0; i < 16; ++i) words[i] = 0;
+        } else {
           float2 d[8];
           tmem_sum<1>(tm + tA + lane_at + j0, 0, d);
           const bool all = back ? j0 > quad * 32 + 31 && j0 + 15 < rows : j0 + 15 < quad * 32;
           if (!all && has_dot) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (j0 + i == row) s_diag[row] = a.scale * (i % 2 ? d[i / 2].y : d[i / 2].x);
-          }
-          const float4* h4 = reinterpret_cast<const float4*>(s_h + j0);
-          if (near) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = h4[i];
-              d[2 * i] = mul2(d[2 * i], mul2(make_float2(f.x, f.y), splat2(mine)));
-              d[2 * i + 1] = mul2(d[2 * i + 1], mul2(make_float2(f.z, f.w), splat2(mine)));
-            }
-          } else {
-            const float sign = back ? -1.0f : 1.0f;
+            const int at = row - j0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              d[i].x *= a.scale * ex2(sign * ((mine - s_f[j0 + 2 * i]) + (rest - s_h[j0 + 2 * i])));
-              d[i].y *= a.scale * ex2(sign * ((mine - s_f[j0 + 2 * i + 1]) + (rest - s_h[j0 + 2 * i + 1])));
+              if (at == 2 * i) s_diag[row] = a.scale * d[i].x;
+              if (at == 2 * i + 1) s_diag[row] = a.scale * d[i].y;
+            }
+          }
+          // exp(G_i - G_j) in two factors, by way of the block's end: neither is above 1 where every row sees every
+          // column, and on the diagonal the row's has no more than 32 tokens to grow over
+          const int ref = back ? j0 : j0 + 15;
+          const float e = (hi - s_hi[ref]) + (lo - s_lo[ref]);
+          if (all || !steep) {
+            const float f = a.scale * ex2(back ? -e : e);
+            const float4* col = reinterpret_cast<const float4*>(s_col + j0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 q = col[i];
+              d[2 * i] = mul2(d[2 * i], mul2(make_float2(q.x, q.y), splat2(f)));
+              d[2 * i + 1] = mul2(d[2 * i + 1], mul2(make_float2(q.z, q.w), splat2(f)));
+            }
+          } else {
+            #pragma unroll 1
+            for (int i = 0; i < 16; ++i) {  // little code: see LinWaiter
+              const float w = a.scale * ex2((back ? -1.0f : 1.0f) * ((hi - s_hi[j0 + i]) + (lo - s_lo[j0 + i])));
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                d[q].x *= i == 2 * q ? w : 1.0f;
+                d[q].y *= i == 2 * q + 1 ? w : 1.0f;
+              }
             }
           }
           if (!all) {
-            const int lo = back ? see - j0 : 0, count = (back ? rows : see) - j0 - lo;
+            const int from = back ? see - j0 : 0, count = max((back ? rows : see) - j0 - from, 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if ((unsigned)(2 * i - lo) >= (unsigned)max(count, 0)) d[i].x = 0.0f;
-              if ((unsigned)(2 * i + 1 - lo) >= (unsigned)max(count, 0)) d[i].y = 0.0f;
+              if ((unsigned)(2 * i - from) >= (unsigned)count) d[i].x = 0.0f;
+              if ((unsigned)(2 * i + 1 - from) >= (unsigned)count) d[i].y = 0.0f;
             }
           }
+          if (terms == 2) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t term[2];
-            split_pair<2>(d[i], term);
-            words[i] = term[0];
-            words[8 + i] = term[1];
+            for (int i = 0; i < 8; ++i) {
+              uint32_t term[2];
+              split_pair<2>(d[i], term);
+              words[i] = term[0];
+              words[8 + i] = term[1];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t term[1];
+              split_pair<1>(d[i], term);
+              words[i] = term[0];
+              words[8 + i] = 0;
+            }
           }
         }
         __syncwarp();
@@ -494,47 +503,67 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       warp_arrive(bars + kGatesFree, lane);
       float self = 0.0f;
       if (has_dot) {
-        named_barrier(2, 32 * kPathWarps);
+        named_barrier(2, 32 * kOutWarps);
         self = s_diag[row];
       }
       tmem_fence_before_sync();
       warp_arrive(bars + kPReady, lane);
 
-      const int64_t at = (int64_t)c * kC + quad * 32;  // the warp's first token
+      const int64_t token = seg.start + (int64_t)c * kC + row;
+      const bool mine = row < rows;
+      const T* dot_row = static_cast<const T*>(role.dot) + token * role.sdot + dot_at;
+      const T* w_row = static_cast<const T*>(role.w) + token * role.sw + w_at;
+      const int64_t out_row = (token * a.Hv + h) * n2;
+      if (warp == kStateWarps) {
+        wait(bars + kUpReady, p);  // what weigh() found
+        wait(bars + kDoneO, p);
+      }
+      named_barrier(2, 32 * kOutWarps);
+      tmem_fence_after_sync();
+      const bool spoilt = *odd;
+      if (!has_dot && whole_out && !spoilt) {
+        // the next products may have D1's and D2's places as soon as they are read
+        Row16 r[kN / 16 / kParts];
+#pragma unroll
+        for (int s = 0; s < kN / 16 / kParts; ++s) {
+          const int c0 = part * (kN / kParts) + 16 * s;
+          float2 e[2][8];
+          load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[s].put(i, fma2(splat2(in), e[1][i], e[0][i]));
+        }
+        tmem_fence_before_sync();
+        warp_arrive(bars + kOutDone, lane);
+        T* to = static_cast<T*>(role.out) + out_row + part * (kN / kParts);
+#pragma unroll
+        for (int s = 0; s < kN / 16 / kParts; ++s)
+          if (mine && part * (kN / kParts) + 16 * s < n2) r[s].store_whole(to + 16 * s);
+        continue;
+      }
       float2 dot = splat2(0.0f);
 #pragma unroll 1
-      for (int s = 0; s < kCols / 16; ++s) {
-        const int c0 = part * kCols + 16 * s;
-        typename R::Raw raw_y, raw_w;
+      for (int s = 0; s < kN / 16 / kParts; ++s) {
+        const int c0 = part * (kN / kParts) + 16 * s, cols = mine ? n2 - c0 : 0;
+        Row16 y, w;
         if (has_dot) {  // the partner's rows, and the values of the token's own pair
-          R::load(static_cast<const T*>(role.dot) + (seg.start + at) * role.sdot + (int64_t)(h / role.rdot) * n2 + c0, role.sdot,
-                  seg.len - at, n2 - c0, lane, raw_y);
-          R::load(static_cast<const T*>(role.w) + (seg.start + at) * role.sw + (int64_t)(h / role.rw) * n2 + c0, role.sw,
-                  seg.len - at, n2 - c0, lane, raw_w);
-        }
-        if (s == 0) {
-          wait(bars + kUpReady, p);  // what weigh() found
-          wait(bars + kDoneO, p);
-          tmem_fence_after_sync();
+          y.load(dot_row + c0, cols, whole_dot);
+          w.load(w_row + c0, cols, whole_w);
         }
         float2 o[8];
-        tmem_sum<1>(tm + tO + lane_at + c0, 0, o);
-        if (has_state) {
-          float2 e[8];
-          tmem_sum<1>(tm + tD1 + lane_at + c0, 0, e);
+        {
+          float2 e[2][8];
+          load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(in), e[i], o[i]);
+          for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(in), e[1][i], e[0][i]);
         }
         if (has_dot) {
-          transpose(raw_y[0], lane);
-          transpose(raw_w[0], lane);
-          R::each(raw_y, 0, [&](int i, float2 y) { dot = fma2(y, o[i], dot); });
-          R::each(raw_w, 0, [&](int i, float2 w) { o[i] = fma2(splat2(self), w, o[i]); });
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = fma2(y.get(i), o[i], dot);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(self), w.get(i), o[i]);
         }
-        if (*odd) {
-          const uint32_t mask = odd_columns(
-              role, static_cast<const T*>(role.w) + (seg.start + (int64_t)c * kC) * role.sw + (int64_t)(h / role.rw) * n2 + c0, row,
-              rows, n2 - c0);
+        if (spoilt) {
+          const uint32_t mask = odd_columns(role, w_row - (int64_t)row * role.sw + c0, row, rows, n2 - c0);
           const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -542,24 +571,216 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             if (mask >> (2 * i + 1) & 1) o[i].y = nan;
           }
         }
-        const int64_t out_at = ((seg.start + at) * a.Hv + h) * n2 + c0;
-        auto store = [&](auto rows_of, auto* base) {
-          using Q = decltype(rows_of);
-          typename Q::Raw raw;
-          Q::put(raw, 0, o);
-          Q::store(base + out_at, (int64_t)a.Hv * n2, seg.len - at, n2 - c0, lane, raw);
-        };
-        if (role.part) store(RF(), static_cast<float*>(role.out));
-        else store(R(), static_cast<T*>(role.out));
+        if (role.part) {
+          float* to = static_cast<float*>(role.out) + out_row + c0;
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            if (2 * i < cols) st_io8(to + 2 * i, &o[i].x);
+        } else {
+          Row16 r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r.put(i, o[i]);
+          r.store(static_cast<T*>(role.out) + out_row + c0, cols, whole_out);
+        }
       }
-      if (has_dot && row < rows) role.dots[((int64_t)part * a.T + seg.start + at + lane) * a.Hv + h] = dot.x + dot.y;
+      if (has_dot && mine) role.dots[((int64_t)part * a.T + token) * a.Hv + h] = dot.x + dot.y;
       tmem_fence_before_sync();
       warp_arrive(bars + kOutDone, lane);
+    }
+  } else {
+    if (warp == kProducts) {  // all lanes go through it together, so that addresses are uniform; one issues
+      {
+        const bool lead = lane == 0;
+        const uint64_t x = smem_desc<128>(smem_u32(sm + L::oX)), y = smem_desc<128>(smem_u32(sm + L::oY));
+        const uint64_t yt = smem_desc<128>(smem_u32(sm + L::oY), kPanel);
+        const uint64_t up = smem_desc<128>(smem_u32(sm + L::oUp), kPanel), st = smem_desc<128>(smem_u32(sm + L::oS), L::kSBlock);
+        for (int k = 0; k < n; ++k) {
+          const uint32_t p = k & 1;
+          wait(bars + kFullX, p, k == 0 && forced_here(a));
+          wait(bars + kFullY, p);
+          if (k > 0) wait(bars + kDoneO, p ^ 1);  // P's place
+          if (__all_sync(0xffffffffu, wait.ok)) {
+            tmem_fence_after_sync();
+            constexpr uint32_t idesc = umma_idesc(kKMajor, kKMajor, kC);
+#pragma unroll 1
+            for (int i = 0; i < KP; ++i)
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                umma_if(lead, tm + tA, x + (i * kPanel + s * 32) / 16, y + (i * kPanel + s * 32) / 16, idesc, i + s > 0 ? 1u : 0u);
+            if (lead) umma_commit(bars + kDoneA);
+          }
+          wait(bars + kStateReady, p);
+          if (k > 0) wait(bars + kOutDone, p ^ 1);
+          if (__all_sync(0xffffffffu, wait.ok)) {
+            tmem_fence_after_sync();
+            constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
+            const int i0 = terms == 2 ? 0 : KP;
+#pragma unroll 1
+            for (int i = i0; i < 2 * KP; ++i) {  // the smaller term first
+              const int term = 1 - i / KP, panel = i % KP;
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                umma_if(lead, tm + tD1, x + (panel * kPanel + s * 32) / 16, st + (term * L::kSTerm + (4 * panel + s) * kStep) / 16, idesc,
+                        i - i0 + s > 0 ? 1u : 0u);
+            }
+            if (lead) umma_commit(bars + kDoneX);
+          }
+          // the other two in the order in which their operands come
+          const uint64_t w = smem_desc<128>(smem_u32(w_image(k)), kPanel);
+          bool need_u = true, need_o = true;
+          int tries = 0;
+          while (need_u || need_o) {
+            const bool alone = !(need_u && need_o);
+            bool now_u = need_u, now_o = need_o;
+            if (!alone) {
+              now_u = __all_sync(0xffffffffu, mbar_try_wait(bars + kUpReady, p));
+              now_o = !now_u && __all_sync(0xffffffffu, mbar_try_wait(bars + kPReady, p));
+              if (!now_u && !now_o) {
+                if (++tries < 256) continue;
+                now_u = true;  // a wait with a limit
+              }
+            }
+            wait(bars + (now_u ? kUpReady : kPReady), p);
+            if (!__all_sync(0xffffffffu, wait.ok)) break;
+            tmem_fence_after_sync();
+            if (now_u) {
+              constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, kN);
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                const int term = 1 - i / 2;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  umma_if(lead, tm + tU, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc,
+                          1u);
+              }
+              if (lead) umma_commit(bars + kDoneU);
+              need_u = false;
+            } else {
+              constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
+              const int i0 = terms == 2 ? 0 : 2;
+#pragma unroll 1
+              for (int i = i0; i < 4; ++i) {
+                const int term = 1 - i / 2;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  umma_ta_if(lead, tm + tO, tm + tA + 16 * ((i & 1) * 4 + s) + 8 * term, w + ((i & 1) * 4 + s) * (kStep / 16), idesc,
+                             i - i0 + s > 0 ? 1u : 0u);
+              }
+              if (lead) umma_commit(bars + kDoneO);
+              need_o = false;
+            }
+          }
+        }
+        if (lead && *stop) {  // products that were not waited for
+          umma_commit(bars + kDrained);
+          mbar_wait(bars + kDrained, 0, kCopyDrainNs);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kCopies) {
+      if (lane == 0 && n > 0) {
+        int xs = 0, ys = 0, ws[2] = {0, 0};  // copies asked for
+        auto load = [&](int map, int head, int at, int panels, int bar, int& asked, int c) {
+          mbar_arrive_expect_tx(bars + bar, (uint32_t)(panels * kPanel));
+          copy_panels(maps.m + map, sm + at, panels, head, seg.start + (int64_t)c * kC, bars + bar);
+          ++asked;
+        };
+        auto load_x = [&](int c) { load(role.mx, h / role.rx, L::oX, KP, kFullX, xs, c); };
+        auto load_y = [&](int c) { load(role.my, h / role.ry, L::oY, KP, kFullY, ys, c); };
+        auto load_w = [&](int k) {
+          const int b = two_w ? k & 1 : 0;
+          mbar_arrive_expect_tx(bars + kFullW + b, (uint32_t)L::kW);
+          copy_panels(maps.m + role.mw, w_image(k), NP, h / role.rw, seg.start + (int64_t)chunk_of(k) * kC, bars + kFullW + b);
+          ++ws[b];
+        };
+        load_x(chunk_of(0));
+        load_y(chunk_of(0));
+        load_w(0);
+        if (two_w && n > 1) load_w(1);
+        for (int k = 0; k + 1 < n; ++k) {
+          const uint32_t p = k & 1;
+          wait(bars + kDoneX, p);
+          if (wait.ok) load_x(chunk_of(k + 1));
+          wait(bars + kDoneU, p);
+          if (wait.ok) load_y(chunk_of(k + 1));
+          wait(bars + kDoneO, p);
+          if (wait.ok && k + (two_w ? 2 : 1) < n) load_w(k + (two_w ? 2 : 1));
+        }
+        // what is on its way comes in before the memory is given back
+        drain_copies(bars + kFullX, xs);
+        drain_copies(bars + kFullY, ys);
+        drain_copies(bars + kFullW, ws[0]);
+        drain_copies(bars + kFullW2, ws[1]);
+      }
+      __syncwarp();
+    } else if (warp == kGatesWarp) {
+      const float* g_base = a.g + seg.start * a.g_token + h;
+      auto load_g = [&](int c, float (&g)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = c * kC + lane * 4 + i;
+          g[i] = r < seg.len ? g_base[(int64_t)r * a.g_token] : 0.0f;
+        }
+      };
+      float g[4];
+      Pair unit{0.0f, 0.0f};  // what S in tensor memory counts in, over ln 2
+      if (n > 0) load_g(chunk_of(0), g);
+      for (int k = 0; k < n; ++k) {
+        Pair last, run = running_sums(g, lane, last);
+        const Pair next = add(unit, last);
+        const bool keep = fabsf(next.hi) < kFar;
+        float up[4], hi[4], lo[4], col[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          run = add(run, Pair{clamp_g(g[i]), 0.0f});
+          const Pair G = over_ln2(run), w = back ? G : add(last, minus(G));
+          up[i] = (back ? a.scale : 1.0f) * exp2_of(keep ? add(w, minus(next)) : w);
+          hi[i] = G.hi;
+          lo[i] = G.lo;
+        }
+        if (k + 1 < n) load_g(chunk_of(k + 1), g);
+        // a column's factor of P's weights, up to the end (back: from the start) of its block of 16
+        const int ref = back ? lane & ~3 : lane | 3;
+        const float rh = __shfl_sync(0xffffffffu, back ? hi[0] : hi[3], ref), rl = __shfl_sync(0xffffffffu, back ? lo[0] : lo[3], ref);
+        // whether G changes more over 32 tokens than a factor can span
+        const float from = __shfl_sync(0xffffffffu, hi[0], lane & ~7);
+        bool flat = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float d = (rh - hi[i]) + (rl - lo[i]);
+          col[i] = ex2(back ? -d : d);
+          flat = flat && fabsf(hi[i] - from) < 60.0f;
+        }
+        const bool steep = !__all_sync(0xffffffffu, flat);
+        const float decay = keep ? 1.0f : exp2_of(next), in_unit = keep ? exp2_of(next) : 1.0f;
+        unit = keep ? next : Pair{0.0f, 0.0f};
+        if (k > 0) wait(bars + kGatesFree, (k - 1) & 1);
+        __syncwarp();
+        float4* to = reinterpret_cast<float4*>(sm + L::oTokens) + lane;
+        to[0] = make_float4(up[0], up[1], up[2], up[3]);
+        to[kC / 4] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+        to[kC / 2] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+        to[3 * kC / 4] = make_float4(col[0], col[1], col[2], col[3]);
+        if (lane == 0) {
+          *s_steep = steep;
+          *s_decay = decay;
+          *s_unit = in_unit;
+          *s_last = last;
+        }
+        warp_arrive(bars + kGatesFull, lane);
+      }
     }
   }
   tmem_fence_before_sync();
   __syncthreads();
   if (warp == kProducts) tmem_dealloc<512>(tm);
+}
+
+template <int KP, int NP, bool back, bool has_dot>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    lin_walk_bf16_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps, int which) {
+  const int64_t item = blockIdx.x / a.Hv;
+  if (item < a.info[0]) walk<KP, NP, back, has_dot>(a, maps, a.role[which], blockIdx.x % a.Hv, item);
 }
 
 // ------------------------------------------------------------------ what a segment adds to the state
@@ -609,21 +830,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   auto chunk_of = [&](int k) { return back ? k : n - 1 - k; };
 
   if (warp == kProducts) {
-    if (lane == 0) {
-      const Operand<128, kMnMajor, 2, L::kW, 0, kPanel> Up(smem_u32(sm + L::oUp));
-      for (int k = 0; k < n; ++k) {
-        wait(up_ready, k & 1, k == 0 && forced_here(a));
-        if (wait.ok) {
-          tmem_fence_after_sync();
-          const Operand<128, kMnMajor, 1, L::kY, 0, kPanel> Yt(smem_u32(sm + L::oY + (k & 1) * L::kY));
-          umma_terms<kN, kC / 16, 2>(tm, Yt, Up, k > 0);
-          umma_commit(done);
+    const bool lead = lane == 0;
+    const uint64_t up = smem_desc<128>(smem_u32(sm + L::oUp), kPanel);
+    constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, kN);
+    for (int k = 0; k < n; ++k) {
+      wait(up_ready, k & 1, k == 0 && forced_here(a));
+      if (__all_sync(0xffffffffu, wait.ok)) {
+        tmem_fence_after_sync();
+        const uint64_t yt = smem_desc<128>(smem_u32(sm + L::oY + (k & 1) * L::kY), kPanel);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {  // the smaller term first
+          const int term = 1 - i / 2;
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            umma_if(lead, tm, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc,
+                    k + i + s > 0 ? 1u : 0u);
         }
+        if (lead) umma_commit(done);
       }
-      if (*stop) {
-        umma_commit(drained);
-        mbar_wait(drained, 0, kCopyDrainNs);
-      }
+      __syncwarp();
+    }
+    if (lead && *stop) {
+      umma_commit(drained);
+      mbar_wait(drained, 0, kCopyDrainNs);
     }
     __syncwarp();
   } else if (warp == kCopies) {
@@ -658,13 +887,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     load_g(chunk_of(0), g);
     Pair behind{0.0f, 0.0f};
     for (int k = 0; k < n; ++k) {
-      const GateSums<4> sums(g, lane);
-      if (k + 1 < n) load_g(chunk_of(k + 1), g);
+      Pair last, run = running_sums(g, lane, last);
       float up[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        up[i] = back ? a.scale * exp2_of(add(behind, sums.G[i])) : exp2_of(add(behind, add(sums.last, minus(sums.G[i]))));
-      behind = add(behind, sums.last);
+      for (int i = 0; i < 4; ++i) {
+        run = add(run, Pair{clamp_g(g[i]), 0.0f});
+        const Pair G = over_ln2(run);
+        up[i] = back ? a.scale * exp2_of(add(behind, G)) : exp2_of(add(behind, add(last, minus(G))));
+      }
+      if (k + 1 < n) load_g(chunk_of(k + 1), g);
+      behind = add(behind, last);
       if (k >= 2) wait(used + (k & 1), ((k - 2) >> 1) & 1);
       __syncwarp();
       reinterpret_cast<float4*>(sm + L::oGates + (k & 1) * 4 * kC)[lane] = make_float4(up[0], up[1], up[2], up[3]);
@@ -677,19 +909,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   } else if (warp < kWeighWarps) {
     for (int k = 0; k < n; ++k) {
       const int b = k & 1, rows = min(kC, seg.len - chunk_of(k) * kC);
-      wait(gates_full + b, (k >> 1) & 1);
-      wait(full + b, (k >> 1) & 1);
-      if (k > 0) wait(done, (k - 1) & 1);  // up * W's place is free
-      weigh<NP, 32 * kWeighWarps>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), rows, t,
+      if (warp == 0) {
+        wait(gates_full + b, (k >> 1) & 1);
+        wait(full + b, (k >> 1) & 1);
+        if (k > 0) wait(done, (k - 1) & 1);  // up * W's place is free
+      }
+      named_barrier(1, 32 * kWeighWarps);
+      if (rows < kC) {
+        clear_rows<KP>(sm + L::oY + b * L::kY, rows, t, 32 * kWeighWarps);
+        clear_rows<NP>(sm + L::oW + b * L::kW, rows, t, 32 * kWeighWarps);
+        named_barrier(1, 32 * kWeighWarps);
+      }
+      weigh<NP, 32 * kWeighWarps>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), t,
                                   nullptr);
-      if (rows < kC) clear_rows<KP>(sm + L::oY + b * L::kY, rows, t, 32 * kWeighWarps);
       fence_async_smem();
       warp_arrive(used + b, lane);
       if (lane == 0) mbar_arrive(up_ready);
     }
-    wait(done, (n - 1) & 1);
+    if (warp == 0) wait(done, (n - 1) & 1);
+    named_barrier(1, 32 * kWeighWarps);
     tmem_fence_after_sync();
-    if (warp < kPathWarps) {
+    if (warp < kStateWarps) {
       const int c0 = (warp >> 2) * kCols;
       const float total = *s_total;
       const float* carry = role.first && (back ? seg.is_last : seg.is_first)
@@ -719,34 +959,54 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (warp == kProducts) tmem_dealloc<128>(tm);
 }
 
-template <int KP, int NP, bool kState>
-cudaError_t run(const LinArgs& a, const LinMaps& maps, int roles, cudaStream_t st) {
+template <int KP, int NP, bool back, bool has_dot>
+cudaError_t run_walk(const LinArgs& a, const LinMaps& maps, int which, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const auto kernel = kState ? lin_state_bf16_kernel<KP, NP> : lin_walk_bf16_kernel<KP, NP>;
-  constexpr size_t bytes = kState ? (size_t)StateSmem<KP, NP>::kBytes : (size_t)WalkSmem<KP, NP>::kBytes;
+  const auto kernel = lin_walk_bf16_kernel<KP, NP, back, has_dot>;
+  constexpr size_t bytes = WalkSmem<KP, NP>::kBytes;
   const cudaError_t e = set_smem(reinterpret_cast<const void*>(kernel), bytes, done);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (kState ? a.max_inner : a.max_segs) * a.Hv * roles;
-  kernel<<<(unsigned)blocks, kWarps * 32, bytes, st>>>(a, maps, roles);
+  kernel<<<(unsigned)(a.max_segs * a.Hv), kWarps * 32, bytes, st>>>(a, maps, which);
   return cudaGetLastError();
 }
 
-template <bool kState>
-cudaError_t pick(const LinArgs& a, const LinMaps& maps, int roles, cudaStream_t st) {
-  int n1 = 0, n2 = 0;
+template <int KP, int NP>
+cudaError_t run_state(const LinArgs& a, const LinMaps& maps, int roles, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = lin_state_bf16_kernel<KP, NP>;
+  constexpr size_t bytes = StateSmem<KP, NP>::kBytes;
+  const cudaError_t e = set_smem(reinterpret_cast<const void*>(kernel), bytes, done);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)(a.max_inner * a.Hv * roles), kWarps * 32, bytes, st>>>(a, maps, roles);
+  return cudaGetLastError();
+}
+
+// A kernel for each direction, with dot products or without: in one for all,
+// whatever each needs would take registers and code from the others.  The
+// backward's three launches follow each other.
+template <int KP, int NP>
+cudaError_t run(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, cudaStream_t st) {
+  if (state_only) return run_state<KP, NP>(a, maps, roles, st);
   for (int i = 0; i < roles; ++i) {
-    n1 = n1 > a.role[i].n1 ? n1 : a.role[i].n1;
-    n2 = n2 > a.role[i].n2 ? n2 : a.role[i].n2;
+    const LinRole& r = a.role[i];
+    const cudaError_t e = r.back ? (r.dot ? run_walk<KP, NP, true, true>(a, maps, i, st) : run_walk<KP, NP, true, false>(a, maps, i, st))
+                                 : (r.dot ? run_walk<KP, NP, false, true>(a, maps, i, st) : run_walk<KP, NP, false, false>(a, maps, i, st));
+    if (e != cudaSuccess) return e;
   }
-  if (n1 > 64) return n2 > 64 ? run<2, 2, kState>(a, maps, roles, st) : run<2, 1, kState>(a, maps, roles, st);
-  return n2 > 64 ? run<1, 2, kState>(a, maps, roles, st) : run<1, 1, kState>(a, maps, roles, st);
+  return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_lin_walk_bf16(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, cudaStream_t st) {
   if ((state_only ? a.max_inner : a.max_segs) == 0) return cudaSuccess;
-  return state_only ? pick<true>(a, maps, roles, st) : pick<false>(a, maps, roles, st);
+  int n1 = 0, n2 = 0;
+  for (int i = 0; i < roles; ++i) {
+    n1 = n1 > a.role[i].n1 ? n1 : a.role[i].n1;
+    n2 = n2 > a.role[i].n2 ? n2 : a.role[i].n2;
+  }
+  if (n1 > 64) return n2 > 64 ? run<2, 2>(a, maps, roles, state_only, st) : run<2, 1>(a, maps, roles, state_only, st);
+  return n2 > 64 ? run<1, 2>(a, maps, roles, state_only, st) : run<1, 1>(a, maps, roles, state_only, st);
 }
 
 }  // namespace vssm

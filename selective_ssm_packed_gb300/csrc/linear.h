@@ -24,7 +24,9 @@
 // (do_t.v_s) to dg of every token in (s, t], so
 //   dg_t = sum over i >= t of (rho_i - sigma_i) + <gradient of S_end, S_end>,
 //   rho_t = q_t . (dq_t without s = t),  sigma_s = v_s . (dv_s without t = s),
-// the sum over the rest of the token's segment, S_end the state at its end.
+// the sum over the rest of the token's segment, S_end the state at its end.  The
+// bf16 walks' dots have the token's own pair in them, the weight that P had for
+// it times q.k or do.v, which is the other walk's x . y.
 //
 // Segments.  A sequence is cut into segments of at most `seg` tokens, which are
 // walked by CTAs of their own once the state before each is known: a first
@@ -63,6 +65,7 @@ struct LinRole {
   int64_t sdot;
   int rdot;
   float* dots;             // (lin_dot_parts, T, Hv)
+  float* pairs;            // bf16: (T, Hv, 2), the token's own x . y and its weight in P, which dots includes
   int back;                // reversed time
   int64_t srow, scol;      // a state's element (row of n1, column of n2) in memory
   const float* first;      // states that the sequences come with, (S, Hv, ., .), or null

@@ -32,7 +32,7 @@ struct LinLayout {
   int seg;
   int64_t max_segs, max_inner;
   size_t table, order, inner, split, slots, decay, fwd_end;
-  size_t slots_back, decay_back, rho, sigma, cross, seg_dg, dq_part, dk_part, bwd_end;
+  size_t slots_back, decay_back, rho, sigma, pairs, cross, seg_dg, dq_part, dk_part, bwd_end;
 };
 
 LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, bool bwd) {
@@ -55,6 +55,7 @@ LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, 
   l.decay_back = o; o += up(inner * Hv * sizeof(float));
   l.rho = o; o += up(lin_dot_parts(io, K) * tokens);
   l.sigma = o; o += up(lin_dot_parts(io, V) * tokens);
+  l.pairs = o; o += io == IO::BF16 ? 2 * up(2 * tokens) : 0;
   l.cross = o; o += up(segs * Hv * tk * sizeof(float));
   l.seg_dg = o; o += up(segs * Hv * sizeof(double));
   l.dq_part = o; o += Hk == Hv ? 0 : up(tokens * K);
@@ -277,6 +278,10 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   if (dg) {
     rq.dot = q; rq.sdot = q_stride; rq.rdot = rep; rq.dots = reinterpret_cast<float*>(p + l.rho);
     rq.against = slots_back; rq.against_last = d_final_states; rq.cross = reinterpret_cast<float*>(p + l.cross);
+    if (io == IO::BF16) {
+      rq.pairs = reinterpret_cast<float*>(p + l.pairs);
+      rv.pairs = reinterpret_cast<float*>(p + l.pairs + up(2 * sizeof(float) * (size_t)T * Hv));
+    }
     rv.dot = v; rv.sdot = v_stride; rv.rdot = 1; rv.dots = reinterpret_cast<float*>(p + l.sigma);
   }
   TRY(check(launch_lin_walk(a, maps, 3, false, io, st), "linear attention backward launch"));

@@ -32,7 +32,7 @@ struct WalkSmem {
   static constexpr bool kRoom = KP == 1 || NP == 1;
   static constexpr int oW2 = kRoom ? oGates : oS + kSTerm, oTokens = kRoom ? oGates + kW : oGates;
   static_assert(kRoom || kSTerm == kW, "");
-  static constexpr int oDiag = oTokens + 4 * 4 * kC, oMisc = oDiag + 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
+  static constexpr int oMisc = oTokens + 4 * 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 constexpr int tA = 0, tD1 = 128, tU = 256, tO = 384;  // columns of tensor memory
@@ -52,6 +52,7 @@ struct Segment {
 };
 
 __device__ __forceinline__ void copy_panels(const CUtensorMap* map, uint8_t* to, int panels, int head, int64_t token, uint64_t* bar) {
+#pragma unroll 1
   for (int p = 0; p < panels; ++p)
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -67,6 +68,12 @@ __device__ __forceinline__ void copy_panels(const CUtensorMap* map, uint8_t* to,
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {  // the first 8
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // 16 columns each from two places of this thread's lane, on their way together.
@@ -129,11 +136,7 @@ struct Row16 {
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
   }
-  __device__ __forceinline__ void store(__nv_bfloat16* p, int cols, bool whole) const {
-    if (whole && cols >= 16) {
-      store_whole(p);
-      return;
-    }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int cols) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (8 * i < cols) reinterpret_cast<uint4*>(p)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -202,16 +205,18 @@ __device__ __forceinline__ void clear_rows(uint8_t* image, int rows, int t, int 
   }
 }
 
-// The columns (of 16 from w on) in which a value of W at the row or an earlier
-// one (back: a later one) is not finite.
-__device__ __noinline__ uint32_t odd_columns(const LinRole& role, const __nv_bfloat16* w, int row, int rows, int cols) {
-  uint32_t mask = 0;
-  if (row >= rows) return mask;
+// NaN in those of a row's results (`cols` of them, from `at` on) in whose column
+// a value of W at the row or an earlier one (back: a later one) is not finite.
+__device__ __noinline__ void spoil_row(const LinRole& role, const __nv_bfloat16* w, int64_t at, int row, int rows, int cols) {
   const int from = role.back ? row : 0, to = role.back ? rows : row + 1;
-  for (int c = 0; c < 16 && c < cols; ++c)
-    for (int r = from; r < to; ++r)
-      if (!isfinite(__bfloat162float(w[(int64_t)r * role.sw + c]))) mask |= 1u << c;
-  return mask;
+  const float nan = __int_as_float(0x7fffffff);
+  for (int c = 0; c < cols; ++c) {
+    bool odd = false;
+    for (int r = from; r < to; ++r) odd = odd || !isfinite(__bfloat162float(w[(int64_t)r * role.sw + c]));
+    if (!odd) continue;
+    if (role.part) static_cast<float*>(role.out)[at + c] = nan;
+    else static_cast<__nv_bfloat16*>(role.out)[at + c] = __float2bfloat16_rn(nan);
+  }
 }
 
 // `role`'s walk of the segment a.order[item], head h.  Its direction, and whether rows have a dot product, are known
@@ -225,7 +230,6 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
   const float* s_up = reinterpret_cast<const float*>(sm + L::oTokens);  // up, G / ln 2 in two floats, P's columns' factors
   const float *s_hi = s_up + kC, *s_lo = s_up + 2 * kC, *s_col = s_up + 3 * kC;
-  float* s_diag = reinterpret_cast<float*>(sm + L::oDiag);
   float* s_sums = reinterpret_cast<float*>(sm + L::oMisc);  // 8
   float *s_decay = s_sums + 8, *s_unit = s_sums + 9;
   volatile int *odd = reinterpret_cast<int*>(s_sums + 10), *stop = odd + 1, *s_steep = odd + 2;
@@ -410,8 +414,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
   } else if (warp < kStateWarps + kOutWarps) {  // the results' path
     const int part = (warp - kStateWarps) >> 2;
     const int64_t dot_at = has_dot ? (int64_t)(h / role.rdot) * n2 : 0, w_at = (int64_t)(h / role.rw) * n2;
-    const bool whole_out = !role.part && whole_rows(role.out, (int64_t)a.Hv * n2, n2), whole_w = whole_rows(role.w, role.sw, n2),
-               whole_dot = whole_rows(role.dot, role.sdot, n2);
+    const bool whole_out = whole_rows(role.out, (int64_t)a.Hv * n2, n2), whole_dot = whole_rows(role.dot, role.sdot, n2);
     for (int k = 0; k < n; ++k) {
       const uint32_t p = k & 1;
       const int c = chunk_of(k), rows = min(kC, seg.len - c * kC);
@@ -424,13 +427,13 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       const Pair G{hi, lo};
       const float in = back ? exp2_of(add(*s_last, minus(G))) : a.scale * exp2_of(G);
       const bool steep = *s_steep;
-      const int see = back ? row + (has_dot ? 1 : 0) : row + (has_dot ? 0 : 1);  // the columns a row sees: j < see, back: see <= j < rows
       tmem_fence_after_sync();
 #pragma unroll 1
       for (int u = 0; u < 8 / kParts; ++u) {
         // a thread's blocks of 16 columns of P, spread over its columns: P is triangular
         const int j0 = 16 * (kParts * u + (u & 1 ? kParts - 1 - part : part));
         uint32_t words[16];
+        float self = 0.0f, weight = 0.0f;
         if (back ? j0 + 15 < quad * 32 || j0 >= rows : j0 > quad * 32 + 31) {  // no row of the warp sees these columns
 #pragma unroll
           for (int i = 0; i < 16; ++i) words[i] = 0;
@@ -438,13 +441,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           float2 d[8];
           tmem_sum<1>(tm + tA + lane_at + j0, 0, d);
           const bool all = back ? j0 > quad * 32 + 31 && j0 + 15 < rows : j0 + 15 < quad * 32;
-          if (!all && has_dot) {
-            const int at = row - j0;
+          const int at = row - j0;  // the diagonal's column
+          if (has_dot && !all) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (at == 2 * i) s_diag[row] = a.scale * d[i].x;
-              if (at == 2 * i + 1) s_diag[row] = a.scale * d[i].y;
-            }
+            for (int i = 0; i < 8; ++i) self = at == 2 * i ? d[i].x : at == 2 * i + 1 ? d[i].y : self;
           }
           // exp(G_i - G_j) in two factors, by way of the block's end: neither is above 1 where every row sees every
           // column, and on the diagonal the row's has no more than 32 tokens to grow over
@@ -471,7 +471,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
             }
           }
           if (!all) {
-            const int from = back ? see - j0 : 0, count = max((back ? rows : see) - j0 - from, 0);
+            const int from = back ? at : 0, count = max((back ? rows - j0 : at + 1) - from, 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if ((unsigned)(2 * i - from) >= (unsigned)count) d[i].x = 0.0f;
@@ -485,6 +485,14 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
               split_pair<2>(d[i], term);
               words[i] = term[0];
               words[8 + i] = term[1];
+              if (!all) {  // the pair's weight as the product with W has it
+                if (at == 2 * i) weight = bf16_lo(term[0]) + bf16_lo(term[1]);
+                if (at == 2 * i + 1) weight = bf16_hi(term[0]) + bf16_hi(term[1]);
+              }
+            }
+            if (!all && (unsigned)at < 16u && row < rows) {
+              float* pairs = role.pairs + ((seg.start + (int64_t)c * kC + row) * a.Hv + h) * 2;
+              *reinterpret_cast<float2*>(pairs) = make_float2(self, weight);
             }
           } else {
 #pragma unroll
@@ -492,28 +500,29 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
               uint32_t term[1];
               split_pair<1>(d[i], term);
               words[i] = term[0];
-              words[8 + i] = 0;
             }
           }
         }
         __syncwarp();
-        tmem_st16(tm + tA + lane_at + j0, words);
+        if (terms == 2) tmem_st16(tm + tA + lane_at + j0, words);
+        else tmem_st8(tm + tA + lane_at + j0, words);
       }
       tmem_wait_st();
       warp_arrive(bars + kGatesFree, lane);
-      float self = 0.0f;
-      if (has_dot) {
-        named_barrier(2, 32 * kOutWarps);
-        self = s_diag[row];
-      }
       tmem_fence_before_sync();
       warp_arrive(bars + kPReady, lane);
 
       const int64_t token = seg.start + (int64_t)c * kC + row;
       const bool mine = row < rows;
-      const T* dot_row = static_cast<const T*>(role.dot) + token * role.sdot + dot_at;
-      const T* w_row = static_cast<const T*>(role.w) + token * role.sw + w_at;
       const int64_t out_row = (token * a.Hv + h) * n2;
+      constexpr int kRuns = kN / 16 / kParts;
+      const int first = part * (kN / kParts), cols = mine ? n2 - first : 0;
+      Row16 r[kRuns];  // the partner's rows, then the results
+      if (has_dot) {
+        const T* from = static_cast<const T*>(role.dot) + token * role.sdot + dot_at + first;
+#pragma unroll
+        for (int s = 0; s < kRuns; ++s) r[s].load(from + 16 * s, cols - 16 * s, whole_dot);
+      }
       if (warp == kStateWarps) {
         wait(bars + kUpReady, p);  // what weigh() found
         wait(bars + kDoneO, p);
@@ -521,71 +530,43 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       named_barrier(2, 32 * kOutWarps);
       tmem_fence_after_sync();
       const bool spoilt = *odd;
-      if (!has_dot && whole_out && !spoilt) {
-        // the next products may have D1's and D2's places as soon as they are read
-        Row16 r[kN / 16 / kParts];
-#pragma unroll
-        for (int s = 0; s < kN / 16 / kParts; ++s) {
-          const int c0 = part * (kN / kParts) + 16 * s;
-          float2 e[2][8];
-          load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[s].put(i, fma2(splat2(in), e[1][i], e[0][i]));
-        }
-        tmem_fence_before_sync();
-        warp_arrive(bars + kOutDone, lane);
-        T* to = static_cast<T*>(role.out) + out_row + part * (kN / kParts);
-#pragma unroll
-        for (int s = 0; s < kN / 16 / kParts; ++s)
-          if (mine && part * (kN / kParts) + 16 * s < n2) r[s].store_whole(to + 16 * s);
-        continue;
-      }
       float2 dot = splat2(0.0f);
-#pragma unroll 1
-      for (int s = 0; s < kN / 16 / kParts; ++s) {
-        const int c0 = part * (kN / kParts) + 16 * s, cols = mine ? n2 - c0 : 0;
-        Row16 y, w;
-        if (has_dot) {  // the partner's rows, and the values of the token's own pair
-          y.load(dot_row + c0, cols, whole_dot);
-          w.load(w_row + c0, cols, whole_w);
-        }
-        float2 o[8];
-        {
-          float2 e[2][8];
-          load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(in), e[1][i], e[0][i]);
-        }
-        if (has_dot) {
+      for (int s = 0; s < kRuns; ++s) {
+        const int c0 = first + 16 * s;
+        float2 e[2][8];
+        load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fma2(y.get(i), o[i], dot);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(self), w.get(i), o[i]);
-        }
-        if (spoilt) {
-          const uint32_t mask = odd_columns(role, w_row - (int64_t)row * role.sw + c0, row, rows, n2 - c0);
-          const float nan = __int_as_float(0x7fffffff);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (mask >> (2 * i) & 1) o[i].x = nan;
-            if (mask >> (2 * i + 1) & 1) o[i].y = nan;
-          }
+        for (int i = 0; i < 8; ++i) {
+          e[0][i] = fma2(splat2(in), e[1][i], e[0][i]);
+          if (has_dot) dot = fma2(r[s].get(i), e[0][i], dot);
         }
         if (role.part) {
           float* to = static_cast<float*>(role.out) + out_row + c0;
 #pragma unroll
           for (int i = 0; i < 8; i += 4)
-            if (2 * i < cols) st_io8(to + 2 * i, &o[i].x);
+            if (16 * s + 2 * i < cols) st_io8(to + 2 * i, &e[0][i].x);
         } else {
-          Row16 r;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r.put(i, o[i]);
-          r.store(static_cast<T*>(role.out) + out_row + c0, cols, whole_out);
+          for (int i = 0; i < 8; ++i) r[s].put(i, e[0][i]);
         }
       }
-      if (has_dot && mine) role.dots[((int64_t)part * a.T + token) * a.Hv + h] = dot.x + dot.y;
+      // the next products may have D1's and D2's places
       tmem_fence_before_sync();
       warp_arrive(bars + kOutDone, lane);
+      if (!role.part) {
+        T* to = static_cast<T*>(role.out) + out_row + first;
+        if (whole_out) {
+#pragma unroll
+          for (int s = 0; s < kRuns; ++s)
+            if (16 * s < cols) r[s].store_whole(to + 16 * s);
+        } else {
+#pragma unroll
+          for (int s = 0; s < kRuns; ++s) r[s].store(to + 16 * s, cols - 16 * s);
+        }
+      }
+      if (spoilt && mine) spoil_row(role, static_cast<const T*>(role.w) + (token - row) * role.sw + w_at + first, out_row + first, row, rows, cols);
+      if (has_dot && mine) role.dots[((int64_t)part * a.T + token) * a.Hv + h] = dot.x + dot.y;
     }
   } else {
     if (warp == kProducts) {  // all lanes go through it together, so that addresses are uniform; one issues
@@ -679,38 +660,33 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       __syncwarp();
     } else if (warp == kCopies) {
       if (lane == 0 && n > 0) {
-        int xs = 0, ys = 0, ws[2] = {0, 0};  // copies asked for
-        auto load = [&](int map, int head, int at, int panels, int bar, int& asked, int c) {
-          mbar_arrive_expect_tx(bars + bar, (uint32_t)(panels * kPanel));
-          copy_panels(maps.m + map, sm + at, panels, head, seg.start + (int64_t)c * kC, bars + bar);
-          ++asked;
-        };
-        auto load_x = [&](int c) { load(role.mx, h / role.rx, L::oX, KP, kFullX, xs, c); };
-        auto load_y = [&](int c) { load(role.my, h / role.ry, L::oY, KP, kFullY, ys, c); };
-        auto load_w = [&](int k) {
-          const int b = two_w ? k & 1 : 0;
-          mbar_arrive_expect_tx(bars + kFullW + b, (uint32_t)L::kW);
-          copy_panels(maps.m + role.mw, w_image(k), NP, h / role.rw, seg.start + (int64_t)chunk_of(k) * kC, bars + kFullW + b);
-          ++ws[b];
-        };
-        load_x(chunk_of(0));
-        load_y(chunk_of(0));
-        load_w(0);
-        if (two_w && n > 1) load_w(1);
-        for (int k = 0; k + 1 < n; ++k) {
-          const uint32_t p = k & 1;
-          wait(bars + kDoneX, p);
-          if (wait.ok) load_x(chunk_of(k + 1));
-          wait(bars + kDoneU, p);
-          if (wait.ok) load_y(chunk_of(k + 1));
-          wait(bars + kDoneO, p);
-          if (wait.ok && k + (two_w ? 2 : 1) < n) load_w(k + (two_w ? 2 : 1));
+        int xs = 0, ys = 0, ws = 0, ws2 = 0;  // copies asked for
+        const int head_x = h / role.rx, head_y = h / role.ry, head_w = h / role.rw;
+        // X, Y and W in turn, each once the products are through with what is in its place; W a chunk ahead
+        // where it has two buffers
+#pragma unroll 1
+        for (int i = two_w ? -1 : 0; i < 3 * n; ++i) {
+          const int op = i < 0 ? 2 : i % 3, k = i < 0 ? 0 : i / 3 + (two_w && op == 2 ? 1 : 0);
+          if (k >= n) continue;
+          const int before = op == 2 && two_w ? k - 2 : k - 1;
+          if (before >= 0) wait(bars + (op == 0 ? kDoneX : op == 1 ? kDoneU : kDoneO), before & 1);
+          if (!wait.ok) break;
+          const int panels = op == 2 ? NP : KP;
+          uint64_t* bar = bars + (op == 0 ? kFullX : op == 1 ? kFullY : two_w && (k & 1) ? kFullW2 : kFullW);
+          uint8_t* to = op == 0 ? sm + L::oX : op == 1 ? sm + L::oY : w_image(k);
+          mbar_arrive_expect_tx(bar, (uint32_t)(panels * kPanel));
+          copy_panels(maps.m + (op == 0 ? role.mx : op == 1 ? role.my : role.mw), to, panels,
+                      op == 0 ? head_x : op == 1 ? head_y : head_w, seg.start + (int64_t)chunk_of(k) * kC, bar);
+          if (op == 0) ++xs;
+          else if (op == 1) ++ys;
+          else if (two_w && (k & 1)) ++ws2;
+          else ++ws;
         }
         // what is on its way comes in before the memory is given back
         drain_copies(bars + kFullX, xs);
         drain_copies(bars + kFullY, ys);
-        drain_copies(bars + kFullW, ws[0]);
-        drain_copies(bars + kFullW2, ws[1]);
+        drain_copies(bars + kFullW, ws);
+        drain_copies(bars + kFullW2, ws2);
       }
       __syncwarp();
     } else if (warp == kGatesWarp) {
@@ -729,14 +705,18 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         Pair last, run = running_sums(g, lane, last);
         const Pair next = add(unit, last);
         const bool keep = fabsf(next.hi) < kFar;
-        float up[4], hi[4], lo[4], col[4];
-#pragma unroll
+        float up[4] = {}, hi[4] = {}, lo[4] = {}, col[4];
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          run = add(run, Pair{clamp_g(g[i]), 0.0f});
+          run = add(run, Pair{clamp_g(i == 0 ? g[0] : i == 1 ? g[1] : i == 2 ? g[2] : g[3]), 0.0f});
           const Pair G = over_ln2(run), w = back ? G : add(last, minus(G));
-          up[i] = (back ? a.scale : 1.0f) * exp2_of(keep ? add(w, minus(next)) : w);
-          hi[i] = G.hi;
-          lo[i] = G.lo;
+          const float f = (back ? a.scale : 1.0f) * exp2_of(keep ? add(w, minus(next)) : w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            up[q] = q == i ? f : up[q];
+            hi[q] = q == i ? G.hi : hi[q];
+            lo[q] = q == i ? G.lo : lo[q];
+          }
         }
         if (k + 1 < n) load_g(chunk_of(k + 1), g);
         // a column's factor of P's weights, up to the end (back: from the start) of its block of 16
@@ -982,31 +962,30 @@ cudaError_t run_state(const LinArgs& a, const LinMaps& maps, int roles, cudaStre
 }
 
 // A kernel for each direction, with dot products or without: in one for all,
-// whatever each needs would take registers and code from the others.  The
-// backward's three launches follow each other.
+// whatever each needs would take registers and code from the others.
 template <int KP, int NP>
-cudaError_t run(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, cudaStream_t st) {
-  if (state_only) return run_state<KP, NP>(a, maps, roles, st);
-  for (int i = 0; i < roles; ++i) {
-    const LinRole& r = a.role[i];
-    const cudaError_t e = r.back ? (r.dot ? run_walk<KP, NP, true, true>(a, maps, i, st) : run_walk<KP, NP, true, false>(a, maps, i, st))
-                                 : (r.dot ? run_walk<KP, NP, false, true>(a, maps, i, st) : run_walk<KP, NP, false, false>(a, maps, i, st));
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+cudaError_t run_role(const LinArgs& a, const LinMaps& maps, int i, cudaStream_t st) {
+  const LinRole& r = a.role[i];
+  if (r.back) return r.dot ? run_walk<KP, NP, true, true>(a, maps, i, st) : run_walk<KP, NP, true, false>(a, maps, i, st);
+  return r.dot ? run_walk<KP, NP, false, true>(a, maps, i, st) : run_walk<KP, NP, false, false>(a, maps, i, st);
 }
 
 }  // namespace
 
 cudaError_t launch_lin_walk_bf16(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, cudaStream_t st) {
   if ((state_only ? a.max_inner : a.max_segs) == 0) return cudaSuccess;
-  int n1 = 0, n2 = 0;
-  for (int i = 0; i < roles; ++i) {
-    n1 = n1 > a.role[i].n1 ? n1 : a.role[i].n1;
-    n2 = n2 > a.role[i].n2 ? n2 : a.role[i].n2;
+  if (state_only) {  // all K x V
+    const bool k2 = a.role[0].n1 > 64, v2 = a.role[0].n2 > 64;
+    if (k2) return v2 ? run_state<2, 2>(a, maps, roles, st) : run_state<2, 1>(a, maps, roles, st);
+    return v2 ? run_state<1, 2>(a, maps, roles, st) : run_state<1, 1>(a, maps, roles, st);
   }
-  if (n1 > 64) return n2 > 64 ? run<2, 2>(a, maps, roles, state_only, st) : run<2, 1>(a, maps, roles, state_only, st);
-  return n2 > 64 ? run<1, 2>(a, maps, roles, state_only, st) : run<1, 1>(a, maps, roles, state_only, st);
+  for (int i = 0; i < roles; ++i) {
+    const bool k2 = a.role[i].n1 > 64, v2 = a.role[i].n2 > 64;
+    const cudaError_t e = k2 ? (v2 ? run_role<2, 2>(a, maps, i, st) : run_role<2, 1>(a, maps, i, st))
+                             : (v2 ? run_role<1, 2>(a, maps, i, st) : run_role<1, 1>(a, maps, i, st));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace vssm

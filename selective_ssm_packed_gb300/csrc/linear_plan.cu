@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs a, int blocks) {
 // the segment's tokens, which it sums up first and then walks from its end.
 // Sums are of two floats: a token's dg is the sum of all later differences, in
 // which most cancels.
-constexpr int kDgHeads = 8, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads;
+constexpr int kDgHeads = 2, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads;
 
 __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts_q, int parts_v, int tiles) {
   __shared__ Pair sums[2][kDgThreads];
@@ -157,6 +157,11 @@ __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts
     Pair v{0.0f, 0.0f};
     for (int p = 0; p < parts_q; ++p) v = add(v, Pair{rho[p * plane + at], 0.0f});
     for (int p = 0; p < parts_v; ++p) v = add(v, Pair{-sigma[p * plane + at], 0.0f});
+    if (a.role[0].pairs) {
+      const float2 q = reinterpret_cast<const float2*>(a.role[0].pairs)[at], k = reinterpret_cast<const float2*>(a.role[1].pairs)[at];
+      v = add(v, Pair{-q.y * k.x, -fmaf(q.y, k.x, -(q.y * k.x))});
+      v = add(v, Pair{k.y * q.x, fmaf(k.y, q.x, -(k.y * q.x))});
+    }
     return v;
   };
   Pair own{0.0f, 0.0f};

@@ -18,11 +18,15 @@ namespace {
 // Everything is read and written once, which bounds the pass.
 template <int kTeam>
 struct Team {
-  static constexpr int kThreads = kTeam <= 32 ? 256 : kTeam, kUnits = kThreads / kTeam;
+  static constexpr int kThreads = kTeam <= 32 ? 128 : kTeam, kUnits = kThreads / kTeam;
 };
 constexpr int kNormSms = 152;
-// Threads an SM: they bound the registers of a thread, 64 and 128.
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;
+// Threads an SM, which bound a thread's registers (65536 between them): as many
+// as leave it enough for two rows on their way and its weights.
+template <typename T, bool kRes>
+constexpr int fwd_threads() { return sizeof(T) == 2 && !kRes ? 768 : 512; }
+template <int kTeam>
+constexpr int bwd_threads() { return kTeam >= 256 ? 512 : 384; }
 
 // v[i] summed over the team, in a fixed order.  flip: which half of the scratch
 // is this sum's; one barrier a sum is enough with two.
@@ -97,7 +101,7 @@ __device__ __forceinline__ void centre(float (&h)[2][8], const Place<kTeam>& at,
 }
 
 template <typename T, bool kRes, int kTeam>
-__global__ void __launch_bounds__(Team<kTeam>::kThreads, kFwdThreads / Team<kTeam>::kThreads)
+__global__ void __launch_bounds__(Team<kTeam>::kThreads, fwd_threads<T, kRes>() / Team<kTeam>::kThreads)
     layer_norm_fwd_kernel(LayerNormArgs a, int64_t slots) {
   __shared__ float scratch[2][3][16];
   const int64_t slot = (int64_t)blockIdx.x * Team<kTeam>::kUnits + threadIdx.x / kTeam;
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(Team<kTeam>::kThreads, kFwdThreads / Team<kTea
 // One row of sums per team goes to `partial`, which a second kernel adds in
 // the teams' order: no atomics, the same bits every time.
 template <typename T, typename H, int kTeam>
-__global__ void __launch_bounds__(Team<kTeam>::kThreads, kBwdThreads / Team<kTeam>::kThreads)
+__global__ void __launch_bounds__(Team<kTeam>::kThreads, bwd_threads<kTeam>() / Team<kTeam>::kThreads)
     layer_norm_bwd_kernel(LayerNormArgs a, int64_t slots) {
   __shared__ float scratch[2][3][16];
   const int64_t slot = (int64_t)blockIdx.x * Team<kTeam>::kUnits + threadIdx.x / kTeam;
@@ -255,13 +259,15 @@ __global__ void __launch_bounds__(Team<kTeam>::kThreads, kBwdThreads / Team<kTea
 }
 
 // blockIdx.x: 32 channels; blockIdx.y: weight or bias.  The teams of a group in
-// eight stretches, each added up in order by a warp, then the eight in order.
-__global__ void __launch_bounds__(256) layer_norm_sum_kernel(LayerNormArgs a, int64_t slots) {
-  __shared__ float s[8][32];
+// kSumParts stretches, each added up in order by a warp, then those in order.
+constexpr int kSumParts = 32;
+
+__global__ void __launch_bounds__(32 * kSumParts) layer_norm_sum_kernel(LayerNormArgs a, int64_t slots) {
+  __shared__ float s[kSumParts][32];
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5, width = a.D / a.groups;
   float* out = blockIdx.y ? a.dbias : a.dweight;
   if (!out) return;
-  const int64_t rows = a.T > 0 ? slots / a.groups : 0, per = (rows + 7) / 8;
+  const int64_t rows = a.T > 0 ? slots / a.groups : 0, per = (rows + kSumParts - 1) / kSumParts;
   float v = 0.0f;
   if (col < a.D) {
     const int group = col / width;
@@ -273,7 +279,8 @@ __global__ void __launch_bounds__(256) layer_norm_sum_kernel(LayerNormArgs a, in
   s[part][threadIdx.x & 31] = v;
   __syncthreads();
   if (part == 0 && col < a.D) {
-    for (int p = 1; p < 8; ++p) v += s[p][threadIdx.x & 31];
+#pragma unroll
+    for (int p = 1; p < kSumParts; ++p) v += s[p][threadIdx.x & 31];
     out[col] = v;
   }
 }
@@ -290,6 +297,14 @@ int64_t slots_of(int64_t T, int D, int groups, int sm_threads) {
   const int64_t use = units < most ? units : most;
   return use < groups ? groups : use / groups * groups;
 }
+
+}  // namespace
+
+int64_t layer_norm_slots(int64_t T, int D, int groups) {
+  return slots_of(T, D, groups, team_of(D / groups) >= 256 ? bwd_threads<256>() : bwd_threads<128>());
+}
+
+namespace {
 
 template <typename F>
 cudaError_t with_team(int width, F f) {
@@ -309,7 +324,7 @@ template <typename T, bool kRes>
 cudaError_t run_fwd(const LayerNormArgs& a, cudaStream_t st) {
   return with_team(a.D / a.groups, [&](auto team) {
     constexpr int kTeam = decltype(team)::value, kUnits = Team<kTeam>::kUnits;
-    const int64_t slots = slots_of(a.T, a.D, a.groups, kFwdThreads);
+    const int64_t slots = slots_of(a.T, a.D, a.groups, fwd_threads<T, kRes>());
     layer_norm_fwd_kernel<T, kRes, kTeam><<<(unsigned)((slots + kUnits - 1) / kUnits), Team<kTeam>::kThreads, 0, st>>>(a, slots);
     return cudaGetLastError();
   });
@@ -319,17 +334,16 @@ template <typename T, typename H>
 cudaError_t run_bwd(const LayerNormArgs& a, cudaStream_t st) {
   return with_team(a.D / a.groups, [&](auto team) {
     constexpr int kTeam = decltype(team)::value, kUnits = Team<kTeam>::kUnits;
-    const int64_t slots = slots_of(a.T, a.D, a.groups, kBwdThreads);
+    const int64_t slots = layer_norm_slots(a.T, a.D, a.groups);
     if (a.T > 0)
       layer_norm_bwd_kernel<T, H, kTeam><<<(unsigned)((slots + kUnits - 1) / kUnits), Team<kTeam>::kThreads, 0, st>>>(a, slots);
-    if (a.dweight || a.dbias) layer_norm_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), 256, 0, st>>>(a, slots);
+    if (a.dweight || a.dbias) layer_norm_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), 32 * kSumParts, 0, st>>>(a, slots);
     return cudaGetLastError();
   });
 }
 
 }  // namespace
 
-int64_t layer_norm_slots(int64_t T, int D, int groups) { return slots_of(T, D, groups, kBwdThreads); }
 
 cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, IO io, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;

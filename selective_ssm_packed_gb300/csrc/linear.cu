@@ -19,28 +19,16 @@ namespace {
 // during U, S during D2.
 constexpr int kLinWorkers = 128 * kLinParts, kLinThreads = kLinWorkers + 32, kLinCtrl = kLinWorkers / 32;
 
-template <IO kIO>
-struct LinGeo {
-  static constexpr int kC = kIO == IO::BF16 ? 128 : 64;
-  static constexpr int kBlocks = kC / 16 / kLinParts;  // of 16 columns of P to a thread
-  static constexpr int kPWords = kIO == IO::BF16 ? 16 : 32;  // columns of tensor memory a block of P takes
-  static constexpr bool kBf16 = kIO == IO::BF16;
-  // columns of tensor memory: in bf16 P takes A's place, and the products with the state's and W's terms side by side
-  // (see umma_blocks) have 64 columns for each
-  static constexpr int kD = kBf16 ? 128 : 64;
-  static constexpr int tA = 0, tP = kBf16 ? 0 : 64, tD1 = kBf16 ? 128 : 192, tU = tD1 + kD, tO = tU + kD;
-  static_assert(tO + 64 <= 512, "tensor memory");
-};
+constexpr int kC = 64, kTerms = 3;  // tokens of a chunk, bf16 terms of a value
+constexpr int kBlockWords = 32;     // columns of tensor memory that a block of 16 columns of P takes, its terms one after the other
+constexpr int tA = 0, tP = 64, tD1 = 192, tU = 256, tO = 320;  // columns of tensor memory
 
-template <IO kIO, int KP>
+template <int KP>
 struct LinSmem {
-  using D = DeltaTerms<kIO>;
-  static constexpr int kC = LinGeo<kIO>::kC, kPanel = kC * 128;  // bytes of 64 columns of a chunk's rows
-  static constexpr int kX = D::kIn * KP * kPanel, kW = D::kIn * kPanel, kUp = D::kMid * kPanel;
-  static constexpr int kSTerm = KP * 64 * 128, kS = D::kMid * kSTerm;
-  static constexpr int kBufs = kIO == IO::BF16 ? 2 : 1;  // of Y and W
-  // (in f32 the products take 128 rows of X's 64: what follows it counts as rows whose results nobody reads)
-  static constexpr int oX = 0, oY = kX, oW = oY + kBufs * kX, oUp = oW + kBufs * kW, oS = oUp + kUp, oGates = oS + kS;
+  static constexpr int kPanel = kC * 128;  // bytes of 64 columns of a chunk's rows
+  static constexpr int kX = kTerms * KP * kPanel, kW = kTerms * kPanel, kSTerm = KP * 64 * 128, kS = kTerms * kSTerm;
+  // (the products take 128 rows of X's 64: what follows it counts as rows whose results nobody reads)
+  static constexpr int oX = 0, oY = kX, oW = oY + kX, oUp = oW + kW, oS = oUp + kW, oGates = oS + kS;
   // of the tokens: G / ln 2 as two floats; in and up; the two factors of P's weights
   static constexpr int oInUp = 8 * kC, oRow = 16 * kC, oCol = 20 * kC, kGates = 24 * kC;
   static constexpr int oEnd = oGates + 2 * kGates;       // exp(G_end) of either buffer, and whether the factors serve
@@ -49,19 +37,14 @@ struct LinSmem {
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ bool odd_bf16(uint32_t pair) {  // either half NaN or infinite
-  return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
-}
+// The six pairs of three terms whose product counts, smallest first.
+__device__ __forceinline__ int first_term(int i) { return (0x124 >> (2 * i)) & 3; }
+__device__ __forceinline__ int second_term(int i) { return (0x046 >> (2 * i)) & 3; }
 
-template <IO kIO, int KP, bool kStateOnly>
+template <int KP, bool kStateOnly>
 __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_constant__ LinArgs a, int roles, int all_tiles) {
-  using T = typename IoType<kIO>::type;
-  using L = LinSmem<kIO, KP>;
-  using G = LinGeo<kIO>;
-  using R = WalkRow<T, 2>;  // 16 columns to a thread
-  using RF = WalkRow<float, 2>;
-  constexpr int kC = L::kC, NQ = DeltaTerms<kIO>::kIn, NT = DeltaTerms<kIO>::kMid, kBufs = L::kBufs;
-  constexpr bool kBf16 = kIO == IO::BF16;
+  using L = LinSmem<KP>;
+  using R = WalkRow<float, 2>;  // 16 columns to a thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* bar_a = reinterpret_cast<uint64_t*>(sm + L::oBar);
@@ -149,48 +132,25 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
     return last;
   };
 
-  const T* xb = static_cast<const T*>(role.x) + start * role.sx + (int64_t)(h / role.rx) * n1;
-  const T* yb = static_cast<const T*>(role.y) + start * role.sy + (int64_t)(h / role.ry) * n1;
-  const T* wb = static_cast<const T*>(role.w) + start * role.sw + (int64_t)(h / role.rw) * n2 + tile * kLinTile;
+  const float* xb = static_cast<const float*>(role.x) + start * role.sx + (int64_t)(h / role.rx) * n1;
+  const float* yb = static_cast<const float*>(role.y) + start * role.sy + (int64_t)(h / role.ry) * n1;
+  const float* wb = static_cast<const float*>(role.w) + start * role.sw + (int64_t)(h / role.rw) * n2 + tile * kLinTile;
   const int wcols = n2 - tile * kLinTile;  // of W from this tile on
 
-  // bf16: rows of kPanels * 64 columns as an image, zero past the chunk's end and the width
-  auto copy_image = [&](uint8_t* image, const T* base, int64_t stride, int panels, int cols, int rows) {
-    const int per_row = panels * 8;
-#pragma unroll 4
-    for (int i = t; i < kC * per_row; i += kLinWorkers) {
-      const int r = i / per_row, ch = i - r * per_row;
-      const bool in = r < rows && ch * 8 < cols;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                       smem_u32(image + (ch >> 3) * L::kPanel + image_chunk<128>(r, ch & 7))),
-                   "l"(in ? base + r * stride + ch * 8 : base), "r"(in ? 16 : 0)
-                   : "memory");
-    }
-  };
-  auto load_x = [&](int c) {
-    if constexpr (kBf16 && !kStateOnly) {
-      copy_image(sm + L::oX, xb + (int64_t)c * kC * role.sx, role.sx, KP, n1, len - c * kC);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-  };
-  auto load_yw = [&](int c, int buf) {
-    if constexpr (kBf16) {
-      copy_image(sm + L::oY + buf * L::kX, yb + (int64_t)c * kC * role.sy, role.sy, KP, n1, len - c * kC);
-      copy_image(sm + L::oW + buf * L::kW, wb + (int64_t)c * kC * role.sw, role.sw, 1, wcols, len - c * kC);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-  };
   auto note_bad = [&](int which_buf, int col, int r) {
     if (back) atomicMax(s_bad + which_buf * 64 + col, r); else atomicMin(s_bad + which_buf * 64 + col, r);
     any_bad[which_buf] = 1;
   };
-  // f32: the images of X, Y, W and up * W, through registers
+  // The images of X, Y, W and up * W, through registers.  A value of W that is
+  // not finite reaches the state, and so every later row, through up * W; in D2,
+  // where 0 times it would reach earlier rows, 0 takes its place, and its
+  // column's rows from it on are made NaN when they are written.
   constexpr int kLoadX = kC * KP * 8 / kLinWorkers, kLoadW = kC * 8 / kLinWorkers;
-  auto load_f32 = [&](int c, int buf) {
-    if constexpr (!kBf16) {
+  auto load_images = [&](int c, int buf) {
+    {
       const int rows = len - c * kC;
       float4 x[kLoadX][2], y[kLoadX][2], w[kLoadW][2];
-      auto get = [&](float4 (&f)[2], const T* base, int64_t stride, int r, int ch, int cols) {
+      auto get = [&](float4 (&f)[2], const float* base, int64_t stride, int r, int ch, int cols) {
         f[0] = f[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (r < rows && ch * 8 < cols) {
           const float4* src = reinterpret_cast<const float4*>(base + (c * kC + r) * stride + ch * 8);
@@ -212,7 +172,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         auto put = [&](int o, const float4 (&f)[2]) {
           const float2 v[4] = {make_float2(f[0].x, f[0].y), make_float2(f[0].z, f[0].w), make_float2(f[1].x, f[1].y),
                                make_float2(f[1].z, f[1].w)};
-          put_chunk<NQ, 128>(sm + o + (ch >> 3) * L::kPanel, KP * L::kPanel, r, ch & 7, v);
+          put_chunk<kTerms, 128>(sm + o + (ch >> 3) * L::kPanel, KP * L::kPanel, r, ch & 7, v);
         };
         put(L::oY, y[u]);
         if (!kStateOnly) put(L::oX, x[u]);
@@ -230,7 +190,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
           up[i] = mul2(v[i], splat2(in_up[r].y));
           trace = fma2(v[i], splat2(0.0f), trace);
         }
-        put_chunk<NT, 128>(sm + L::oUp, L::kPanel, r, ch, up);
+        put_chunk<kTerms, 128>(sm + L::oUp, L::kPanel, r, ch, up);
         if (trace.x + trace.y != 0.0f) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -238,47 +198,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
             if (v[i].y * 0.0f != 0.0f) { note_bad(buf, ch * 8 + 2 * i + 1, r); v[i].y = 0.0f; }
           }
         }
-        if (!kStateOnly) put_chunk<NQ, 128>(sm + L::oW, L::kPanel, r, ch, v);
+        if (!kStateOnly) put_chunk<kTerms, 128>(sm + L::oW, L::kPanel, r, ch, v);
       }
     }
   };
-  // bf16: up * W from W's image.  A value of W that is not finite reaches the
-  // state, and so every later row, through up * W; in D2, where 0 times it would
-  // reach earlier rows, 0 takes its place, and its column's rows from it on are
-  // made NaN when they are written.
-  auto weigh = [&](int buf) {
-    if constexpr (kBf16) {
-      const float2* in_up = reinterpret_cast<const float2*>(sm + L::oGates + buf * L::kGates + L::oInUp);
-      uint8_t* image = sm + L::oW + buf * L::kW;
-#pragma unroll
-      for (int u = 0; u < kC * 8 / kLinWorkers; ++u) {
-        const int i = t + u * kLinWorkers, r = i / 8, ch = i % 8;
-        uint4* at = reinterpret_cast<uint4*>(image + image_chunk<128>(r, ch));
-        const uint4 q = *at;
-        float2 v[4];
-        unpack(q, v);
-        float2 trace = splat2(0.0f);
-        const float f = in_up[r].y;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          trace = fma2(v[k], splat2(0.0f), trace);
-          v[k] = mul2(v[k], splat2(f));
-        }
-        put_chunk<NT, 128>(sm + L::oUp, L::kPanel, r, ch, v);
-        if (!kStateOnly && trace.x + trace.y != 0.0f) {
-          uint32_t p[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (odd_bf16(p[k])) {
-              if ((p[k] & 0x7f80u) == 0x7f80u) { note_bad(buf, ch * 8 + 2 * k, r); p[k] &= 0xffff0000u; }
-              if ((p[k] & 0x7f800000u) == 0x7f800000u) { note_bad(buf, ch * 8 + 2 * k + 1, r); p[k] &= 0xffffu; }
-            }
-          *at = make_uint4(p[0], p[1], p[2], p[3]);
-        }
-      }
-    }
-  };
-
   const int quad = warp & 3, part = (warp >> 2) & (kLinParts - 1), row = quad * 32 + lane;
   const int col0 = tile * kLinTile + part * 16;  // this thread's columns of the state and of the results
   const bool state_row = row < n1 && warp < kLinCtrl;
@@ -310,83 +233,88 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   LinWaiter wait{a, stop};
   auto chunk_of = [&](int k) { return back ? n - 1 - k : k; };
 
-  if (warp == kLinCtrl) {
+  if (warp == kLinCtrl) {  // all lanes go through it together, so that addresses are uniform; one issues
+    const bool lead = lane == 0;
     Pair total{0.0f, 0.0f};
     if (n > 0) total = make_gates(chunk_of(0), 0);
-    if (!kBf16 && n > 0) named_barrier(4, kLinThreads);
+    if (n > 0) named_barrier(4, kLinThreads);
     for (int k = 0; k < n; ++k) {
-      const int buf = k & 1, lb = kBufs == 2 ? buf : 0;
+      const int buf = k & 1;
       if (lane == 0) *leave = *stop;
       named_barrier(1, kLinThreads);
       if (*leave) break;
-      const uint32_t sx = smem_u32(sm + L::oX), sy = smem_u32(sm + L::oY + lb * L::kX), sw = smem_u32(sm + L::oW + lb * L::kW);
-      if (!kStateOnly && lane == 0 && !*stop) {
+      const uint64_t x = smem_desc<128>(smem_u32(sm + L::oX)), y = smem_desc<128>(smem_u32(sm + L::oY));
+      if (!kStateOnly && !*stop) {
         tmem_fence_after_sync();
-        const Operand<128, kKMajor, NQ, KP * L::kPanel, L::kPanel> X(sx), Y(sy);
-        umma_terms<kC, KP * 4, NQ>(tm + G::tA, X, Y, false);
-        umma_commit(bar_a);
+        constexpr uint32_t idesc = umma_idesc(kKMajor, kKMajor, kC), idesc_s = umma_idesc(kKMajor, kMnMajor, 64);
+#pragma unroll 1
+        for (int i = 0; i < 6 * KP; ++i) {
+          const int first = first_term(i / KP), second = second_term(i / KP), panel = i % KP;
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            umma_if(lead, tm + tA, x + ((first * KP + panel) * L::kPanel + s * 32) / 16,
+                    y + ((second * KP + panel) * L::kPanel + s * 32) / 16, idesc, i + s > 0 ? 1u : 0u);
+        }
+        if (lead) umma_commit(bar_a);
         if (k > 0 || has_carry) {
-          const Operand<128, kMnMajor, NT, L::kSTerm, 0, L::kSTerm> St(smem_u32(sm + L::oS));
-          if constexpr (kBf16) umma_blocks<64, KP * 4, NT, true>(tm + G::tD1, X, St);
-          else umma_terms<64, KP * 4, NT>(tm + G::tD1, X, St, false);
+          const uint64_t st = smem_desc<128>(smem_u32(sm + L::oS), L::kSTerm);
+#pragma unroll 1
+          for (int i = 0; i < 6 * KP; ++i) {
+            const int first = first_term(i / KP), second = second_term(i / KP), panel = i % KP;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              umma_if(lead, tm + tD1, x + ((first * KP + panel) * L::kPanel + s * 32) / 16,
+                      st + (second * L::kSTerm + (4 * panel + s) * 2048) / 16, idesc_s, i + s > 0 ? 1u : 0u);
+          }
         }
       }
       __syncwarp();
       named_barrier(2, kLinThreads);
-      if (lane == 0 && !*stop) {
+      if (!*stop) {
         tmem_fence_after_sync();
-        const Operand<128, kMnMajor, NQ, KP * L::kPanel, 0, L::kPanel> Yt(sy);
-        const Operand<128, kMnMajor, NT, L::kPanel, 0, L::kPanel> Up(smem_u32(sm + L::oUp));
-        if constexpr (kBf16) umma_blocks<64, kC / 16, NT, true>(tm + G::tU, Yt, Up);
-        else umma_terms<64, kC / 16, NT>(tm + G::tU, Yt, Up, false);
-        umma_commit(bar_u);
+        constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, 64);
+        const uint64_t yt = smem_desc<128>(smem_u32(sm + L::oY), L::kPanel), up = smem_desc<128>(smem_u32(sm + L::oUp), L::kPanel);
+#pragma unroll 1
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+          for (int s = 0; s < kC / 16; ++s)
+            umma_if(lead, tm + tU, yt + (first_term(i) * KP * L::kPanel + s * 2048) / 16, up + (second_term(i) * L::kPanel + s * 2048) / 16,
+                    idesc, i + s > 0 ? 1u : 0u);
+        if (lead) umma_commit(bar_u);
       }
       __syncwarp();
       if (k + 1 < n) total = add(total, make_gates(chunk_of(k + 1), buf ^ 1));
       if constexpr (!kStateOnly) {
         named_barrier(3, kLinThreads);
-        if (lane == 0 && !*stop) {
+        if (!*stop) {
           tmem_fence_after_sync();
-          const Operand<128, kMnMajor, NQ, L::kPanel> W(sw);
           constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, 64);
-          uint32_t acc = 0;
+          const uint64_t w = smem_desc<128>(smem_u32(sm + L::oW));
+#pragma unroll 1
+          for (int i = 0; i < 6; ++i)
 #pragma unroll
-          for (int sum = NT - 1; sum >= 0; --sum)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const int j = sum - i;
-              if (j < 0 || j >= NQ) continue;
-#pragma unroll
-              for (int s = 0; s < kC / 16; ++s) {
-                umma_ta(tm + G::tO, tm + G::tP + G::kPWords * s + 8 * i, W.at(j, s), idesc, acc);
-                acc = 1;
-              }
-            }
-          umma_commit(bar_o);
+            for (int s = 0; s < kC / 16; ++s)
+              umma_ta_if(lead, tm + tO, tm + tP + kBlockWords * s + 8 * first_term(i), w + (second_term(i) * L::kPanel + s * 2048) / 16,
+                         idesc, i + s > 0 ? 1u : 0u);
+          if (lead) umma_commit(bar_o);
         }
         __syncwarp();
       }
-      if (!kBf16 && k + 1 < n) named_barrier(4, kLinThreads);
+      if (k + 1 < n) named_barrier(4, kLinThreads);
     }
     if (kStateOnly && lane == 0 && tile == 0) role.decay[item * a.Hv + h] = exp2_of(total);
   } else {
     uint32_t phase = 0;
     if (n > 0) {
-      if constexpr (kBf16) {
-        load_x(chunk_of(0));
-        load_yw(chunk_of(0), 0);
-      } else {
-        named_barrier(4, kLinThreads);  // the gates
-        load_f32(chunk_of(0), 0);
-      }
+      named_barrier(4, kLinThreads);  // the gates
+      load_images(chunk_of(0), 0);
     }
     if (!kStateOnly && has_carry && row < KP * 64)
-      put_row<NT, 128>(sm + L::oS, L::kSTerm, row, part * 2, S);
+      put_row<kTerms, 128>(sm + L::oS, L::kSTerm, row, part * 2, S);
     for (int k = 0; k < n; ++k, phase ^= 1) {
-      const int c = chunk_of(k), buf = k & 1, lb = kBufs == 2 ? buf : 0;
+      const int c = chunk_of(k), buf = k & 1;
       const int rows = min(kC, len - c * kC);
       const bool more = k + 1 < n, has_state = k > 0 || has_carry;
-      if constexpr (kBf16) asm volatile("cp.async.wait_group 0;" ::: "memory");
       fence_async_smem();
       tmem_fence_before_sync();
       named_barrier(1, kLinThreads);
@@ -394,9 +322,6 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
       if (*leave) break;
       if (t < 64) s_bad[(buf ^ 1) * 64 + t] = bad_none();
       if (t == 0) any_bad[buf ^ 1] = 0;
-      if (more) load_yw(chunk_of(k + 1), lb ^ 1);
-      weigh(lb);
-      fence_async_smem();
       asm volatile("bar.arrive %0, %1;" ::"r"(2), "r"(kLinThreads) : "memory");
 
       if constexpr (!kStateOnly) {
@@ -408,16 +333,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
           // the columns a row sees: fwd j < see, back see <= j < rows
           const int see = back ? row + (has_dot ? 1 : 0) : row + (has_dot ? 0 : 1);
           const bool near = s_near[buf];
+          {
+            const int j0 = 16 * part;
+            uint32_t words[kBlockWords];
 #pragma unroll
-          for (int u = 0; u < G::kBlocks; ++u) {
-            // the blocks of a part are one from either end: P is triangular
-            const int block = u == 0 ? part : 2 * kLinParts - 1 - part, j0 = 16 * block;
-            uint32_t words[G::kPWords];
-#pragma unroll
-            for (int i = 0; i < G::kPWords; ++i) words[i] = 0;
+            for (int i = 0; i < kBlockWords; ++i) words[i] = 0;
             if (back ? j0 + 15 >= quad * 32 && j0 < rows : j0 <= quad * 32 + 31) {  // the warp has rows that see these columns
               float2 d[8];
-              tmem_sum<1>(tm + G::tA + lane_at + j0, 0, d);
+              tmem_sum<1>(tm + tA + lane_at + j0, 0, d);
               const bool all = back ? j0 > quad * 32 + 31 && j0 + 15 < rows : j0 + 15 < quad * 32;
               if (!all && has_dot) {
 #pragma unroll
@@ -453,15 +376,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                uint32_t term[NT];
-                split_pair<NT>(d[i], term);
+                uint32_t term[kTerms];
+                split_pair<kTerms>(d[i], term);
 #pragma unroll
-                for (int q = 0; q < NT; ++q) words[8 * q + i] = term[q];
+                for (int q = 0; q < kTerms; ++q) words[8 * q + i] = term[q];
               }
             }
             __syncwarp();
-            if constexpr (kBf16) tmem_st16(tm + G::tP + lane_at + j0, words);
-            else tmem_st32(tm + G::tP + lane_at + 2 * j0, words);
+            tmem_st32(tm + tP + lane_at + 2 * j0, words);
           }
           tmem_wait_st();
         }
@@ -471,14 +393,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
 
       wait(bar_u, phase, kStateOnly && k == 0 && t == 0 && forced_here(a));
       tmem_fence_after_sync();
-      if (more) load_x(chunk_of(k + 1));
       if (row < KP * 64) {
         const float end = s_end[buf];
         float2 d[8];
-        tmem_sum<kBf16 ? NT : 1>(tm + G::tU + lane_at + part * 16, 64, d);
+        tmem_sum<1>(tm + tU + lane_at + part * 16, 64, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) S[i] = fma2(splat2(end), S[i], d[i]);
-        if (!kStateOnly && more) put_row<NT, 128>(sm + L::oS, L::kSTerm, row, part * 2, S);
+        if (!kStateOnly && more) put_row<kTerms, 128>(sm + L::oS, L::kSTerm, row, part * 2, S);
       }
 
       if constexpr (!kStateOnly) {
@@ -487,17 +408,17 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         if (row < kC) {
           const int64_t at = (int64_t)c * kC + quad * 32;  // the warp's first token
           float2 o[8];
-          tmem_sum<1>(tm + G::tO + lane_at + part * 16, 0, o);
+          tmem_sum<1>(tm + tO + lane_at + part * 16, 0, o);
           if (has_state) {
             const float in = reinterpret_cast<const float2*>(sm + L::oGates + buf * L::kGates + L::oInUp)[row].x;
             float2 e[8];
-            tmem_sum<kBf16 ? NT : 1>(tm + G::tD1 + lane_at + part * 16, 64, e);
+            tmem_sum<1>(tm + tD1 + lane_at + part * 16, 64, e);
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(in), e[i], o[i]);
           }
           if (has_dot) {  // rho or sigma, then the token's own pair
             typename R::Raw raw;
-            R::load(static_cast<const T*>(role.dot) + (start + at) * role.sdot + (int64_t)(h / role.rdot) * n2 + col0, role.sdot,
+            R::load(static_cast<const float*>(role.dot) + (start + at) * role.sdot + (int64_t)(h / role.rdot) * n2 + col0, role.sdot,
                     len - at, n2 - col0, lane, raw);
 #pragma unroll
             for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
@@ -509,9 +430,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
             for (int q = 0; q < 2; ++q) {
               const uint32_t place = image_chunk<128>(row, part * 2 + q);
 #pragma unroll
-              for (int term = NQ - 1; term >= 0; --term) {
+              for (int term = kTerms - 1; term >= 0; --term) {
                 float2 w[4];
-                unpack(*reinterpret_cast<const uint4*>(sm + L::oW + lb * L::kW + term * L::kPanel + place), w);
+                unpack(*reinterpret_cast<const uint4*>(sm + L::oW + term * L::kPanel + place), w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[4 * q + i] = fma2(splat2(self), w[i], o[4 * q + i]);
               }
@@ -527,24 +448,16 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
             }
           }
           const int64_t out_at = ((start + at) * a.Hv + h) * n2 + col0;
-          auto store = [&](auto rows_of, auto* base) {
-            using Q = decltype(rows_of);
-            typename Q::Raw raw;
-            Q::put(raw, 0, o);
-            Q::store(base + out_at, (int64_t)a.Hv * n2, len - at, n2 - col0, lane, raw);
-          };
-          if (kBf16 && role.part) store(RF(), static_cast<float*>(role.out));
-          else store(R(), static_cast<T*>(role.out));
+          typename R::Raw raw;
+          R::put(raw, 0, o);
+          R::store(static_cast<float*>(role.out) + out_at, (int64_t)a.Hv * n2, len - at, n2 - col0, lane, raw);
         }
       }
-      if constexpr (!kBf16) {
-        if (more) {
-          named_barrier(4, kLinThreads);  // everyone is through with the images, and the next gates are there
-          load_f32(chunk_of(k + 1), buf ^ 1);
-        }
+      if (more) {
+        named_barrier(4, kLinThreads);  // everyone is through with the images, and the next gates are there
+        load_images(chunk_of(k + 1), buf ^ 1);
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
     // the state the segment leaves
     float* to = nullptr;
     if (kStateOnly) to = role.slots + (item * a.Hv + h) * state_size;
@@ -583,24 +496,17 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   }
 }
 
-template <IO kIO, int KP, bool kStateOnly>
+template <int KP, bool kStateOnly>
 cudaError_t run_walk(const LinArgs& a, int roles, cudaStream_t st) {
-  constexpr size_t bytes = LinSmem<kIO, KP>::kBytes;
+  constexpr size_t bytes = LinSmem<KP>::kBytes;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = set_smem(reinterpret_cast<const void*>(lin_walk_kernel<kIO, KP, kStateOnly>), bytes, done);
+  cudaError_t e = set_smem(reinterpret_cast<const void*>(lin_walk_kernel<KP, kStateOnly>), bytes, done);
   if (e != cudaSuccess) return e;
   int tiles = 0;
   for (int i = 0; i < roles; ++i) tiles += lin_tiles(a.role[i].n2);
   const int64_t blocks = (kStateOnly ? a.max_inner : a.max_segs) * a.Hv * tiles;
-  lin_walk_kernel<kIO, KP, kStateOnly><<<(unsigned)blocks, kLinThreads, bytes, st>>>(a, roles, tiles);
+  lin_walk_kernel<KP, kStateOnly><<<(unsigned)blocks, kLinThreads, bytes, st>>>(a, roles, tiles);
   return cudaGetLastError();
-}
-
-template <IO kIO, bool kStateOnly>
-cudaError_t pick_walk(const LinArgs& a, int roles, cudaStream_t st) {
-  int width = 0;
-  for (int i = 0; i < roles; ++i) width = width > a.role[i].n1 ? width : a.role[i].n1;
-  return width > 64 ? run_walk<kIO, 2, kStateOnly>(a, roles, st) : run_walk<kIO, 1, kStateOnly>(a, roles, st);
 }
 
 }  // namespace
@@ -608,7 +514,10 @@ cudaError_t pick_walk(const LinArgs& a, int roles, cudaStream_t st) {
 cudaError_t launch_lin_walk(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, IO io, cudaStream_t st) {
   if (io == IO::BF16) return launch_lin_walk_bf16(a, maps, roles, state_only, st);
   if ((state_only ? a.max_inner : a.max_segs) == 0) return cudaSuccess;
-  return state_only ? pick_walk<IO::F32, true>(a, roles, st) : pick_walk<IO::F32, false>(a, roles, st);
+  int width = 0;
+  for (int i = 0; i < roles; ++i) width = width > a.role[i].n1 ? width : a.role[i].n1;
+  if (width > 64) return state_only ? run_walk<2, true>(a, roles, st) : run_walk<2, false>(a, roles, st);
+  return state_only ? run_walk<1, true>(a, roles, st) : run_walk<1, false>(a, roles, st);
 }
 
 }  // namespace vssm

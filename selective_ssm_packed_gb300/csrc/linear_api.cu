@@ -22,9 +22,9 @@ int check_lin_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
 // no fewer than two chunks.
 int lin_segment(int64_t T, int64_t S, int Hv, int ctas, IO io) {
   const int64_t chunk = lin_chunk(io), share = T * Hv * ctas / 152, longest = 4 * T / (S > 0 ? S : 1);
-  if (longest <= share) return 4096;
+  if (longest <= share) return kLinMaxSegment;
   int64_t seg = (share / 4 + chunk - 1) / chunk * chunk;
-  seg = seg < 2 * chunk ? 2 * chunk : seg > 4096 ? 4096 : seg;
+  seg = seg < 2 * chunk ? 2 * chunk : seg > kLinMaxSegment ? kLinMaxSegment : seg;
   return (int)seg;
 }
 

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs a, int blocks) {
 // the segment's tokens, which it sums up first and then walks from its end.
 // Sums are of two floats: a token's dg is the sum of all later differences, in
 // which most cancels.
-constexpr int kDgHeads = 2, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads;
+constexpr int kDgHeads = 2, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads, kDgPer = kLinMaxSegment / kDgParts;
 
 __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts_q, int parts_v, int tiles) {
   __shared__ Pair sums[2][kDgThreads];
@@ -164,9 +164,11 @@ __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts
     }
     return v;
   };
-  Pair own{0.0f, 0.0f};
-#pragma unroll 4
-  for (int i = hi - 1; i >= lo; --i) own = add(own, diff(i));
+  Pair d[kDgPer], own{0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kDgPer; ++i) d[i] = lo + i < hi ? diff(lo + i) : Pair{0.0f, 0.0f};
+#pragma unroll
+  for (int i = kDgPer - 1; i >= 0; --i) own = add(own, d[i]);
   sums[0][t] = own;
   __syncthreads();
   int from = 0;  // the sums over this part and the next 1, 3, 7, ..
@@ -177,10 +179,11 @@ __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts
   Pair run = part + 1 < kDgParts ? sums[from][t + kDgHeads] : Pair{0.0f, 0.0f}, total{0.0f, 0.0f};
   if (in)
     for (int i = 0; i < tiles; ++i) run = add(run, Pair{a.role[0].cross[((int64_t)seg * a.Hv + h) * tiles + i], 0.0f});
-#pragma unroll 4
-  for (int i = hi - 1; i >= lo; --i) {
-    run = add(run, diff(i));
-    if (a.g_token) a.dg[((int64_t)entry.y + i) * a.Hv + h] = run.hi + run.lo;
+#pragma unroll
+  for (int i = kDgPer - 1; i >= 0; --i) {
+    if (lo + i >= hi) continue;
+    run = add(run, d[i]);
+    if (a.g_token) a.dg[((int64_t)entry.y + lo + i) * a.Hv + h] = run.hi + run.lo;
     else total = add(total, run);
   }
   if (a.g_token) return;

@@ -524,8 +524,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         for (int s = 0; s < kRuns; ++s) r[s].load(from + 16 * s, cols - 16 * s, whole_dot);
       }
       if (warp == kStateWarps) {
-        wait(bars + kUpReady, p);  // what weigh() found
-        wait(bars + kDoneO, p);
+        wait(bars + kDoneO, p);  // behind the weighing of this chunk, too
       }
       named_barrier(2, 32 * kOutWarps);
       tmem_fence_after_sync();
@@ -575,11 +574,25 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         const uint64_t x = smem_desc<128>(smem_u32(sm + L::oX)), y = smem_desc<128>(smem_u32(sm + L::oY));
         const uint64_t yt = smem_desc<128>(smem_u32(sm + L::oY), kPanel);
         const uint64_t up = smem_desc<128>(smem_u32(sm + L::oUp), kPanel), st = smem_desc<128>(smem_u32(sm + L::oS), L::kSBlock);
+        // W's copies are asked for here, in the order of the products that use it: whoever waits for a phase has to
+        // have done so before it can come around again
+        int ws[2] = {0, 0};
+        auto load_w = [&](int k) {
+          const int b = two_w ? k & 1 : 0;
+          mbar_arrive_expect_tx(bars + kFullW + b, (uint32_t)L::kW);
+          copy_panels(maps.m + role.mw, w_image(k), NP, h / role.rw, seg.start + (int64_t)chunk_of(k) * kC, bars + kFullW + b);
+          ++ws[b];
+        };
+        if (lead && n > 0) load_w(0);
+        if (lead && two_w && n > 1) load_w(1);
         for (int k = 0; k < n; ++k) {
           const uint32_t p = k & 1;
           wait(bars + kFullX, p, k == 0 && forced_here(a));
           wait(bars + kFullY, p);
-          if (k > 0) wait(bars + kDoneO, p ^ 1);  // P's place
+          if (k > 0) {
+            wait(bars + kDoneO, p ^ 1);  // P's place, and W's
+            if (lead && wait.ok && k + (two_w ? 1 : 0) < n) load_w(k + (two_w ? 1 : 0));
+          }
           if (__all_sync(0xffffffffu, wait.ok)) {
             tmem_fence_after_sync();
             constexpr uint32_t idesc = umma_idesc(kKMajor, kKMajor, kC);
@@ -606,51 +619,39 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
             }
             if (lead) umma_commit(bars + kDoneX);
           }
-          // the other two in the order in which their operands come
-          const uint64_t w = smem_desc<128>(smem_u32(w_image(k)), kPanel);
-          bool need_u = true, need_o = true;
-          int tries = 0;
-          while (need_u || need_o) {
-            const bool alone = !(need_u && need_o);
-            bool now_u = need_u, now_o = need_o;
-            if (!alone) {
-              now_u = __all_sync(0xffffffffu, mbar_try_wait(bars + kUpReady, p));
-              now_o = !now_u && __all_sync(0xffffffffu, mbar_try_wait(bars + kPReady, p));
-              if (!now_u && !now_o) {
-                if (++tries < 256) continue;
-                now_u = true;  // a wait with a limit
-              }
-            }
-            wait(bars + (now_u ? kUpReady : kPReady), p);
-            if (!__all_sync(0xffffffffu, wait.ok)) break;
+          wait(bars + kUpReady, p);
+          if (__all_sync(0xffffffffu, wait.ok)) {
             tmem_fence_after_sync();
-            if (now_u) {
-              constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, kN);
+            constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, kN);
 #pragma unroll 1
-              for (int i = 0; i < 4; ++i) {
-                const int term = 1 - i / 2;
+            for (int i = 0; i < 4; ++i) {
+              const int term = 1 - i / 2;
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                  umma_if(lead, tm + tU, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc,
-                          1u);
-              }
-              if (lead) umma_commit(bars + kDoneU);
-              need_u = false;
-            } else {
-              constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
-              const int i0 = terms == 2 ? 0 : 2;
-#pragma unroll 1
-              for (int i = i0; i < 4; ++i) {
-                const int term = 1 - i / 2;
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                  umma_ta_if(lead, tm + tO, tm + tA + 16 * ((i & 1) * 4 + s) + 8 * term, w + ((i & 1) * 4 + s) * (kStep / 16), idesc,
-                             i - i0 + s > 0 ? 1u : 0u);
-              }
-              if (lead) umma_commit(bars + kDoneO);
-              need_o = false;
+              for (int s = 0; s < 4; ++s)
+                umma_if(lead, tm + tU, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc, 1u);
             }
+            if (lead) umma_commit(bars + kDoneU);
           }
+          wait(bars + kPReady, p);
+          if (__all_sync(0xffffffffu, wait.ok)) {
+            tmem_fence_after_sync();
+            const uint64_t w = smem_desc<128>(smem_u32(w_image(k)), kPanel);
+            constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
+            constexpr int i0 = terms == 2 ? 0 : 2;
+#pragma unroll 1
+            for (int i = i0; i < 4; ++i) {
+              const int term = 1 - i / 2;
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                umma_ta_if(lead, tm + tO, tm + tA + 16 * ((i & 1) * 4 + s) + 8 * term, w + ((i & 1) * 4 + s) * (kStep / 16), idesc,
+                           i - i0 + s > 0 ? 1u : 0u);
+            }
+            if (lead) umma_commit(bars + kDoneO);
+          }
+        }
+        if (lead) {  // what is on its way comes in before the memory is given back
+          drain_copies(bars + kFullW, ws[0]);
+          drain_copies(bars + kFullW2, ws[1]);
         }
         if (lead && *stop) {  // products that were not waited for
           umma_commit(bars + kDrained);
@@ -660,33 +661,22 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       __syncwarp();
     } else if (warp == kCopies) {
       if (lane == 0 && n > 0) {
-        int xs = 0, ys = 0, ws = 0, ws2 = 0;  // copies asked for
-        const int head_x = h / role.rx, head_y = h / role.ry, head_w = h / role.rw;
-        // X, Y and W in turn, each once the products are through with what is in its place; W a chunk ahead
-        // where it has two buffers
+        int asked = 0;
+        // X and Y in turn, each once the products are through with what is in its place
 #pragma unroll 1
-        for (int i = two_w ? -1 : 0; i < 3 * n; ++i) {
-          const int op = i < 0 ? 2 : i % 3, k = i < 0 ? 0 : i / 3 + (two_w && op == 2 ? 1 : 0);
-          if (k >= n) continue;
-          const int before = op == 2 && two_w ? k - 2 : k - 1;
-          if (before >= 0) wait(bars + (op == 0 ? kDoneX : op == 1 ? kDoneU : kDoneO), before & 1);
+        for (int i = 0; i < 2 * n; ++i) {
+          const int k = i / 2;
+          const bool is_x = i % 2 == 0;
+          if (k > 0) wait(bars + (is_x ? kDoneX : kDoneU), (k - 1) & 1);
           if (!wait.ok) break;
-          const int panels = op == 2 ? NP : KP;
-          uint64_t* bar = bars + (op == 0 ? kFullX : op == 1 ? kFullY : two_w && (k & 1) ? kFullW2 : kFullW);
-          uint8_t* to = op == 0 ? sm + L::oX : op == 1 ? sm + L::oY : w_image(k);
-          mbar_arrive_expect_tx(bar, (uint32_t)(panels * kPanel));
-          copy_panels(maps.m + (op == 0 ? role.mx : op == 1 ? role.my : role.mw), to, panels,
-                      op == 0 ? head_x : op == 1 ? head_y : head_w, seg.start + (int64_t)chunk_of(k) * kC, bar);
-          if (op == 0) ++xs;
-          else if (op == 1) ++ys;
-          else if (two_w && (k & 1)) ++ws2;
-          else ++ws;
+          uint64_t* bar = bars + (is_x ? kFullX : kFullY);
+          mbar_arrive_expect_tx(bar, (uint32_t)L::kX);
+          copy_panels(maps.m + (is_x ? role.mx : role.my), sm + (is_x ? L::oX : L::oY), KP, is_x ? h / role.rx : h / role.ry,
+                      seg.start + (int64_t)chunk_of(k) * kC, bar);
+          ++asked;
         }
-        // what is on its way comes in before the memory is given back
-        drain_copies(bars + kFullX, xs);
-        drain_copies(bars + kFullY, ys);
-        drain_copies(bars + kFullW, ws);
-        drain_copies(bars + kFullW2, ws2);
+        drain_copies(bars + kFullX, (asked + 1) / 2);
+        drain_copies(bars + kFullY, asked / 2);
       }
       __syncwarp();
     } else if (warp == kGatesWarp) {
@@ -784,7 +774,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   constexpr int kN = NP * 64, kCols = NP * 32;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
-  uint64_t *full = bars, *gates_full = bars + 2, *used = bars + 4, *up_ready = bars + 6, *done = bars + 7, *drained = bars + 8;
+  uint64_t *full = bars, *gates_full = bars + 2, *used = bars + 4, *up_ready = bars + 6, *done = bars + 7, *drained = bars + 9;
   float* s_total = reinterpret_cast<float*>(sm + L::oMisc);
   volatile int* stop = reinterpret_cast<int*>(s_total + 1);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(s_total + 2);
@@ -797,7 +787,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int n1 = role.n1, n2 = role.n2, n = seg.n;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, row = quad * 32 + lane;
   if (t == 0) {
-    for (int i = 0; i < 9; ++i) mbar_init(bars + i, i == 6 || (i == 4 || i == 5) ? kWeighWarps : 1);
+    for (int i = 0; i < 10; ++i) mbar_init(bars + i, i == 6 || (i == 4 || i == 5) ? kWeighWarps : 1);
     *stop = 0;
     fence_mbar_init();
   }
@@ -826,7 +816,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             umma_if(lead, tm, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc,
                     k + i + s > 0 ? 1u : 0u);
         }
-        if (lead) umma_commit(done);
+        if (lead) umma_commit(done + (k & 1));
       }
       __syncwarp();
     }
@@ -848,7 +838,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       };
       for (int k = 0; k < 2 && k < n; ++k) load(k);
       for (int k = 0; k + 2 < n; ++k) {
-        wait(done, k & 1);  // Y's buffer; W's was read before
+        wait(done + (k & 1), (k >> 1) & 1);  // Y's buffer; W's was read before
         if (wait.ok) load(k + 2);
       }
       for (int b = 0; b < 2; ++b) drain_copies(full + b, asked[b]);
@@ -892,7 +882,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (warp == 0) {
         wait(gates_full + b, (k >> 1) & 1);
         wait(full + b, (k >> 1) & 1);
-        if (k > 0) wait(done, (k - 1) & 1);  // up * W's place is free
+        if (k > 0) wait(done + ((k - 1) & 1), ((k - 1) >> 1) & 1);  // up * W's place is free
       }
       named_barrier(1, 32 * kWeighWarps);
       if (rows < kC) {
@@ -906,7 +896,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       warp_arrive(used + b, lane);
       if (lane == 0) mbar_arrive(up_ready);
     }
-    if (warp == 0) wait(done, (n - 1) & 1);
+    if (warp == 0) wait(done + ((n - 1) & 1), ((n - 1) >> 1) & 1);
     named_barrier(1, 32 * kWeighWarps);
     tmem_fence_after_sync();
     if (warp < kStateWarps) {

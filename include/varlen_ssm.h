@@ -456,11 +456,15 @@ int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t
  * g: f32 log decays, usually <= 0 (values below -256 are taken as -256: both
  *   decay to zero).  g_per_token != 0: (T, Hv); 0: (Hv), one decay a head for
  *   every token.
- * Precision as the gated delta rule's: FP32 operands of the tensor cores'
- *   products are sums of bf16 terms, three for f32 I/O, two for bf16 I/O;
- *   accumulation and the state are float32.
+ * Precision: FP32 operands of the tensor cores' products are sums of bf16
+ *   terms, three for f32 I/O, two for bf16 I/O; accumulation and the state
+ *   are float32.  With bf16 I/O the weights of pairs and the state that a
+ *   token's query meets are one term on the way to out, which adds about one
+ *   rounding to bf16 to that of out itself; final_states has 16 bits or more.
  * A value that is not finite reaches what the recurrence carries it to and
- *   nothing else, as there.
+ *   nothing else, as there; beside a g that is not finite the earlier tokens
+ *   of its chunk (of 64 tokens in f32, 128 in bf16) keep their values, but
+ *   not their last bits.
  * Long sequences are cut into segments that are walked at once; their length
  *   goes by the sizes alone (vssm_linear_attn_segment), so equal calls have
  *   equal bits.

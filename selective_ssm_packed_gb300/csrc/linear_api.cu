@@ -18,14 +18,17 @@ int check_lin_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
 // which dg's sums run).  An SM has `share` tokens to walk; where no sequence is
 // likely to be longer than that (the longest is taken for four times the mean:
 // only the GPU knows it) they are better left whole, which spares the walk
-// before and the scan; otherwise a quarter of it each fills the GPU evenly, but
-// no fewer than two chunks.
+// before and the scan (32768 packed tokens of 32 heads in bf16: 360 us, and 436
+// in segments of 1792); otherwise a quarter of it each fills the GPU evenly, but
+// no fewer than 256 tokens (3001 of 6 heads in f32: 82 us, 97 with 128, 105 with
+// 384; 4000 of 8 in bf16: 48 us, 63 with 128, 55 with 512), and no pack of 512
+// is worth it (500 tokens in bf16: 30 us, 35 with 256).
 int lin_segment(int64_t T, int64_t S, int Hv, int ctas, IO io) {
   const int64_t chunk = lin_chunk(io), share = T * Hv * ctas / 152, longest = 4 * T / (S > 0 ? S : 1);
   if (longest <= share) return kLinMaxSegment;
   int64_t seg = (share / 4 + chunk - 1) / chunk * chunk;
-  seg = seg < 2 * chunk ? 2 * chunk : seg > kLinMaxSegment ? kLinMaxSegment : seg;
-  return (int)seg;
+  const int64_t least = T <= 512 ? 512 : 256;
+  return (int)(seg < least ? least : seg > kLinMaxSegment ? kLinMaxSegment : seg);
 }
 
 struct LinLayout {
@@ -70,8 +73,8 @@ int check_lin_pack(int64_t T, int32_t S, const int32_t* cu, int32_t Hk, int32_t 
   if (T > 0 && S < 1) return bad(VSSM_ERR_ARG, "%lld tokens but num_seqs = %d", (long long)T, S);
   if (!cu) return bad(VSSM_ERR_ARG, "cu_seqlens is NULL");
   TRY(check_lin_heads(Hk, Hv, K, V));
-  // segments (at least 128 tokens each but the sequences' last), heads and tiles of three roles
-  if ((T / 128 + S) * Hv * 6 > 2147483647LL)
+  // segments (at least 256 tokens each but the sequences' last), heads and tiles of three roles
+  if ((T / 256 + S) * Hv * 6 > 2147483647LL)
     return bad(VSSM_ERR_UNSUPPORTED, "too many sequences, tokens and heads for one call");
   return VSSM_OK;
 }

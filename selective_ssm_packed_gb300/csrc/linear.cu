@@ -466,9 +466,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
       to[at] = S[i].x;
       to[at + role.scol] = S[i].y;
     });
-    if (!kStateOnly && role.cross) {
-      const float* e = is_last ? (role.against_last ? role.against_last + ((int64_t)entry.x * a.Hv + h) * state_size : nullptr)
-                               : role.against + (inner_before * a.Hv + h) * state_size;
+    if (!kStateOnly && role.cross && (!back || is_first)) {
+      const float* e = nullptr;
+      if (!back && !is_last) e = role.against + (inner_before * a.Hv + h) * state_size;
+      else if (role.against_last) e = role.against_last + ((int64_t)entry.x * a.Hv + h) * state_size;
       float2 sum = splat2(0.0f);
       if (e) state_io([&](int i, int64_t at) { sum = fma2(S[i], make_float2(e[at], e[at + role.scol]), sum); });
       float v = sum.x + sum.y;

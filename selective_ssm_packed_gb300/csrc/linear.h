@@ -23,10 +23,19 @@
 // the states S1 and S0.)  A pair of tokens s < t adds W_ts = scale exp(..) (q_t.k_s)
 // (do_t.v_s) to dg of every token in (s, t], so
 //   dg_t = sum over i >= t of (rho_i - sigma_i) + <gradient of S_end, S_end>,
-//   rho_t = q_t . (dq_t without s = t),  sigma_s = v_s . (dv_s without t = s),
-// the sum over the rest of the token's segment, S_end the state at its end.  The
-// bf16 walks' dots have the token's own pair in them, the weight that P had for
-// it times q.k or do.v, which is the other walk's x . y.
+//   rho_t = q_t . (dq_t without s = t),  sigma_s = k_s . (dk_s without t = s),
+// the sum over the rest of the token's segment, S_end the state at its end.  Both
+// walks have the same A = do v^T and, but for a float's last bits, the same P,
+// so what is rounded off a pair of one chunk leaves the sum again behind both its
+// tokens (the other choice for sigma, v_s . dv_s, has a P of its own: rounded to
+// two bf16 terms, dg was then 1.6e-5 off over sequences of 4096 tokens).
+// The bf16 walks' dots have the token's own pair in them, the weight that P had
+// for it times q.k, which is x . y of dv's walk.
+// That sum is known at a segment's first token as well: <gradient of S_begin,
+// S_begin>, the product at the end of the segment before, or that with the
+// initial state, or nothing.  What it is off by there has piled up over the
+// segment, and each token takes back the share of the tokens from it on (bf16,
+// 32768 tokens in sequences of up to 4096: 8.4e-6 -> 5.2e-6 of dg's norm).
 //
 // Segments.  A sequence is cut into segments of at most `seg` tokens, which are
 // walked by CTAs of their own once the state before each is known: a first
@@ -66,16 +75,17 @@ struct LinRole {
   int64_t sdot;
   int rdot;
   float* dots;             // (lin_dot_parts, T, Hv)
-  float* pairs;            // bf16: (T, Hv, 2), the token's own x . y and its weight in P, which dots includes
+  float* pairs;            // bf16: (T, Hv), or null: the weight that P has for the token's own pair, which dots includes;
+                           // without dots, the token's x . y
   int back;                // reversed time
   int64_t srow, scol;      // a state's element (row of n1, column of n2) in memory
   const float* first;      // states that the sequences come with, (S, Hv, ., .), or null
   float* last;             // states that they leave, or null
   float* slots;            // states between segments, (inner segments, Hv, ., .)
   float* decay;            // (inner segments, Hv): exp of the segment's sum of g (the state-only walks write it)
-  const float* against;    // gradient of the state at a segment's end, as `slots` and `first` of a reversed role
-  const float* against_last;
-  float* cross;            // (segments, Hv, lin_ctas): its product with that state
+  const float* against;    // gradients of the states at the segments' ends, as `slots` of a reversed role, or null
+  const float* against_last;  // of those that a sequence leaves; of a reversed role, the states it comes with; or null
+  float* cross;            // (segments, Hv, lin_ctas): their products with the states, or null
 };
 
 struct LinArgs {

@@ -35,7 +35,7 @@ struct LinLayout {
   int seg;
   int64_t max_segs, max_inner;
   size_t table, order, inner, split, slots, decay, fwd_end;
-  size_t slots_back, decay_back, rho, sigma, pairs, cross, seg_dg, dq_part, dk_part, bwd_end;
+  size_t slots_back, decay_back, rho, sigma, pairs, cross, cross_back, seg_dg, dq_part, dk_part, bwd_end;
 };
 
 LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, bool bwd) {
@@ -57,9 +57,10 @@ LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, 
   l.slots_back = o; o += up(inner * state);
   l.decay_back = o; o += up(inner * Hv * sizeof(float));
   l.rho = o; o += up(lin_dot_parts(io, K) * tokens);
-  l.sigma = o; o += up(lin_dot_parts(io, V) * tokens);
-  l.pairs = o; o += io == IO::BF16 ? 2 * up(2 * tokens) : 0;
+  l.sigma = o; o += up(lin_dot_parts(io, K) * tokens);
+  l.pairs = o; o += io == IO::BF16 ? 3 * up(tokens) : 0;
   l.cross = o; o += up(segs * Hv * tk * sizeof(float));
+  l.cross_back = o; o += up(segs * Hv * tk * sizeof(float));
   l.seg_dg = o; o += up(segs * Hv * sizeof(double));
   l.dq_part = o; o += Hk == Hv ? 0 : up(tokens * K);
   l.dk_part = o; o += Hk == Hv ? 0 : up(tokens * K);
@@ -266,11 +267,11 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   rq.rx = rq.ry = 1; rq.rw = rep; rq.n1 = V; rq.n2 = K;
   rq.out = rep > 1 ? a.dq_part : dq; rq.part = rep > 1;
   rq.srow = 1; rq.scol = V; rq.first = initial_states; rq.slots = slots;
-  LinRole& rv = a.role[1];
+  LinRole& rv = a.role[2];
   rv.x = k; rv.y = q; rv.w = dout; rv.sx = k_stride; rv.sy = q_stride; rv.sw = so;
   rv.rx = rv.ry = rep; rv.rw = 1; rv.n1 = K; rv.n2 = V; rv.out = dv; rv.back = 1;
   rv.srow = V; rv.scol = 1; rv.first = d_final_states; rv.last = d_initial_states; rv.slots = slots_back;
-  LinRole& rk = a.role[2];
+  LinRole& rk = a.role[1];
   rk.x = v; rk.y = dout; rk.w = q; rk.sx = v_stride; rk.sy = so; rk.sw = q_stride;
   rk.rx = rk.ry = 1; rk.rw = rep; rk.n1 = V; rk.n2 = K;
   rk.out = rep > 1 ? a.dk_part : dk; rk.part = rep > 1; rk.back = 1;
@@ -281,11 +282,13 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   if (dg) {
     rq.dot = q; rq.sdot = q_stride; rq.rdot = rep; rq.dots = reinterpret_cast<float*>(p + l.rho);
     rq.against = slots_back; rq.against_last = d_final_states; rq.cross = reinterpret_cast<float*>(p + l.cross);
-    if (io == IO::BF16) {
-      rq.pairs = reinterpret_cast<float*>(p + l.pairs);
-      rv.pairs = reinterpret_cast<float*>(p + l.pairs + up(2 * sizeof(float) * (size_t)T * Hv));
+    if (io == IO::BF16)
+      for (int i = 0; i < 3; ++i) a.role[i].pairs = reinterpret_cast<float*>(p + l.pairs + i * up(sizeof(float) * (size_t)T * Hv));
+    if (initial_states) {
+      rk.against_last = initial_states;
+      rk.cross = reinterpret_cast<float*>(p + l.cross_back);
     }
-    rv.dot = v; rv.sdot = v_stride; rv.rdot = 1; rv.dots = reinterpret_cast<float*>(p + l.sigma);
+    rk.dot = k; rk.sdot = k_stride; rk.rdot = rep; rk.dots = reinterpret_cast<float*>(p + l.sigma);
   }
   TRY(check(launch_lin_walk(a, maps, 3, false, io, st), "linear attention backward launch"));
   if (dg) TRY(check(launch_lin_dg(a, io, st), "linear attention decay gradient launch"));

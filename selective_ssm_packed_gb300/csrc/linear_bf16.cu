@@ -317,7 +317,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
     }
     fence_async_smem();
     warp_arrive(bars + kStateReady, lane);
-    const bool wanted = role.cross || (role.last && (back ? seg.is_first : seg.is_last));
+    const bool wanted = (role.cross && (!back || seg.is_first)) || (role.last && (back ? seg.is_first : seg.is_last));
     for (int k = 0; k < n; ++k) {
       const uint32_t p = k & 1;
       const bool more = k + 1 < n;
@@ -370,7 +370,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       float* to = role.last && (back ? seg.is_first : seg.is_last) ? role.last + ((int64_t)seg.seq * a.Hv + h) * state_size : nullptr;
       const float* e = nullptr;
       if (role.cross) {
-        if (!seg.is_last) e = role.against + (seg.inner_before * a.Hv + h) * state_size;
+        if (!back && !seg.is_last) e = role.against + (seg.inner_before * a.Hv + h) * state_size;
         else if (role.against_last) e = role.against_last + ((int64_t)seg.seq * a.Hv + h) * state_size;
       }
       float2 sum = splat2(0.0f);
@@ -442,7 +442,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           tmem_sum<1>(tm + tA + lane_at + j0, 0, d);
           const bool all = back ? j0 > quad * 32 + 31 && j0 + 15 < rows : j0 + 15 < quad * 32;
           const int at = row - j0;  // the diagonal's column
-          if (has_dot && !all) {
+          if (back && !has_dot && !all) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) self = at == 2 * i ? d[i].x : at == 2 * i + 1 ? d[i].y : self;
           }
@@ -491,10 +491,11 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
               }
             }
             if (!all && (unsigned)at < 16u && row < rows) {
-              float* pairs = role.pairs + ((seg.start + (int64_t)c * kC + row) * a.Hv + h) * 2;
-              *reinterpret_cast<float2*>(pairs) = make_float2(self, weight);
+              role.pairs[(seg.start + (int64_t)c * kC + row) * a.Hv + h] = weight;
             }
           } else {
+            if (back && !all && role.pairs && (unsigned)at < 16u && row < rows)
+              role.pairs[(seg.start + (int64_t)c * kC + row) * a.Hv + h] = self;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint32_t term[1];
@@ -529,17 +530,19 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       named_barrier(2, 32 * kOutWarps);
       tmem_fence_after_sync();
       const bool spoilt = *odd;
-      float2 dot = splat2(0.0f);
+      Pair dot{0.0f, 0.0f};  // short sums, put together without a rounding: over a segment dg adds thousands of them
 #pragma unroll
       for (int s = 0; s < kRuns; ++s) {
         const int c0 = first + 16 * s;
         float2 e[2][8];
         load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
+        float2 sum = splat2(0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           e[0][i] = fma2(splat2(in), e[1][i], e[0][i]);
-          if (has_dot) dot = fma2(r[s].get(i), e[0][i], dot);
+          if (has_dot) sum = fma2(r[s].get(i), e[0][i], sum);
         }
+        if (has_dot) dot = add(dot, Pair{sum.x + sum.y, 0.0f});
         if (role.part) {
           float* to = static_cast<float*>(role.out) + out_row + c0;
 #pragma unroll
@@ -565,7 +568,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         }
       }
       if (spoilt && mine) spoil_row(role, static_cast<const T*>(role.w) + (token - row) * role.sw + w_at + first, out_row + first, row, rows, cols);
-      if (has_dot && mine) role.dots[((int64_t)part * a.T + token) * a.Hv + h] = dot.x + dot.y;
+      if (has_dot && mine) role.dots[((int64_t)part * a.T + token) * a.Hv + h] = dot.hi + dot.lo;
     }
   } else {
     if (warp == kProducts) {  // all lanes go through it together, so that addresses are uniform; one issues

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs a, int blocks) {
 // which most cancels.
 constexpr int kDgHeads = 2, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads, kDgPer = kLinMaxSegment / kDgParts;
 
-__global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts_q, int parts_v, int tiles) {
+__global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts, int tiles) {
   __shared__ Pair sums[2][kDgThreads];
   const int seg = blockIdx.x;
   if (seg >= a.info[0]) return;
@@ -155,12 +155,11 @@ __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts
   auto diff = [&](int i) {
     const int64_t at = ((int64_t)entry.y + i) * a.Hv + h;
     Pair v{0.0f, 0.0f};
-    for (int p = 0; p < parts_q; ++p) v = add(v, Pair{rho[p * plane + at], 0.0f});
-    for (int p = 0; p < parts_v; ++p) v = add(v, Pair{-sigma[p * plane + at], 0.0f});
+    for (int p = 0; p < parts; ++p) v = add(v, Pair{rho[p * plane + at], 0.0f});
+    for (int p = 0; p < parts; ++p) v = add(v, Pair{-sigma[p * plane + at], 0.0f});
     if (a.role[0].pairs) {
-      const float2 q = reinterpret_cast<const float2*>(a.role[0].pairs)[at], k = reinterpret_cast<const float2*>(a.role[1].pairs)[at];
-      v = add(v, Pair{-q.y * k.x, -fmaf(q.y, k.x, -(q.y * k.x))});
-      v = add(v, Pair{k.y * q.x, fmaf(k.y, q.x, -(k.y * q.x))});
+      const float w = a.role[1].pairs[at] - a.role[0].pairs[at], qk = a.role[2].pairs[at];
+      v = add(v, Pair{w * qk, fmaf(w, qk, -(w * qk))});
     }
     return v;
   };
@@ -177,14 +176,28 @@ __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts
     __syncthreads();
   }
   Pair run = part + 1 < kDgParts ? sums[from][t + kDgHeads] : Pair{0.0f, 0.0f}, total{0.0f, 0.0f};
-  if (in)
-    for (int i = 0; i < tiles; ++i) run = add(run, Pair{a.role[0].cross[((int64_t)seg * a.Hv + h) * tiles + i], 0.0f});
+  Pair gap = sums[from][t % kDgHeads];  // what the sum over all tokens is off by
+  float share = 0.0f;
+  if (in) {
+    const bool first = entry.w & kLinFirst;
+    const float *at_end = a.role[0].cross + ((int64_t)seg * a.Hv + h) * tiles;
+    const float *at_begin = first ? a.role[1].cross ? a.role[1].cross + ((int64_t)seg * a.Hv + h) * tiles : nullptr
+                                  : at_end - (int64_t)a.Hv * tiles;
+    for (int i = 0; i < tiles; ++i) {
+      run = add(run, Pair{at_end[i], 0.0f});
+      gap = add(gap, Pair{at_end[i], 0.0f});
+      if (at_begin) gap = add(gap, Pair{-at_begin[i], 0.0f});
+    }
+    share = (gap.hi + gap.lo) / (float)max(entry.z, 1);
+    if (!isfinite(share)) share = 0.0f;  // tokens behind what is not finite keep their sums
+  }
 #pragma unroll
   for (int i = kDgPer - 1; i >= 0; --i) {
     if (lo + i >= hi) continue;
     run = add(run, d[i]);
-    if (a.g_token) a.dg[((int64_t)entry.y + lo + i) * a.Hv + h] = run.hi + run.lo;
-    else total = add(total, run);
+    const float off = share * (float)(entry.z - (lo + i));
+    if (a.g_token) a.dg[((int64_t)entry.y + lo + i) * a.Hv + h] = run.hi + (run.lo - off);
+    else total = add(total, Pair{run.hi, run.lo - off});
   }
   if (a.g_token) return;
   __syncthreads();
@@ -251,7 +264,7 @@ cudaError_t launch_lin_scan(const LinArgs& a, int roles, cudaStream_t st) {
 cudaError_t launch_lin_dg(const LinArgs& a, IO io, cudaStream_t st) {
   if (a.max_segs > 0)
     lin_dg_kernel<<<dim3((unsigned)a.max_segs, (unsigned)((a.Hv + kDgHeads - 1) / kDgHeads)), kDgThreads, 0, st>>>(
-        a, lin_dot_parts(io, a.K), lin_dot_parts(io, a.V), lin_ctas(io, a.K));
+        a, lin_dot_parts(io, a.K), lin_ctas(io, a.K));
   if (!a.g_token) lin_dg_head_kernel<<<(unsigned)((a.Hv + 31) / 32), 256, 0, st>>>(a);
   return cudaGetLastError();
 }

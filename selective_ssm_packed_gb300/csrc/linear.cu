@@ -1,13 +1,14 @@
-// linear.cu -- linear attention's walk over the chunks of a segment: the
-// forward, each of its three gradients, and the states between segments.
+// linear.cu -- linear attention's walk over the chunks of a segment in f32: the
+// forward, each of its three gradients, and the states between segments.  The
+// bf16 walks are linear_bf16.cu's.
 #include "linear.cuh"
 
 namespace vssm {
 namespace {
 
 // One CTA per (segment, value head, role, 64 columns of the state; the columns
-// never mix).  A chunk (128 tokens in bf16, 64 in f32) is four products on the
-// matrix unit:
+// never mix).  A chunk of 64 tokens is four products on the matrix unit, every
+// operand in three bf16 terms (24 bits):
 //   A  = X Y^T             read back, weighted and masked: P, bf16 terms in tensor memory
 //   D1 = X S
 //   U  = Y^T (up * W)      S = exp(G_end) S + U, in registers and as bf16 terms in shared memory
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   if (warp == kLinCtrl) tmem_alloc<512>(tmem_at);
 
   const float* g_base = a.g + start * a.g_token + h;
-  // warp 8: the gates of chunk c; returns the chunk's sum of g over ln 2
+  // the gates of chunk c; returns the chunk's sum of g over ln 2
   auto make_gates = [&](int c, int buf) -> Pair {
     constexpr int kPer = kC / 32;
     const int rows = min(kC, len - c * kC);

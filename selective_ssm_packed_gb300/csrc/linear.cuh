@@ -51,19 +51,9 @@ struct LinWaiter {
   }
 };
 
-// Like umma, A in tensor memory: its rows in the lanes, two bf16 to a column.
-__device__ __forceinline__ void umma_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t desc_b, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(desc_b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The same instructions, issued by the lane for which `lead` holds of a warp
-// that goes through them together: the operands then come from the uniform
+// As umma (and with A in tensor memory, its rows in the lanes, two bf16 to a
+// column), issued by the lane for which `lead` holds of a warp that goes through
+// it together: the operands then come from the uniform
 // registers that the instruction takes them from, where a lane by itself would
 // move each of them there (a step took 110 cycles to issue, of 64 that it runs).
 __device__ __forceinline__ void umma_if(bool lead, uint32_t tmem_d, uint64_t desc_a, uint64_t desc_b, uint32_t idesc,

@@ -49,11 +49,11 @@
 
 namespace vssm {
 
-constexpr int kLinTile = 64;   // columns of the state that a CTA walks
+constexpr int kLinTile = 64;   // columns of the state that an f32 walk's CTA has
 constexpr int kLinMaxK = 128, kLinMaxV = 128;
 constexpr int kLinRoles = 3;
 constexpr int kLinMaxSegment = 4096;  // tokens
-constexpr int kLinParts = 4;   // threads to a row, 16 columns of the tile each
+constexpr int kLinParts = 4;   // f32: threads to a row, 16 columns of the tile each
 
 // CTAs that share the columns of a state: in bf16 one walks them all.
 inline int lin_ctas(IO io, int n2) { return io == IO::BF16 ? 1 : (n2 + kLinTile - 1) / kLinTile; }

@@ -158,13 +158,13 @@ __device__ __noinline__ void clear_odd(uint8_t* at, int step, int count) {
     }
 }
 
-// Up * W as images of two terms from W's image, by kThreads threads, each along
+// Up * W as images of kTerms terms from W's image, by kThreads threads, each along
 // a column of 16-byte chunks whose place in the swizzle is the same in all its
 // rows.  A value of W that is not finite reaches the state, and so every later
 // row, through up * W; in D2, where 0 times it would reach earlier rows, 0 takes
 // its place in W, and *odd has the rows it should reach made NaN when they are
 // written.
-template <int NP, int kThreads>
+template <int NP, int kTerms, int kThreads>
 __device__ __forceinline__ void weigh(uint8_t* w_image, uint8_t* up_image, const float* up, int t, volatile int* odd) {
   constexpr int kRowChunks = NP * 8, kRows = kThreads / kRowChunks;
   static_assert(kRows % 8 == 0, "the swizzle repeats every 8 rows");
@@ -177,18 +177,19 @@ __device__ __forceinline__ void weigh(uint8_t* w_image, uint8_t* up_image, const
     const uint4 q = *reinterpret_cast<const uint4*>(w_image + at + u * kRows * 128);
     const float2 f = splat2(up[r0 + u * kRows]);
     const uint32_t p[4] = {q.x, q.y, q.z, q.w};
-    uint32_t hi[4], lo[4];
+    uint32_t terms[kTerms][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (odd) trace = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&p[k]), zero, trace);
-      uint32_t term[2];
-      split_pair<2>(mul2(make_float2(bf16_lo(p[k]), bf16_hi(p[k])), f), term);
-      hi[k] = term[0];
-      lo[k] = term[1];
+      uint32_t term[kTerms];
+      split_pair<kTerms>(mul2(make_float2(bf16_lo(p[k]), bf16_hi(p[k])), f), term);
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) terms[i][k] = term[i];
     }
     uint8_t* to = up_image + at + u * kRows * 128;
-    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(to + NP * kPanel) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i)
+      *reinterpret_cast<uint4*>(to + i * NP * kPanel) = make_uint4(terms[i][0], terms[i][1], terms[i][2], terms[i][3]);
   }
   if (odd && (*reinterpret_cast<const uint32_t*>(&trace) & 0x7fff7fffu)) {
     clear_odd(w_image + at, kRows * 128, kC / kRows);
@@ -336,7 +337,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         clear_rows<NP>(w_image(k), rows, t, 32 * kStateWarps);
         named_barrier(1, 32 * kStateWarps);
       }
-      weigh<NP, 32 * kStateWarps>(w_image(k), sm + L::oUp, s_up, t, odd);
+      weigh<NP, 2, 32 * kStateWarps>(w_image(k), sm + L::oUp, s_up, t, odd);
       warp_arrive(bars + kGatesFree, lane);
       if (decay != 1.0f && has_row) decay_state<kCols>(tm + tU + lane_at + c0, decay);
       tmem_fence_before_sync();
@@ -368,7 +369,8 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
     if (wanted) {
       tmem_fence_after_sync();
       float* to = role.last && (back ? seg.is_first : seg.is_last) ? role.last + ((int64_t)seg.seq * a.Hv + h) * state_size : nullptr;
-      const float* e = nullptr;
+      const float *e = nullptr, *at_end = nullptr;  // between segments: the state as it was made for the next one
+      if (role.cross && !back && !seg.is_last) at_end = role.slots + (seg.inner_before * a.Hv + h) * state_size;
       if (role.cross) {
         if (!back && !seg.is_last) e = role.against + (seg.inner_before * a.Hv + h) * state_size;
         else if (role.against_last) e = role.against_last + ((int64_t)seg.seq * a.Hv + h) * state_size;
@@ -382,6 +384,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           for (int i = 0; i < 8; ++i) d[i] = splat2(0.0f);
           if (n > 0 || has_carry) tmem_sum<1>(tm + tU + lane_at + c0 + 16 * u, 0, d);
           scale_row(d, unit);
+          if (at_end) load_state(at_end, c0 + 16 * u, d);
           if (e) {
             float2 x[8];
             load_state(e, c0 + 16 * u, x);
@@ -761,9 +764,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // the weights up to the segment's end, so that the chunks add up in tensor
 // memory with nothing read back in between: the chunk next to that end comes
 // first, and each earlier one's weights carry the decay over the ones behind it.
+// Three terms, all 24 bits: these states are what dg is held to at the ends of
+// the segments.
+constexpr int kStateTerms = 3;
 template <int KP, int NP>
 struct StateSmem {
-  static constexpr int kY = KP * kPanel, kW = NP * kPanel, kUp = 2 * kW;
+  static constexpr int kY = KP * kPanel, kW = NP * kPanel, kUp = kStateTerms * kW;
   static constexpr int oY = 0, oW = 2 * kY, oUp = oW + 2 * kW, oGates = oUp + kUp, oMisc = oGates + 2 * 4 * kC;
   static constexpr int oBar = oMisc + 64, kBytes = oBar + 16 * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -812,8 +818,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         tmem_fence_after_sync();
         const uint64_t yt = smem_desc<128>(smem_u32(sm + L::oY + (k & 1) * L::kY), kPanel);
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {  // the smaller term first
-          const int term = 1 - i / 2;
+        for (int i = 0; i < 2 * kStateTerms; ++i) {  // the smallest term first
+          const int term = kStateTerms - 1 - i / 2;
 #pragma unroll
           for (int s = 0; s < 4; ++s)
             umma_if(lead, tm, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc,
@@ -893,7 +899,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         clear_rows<NP>(sm + L::oW + b * L::kW, rows, t, 32 * kWeighWarps);
         named_barrier(1, 32 * kWeighWarps);
       }
-      weigh<NP, 32 * kWeighWarps>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), t,
+      weigh<NP, kStateTerms, 32 * kWeighWarps>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), t,
                                   nullptr);
       fence_async_smem();
       warp_arrive(used + b, lane);

@@ -18,7 +18,7 @@ the sum is off by sqrt(2 sum of i^2 over i < n) = 0.82 n^1.5 of them a segment, 
 sqrt(T) in all, that is 0.82 * 385 * 2^-16 = 4.8e-3 (bf16) or 0.82 * 385 * 8e-6 =
 2.5e-3 (f32) of the 2-norm of the tokens' dg, against which it is held.
 In bf16 the weights of pairs and the state that a row meets are rounded to bf16
-once on the way to out and dk, 2^-9 of each value on the average of its binade and
+once on the way to out and dv, 2^-9 of each value on the average of its binade and
 2^-8 at most, besides the result's own rounding: 2 * 2^-8.
 """
 import numpy as np
@@ -48,7 +48,7 @@ def _built():
 def close(name, got, ref, dtype, size=None):
     tol = {"dg": DG, "dg_head": DG_HEAD}.get(name, NET)[dtype]
     if got.dtype == torch.bfloat16:
-        tol += (2 if name in ("out", "dk") else 1) * 2.0 ** -8
+        tol += (2 if name in ("out", "dv") else 1) * 2.0 ** -8
     g = got.double().cpu().numpy()
     assert g.shape == ref.shape, (name, g.shape, ref.shape)
     if not ref.size:
@@ -154,6 +154,22 @@ def test_a_sequence_across_segments():
             seg = binding.linear_attn_segment(T, 2, 1, 2, 64, 64, CODE[dtype], back)
             assert seg == 256  # the first sequence has four of them
         check(inputs([784, 5], 1, 2, 64, 64, dtype, 31, True), dtype, True)
+
+
+@pytest.mark.parametrize("decay", ["token", "head"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decays_gradient_between_segments(dtype, decay):
+    """The bf16 walks' operands have two terms, rounded by 2^-18 of a value at most and half of that on the average; dg
+    sums the two walks' difference of that over a segment, from a known value at either end: with the 2^-17 of a
+    pair's weight, 2^-16 = 1.5e-5 of the tokens' dg (in f32 2^-20, by three terms and FP32 sums).  A sum over T tokens is
+    off by sqrt(T) times that at most."""
+    x = inputs([2100, 300], 2, 4, 128, 64, dtype, 21, True, decay)
+    seg = binding.linear_attn_segment(2400, 2, 2, 4, 128, 64, CODE[dtype], True)
+    assert seg < 2100
+    got, ref = run(x, states=True)["dg"], reference(x)["dg"]
+    tokens = reference(dict(x, g=x["g"].expand(2400, -1)))["dg"] if decay == "head" else ref
+    size = np.linalg.norm(tokens) * (2400 ** 0.5 if decay == "head" else 1.0)
+    assert np.linalg.norm(host(got) - ref) <= {"f32": 2.0 ** -20, "bf16": 2.0 ** -16}[dtype] * size
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

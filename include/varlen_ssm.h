@@ -486,10 +486,14 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
  * states are made again; nothing of the forward call has to be kept.
  * d_final_states: nullable, the gradient reaching the final states.  dq and dk
  * add the value heads that share a head, in order; no atomics, bitwise
- * repeatable.  A value that is not finite in q, k, v, dout or the states
- * reaches the gradients that the formula carries it to; dg, a sum over a
- * segment, is not finite before it in the sequence's segments, and a g that is
- * not finite leaves NaN in its whole chunk.  Other sequences keep their bits. */
+ * repeatable.  With bf16 I/O dv (without dg, dq and dk too) has the one rounding
+ * more that out has, and dg is about 5e-6 of its norm off; data in bf16 whose
+ * dg and states are wanted with all bits are passed as f32.
+ * A value that is not finite in q, k, v, dout or the states reaches the
+ * gradients that the formula carries it to; dg, a sum over a segment, is not
+ * finite before it in the sequence's segments and keeps its value, but not its
+ * last bits, behind it in its own, and a g that is not finite leaves NaN in its
+ * whole chunk.  Other sequences keep their bits. */
 size_t varlen_linear_attn_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
                                              int32_t K, int32_t V, vssm_dtype dtype);
 int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,

@@ -9,7 +9,7 @@ namespace {
 // One CTA: a pack has a few thousand sequences.  Running sums of the segments
 // and inner segments give each sequence its places; the order is by length
 // class (of 64, longest first) and within a class left to chance: it decides
-// when a segment is walked, not how.
+// when a segment is walked, not how.  5 us, of which 2 to 3 are a launch's.
 constexpr int kPlanThreads = 1024;
 
 __device__ __forceinline__ int length_class(int len, int seg) {
@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs a, int blocks) {
 // One CTA per (segment, kDgHeads heads): a thread has one head and a stretch of
 // the segment's tokens, which it sums up first and then walks from its end.
 // Sums are of two floats: a token's dg is the sum of all later differences, in
-// which most cancels.
+// which most cancels.  32768 tokens, 32 heads: 44 us for 34 MB, whose loads
+// are of two heads next to each other: more of them to a CTA leave each a longer stretch.
 constexpr int kDgHeads = 2, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads, kDgPer = kLinMaxSegment / kDgParts;
 
 __global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts, int tiles) {
@@ -227,7 +228,8 @@ __global__ void __launch_bounds__(256) lin_dg_head_kernel(LinArgs a) {
 
 // ------------------------------------------------------------------ shared heads
 // dq and dk: the value heads' parts that share a head, added in order.
-// blockIdx.y: dq or dk.  A thread has four values.
+// blockIdx.y: dq or dk.  A thread has four values.  16384 tokens, 64 value heads on 8
+// of 128: 163 us for 1.1 GB, 6.9 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(256) lin_head_sum_kernel(LinArgs a, int64_t count) {
   if (a.info[0] < 0) return;

@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
             for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
             float2 sum = splat2(0.0f);
             R::each(raw, 0, [&](int i, float2 y) { sum = fma2(y, o[i], sum); });
-            if (row < rows) role.dots[((int64_t)(tile * kLinParts + part) * a.T + start + at + lane) * a.Hv + h] = sum.x + sum.y;
+            if (row < rows) role.dots[((int64_t)(tile * kLinParts + part) * a.Hv + h) * a.T + start + at + lane] = sum.x + sum.y;
             const float self = s_diag[row];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {

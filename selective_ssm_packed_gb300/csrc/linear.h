@@ -74,8 +74,8 @@ struct LinRole {
   const void* dot;         // rho's or sigma's partner rows, or null
   int64_t sdot;
   int rdot;
-  float* dots;             // (lin_dot_parts, T, Hv)
-  float* pairs;            // bf16: (T, Hv), or null: the weight that P has for the token's own pair, which dots includes;
+  float* dots;             // (lin_dot_parts, Hv, T)
+  float* pairs;            // bf16: (Hv, T), or null: the weight that P has for the token's own pair, which dots includes;
                            // without dots, the token's x . y
   int back;                // reversed time
   int64_t srow, scol;      // a state's element (row of n1, column of n2) in memory

@@ -23,7 +23,7 @@ namespace {
 // than a chunk's 5 us by itself: tensor memory, shared memory and the products'
 // operands take one data path of the SM, 8000 cycles of it a chunk.
 // 32768 tokens, 32 heads of 128: 250 us forward (807 MB, 3.2 TB/s), the gradients
-// 312 (dq), 334 (dk) and 284 us (dv); a key head shared by 8 value heads writes its
+// 305 (dq), 345 (dk) and 286 us (dv); a key head shared by 8 value heads writes its
 // dq and dk as f32 parts of each, 512 MB more (16384 tokens, 64 heads of 64: 390
 // and 416 us).
 //
@@ -509,11 +509,11 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
               }
             }
             if (!all && (unsigned)at < 16u && row < rows) {
-              role.pairs[(seg.start + (int64_t)c * kC + row) * a.Hv + h] = weight;
+              role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = weight;
             }
           } else {
             if (back && !all && role.pairs && (unsigned)at < 16u && row < rows)
-              role.pairs[(seg.start + (int64_t)c * kC + row) * a.Hv + h] = self;
+              role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = self;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint32_t term[1];
@@ -586,7 +586,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         }
       }
       if (spoilt && mine) spoil_row(role, static_cast<const T*>(role.w) + (token - row) * role.sw + w_at + first, out_row + first, row, rows, cols);
-      if (has_dot && mine) role.dots[((int64_t)part * a.T + token) * a.Hv + h] = dot.hi + dot.lo;
+      if (has_dot && mine) role.dots[((int64_t)part * a.Hv + h) * a.T + token] = dot.hi + dot.lo;
     }
   } else {
     if (warp == kProducts) {  // all lanes go through it together, so that addresses are uniform; one issues

@@ -136,79 +136,91 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinArgs a, int blocks) {
 }
 
 // ------------------------------------------------------------------ gradient of the decays
-// One CTA per (segment, kDgHeads heads): a thread has one head and a stretch of
-// the segment's tokens, which it sums up first and then walks from its end.
-// Sums are of two floats: a token's dg is the sum of all later differences, in
-// which most cancels.  32768 tokens, 32 heads: 44 us for 34 MB, whose loads
-// are of two heads next to each other: more of them to a CTA leave each a longer stretch.
-constexpr int kDgHeads = 2, kDgThreads = 1024, kDgParts = kDgThreads / kDgHeads, kDgPer = kLinMaxSegment / kDgParts;
+// One CTA per (segment, head): a thread has a stretch of the segment's tokens,
+// which it sums up first and then walks from its end.  Sums are of two floats: a
+// token's dg is the sum of all later differences, in which most cancels.
+// 32768 tokens, 32 heads: 27 us for 34 MB, two CTAs an SM (44 with rows of all heads and two heads to a
+// CTA of 1024, 37 with a CTA alone on its SM).
+constexpr int kDgThreads = 512, kDgWarps = kDgThreads / 32, kDgPer = kLinMaxSegment / kDgThreads;
 
-__global__ void __launch_bounds__(kDgThreads) lin_dg_kernel(LinArgs a, int parts, int tiles) {
-  __shared__ Pair sums[2][kDgThreads];
-  const int seg = blockIdx.x;
+__device__ __forceinline__ Pair shfl_down(Pair v, int o) {
+  return Pair{__shfl_down_sync(0xffffffffu, v.hi, o), __shfl_down_sync(0xffffffffu, v.lo, o)};
+}
+// The sum over this lane and those behind it.
+__device__ __forceinline__ Pair sum_behind(Pair v, int lane) {
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair w = shfl_down(v, o);
+    if (lane + o < 32) v = add(v, w);
+  }
+  return v;
+}
+
+template <IO kIO, int kParts>
+__global__ void __launch_bounds__(kDgThreads, 2) lin_dg_kernel(LinArgs a, int tiles) {
+  __shared__ Pair sums[kDgWarps];
+  const int seg = blockIdx.x, h = blockIdx.y;
   if (seg >= a.info[0]) return;
   const int4 entry = a.table[seg];
-  const int t = threadIdx.x, part = t / kDgHeads, h = blockIdx.y * kDgHeads + t % kDgHeads;
-  const bool in = h < a.Hv;
-  const int per = (entry.z + kDgParts - 1) / kDgParts, lo = min(entry.z, part * per), hi = in ? min(entry.z, lo + per) : lo;
-  const float *rho = a.role[0].dots, *sigma = a.role[1].dots;
-  const int64_t plane = a.T * a.Hv;
-  auto diff = [&](int i) {
-    const int64_t at = ((int64_t)entry.y + i) * a.Hv + h;
-    Pair v{0.0f, 0.0f};
-    for (int p = 0; p < parts; ++p) v = add(v, Pair{rho[p * plane + at], 0.0f});
-    for (int p = 0; p < parts; ++p) v = add(v, Pair{-sigma[p * plane + at], 0.0f});
-    if (a.role[0].pairs) {
-      const float w = a.role[1].pairs[at] - a.role[0].pairs[at], qk = a.role[2].pairs[at];
-      v = add(v, Pair{w * qk, fmaf(w, qk, -(w * qk))});
-    }
-    return v;
-  };
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int per = (entry.z + kDgThreads - 1) / kDgThreads, lo = min(entry.z, t * per), n = min(entry.z - lo, per);
+  const int64_t plane = a.T * a.Hv, first = h * a.T + entry.y + lo;
   Pair d[kDgPer], own{0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < kDgPer; ++i) d[i] = lo + i < hi ? diff(lo + i) : Pair{0.0f, 0.0f};
+  for (int i = 0; i < kDgPer; ++i) {
+    d[i] = Pair{0.0f, 0.0f};
+    if (i >= n) continue;
+    const int64_t at = first + i;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) d[i] = add(d[i], Pair{a.role[0].dots[p * plane + at], 0.0f});
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) d[i] = add(d[i], Pair{-a.role[1].dots[p * plane + at], 0.0f});
+    if (kIO == IO::BF16) {  // without the token's own pair
+      const float w = a.role[1].pairs[at] - a.role[0].pairs[at], qk = a.role[2].pairs[at];
+      d[i] = add(d[i], Pair{w * qk, fmaf(w, qk, -(w * qk))});
+    }
+  }
 #pragma unroll
   for (int i = kDgPer - 1; i >= 0; --i) own = add(own, d[i]);
-  sums[0][t] = own;
+  const Pair incl = sum_behind(own, lane);
+  if (lane == 0) sums[warp] = incl;
   __syncthreads();
-  int from = 0;  // the sums over this part and the next 1, 3, 7, ..
-  for (int o = 1; o < kDgParts; o *= 2, from ^= 1) {
-    sums[from ^ 1][t] = part + o < kDgParts ? add(sums[from][t], sums[from][t + o * kDgHeads]) : sums[from][t];
-    __syncthreads();
+  if (warp == 0) {
+    const Pair v = sum_behind(lane < kDgWarps ? sums[lane] : Pair{0.0f, 0.0f}, lane);
+    if (lane < kDgWarps) sums[lane] = v;
   }
-  Pair run = part + 1 < kDgParts ? sums[from][t + kDgHeads] : Pair{0.0f, 0.0f}, total{0.0f, 0.0f};
-  Pair gap = sums[from][t % kDgHeads];  // what the sum over all tokens is off by
-  float share = 0.0f;
-  if (in) {
-    const bool first = entry.w & kLinFirst;
-    const float *at_end = a.role[0].cross + ((int64_t)seg * a.Hv + h) * tiles;
-    const float *at_begin = first ? a.role[1].cross ? a.role[1].cross + ((int64_t)seg * a.Hv + h) * tiles : nullptr
-                                  : at_end - (int64_t)a.Hv * tiles;
-    for (int i = 0; i < tiles; ++i) {
-      run = add(run, Pair{at_end[i], 0.0f});
-      gap = add(gap, Pair{at_end[i], 0.0f});
-      if (at_begin) gap = add(gap, Pair{-at_begin[i], 0.0f});
-    }
-    share = (gap.hi + gap.lo) / (float)max(entry.z, 1);
-    if (!isfinite(share)) share = 0.0f;  // tokens behind what is not finite keep their sums
+  __syncthreads();
+  Pair run = shfl_down(incl, 1), total{0.0f, 0.0f}, gap = sums[0];  // gap: what the sum over all tokens is off by
+  if (lane == 31) run = Pair{0.0f, 0.0f};
+  if (warp + 1 < kDgWarps) run = add(run, sums[warp + 1]);
+  const float *at_end = a.role[0].cross + ((int64_t)seg * a.Hv + h) * tiles;
+  const float *at_begin = !(entry.w & kLinFirst) ? at_end - (int64_t)a.Hv * tiles
+                          : a.role[1].cross      ? a.role[1].cross + ((int64_t)seg * a.Hv + h) * tiles
+                                                 : nullptr;
+  for (int i = 0; i < tiles; ++i) {
+    run = add(run, Pair{at_end[i], 0.0f});
+    gap = add(gap, Pair{at_end[i], 0.0f});
+    if (at_begin) gap = add(gap, Pair{-at_begin[i], 0.0f});
   }
+  float share = (gap.hi + gap.lo) / (float)max(entry.z, 1);
+  if (!isfinite(share)) share = 0.0f;  // tokens behind what is not finite keep their sums
 #pragma unroll
   for (int i = kDgPer - 1; i >= 0; --i) {
-    if (lo + i >= hi) continue;
+    if (i >= n) continue;
     run = add(run, d[i]);
     const float off = share * (float)(entry.z - (lo + i));
     if (a.g_token) a.dg[((int64_t)entry.y + lo + i) * a.Hv + h] = run.hi + (run.lo - off);
     else total = add(total, Pair{run.hi, run.lo - off});
   }
   if (a.g_token) return;
+  total = sum_behind(total, lane);
   __syncthreads();
-  sums[0][t] = total;
+  if (lane == 0) sums[warp] = total;
   __syncthreads();
-  for (int o = kDgParts / 2; o >= 1; o /= 2) {
-    if (part < o) sums[0][t] = add(sums[0][t], sums[0][t + o * kDgHeads]);
-    __syncthreads();
+  if (warp == 0) {
+    total = sum_behind(lane < kDgWarps ? sums[lane] : Pair{0.0f, 0.0f}, lane);
+    if (lane == 0) a.seg_dg[(int64_t)seg * a.Hv + h] = (double)total.hi + (double)total.lo;
   }
-  if (in && part == 0) a.seg_dg[(int64_t)seg * a.Hv + h] = (double)sums[0][t].hi + (double)sums[0][t].lo;
 }
 
 // One decay a head: the segments' sums, in order.
@@ -264,9 +276,13 @@ cudaError_t launch_lin_scan(const LinArgs& a, int roles, cudaStream_t st) {
 }
 
 cudaError_t launch_lin_dg(const LinArgs& a, IO io, cudaStream_t st) {
-  if (a.max_segs > 0)
-    lin_dg_kernel<<<dim3((unsigned)a.max_segs, (unsigned)((a.Hv + kDgHeads - 1) / kDgHeads)), kDgThreads, 0, st>>>(
-        a, lin_dot_parts(io, a.K), lin_ctas(io, a.K));
+  const dim3 grid((unsigned)a.max_segs, (unsigned)a.Hv);
+  const int tiles = lin_ctas(io, a.K);
+  if (a.max_segs > 0) {
+    if (io == IO::BF16) lin_dg_kernel<IO::BF16, 2><<<grid, kDgThreads, 0, st>>>(a, tiles);
+    else if (tiles == 1) lin_dg_kernel<IO::F32, kLinParts><<<grid, kDgThreads, 0, st>>>(a, tiles);
+    else lin_dg_kernel<IO::F32, 2 * kLinParts><<<grid, kDgThreads, 0, st>>>(a, tiles);
+  }
   if (!a.g_token) lin_dg_head_kernel<<<(unsigned)((a.Hv + 31) / 32), 256, 0, st>>>(a);
   return cudaGetLastError();
 }

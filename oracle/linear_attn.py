@@ -64,7 +64,7 @@ def linear_bwd(q, k, v, g, dout, cu, scale, init=None, dfinal=None):
             d["dg"][t] = (D * before).sum((-2, -1))
         d["dinit"][s] = D
     for n in ("dq", "dk"):
-        d[n] = d[n].reshape(T, Hk, rep, -1).sum(2)
+        d[n] = d[n].reshape(T, Hk, rep, q.shape[2]).sum(2)
     if np.ndim(g) == 1:
         d["dg"] = d["dg"].sum(0)
     return d

@@ -711,7 +711,16 @@ _HERE = _Here()
 def _device_of(t):
     """A context in which t's device is the current one, which the library
     launches on."""
-    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
+
+
+def _together(first, *others):
+    """Refuses tensors on several devices: a kernel would read memory that is
+    not its device's."""
+    device = first.get_device()
+    for t in others:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != device:
+            raise ValueError(f"the tensors of a call must be on one device, got {first.device} and {t.device}")
 
 
 def linear_attn_fwd_workspace_size(T, S, Hk, Hv, K, V, dtype):
@@ -747,6 +756,7 @@ def varlen_linear_attn_fwd(q, k, v, g, cu_seqlens, scale=None, out=None, workspa
     True or a tensor to fill."""
     args, (T, Hk, Hv, K, V) = _linear_args(q, k, v, g)
     S, dt = _num_seqs(cu_seqlens), _dt(q)
+    _together(q, k, v, g, cu_seqlens, out, workspace, initial_states, final_states)
     with _device_of(q):
         out, op = _result(out, "out", v, stream)
         want_final = final_states is not None and final_states is not False
@@ -773,6 +783,7 @@ def varlen_linear_attn_bwd(q, k, v, g, dout, cu_seqlens, scale=None, grads=None,
     r = dict(grads or {})
     shapes = {"dq": ((T, Hk, K), q.dtype), "dk": ((T, Hk, K), q.dtype), "dv": ((T, Hv, V), q.dtype),
               "dg": (tuple(g.shape), torch.float32)}
+    _together(q, k, v, g, dout, cu_seqlens, workspace, initial_states, d_final_states, d_initial_states, *r.values())
     with _device_of(q):
         for n, (shape, d) in shapes.items():
             if n not in r:
@@ -800,6 +811,7 @@ def varlen_linear_attn_step(q, k, v, g, states, state_indices=None, scale=None, 
     if _cuda(states, "states").dim() != 4:
         raise ValueError(f"states must be (slots, {Hv}, {K}, {V}), got {tuple(states.shape)}")
     slots = states.shape[0]
+    _together(q, k, v, g, states, state_indices, out, status)
     with _device_of(q):
         out, op = _result(out, "out", v, stream)
         _check(lib().varlen_linear_attn_step(
@@ -832,6 +844,7 @@ def varlen_layer_norm_fwd(x, weight=None, bias=None, groups=1, eps=1e-5, residua
     T, D = x.shape
     if residual is None and sum_out is not None:
         raise ValueError("sum_out needs a residual")
+    _together(x, weight, bias, residual, out, sum_out)
     with _device_of(x):
         out, op = _result(out, "out", x, stream)
         rp = _shaped(residual, "residual", (T, D))
@@ -861,6 +874,7 @@ def varlen_layer_norm_bwd(x, weight, bias, dout, groups=1, eps=1e-5, residual=Fa
     g = dict(grads or {})
     make = {"dx": ((T, D), dout.dtype), "dresidual": ((T, D), torch.float32), "dweight": ((D,), torch.float32),
             "dbias": ((D,), torch.float32)}
+    _together(x, weight, dout, dsum, workspace, *g.values())
     with _device_of(x):
         for n, wanted in (("dx", True), ("dresidual", residual), ("dweight", weight is not None),
                           ("dbias", bias is not None)):

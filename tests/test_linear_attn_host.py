@@ -178,3 +178,23 @@ def test_sizes(lib):
             assert 256 <= seg <= 4096 and seg % 128 == 0
     assert lib.varlen_layer_norm_bwd_workspace_size(4, 60, 1) == 0
     assert 0 < lib.varlen_layer_norm_bwd_workspace_size(0, 64, 1) <= lib.varlen_layer_norm_bwd_workspace_size(4096, 64, 1)
+
+
+def test_tensors_of_several_devices_are_refused():
+    import torch
+
+    class On(torch.Tensor):  # a tensor that says it is on a GPU
+        @staticmethod
+        def __new__(cls, device):
+            t = torch.Tensor._make_subclass(cls, torch.zeros(1))
+            t.at = device
+            return t
+
+        is_cuda = True
+
+        def get_device(self):
+            return self.at
+
+    binding._together(On(1), None, True, On(1))
+    with pytest.raises(ValueError):
+        binding._together(On(0), None, On(1))

@@ -220,8 +220,7 @@ struct WalkRow {
 // it then says in the status word and to the CTA's other threads, who give up
 // theirs (*stop, a word in shared memory, 0 at first).  The timer is read once
 // in 64 tries.  forced: a test's wait, which counts as run out once it is over.
-template <typename Args>
-__device__ __forceinline__ bool wait_or_stop(const Args& a, volatile int* stop, uint64_t* bar, uint32_t parity,
+__device__ __forceinline__ bool wait_or_stop(const DeltaArgs& a, volatile int* stop, uint64_t* bar, uint32_t parity,
                                              bool forced = false) {
   if (!forced && mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;

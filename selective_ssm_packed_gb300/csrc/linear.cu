@@ -101,9 +101,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = lane * kPer + i;
-      float v = r < rows ? g_base[(int64_t)(c * kC + r) * a.g_token] : 0.0f;
-      v = v < -256.0f ? -256.0f : v;  // exp of either is 0; -inf would leave inf - inf
-      incl = add(incl, Pair{v, 0.0f});
+      incl = add(incl, Pair{r < rows ? clamp_g(g_base[(int64_t)(c * kC + r) * a.g_token]) : 0.0f, 0.0f});
       own[i] = incl;
     }
 #pragma unroll

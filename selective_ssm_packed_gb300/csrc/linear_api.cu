@@ -18,11 +18,11 @@ int check_lin_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
 // which dg's sums run).  An SM has `share` tokens to walk; where no sequence is
 // likely to be longer than that (the longest is taken for four times the mean:
 // only the GPU knows it) they are better left whole, which spares the walk
-// before and the scan (32768 packed tokens of 32 heads in bf16: 360 us, and 436
+// before and the scan (32768 packed tokens of 32 heads in bf16: 271 us, and 352
 // in segments of 1792); otherwise a quarter of it each fills the GPU evenly, but
-// no fewer than 256 tokens (3001 of 6 heads in f32: 82 us, 97 with 128, 105 with
-// 384; 4000 of 8 in bf16: 48 us, 63 with 128, 55 with 512), and no pack of 512
-// is worth it (500 tokens in bf16: 30 us, 35 with 256).
+// no fewer than 256 tokens (3001 of 6 heads in f32: 83 us, 97 with 128, 107 with
+// 384; 4000 of 8 in bf16: 52 us, 68 with 128, 60 with 512), and no pack of 512
+// is worth it (500 tokens in bf16: 29 us, 36 with 256).
 int lin_segment(int64_t T, int64_t S, int Hv, int ctas, IO io) {
   const int64_t chunk = lin_chunk(io), share = T * Hv * ctas / 152, longest = 4 * T / (S > 0 ? S : 1);
   if (longest <= share) return kLinMaxSegment;

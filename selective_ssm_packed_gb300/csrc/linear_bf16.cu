@@ -24,8 +24,8 @@ namespace {
 // operands take one data path of the SM, 8000 cycles of it a chunk.
 // 32768 tokens, 32 heads of 128: 250 us forward (807 MB, 3.2 TB/s), the gradients
 // 305 (dq), 345 (dk) and 286 us (dv); a key head shared by 8 value heads writes its
-// dq and dk as f32 parts of each, 512 MB more (16384 tokens, 64 heads of 64: 390
-// and 416 us).
+// dq and dk as f32 parts of each, 512 MB more (16384 tokens, 64 heads of 64: 383
+// and 439 us).
 //
 // Terms: inputs are exact in one; up * W and, for the roles with dot products, P
 // and S in D1 have two, 16 bits, which leaves dg 5e-6 off (three would not fit

@@ -458,9 +458,8 @@ int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t
  *   every token.
  * Precision: FP32 operands of the tensor cores' products are sums of bf16
  *   terms, three for f32 I/O, two for bf16 I/O; accumulation and the state
- *   are float32.  With bf16 I/O the weights of pairs and the state that a
- *   token's query meets are one term on the way to out, which adds about one
- *   rounding to bf16 to that of out itself; final_states has 16 bits or more.
+ *   are float32.  bf16 results lose no more than their own rounding;
+ *   final_states of bf16 calls has 16 bits or more.
  * A value that is not finite reaches what the recurrence carries it to and
  *   nothing else, as there; beside a g that is not finite the earlier tokens
  *   of its chunk (of 64 tokens in f32, 128 in bf16) keep their values, but
@@ -486,8 +485,7 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
  * states are made again; nothing of the forward call has to be kept.
  * d_final_states: nullable, the gradient reaching the final states.  dq and dk
  * add the value heads that share a head, in order; no atomics, bitwise
- * repeatable.  With bf16 I/O dv (without dg, dq and dk too) has the one rounding
- * more that out has, and dg is about 5e-6 of its norm off; data in bf16 whose
+ * repeatable.  With bf16 I/O dg is about 5e-6 of its norm off; data in bf16 whose
  * dg and states are wanted with all bits are passed as f32.
  * A value that is not finite in q, k, v, dout or the states reaches the
  * gradients that the formula carries it to; dg, a sum over a segment, is not

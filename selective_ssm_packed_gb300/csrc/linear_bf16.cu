@@ -27,11 +27,9 @@ namespace {
 // dq and dk as f32 parts of each, 512 MB more (16384 tokens, 64 heads of 64: 383
 // and 439 us).
 //
-// Terms: inputs are exact in one; up * W and, for the roles with dot products, P
-// and S in D1 have two, 16 bits, which leaves dg 5e-6 off (three would not fit
-// in tensor memory).  The other roles' results are only rounded to bf16, for
-// which P and S have one term, rounded to nearest: out is then 2.2e-3 of its norm
-// off (1.7e-3 with two), and W's second buffer has room.
+// Terms: inputs are exact in one; up * W, P and S in D1 have two, 16 bits, so
+// that results lose no more than their own rounding to bf16 (with one term of P
+// and S out was 2.3e-3 of its norm off, 1.7e-3 with two).
 constexpr int kC = 128, kStateWarps = 8, kOutWarps = 8, kParts = kOutWarps / 4;
 constexpr int kProducts = kStateWarps + kOutWarps, kCopies = kProducts + 1, kGatesWarp = kProducts + 2, kWarps = kProducts + 4;
 constexpr int kPanel = kC * 128;  // bytes of 64 columns of a chunk's rows
@@ -43,10 +41,8 @@ template <int KP, int NP>  // panels of 64 columns of X and Y, and of W
 struct WalkSmem {
   static constexpr int kX = KP * kPanel, kW = NP * kPanel, kUp = 2 * kW, kSBlock = KP * 8192, kSTerm = NP * kSBlock;
   static constexpr int oX = 0, oY = kX, oW = 2 * kX, oUp = oW + kW, oS = oUp + kUp, oGates = oS + 2 * kSTerm;
-  // W's second buffer: where nothing else is left, the place of S's second term, which only rows with a dot product use
-  static constexpr bool kRoom = KP == 1 || NP == 1;
-  static constexpr int oW2 = kRoom ? oGates : oS + kSTerm, oTokens = kRoom ? oGates + kW : oGates;
-  static_assert(kRoom || kSTerm == kW, "");
+  static constexpr bool kRoom = KP == 1 || NP == 1;  // for a second buffer of W
+  static constexpr int oW2 = kRoom ? oGates : oW, oTokens = kRoom ? oGates + kW : oGates;
   static constexpr int oMisc = oTokens + 4 * 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -83,12 +79,6 @@ __device__ __forceinline__ void copy_panels(const CUtensorMap* map, uint8_t* to,
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {  // the first 8
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 // 16 columns each from two places of this thread's lane, on their way together.
@@ -252,8 +242,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
   Pair* s_last = reinterpret_cast<Pair*>(s_sums + 14);  // the chunk's sum
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(s_sums + 13);
 
-  constexpr int terms = has_dot ? 2 : 1;  // of P, and of S in D1
-  constexpr bool two_w = L::kRoom || !has_dot;
+  constexpr bool two_w = L::kRoom;
   auto w_image = [&](int k) { return sm + (two_w && (k & 1) ? L::oW2 : L::oW); };
   const int seg_at = a.order[item];
   const Segment seg(a.table[seg_at]);
@@ -292,8 +281,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
     auto state_at = [&](int col) { return (int64_t)row * role.srow + (int64_t)col * role.scol; };
     auto put_state = [&](int col, const float2 (&d)[8]) {
       uint8_t* image = sm + L::oS + col / 64 * L::kSBlock;
-      if (terms == 2) put_row<2, 128>(image, L::kSTerm, row, col % 64 / 8, d);
-      else put_row<1, 128>(image, 0, row, col % 64 / 8, d);
+      put_row<2, 128>(image, L::kSTerm, row, col % 64 / 8, d);
     };
     auto load_state = [&](const float* from, int col, float2 (&d)[8]) {  // 16 columns of this thread's row
 #pragma unroll
@@ -496,35 +484,24 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
               if ((unsigned)(2 * i + 1 - from) >= (unsigned)count) d[i].y = 0.0f;
             }
           }
-          if (terms == 2) {
+          if (back && !has_dot && !all && role.pairs && (unsigned)at < 16u && row < rows)
+            role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = self;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t term[2];
-              split_pair<2>(d[i], term);
-              words[i] = term[0];
-              words[8 + i] = term[1];
-              if (!all) {  // the pair's weight as the product with W has it
-                if (at == 2 * i) weight = bf16_lo(term[0]) + bf16_lo(term[1]);
-                if (at == 2 * i + 1) weight = bf16_hi(term[0]) + bf16_hi(term[1]);
-              }
-            }
-            if (!all && (unsigned)at < 16u && row < rows) {
-              role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = weight;
-            }
-          } else {
-            if (back && !all && role.pairs && (unsigned)at < 16u && row < rows)
-              role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = self;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t term[1];
-              split_pair<1>(d[i], term);
-              words[i] = term[0];
+          for (int i = 0; i < 8; ++i) {
+            uint32_t term[2];
+            split_pair<2>(d[i], term);
+            words[i] = term[0];
+            words[8 + i] = term[1];
+            if (has_dot && !all) {  // the pair's weight as the product with W has it
+              if (at == 2 * i) weight = bf16_lo(term[0]) + bf16_lo(term[1]);
+              if (at == 2 * i + 1) weight = bf16_hi(term[0]) + bf16_hi(term[1]);
             }
           }
+          if (has_dot && !all && (unsigned)at < 16u && row < rows)
+            role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = weight;
         }
         __syncwarp();
-        if (terms == 2) tmem_st16(tm + tA + lane_at + j0, words);
-        else tmem_st8(tm + tA + lane_at + j0, words);
+        tmem_st16(tm + tA + lane_at + j0, words);
       }
       tmem_wait_st();
       warp_arrive(bars + kGatesFree, lane);
@@ -629,14 +606,13 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           if (__all_sync(0xffffffffu, wait.ok)) {
             tmem_fence_after_sync();
             constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
-            const int i0 = terms == 2 ? 0 : KP;
 #pragma unroll 1
-            for (int i = i0; i < 2 * KP; ++i) {  // the smaller term first
+            for (int i = 0; i < 2 * KP; ++i) {  // the smaller term first
               const int term = 1 - i / KP, panel = i % KP;
 #pragma unroll
               for (int s = 0; s < 4; ++s)
                 umma_if(lead, tm + tD1, x + (panel * kPanel + s * 32) / 16, st + (term * L::kSTerm + (4 * panel + s) * kStep) / 16, idesc,
-                        i - i0 + s > 0 ? 1u : 0u);
+                        i + s > 0 ? 1u : 0u);
             }
             if (lead) umma_commit(bars + kDoneX);
           }
@@ -658,14 +634,13 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
             tmem_fence_after_sync();
             const uint64_t w = smem_desc<128>(smem_u32(w_image(k)), kPanel);
             constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
-            constexpr int i0 = terms == 2 ? 0 : 2;
 #pragma unroll 1
-            for (int i = i0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const int term = 1 - i / 2;
 #pragma unroll
               for (int s = 0; s < 4; ++s)
                 umma_ta_if(lead, tm + tO, tm + tA + 16 * ((i & 1) * 4 + s) + 8 * term, w + ((i & 1) * 4 + s) * (kStep / 16), idesc,
-                           i - i0 + s > 0 ? 1u : 0u);
+                           i + s > 0 ? 1u : 0u);
             }
             if (lead) umma_commit(bars + kDoneO);
           }

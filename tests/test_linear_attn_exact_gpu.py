@@ -1,0 +1,50 @@
+"""How exact linear attention is on the GPU, where its first tests look at a
+whole tensor's norm or leave room for more: results in bf16, states and decays'
+gradients of bf16 calls, decays that forget, tails without a gradient, values
+that are not finite, at the widths of one and of two panels of 64 columns.
+
+Errors and references are 2-norms over what is named.
+"""
+import numpy as np
+import pytest
+import torch
+
+import selective_ssm_packed_gb300 as vs
+from selective_ssm_packed_gb300 import binding
+from test_linear_attn_gpu import host, inputs, reference, run
+
+pytestmark = pytest.mark.gpu
+
+WIDTHS = [(64, 64), (128, 128), (128, 64), (64, 128)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from selective_ssm_packed_gb300 import build
+    build.build()
+    binding.lib()
+
+
+def rounded(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(torch.bfloat16).double().numpy()
+
+
+def off(got, ref):
+    return np.linalg.norm(got - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("lens", [[500, 130, 3], [3000]])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_bf16_results_lose_no_more_than_their_rounding(K, V, lens):
+    """A result that is off by e before it is rounded gets another bf16 value than the exact one with a probability of
+    |e| / step, and is then one step off: the squares add up to |e| step, the step being 2^-7 of the value at most.  An
+    operand of two terms is 2^-17 off at most, and a result has three of them: e is 3 * 2^-17 < 2^-15 of the size of
+    the values, so that what differs is sqrt(2^-15 * 2^-7) = 2^-11."""
+    x = inputs(lens, 1, 2, K, V, "bf16", 40, True)
+    got, ref = run(x, states=True), reference(x)
+    for n in ("out", "dq", "dk", "dv"):
+        assert off(host(got[n]), rounded(ref[n])) <= 2.0 ** -11, n
+    g = vs.varlen_linear_attn_bwd(x["q"], x["k"], x["v"], x["g"], x["dout"], x["cu"], initial_states=x["init"],
+                                  d_final_states=x["dfinal"], dg=False)
+    for n in ("dq", "dk", "dv"):
+        assert off(host(g[n]), rounded(ref[n])) <= 2.0 ** -11, n

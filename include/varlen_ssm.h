@@ -523,7 +523,8 @@ int varlen_linear_attn_step(const void* q, const void* k, const void* v, int64_t
  *   may be residual.
  * out (T, D) io, contiguous; all pointers 16-byte aligned.
  * D / groups a multiple of 8, 8 to 8192; groups at most 65535.
- * Statistics are float32, of the differences from the mean.
+ * Statistics are float32, of the differences from the mean, whose own rounding is
+ * taken out: a mean far from zero costs no digits, constant rows give the bias.
  */
 int varlen_layer_norm_fwd(const void* x, int64_t x_stride, const float* residual, const float* weight,
                           const float* bias, int64_t total_tokens, int32_t D, int32_t groups, float eps,

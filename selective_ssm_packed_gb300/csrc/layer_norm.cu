@@ -15,6 +15,11 @@ namespace {
 // where the mean is far from 0), both in f32.  A team walks over rows of one
 // group, so that its weights, and in the backward their gradients, are
 // registers too; the next row is on its way while one is worked on.
+// The mean that is taken from a row is itself rounded, by up to 2^-20 of a mean
+// that may be a thousand deviations away.  What it leaves is the same in all of
+// the row: the mean of the centred row, whose sum is exact to 2^-20 of its own
+// small size and comes with the squares' in one pass over the team.  It is taken
+// from the row, and its square from the variance.
 // Everything is read and written once, which bounds the pass: 32768 x 2048 in
 // bf16 with the f32 stream 117 us (6.9 TB/s, some of it left in L2), 32 groups of 128 in 4096
 // channels 83 us (6.5 TB/s), one row of 2048 4 us.
@@ -33,7 +38,7 @@ constexpr int bwd_threads() { return kTeam >= 256 ? 512 : 384; }
 // v[i] summed over the team, in a fixed order.  flip: which half of the scratch
 // is this sum's; one barrier a sum is enough with two.
 template <int kTeam, int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], float (*scratch)[3][16], int& flip) {
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*scratch)[4][16], int& flip) {
   constexpr int kWidth = kTeam < 32 ? kTeam : 32;
 #pragma unroll
   for (int i = 0; i < N; ++i)
@@ -86,9 +91,9 @@ __device__ __forceinline__ void load_params(const float* p, const Place<kTeam>& 
   }
 }
 
-// The row's centred values and 1 / its standard deviation.
+// The row's centred values, but for the mean's own rounding.
 template <int kTeam>
-__device__ __forceinline__ void centre(float (&h)[2][8], const Place<kTeam>& at, float inv_count, float (*scratch)[3][16], int& flip) {
+__device__ __forceinline__ void centre(float (&h)[2][8], const Place<kTeam>& at, float inv_count, float (*scratch)[4][16], int& flip) {
   float s[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -102,10 +107,16 @@ __device__ __forceinline__ void centre(float (&h)[2][8], const Place<kTeam>& at,
     for (int j = 0; j < 8; ++j) h[i][j] = at.in[i] ? h[i][j] - mean : 0.0f;
 }
 
+// 1 / the standard deviation, from the centred row's sum of squares and its own mean.
+__device__ __forceinline__ float inv_std(float squares, float rest, float inv_count, float eps) {
+  const float var = fmaf(-rest, rest, squares * inv_count);
+  return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);  // below 0 by rounding only; NaN stays
+}
+
 template <typename T, bool kRes, int kTeam>
 __global__ void __launch_bounds__(Team<kTeam>::kThreads, fwd_threads<T, kRes>() / Team<kTeam>::kThreads)
     layer_norm_fwd_kernel(LayerNormArgs a, int64_t slots) {
-  __shared__ float scratch[2][3][16];
+  __shared__ float scratch[2][4][16];
   const int64_t slot = (int64_t)blockIdx.x * Team<kTeam>::kUnits + threadIdx.x / kTeam;
   const Place<kTeam> at(a, slot);
   const float inv_count = 1.0f / (float)(a.D / a.groups);
@@ -148,33 +159,36 @@ __global__ void __launch_bounds__(Team<kTeam>::kThreads, fwd_threads<T, kRes>() 
       for (int i = 0; i < 2; ++i)
         if (mine && at.in[i]) st_io8(a.sum + row + at.d[i], h[i]);
     centre(h, at, inv_count, scratch, flip);
-    float s[1] = {0.0f};
+    float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);
+      for (int j = 0; j < 8; ++j) {
+        s[0] = fmaf(h[i][j], h[i][j], s[0]);
+        s[1] += h[i][j];
+      }
     team_sum<kTeam>(s, scratch, flip);
-    const float r = 1.0f / sqrtf(fmaf(s[0], inv_count, a.eps));
+    const float rest = s[1] * inv_count, r = inv_std(s[0], rest, inv_count, a.eps);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j] * r, w[i][j], b[i][j]);
+      for (int j = 0; j < 8; ++j) h[i][j] = fmaf((h[i][j] - rest) * r, w[i][j], b[i][j]);
       if (mine && at.in[i]) st_io8(static_cast<T*>(a.out) + row + at.d[i], h[i]);
     }
   }
 }
 
-// With c the centred row, r = 1 / its standard deviation, n = c r and u = dy w:
+// With c the centred row without its own mean, r = 1 / its standard deviation, n = c r and u = dy w:
 //   dh = r (u - mean(u) - n mean(u n)) + dsum
 //   dweight = sum over tokens of dy n,  dbias = sum of dy
 // One row of sums per team goes to `partial`, which a second kernel adds in
 // the teams' order: no atomics, the same bits every time.  32768 x 2048 with the
-// stream 151 us (6.2 TB/s), 32 groups of 128 in 4096 channels 143 us (5.6 TB/s: four sums
+// stream 151 us (6.2 TB/s), 32 groups of 128 in 4096 channels 143 us (5.5 TB/s: five sums
 // a row of 8 threads keep the issue slots 60% busy), the teams' sums 8 us.
 template <typename T, typename H, int kTeam>
 __global__ void __launch_bounds__(Team<kTeam>::kThreads, bwd_threads<kTeam>() / Team<kTeam>::kThreads)
     layer_norm_bwd_kernel(LayerNormArgs a, int64_t slots) {
-  __shared__ float scratch[2][3][16];
+  __shared__ float scratch[2][4][16];
   const int64_t slot = (int64_t)blockIdx.x * Team<kTeam>::kUnits + threadIdx.x / kTeam;
   const Place<kTeam> at(a, slot);
   const int width = a.D / a.groups;
@@ -216,7 +230,7 @@ __global__ void __launch_bounds__(Team<kTeam>::kThreads, bwd_threads<kTeam>() / 
 #pragma unroll
       for (int i = 0; i < 2; ++i) rs[i].load(a.dsum + row + at.d[i], mine && at.in[i]);
     centre(h, at, inv_count, scratch, flip);
-    float s[3] = {0.0f, 0.0f, 0.0f};
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -225,15 +239,17 @@ __global__ void __launch_bounds__(Team<kTeam>::kThreads, bwd_threads<kTeam>() / 
         s[0] = fmaf(h[i][j], h[i][j], s[0]);
         s[1] += u;
         s[2] = fmaf(u, h[i][j], s[2]);
+        s[3] += h[i][j];
       }
     team_sum<kTeam>(s, scratch, flip);
-    const float r = 1.0f / sqrtf(fmaf(s[0], inv_count, a.eps));
-    const float mean_u = s[1] * inv_count, f = s[2] * inv_count * r * r;
+    const float rest = s[3] * inv_count, r = inv_std(s[0], rest, inv_count, a.eps);
+    const float mean_u = s[1] * inv_count, f = fmaf(-rest, s[1], s[2]) * inv_count * r * r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        h[i][j] -= rest;
         if (mine) {
           gw[i][j] = fmaf(g[i][j], h[i][j] * r, gw[i][j]);
           gb[i][j] += g[i][j];

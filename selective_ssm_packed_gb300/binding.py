@@ -874,7 +874,8 @@ def varlen_layer_norm_bwd(x, weight, bias, dout, groups=1, eps=1e-5, residual=Fa
     g = dict(grads or {})
     make = {"dx": ((T, D), dout.dtype), "dresidual": ((T, D), torch.float32), "dweight": ((D,), torch.float32),
             "dbias": ((D,), torch.float32)}
-    _together(x, weight, dout, dsum, workspace, *g.values())
+    _together(x, weight, bias, dout, dsum, workspace, *g.values())
+    _shaped(bias, "bias", (D,))  # the call needs none of its values
     with _device_of(x):
         for n, wanted in (("dx", True), ("dresidual", residual), ("dweight", weight is not None),
                           ("dbias", bias is not None)):

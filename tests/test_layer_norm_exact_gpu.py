@@ -1,7 +1,9 @@
 """Layer norm on the GPU where rows lie far from zero or have no variance, and
 its refusals of a bias in the backward."""
 import pytest
+import torch
 
+import selective_ssm_packed_gb300 as vs
 from selective_ssm_packed_gb300 import binding
 from test_layer_norm_gpu import check, host, inputs, run
 from oracle import linear_attn as ol
@@ -42,3 +44,27 @@ def test_constant_rows_have_no_output(D, groups, value, dtype):
     size = abs(dx).max()
     assert abs(host(got["dx"]) - dx).max() <= (1e-5 + (0.0 if dtype == "f32" else 2.0 ** -8)) * size
     assert abs(host(got["dweight"])).max() <= 2.0 ** -28 * abs(value)
+
+
+def test_the_backward_looks_at_the_bias():
+    x = inputs(5, 64, "f32", False, True, 32)
+    a = (x["x"], x["w"])
+    for bias, error in ((x["b"][:32].contiguous(), ValueError), (x["b"].double(), TypeError), (object(), TypeError), (x["b"].cpu(), TypeError)):
+        with pytest.raises(error):
+            vs.varlen_layer_norm_fwd(*a, bias)
+        with pytest.raises(error):
+            vs.varlen_layer_norm_bwd(*a, bias, x["dy"])
+
+
+def test_every_tensor_of_a_call_is_looked_at_for_its_device(monkeypatch):
+    seen = []
+    monkeypatch.setattr(binding, "_together", lambda *t: seen.append({id(x) for x in t}))
+    y, w = torch.zeros((5, 64), device="cuda"), torch.ones(64, device="cuda")
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    fwd = dict(x=y, weight=w, bias=w.clone(), residual=y.clone(), out=y.clone(), sum_out=y.clone())
+    bwd = dict(x=y, weight=w, bias=w.clone(), dout=y.clone(), dsum=y.clone(), workspace=ws)
+    dx = y.clone()
+    vs.varlen_layer_norm_fwd(**fwd)
+    vs.varlen_layer_norm_bwd(**bwd, residual=True, grads={"dx": dx})
+    for at, given in zip(seen, (fwd, dict(bwd, dx=dx)), strict=True):
+        assert all(id(t) in at for t in given.values())

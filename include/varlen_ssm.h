@@ -459,7 +459,8 @@ int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t
  * Precision: FP32 operands of the tensor cores' products are sums of bf16
  *   terms, three for f32 I/O, two for bf16 I/O; accumulation and the state
  *   are float32.  bf16 results lose no more than their own rounding;
- *   final_states of bf16 calls has 16 bits or more.
+ *   final_states (and the backward's d_initial_states) keep all 24 bits, in
+ *   bf16 calls by a walk of their own.
  * A value that is not finite reaches what the recurrence carries it to and
  *   nothing else, as there; beside a g that is not finite the earlier tokens
  *   of its chunk (of 64 tokens in f32, 128 in bf16) keep their values, but
@@ -486,7 +487,7 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
  * d_final_states: nullable, the gradient reaching the final states.  dq and dk
  * add the value heads that share a head, in order; no atomics, bitwise
  * repeatable.  With bf16 I/O dg is about 5e-6 of its norm off; data in bf16 whose
- * dg and states are wanted with all bits are passed as f32.
+ * dg is wanted with all bits are passed as f32.
  * A value that is not finite in q, k, v, dout or the states reaches the
  * gradients that the formula carries it to; dg, a sum over a segment, is not
  * finite before it in the sequence's segments and keeps its value, but not its

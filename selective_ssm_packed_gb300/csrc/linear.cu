@@ -515,7 +515,7 @@ cudaError_t run_walk(const LinArgs& a, int roles, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_lin_walk(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, IO io, cudaStream_t st) {
-  if (io == IO::BF16) return launch_lin_walk_bf16(a, maps, roles, state_only, st);
+  if (io == IO::BF16) return state_only ? launch_lin_state_bf16(a, maps, roles, false, st) : launch_lin_walk_bf16(a, maps, roles, st);
   if ((state_only ? a.max_inner : a.max_segs) == 0) return cudaSuccess;
   int width = 0;
   for (int i = 0; i < roles; ++i) width = width > a.role[i].n1 ? width : a.role[i].n1;

@@ -80,7 +80,7 @@ struct LinRole {
   int back;                // reversed time
   int64_t srow, scol;      // a state's element (row of n1, column of n2) in memory
   const float* first;      // states that the sequences come with, (S, Hv, ., .), or null
-  float* last;             // states that they leave, or null
+  float* last;             // states that they leave, or null (bf16: of the state-only walks)
   float* slots;            // states between segments, (inner segments, Hv, ., .)
   float* decay;            // (inner segments, Hv): exp of the segment's sum of g (the state-only walks write it)
   const float* against;    // gradients of the states at the segments' ends, as `slots` of a reversed role, or null
@@ -123,7 +123,9 @@ constexpr int kLinFirst = 1, kLinLast = 2, kLinPlaceShift = 2;
 cudaError_t launch_lin_plan(const LinArgs& a, cudaStream_t st);
 // state_only: the inner segments of roles [0, roles), otherwise all segments.
 cudaError_t launch_lin_walk(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, IO io, cudaStream_t st);
-cudaError_t launch_lin_walk_bf16(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, cudaStream_t st);
+cudaError_t launch_lin_walk_bf16(const LinArgs& a, const LinMaps& maps, int roles, cudaStream_t st);
+// bf16, ends: the states that the sequences leave (the f32 walk writes them as it goes).
+cudaError_t launch_lin_state_bf16(const LinArgs& a, const LinMaps& maps, int roles, bool ends, cudaStream_t st);
 cudaError_t launch_lin_scan(const LinArgs& a, int roles, cudaStream_t st);
 cudaError_t launch_lin_dg(const LinArgs& a, IO io, cudaStream_t st);
 cudaError_t launch_lin_head_sum(const LinArgs& a, IO io, cudaStream_t st);

@@ -201,6 +201,7 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
   TRY(check(launch_lin_walk(a, maps, 1, true, io, st), "linear attention state launch"));
   TRY(check(launch_lin_scan(a, 1, st), "linear attention scan launch"));
   TRY(check(launch_lin_walk(a, maps, 1, false, io, st), "linear attention forward launch"));
+  if (io == IO::BF16 && final_states) TRY(check(launch_lin_state_bf16(a, maps, 1, true, st), "linear attention final state launch"));
   const void* outs[] = {out, final_states};
   const int64_t counts[] = {T * Hv * V, (int64_t)num_seqs * Hv * K * V};
   const bool f32[] = {io == IO::F32, true};
@@ -291,6 +292,11 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
     rk.dot = k; rk.sdot = k_stride; rk.rdot = rep; rk.dots = reinterpret_cast<float*>(p + l.sigma);
   }
   TRY(check(launch_lin_walk(a, maps, 3, false, io, st), "linear attention backward launch"));
+  if (io == IO::BF16 && d_initial_states) {
+    s.role[0] = s.role[1];
+    s.role[0].last = d_initial_states;
+    TRY(check(launch_lin_state_bf16(s, maps, 1, true, st), "linear attention initial state launch"));
+  }
   if (dg) TRY(check(launch_lin_dg(a, io, st), "linear attention decay gradient launch"));
   if (rep > 1) TRY(check(launch_lin_head_sum(a, io, st), "linear attention head sum launch"));
   const void* outs[] = {dq, dk, dv, dg, d_initial_states};

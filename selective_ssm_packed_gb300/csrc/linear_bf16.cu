@@ -321,7 +321,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
     }
     fence_async_smem();
     warp_arrive(bars + kStateReady, lane);
-    const bool wanted = (role.cross && (!back || seg.is_first)) || (role.last && (back ? seg.is_first : seg.is_last));
+    const bool wanted = role.cross && (!back || seg.is_first);
     for (int k = 0; k < n; ++k) {
       const uint32_t p = k & 1;
       const bool more = k + 1 < n;
@@ -371,50 +371,37 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
     }
     if (wanted) {
       tmem_fence_after_sync();
-      float* to = role.last && (back ? seg.is_first : seg.is_last) ? role.last + ((int64_t)seg.seq * a.Hv + h) * state_size : nullptr;
       const float *e = nullptr, *at_end = nullptr;  // between segments: the state as it was made for the next one
-      if (role.cross && !back && !seg.is_last) at_end = role.slots + (seg.inner_before * a.Hv + h) * state_size;
-      if (role.cross) {
-        if (!back && !seg.is_last) e = role.against + (seg.inner_before * a.Hv + h) * state_size;
-        else if (role.against_last) e = role.against_last + ((int64_t)seg.seq * a.Hv + h) * state_size;
+      if (!back && !seg.is_last) {
+        at_end = role.slots + (seg.inner_before * a.Hv + h) * state_size;
+        e = role.against + (seg.inner_before * a.Hv + h) * state_size;
+      } else if (role.against_last) {
+        e = role.against_last + ((int64_t)seg.seq * a.Hv + h) * state_size;
       }
       float2 sum = splat2(0.0f);
-      if (has_row && (to || e)) {
+      if (has_row && e) {
 #pragma unroll 1
         for (int u = 0; u < kCols / 16; ++u) {
-          float2 d[8];
+          float2 d[8], x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] = splat2(0.0f);
           if (n > 0 || has_carry) tmem_sum<1>(tm + tU + lane_at + c0 + 16 * u, 0, d);
           scale_row(d, unit);
           if (at_end) load_state(at_end, c0 + 16 * u, d);
-          if (e) {
-            float2 x[8];
-            load_state(e, c0 + 16 * u, x);
+          load_state(e, c0 + 16 * u, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)  // past the state d may be what the matrix unit made of other rows
-              if (row < n1 && c0 + 16 * u + 2 * i < n2) sum = fma2(d[i], x[i], sum);
-          }
-          if (to)
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const int col = c0 + 16 * u + 2 * i;
-              if (row >= n1 || col >= n2) continue;
-              float* q = to + state_at(col);  // these are never the transposed ones
-              *reinterpret_cast<float4*>(q) = make_float4(d[i].x, d[i].y, d[i + 1].x, d[i + 1].y);
-            }
+          for (int i = 0; i < 8; ++i)  // past the state d may be what the matrix unit made of other rows
+            if (row < n1 && c0 + 16 * u + 2 * i < n2) sum = fma2(d[i], x[i], sum);
         }
       }
-      if (role.cross) {
-        float v = sum.x + sum.y;
+      float v = sum.x + sum.y;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) s_sums[warp] = v;
-        named_barrier(1, 32 * kStateWarps);
-        if (t == 0) {
-          for (int i = 1; i < kStateWarps; ++i) v += s_sums[i];
-          role.cross[(int64_t)seg_at * a.Hv + h] = v;
-        }
+      for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) s_sums[warp] = v;
+      named_barrier(1, 32 * kStateWarps);
+      if (t == 0) {
+        for (int i = 1; i < kStateWarps; ++i) v += s_sums[i];
+        role.cross[(int64_t)seg_at * a.Hv + h] = v;
       }
     }
   } else if (warp < kStateWarps + kOutWarps) {  // the results' path
@@ -750,14 +737,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 }
 
 // ------------------------------------------------------------------ what a segment adds to the state
-// One CTA per (inner segment, value head, role): the sum of Y^T (up * W) with up
-// the weights up to the segment's end, so that the chunks add up in tensor
-// memory with nothing read back in between: the chunk next to that end comes
-// first, and each earlier one's weights carry the decay over the ones behind it.
-// One sequence of 32768 tokens, 32 heads of 128: 144 us (537 MB, 3.7 TB/s;
-// 24 us of it for the third term).
-// Three terms, all 24 bits: these states are what dg is held to at the ends of
-// the segments.
+// One CTA per (segment, value head, role): the sum of Y^T (up * W) with up the
+// weights up to the segment's end, in which the chunks just add up: the one next
+// to that end comes first, and each earlier one's weights carry the decay over
+// the ones behind it.  up * W has three terms, all 24 bits, and a chunk's sum is
+// added in registers while the next one's is made: the matrix unit cuts off what
+// it adds to a running sum, which left the state of 4096 tokens of slow decays
+// 6.6e-6 too small.  First the segments that others follow, for the scan; once
+// the states before all segments are known, those that a sequence ends with (back:
+// starts with), where its last state is asked for.
+// One sequence of 32768 tokens, 32 heads of 128: 144 us (537 MB, 3.7 TB/s).
 constexpr int kStateTerms = 3;
 template <int KP, int NP>
 struct StateSmem {
@@ -770,9 +759,9 @@ constexpr int kWeighWarps = 16;
 
 template <int KP, int NP>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-    lin_state_bf16_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps, int roles) {
+    lin_state_bf16_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps, int roles, bool ends) {
   using L = StateSmem<KP, NP>;
-  constexpr int kN = NP * 64, kCols = NP * 32;
+  constexpr int kN = NP * 64, kCols = NP * 16;  // columns of W, and to a thread of the sum
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
   uint64_t *full = bars, *gates_full = bars + 2, *used = bars + 4, *up_ready = bars + 6, *done = bars + 7, *drained = bars + 9;
@@ -781,10 +770,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(s_total + 2);
   const int which = blockIdx.x % roles, h = blockIdx.x / roles % a.Hv;
   const int64_t item = blockIdx.x / roles / a.Hv;
-  if (item >= a.info[1]) return;
+  if (item >= a.info[ends ? 0 : 1]) return;
   const LinRole& role = a.role[which];
   const bool back = role.back != 0;
-  const Segment seg(a.table[a.inner[item] + (back ? 1 : 0)]);
+  const Segment seg(a.table[ends ? a.order[item] : a.inner[item] + (back ? 1 : 0)]);
+  if (ends && !(back ? seg.is_first : seg.is_last)) return;
   const int n1 = role.n1, n2 = role.n2, n = seg.n;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, row = quad * 32 + lane;
   if (t == 0) {
@@ -792,7 +782,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     *stop = 0;
     fence_mbar_init();
   }
-  if (warp == kProducts) tmem_alloc<128>(tmem_at);
+  if (warp == kProducts) tmem_alloc<256>(tmem_at);
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
@@ -814,8 +804,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const int term = kStateTerms - 1 - i / 2;
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            umma_if(lead, tm, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc,
-                    k + i + s > 0 ? 1u : 0u);
+            umma_if(lead, tm + (k & 1) * 128, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16,
+                    idesc, i + s > 0 ? 1u : 0u);
         }
         if (lead) umma_commit(done + (k & 1));
       }
@@ -855,7 +845,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
     };
     float g[4];
-    load_g(chunk_of(0), g);
+    if (n > 0) load_g(chunk_of(0), g);
     Pair behind{0.0f, 0.0f};
     for (int k = 0; k < n; ++k) {
       Pair last, run = running_sums(g, lane, last);
@@ -873,61 +863,86 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       reinterpret_cast<float4*>(sm + L::oGates + (k & 1) * 4 * kC)[lane] = make_float4(up[0], up[1], up[2], up[3]);
       if (k + 1 == n && lane == 0) {
         *s_total = exp2_of(behind);
-        role.decay[item * a.Hv + h] = *s_total;
+        if (!ends) role.decay[item * a.Hv + h] = *s_total;
       }
       warp_arrive(gates_full + (k & 1), lane);
     }
   } else if (warp < kWeighWarps) {
+    constexpr int kThreads = 32 * kWeighWarps;
+    const int c0 = (warp >> 2) * kCols;
+    float2 sum[kCols / 16][8];
+#pragma unroll
+    for (int u = 0; u < kCols / 16; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[u][i] = splat2(0.0f);
+    auto take = [&](int k) {
+      if (row >= KP * 64) return;
+#pragma unroll
+      for (int u = 0; u < kCols / 16; ++u) {
+        float2 d[8];
+        tmem_sum<1>(tm + (k & 1) * 128 + lane_at + c0 + 16 * u, 0, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[u][i] = add2(sum[u][i], d[i]);
+      }
+    };
     for (int k = 0; k < n; ++k) {
       const int b = k & 1, rows = min(kC, seg.len - chunk_of(k) * kC);
       if (warp == 0) {
         wait(gates_full + b, (k >> 1) & 1);
         wait(full + b, (k >> 1) & 1);
-        if (k > 0) wait(done + ((k - 1) & 1), ((k - 1) >> 1) & 1);  // up * W's place is free
+        if (k > 0) wait(done + ((k - 1) & 1), ((k - 1) >> 1) & 1);  // up * W's place is free, and there is a sum
       }
-      named_barrier(1, 32 * kWeighWarps);
+      named_barrier(1, kThreads);
       if (rows < kC) {
-        clear_rows<KP>(sm + L::oY + b * L::kY, rows, t, 32 * kWeighWarps);
-        clear_rows<NP>(sm + L::oW + b * L::kW, rows, t, 32 * kWeighWarps);
-        named_barrier(1, 32 * kWeighWarps);
+        clear_rows<KP>(sm + L::oY + b * L::kY, rows, t, kThreads);
+        clear_rows<NP>(sm + L::oW + b * L::kW, rows, t, kThreads);
+        named_barrier(1, kThreads);
       }
-      weigh<NP, kStateTerms, 32 * kWeighWarps>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), t,
-                                  nullptr);
+      weigh<NP, kStateTerms, kThreads>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), t,
+                                       nullptr);
+      tmem_fence_before_sync();
       fence_async_smem();
       warp_arrive(used + b, lane);
       if (lane == 0) mbar_arrive(up_ready);
-    }
-    if (warp == 0) wait(done + ((n - 1) & 1), ((n - 1) >> 1) & 1);
-    named_barrier(1, 32 * kWeighWarps);
-    tmem_fence_after_sync();
-    if (warp < kStateWarps) {
-      const int c0 = (warp >> 2) * kCols;
-      const float total = *s_total;
-      const float* carry = role.first && (back ? seg.is_last : seg.is_first)
-                               ? role.first + ((int64_t)seg.seq * a.Hv + h) * ((int64_t)n1 * n2) : nullptr;
-      float* to = role.slots + (item * a.Hv + h) * ((int64_t)n1 * n2);
-#pragma unroll 1
-      for (int u = 0; u < kCols / 16; ++u) {
-        float2 d[8];
-        tmem_sum<1>(tm + lane_at + c0 + 16 * u, 0, d);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const int col = c0 + 16 * u + 2 * i;
-          if (row >= n1 || col >= n2) continue;
-          const int64_t at = (int64_t)row * n2 + col;
-          if (carry) {
-            const float4 f = *reinterpret_cast<const float4*>(carry + at);
-            d[i] = fma2(splat2(total), make_float2(f.x, f.y), d[i]);
-            d[i + 1] = fma2(splat2(total), make_float2(f.z, f.w), d[i + 1]);
-          }
-          *reinterpret_cast<float4*>(to + at) = make_float4(d[i].x, d[i].y, d[i + 1].x, d[i + 1].y);
-        }
+      if (k > 0) {
+        tmem_fence_after_sync();
+        take(k - 1);
       }
     }
+    if (n > 0) {
+      if (warp == 0) wait(done + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+      named_barrier(1, kThreads);
+      tmem_fence_after_sync();
+      take(n - 1);
+    }
+    const int64_t size = (int64_t)n1 * n2;
+    const float total = n > 0 ? *s_total : 1.0f;
+    const float* carry = nullptr;
+    if (back ? seg.is_last : seg.is_first) {
+      if (role.first) carry = role.first + ((int64_t)seg.seq * a.Hv + h) * size;
+    } else if (ends) {
+      carry = role.slots + ((back ? seg.inner_before : seg.inner_before - 1) * a.Hv + h) * size;
+    }
+    float* to = ends ? role.last + ((int64_t)seg.seq * a.Hv + h) * size : role.slots + (item * a.Hv + h) * size;
+#pragma unroll
+    for (int u = 0; u < kCols / 16; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const int col = c0 + 16 * u + 2 * i;
+        if (row >= n1 || col >= n2) continue;
+        const int64_t at = (int64_t)row * n2 + col;
+        float2 x = sum[u][i], y = sum[u][i + 1];
+        if (carry) {
+          const float4 f = *reinterpret_cast<const float4*>(carry + at);
+          x = fma2(splat2(total), make_float2(f.x, f.y), x);
+          y = fma2(splat2(total), make_float2(f.z, f.w), y);
+        }
+        *reinterpret_cast<float4*>(to + at) = make_float4(x.x, x.y, y.x, y.y);
+      }
   }
   tmem_fence_before_sync();
   __syncthreads();
-  if (warp == kProducts) tmem_dealloc<128>(tm);
+  if (warp == kProducts) tmem_dealloc<256>(tm);
 }
 
 template <int KP, int NP, bool back, bool has_dot>
@@ -942,13 +957,13 @@ cudaError_t run_walk(const LinArgs& a, const LinMaps& maps, int which, cudaStrea
 }
 
 template <int KP, int NP>
-cudaError_t run_state(const LinArgs& a, const LinMaps& maps, int roles, cudaStream_t st) {
+cudaError_t run_state(const LinArgs& a, const LinMaps& maps, int roles, bool ends, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const auto kernel = lin_state_bf16_kernel<KP, NP>;
   constexpr size_t bytes = StateSmem<KP, NP>::kBytes;
   const cudaError_t e = set_smem(reinterpret_cast<const void*>(kernel), bytes, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(a.max_inner * a.Hv * roles), kWarps * 32, bytes, st>>>(a, maps, roles);
+  kernel<<<(unsigned)((ends ? a.max_segs : a.max_inner) * a.Hv * roles), kWarps * 32, bytes, st>>>(a, maps, roles, ends);
   return cudaGetLastError();
 }
 
@@ -963,13 +978,15 @@ cudaError_t run_role(const LinArgs& a, const LinMaps& maps, int i, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_lin_walk_bf16(const LinArgs& a, const LinMaps& maps, int roles, bool state_only, cudaStream_t st) {
-  if ((state_only ? a.max_inner : a.max_segs) == 0) return cudaSuccess;
-  if (state_only) {  // all K x V
-    const bool k2 = a.role[0].n1 > 64, v2 = a.role[0].n2 > 64;
-    if (k2) return v2 ? run_state<2, 2>(a, maps, roles, st) : run_state<2, 1>(a, maps, roles, st);
-    return v2 ? run_state<1, 2>(a, maps, roles, st) : run_state<1, 1>(a, maps, roles, st);
-  }
+cudaError_t launch_lin_state_bf16(const LinArgs& a, const LinMaps& maps, int roles, bool ends, cudaStream_t st) {
+  if ((ends ? a.max_segs : a.max_inner) == 0) return cudaSuccess;
+  const bool k2 = a.role[0].n1 > 64, v2 = a.role[0].n2 > 64;  // of all roles: K x V
+  if (k2) return v2 ? run_state<2, 2>(a, maps, roles, ends, st) : run_state<2, 1>(a, maps, roles, ends, st);
+  return v2 ? run_state<1, 2>(a, maps, roles, ends, st) : run_state<1, 1>(a, maps, roles, ends, st);
+}
+
+cudaError_t launch_lin_walk_bf16(const LinArgs& a, const LinMaps& maps, int roles, cudaStream_t st) {
+  if (a.max_segs == 0) return cudaSuccess;
   for (int i = 0; i < roles; ++i) {
     const bool k2 = a.role[i].n1 > 64, v2 = a.role[i].n2 > 64;
     const cudaError_t e = k2 ? (v2 ? run_role<2, 2>(a, maps, i, st) : run_role<2, 1>(a, maps, i, st))

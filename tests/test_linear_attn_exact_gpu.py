@@ -48,3 +48,18 @@ def test_bf16_results_lose_no_more_than_their_rounding(K, V, lens):
                                   d_final_states=x["dfinal"], dg=False)
     for n in ("dq", "dk", "dv"):
         assert off(host(g[n]), rounded(ref[n])) <= 2.0 ** -11, n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", [1e-4, 1e-2, 0.5])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_states_carry_24_bits(K, V, decay, dtype):
+    """bf16 inputs and f32 ones: weights are 2^-22 off (the power) and the products' operands 2^-24; sums are of f32, 900
+    tokens in steps of 16 and three terms, of which the matrix unit may cut off each time up to 2^-24 of the running
+    sum: 168 * 2^-24 = 1e-5 were all of one sign and as large, and sqrt(168) * 2^-24 = 8e-7 as they are of both.  With the
+    weights, 2^-20."""
+    x = inputs([900, 70], 1, 2, K, V, dtype, 41, True)
+    x["g"] = (-decay * torch.exp(0.5 * torch.randn(x["g"].shape, generator=torch.Generator().manual_seed(1)))).cuda()
+    got, ref = run(x, states=True), reference(x)
+    for n in ("final", "dinit"):
+        assert off(host(got[n]), ref[n]) <= 2.0 ** -20, n

@@ -35,7 +35,7 @@ struct LinLayout {
   int seg;
   int64_t max_segs, max_inner;
   size_t table, order, inner, split, slots, decay, fwd_end;
-  size_t slots_back, decay_back, rho, sigma, pairs, cross, cross_back, seg_dg, dq_part, dk_part, bwd_end;
+  size_t slots_back, decay_back, rho, sigma, cross, cross_back, seg_dg, dq_part, dk_part, bwd_end;
 };
 
 LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, bool bwd) {
@@ -58,7 +58,6 @@ LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, 
   l.decay_back = o; o += up(inner * Hv * sizeof(float));
   l.rho = o; o += up(lin_dot_parts(io, K) * tokens);
   l.sigma = o; o += up(lin_dot_parts(io, K) * tokens);
-  l.pairs = o; o += io == IO::BF16 ? 3 * up(tokens) : 0;
   l.cross = o; o += up(segs * Hv * tk * sizeof(float));
   l.cross_back = o; o += up(segs * Hv * tk * sizeof(float));
   l.seg_dg = o; o += up(segs * Hv * sizeof(double));
@@ -283,8 +282,6 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   if (dg) {
     rq.dot = q; rq.sdot = q_stride; rq.rdot = rep; rq.dots = reinterpret_cast<float*>(p + l.rho);
     rq.against = slots_back; rq.against_last = d_final_states; rq.cross = reinterpret_cast<float*>(p + l.cross);
-    if (io == IO::BF16)
-      for (int i = 0; i < 3; ++i) a.role[i].pairs = reinterpret_cast<float*>(p + l.pairs + i * up(sizeof(float) * (size_t)T * Hv));
     if (initial_states) {
       rk.against_last = initial_states;
       rk.cross = reinterpret_cast<float*>(p + l.cross_back);

@@ -43,7 +43,7 @@ struct WalkSmem {
   static constexpr int oX = 0, oY = kX, oW = 2 * kX, oUp = oW + kW, oS = oUp + kUp, oGates = oS + 2 * kSTerm;
   static constexpr bool kRoom = KP == 1 || NP == 1;  // for a second buffer of W
   static constexpr int oW2 = kRoom ? oGates : oW, oTokens = kRoom ? oGates + kW : oGates;
-  static constexpr int oMisc = oTokens + 4 * 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
+  static constexpr int oMisc = oTokens + 5 * 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 constexpr int tA = 0, tD1 = 128, tU = 256, tO = 384;  // columns of tensor memory
@@ -236,6 +236,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
   const float* s_up = reinterpret_cast<const float*>(sm + L::oTokens);  // up, G / ln 2 in two floats, P's columns' factors
   const float *s_hi = s_up + kC, *s_lo = s_up + 2 * kC, *s_col = s_up + 3 * kC;
+  float* s_self = reinterpret_cast<float*>(sm + L::oTokens) + 4 * kC;  // rows with dots: the weight of the token's own pair
   float* s_sums = reinterpret_cast<float*>(sm + L::oMisc);  // 8
   float *s_decay = s_sums + 8, *s_unit = s_sums + 9;
   volatile int *odd = reinterpret_cast<int*>(s_sums + 10), *stop = odd + 1, *s_steep = odd + 2;
@@ -426,7 +427,6 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         // a thread's blocks of 16 columns of P, spread over its columns: P is triangular
         const int j0 = 16 * (kParts * u + (u & 1 ? kParts - 1 - part : part));
         uint32_t words[16];
-        float self = 0.0f, weight = 0.0f;
         if (back ? j0 + 15 < quad * 32 || j0 >= rows : j0 > quad * 32 + 31) {  // no row of the warp sees these columns
 #pragma unroll
           for (int i = 0; i < 16; ++i) words[i] = 0;
@@ -435,9 +435,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           tmem_sum<1>(tm + tA + lane_at + j0, 0, d);
           const bool all = back ? j0 > quad * 32 + 31 && j0 + 15 < rows : j0 + 15 < quad * 32;
           const int at = row - j0;  // the diagonal's column
-          if (back && !has_dot && !all) {
+          if (has_dot && !all) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) self = at == 2 * i ? d[i].x : at == 2 * i + 1 ? d[i].y : self;
+            for (int i = 0; i < 16; ++i)
+              if (at == i) s_self[row] = a.scale * (i % 2 ? d[i / 2].y : d[i / 2].x);
           }
           // exp(G_i - G_j) in two factors, by way of the block's end: neither is above 1 where every row sees every
           // column, and on the diagonal the row's has no more than 32 tokens to grow over
@@ -464,28 +465,21 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
             }
           }
           if (!all) {
-            const int from = back ? at : 0, count = max((back ? rows - j0 : at + 1) - from, 0);
+            constexpr int own = has_dot ? 0 : 1;
+            const int from = back ? at + 1 - own : 0, count = max((back ? rows - j0 : at + own) - from, 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if ((unsigned)(2 * i - from) >= (unsigned)count) d[i].x = 0.0f;
               if ((unsigned)(2 * i + 1 - from) >= (unsigned)count) d[i].y = 0.0f;
             }
           }
-          if (back && !has_dot && !all && role.pairs && (unsigned)at < 16u && row < rows)
-            role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = self;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t term[2];
             split_pair<2>(d[i], term);
             words[i] = term[0];
             words[8 + i] = term[1];
-            if (has_dot && !all) {  // the pair's weight as the product with W has it
-              if (at == 2 * i) weight = bf16_lo(term[0]) + bf16_lo(term[1]);
-              if (at == 2 * i + 1) weight = bf16_hi(term[0]) + bf16_hi(term[1]);
-            }
           }
-          if (has_dot && !all && (unsigned)at < 16u && row < rows)
-            role.pairs[h * a.T + seg.start + (int64_t)c * kC + row] = weight;
         }
         __syncwarp();
         tmem_st16(tm + tA + lane_at + j0, words);
@@ -507,6 +501,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         for (int s = 0; s < kRuns; ++s) r[s].load(from + 16 * s, cols - 16 * s, whole_dot);
       }
       if (warp == kStateWarps) {
+        if (has_dot) wait(bars + kFullW + (two_w ? p : 0), two_w ? (k >> 1) & 1 : p);
         wait(bars + kDoneO, p);  // behind the weighing of this chunk, too
       }
       named_barrier(2, 32 * kOutWarps);
@@ -524,7 +519,17 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           e[0][i] = fma2(splat2(in), e[1][i], e[0][i]);
           if (has_dot) sum = fma2(r[s].get(i), e[0][i], sum);
         }
-        if (has_dot) dot = add(dot, Pair{sum.x + sum.y, 0.0f});
+        if (has_dot) {
+          dot = add(dot, Pair{sum.x + sum.y, 0.0f});
+          const float2 self = splat2(s_self[row]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float2 w[4];
+            unpack(*reinterpret_cast<const uint4*>(w_image(k) + (c0 >> 6) * kPanel + image_chunk<128>(row, (c0 & 63) / 8 + q)), w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[0][4 * q + i] = fma2(self, w[i], e[0][4 * q + i]);
+          }
+        }
         if (role.part) {
           float* to = static_cast<float*>(role.out) + out_row + c0;
 #pragma unroll
@@ -568,6 +573,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           copy_panels(maps.m + role.mw, w_image(k), NP, h / role.rw, seg.start + (int64_t)chunk_of(k) * kC, bars + kFullW + b);
           ++ws[b];
         };
+        constexpr int ahead = two_w ? 1 : 0;
         if (lead && n > 0) load_w(0);
         if (lead && two_w && n > 1) load_w(1);
         for (int k = 0; k < n; ++k) {
@@ -576,7 +582,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           wait(bars + kFullY, p);
           if (k > 0) {
             wait(bars + kDoneO, p ^ 1);  // P's place, and W's
-            if (lead && wait.ok && k + (two_w ? 1 : 0) < n) load_w(k + (two_w ? 1 : 0));
+            if (!has_dot && lead && wait.ok && k + ahead < n) load_w(k + ahead);
           }
           if (__all_sync(0xffffffffu, wait.ok)) {
             tmem_fence_after_sync();
@@ -589,7 +595,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
             if (lead) umma_commit(bars + kDoneA);
           }
           wait(bars + kStateReady, p);
-          if (k > 0) wait(bars + kOutDone, p ^ 1);
+          if (k > 0) {
+            wait(bars + kOutDone, p ^ 1);
+            if (has_dot && lead && wait.ok && k + ahead < n) load_w(k + ahead);  // rows' own pairs are read from W at the end
+          }
           if (__all_sync(0xffffffffu, wait.ok)) {
             tmem_fence_after_sync();
             constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);

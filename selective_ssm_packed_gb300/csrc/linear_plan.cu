@@ -156,7 +156,7 @@ __device__ __forceinline__ Pair sum_behind(Pair v, int lane) {
   return v;
 }
 
-template <IO kIO, int kParts>
+template <int kParts>
 __global__ void __launch_bounds__(kDgThreads, 2) lin_dg_kernel(LinArgs a, int tiles) {
   __shared__ Pair sums[kDgWarps];
   const int seg = blockIdx.x, h = blockIdx.y;
@@ -175,10 +175,6 @@ __global__ void __launch_bounds__(kDgThreads, 2) lin_dg_kernel(LinArgs a, int ti
     for (int p = 0; p < kParts; ++p) d[i] = add(d[i], Pair{a.role[0].dots[p * plane + at], 0.0f});
 #pragma unroll
     for (int p = 0; p < kParts; ++p) d[i] = add(d[i], Pair{-a.role[1].dots[p * plane + at], 0.0f});
-    if (kIO == IO::BF16) {  // without the token's own pair
-      const float w = a.role[1].pairs[at] - a.role[0].pairs[at], qk = a.role[2].pairs[at];
-      d[i] = add(d[i], Pair{w * qk, fmaf(w, qk, -(w * qk))});
-    }
   }
 #pragma unroll
   for (int i = kDgPer - 1; i >= 0; --i) own = add(own, d[i]);
@@ -279,9 +275,9 @@ cudaError_t launch_lin_dg(const LinArgs& a, IO io, cudaStream_t st) {
   const dim3 grid((unsigned)a.max_segs, (unsigned)a.Hv);
   const int tiles = lin_ctas(io, a.K);
   if (a.max_segs > 0) {
-    if (io == IO::BF16) lin_dg_kernel<IO::BF16, 2><<<grid, kDgThreads, 0, st>>>(a, tiles);
-    else if (tiles == 1) lin_dg_kernel<IO::F32, kLinParts><<<grid, kDgThreads, 0, st>>>(a, tiles);
-    else lin_dg_kernel<IO::F32, 2 * kLinParts><<<grid, kDgThreads, 0, st>>>(a, tiles);
+    if (io == IO::BF16) lin_dg_kernel<2><<<grid, kDgThreads, 0, st>>>(a, tiles);
+    else if (tiles == 1) lin_dg_kernel<kLinParts><<<grid, kDgThreads, 0, st>>>(a, tiles);
+    else lin_dg_kernel<2 * kLinParts><<<grid, kDgThreads, 0, st>>>(a, tiles);
   }
   if (!a.g_token) lin_dg_head_kernel<<<(unsigned)((a.Hv + 31) / 32), 256, 0, st>>>(a);
   return cudaGetLastError();

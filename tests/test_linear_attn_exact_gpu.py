@@ -63,3 +63,17 @@ def test_states_carry_24_bits(K, V, decay, dtype):
     got, ref = run(x, states=True), reference(x)
     for n in ("final", "dinit"):
         assert off(host(got[n]), ref[n]) <= 2.0 ** -20, n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_dg_of_decays_that_forget_within_a_token(K, V, dtype):
+    """dg falls as exp(g), and so do all its terms but the token's own pair, which is none of them.  Two walks make each
+    pair's weight, by powers 2^-22 off; what they differ by adds up over a segment as its square root: of 300
+    tokens 17 * 2^-22 = 4e-6, and a weight's own rounding to two terms is 2^-17 at most: 2^-16 in all, of each head's own
+    size."""
+    x = inputs([300, 40], 2, 4, K, V, dtype, 42)
+    x["g"] = torch.tensor([-3.0, -6.0, -9.0, -12.0], device="cuda").expand(340, 4).contiguous()
+    got, ref = host(run(x)["dg"]), reference(x)["dg"]
+    for h in range(4):
+        assert off(got[:, h], ref[:, h]) <= 2.0 ** -16, h

@@ -457,7 +457,8 @@ int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t
  *   decay to zero).  g_per_token != 0: (T, Hv); 0: (Hv), one decay a head for
  *   every token.
  * Precision: FP32 operands of the tensor cores' products are sums of bf16
- *   terms, three for f32 I/O, two for bf16 I/O; accumulation and the state
+ *   terms: three for f32 I/O, and for bf16 I/O two where only bf16 results come
+ *   of them, three otherwise; accumulation and the state
  *   are float32.  bf16 results lose no more than their own rounding;
  *   final_states (and the backward's d_initial_states) keep all 24 bits, in
  *   bf16 calls by a walk of their own.
@@ -486,8 +487,9 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
  * states are made again; nothing of the forward call has to be kept.
  * d_final_states: nullable, the gradient reaching the final states.  dq and dk
  * add the value heads that share a head, in order; no atomics, bitwise
- * repeatable.  With bf16 I/O dg is about 5e-6 of its norm off; data in bf16 whose
- * dg is wanted with all bits are passed as f32.
+ * repeatable.  dg keeps an f32's digits in bf16 calls too (6e-7 to 8e-7 of its
+ * norm off over 32768 and 16384 packed tokens); with dg = NULL the walks of dq and
+ * dk take a third less.
  * A value that is not finite in q, k, v, dout or the states reaches the
  * gradients that the formula carries it to; dg, a sum over a segment, is not
  * finite before it in the sequence's segments and keeps its value, but not its

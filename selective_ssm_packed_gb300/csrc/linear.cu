@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   auto chunk_of = [&](int k) { return back ? n - 1 - k : k; };
 
   if (warp == kLinCtrl) {  // all lanes go through it together, so that addresses are uniform; one issues
-    const bool lead = lane == 0;
+    const bool lead = elect_one();
     Pair total{0.0f, 0.0f};
     if (n > 0) total = make_gates(chunk_of(0), 0);
     if (n > 0) named_barrier(4, kLinThreads);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
           const int first = first_term(i / KP), second = second_term(i / KP), panel = i % KP;
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            umma_if(lead, tm + tA, x + ((first * KP + panel) * L::kPanel + s * 32) / 16,
+            umma_one(tm + tA, x + ((first * KP + panel) * L::kPanel + s * 32) / 16,
                     y + ((second * KP + panel) * L::kPanel + s * 32) / 16, idesc, i + s > 0 ? 1u : 0u);
         }
         if (lead) umma_commit(bar_a);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
             const int first = first_term(i / KP), second = second_term(i / KP), panel = i % KP;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              umma_if(lead, tm + tD1, x + ((first * KP + panel) * L::kPanel + s * 32) / 16,
+              umma_one(tm + tD1, x + ((first * KP + panel) * L::kPanel + s * 32) / 16,
                       st + (second * L::kSTerm + (4 * panel + s) * 2048) / 16, idesc_s, i + s > 0 ? 1u : 0u);
           }
         }
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
         for (int i = 0; i < 6; ++i)
 #pragma unroll
           for (int s = 0; s < kC / 16; ++s)
-            umma_if(lead, tm + tU, yt + (first_term(i) * KP * L::kPanel + s * 2048) / 16, up + (second_term(i) * L::kPanel + s * 2048) / 16,
+            umma_one(tm + tU, yt + (first_term(i) * KP * L::kPanel + s * 2048) / 16, up + (second_term(i) * L::kPanel + s * 2048) / 16,
                     idesc, i + s > 0 ? 1u : 0u);
         if (lead) umma_commit(bar_u);
       }
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
           for (int i = 0; i < 6; ++i)
 #pragma unroll
             for (int s = 0; s < kC / 16; ++s)
-              umma_ta_if(lead, tm + tO, tm + tP + kBlockWords * s + 8 * first_term(i), w + (second_term(i) * L::kPanel + s * 2048) / 16,
+              umma_ta_one(tm + tO, tm + tP + kBlockWords * s + 8 * first_term(i), w + (second_term(i) * L::kPanel + s * 2048) / 16,
                          idesc, i + s > 0 ? 1u : 0u);
           if (lead) umma_commit(bar_o);
         }
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
   tmem_fence_before_sync();
   __syncthreads();
   if (warp == kLinCtrl) {
-    if (lane == 0 && *stop) {  // products that were not waited for
+    if (elect_one() && *stop) {  // products that were not waited for
       umma_commit(drained);
       mbar_wait(drained, 0, kCopyDrainNs);
     }

@@ -8,9 +8,9 @@ namespace {
 // ------------------------------------------------------------------ the walk
 // One CTA per (segment, value head, role).  A chunk of 128 tokens is four
 // products on the matrix unit:
-//   A  = X Y^T             read back, weighted and masked: P, bf16 terms in A's place in tensor memory
+//   A  = X Y^T             read back, weighted and masked: P, bf16 terms in tensor memory
 //   D1 = X S
-//   S  = S + Y^T (up * W)  in tensor memory, decayed by exp(G_end) before; as bf16 terms in shared memory for D1
+//   S  = exp(G_end) S + Y^T (up * W)   as bf16 terms in shared memory for D1
 //   D2 = P W               out = in * D1 + D2
 // with in and up the weights of a row for the state and in it.  The two paths,
 // of the state (up * W, S) and of the results (P, out), need each other only
@@ -19,34 +19,62 @@ namespace {
 // mbarrier, and each phase of one is a chunk.  Chunks of 128 rows fill the
 // lanes of tensor memory and halve the steps of the chain A, P, D2 (and U, S,
 // D1), which is what a CTA alone on its SM waits for; all columns in one CTA
-// spare a second A, P and copy of X and Y.  Each hand-over would fit in less
-// than a chunk's 5 us by itself: tensor memory, shared memory and the products'
-// operands take one data path of the SM, 8000 cycles of it a chunk.
-// 32768 tokens, 32 heads of 128: 250 us forward (807 MB, 3.2 TB/s), the gradients
-// 305 (dq), 345 (dk) and 286 us (dv); a key head shared by 8 value heads writes its
-// dq and dk as f32 parts of each, 512 MB more (16384 tokens, 64 heads of 64: 383
-// and 439 us).
+// spare a second A, P and copy of X and Y.  What bounds it is that chain: a chunk
+// takes 9500 cycles, with dots 16000, of which the matrix unit is busy for a
+// quarter, and each of its 56 (80) products takes 60 to 80 to issue.  32768 tokens,
+// 32 heads of 128: 266 us forward (807 MB, 3.0 TB/s), the gradients 477 (dq), 466
+// (dk) and 276 us (dv); a key head shared by 8 value heads writes its dq and dk as
+// f32 parts of each, 512 MB more (16384 tokens, 64 heads of 64: 524 and 511 us).
 //
-// Terms: inputs are exact in one; up * W, P and S in D1 have two, 16 bits, so
-// that results lose no more than their own rounding to bf16 (with one term of P
-// and S out was 2.3e-3 of its norm off, 1.7e-3 with two).
-constexpr int kC = 128, kStateWarps = 8, kOutWarps = 8, kParts = kOutWarps / 4;
-constexpr int kProducts = kStateWarps + kOutWarps, kCopies = kProducts + 1, kGatesWarp = kProducts + 2, kWarps = kProducts + 4;
+// Terms: inputs are exact in one.  Without dots up * W, P and S have two, 16
+// bits, so that results lose no more than their own rounding to bf16 (with one
+// term of P and S out was 2.3e-3 of its norm off, 1.7e-3 with two), and S is left
+// in tensor memory, where the products add to it.  Rows with dots, whose sums
+// give dg, have three, all 24 bits, and S, whose terms are a float's digits, takes
+// up U = Y^T (up * W) with one rounding a chunk (the matrix unit cuts off what it
+// adds to a running sum).  They have room because up * W comes in stretches of
+// rows, issued by a thread of their own, P reaches over A, and D1 comes after D2,
+// where P was.  dg is 6e-7 to 8e-7 of its norm off, where two terms left 3e-6 to
+// 7e-6, at 470 us a walk instead of 310 to 350 (32768 tokens, 32 heads of 128).  D1
+// before D2, which then adds to it in its place, takes 432 us, but all 24 additions of
+// D2 are cut off at D1's size: 1.1e-6.  Walks of 64 columns, with room for all of
+// that, issue twice the products: 600 us.
+constexpr int kC = 128, kStateWarps = 8;
+template <bool has_dot>
+struct WalkWarps {
+  static constexpr int kParts = 2, kOut = 4 * kParts;  // for the results: threads to a row
+  static constexpr int kProducts = kStateWarps + kOut, kCopies = kProducts + 1, kGates = kProducts + 2, kStateMma = kProducts + 3;
+  static constexpr int kThreads = 32 * (kProducts + 4);
+};
 constexpr int kPanel = kC * 128;  // bytes of 64 columns of a chunk's rows
 constexpr int kStep = 16 * 128;   // bytes of 16 rows, a step of a product over the rows
 
-enum Bar : int { kFullX, kFullY, kFullW, kFullW2, kGatesFull, kGatesFree, kUpReady, kStateReady, kPReady, kOutDone, kDoneA, kDoneX, kDoneU, kDoneO, kDrained, kBars };
+enum Bar : int {
+  kFullX, kFullY, kFullW, kFullW2, kGatesFull, kGatesFree, kStateReady, kPReady, kOutDone, kDoneA, kDoneX, kDoneU, kDoneO, kDrained,
+  kUpReady, kUpReadyLast = kUpReady + 3, kUpFree, kUpFreeLast = kUpFree + 3,  // rows with dots: of each stretch; otherwise the first
+  kWClean, kWClean2, kDrained2, kBars
+};
 
-template <int KP, int NP>  // panels of 64 columns of X and Y, and of W
+template <int KP, int NP, bool has_dot>  // panels of 64 columns of X and Y, and of W
 struct WalkSmem {
-  static constexpr int kX = KP * kPanel, kW = NP * kPanel, kUp = 2 * kW, kSBlock = KP * 8192, kSTerm = NP * kSBlock;
-  static constexpr int oX = 0, oY = kX, oW = 2 * kX, oUp = oW + kW, oS = oUp + kUp, oGates = oS + 2 * kSTerm;
-  static constexpr bool kRoom = KP == 1 || NP == 1;  // for a second buffer of W
+  static constexpr int kTerms = has_dot ? 3 : 2;  // of up * W and S
+  static constexpr bool kRoom = KP == 1 || NP == 1;  // for a second buffer of W, and for four stretches of up * W
+  static constexpr int kX = KP * kPanel, kW = NP * kPanel, kSBlock = KP * 8192, kSTerm = NP * kSBlock;
+  // up * W: all rows, or with dots stretches of them in two places or four
+  static constexpr int kUpRows = has_dot ? 32 / NP : kC, kUpPanel = kUpRows * 128, kUpTerm = NP * kUpPanel, kUp = kTerms * kUpTerm;
+  static constexpr int kUps = !has_dot ? 1 : kRoom ? 4 : 2;
+  static constexpr int oX = 0, oY = kX, oW = 2 * kX, oUp = oW + kW, oS = oUp + kUps * kUp, oGates = oS + kTerms * kSTerm;
   static constexpr int oW2 = kRoom ? oGates : oW, oTokens = kRoom ? oGates + kW : oGates;
   static constexpr int oMisc = oTokens + 5 * 4 * kC, oBar = oMisc + 64, kBytes = oBar + kBars * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
-constexpr int tA = 0, tD1 = 128, tU = 256, tO = 384;  // columns of tensor memory
+// Columns of tensor memory.  P of two terms takes A's place.  P of three reaches from before A into it, and D1 comes
+// after D2, where P was.
+template <bool has_dot>
+struct WalkTmem {
+  static constexpr int kStep = has_dot ? 24 : 16;  // of 16 columns of P
+  static constexpr int tP = 0, tA = has_dot ? 128 : 0, tD1 = has_dot ? 0 : 128, tU = 256, tO = 384;
+};
 
 // S in tensor memory is left undecayed, in a unit that shrinks with the sum of
 // g, until that is down to 2^-kFar, which leaves the rest of a float's range to
@@ -79,6 +107,12 @@ __device__ __forceinline__ void copy_panels(const CUtensorMap* map, uint8_t* to,
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // 16 columns each from two places of this thread's lane, on their way together.
@@ -163,6 +197,25 @@ __device__ __noinline__ void clear_odd(uint8_t* at, int step, int count) {
     }
 }
 
+// A 16-byte chunk of W times its row's weight as bf16 terms.
+template <int kTerms>
+__device__ __forceinline__ void weigh(uint4 q, float up, uint4 (&terms)[kTerms]) {
+  const uint32_t p[4] = {q.x, q.y, q.z, q.w};
+  uint32_t t[4][kTerms];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split_pair<kTerms>(mul2(make_float2(bf16_lo(p[k]), bf16_hi(p[k])), splat2(up)), t[k]);
+#pragma unroll
+  for (int i = 0; i < kTerms; ++i) terms[i] = make_uint4(t[0][i], t[1][i], t[2][i], t[3][i]);
+}
+// x * 0 added up: not 0 once a value is not finite.
+__device__ __forceinline__ void look_over(uint4 q, __nv_bfloat162& trace) {
+  const uint32_t p[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    trace = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&p[k]), __floats2bfloat162_rn(0.0f, 0.0f), trace);
+}
+__device__ __forceinline__ bool is_odd(__nv_bfloat162 trace) { return *reinterpret_cast<const uint32_t*>(&trace) & 0x7fff7fffu; }
+
 // Up * W as images of kTerms terms from W's image, by kThreads threads, each along
 // a column of 16-byte chunks whose place in the swizzle is the same in all its
 // rows.  A value of W that is not finite reaches the state, and so every later
@@ -170,33 +223,23 @@ __device__ __noinline__ void clear_odd(uint8_t* at, int step, int count) {
 // its place in W, and *odd has the rows it should reach made NaN when they are
 // written.
 template <int NP, int kTerms, int kThreads>
-__device__ __forceinline__ void weigh(uint8_t* w_image, uint8_t* up_image, const float* up, int t, volatile int* odd) {
+__device__ __forceinline__ void weigh_all(uint8_t* w_image, uint8_t* up_image, const float* up, int t, volatile int* odd) {
   constexpr int kRowChunks = NP * 8, kRows = kThreads / kRowChunks;
   static_assert(kRows % 8 == 0, "the swizzle repeats every 8 rows");
   const int r0 = t / kRowChunks, ch = t % kRowChunks;
   const uint32_t at = (ch >> 3) * kPanel + image_chunk<128>(r0, ch & 7);
-  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
-  __nv_bfloat162 trace = zero;  // not 0 once a value is not finite
+  __nv_bfloat162 trace = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll 2
   for (int u = 0; u < kC / kRows; ++u) {
     const uint4 q = *reinterpret_cast<const uint4*>(w_image + at + u * kRows * 128);
-    const float2 f = splat2(up[r0 + u * kRows]);
-    const uint32_t p[4] = {q.x, q.y, q.z, q.w};
-    uint32_t terms[kTerms][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (odd) trace = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&p[k]), zero, trace);
-      uint32_t term[kTerms];
-      split_pair<kTerms>(mul2(make_float2(bf16_lo(p[k]), bf16_hi(p[k])), f), term);
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) terms[i][k] = term[i];
-    }
+    uint4 terms[kTerms];
+    if (odd) look_over(q, trace);
+    weigh<kTerms>(q, up[r0 + u * kRows], terms);
     uint8_t* to = up_image + at + u * kRows * 128;
 #pragma unroll
-    for (int i = 0; i < kTerms; ++i)
-      *reinterpret_cast<uint4*>(to + i * NP * kPanel) = make_uint4(terms[i][0], terms[i][1], terms[i][2], terms[i][3]);
+    for (int i = 0; i < kTerms; ++i) *reinterpret_cast<uint4*>(to + i * NP * kPanel) = terms[i];
   }
-  if (odd && (*reinterpret_cast<const uint32_t*>(&trace) & 0x7fff7fffu)) {
+  if (odd && is_odd(trace)) {
     clear_odd(w_image + at, kRows * 128, kC / kRows);
     *odd = 1;
   }
@@ -230,7 +273,12 @@ __device__ __noinline__ void spoil_row(const LinRole& role, const __nv_bfloat16*
 template <int KP, int NP, bool back, bool has_dot>
 __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, const LinRole& role, int h, int64_t item) {
   using T = __nv_bfloat16;
-  using L = WalkSmem<KP, NP>;
+  using L = WalkSmem<KP, NP, has_dot>;
+  using M = WalkTmem<has_dot>;
+  using Warps = WalkWarps<has_dot>;
+  constexpr int kParts = Warps::kParts, kOutWarps = Warps::kOut, kProducts = Warps::kProducts, kCopies = Warps::kCopies;
+  constexpr int kTerms = L::kTerms;  // of P, of up * W and of S
+  constexpr int tP = M::tP, tA = M::tA, tD1 = M::tD1, tU = M::tU, tO = M::tO;
   constexpr int kN = NP * 64, kCols = NP * 32;  // columns of W, and to a thread of the state's path
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
@@ -251,10 +299,11 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quad = warp & 3, row = quad * 32 + lane;
   if (t == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bars + i, i == kUpReady || i == kStateReady ? kStateWarps
-                          : i == kPReady || i == kOutDone   ? kOutWarps
-                          : i == kGatesFree                 ? kStateWarps + kOutWarps
-                                                            : 1);
+      mbar_init(bars + i, i == kStateReady || i == kWClean || i == kWClean2 ? kStateWarps
+                          : i >= kUpReady && i <= kUpReadyLast              ? (has_dot ? kStateWarps / 2 : kStateWarps)
+                          : i == kPReady || i == kOutDone                   ? kOutWarps
+                          : i == kGatesFree                                 ? kStateWarps + kOutWarps
+                                                                            : 1);
     *stop = *odd = 0;
     fence_mbar_init();
   }
@@ -277,12 +326,30 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
 
   if (warp < kStateWarps) {  // the state's path
     const int c0 = (warp >> 2) * kCols;
-    float unit = 1.0f;  // S is this many times what tensor memory has
+    float unit = 1.0f, decay = 1.0f;  // without dots S is `unit` times what tensor memory has
     const bool has_row = row < KP * 64;
     auto state_at = [&](int col) { return (int64_t)row * role.srow + (int64_t)col * role.scol; };
     auto put_state = [&](int col, const float2 (&d)[8]) {
       uint8_t* image = sm + L::oS + col / 64 * L::kSBlock;
-      put_row<2, 128>(image, L::kSTerm, row, col % 64 / 8, d);
+      put_row<kTerms, 128>(image, L::kSTerm, row, col % 64 / 8, d);
+    };
+    auto next_state = [&](int col, float2 (&d)[8]) {  // with dots: of S, whose three terms are its digits, and U
+      tmem_sum<1>(tm + tU + lane_at + col, 0, d);
+      const uint8_t* image = sm + L::oS + col / 64 * L::kSBlock;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t place = image_chunk<128>(row, col % 64 / 8 + q);
+        float2 sum[4];
+#pragma unroll
+        for (int term = kTerms - 1; term >= 0; --term) {
+          float2 v[4];
+          unpack(*reinterpret_cast<const uint4*>(image + term * L::kSTerm + place), v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] = term == kTerms - 1 ? v[i] : add2(sum[i], v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[4 * q + i] = fma2(splat2(decay), sum[i], d[4 * q + i]);
+      }
     };
     auto load_state = [&](const float* from, int col, float2 (&d)[8]) {  // 16 columns of this thread's row
 #pragma unroll
@@ -301,28 +368,35 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
 #pragma unroll 1
       for (int u = 0; u < kCols / 16; ++u) {
         float2 d[8];
-        uint32_t words[16];
         if (has_carry) {
           load_state(carry, c0 + 16 * u, d);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] = splat2(0.0f);
         }
+        if constexpr (!has_dot) {
+          uint32_t words[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          words[2 * i] = __float_as_uint(d[i].x);
-          words[2 * i + 1] = __float_as_uint(d[i].y);
+          for (int i = 0; i < 8; ++i) {
+            words[2 * i] = __float_as_uint(d[i].x);
+            words[2 * i + 1] = __float_as_uint(d[i].y);
+          }
+          __syncwarp();
+          tmem_st16(tm + tU + lane_at + c0 + 16 * u, words);
         }
-        __syncwarp();
-        tmem_st16(tm + tU + lane_at + c0 + 16 * u, words);
         put_state(c0 + 16 * u, d);
       }
-      tmem_wait_st();
+      if constexpr (!has_dot) tmem_wait_st();
       tmem_fence_before_sync();
     }
     fence_async_smem();
     warp_arrive(bars + kStateReady, lane);
-    const bool wanted = role.cross && (!back || seg.is_first);
+    const bool wanted = has_dot && role.cross && (!back || seg.is_first);
+    // with dots: the first four warps weigh every other stretch of rows, the others those between.  A thread's chunks of W
+    // have the same place in the swizzle.
+    constexpr int kHalf = L::kUpRows / 2;
+    const int half = warp >> 2, r = (t & 127) / (NP * 8), ch = (t & 127) % (NP * 8);
+    int put = ~0;  // the phases of the places
     for (int k = 0; k < n; ++k) {
       const uint32_t p = k & 1;
       const bool more = k + 1 < n;
@@ -334,34 +408,77 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         if (rows < kC) wait(bars + kFullY, p);
       }
       named_barrier(1, 32 * kStateWarps);
-      const float decay = *s_decay;
+      decay = *s_decay;
       unit = *s_unit;
       if (rows < kC) {
         clear_rows<KP>(sm + L::oY, rows, t, 32 * kStateWarps);
         clear_rows<NP>(w_image(k), rows, t, 32 * kStateWarps);
         named_barrier(1, 32 * kStateWarps);
       }
-      weigh<NP, 2, 32 * kStateWarps>(w_image(k), sm + L::oUp, s_up, t, odd);
-      warp_arrive(bars + kGatesFree, lane);
-      if (decay != 1.0f && has_row) decay_state<kCols>(tm + tU + lane_at + c0, decay);
-      tmem_fence_before_sync();
-      fence_async_smem();
-      warp_arrive(bars + kUpReady, lane);
+      if constexpr (has_dot) {
+        uint8_t* w = w_image(k) + (ch >> 3) * kPanel + half * L::kUpPanel + image_chunk<128>(r, ch & 7);
+        __nv_bfloat162 trace = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kC / L::kUpRows; ++i)
+          look_over(*reinterpret_cast<const uint4*>(w + (i / 2 * 2 * L::kUpRows + i % 2 * kHalf) * 128), trace);
+        const bool any_odd = __any_sync(0xffffffffu, is_odd(trace));
+        tmem_fence_before_sync();  // what was read of U
+        fence_async_smem();        // rows cleared
+        if (!any_odd) warp_arrive(bars + kWClean + p, lane);
+#pragma unroll 1
+        for (int row0 = 0; row0 + half * L::kUpRows < rows; row0 += 2 * L::kUpRows) {
+          uint4 terms[2][kTerms];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            weigh<kTerms>(*reinterpret_cast<const uint4*>(w + (row0 + j * kHalf) * 128), s_up[row0 + half * L::kUpRows + j * kHalf + r], terms[j]);
+          const int place = half + (L::kUps > 2 ? row0 / L::kUpRows & 2 : 0);
+          if (lane == 0) wait(bars + kUpFree + place, put >> place & 1);
+          __syncwarp();
+          put ^= 1 << place;
+          uint8_t* to = sm + L::oUp + place * L::kUp + (ch >> 3) * L::kUpPanel + image_chunk<128>(r, ch & 7);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < kTerms; ++i) *reinterpret_cast<uint4*>(to + i * L::kUpTerm + j * kHalf * 128) = terms[j][i];
+          fence_async_smem();
+          warp_arrive(bars + kUpReady + place, lane);
+        }
+        if (any_odd) {
+          if (is_odd(trace)) {
+            for (int i = 0; i < 2; ++i) clear_odd(w + i * kHalf * 128, 2 * L::kUpRows * 128, kC / (2 * L::kUpRows));
+            *odd = 1;
+          }
+          fence_async_smem();
+          warp_arrive(bars + kWClean + p, lane);
+        }
+        warp_arrive(bars + kGatesFree, lane);
+      } else {
+        weigh_all<NP, kTerms, 32 * kStateWarps>(w_image(k), sm + L::oUp, s_up, t, odd);
+        warp_arrive(bars + kGatesFree, lane);
+        if (decay != 1.0f && has_row) decay_state<kCols>(tm + tU + lane_at + c0, decay);
+        tmem_fence_before_sync();
+        fence_async_smem();
+        warp_arrive(bars + kUpReady, lane);
+      }
       if (more || wanted) {
         if (warp == 0) {
           wait(bars + kDoneX, p);
           wait(bars + kDoneU, p);
         }
         named_barrier(1, 32 * kStateWarps);
+        tmem_fence_after_sync();
       }
       if (more) {
-        tmem_fence_after_sync();
         if (has_row) {
 #pragma unroll 1
           for (int u = 0; u < kCols / 16; ++u) {
             float2 d[8];
-            tmem_sum<1>(tm + tU + lane_at + c0 + 16 * u, 0, d);
-            scale_row(d, unit);
+            if constexpr (has_dot) {
+              next_state(c0 + 16 * u, d);
+            } else {
+              tmem_sum<1>(tm + tU + lane_at + c0 + 16 * u, 0, d);
+              scale_row(d, unit);
+            }
             put_state(c0 + 16 * u, d);
           }
         }
@@ -370,8 +487,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         warp_arrive(bars + kStateReady, lane);
       }
     }
-    if (wanted) {
-      tmem_fence_after_sync();
+    if (has_dot && wanted) {
       const float *e = nullptr, *at_end = nullptr;  // between segments: the state as it was made for the next one
       if (!back && !seg.is_last) {
         at_end = role.slots + (seg.inner_before * a.Hv + h) * state_size;
@@ -386,9 +502,9 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           float2 d[8], x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] = splat2(0.0f);
-          if (n > 0 || has_carry) tmem_sum<1>(tm + tU + lane_at + c0 + 16 * u, 0, d);
-          scale_row(d, unit);
           if (at_end) load_state(at_end, c0 + 16 * u, d);
+          else if (n > 0) next_state(c0 + 16 * u, d);
+          else if (has_carry) load_state(carry, c0 + 16 * u, d);
           load_state(e, c0 + 16 * u, x);
 #pragma unroll
           for (int i = 0; i < 8; ++i)  // past the state d may be what the matrix unit made of other rows
@@ -426,10 +542,12 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       for (int u = 0; u < 8 / kParts; ++u) {
         // a thread's blocks of 16 columns of P, spread over its columns: P is triangular
         const int j0 = 16 * (kParts * u + (u & 1 ? kParts - 1 - part : part));
-        uint32_t words[16];
+        uint32_t words[kTerms][8];
         if (back ? j0 + 15 < quad * 32 || j0 >= rows : j0 > quad * 32 + 31) {  // no row of the warp sees these columns
 #pragma unroll
-          for (int i = 0; i < 16; ++i) words[i] = 0;
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int q = 0; q < kTerms; ++q) words[q][i] = 0;
         } else {
           float2 d[8];
           tmem_sum<1>(tm + tA + lane_at + j0, 0, d);
@@ -475,14 +593,16 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            uint32_t term[2];
-            split_pair<2>(d[i], term);
-            words[i] = term[0];
-            words[8 + i] = term[1];
+            uint32_t term[kTerms];
+            split_pair<kTerms>(d[i], term);
+#pragma unroll
+            for (int q = 0; q < kTerms; ++q) words[q][i] = term[q];
           }
         }
         __syncwarp();
-        tmem_st16(tm + tA + lane_at + j0, words);
+        if (has_dot && u == 2) named_barrier(3 + quad, 32 * kParts);  // the last blocks of P lie on the first ones of A
+#pragma unroll
+        for (int q = 0; q < kTerms; ++q) tmem_st8(tm + tP + lane_at + j0 / 16 * M::kStep + 8 * q, words[q]);
       }
       tmem_wait_st();
       warp_arrive(bars + kGatesFree, lane);
@@ -502,7 +622,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       }
       if (warp == kStateWarps) {
         if (has_dot) wait(bars + kFullW + (two_w ? p : 0), two_w ? (k >> 1) & 1 : p);
-        wait(bars + kDoneO, p);  // behind the weighing of this chunk, too
+        wait(bars + (has_dot ? kDoneX : kDoneO), p);  // the later of D1 and D2; behind the weighing of this chunk, too
       }
       named_barrier(2, 32 * kOutWarps);
       tmem_fence_after_sync();
@@ -512,8 +632,8 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       for (int s = 0; s < kRuns; ++s) {
         const int c0 = first + 16 * s;
         float2 e[2][8];
-        load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
         float2 sum = splat2(0.0f);
+        load_two(tm + tO + lane_at + c0, tm + tD1 + lane_at + c0, e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           e[0][i] = fma2(splat2(in), e[1][i], e[0][i]);
@@ -558,31 +678,51 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       if (has_dot && mine) role.dots[((int64_t)part * a.Hv + h) * a.T + token] = dot.hi + dot.lo;
     }
   } else {
+    // W's copies are asked for by whoever knows that its place is free: whoever waits for a phase has to have done so
+    // before it can come around again
+    int ws[2] = {0, 0};
+    constexpr int ahead = two_w ? 1 : 0;
+    auto load_w = [&](int k) {
+      const int b = two_w ? k & 1 : 0;
+      mbar_arrive_expect_tx(bars + kFullW + b, (uint32_t)L::kW);
+      copy_panels(maps.m + role.mw, w_image(k), NP, h / role.rw, seg.start + (int64_t)chunk_of(k) * kC, bars + kFullW + b);
+      ++ws[b];
+    };
+    auto drain_w = [&]() {  // what is on its way comes in before the memory is given back
+      drain_copies(bars + kFullW, ws[0]);
+      drain_copies(bars + kFullW2, ws[1]);
+    };
     if (warp == kProducts) {  // all lanes go through it together, so that addresses are uniform; one issues
       {
-        const bool lead = lane == 0;
+        const bool lead = elect_one();
         const uint64_t x = smem_desc<128>(smem_u32(sm + L::oX)), y = smem_desc<128>(smem_u32(sm + L::oY));
         const uint64_t yt = smem_desc<128>(smem_u32(sm + L::oY), kPanel);
         const uint64_t up = smem_desc<128>(smem_u32(sm + L::oUp), kPanel), st = smem_desc<128>(smem_u32(sm + L::oS), L::kSBlock);
-        // W's copies are asked for here, in the order of the products that use it: whoever waits for a phase has to
-        // have done so before it can come around again
-        int ws[2] = {0, 0};
-        auto load_w = [&](int k) {
-          const int b = two_w ? k & 1 : 0;
-          mbar_arrive_expect_tx(bars + kFullW + b, (uint32_t)L::kW);
-          copy_panels(maps.m + role.mw, w_image(k), NP, h / role.rw, seg.start + (int64_t)chunk_of(k) * kC, bars + kFullW + b);
-          ++ws[b];
+        if (!has_dot && lead && n > 0) load_w(0);
+        if (!has_dot && lead && two_w && n > 1) load_w(1);
+        auto add_state = [&](uint32_t p) {  // D1
+          wait(bars + kStateReady, p);
+          if (__all_sync(0xffffffffu, wait.ok)) {
+            tmem_fence_after_sync();
+            constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
+#pragma unroll 1
+            for (int i = 0; i < kTerms * KP; ++i) {  // the smallest term first
+              const int term = kTerms - 1 - i / KP, panel = i % KP;
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                umma_one(tm + tD1, x + (panel * kPanel + s * 32) / 16, st + (term * L::kSTerm + (4 * panel + s) * kStep) / 16, idesc,
+                        i + s > 0 ? 1u : 0u);
+            }
+            if (lead) umma_commit(bars + kDoneX);
+          }
         };
-        constexpr int ahead = two_w ? 1 : 0;
-        if (lead && n > 0) load_w(0);
-        if (lead && two_w && n > 1) load_w(1);
         for (int k = 0; k < n; ++k) {
           const uint32_t p = k & 1;
           wait(bars + kFullX, p, k == 0 && forced_here(a));
           wait(bars + kFullY, p);
-          if (k > 0) {
+          if (!has_dot && k > 0) {
             wait(bars + kDoneO, p ^ 1);  // P's place, and W's
-            if (!has_dot && lead && wait.ok && k + ahead < n) load_w(k + ahead);
+            if (lead && wait.ok && k + ahead < n) load_w(k + ahead);
           }
           if (__all_sync(0xffffffffu, wait.ok)) {
             tmem_fence_after_sync();
@@ -591,29 +731,14 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
             for (int i = 0; i < KP; ++i)
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                umma_if(lead, tm + tA, x + (i * kPanel + s * 32) / 16, y + (i * kPanel + s * 32) / 16, idesc, i + s > 0 ? 1u : 0u);
+                umma_one(tm + tA, x + (i * kPanel + s * 32) / 16, y + (i * kPanel + s * 32) / 16, idesc, i + s > 0 ? 1u : 0u);
             if (lead) umma_commit(bars + kDoneA);
           }
-          wait(bars + kStateReady, p);
-          if (k > 0) {
-            wait(bars + kOutDone, p ^ 1);
-            if (has_dot && lead && wait.ok && k + ahead < n) load_w(k + ahead);  // rows' own pairs are read from W at the end
-          }
-          if (__all_sync(0xffffffffu, wait.ok)) {
-            tmem_fence_after_sync();
-            constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
-#pragma unroll 1
-            for (int i = 0; i < 2 * KP; ++i) {  // the smaller term first
-              const int term = 1 - i / KP, panel = i % KP;
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                umma_if(lead, tm + tD1, x + (panel * kPanel + s * 32) / 16, st + (term * L::kSTerm + (4 * panel + s) * kStep) / 16, idesc,
-                        i + s > 0 ? 1u : 0u);
-            }
-            if (lead) umma_commit(bars + kDoneX);
-          }
-          wait(bars + kUpReady, p);
-          if (__all_sync(0xffffffffu, wait.ok)) {
+          if (k > 0) wait(bars + kOutDone, p ^ 1);
+          if constexpr (!has_dot) add_state(p);
+          if (has_dot) wait(bars + kWClean + p, (k >> 1) & 1);
+          else wait(bars + kUpReady, p);
+          if (!has_dot && __all_sync(0xffffffffu, wait.ok)) {
             tmem_fence_after_sync();
             constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, kN);
 #pragma unroll 1
@@ -621,7 +746,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
               const int term = 1 - i / 2;
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                umma_if(lead, tm + tU, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc, 1u);
+                umma_one(tm + tU, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16, idesc, 1u);
             }
             if (lead) umma_commit(bars + kDoneU);
           }
@@ -631,20 +756,21 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
             const uint64_t w = smem_desc<128>(smem_u32(w_image(k)), kPanel);
             constexpr uint32_t idesc = umma_idesc(kKMajor, kMnMajor, kN);
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              const int term = 1 - i / 2;
+            for (int i = 0; i < 2 * kTerms; ++i) {
+              const int term = kTerms - 1 - i / 2;
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                umma_ta_if(lead, tm + tO, tm + tA + 16 * ((i & 1) * 4 + s) + 8 * term, w + ((i & 1) * 4 + s) * (kStep / 16), idesc,
-                           i + s > 0 ? 1u : 0u);
+                umma_ta_one(tm + tO, tm + tP + M::kStep * ((i & 1) * 4 + s) + 8 * term, w + ((i & 1) * 4 + s) * (kStep / 16), idesc,
+                            i + s > 0 ? 1u : 0u);
             }
             if (lead) umma_commit(bars + kDoneO);
           }
+          if constexpr (has_dot) {
+            wait(bars + kDoneO, p);  // D1 takes P's place
+            add_state(p);
+          }
         }
-        if (lead) {  // what is on its way comes in before the memory is given back
-          drain_copies(bars + kFullW, ws[0]);
-          drain_copies(bars + kFullW2, ws[1]);
-        }
+        if (lead) drain_w();
         if (lead && *stop) {  // products that were not waited for
           umma_commit(bars + kDrained);
           mbar_wait(bars + kDrained, 0, kCopyDrainNs);
@@ -654,24 +780,34 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
     } else if (warp == kCopies) {
       if (lane == 0 && n > 0) {
         int asked = 0;
-        // X and Y in turn, each once the products are through with what is in its place
+        if (has_dot) load_w(0);
+        if (has_dot && two_w && n > 1) load_w(1);
+        // X and Y in turn, each once the products are through with what is in its place; then, with dots, W
 #pragma unroll 1
         for (int i = 0; i < 2 * n; ++i) {
           const int k = i / 2;
           const bool is_x = i % 2 == 0;
-          if (k > 0) wait(bars + (is_x ? kDoneX : kDoneU), (k - 1) & 1);
+          if (k > 0) {
+            wait(bars + (is_x ? kDoneX : kDoneU), (k - 1) & 1);
+            if (!is_x && has_dot) wait(bars + kDoneA, (k - 1) & 1);  // otherwise issued before U
+          }
           if (!wait.ok) break;
           uint64_t* bar = bars + (is_x ? kFullX : kFullY);
           mbar_arrive_expect_tx(bar, (uint32_t)L::kX);
           copy_panels(maps.m + (is_x ? role.mx : role.my), sm + (is_x ? L::oX : L::oY), KP, is_x ? h / role.rx : h / role.ry,
                       seg.start + (int64_t)chunk_of(k) * kC, bar);
           ++asked;
+          if (has_dot && !is_x && k > 0 && k + ahead < n) {
+            wait(bars + kOutDone, (k - 1) & 1);  // rows' own pairs are read from W
+            if (wait.ok) load_w(k + ahead);
+          }
         }
         drain_copies(bars + kFullX, (asked + 1) / 2);
         drain_copies(bars + kFullY, asked / 2);
+        if (has_dot) drain_w();
       }
       __syncwarp();
-    } else if (warp == kGatesWarp) {
+    } else if (warp == Warps::kGates) {
       const float* g_base = a.g + seg.start * a.g_token + h;
       auto load_g = [&](int c, float (&g)[4]) {
 #pragma unroll
@@ -685,8 +821,8 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
       if (n > 0) load_g(chunk_of(0), g);
       for (int k = 0; k < n; ++k) {
         Pair last, run = running_sums(g, lane, last);
-        const Pair next = add(unit, last);
-        const bool keep = fabsf(next.hi) < kFar;
+        const Pair next = has_dot ? last : add(unit, last);  // with dots S is decayed in every chunk
+        const bool keep = !has_dot && fabsf(next.hi) < kFar;
         float up[4] = {}, hi[4] = {}, lo[4] = {}, col[4];
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
@@ -731,6 +867,39 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
         }
         warp_arrive(bars + kGatesFull, lane);
       }
+    } else if (has_dot && warp == Warps::kStateMma) {  // U, stretch by stretch; all lanes together, as for the other products
+      const bool lead = elect_one();
+      const uint64_t yt = smem_desc<128>(smem_u32(sm + L::oY), kPanel);
+      const uint64_t up = smem_desc<128>(smem_u32(sm + L::oUp), L::kUpPanel);
+      constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, kN);
+      int got = 0;  // the phases of the places
+      for (int k = 0; k < n; ++k) {
+        const int rows = min(kC, seg.len - chunk_of(k) * kC);
+        wait(bars + kFullY, k & 1);
+#pragma unroll 1
+        for (int row0 = 0; row0 < rows; row0 += L::kUpRows) {
+          const int j = row0 / L::kUpRows & (L::kUps - 1);
+          wait(bars + kUpReady + j, got >> j & 1);
+          got ^= 1 << j;
+          if (!__all_sync(0xffffffffu, wait.ok)) continue;
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int q = 0; q < L::kUpRows / 16; ++q)
+#pragma unroll
+            for (int term = kTerms - 1; term >= 0; --term)  // the smallest first
+              umma_one(tm + tU, yt + (row0 * 128 + q * kStep) / 16, up + (j * L::kUp + term * L::kUpTerm + q * kStep) / 16,
+                       idesc, row0 + q > 0 || term < kTerms - 1 ? 1u : 0u);
+          if (lead) umma_commit(bars + kUpFree + j);
+        }
+        if (lead && wait.ok) umma_commit(bars + kDoneU);
+        __syncwarp();
+      }
+      if (lead && n > 0) wait(bars + kDoneU, (n - 1) & 1);  // nobody else may
+      if (lead && *stop) {
+        umma_commit(bars + kDrained2);
+        mbar_wait(bars + kDrained2, 0, kCopyDrainNs);
+      }
+      __syncwarp();
     }
   }
   tmem_fence_before_sync();
@@ -739,7 +908,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
 }
 
 template <int KP, int NP, bool back, bool has_dot>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(WalkWarps<has_dot>::kThreads, 1)
     lin_walk_bf16_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps, int which) {
   const int64_t item = blockIdx.x / a.Hv;
   if (item < a.info[0]) walk<KP, NP, back, has_dot>(a, maps, a.role[which], blockIdx.x % a.Hv, item);
@@ -764,7 +933,7 @@ struct StateSmem {
   static constexpr int oBar = oMisc + 64, kBytes = oBar + 16 * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
-constexpr int kWeighWarps = 16;
+constexpr int kWeighWarps = 16, kProducts = kWeighWarps, kCopies = kProducts + 1, kGatesWarp = kProducts + 2, kWarps = kProducts + 3;
 
 template <int KP, int NP>
 __global__ void __launch_bounds__(kWarps * 32, 1)
@@ -800,7 +969,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   auto chunk_of = [&](int k) { return back ? k : n - 1 - k; };
 
   if (warp == kProducts) {
-    const bool lead = lane == 0;
+    const bool lead = elect_one();
     const uint64_t up = smem_desc<128>(smem_u32(sm + L::oUp), kPanel);
     constexpr uint32_t idesc = umma_idesc(kMnMajor, kMnMajor, kN);
     for (int k = 0; k < n; ++k) {
@@ -813,7 +982,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const int term = kStateTerms - 1 - i / 2;
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            umma_if(lead, tm + (k & 1) * 128, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16,
+            umma_one(tm + (k & 1) * 128, yt + ((i & 1) * 4 + s) * (kStep / 16), up + (term * L::kW + ((i & 1) * 4 + s) * kStep) / 16,
                     idesc, i + s > 0 ? 1u : 0u);
         }
         if (lead) umma_commit(done + (k & 1));
@@ -907,7 +1076,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         clear_rows<NP>(sm + L::oW + b * L::kW, rows, t, kThreads);
         named_barrier(1, kThreads);
       }
-      weigh<NP, kStateTerms, kThreads>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), t,
+      weigh_all<NP, kStateTerms, kThreads>(sm + L::oW + b * L::kW, sm + L::oUp, reinterpret_cast<const float*>(sm + L::oGates + b * 4 * kC), t,
                                        nullptr);
       tmem_fence_before_sync();
       fence_async_smem();
@@ -958,10 +1127,10 @@ template <int KP, int NP, bool back, bool has_dot>
 cudaError_t run_walk(const LinArgs& a, const LinMaps& maps, int which, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const auto kernel = lin_walk_bf16_kernel<KP, NP, back, has_dot>;
-  constexpr size_t bytes = WalkSmem<KP, NP>::kBytes;
+  constexpr size_t bytes = WalkSmem<KP, NP, has_dot>::kBytes;
   const cudaError_t e = set_smem(reinterpret_cast<const void*>(kernel), bytes, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(a.max_segs * a.Hv), kWarps * 32, bytes, st>>>(a, maps, which);
+  kernel<<<(unsigned)(a.max_segs * a.Hv), WalkWarps<has_dot>::kThreads, bytes, st>>>(a, maps, which);
   return cudaGetLastError();
 }
 

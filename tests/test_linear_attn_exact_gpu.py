@@ -11,7 +11,7 @@ import torch
 
 import selective_ssm_packed_gb300 as vs
 from selective_ssm_packed_gb300 import binding
-from test_linear_attn_gpu import host, inputs, reference, run
+from test_linear_attn_gpu import bits, host, inputs, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,40 @@ def test_dg_of_decays_that_forget_within_a_token(K, V, dtype):
     got, ref = host(run(x)["dg"]), reference(x)["dg"]
     for h in range(4):
         assert off(got[:, h], ref[:, h]) <= 2.0 ** -16, h
+
+
+@pytest.mark.parametrize("decay", [2e-3, 2e-2, 0.3, 4.0])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_dg_of_bf16_calls_keeps_an_f32_s_digits(K, V, decay):
+    """With all operands of three terms what is left is the powers' 2^-22 and the sums' rounding, as in f32 calls: a
+    token's rho and sigma are a few 2^-22 off, which over the 600 tokens of a segment add up as their square root, 25 * 2^-22,
+    of a rho, and dg of slow decays is a sum of as many of them: 2^-19 of dg at all decays."""
+    x = inputs([600, 100], 1, 2, K, V, "bf16", 43)
+    x["g"] = (-decay * torch.exp(0.5 * torch.randn(x["g"].shape, generator=torch.Generator().manual_seed(2)))).cuda()
+    assert off(host(run(x)["dg"]), reference(x)["dg"]) <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dg", [True, False])
+@pytest.mark.parametrize("T", [300, 900])  # one segment, several; three chunks and more
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_a_wait_that_runs_out_is_reported(K, V, T, dg, dtype):
+    x = inputs([T], 1, 2, K, V, dtype, 49)
+    a = (x["q"], x["k"], x["v"], x["g"])
+    code = binding.VSSM_F32 if dtype == "f32" else binding.VSSM_BF16
+    ws = torch.zeros(binding.linear_attn_bwd_workspace_size(T, 1, 1, 2, K, V, code), dtype=torch.uint8, device="cuda")
+    want = vs.varlen_linear_attn_fwd(*a, x["cu"])
+    grads = vs.varlen_linear_attn_bwd(*a, x["dout"], x["cu"], dg=dg)
+    binding.debug_set(binding.VSSM_DBG_FORCE_COPY_TIMEOUT, 0)
+    try:
+        vs.varlen_linear_attn_fwd(*a, x["cu"], workspace=ws)
+        assert vs.read_status(ws) == -17
+        vs.varlen_linear_attn_bwd(*a, x["dout"], x["cu"], workspace=ws, dg=dg)
+        assert vs.read_status(ws) == -17
+    finally:
+        binding.debug_set(binding.VSSM_DBG_FORCE_COPY_TIMEOUT, -1)
+    again = vs.varlen_linear_attn_bwd(*a, x["dout"], x["cu"], workspace=ws, dg=dg)
+    assert vs.read_status(ws) == 0
+    assert torch.equal(bits(vs.varlen_linear_attn_fwd(*a, x["cu"], workspace=ws)), bits(want))
+    for n, t in grads.items():
+        assert t is None or torch.equal(bits(t), bits(again[n])), n

@@ -491,10 +491,11 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
  * norm off over 32768 and 16384 packed tokens); with dg = NULL the walks of dq and
  * dk take a third less.
  * A value that is not finite in q, k, v, dout or the states reaches the
- * gradients that the formula carries it to; dg, a sum over a segment, is not
- * finite before it in the sequence's segments and keeps its value, but not its
- * last bits, behind it in its own, and a g that is not finite leaves NaN in its
- * whole chunk.  Other sequences keep their bits. */
+ * gradients that the formula carries it to: from k and v at a token dg of those
+ * behind it, from q and dout of it and those before.  As dg is a sum over the rest
+ * of a segment, the tokens before a k or v in its own segment lose theirs too;
+ * behind a q or dout dg keeps its value, but not its last bits.  A g that is not
+ * finite leaves NaN in its whole chunk.  Other sequences keep their bits. */
 size_t varlen_linear_attn_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t Hk, int32_t Hv,
                                              int32_t K, int32_t V, vssm_dtype dtype);
 int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,

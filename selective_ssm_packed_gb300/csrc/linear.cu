@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = fma2(splat2(in), e[i], o[i]);
           }
+          float dot = 0.0f;
           if (has_dot) {  // rho or sigma, then the token's own pair
             typename R::Raw raw;
             R::load(static_cast<const float*>(role.dot) + (start + at) * role.sdot + (int64_t)(h / role.rdot) * n2 + col0, role.sdot,
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
             for (int i = 0; i < R::kParts; ++i) transpose(raw[i], lane);
             float2 sum = splat2(0.0f);
             R::each(raw, 0, [&](int i, float2 y) { sum = fma2(y, o[i], sum); });
-            if (row < rows) role.dots[((int64_t)(tile * kLinParts + part) * a.Hv + h) * a.T + start + at + lane] = sum.x + sum.y;
+            dot = sum.x + sum.y;
             const float self = s_diag[row];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -447,8 +448,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) lin_walk_kernel(const __grid_c
             for (int i = 0; i < 8; ++i) {
               if (back ? row <= bad[2 * i] : row >= bad[2 * i]) o[i].x = nan;
               if (back ? row <= bad[2 * i + 1] : row >= bad[2 * i + 1]) o[i].y = nan;
+              if (back ? row < max(bad[2 * i], bad[2 * i + 1]) : row > min(bad[2 * i], bad[2 * i + 1])) dot = nan;  // another row's
             }
           }
+          if (has_dot && row < rows) role.dots[((int64_t)(tile * kLinParts + part) * a.Hv + h) * a.T + start + at + lane] = dot;
           const int64_t out_at = ((start + at) * a.Hv + h) * n2 + col0;
           typename R::Raw raw;
           R::put(raw, 0, o);

@@ -256,16 +256,23 @@ __device__ __forceinline__ void clear_rows(uint8_t* image, int rows, int t, int 
 
 // NaN in those of a row's results (`cols` of them, from `at` on) in whose column
 // a value of W at the row or an earlier one (back: a later one) is not finite.
-__device__ __noinline__ void spoil_row(const LinRole& role, const __nv_bfloat16* w, int64_t at, int row, int rows, int cols) {
+// Whether one is at another row: then the row's dot product has it, too.
+__device__ __noinline__ bool spoil_row(const LinRole& role, const __nv_bfloat16* w, int64_t at, int row, int rows, int cols) {
   const int from = role.back ? row : 0, to = role.back ? rows : row + 1;
   const float nan = __int_as_float(0x7fffffff);
+  bool others = false;
   for (int c = 0; c < cols; ++c) {
     bool odd = false;
-    for (int r = from; r < to; ++r) odd = odd || !isfinite(__bfloat162float(w[(int64_t)r * role.sw + c]));
+    for (int r = from; r < to; ++r) {
+      const bool here = !isfinite(__bfloat162float(w[(int64_t)r * role.sw + c]));
+      odd = odd || here;
+      others = others || (here && r != row);
+    }
     if (!odd) continue;
     if (role.part) static_cast<float*>(role.out)[at + c] = nan;
     else static_cast<__nv_bfloat16*>(role.out)[at + c] = __float2bfloat16_rn(nan);
   }
+  return others;
 }
 
 // `role`'s walk of the segment a.order[item], head h.  Its direction, and whether rows have a dot product, are known
@@ -674,8 +681,11 @@ __device__ __forceinline__ void walk(const LinArgs& a, const LinMaps& maps, cons
           for (int s = 0; s < kRuns; ++s) r[s].store(to + 16 * s, cols - 16 * s);
         }
       }
-      if (spoilt && mine) spoil_row(role, static_cast<const T*>(role.w) + (token - row) * role.sw + w_at + first, out_row + first, row, rows, cols);
-      if (has_dot && mine) role.dots[((int64_t)part * a.Hv + h) * a.T + token] = dot.hi + dot.lo;
+      float rest = dot.hi + dot.lo;
+      if (spoilt && mine &&
+          spoil_row(role, static_cast<const T*>(role.w) + (token - row) * role.sw + w_at + first, out_row + first, row, rows, cols))
+        rest = __int_as_float(0x7fffffff);
+      if (has_dot && mine) role.dots[((int64_t)part * a.Hv + h) * a.T + token] = rest;
     }
   } else {
     // W's copies are asked for by whoever knows that its place is free: whoever waits for a phase has to have done so

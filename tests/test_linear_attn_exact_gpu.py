@@ -11,7 +11,7 @@ import torch
 
 import selective_ssm_packed_gb300 as vs
 from selective_ssm_packed_gb300 import binding
-from test_linear_attn_gpu import bits, host, inputs, reference, run
+from test_linear_attn_gpu import bits, close, host, inputs, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -88,6 +88,28 @@ def test_dg_of_bf16_calls_keeps_an_f32_s_digits(K, V, decay):
     x = inputs([600, 100], 1, 2, K, V, "bf16", 43)
     x["g"] = (-decay * torch.exp(0.5 * torch.randn(x["g"].shape, generator=torch.Generator().manual_seed(2)))).cuda()
     assert off(host(run(x)["dg"]), reference(x)["dg"]) <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["q", "k", "v", "dout"])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_dg_beside_a_value_that_is_not_finite(K, V, name, bad, dtype):
+    """dg_t has the pairs (s, r) with s < t <= r: a bad q or dout at token b reaches dg of b and of what is before it; a bad
+    k or v what is behind it, and in a sum over the rest of the segment what is before it, too."""
+    for b in (50 + 140, 50 + 290):  # chunks before the last and the last, without gradients of the final states
+        x = inputs([50, 300, 20], 1, 2, K, V, dtype, 46)
+        clean = run(x)["dg"]
+        x[name][b, 0, 5] = bad
+        dg = run(x)["dg"]
+        for lo, hi in ((0, 50), (350, 370)):
+            assert torch.equal(bits(dg[lo:hi]), bits(clean[lo:hi]))
+        behind = dg[b + 1:350, 0]
+        if name in ("q", "dout"):
+            assert not torch.isfinite(dg[b, 0]).any()
+            close("dg", behind, host(clean[b + 1:350, 0]), dtype)
+        else:
+            assert not torch.isfinite(behind).any()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

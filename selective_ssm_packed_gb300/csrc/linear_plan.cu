@@ -146,6 +146,14 @@ constexpr int kDgThreads = 512, kDgWarps = kDgThreads / 32, kDgPer = kLinMaxSegm
 __device__ __forceinline__ Pair shfl_down(Pair v, int o) {
   return Pair{__shfl_down_sync(0xffffffffu, v.hi, o), __shfl_down_sync(0xffffffffu, v.lo, o)};
 }
+__device__ __forceinline__ float sum_behind(float v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float w = __shfl_down_sync(0xffffffffu, v, o);
+    if (lane + o < 32) v += w;
+  }
+  return v;
+}
 // The sum over this lane and those behind it.
 __device__ __forceinline__ Pair sum_behind(Pair v, int lane) {
 #pragma unroll 1
@@ -159,6 +167,7 @@ __device__ __forceinline__ Pair sum_behind(Pair v, int lane) {
 template <int kParts>
 __global__ void __launch_bounds__(kDgThreads, 2) lin_dg_kernel(LinArgs a, int tiles) {
   __shared__ Pair sums[kDgWarps];
+  __shared__ float sizes[kDgWarps];
   const int seg = blockIdx.x, h = blockIdx.y;
   if (seg >= a.info[0]) return;
   const int4 entry = a.table[seg];
@@ -166,29 +175,45 @@ __global__ void __launch_bounds__(kDgThreads, 2) lin_dg_kernel(LinArgs a, int ti
   const int per = (entry.z + kDgThreads - 1) / kDgThreads, lo = min(entry.z, t * per), n = min(entry.z - lo, per);
   const int64_t plane = a.T * a.Hv, first = h * a.T + entry.y + lo;
   Pair d[kDgPer], own{0.0f, 0.0f};
+  float size[kDgPer], own_size = 0.0f;  // |rho| + |sigma|
 #pragma unroll
   for (int i = 0; i < kDgPer; ++i) {
     d[i] = Pair{0.0f, 0.0f};
+    size[i] = 0.0f;
     if (i >= n) continue;
     const int64_t at = first + i;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) d[i] = add(d[i], Pair{a.role[0].dots[p * plane + at], 0.0f});
+    size[i] = fabsf(d[i].hi);
+    Pair sigma{0.0f, 0.0f};
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) d[i] = add(d[i], Pair{-a.role[1].dots[p * plane + at], 0.0f});
+    for (int p = 0; p < kParts; ++p) sigma = add(sigma, Pair{-a.role[1].dots[p * plane + at], 0.0f});
+    size[i] += fabsf(sigma.hi);
+    d[i] = add(d[i], sigma);
   }
 #pragma unroll
-  for (int i = kDgPer - 1; i >= 0; --i) own = add(own, d[i]);
+  for (int i = kDgPer - 1; i >= 0; --i) {
+    own = add(own, d[i]);
+    own_size += size[i];
+  }
   const Pair incl = sum_behind(own, lane);
+  const float incl_size = sum_behind(own_size, lane);
   if (lane == 0) sums[warp] = incl;
+  if (lane == 0) sizes[warp] = incl_size;
   __syncthreads();
   if (warp == 0) {
     const Pair v = sum_behind(lane < kDgWarps ? sums[lane] : Pair{0.0f, 0.0f}, lane);
+    const float w = sum_behind(lane < kDgWarps ? sizes[lane] : 0.0f, lane);
     if (lane < kDgWarps) sums[lane] = v;
+    if (lane < kDgWarps) sizes[lane] = w;
   }
   __syncthreads();
   Pair run = shfl_down(incl, 1), total{0.0f, 0.0f}, gap = sums[0];  // gap: what the sum over all tokens is off by
   if (lane == 31) run = Pair{0.0f, 0.0f};
   if (warp + 1 < kDgWarps) run = add(run, sums[warp + 1]);
+  float behind = __shfl_down_sync(0xffffffffu, incl_size, 1);
+  if (lane == 31) behind = 0.0f;
+  if (warp + 1 < kDgWarps) behind += sizes[warp + 1];
   const float *at_end = a.role[0].cross + ((int64_t)seg * a.Hv + h) * tiles;
   const float *at_begin = !(entry.w & kLinFirst) ? at_end - (int64_t)a.Hv * tiles
                           : a.role[1].cross      ? a.role[1].cross + ((int64_t)seg * a.Hv + h) * tiles
@@ -198,13 +223,16 @@ __global__ void __launch_bounds__(kDgThreads, 2) lin_dg_kernel(LinArgs a, int ti
     gap = add(gap, Pair{at_end[i], 0.0f});
     if (at_begin) gap = add(gap, Pair{-at_begin[i], 0.0f});
   }
-  float share = (gap.hi + gap.lo) / (float)max(entry.z, 1);
+  // A token's part in it goes by the size of its terms: one without any has no error, and one of 1000 times the others'
+  // size has it all.
+  float share = (gap.hi + gap.lo) / sizes[0];
   if (!isfinite(share)) share = 0.0f;  // tokens behind what is not finite keep their sums
 #pragma unroll
   for (int i = kDgPer - 1; i >= 0; --i) {
     if (i >= n) continue;
     run = add(run, d[i]);
-    const float off = share * (float)(entry.z - (lo + i));
+    behind += size[i];
+    const float off = share * behind;
     if (a.g_token) a.dg[((int64_t)entry.y + lo + i) * a.Hv + h] = run.hi + (run.lo - off);
     else total = add(total, Pair{run.hi, run.lo - off});
   }

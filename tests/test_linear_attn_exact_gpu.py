@@ -91,6 +91,29 @@ def test_dg_of_bf16_calls_keeps_an_f32_s_digits(K, V, decay):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_dg_of_a_tail_without_gradient_is_zero(K, V, dtype):
+    x = inputs([400, 30], 1, 2, K, V, dtype, 44)
+    x["dout"][300:400] = 0  # a masked loss
+    dg = run(x)["dg"]
+    assert (dg[300:400] == 0).all()
+    assert (dg[1:300] != 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_dg_behind_a_large_token_keeps_its_own_scale(dtype):
+    """Token 100 has a key of 1000 times the others' size, which token 110 forgets.  What the pairs of tokens 101 to 109 are
+    off by, a few 2^-22 of 1000 times a pair, is not theirs behind it, of which there are 290: as of decays that forget,
+    2^-16 of their own size."""
+    x = inputs([400], 1, 2, 64, 64, dtype, 45)
+    x["k"][100] *= 1000
+    x["g"][110] = -60.0
+    got, ref = host(run(x)["dg"]), reference(x)["dg"]
+    for h in range(2):
+        assert off(got[111:, h], ref[111:, h]) <= 2.0 ** -16, h
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("name", ["q", "k", "v", "dout"])
 @pytest.mark.parametrize("K,V", WIDTHS)

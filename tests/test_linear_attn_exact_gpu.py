@@ -135,6 +135,57 @@ def test_dg_beside_a_value_that_is_not_finite(K, V, name, bad, dtype):
             assert not torch.isfinite(behind).any()
 
 
+KINDS = ["steep", "very steep", "none", "mixed", "growing"]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_decays_of_every_size(K, V, kind, dtype):
+    x = inputs([420, 40], 1, 2, K, V, dtype, 47, True)
+    g, r = x["g"], np.random.default_rng(1)
+    if kind == "steep":
+        g.fill_(-6.0)
+    elif kind == "very steep":
+        g.copy_(torch.from_numpy(-np.exp(r.uniform(2, 5.5, g.shape))).float())
+    elif kind == "none":
+        g[r.integers(0, 460, 20)] = float("-inf")
+        g[r.integers(0, 460, 20)] = -1e30
+    elif kind == "mixed":
+        g[100:140] = -40.0
+        g[150:160] = 0.0
+        g[200] = -300.0
+    else:
+        g.copy_(torch.from_numpy(r.uniform(-0.05, 0.04, g.shape)).float())
+    got, ref = run(x, states=True), reference(x)
+    for n, t in got.items():
+        close(n, t, ref[n], dtype, max(np.linalg.norm(ref[n]), 0.05 * np.linalg.norm(ref["dv"])) if n == "dg" else None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("name", ["q", "k", "v", "dout"])
+@pytest.mark.parametrize("K,V", WIDTHS[1:])
+def test_a_value_that_is_not_finite_reaches_what_the_formulas_carry_it_to(K, V, name, bad, dtype):
+    lens, t, c = [50, 400, 20], 50 + 140, 5
+    x = inputs(lens, 1, 2, K, V, dtype, 48, True)
+    clean = run(x, states=True)
+    x[name][t, 0, c] = bad
+    got = run(x, states=True)
+    heads = [0] if name in ("v", "dout") else [0, 1]
+    spans = {"out": {"q": (t, t + 1), "k": (t, 450), "v": (t, 450)}, "dq": {"k": (t, 450), "v": (t, 450), "dout": (t, t + 1)},
+             "dk": {"q": (50, t + 1), "v": (t, t + 1), "dout": (50, t + 1)}, "dv": {"q": (50, t + 1), "k": (t, t + 1), "dout": (50, t + 1)}}
+    column = {("out", "v"), ("dq", "k"), ("dk", "q"), ("dv", "dout")}  # it stays in its column
+    for n, by in spans.items():
+        hit = torch.zeros_like(got[n], dtype=torch.bool)
+        if name in by:
+            lo, hi = by[name]
+            for h in heads if n in ("out", "dv") else [0]:
+                hit[(slice(lo, hi), h, c) if (n, name) in column else (slice(lo, hi), h)] = True
+        assert not torch.isfinite(got[n][hit]).any(), n
+        assert torch.equal(bits(got[n])[~hit], bits(clean[n])[~hit]), n
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("dg", [True, False])
 @pytest.mark.parametrize("T", [300, 900])  # one segment, several; three chunks and more
@@ -159,3 +210,24 @@ def test_a_wait_that_runs_out_is_reported(K, V, T, dg, dtype):
     assert torch.equal(bits(vs.varlen_linear_attn_fwd(*a, x["cu"], workspace=ws)), bits(want))
     for n, t in grads.items():
         assert t is None or torch.equal(bits(t), bits(again[n])), n
+
+
+def test_every_tensor_of_a_call_is_looked_at_for_its_device(monkeypatch):
+    seen = []
+    monkeypatch.setattr(binding, "_together", lambda *t: seen.append({id(x) for x in t}))
+    x = inputs([20], 1, 2, 64, 64, "f32", 50, True)
+    a = (x["q"], x["k"], x["v"], x["g"])
+
+    def looks(f, *args, **kw):
+        seen.clear()
+        f(*args, **kw)
+        given = [t for t in (*args, *kw.values(), *kw.get("grads", {}).values()) if isinstance(t, torch.Tensor)]
+        assert len(seen) == 1 and all(id(t) in seen[0] for t in given), f
+
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    looks(vs.varlen_linear_attn_fwd, *a, x["cu"], out=torch.empty_like(x["v"]), workspace=ws, initial_states=x["init"],
+          final_states=torch.empty_like(x["init"]))
+    looks(vs.varlen_linear_attn_bwd, *a, x["dout"], x["cu"], grads={"dq": torch.empty_like(x["q"])}, workspace=ws,
+          initial_states=x["init"], d_final_states=x["dfinal"], d_initial_states=torch.empty_like(x["init"]))
+    looks(vs.varlen_linear_attn_step, *a, torch.zeros((20, 2, 64, 64), device="cuda"), out=torch.empty_like(x["v"]),
+          state_indices=torch.arange(20, dtype=torch.int32, device="cuda"), status=torch.zeros(1, dtype=torch.int32, device="cuda"))

@@ -15,18 +15,25 @@ int check_lin_heads(int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
 }
 
 // Tokens of a segment, at most 4096 (whose state is 3% of the data, and over
-// which dg's sums run).  An SM has `share` tokens to walk; where no sequence is
-// likely to be longer than that (the longest is taken for four times the mean:
-// only the GPU knows it) they are better left whole, which spares the walk
-// before and the scan (32768 packed tokens of 32 heads in bf16: 271 us, and 352
-// in segments of 1792); otherwise a quarter of it each fills the GPU evenly, but
-// no fewer than 256 tokens (3001 of 6 heads in f32: 83 us, 97 with 128, 107 with
-// 384; 4000 of 8 in bf16: 52 us, 68 with 128, 60 with 512), and no pack of 512
-// is worth it (500 tokens in bf16: 29 us, 36 with 256).
-int lin_segment(int64_t T, int64_t S, int Hv, int ctas, IO io) {
+// which dg's sums run).  An SM has `share` tokens to walk in a launch of `ctas`
+// for a segment's head; where no sequence is likely to be longer than that (the
+// longest is taken for four times the mean: only the GPU knows it) they are
+// better left whole, which spares the walk before and the scan (32768 packed
+// tokens of 32 heads in bf16: 282 us, and 361 in segments of 1792).  Otherwise a
+// quarter of it fills the GPU evenly, but no fewer than 256 tokens (3001 of 6 heads
+// in f32: 75 us, 85 with 128, 93 with 384; 4000 of 8 in bf16: 50 us, 67 with 128, 58
+// with 512), and no pack of 512 is worth it (500 tokens in bf16: 28 us, 40 with 256).
+// The bf16 backward walks two roles for the states before, and each role in a
+// launch of its own: it takes all of the share (32768 tokens of 8 heads in sequences
+// of up to 4096 415 us, share 1724; 523 with 512, 628 whole; 9000 of 16 heads 250,
+// share 947; 388 with 256, 454 whole; one sequence of 16384, 8 heads, 286, share 862;
+// 404 with 256), and leaves sequences of half as much again whole (32768 of 16 heads,
+// share 3449: 592 us, 641 with 3584; of 12, share 2586: 640, and 571 with 2048).
+int lin_segment(int64_t T, int64_t S, int Hv, int ctas, int parts, IO io) {
   const int64_t chunk = lin_chunk(io), share = T * Hv * ctas / 152, longest = 4 * T / (S > 0 ? S : 1);
-  if (longest <= share) return kLinMaxSegment;
-  int64_t seg = (share / 4 + chunk - 1) / chunk * chunk;
+  if (longest <= (parts == 1 ? share * 3 / 2 : share)) return kLinMaxSegment;
+  const int64_t step = parts == 1 ? 2 * chunk : chunk;
+  int64_t seg = (share / parts + step - 1) / step * step;
   const int64_t least = T <= 512 ? 512 : 256;
   return (int)(seg < least ? least : seg > kLinMaxSegment ? kLinMaxSegment : seg);
 }
@@ -41,7 +48,7 @@ struct LinLayout {
 LinLayout lin_layout(int64_t T, int64_t S, int Hk, int Hv, int K, int V, IO io, bool bwd) {
   LinLayout l;
   const int tk = lin_ctas(io, K), tv = lin_ctas(io, V);
-  l.seg = lin_segment(T, S, Hv, bwd ? 2 * tk + tv : tv, io);
+  l.seg = io == IO::BF16 ? lin_segment(T, S, Hv, 1, bwd ? 1 : 4, io) : lin_segment(T, S, Hv, bwd ? 2 * tk + tv : tv, 4, io);
   l.max_inner = T > l.seg ? T / l.seg : 0;
   l.max_segs = T / l.seg + S;
   const size_t segs = (size_t)l.max_segs, inner = (size_t)l.max_inner, state = (size_t)Hv * K * V * sizeof(float);

@@ -489,7 +489,7 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
  * add the value heads that share a head, in order; no atomics, bitwise
  * repeatable.  dg keeps an f32's digits in bf16 calls too (6e-7 to 8e-7 of its
  * norm off over 32768 and 16384 packed tokens); with dg = NULL the walks of dq and
- * dk take a third less.
+ * dk take 40% less.
  * A value that is not finite in q, k, v, dout or the states reaches the
  * gradients that the formula carries it to: from k and v at a token dg of those
  * behind it, from q and dout of it and those before.  As dg is a sum over the rest

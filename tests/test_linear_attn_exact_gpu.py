@@ -212,6 +212,42 @@ def test_a_wait_that_runs_out_is_reported(K, V, T, dg, dtype):
         assert t is None or torch.equal(bits(t), bits(again[n])), n
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[300], [900, 0, 40]])
+def test_a_wait_that_runs_out_with_states_is_reported(lens, dtype):
+    x = inputs(lens, 1, 2, 128, 128, dtype, 51, True)
+    a = (x["q"], x["k"], x["v"], x["g"])
+    code = binding.VSSM_F32 if dtype == "f32" else binding.VSSM_BF16
+    n = binding.linear_attn_bwd_workspace_size(sum(lens), len(lens), 1, 2, 128, 128, code)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    want = run(x, states=True)
+    binding.debug_set(binding.VSSM_DBG_FORCE_COPY_TIMEOUT, 0)
+    try:
+        vs.varlen_linear_attn_fwd(*a, x["cu"], workspace=ws, initial_states=x["init"], final_states=True)
+        assert vs.read_status(ws) == -17
+        vs.varlen_linear_attn_bwd(*a, x["dout"], x["cu"], workspace=ws, initial_states=x["init"], d_final_states=x["dfinal"],
+                                  d_initial_states=True)
+        assert vs.read_status(ws) == -17
+    finally:
+        binding.debug_set(binding.VSSM_DBG_FORCE_COPY_TIMEOUT, -1)
+    got = run(x, states=True, workspace=ws)
+    for m, t in want.items():
+        assert torch.equal(bits(t), bits(got[m])), m
+    assert vs.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[200, 0, 70], [100]])
+def test_states_may_take_the_place_of_those_a_call_comes_with(lens, dtype):
+    """Sequences of one segment, as in a serving pool: f32 walks of several would write a state that others still read."""
+    x = inputs(lens, 1, 2, 64, 128, dtype, 52, True)
+    a = (x["q"], x["k"], x["v"], x["g"])
+    want = run(x, states=True, bwd=False)
+    pool = x["init"].clone()
+    out, final = vs.varlen_linear_attn_fwd(*a, x["cu"], initial_states=pool, final_states=pool)
+    assert final is pool and torch.equal(bits(out), bits(want["out"])) and torch.equal(bits(pool), bits(want["final"]))
+
+
 def test_every_tensor_of_a_call_is_looked_at_for_its_device(monkeypatch):
     seen = []
     monkeypatch.setattr(binding, "_together", lambda *t: seen.append({id(x) for x in t}))

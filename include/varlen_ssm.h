@@ -461,7 +461,10 @@ int varlen_gated_delta_step(const void* q, const void* k, const void* v, int64_t
  *   of them, three otherwise; accumulation and the state
  *   are float32.  bf16 results lose no more than their own rounding;
  *   final_states (and the backward's d_initial_states) keep all 24 bits, in
- *   bf16 calls by a walk of their own.
+ *   bf16 calls by a walk of their own, behind the others.
+ * final_states may be initial_states, in f32 only where total_tokens is below
+ *   a segment's (VSSM_ERR_ARG otherwise); d_initial_states may be
+ *   d_final_states, in bf16.
  * A value that is not finite reaches what the recurrence carries it to and
  *   nothing else, as there; beside a g that is not finite the earlier tokens
  *   of its chunk (of 64 tokens in f32, 128 in bf16) keep their values, but

@@ -186,6 +186,8 @@ int varlen_linear_attn_fwd(const void* q, const void* k, const void* v, int64_t 
   TRY(check_ptr(initial_states, "initial_states", false));
   TRY(check_ptr(final_states, "final_states", false));
   const LinLayout l = lin_layout(T, num_seqs, Hk, Hv, K, V, io, false);
+  if (io == IO::F32 && final_states && final_states == initial_states && l.max_inner > 0)
+    return bad(VSSM_ERR_ARG, "final_states are initial_states, which the walks of a sequence's segments (%d tokens) read meanwhile", l.seg);
   TRY(check_room(workspace, workspace_bytes, l.fwd_end, "workspace"));
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -234,6 +236,8 @@ int varlen_linear_attn_bwd(const void* q, const void* k, const void* v, int64_t 
   TRY(check_ptr(dk, "dk", T > 0));
   TRY(check_ptr(dv, "dv", T > 0));
   const LinLayout l = lin_layout(T, num_seqs, Hk, Hv, K, V, io, true);
+  if (io == IO::F32 && d_initial_states && (d_initial_states == d_final_states || d_initial_states == initial_states))
+    return bad(VSSM_ERR_ARG, "d_initial_states is an array of states that the walks of other gradients read meanwhile");
   TRY(check_room(workspace, workspace_bytes, l.bwd_end, "workspace"));
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);

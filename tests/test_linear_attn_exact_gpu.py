@@ -236,16 +236,30 @@ def test_a_wait_that_runs_out_with_states_is_reported(lens, dtype):
     assert vs.read_status(ws) == 0
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("lens", [[200, 0, 70], [100]])
+@pytest.mark.parametrize("dtype,lens", [("f32", [200, 0, 70]), ("bf16", [200, 0, 70]), ("bf16", [900, 40])])
 def test_states_may_take_the_place_of_those_a_call_comes_with(lens, dtype):
-    """Sequences of one segment, as in a serving pool: f32 walks of several would write a state that others still read."""
     x = inputs(lens, 1, 2, 64, 128, dtype, 52, True)
     a = (x["q"], x["k"], x["v"], x["g"])
-    want = run(x, states=True, bwd=False)
+    want = run(x, states=True)
     pool = x["init"].clone()
     out, final = vs.varlen_linear_attn_fwd(*a, x["cu"], initial_states=pool, final_states=pool)
     assert final is pool and torch.equal(bits(out), bits(want["out"])) and torch.equal(bits(pool), bits(want["final"]))
+    if dtype == "bf16":
+        pool = x["dfinal"].clone()
+        g = vs.varlen_linear_attn_bwd(*a, x["dout"], x["cu"], initial_states=x["init"], d_final_states=pool, d_initial_states=pool)
+        assert torch.equal(bits(pool), bits(want["dinit"]))
+        for n in ("dq", "dk", "dv", "dg"):
+            assert torch.equal(bits(g[n]), bits(want[n])), n
+
+
+def test_f32_states_that_other_walks_read_are_not_written():
+    x = inputs([900, 40], 1, 2, 64, 64, "f32", 53, True)
+    a = (x["q"], x["k"], x["v"], x["g"])
+    with pytest.raises(vs.VssmError):
+        vs.varlen_linear_attn_fwd(*a, x["cu"], initial_states=x["init"], final_states=x["init"])
+    for given in ("init", "dfinal"):
+        with pytest.raises(vs.VssmError):
+            vs.varlen_linear_attn_bwd(*a, x["dout"], x["cu"], initial_states=x["init"], d_final_states=x["dfinal"], d_initial_states=x[given])
 
 
 def test_every_tensor_of_a_call_is_looked_at_for_its_device(monkeypatch):

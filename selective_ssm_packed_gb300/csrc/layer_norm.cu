@@ -22,7 +22,7 @@ namespace {
 // from the row, and its square from the variance.
 // Everything is read and written once, which bounds the pass: 32768 x 2048 in
 // bf16 with the f32 stream 117 us (6.9 TB/s, some of it left in L2), 32 groups of 128 in 4096
-// channels 83 us (6.5 TB/s), one row of 2048 4 us.
+// channels 84 us (6.4 TB/s), one row of 2048 4 us.
 template <int kTeam>
 struct Team {
   static constexpr int kThreads = kTeam <= 32 ? 128 : kTeam, kUnits = kThreads / kTeam;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(Team<kTeam>::kThreads, fwd_threads<T, kRes>() 
 //   dweight = sum over tokens of dy n,  dbias = sum of dy
 // One row of sums per team goes to `partial`, which a second kernel adds in
 // the teams' order: no atomics, the same bits every time.  32768 x 2048 with the
-// stream 151 us (6.2 TB/s), 32 groups of 128 in 4096 channels 143 us (5.5 TB/s: five sums
+// stream 152 us (6.2 TB/s), 32 groups of 128 in 4096 channels 145 us (5.5 TB/s: five sums
 // a row of 8 threads keep the issue slots 60% busy), the teams' sums 8 us.
 template <typename T, typename H, int kTeam>
 __global__ void __launch_bounds__(Team<kTeam>::kThreads, bwd_threads<kTeam>() / Team<kTeam>::kThreads)

@@ -19,7 +19,7 @@ namespace {
 // leaves is worked on while the next one runs: up * W during A and D1, P
 // during U, S during D2.  Chunks of 64 tokens and tiles of 64 columns are what
 // shared memory holds of three terms; the chain of a chunk is what bounds it
-// (3001 tokens, 6 heads of 96 x 80: 58 us forward, 151 the gradients; 11 us for
+// (3001 tokens, 6 heads of 96 x 80: 51 us forward, 130 the gradients; 11 us for
 // 16 tokens).
 constexpr int kLinWorkers = 128 * kLinParts, kLinThreads = kLinWorkers + 32, kLinCtrl = kLinWorkers / 32;
 
